@@ -406,6 +406,176 @@ int moe_layer_backward(const moe_config_t* cfg, const void* x, const void* dy, c
                        float z_coef, const moe_grads_t* grads, void* ws, size_t ws_bytes,
                        moe_stream_t stream);
 
+/* ---------------------------------------------------------------- scored routing */
+
+/*
+ * Routing from expert scores with a selection bias (Lec16 "DeepSeek V3 MoE": expert groups,
+ * limited groups, the balance without an auxiliary loss that a per-expert bias gives).
+ * For the logits l of one token:
+ *   scores     s_e = 1 / (1 + exp(-l_e)) (MOE_SCORE_SIGMOID) or softmax(l)_e
+ *              (MOE_SCORE_SOFTMAX)
+ *   selection  c_e = s_e + select_bias[e] (no bias: c_e = s_e)
+ *   groups     (n_expert_groups > 1) a group's score is the sum of its group_top best c_e
+ *              (of its only one, if it has one); the topk_groups best groups stay
+ *   experts    the k largest c_e of the groups that stay, largest first
+ *   weights    w_j = scale * s_{id_j} / sum_i s_{id_i} (renorm 1) or scale * s_{id_j} (0);
+ *              the bias takes no part in them.
+ * Equal c_e rank the lower expert, equal group scores the lower group. The scores that
+ * decide are those of the fp64 evaluation of the fp32 logits and biases, so the ids are a
+ * pure function of them; the weights are fp32.
+ *   score: MOE_SCORE_*; group_top: 1 or 2; renorm: 0 or 1; scale: finite.
+ */
+enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
+typedef struct {
+  int32_t score;
+  int32_t group_top;
+  int32_t renorm;
+  float scale;
+} moe_score_t;
+
+/*
+ * moe_route with scored selection: fills every field of *out from logits [S, E] and
+ * select_bias (float [E], nullable), capacity slots and rows as moe_route does. Of cfg it
+ * takes S, G, E, k, capacity_factor, n_expert_groups and topk_groups; random_routing and
+ * uniform_assignment must be 0 and gate_norm MOE_GATE_SOFTMAX_TOPK (the weights are those
+ * above): MOE_ERR_UNSUPPORTED otherwise. aux_loss is E * sum_e f_e P_e per group with P_e the
+ * mean over the group's tokens of s_e / sum_e' s_e' (the softmax probabilities themselves
+ * with MOE_SCORE_SOFTMAX); z_loss as in moe_route. Non-finite logits and biases set
+ * MOE_ERR_NONFINITE and take their expert out of the selection (its score is 0); a token
+ * left with fewer than k experts takes the lowest of the others with weight 0.
+ * ws: MOE_WS_STEP bytes.
+ */
+int moe_route_scored(const moe_config_t* cfg, const moe_score_t* score, const float* logits,
+                     const float* select_bias, const moe_route_out_t* out, void* ws,
+                     size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * The gradient of moe_route_scored to the logits, the selection held fixed:
+ *     dlogits [S, E] = d( sum(dgate * w over the kept choices) + aux_coef * aux_loss
+ *                         + z_coef * z_loss ) / d logits
+ * dgate float [S, k]; r: the forward's routing outputs, of which expert_id, row (-1 = not
+ * kept, no gradient) and counts_routed are read. Every entry of dlogits is written. No
+ * workspace.
+ */
+int moe_route_scored_backward(const moe_config_t* cfg, const moe_score_t* score,
+                              const float* logits, const moe_route_out_t* r, const float* dgate,
+                              float aux_coef, float z_coef, float* dlogits, moe_stream_t stream);
+
+/*
+ * moe_layer_forward and moe_layer_backward with moe_route_scored as the routing (the router
+ * projection first, its logits in logits_out or, when that is null, in ws). bias is the
+ * per-expert offset of the logits as in moe_router, select_bias the selection's; both may be
+ * NULL. The backward takes the logits of the forward (its logits_out) and the same score;
+ * everything else is as in the calls of the same name without _scored.
+ */
+int moe_layer_forward_scored(const moe_config_t* cfg, const moe_score_t* score, const void* x,
+                             const void* W_g, const float* bias, const float* select_bias,
+                             const void* W_in_packed, const void* W_out_packed,
+                             const void* Ws_in_packed, const void* Ws_out_packed,
+                             const void* residual, void* y, float* logits_out,
+                             const moe_route_out_t* r, void* ws, size_t ws_bytes,
+                             moe_stream_t stream);
+int moe_layer_backward_scored(const moe_config_t* cfg, const moe_score_t* score, const void* x,
+                              const void* dy, const void* W_g, const void* W_in_packed,
+                              const void* Wt_in_packed, const void* Wt_out_packed,
+                              const void* Ws_in_packed, const void* Wst_in_packed,
+                              const void* Wst_out_packed, const float* logits,
+                              const moe_route_out_t* r, const void* fwd_ws, size_t fwd_ws_bytes,
+                              int residual, float aux_coef, float z_coef, const moe_grads_t* grads,
+                              void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- layer norm */
+
+/*
+ * Layer norm over the columns of a [rows, cols] matrix, with the residual addition in front:
+ *     h = x (+ residual),  y = (h - mean(h)) / sqrt(var(h) + eps) * gamma (+ beta)
+ * var the mean of the squared deviations. Sums, statistics and h itself are fp32; y and the
+ * stored h are rounded once to the element type. rows >= 0 (0: nothing is launched, the
+ * backward zeroes dgamma and dbeta), cols >= 1, eps >= 0. ld*: elements between rows (>=
+ * cols); no other alignment than the element's.
+ *   forward:   ldx of x, ldr of residual, ldh of h, ldy of y
+ *   backward:  ldx of h, ldr of dh, ldh of dx, ldy of dy
+ */
+typedef struct {
+  int32_t rows, cols;
+  int32_t dtype; /* MOE_F32 / MOE_BF16: x, residual, h, y and their gradients */
+  float eps;
+  int64_t ldx, ldr, ldh, ldy;
+} moe_norm_t;
+
+/*
+ * residual, beta, h, mean and rstd may be NULL. gamma, beta float [cols]; mean, rstd float
+ * [rows] (rstd = 1 / sqrt(var + eps)). y or h may be x or residual itself (same stride), not
+ * otherwise overlap them, nor each other.
+ */
+int moe_norm_forward(const moe_norm_t* n, const void* x, const void* residual, const float* gamma,
+                     const float* beta, void* h, void* y, float* mean, float* rstd,
+                     moe_stream_t stream);
+
+/* Workspace of moe_norm_backward: a zero-filled header and partial sums (256-byte aligned). */
+int moe_norm_workspace_bytes(const moe_norm_t* n, size_t* bytes);
+
+/*
+ * With xh = (h - mean) * rstd, g = dy * gamma:
+ *     dx = rstd * (g - mean(g) - xh * mean(g * xh)) (+ dh)      (h, rounded once)
+ *     dgamma = sum over rows of dy * xh,  dbeta = sum over rows of dy   (float [cols])
+ * dh (nullable) is the gradient that reaches h on its other path (the residual stream), so
+ * dx is the gradient of x and of residual alike. dgamma and dbeta may be NULL. dx may be dy
+ * or dh itself (same stride). The sums over rows have an order fixed by the shape.
+ */
+int moe_norm_backward(const moe_norm_t* n, const void* dy, const void* h, const float* gamma,
+                      const float* mean, const float* rstd, const void* dh, void* dx,
+                      float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                      moe_stream_t stream);
+
+/* ---------------------------------------------------------------- linear layer */
+
+/* Activations of the linear layer: gelu(v) = v * Phi(v) by erf, or its tanh form. */
+enum { MOE_LIN_NONE = 0, MOE_LIN_RELU = 1, MOE_LIN_GELU = 2, MOE_LIN_GELU_TANH = 3, MOE_LIN_SILU = 4 };
+
+/*
+ * A dense layer with its epilogue (the dense feed-forward halves that alternate with MoE
+ * layers, GShard "MoE Transformer"; Lec16 "DeepSeek V3 MoE": the first layers are dense):
+ *     pre = x W^T (+ bias),  y = act(pre) (+ residual)
+ * x [T, K], W [N, K], residual, y and pre [T, N] in the element type, bias float [N];
+ * T >= 0, N >= 1, K >= 1, any size. Products are summed in fp32 and each output rounded once.
+ * ld*: elements between rows (0: the row's length). bf16 runs on the tensor cores; operands
+ * whose rows are not on 16-byte boundaries are copied into the workspace first. fp32 (the
+ * plain-FMA path, meant for small layers).
+ */
+typedef struct {
+  int32_t T, N, K;
+  int32_t act;   /* MOE_LIN_* */
+  int32_t dtype; /* MOE_F32 / MOE_BF16 */
+  int64_t ldx, ldw, ldy, ldr, ldp; /* x, W, y (backward: dy), residual, pre */
+  int64_t lddx, lddw;              /* backward: dx, dW */
+} moe_linear_t;
+
+/*
+ * Workspace (256-byte aligned, its first 256 bytes zero before first use: status word and
+ * wait limit as every workspace's). backward: 1 for both directions, 0 for the forward
+ * alone. unaligned: 1 makes room for the copies of every bf16 operand; 0 for those that the
+ * strides call for (an operand that does not start on a 16-byte boundary then gives
+ * MOE_ERR_WORKSPACE).
+ */
+int moe_linear_workspace_bytes(const moe_linear_t* p, int backward, int unaligned, size_t* bytes);
+
+/* bias, residual and pre may be NULL; y may be residual itself (same stride). */
+int moe_linear_forward(const moe_linear_t* p, const void* x, const void* W, const float* bias,
+                       const void* residual, void* y, void* pre, void* ws, size_t ws_bytes,
+                       moe_stream_t stream);
+
+/*
+ * With d = dy * act'(pre) (pre as the forward stored it; NULL for MOE_LIN_NONE):
+ *     dx [T, K] = d W,  dW [N, K] = d^T x  (element type),  dbias float [N] = sum over t of d
+ * dx, dW and dbias may be NULL. bf16 with an activation: d is rounded to bf16 for the two
+ * products (the tensor cores' operand type), hence dW in the element type; dbias sums the
+ * unrounded d. The residual's gradient is dy itself. relu'(0) = 0.
+ */
+int moe_linear_backward(const moe_linear_t* p, const void* dy, const void* x, const void* W,
+                        const void* pre, void* dx, void* dW, float* dbias, void* ws,
+                        size_t ws_bytes, moe_stream_t stream);
+
 /*
  * Synchronises `stream`, reads the status word in ws, clears it, and returns MOE_OK or
  * the device error recorded since the last call (MOE_ERR_TIMEOUT, MOE_ERR_NONFINITE or

@@ -37,6 +37,25 @@ class MoeRouteOut(ctypes.Structure):
     _fields_ = [(n, c_void_p) for n in ROUTE_FIELDS]
 
 
+SCORES = {"sigmoid": 0, "softmax": 1}
+LIN_ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+class MoeScore(ctypes.Structure):
+    _fields_ = [("score", c_int32), ("group_top", c_int32), ("renorm", c_int32), ("scale", c_float)]
+
+
+class MoeNorm(ctypes.Structure):
+    _fields_ = [("rows", c_int32), ("cols", c_int32), ("dtype", c_int32), ("eps", c_float),
+                ("ldx", c_int64), ("ldr", c_int64), ("ldh", c_int64), ("ldy", c_int64)]
+
+
+class MoeLinear(ctypes.Structure):
+    _fields_ = [("T", c_int32), ("N", c_int32), ("K", c_int32), ("act", c_int32), ("dtype", c_int32),
+                ("ldx", c_int64), ("ldw", c_int64), ("ldy", c_int64), ("ldr", c_int64), ("ldp", c_int64),
+                ("lddx", c_int64), ("lddw", c_int64)]
+
+
 GRAD_FIELDS = ("dx", "dW_g", "dbias", "dW_in", "dW_up", "dW_out", "dWs_in", "dWs_up", "dWs_out")
 
 
@@ -86,6 +105,27 @@ _PROTOTYPES = {
                            c_void_p, c_void_p, c_void_p, c_void_p, _P(MoeRouteOut), c_void_p,
                            c_size_t, ctypes.c_int, c_float, c_float, _P(MoeGrads), c_void_p,
                            c_size_t, c_void_p],
+    "moe_route_scored": [_P(MoeConfig), _P(MoeScore), c_void_p, c_void_p, _P(MoeRouteOut), c_void_p,
+                         c_size_t, c_void_p],
+    "moe_route_scored_backward": [_P(MoeConfig), _P(MoeScore), c_void_p, _P(MoeRouteOut), c_void_p,
+                                  c_float, c_float, c_void_p, c_void_p],
+    "moe_layer_forward_scored": [_P(MoeConfig), _P(MoeScore), c_void_p, c_void_p, c_void_p, c_void_p,
+                                 c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                 _P(MoeRouteOut), c_void_p, c_size_t, c_void_p],
+    "moe_layer_backward_scored": [_P(MoeConfig), _P(MoeScore), c_void_p, c_void_p, c_void_p, c_void_p,
+                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                  _P(MoeRouteOut), c_void_p, c_size_t, ctypes.c_int, c_float, c_float,
+                                  _P(MoeGrads), c_void_p, c_size_t, c_void_p],
+    "moe_norm_forward": [_P(MoeNorm), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                         c_void_p, c_void_p, c_void_p],
+    "moe_norm_workspace_bytes": [_P(MoeNorm), _P(c_size_t)],
+    "moe_norm_backward": [_P(MoeNorm), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                          c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p],
+    "moe_linear_workspace_bytes": [_P(MoeLinear), ctypes.c_int, ctypes.c_int, _P(c_size_t)],
+    "moe_linear_forward": [_P(MoeLinear), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                           c_void_p, c_size_t, c_void_p],
+    "moe_linear_backward": [_P(MoeLinear), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                            c_void_p, c_void_p, c_size_t, c_void_p],
     "moe_get_device_status": [c_void_p, c_void_p],
     "moe_set_wait_limit": [c_void_p, ctypes.c_uint64, c_void_p],
 }

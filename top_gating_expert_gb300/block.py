@@ -1,0 +1,295 @@
+"""The operators around the MoE layer in a Transformer block, and blocks made of them.
+
+``layer_norm`` and ``linear`` (with their backward passes) are the C ABI's moe_norm_* and
+moe_linear_* on torch tensors: arguments are checked here, outputs that are not given are
+allocated, and nothing else happens on the host. ``MoeBlock`` and ``DenseBlock`` are the two
+feed-forward halves that alternate in an MoE Transformer: x + MoE(norm(x)) and
+x + W2 act(W1 norm(x)).
+
+Matrices are 2-D CUDA tensors of float32 or bfloat16 whose columns are contiguous (any row
+stride, any alignment); norm and bias parameters, row statistics and their gradients are
+float32. A `stream` other than the current one is the caller's to order, as in `moe`.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import _native as N
+from . import moe
+from .moe import _check, _ptr, _stream
+
+_DTYPES = {torch.float32: N.MOE_F32, torch.bfloat16: N.MOE_BF16}
+
+
+def _matrix(t, name, where, rows=None, cols=None, dtype=None, device=None):
+    """Checks one matrix; returns its row stride in elements."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{where}: {name} must be a 2-D tensor")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{where}: {name} must be on {device or 'a CUDA device'}")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{where}: {name} must be {dtype or 'float32 or bfloat16'}, not {t.dtype}")
+    r, c = t.shape
+    if c < 1 or (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected "
+                         f"({'any' if rows is None else rows}, {'any >= 1' if cols is None else cols})")
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{where}: the columns of {name} must be contiguous")
+    if r > 1 and t.stride(0) < c:
+        raise ValueError(f"{where}: the rows of {name} overlap (row stride {t.stride(0)})")
+    return max(t.stride(0), c) if r > 1 else c
+
+
+def _vector(t, name, where, n, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != (n,) \
+            or t.device != device or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{where}: {name} must be a contiguous float32 tensor of {n} elements on {device}")
+
+
+def _workspace_ok(ws, where, device):
+    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
+        raise ValueError(f"{where}: ws must be a contiguous uint8 tensor on {device}")
+
+
+def _on(stream):
+    """Allocations made for a call belong to the stream that the call runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+# ------------------------------------------------------------------ layer norm
+def layer_norm(x, gamma, beta=None, eps=1e-5, residual=None, *, out=None, h=None, mean=None, rstd=None,
+               stream=None):
+    """(y, h, mean, rstd): h = x (+ residual) and y = (h - mean) * rstd * gamma (+ beta), row by
+    row, rstd = 1 / sqrt(var + eps). Without a residual h is x itself, and nothing is stored."""
+    w = "layer_norm"
+    ldx = _matrix(x, "x", w)
+    T, M = x.shape
+    dev, dt = x.device, x.dtype
+    ldr = M if residual is None else _matrix(residual, "residual", w, T, M, dt, dev)
+    _vector(gamma, "gamma", w, M, dev)
+    if beta is not None:
+        _vector(beta, "beta", w, M, dev)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, M), dtype=dt, device=dev)
+        if residual is not None and h is None:
+            h = torch.empty((T, M), dtype=dt, device=dev)
+        if mean is None:
+            mean = torch.empty(T, dtype=torch.float32, device=dev)
+        if rstd is None:
+            rstd = torch.empty(T, dtype=torch.float32, device=dev)
+    ldy = _matrix(out, "out", w, T, M, dt, dev)
+    ldh = M if h is None else _matrix(h, "h", w, T, M, dt, dev)
+    _vector(mean, "mean", w, T, dev)
+    _vector(rstd, "rstd", w, T, dev)
+    n = N.MoeNorm(rows=T, cols=M, dtype=_DTYPES[dt], eps=float(eps), ldx=ldx, ldr=ldr, ldh=ldh, ldy=ldy)
+    _check(N.lib().moe_norm_forward(ctypes.byref(n), _ptr(x), _ptr(residual), _ptr(gamma), _ptr(beta),
+                                    _ptr(h), _ptr(out), _ptr(mean), _ptr(rstd), _stream(stream)),
+           "moe_norm_forward")
+    return out, (x if h is None else h), mean, rstd
+
+
+def layer_norm_workspace(T, M, dtype=torch.bfloat16, device="cuda"):
+    """A zero-filled workspace for layer_norm_backward on [T, M] matrices."""
+    n = N.MoeNorm(rows=T, cols=M, dtype=_DTYPES[dtype], eps=0.0, ldx=M, ldr=M, ldh=M, ldy=M)
+    b = N.c_size_t()
+    _check(N.lib().moe_norm_workspace_bytes(ctypes.byref(n), ctypes.byref(b)), "moe_norm_workspace_bytes")
+    return torch.zeros(b.value, dtype=torch.uint8, device=device)
+
+
+def layer_norm_backward(dy, h, gamma, mean, rstd, dh=None, *, need_beta=True, dx=None, dgamma=None,
+                        dbeta=None, ws=None, stream=None):
+    """(dx, dgamma, dbeta) of layer_norm from the gradient dy of y and, when given, the gradient
+    dh that reaches h on its other path; dx is the gradient of x and of the residual alike.
+    dbeta is None unless need_beta."""
+    w = "layer_norm_backward"
+    ldy = _matrix(dy, "dy", w)
+    T, M = dy.shape
+    dev, dt = dy.device, dy.dtype
+    ldx = _matrix(h, "h", w, T, M, dt, dev)
+    ldr = M if dh is None else _matrix(dh, "dh", w, T, M, dt, dev)
+    _vector(gamma, "gamma", w, M, dev)
+    _vector(mean, "mean", w, T, dev)
+    _vector(rstd, "rstd", w, T, dev)
+    with _on(stream):
+        if dx is None:
+            dx = torch.empty((T, M), dtype=dt, device=dev)
+        if dgamma is None:
+            dgamma = torch.empty(M, dtype=torch.float32, device=dev)
+        if need_beta and dbeta is None:
+            dbeta = torch.empty(M, dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = layer_norm_workspace(T, M, dt, dev)
+    ldh = _matrix(dx, "dx", w, T, M, dt, dev)
+    _vector(dgamma, "dgamma", w, M, dev)
+    if dbeta is not None:
+        _vector(dbeta, "dbeta", w, M, dev)
+    _workspace_ok(ws, w, dev)
+    n = N.MoeNorm(rows=T, cols=M, dtype=_DTYPES[dt], eps=0.0, ldx=ldx, ldr=ldr, ldh=ldh, ldy=ldy)
+    _check(N.lib().moe_norm_backward(ctypes.byref(n), _ptr(dy), _ptr(h), _ptr(gamma), _ptr(mean),
+                                     _ptr(rstd), _ptr(dh), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
+                                     _ptr(ws), ws.numel(), _stream(stream)), "moe_norm_backward")
+    return dx, dgamma, dbeta
+
+
+# ------------------------------------------------------------------ linear layer
+def linear_workspace(T, N_out, K, dtype=torch.bfloat16, device="cuda", *, backward=True, aligned=False):
+    """A zero-filled workspace for linear (and linear_backward, unless backward is False) with
+    x [T, K] and W [N_out, K]. aligned: every matrix starts on a 16-byte boundary and has rows
+    of a multiple of 16 bytes, so that no room is needed for copies of them."""
+    p = N.MoeLinear(T=T, N=N_out, K=K, act=N.LIN_ACTS["silu"], dtype=_DTYPES[dtype])
+    b = N.c_size_t()
+    _check(N.lib().moe_linear_workspace_bytes(ctypes.byref(p), int(bool(backward)), int(not aligned),
+                                              ctypes.byref(b)), "moe_linear_workspace_bytes")
+    return torch.zeros(b.value, dtype=torch.uint8, device=device)
+
+
+def linear(x, W, bias=None, *, act="none", residual=None, save_pre=False, out=None, pre=None, ws=None,
+           stream=None):
+    """(y, pre): y = act(x W^T + bias) + residual for x [T, K], W [N, K], bias float32 [N],
+    residual [T, N]; pre = x W^T + bias is stored when save_pre (or a buffer for it) is given,
+    for linear_backward, and None otherwise. act: "none", "relu", "gelu", "gelu_tanh", "silu".
+    """
+    w = "linear"
+    if act not in N.LIN_ACTS:
+        raise ValueError(f"{w}: act must be one of {sorted(N.LIN_ACTS)}, not {act!r}")
+    ldx = _matrix(x, "x", w)
+    T, K = x.shape
+    dev, dt = x.device, x.dtype
+    ldw = _matrix(W, "W", w, None, K, dt, dev)
+    n_out = W.shape[0]
+    if n_out < 1:
+        raise ValueError(f"{w}: W has no rows")
+    if bias is not None:
+        _vector(bias, "bias", w, n_out, dev)
+    ldr = n_out if residual is None else _matrix(residual, "residual", w, T, n_out, dt, dev)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((T, n_out), dtype=dt, device=dev)
+        if save_pre and pre is None:
+            pre = torch.empty((T, n_out), dtype=dt, device=dev)
+        if ws is None:
+            ws = linear_workspace(T, n_out, K, dt, dev, backward=False)
+    ldy = _matrix(out, "out", w, T, n_out, dt, dev)
+    ldp = n_out if pre is None else _matrix(pre, "pre", w, T, n_out, dt, dev)
+    _workspace_ok(ws, w, dev)
+    p = N.MoeLinear(T=T, N=n_out, K=K, act=N.LIN_ACTS[act], dtype=_DTYPES[dt], ldx=ldx, ldw=ldw, ldy=ldy,
+                    ldr=ldr, ldp=ldp)
+    _check(N.lib().moe_linear_forward(ctypes.byref(p), _ptr(x), _ptr(W), _ptr(bias), _ptr(residual),
+                                      _ptr(out), _ptr(pre), _ptr(ws), ws.numel(), _stream(stream)),
+           "moe_linear_forward")
+    return out, pre
+
+
+def linear_backward(dy, x, W, *, act="none", pre=None, need_x=True, need_W=True, need_bias=True, dx=None,
+                    dW=None, dbias=None, ws=None, stream=None):
+    """(dx, dW, dbias) of linear from dy [T, N] and the stored pre (not needed for act "none");
+    dx and dW in the element type, dbias float32; None for what is not needed. The gradient
+    of the residual is dy itself."""
+    w = "linear_backward"
+    if act not in N.LIN_ACTS:
+        raise ValueError(f"{w}: act must be one of {sorted(N.LIN_ACTS)}, not {act!r}")
+    ldy = _matrix(dy, "dy", w)
+    T, n_out = dy.shape
+    dev, dt = dy.device, dy.dtype
+    ldx = _matrix(x, "x", w, T, None, dt, dev)
+    K = x.shape[1]
+    ldw = _matrix(W, "W", w, n_out, K, dt, dev)
+    if act != "none" and pre is None:
+        raise ValueError(f"{w}: act {act!r} needs the forward's pre")
+    ldp = n_out if pre is None else _matrix(pre, "pre", w, T, n_out, dt, dev)
+    with _on(stream):
+        if need_x and dx is None:
+            dx = torch.empty((T, K), dtype=dt, device=dev)
+        if need_W and dW is None:
+            dW = torch.empty((n_out, K), dtype=dt, device=dev)
+        if need_bias and dbias is None:
+            dbias = torch.empty(n_out, dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = linear_workspace(T, n_out, K, dt, dev)
+    lddx = K if dx is None else _matrix(dx, "dx", w, T, K, dt, dev)
+    lddw = K if dW is None else _matrix(dW, "dW", w, n_out, K, dt, dev)
+    if dbias is not None:
+        _vector(dbias, "dbias", w, n_out, dev)
+    _workspace_ok(ws, w, dev)
+    p = N.MoeLinear(T=T, N=n_out, K=K, act=N.LIN_ACTS[act], dtype=_DTYPES[dt], ldx=ldx, ldw=ldw, ldy=ldy,
+                    ldp=ldp, lddx=lddx, lddw=lddw)
+    _check(N.lib().moe_linear_backward(ctypes.byref(p), _ptr(dy), _ptr(x), _ptr(W), _ptr(pre), _ptr(dx),
+                                       _ptr(dW), _ptr(dbias), _ptr(ws), ws.numel(), _stream(stream)),
+           "moe_linear_backward")
+    return dx, dW, dbias
+
+
+# ------------------------------------------------------------------ blocks
+class MoeBlock:
+    """out = x + MoE(norm(x)): the pre-norm MoE half of a Transformer block, with the routing
+    by expert scores when `score` is given (see moe.make_score). weights: those of MoeLayer,
+    and "norm_gamma", "norm_beta" (float32 [M])."""
+
+    def __init__(self, cfg: dict, weights: dict, device="cuda", score=None, eps=1e-5):
+        self.layer = moe.MoeLayer(cfg, weights, device, score=score)
+        c, dev = self.layer.cfg, self.layer.device
+        vec = lambda n: weights[n].to(dev, torch.float32).contiguous()
+        self.gamma, self.beta, self.eps = vec("norm_gamma"), vec("norm_beta"), eps
+        dt = moe.torch_dtype(c)
+        self.n = torch.empty((c.S, c.M), dtype=dt, device=dev)
+        self.mean, self.rstd = torch.empty((2, c.S), dtype=torch.float32, device=dev).unbind(0)
+        self.y = torch.empty((c.S, c.M), dtype=dt, device=dev)
+
+    def forward(self, x, u=None, stream=None):
+        layer_norm(x, self.gamma, self.beta, self.eps, out=self.n, mean=self.mean, rstd=self.rstd,
+                   stream=stream)
+        return self.layer.forward(self.n, u, residual=x, stream=stream, out=self.y)
+
+    def enable_backward(self, weights: dict):
+        self.layer.enable_backward(weights)
+        c = self.layer.cfg
+        self.norm_ws = layer_norm_workspace(c.S, c.M, self.n.dtype, self.layer.device)
+
+    def backward(self, x, dy, aux_coef=0.0, z_coef=0.0, stream=None):
+        """(dx, dgamma, dbeta, grads) for the last forward on x; grads holds the layer's weight
+        gradients (its dx is the normalised input's)."""
+        g = self.layer.backward(self.n, dy, residual=False, aux_coef=aux_coef, z_coef=z_coef, stream=stream)
+        dx, dgamma, dbeta = layer_norm_backward(g.dx, x, self.gamma, self.mean, self.rstd, dh=dy,
+                                                ws=self.norm_ws, stream=stream)
+        return dx, dgamma, dbeta, g
+
+
+class DenseBlock:
+    """out = x + W2 act(W1 norm(x) + b1) + b2: the dense feed-forward half of the layers without
+    experts. weights: W1 [H, M], W2 [M, H] (the element type), b1, b2, norm_gamma, norm_beta
+    (float32)."""
+
+    def __init__(self, T: int, weights: dict, act="gelu", dtype=torch.bfloat16, device="cuda", eps=1e-5):
+        dev = torch.device(device)
+        mat = lambda n: weights[n].to(device=dev, dtype=dtype).contiguous()
+        vec = lambda n: weights[n].to(dev, torch.float32).contiguous()
+        self.W1, self.W2, self.b1, self.b2 = mat("W1"), mat("W2"), vec("b1"), vec("b2")
+        self.gamma, self.beta, self.act, self.eps = vec("norm_gamma"), vec("norm_beta"), act, eps
+        H, M = self.W1.shape
+        new = lambda *s: torch.empty(s, dtype=dtype, device=dev)
+        self.n, self.pre, self.a, self.y = new(T, M), new(T, H), new(T, H), new(T, M)
+        self.mean, self.rstd = torch.empty((2, T), dtype=torch.float32, device=dev).unbind(0)
+        self.ws1 = linear_workspace(T, H, M, dtype, dev)
+        self.ws2 = linear_workspace(T, M, H, dtype, dev)
+        self.norm_ws = layer_norm_workspace(T, M, dtype, dev)
+
+    def forward(self, x, stream=None):
+        layer_norm(x, self.gamma, self.beta, self.eps, out=self.n, mean=self.mean, rstd=self.rstd,
+                   stream=stream)
+        linear(self.n, self.W1, self.b1, act=self.act, out=self.a, pre=self.pre, ws=self.ws1, stream=stream)
+        return linear(self.a, self.W2, self.b2, residual=x, out=self.y, ws=self.ws2, stream=stream)[0]
+
+    def backward(self, x, dy, stream=None):
+        """The gradients of the last forward on x: a dict of dx, W1, b1, W2, b2, norm_gamma and
+        norm_beta's."""
+        da, dW2, db2 = linear_backward(dy, self.a, self.W2, ws=self.ws2, stream=stream)
+        dn, dW1, db1 = linear_backward(da, self.n, self.W1, act=self.act, pre=self.pre, ws=self.ws1,
+                                       stream=stream)
+        dx, dgamma, dbeta = layer_norm_backward(dn, x, self.gamma, self.mean, self.rstd, dh=dy,
+                                                ws=self.norm_ws, stream=stream)
+        return dict(dx=dx, W1=dW1, b1=db1, W2=dW2, b2=db2, norm_gamma=dgamma, norm_beta=dbeta)

@@ -107,6 +107,18 @@ int prepare(const moe_config_t* cfg, Prep* p) {
   return MOE_OK;
 }
 
+// prepare for the scored routing: it defines its own selection and weights
+int prepare_scored(const moe_config_t* cfg, const moe_score_t* s, Prep* p) {
+  const int rc = prepare(cfg, p);
+  if (rc != MOE_OK) return rc;
+  if (!s || (s->score != MOE_SCORE_SIGMOID && s->score != MOE_SCORE_SOFTMAX)) return MOE_ERR_INVALID_ARG;
+  if (s->group_top < 1 || s->group_top > 2 || (s->renorm != 0 && s->renorm != 1) || !isfinite(s->scale))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->random_routing || cfg->uniform_assignment || cfg->gate_norm != MOE_GATE_SOFTMAX_TOPK)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 unsigned* status_of(void* ws, const WsLayout& L) {
   return reinterpret_cast<unsigned*>(static_cast<char*>(ws) + L.status);
 }
@@ -395,13 +407,15 @@ int moe_combine(const moe_config_t* cfg, const void* y_perm, const moe_route_out
   return launch_combine(*cfg, y_perm, r->row, shared_out, residual, y, p.R_max, stream);
 }
 
-int moe_layer_forward(const moe_config_t* cfg, const void* x, const void* W_g, const float* bias,
-                      const void* W_in_packed, const void* W_out_packed, const void* Ws_in_packed,
-                      const void* Ws_out_packed, const float* u, const void* residual, void* y,
-                      float* logits_out, const moe_route_out_t* r, void* ws, size_t ws_bytes,
-                      moe_stream_t stream) {
+// moe_layer_forward, or with a score moe_layer_forward_scored
+static int layer_forward(const moe_config_t* cfg, const moe_score_t* score, const float* select_bias,
+                         const void* x, const void* W_g, const float* bias, const void* W_in_packed,
+                         const void* W_out_packed, const void* Ws_in_packed,
+                         const void* Ws_out_packed, const float* u, const void* residual, void* y,
+                         float* logits_out, const moe_route_out_t* r, void* ws, size_t ws_bytes,
+                         moe_stream_t stream) {
   Prep p;
-  int rc = prepare(cfg, &p);
+  int rc = score ? prepare_scored(cfg, score, &p) : prepare(cfg, &p);
   if (rc != MOE_OK) return rc;
   if (!x || !W_g || !W_in_packed || !W_out_packed || !y) return MOE_ERR_INVALID_ARG;
   if (cfg->n_shared > 0 && (!Ws_in_packed || !Ws_out_packed)) return MOE_ERR_INVALID_ARG;
@@ -413,7 +427,7 @@ int moe_layer_forward(const moe_config_t* cfg, const void* x, const void* W_g, c
   void* h_perm = w + p.L.h_perm;
   void* y_perm = w + p.L.y_perm;
   void* shared_out = cfg->n_shared > 0 ? static_cast<void*>(w + p.L.s_out) : nullptr;
-  if (cfg->dtype == MOE_F32 && !logits) logits = reinterpret_cast<float*>(w + p.L.logits);
+  if ((cfg->dtype == MOE_F32 || score) && !logits) logits = reinterpret_cast<float*>(w + p.L.logits);
   // routing's last kernel also writes x_perm, and brings GEMM 1's first wave of weight
   // tiles (one BN x M tile per CTA pair, at most 40 MB) into L2 while the routing finishes
   DispatchFuse fuse{x, x_perm, nullptr, 0, nullptr, 0};
@@ -428,8 +442,13 @@ int moe_layer_forward(const moe_config_t* cfg, const void* x, const void* W_g, c
     fuse.prefetch = W_in_packed;
     fuse.prefetch_bytes = pf;
   }
-  if ((rc = router_route(cfg, x, W_g, bias, u, logits, r, ws, ws_bytes, &fuse, stream)) != MOE_OK)
-    return rc;
+  if (score) {
+    if ((rc = moe_router(cfg, x, W_g, bias, logits, ws, ws_bytes, stream)) != MOE_OK) return rc;
+    rc = launch_route_scored(*cfg, *score, p.C, logits, select_bias, *r, w, p.L, stream, &fuse);
+  } else {
+    rc = router_route(cfg, x, W_g, bias, u, logits, r, ws, ws_bytes, &fuse, stream);
+  }
+  if (rc != MOE_OK) return rc;
   if ((rc = moe_expert_ffn(cfg, x_perm, r->expert_offsets, r->w_perm, W_in_packed, W_out_packed,
                            h_perm, y_perm, ws, ws_bytes, stream)) != MOE_OK)
     return rc;
@@ -438,6 +457,53 @@ int moe_layer_forward(const moe_config_t* cfg, const void* x, const void* W_g, c
                            ws_bytes, stream)) != MOE_OK)
     return rc;
   return moe_combine(cfg, y_perm, r, shared_out, residual, y, stream);
+}
+
+int moe_layer_forward(const moe_config_t* cfg, const void* x, const void* W_g, const float* bias,
+                      const void* W_in_packed, const void* W_out_packed, const void* Ws_in_packed,
+                      const void* Ws_out_packed, const float* u, const void* residual, void* y,
+                      float* logits_out, const moe_route_out_t* r, void* ws, size_t ws_bytes,
+                      moe_stream_t stream) {
+  return layer_forward(cfg, nullptr, nullptr, x, W_g, bias, W_in_packed, W_out_packed, Ws_in_packed,
+                       Ws_out_packed, u, residual, y, logits_out, r, ws, ws_bytes, stream);
+}
+
+int moe_layer_forward_scored(const moe_config_t* cfg, const moe_score_t* score, const void* x,
+                             const void* W_g, const float* bias, const float* select_bias,
+                             const void* W_in_packed, const void* W_out_packed,
+                             const void* Ws_in_packed, const void* Ws_out_packed,
+                             const void* residual, void* y, float* logits_out,
+                             const moe_route_out_t* r, void* ws, size_t ws_bytes,
+                             moe_stream_t stream) {
+  if (!score) return MOE_ERR_INVALID_ARG;
+  return layer_forward(cfg, score, select_bias, x, W_g, bias, W_in_packed, W_out_packed,
+                       Ws_in_packed, Ws_out_packed, nullptr, residual, y, logits_out, r, ws,
+                       ws_bytes, stream);
+}
+
+int moe_route_scored(const moe_config_t* cfg, const moe_score_t* score, const float* logits,
+                     const float* select_bias, const moe_route_out_t* out, void* ws,
+                     size_t ws_bytes, moe_stream_t stream) {
+  Prep p;
+  int rc = prepare_scored(cfg, score, &p);
+  if (rc != MOE_OK) return rc;
+  if (!logits) return MOE_ERR_INVALID_ARG;
+  if ((rc = check_route_out(*cfg, out)) != MOE_OK) return rc;
+  if ((rc = check_ws(ws, ws_bytes, p.L.step_bytes)) != MOE_OK) return rc;
+  return launch_route_scored(*cfg, *score, p.C, logits, select_bias, *out, static_cast<char*>(ws), p.L,
+                             stream);
+}
+
+int moe_route_scored_backward(const moe_config_t* cfg, const moe_score_t* score,
+                              const float* logits, const moe_route_out_t* r, const float* dgate,
+                              float aux_coef, float z_coef, float* dlogits, moe_stream_t stream) {
+  Prep p;
+  const int rc = prepare_scored(cfg, score, &p);
+  if (rc != MOE_OK) return rc;
+  if (!logits || !r || !r->expert_id || !r->row || !r->counts_routed || !dgate || !dlogits)
+    return MOE_ERR_INVALID_ARG;
+  return launch_route_scored_backward(*cfg, *score, logits, *r, dgate, nullptr, 0, aux_coef, z_coef,
+                                      dlogits, nullptr, 0, stream);
 }
 
 int moe_pack_weights_backward(const moe_config_t* cfg, const void* W_in, const void* W_up,
@@ -558,7 +624,8 @@ int layer_backward_f32(const moe_config_t& c, const Prep& p, const void* x, cons
                        const void* Wst_in_packed, const void* Wst_out_packed, const float* logits,
                        const moe_route_out_t& r, const char* fw, char* w, const WsLayoutBwd& B,
                        const RouterBwdBufs& rb, int residual, float aux_coef, float z_coef,
-                       const moe_grads_t& grads, unsigned* status, cudaStream_t stream) {
+                       const moe_grads_t& grads, unsigned* status, const moe_score_t* score,
+                       cudaStream_t stream) {
   const bool sw = c.act == MOE_ACT_SWIGLU;
   const int64_t R = p.R_max;
   const int F = sw ? 2 * c.H : c.H;
@@ -587,7 +654,7 @@ int layer_backward_f32(const moe_config_t& c, const Prep& p, const void* x, cons
   // the router: dlogits from the gates' gradients, aux and z; then dx, dW_g, dbias
   if ((rc = launch_router_backward(c, logits, r, reinterpret_cast<const float*>(w + B.gpart),
                                    B.n_tiles2, aux_coef, z_coef, rb, x, W_g, grads.dW_g,
-                                   grads.dbias, status, stream)) != MOE_OK)
+                                   grads.dbias, status, stream, score)) != MOE_OK)
     return rc;
   // shared experts: one dense segment of all S tokens, weight 1
   void* dxs = nullptr;
@@ -616,15 +683,17 @@ int layer_backward_f32(const moe_config_t& c, const Prep& p, const void* x, cons
                         rb.dx_r);
 }
 
-int moe_layer_backward(const moe_config_t* cfg, const void* x, const void* dy, const void* W_g,
-                       const void* W_in_packed, const void* Wt_in_packed, const void* Wt_out_packed,
-                       const void* Ws_in_packed, const void* Wst_in_packed,
-                       const void* Wst_out_packed, const float* logits, const moe_route_out_t* r,
-                       const void* fwd_ws, size_t fwd_ws_bytes, int residual, float aux_coef,
-                       float z_coef, const moe_grads_t* grads, void* ws, size_t ws_bytes,
-                       moe_stream_t stream) {
+// moe_layer_backward, or with a score moe_layer_backward_scored
+static int layer_backward(const moe_config_t* cfg, const moe_score_t* score, const void* x,
+                          const void* dy, const void* W_g, const void* W_in_packed,
+                          const void* Wt_in_packed, const void* Wt_out_packed,
+                          const void* Ws_in_packed, const void* Wst_in_packed,
+                          const void* Wst_out_packed, const float* logits, const moe_route_out_t* r,
+                          const void* fwd_ws, size_t fwd_ws_bytes, int residual, float aux_coef,
+                          float z_coef, const moe_grads_t* grads, void* ws, size_t ws_bytes,
+                          moe_stream_t stream) {
   Prep p;
-  int rc = prepare(cfg, &p);
+  int rc = score ? prepare_scored(cfg, score, &p) : prepare(cfg, &p);
   if (rc != MOE_OK) return rc;
   const moe_config_t& c = *cfg;
   if (c.uniform_assignment) return MOE_ERR_UNSUPPORTED;
@@ -662,7 +731,7 @@ int moe_layer_backward(const moe_config_t* cfg, const void* x, const void* dy, c
   if (c.dtype == MOE_F32)
     return layer_backward_f32(c, p, x, dy, W_g, W_in_packed, Wt_in_packed, Wt_out_packed,
                               Ws_in_packed, Wst_in_packed, Wst_out_packed, logits, *r, fw, w, B,
-                              rb, residual, aux_coef, z_coef, *grads, status, stream);
+                              rb, residual, aux_coef, z_coef, *grads, status, score, stream);
 
   // routed experts: data gradients (tcgen05 GEMMs over the expert segments)
   if ((rc = launch_dispatch(c, R, dy, r->token_of, r->expert_offsets, w + B.dy_perm, stream)) != MOE_OK)
@@ -705,7 +774,7 @@ int moe_layer_backward(const moe_config_t* cfg, const void* x, const void* dy, c
   // the router: dlogits from the gates' gradients, aux and z; then dx, dW_g (tcgen05), dbias
   if ((rc = launch_router_backward(c, logits, *r, reinterpret_cast<const float*>(w + B.gpart),
                                    B.n_tiles2, aux_coef, z_coef, rb, x, W_g, grads->dW_g,
-                                   grads->dbias, status, stream)) != MOE_OK)
+                                   grads->dbias, status, stream, score)) != MOE_OK)
     return rc;
   // shared experts: one dense segment of all S tokens, weight 1
   void* dxs = nullptr;
@@ -728,6 +797,32 @@ int moe_layer_backward(const moe_config_t* cfg, const void* x, const void* dy, c
   // dx = sum over kept choices of the rows' gradients (+ shared) (+ dy) + the router's
   return launch_combine(c, w + B.dx_perm, r->row, dxs, residual ? dy : nullptr, grads->dx, R,
                         stream, reinterpret_cast<const float*>(w + B.dx_r));
+}
+
+int moe_layer_backward(const moe_config_t* cfg, const void* x, const void* dy, const void* W_g,
+                       const void* W_in_packed, const void* Wt_in_packed, const void* Wt_out_packed,
+                       const void* Ws_in_packed, const void* Wst_in_packed,
+                       const void* Wst_out_packed, const float* logits, const moe_route_out_t* r,
+                       const void* fwd_ws, size_t fwd_ws_bytes, int residual, float aux_coef,
+                       float z_coef, const moe_grads_t* grads, void* ws, size_t ws_bytes,
+                       moe_stream_t stream) {
+  return layer_backward(cfg, nullptr, x, dy, W_g, W_in_packed, Wt_in_packed, Wt_out_packed,
+                        Ws_in_packed, Wst_in_packed, Wst_out_packed, logits, r, fwd_ws, fwd_ws_bytes,
+                        residual, aux_coef, z_coef, grads, ws, ws_bytes, stream);
+}
+
+int moe_layer_backward_scored(const moe_config_t* cfg, const moe_score_t* score, const void* x,
+                              const void* dy, const void* W_g, const void* W_in_packed,
+                              const void* Wt_in_packed, const void* Wt_out_packed,
+                              const void* Ws_in_packed, const void* Wst_in_packed,
+                              const void* Wst_out_packed, const float* logits,
+                              const moe_route_out_t* r, const void* fwd_ws, size_t fwd_ws_bytes,
+                              int residual, float aux_coef, float z_coef, const moe_grads_t* grads,
+                              void* ws, size_t ws_bytes, moe_stream_t stream) {
+  if (!score) return MOE_ERR_INVALID_ARG;
+  return layer_backward(cfg, score, x, dy, W_g, W_in_packed, Wt_in_packed, Wt_out_packed,
+                        Ws_in_packed, Wst_in_packed, Wst_out_packed, logits, r, fwd_ws, fwd_ws_bytes,
+                        residual, aux_coef, z_coef, grads, ws, ws_bytes, stream);
 }
 
 int moe_set_wait_limit(void* ws, uint64_t limit_ns, moe_stream_t stream) {

@@ -480,12 +480,16 @@ int router_dbias(const moe_config_t& c, const RouterBwdBufs& b, float* dbias, cu
 int launch_router_backward(const moe_config_t& c, const float* logits, const moe_route_out_t& r,
                            const float* gpart, int n_tiles, float aux_coef, float z_coef,
                            const RouterBwdBufs& b, const void* x, const void* W_g, float* dW_g,
-                           float* dbias, unsigned* status, cudaStream_t st) {
+                           float* dbias, unsigned* status, cudaStream_t st,
+                           const moe_score_t* score) {
   if (c.E > 256) return MOE_ERR_UNSUPPORTED;
   const int Ep = (c.E + 63) / 64 * 64;
   const unsigned blocks = unsigned((int64_t(c.S) * 32 + 255) / 256);
   int rc;
-  if (c.k <= 2)
+  if (score)
+    rc = launch_route_scored_backward(c, *score, logits, r, nullptr, gpart, n_tiles, aux_coef, z_coef,
+                                      b.dlogits, b.dlb, Ep, st);
+  else if (c.k <= 2)
     rc = launch_kernel(router_bwd_kernel<2>, dim3(blocks), dim3(256), 0, st, logits, r.expert_id, r.row,
                        gpart, n_tiles, r.counts_routed, c.S, c.G, c.E, c.k, c.gate_norm, c.gate_p, aux_coef,
                        z_coef, b.dlogits, static_cast<__nv_bfloat16*>(b.dlb), Ep);

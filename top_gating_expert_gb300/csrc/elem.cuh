@@ -1,0 +1,33 @@
+// Loads and stores of the two element types (float, bf16) as fp32, shared by the norm and
+// linear kernels.
+#pragma once
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace moe {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Sum over the block of NW warps of one float per thread, valid in every thread; the order
+// is a fixed tree. s_red: NW floats that no thread uses until the next barrier.
+template <int NW>
+__device__ __forceinline__ float block_sum_all(float v, float* s_red) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if constexpr (NW == 1) return v;
+  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float r = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) r += s_red[w];
+  return r;
+}
+
+}  // namespace moe

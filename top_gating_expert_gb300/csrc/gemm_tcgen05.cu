@@ -636,19 +636,6 @@ __device__ __forceinline__ void epilogue_f32_tma(const KParams& p, const CUtenso
   }
 }
 
-// Shared-memory descriptor of an MN-major operand staged as 64-column TMA boxes (128-byte
-// rows, one K index a row, 128-byte swizzle): the swizzle atom is 8 K rows of 64 MN
-// elements; atoms follow each other along K every 1024 bytes (stride offset) and along MN
-// every 8 KB, the next box (leading offset).
-__device__ __forceinline__ uint64_t mn_sw128_desc(uint32_t saddr) {
-  uint64_t d = uint64_t((saddr & 0x3FFFFu) >> 4);
-  d |= uint64_t(8192 >> 4) << 16;  // leading-dimension offset: next 64 MN elements
-  d |= uint64_t(1024 >> 4) << 32;  // stride-dimension offset: next 8 K rows
-  d |= uint64_t(1) << 46;
-  d |= uint64_t(2) << 61;
-  return d;
-}
-
 // ------------------------------------------------------------------ the kernel
 template <int BN, int EPI, bool PAIR, bool KRAG, bool MN = false>
 __global__ void __launch_bounds__(64 + 32 * epi_warps<EPI, KRAG>(), 1)
@@ -1549,6 +1536,22 @@ int run_wgrad_resident(const GemmDesc& d, cudaStream_t st) {
 }
 
 }  // namespace
+
+int make_tma_map_strided(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld,
+                         int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return MOE_ERR_CUDA;
+  if (reinterpret_cast<uintptr_t>(base) % 16 != 0 || ld % 8 != 0 || ld < cols || rows < 1 || cols < 1)
+    return MOE_ERR_INVALID_ARG;
+  cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+  cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+  cuuint32_t box[2] = {cuuint32_t(BK), cuuint32_t(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
 
 int make_tma_map_rows(CUtensorMap* m, const void* base, int64_t rows, int K, int box_rows) {
   return make_map(m, base, rows, K, box_rows);

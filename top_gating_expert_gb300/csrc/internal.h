@@ -177,6 +177,19 @@ int launch_router_route(const moe_config_t& c, int C, const void* x, const void*
                         const moe_route_out_t& out, char* ws, const WsLayout& L, cudaStream_t st,
                         const DispatchFuse* d = nullptr);
 
+// route_scored.cu: routing from expert scores and a selection bias, then launch_route's scan
+// and finalize kernels (select_bias nullable).
+int launch_route_scored(const moe_config_t& c, const moe_score_t& sc, int C, const float* logits,
+                        const float* select_bias, const moe_route_out_t& out, char* ws,
+                        const WsLayout& L, cudaStream_t st, const DispatchFuse* d = nullptr);
+// its gradient to the logits: the choices' gradients come from dgate [S, k], or (dgate null)
+// from the n_tiles partials gpart[row][n_tiles] of the kept choices. dlb (nullable): also
+// bf16 [S][Ep], zeros in columns E .. Ep - 1.
+int launch_route_scored_backward(const moe_config_t& c, const moe_score_t& sc, const float* logits,
+                                 const moe_route_out_t& r, const float* dgate, const float* gpart,
+                                 int n_tiles, float aux_coef, float z_coef, float* dlogits, void* dlb,
+                                 int Ep, cudaStream_t st);
+
 // permute.cu
 int launch_dispatch(const moe_config_t& c, int64_t R_max, const void* x, const int32_t* token_of,
                     const int32_t* offsets, void* x_perm, cudaStream_t st);
@@ -243,6 +256,10 @@ int launch_gemm_bf16(const GemmDesc& d, cudaStream_t st);
 // 2-D tensor map over a row-major bf16 [rows, K] matrix, boxes of 64 columns x box_rows rows,
 // 128-byte swizzle (the operand layout of the tcgen05 kernels).
 int make_tma_map_rows(CUtensorMap* m, const void* base, int64_t rows, int K, int box_rows);
+// the same over a [rows, cols] matrix with row stride ld (a multiple of 8 elements); columns
+// past cols and rows past rows read as zeros
+int make_tma_map_strided(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld,
+                         int box_rows);
 
 // simt_f32.cu : plain-FMA fp32 path for small layers.
 int launch_router_f32(const moe_config_t& c, const float* x, const float* W_g, const float* bias,
@@ -283,7 +300,8 @@ struct RouterBwdBufs {
 int launch_router_backward(const moe_config_t& c, const float* logits, const moe_route_out_t& r,
                            const float* gpart, int n_tiles, float aux_coef, float z_coef,
                            const RouterBwdBufs& b, const void* x, const void* W_g, float* dW_g,
-                           float* dbias, unsigned* status, cudaStream_t st);
+                           float* dbias, unsigned* status, cudaStream_t st,
+                           const moe_score_t* score = nullptr);  // null: the default routing
 
 // backward_f32.cu: the fp32 path's backward on plain FMA.
 // One expert FFN's data gradients on (ragged or dense) row segments, fp32 row-major: D =

@@ -1,0 +1,324 @@
+// The linear layer y = act(x W^T + bias) + residual and its backward: argument checks, the
+// workspace, the activation's derivative with the bias's gradient, and the copies of bf16
+// operands that TMA cannot read in place. The products are in linear_bf16.cu and
+// linear_f32.cu.
+#include <algorithm>
+
+#include "linear.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kColThreads = 32, kRowLanes = 8;
+
+template <typename T, int VEC>
+struct Vec {
+  T v[VEC];
+};
+template <typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> load_vec(const T* p) {
+  Vec<T, VEC> r;
+  if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<uint4*>(r.v) = *reinterpret_cast<const uint4*>(p);
+  else r.v[0] = *p;
+  return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T* p, const Vec<T, VEC>& r) {
+  if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(r.v);
+  else *p = r.v[0];
+}
+
+// d = dy act'(pre) (written to d when it is given) and the partial column sums of the
+// unrounded d over a slice of rows: part[slice][N]. CTA: 32 threads of VEC columns by 8 row
+// lanes; the lanes' sums are added in order.
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kColThreads * kRowLanes)
+    linear_dact_kernel(const T* __restrict__ dy, int64_t ldy, const T* __restrict__ pre, int64_t ldp,
+                       T* __restrict__ d, int64_t ldd, int rows, int N, int slice, float* __restrict__ part) {
+  __shared__ float s_sum[kRowLanes][kColThreads * VEC];
+  pdl_wait();
+  pdl_trigger();
+  const int cx = threadIdx.x % kColThreads, ry = threadIdx.x / kColThreads;
+  const int c = (blockIdx.x * kColThreads + cx) * VEC;
+  const int64_t r0 = int64_t(blockIdx.y) * slice, r1 = min(int64_t(rows), r0 + slice);
+  float acc[VEC];
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) acc[q] = 0.f;
+  if (c < N) {
+#pragma unroll 2
+    for (int64_t r = r0 + ry; r < r1; r += kRowLanes) {
+      const Vec<T, VEC> g = load_vec<T, VEC>(dy + r * ldy + c);
+      Vec<T, VEC> o, w;
+      if constexpr (ACT != MOE_LIN_NONE) w = load_vec<T, VEC>(pre + r * ldp + c);
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) {
+        float v = to_f32(g.v[q]);
+        if constexpr (ACT != MOE_LIN_NONE) v *= act_slope<ACT>(to_f32(w.v[q]));
+        acc[q] += v;
+        o.v[q] = from_f32<T>(v);
+      }
+      if (d) store_vec<T, VEC>(d + r * ldd + c, o);
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) s_sum[ry][cx * VEC + q] = acc[q];
+  __syncthreads();
+  for (int x = threadIdx.x; x < kColThreads * VEC; x += kColThreads * kRowLanes) {
+    const int cc = blockIdx.x * kColThreads * VEC + x;
+    if (cc >= N) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int l = 0; l < kRowLanes; ++l) s += s_sum[l][x];
+    part[int64_t(blockIdx.y) * N + cc] = s;
+  }
+}
+
+// out[c] = sum over the slices, in order, of part[s][c]
+__global__ void __launch_bounds__(256)
+    linear_dbias_kernel(const float* __restrict__ part, int slices, int N, float* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= N) return;
+  float s = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < slices; ++i) s += part[int64_t(i) * N + c];
+  out[c] = s;
+}
+
+// dst [rows][ldd] (16-byte rows) = src [rows][cols] of any alignment
+__global__ void __launch_bounds__(256)
+    linear_align_kernel(const __nv_bfloat16* __restrict__ src, int64_t ld, int64_t rows, int cols,
+                        __nv_bfloat16* __restrict__ dst, int64_t ldd) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t per = ldd / 8, n = rows * per;
+  for (int64_t x = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; x < n; x += int64_t(gridDim.x) * blockDim.x) {
+    const int64_t r = x / per;
+    const int c = int(x % per) * 8;
+    const __nv_bfloat16* s = src + r * ld + c;
+    Vec<__nv_bfloat16, 8> v;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v.v[q] = c + q < cols ? s[q] : __float2bfloat16_rn(0.f);
+    store_vec<__nv_bfloat16, 8>(dst + r * ldd + c, v);
+  }
+}
+
+int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
+
+// slices of the bias's gradient: about 1216 CTAs of 256 columns (eight an SM) at most
+int bias_slices(int T, int N) {
+  const int cblocks = (N + 255) / 256;
+  const int s = std::max(1, std::min(256, 1216 / cblocks));
+  return std::max(1, std::min(s, (T + kRowLanes - 1) / kRowLanes));
+}
+
+int check_linear(const moe_linear_t* p, moe_linear_t* q) {
+  if (!p || p->T < 0 || p->N < 1 || p->K < 1) return MOE_ERR_INVALID_ARG;
+  if (p->act < MOE_LIN_NONE || p->act > MOE_LIN_SILU) return MOE_ERR_INVALID_ARG;
+  if (p->dtype != MOE_F32 && p->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (p->T > (1 << 30) || p->N > (1 << 22) || p->K > (1 << 22)) return MOE_ERR_UNSUPPORTED;
+  *q = *p;
+  auto ld = [](int64_t& v, int64_t n) {
+    if (v == 0) v = n;
+    return v >= n;
+  };
+  if (!ld(q->ldx, p->K) || !ld(q->ldw, p->K) || !ld(q->ldy, p->N) || !ld(q->ldr, p->N) ||
+      !ld(q->ldp, p->N) || !ld(q->lddx, p->K) || !ld(q->lddw, p->K))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// Carves the workspace: regions in a fixed order, their total compared with what there is.
+struct Carver {
+  char* base;
+  size_t at = 256;
+  void* take(size_t bytes) {
+    void* p = base ? base + at : nullptr;
+    at = align256(at + bytes);
+    return p;
+  }
+};
+
+size_t ws_need(const moe_linear_t& p, bool backward, bool all) {
+  Carver c{nullptr};
+  const int64_t Kp = up8(p.K), Np = up8(p.N);
+  if (p.dtype == MOE_F32) {
+    c.take(kPartBytes);
+    if (backward && p.act != MOE_LIN_NONE) c.take(size_t(p.T) * Np * 4);
+  } else {
+    if (all || p.ldx % 8) c.take(size_t(p.T) * Kp * 2);
+    if (all || p.ldw % 8) c.take(size_t(p.N) * Kp * 2);
+    if (backward && (all || p.act != MOE_LIN_NONE || p.ldy % 8)) c.take(size_t(p.T) * Np * 2);
+  }
+  if (backward) c.take(size_t(bias_slices(p.T, p.N)) * p.N * 4);
+  return c.at;
+}
+
+bool in_place(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
+
+// The operand [rows, cols] as TMA can read it: in place, or copied to 16-byte rows.
+int align_operand(const void* src, int64_t ld, int64_t rows, int cols, Carver& c, size_t ws_bytes,
+                  const void** out, int64_t* ldo, bool launch, cudaStream_t st) {
+  *out = src;
+  *ldo = ld;
+  if (in_place(src, ld)) return MOE_OK;
+  *ldo = up8(cols);
+  void* dst = c.take(size_t(rows) * *ldo * 2);
+  *out = dst;
+  if (c.at > ws_bytes) return MOE_ERR_WORKSPACE;
+  if (!launch) return MOE_OK;
+  const int64_t n = rows * (*ldo / 8);
+  return launch_kernel(linear_align_kernel, dim3(unsigned(std::min<int64_t>((n + 255) / 256, 16 * num_sms()))),
+                       dim3(256), 0, st, static_cast<const __nv_bfloat16*>(src), ld, rows, cols,
+                       static_cast<__nv_bfloat16*>(dst), *ldo);
+}
+
+template <typename T>
+int launch_dact(const moe_linear_t& p, const void* dy, const void* pre, void* d, int64_t ldd, float* part,
+                cudaStream_t st) {
+  constexpr int V = 16 / int(sizeof(T));
+  auto ok = [](const void* q, int64_t ld) {
+    return !q || (reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % V == 0);
+  };
+  const bool vec = p.N % V == 0 && ok(dy, p.ldy) && ok(pre, p.ldp) && ok(d, ldd);
+  const int slices = bias_slices(p.T, p.N), slice = (p.T + slices - 1) / slices;
+  return with_act(p.act, [&](auto tag) {
+    constexpr int ACT = decltype(tag)::value;
+    const int cols = kColThreads * (vec ? V : 1);
+    auto kern = vec ? linear_dact_kernel<T, V, ACT> : linear_dact_kernel<T, 1, ACT>;
+    return launch_kernel(kern, dim3(unsigned((p.N + cols - 1) / cols), unsigned(slices)),
+                         dim3(kColThreads * kRowLanes), 0, st, static_cast<const T*>(dy), p.ldy,
+                         static_cast<const T*>(pre), p.ldp, static_cast<T*>(d), ldd, p.T, p.N, slice, part);
+  });
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_linear_workspace_bytes(const moe_linear_t* p, int backward, int unaligned, size_t* bytes) {
+  moe_linear_t q;
+  const int rc = check_linear(p, &q);
+  if (rc != MOE_OK) return rc;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = ws_need(q, backward != 0, unaligned != 0);
+  return MOE_OK;
+}
+
+int moe_linear_forward(const moe_linear_t* p, const void* x, const void* W, const float* bias,
+                       const void* residual, void* y, void* pre, void* ws, size_t ws_bytes,
+                       moe_stream_t stream) {
+  moe_linear_t q;
+  int rc = check_linear(p, &q);
+  if (rc != MOE_OK) return rc;
+  if (q.T == 0) return MOE_OK;
+  if (!x || !W || !y || (pre && pre == y)) return MOE_ERR_INVALID_ARG;
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < ws_need(q, false, false))
+    return MOE_ERR_WORKSPACE;
+  LinearEpi e;
+  e.bias = bias; e.res = residual; e.out = y; e.pre = pre;
+  e.ldo = q.ldy; e.ldr = q.ldr; e.ldp = q.ldp;
+  e.act = q.act;
+  Carver c{static_cast<char*>(ws)};
+  if (q.dtype == MOE_F32) {
+    float* part = static_cast<float*>(c.take(kPartBytes));
+    return launch_linear_f32(static_cast<const float*>(x), q.ldx, 1, static_cast<const float*>(W), q.ldw,
+                             1, q.T, q.N, q.K, e, part, stream);
+  }
+  LinearOperand a{nullptr, 0, false}, b{nullptr, 0, false};
+  for (int launch = 0; launch < 2; ++launch) {  // room first: nothing is launched without it
+    c.at = 256;
+    if ((rc = align_operand(x, q.ldx, q.T, q.K, c, ws_bytes, &a.p, &a.ld, launch, stream)) != MOE_OK ||
+        (rc = align_operand(W, q.ldw, q.N, q.K, c, ws_bytes, &b.p, &b.ld, launch, stream)) != MOE_OK)
+      return rc;
+  }
+  return launch_linear_bf16(a, b, q.T, q.N, q.K, e, static_cast<unsigned*>(ws), stream);
+}
+
+int moe_linear_backward(const moe_linear_t* p, const void* dy, const void* x, const void* W,
+                        const void* pre, void* dx, void* dW, float* dbias, void* ws,
+                        size_t ws_bytes, moe_stream_t stream) {
+  moe_linear_t q;
+  int rc = check_linear(p, &q);
+  if (rc != MOE_OK) return rc;
+  const size_t eb = q.dtype == MOE_BF16 ? 2 : 4;
+  if (q.T == 0) {
+    if (dW) MOE_CUDA_CHECK(cudaMemset2DAsync(dW, size_t(q.lddw) * eb, 0, size_t(q.K) * eb, size_t(q.N), stream));
+    if (dbias) MOE_CUDA_CHECK(cudaMemsetAsync(dbias, 0, size_t(q.N) * 4, stream));
+    return MOE_OK;
+  }
+  if (!dy || (dx && !W) || (dW && !x) || (q.act != MOE_LIN_NONE && !pre)) return MOE_ERR_INVALID_ARG;
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < ws_need(q, true, false))
+    return MOE_ERR_WORKSPACE;
+  if (q.act == MOE_LIN_NONE) pre = nullptr;
+  const int64_t Np = up8(q.N);
+  Carver c{static_cast<char*>(ws)};
+  if (q.dtype == MOE_F32) {
+    float* part = static_cast<float*>(c.take(kPartBytes));
+    void* d = pre ? c.take(size_t(q.T) * Np * 4) : nullptr;
+    float* dbp = static_cast<float*>(c.take(size_t(bias_slices(q.T, q.N)) * q.N * 4));
+    if ((pre || dbias) &&
+        (rc = launch_dact<float>(q, dy, pre, d, Np, dbias ? dbp : nullptr, stream)) != MOE_OK)
+      return rc;
+    if (dbias && (rc = launch_kernel(linear_dbias_kernel, dim3(unsigned((q.N + 255) / 256)), dim3(256), 0,
+                                     stream, static_cast<const float*>(dbp), bias_slices(q.T, q.N), q.N,
+                                     dbias)) != MOE_OK)
+      return rc;
+    const float* df = static_cast<const float*>(pre ? d : dy);
+    const int64_t ldd = pre ? Np : q.ldy;
+    LinearEpi e;
+    if (dx) {
+      e.out = dx; e.ldo = q.lddx;
+      if ((rc = launch_linear_f32(df, ldd, 1, static_cast<const float*>(W), 1, q.ldw, q.T, q.K, q.N, e,
+                                  part, stream)) != MOE_OK)
+        return rc;
+    }
+    if (dW) {
+      e.out = dW; e.ldo = q.lddw;
+      return launch_linear_f32(df, 1, ldd, static_cast<const float*>(x), 1, q.ldx, q.N, q.K, q.T, e, part,
+                               stream);
+    }
+    return MOE_OK;
+  }
+  const bool make_d = pre || !in_place(dy, q.ldy);  // d written out: the products' operand
+  LinearOperand xo{nullptr, 0, true}, wo{nullptr, 0, true};
+  void* d = nullptr;
+  float* dbp = nullptr;
+  for (int launch = 0; launch < 2; ++launch) {
+    c.at = 256;
+    if (dW && (rc = align_operand(x, q.ldx, q.T, q.K, c, ws_bytes, &xo.p, &xo.ld, launch, stream)) != MOE_OK)
+      return rc;
+    if (dx && (rc = align_operand(W, q.ldw, q.N, q.K, c, ws_bytes, &wo.p, &wo.ld, launch, stream)) != MOE_OK)
+      return rc;
+    if (make_d) d = c.take(size_t(q.T) * Np * 2);
+    dbp = static_cast<float*>(c.take(size_t(bias_slices(q.T, q.N)) * q.N * 4));
+    if (c.at > ws_bytes) return MOE_ERR_WORKSPACE;
+  }
+  if ((make_d || dbias) &&
+      (rc = launch_dact<__nv_bfloat16>(q, dy, pre, d, Np, dbias ? dbp : nullptr, stream)) != MOE_OK)
+    return rc;
+  if (dbias && (rc = launch_kernel(linear_dbias_kernel, dim3(unsigned((q.N + 255) / 256)), dim3(256), 0,
+                                   stream, static_cast<const float*>(dbp), bias_slices(q.T, q.N), q.N,
+                                   dbias)) != MOE_OK)
+    return rc;
+  LinearOperand dk{make_d ? d : dy, make_d ? Np : q.ldy, false};
+  unsigned* status = static_cast<unsigned*>(ws);
+  LinearEpi e;
+  if (dx) {  // d W: W's rows run along the reduction, so it is read MN-major
+    e.out = dx; e.ldo = q.lddx;
+    if ((rc = launch_linear_bf16(dk, wo, q.T, q.K, q.N, e, status, stream)) != MOE_OK) return rc;
+  }
+  if (dW) {  // d^T x: both operands' rows run along the reduction
+    e.out = dW; e.ldo = q.lddw;
+    dk.mn = true;
+    return launch_linear_bf16(dk, xo, q.N, q.K, q.T, e, status, stream);
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

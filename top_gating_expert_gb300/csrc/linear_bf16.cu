@@ -1,0 +1,352 @@
+// The linear layer's products in bf16 on the 5th-generation tensor cores (tcgen05 + TMEM,
+// operands by TMA), fp32 accumulation, the epilogue applied to the fp32 sums:
+//
+//   out(i, j) = act(sum_k A(i, k) B(j, k) + bias[j]) + residual(i, j)
+//
+// for the forward (A = x, B = W), dx (A = d, B = W^T) and dW (A = d^T, B = x^T). Each operand
+// is K-major (its rows contiguous along k) or MN-major (contiguous along i or j): the MMA
+// reads either from the 128-byte-swizzled boxes that TMA writes, so nothing is transposed in
+// memory. Rows, columns and k past the ends read as zeros (TMA's fill), so every size runs on
+// the same path.
+//
+// linear_tile_kernel: one CTA per 128 x BN tile of D and per split of K.
+//   warp 0      TMA producer (a ring of `stages` stages of 64-wide k-blocks)
+//   warp 1      TMEM owner and MMA issuer
+//   warps 2..5  move the finished accumulator into shared memory (over the drained ring)
+//   all warps   epilogue: contiguous runs of an output row, 4 columns a thread
+// With few rows (a serving step) the roles are exchanged (TRANS): the 128-row side is W and
+// the narrow side the tokens, so the MMA's M is full and the kernel streams W at the rate of
+// memory. When the tiles are fewer than the SMs, K is split over the CTAs of a cluster;
+// each then sums its share of the tile over the cluster's shared memories in split order, so
+// the result does not depend on timing and no scratch in memory is needed.
+//
+// Every wait is bounded, as in the grouped GEMM: a role that gives up sets the status word
+// and the CTA's abort flag, the loads and MMAs in flight are drained, TMEM is freed.
+#include <algorithm>
+
+#include "linear.cuh"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace sm100;
+
+constexpr int BM = 128;
+constexpr int BK = 64;  // bf16 elements of a 128-byte swizzled row
+constexpr int kThreadsT = 192;
+constexpr int kMaxStages = 8;
+
+struct TileArgs {
+  int rows, cols, nkb, splits, stages;
+  int a_mn, b_mn;
+  LinearEpi e;
+  unsigned* status;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+__device__ __forceinline__ void store4(void* base, int64_t at, const float (&v)[4], int n) {
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(base) + at;
+  if (n == 4 && aligned8(o)) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < n) o[q] = __float2bfloat16_rn(v[q]);
+  }
+}
+
+// The epilogue of 4 consecutive columns c .. of output row r, the first n of them valid.
+__device__ __forceinline__ void emit4(const LinearEpi& e, int64_t r, int64_t c, float (&v)[4], int n) {
+  if (e.bias) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < n) v[q] += __ldg(e.bias + c + q);
+  }
+  if (e.pre) store4(e.pre, r * e.ldp + c, v, n);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = act_any(e.act, v[q]);
+  if (e.res) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(e.res) + r * e.ldr + c;
+    if (n == 4 && aligned8(p)) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
+      const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
+      v[0] += a.x; v[1] += a.y; v[2] += b.x; v[3] += b.y;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < n) v[q] += __bfloat162float(p[q]);
+    }
+  }
+  store4(e.out, r * e.ldo + c, v, n);
+}
+
+template <int BN, bool TRANS>
+struct TileCfg {
+  static constexpr int A_BYTES = BM * BK * 2;
+  static constexpr int B_BYTES = BN * BK * 2;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int PITCH = (TRANS ? BM : BN) + 4;  // floats of a staged output row
+  static constexpr int DUMP = (TRANS ? BN : BM) * PITCH * 4;
+  static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
+};
+
+template <int BN, bool TRANS>
+__global__ void __launch_bounds__(kThreadsT)
+    linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const TileArgs p) {
+  using C = TileCfg<BN, TRANS>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bars[2 * kMaxStages + 1];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const int NS = p.stages;
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + NS * C::A_BYTES;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kMaxStages;
+  const uint32_t done_bar = empty0 + 8 * kMaxStages;
+  const int i0 = blockIdx.x * BM, j0 = blockIdx.y * BN;
+  const int split = blockIdx.z;  // the CTA's rank in its cluster when splits > 1
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(done_bar, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_map(&tmA);
+    tma_prefetch_map(&tmB);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&s_tmem), C::TMEM_COLS);
+  pdl_wait();
+  pdl_trigger();
+  const uint64_t wlimit = wait_limit_ns(p.status);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  // this split's k-blocks
+  const int kb0 = int(int64_t(p.nkb) * split / p.splits);
+  const int kb1 = int(int64_t(p.nkb) * (split + 1) / p.splits);
+  bool any = false;  // warp 0: loads issued; warp 1: MMAs issued
+  int stage = 0;
+  uint32_t phase = 0;
+  uint32_t issued = 0, issued_par = 0;
+  if (warp == 0) {
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ok = __all_sync(0xffffffffu, wait_bounded(empty0 + 8 * stage, phase ^ 1u, &s_abort, p.status, wlimit));
+      if (!ok) break;
+      if (lane == 0) {
+        const uint32_t fb = full0 + 8 * stage;
+        const uint32_t dA = smem_u32(sA + stage * C::A_BYTES), dB = smem_u32(sB + stage * C::B_BYTES);
+        mbar_expect_tx(fb, C::STAGE);
+        if (p.a_mn) {
+          tma_load_2d(dA, &tmA, i0, kb * BK, fb);
+          tma_load_2d(dA + 8192, &tmA, i0 + 64, kb * BK, fb);
+        } else {
+          tma_load_2d(dA, &tmA, kb * BK, i0, fb);
+        }
+        if constexpr (BN >= 64) {
+          if (p.b_mn) {
+#pragma unroll
+            for (int b = 0; b < BN / 64; ++b) tma_load_2d(dB + b * 8192, &tmB, j0 + 64 * b, kb * BK, fb);
+          } else {
+            tma_load_2d(dB, &tmB, kb * BK, j0, fb);
+          }
+        } else {
+          tma_load_2d(dB, &tmB, kb * BK, j0, fb);
+        }
+      }
+      __syncwarp();
+      issued |= 1u << stage;
+      issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+      if (++stage == NS) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  } else if (warp == 1) {
+    const uint32_t idesc = idesc_bf16(BM, BN) | (p.a_mn ? 1u << 15 : 0u) | (p.b_mn ? 1u << 16 : 0u);
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ok = __all_sync(0xffffffffu, wait_bounded(full0 + 8 * stage, phase, &s_abort, p.status, wlimit));
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t a0 = smem_u32(sA + stage * C::A_BYTES), b0 = smem_u32(sB + stage * C::B_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk) {
+          const uint64_t ad = p.a_mn ? mn_sw128_desc(a0 + kk * 2048) : sw128_desc(a0 + kk * 32);
+          const uint64_t bd = p.b_mn ? mn_sw128_desc(b0 + kk * 2048) : sw128_desc(b0 + kk * 32);
+          mma_bf16(tmem, ad, bd, idesc, (kb != kb0 || kk != 0) ? 1u : 0u);
+        }
+        mma_commit(empty0 + 8 * stage);
+      }
+      __syncwarp();
+      any = true;
+      if (++stage == NS) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (lane == 0 && any) mma_commit(done_bar);  // on a failure too: what was issued finishes
+    __syncwarp();
+  } else {
+    const bool ok = __all_sync(0xffffffffu, wait_bounded(done_bar, 0u, &s_abort, p.status, wlimit));
+    tc_fence_after();
+    if (ok) {
+      const int q = warp & 3, row = 32 * q + lane;  // this lane's accumulator row
+      float* dump = reinterpret_cast<float*>(smem);
+      const uint32_t tbase = tmem + (uint32_t(q * 32) << 16);
+#pragma unroll 1
+      for (int c0 = 0; c0 < BN; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld16(tbase + c0, v);
+        tmem_ld_wait();
+        if constexpr (TRANS) {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) dump[(c0 + x) * C::PITCH + row] = __uint_as_float(v[x]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<uint4*>(dump + row * C::PITCH + c0 + 4 * x) =
+                make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (s_abort) {
+    // loads issued land and MMAs issued finish before shared and tensor memory go away
+    if (warp == 0 && lane == 0)
+      for (int s = 0; s < NS; ++s)
+        if ((issued >> s) & 1u) wait_drain(full0 + 8 * s, (issued_par >> s) & 1u);
+    if (warp == 1 && any) wait_drain(done_bar, 0u);
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+  if (p.splits > 1) cluster_sync_all();  // every split's tile is in its shared memory
+
+  // epilogue: this CTA's share of the output rows of the tile
+  constexpr int OR = TRANS ? BN : BM, OC = TRANS ? BM : BN;
+  const int or0 = OR * split / p.splits, or1 = OR * (split + 1) / p.splits;
+  const int r0 = TRANS ? j0 : i0, c0 = TRANS ? i0 : j0;
+  const int nr = TRANS ? p.cols : p.rows, nc = TRANS ? p.rows : p.cols;
+  const uint32_t base = smem_u32(smem);
+  for (int x = threadIdx.x; x < (or1 - or0) * (OC / 4); x += kThreadsT) {
+    const int r = or0 + x / (OC / 4), c = (x % (OC / 4)) * 4;
+    if (r0 + r >= nr || c0 + c >= nc) continue;
+    const uint32_t off = base + uint32_t(r * C::PITCH + c) * 4;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.splits > 1) {
+      for (int s = 0; s < p.splits; ++s) {
+        const float4 f = ld_cluster_f4(cluster_addr(off, uint32_t(s)));
+        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+      }
+    } else {
+      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(smem + (off - base));
+    }
+    emit4(p.e, r0 + r, c0 + c, v, min(4, nc - (c0 + c)));
+  }
+  __syncwarp();
+  if (p.splits > 1) cluster_sync_all();  // no CTA leaves while another reads its tile
+}
+
+int map_operand(CUtensorMap* m, const LinearOperand& o, int rows, int K, int box) {
+  return o.mn ? make_tma_map_strided(m, o.p, K, rows, o.ld, 64)
+              : make_tma_map_strided(m, o.p, rows, K, o.ld, box);
+}
+
+template <int BN, bool TRANS>
+int run_tile(const LinearOperand& A, const LinearOperand& B, int rows, int cols, int K, int splits,
+             const LinearEpi& e, unsigned* status, cudaStream_t st) {
+  using C = TileCfg<BN, TRANS>;
+  if (B.mn && BN < 64) return MOE_ERR_UNSUPPORTED;
+  CUtensorMap ta, tb;
+  int rc;
+  if ((rc = map_operand(&ta, A, rows, K, BM)) != MOE_OK) return rc;
+  if ((rc = map_operand(&tb, B, cols, K, BN)) != MOE_OK) return rc;
+  TileArgs p;
+  p.rows = rows; p.cols = cols;
+  p.nkb = (K + BK - 1) / BK;
+  p.splits = splits;
+  p.a_mn = A.mn; p.b_mn = B.mn;
+  p.e = e;
+  p.status = status;
+  p.stages = std::min(kMaxStages, (232448 - 2048) / C::STAGE);
+  const int smem = 1024 + p.stages * C::STAGE;
+  if (p.stages * C::STAGE < C::DUMP) return MOE_ERR_UNSUPPORTED;
+  auto kern = linear_tile_kernel<BN, TRANS>;
+  MOE_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  cudaLaunchConfig_t lc = {};
+  const int64_t tj = (int64_t(cols) + BN - 1) / BN;
+  if (tj > 65535) return MOE_ERR_UNSUPPORTED;
+  lc.gridDim = dim3(unsigned((rows + BM - 1) / BM), unsigned(tj), unsigned(splits));
+  lc.blockDim = dim3(kThreadsT);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  cudaLaunchAttribute attr[2];
+  lc.attrs = attr;
+  lc.numAttrs = 0;
+  if (splits > 1) {
+    attr[lc.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[lc.numAttrs].val.clusterDim.x = 1;
+    attr[lc.numAttrs].val.clusterDim.y = 1;
+    attr[lc.numAttrs].val.clusterDim.z = unsigned(splits);
+    ++lc.numAttrs;
+  }
+  if (pdl_enabled()) {
+    attr[lc.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[lc.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++lc.numAttrs;
+  }
+  MOE_CUDA_CHECK(cudaLaunchKernelEx(&lc, kern, ta, tb, p));
+  return MOE_OK;
+}
+
+// K splits for `tiles` tiles: the power of two (at most 8, the portable cluster) that brings
+// the CTAs closest to one wave, with at least four k-blocks each.
+int pick_splits(int64_t tiles, int K) {
+  const int nkb = (K + BK - 1) / BK;
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= num_sms() && nkb >= s * 8) s *= 2;
+  return s;
+}
+
+}  // namespace
+
+int launch_linear_bf16(const LinearOperand& A, const LinearOperand& B, int rows, int cols, int K,
+                       const LinearEpi& e, unsigned* status, cudaStream_t st) {
+  const int64_t wide = (int64_t(cols) + BM - 1) / BM;
+  if (rows <= 64 && !A.mn) {  // few rows: the wide side becomes the MMA's 128 rows
+    const int s = pick_splits(wide, K);
+    if (rows <= 16) return run_tile<16, true>(B, A, cols, rows, K, s, e, status, st);
+    if (rows <= 32) return run_tile<32, true>(B, A, cols, rows, K, s, e, status, st);
+    return run_tile<64, true>(B, A, cols, rows, K, s, e, status, st);
+  }
+  const int64_t tiles = wide * ((int64_t(rows) + BM - 1) / BM);
+  return run_tile<128, false>(A, B, rows, cols, K, pick_splits(tiles, K), e, status, st);
+}
+
+}  // namespace moe

@@ -443,6 +443,8 @@ bool uses_variants(const moe_config_t& c) {
   return c.gate_norm != MOE_GATE_SOFTMAX_TOPK || c.n_expert_groups > 1 || c.uniform_assignment;
 }
 
+}  // namespace
+
 RouteArgs route_args(const moe_config_t& c, int C, const float* logits, const float* u,
                      const moe_route_out_t& out, char* ws, const WsLayout& L) {
   RouteArgs a;
@@ -499,8 +501,6 @@ int launch_scan_finalize(const moe_config_t& c, const RouteArgs& a, const Dispat
   const int64_t n = int64_t(c.S) * c.k;
   return launch_kernel(route_finalize_kernel, dim3(unsigned((n + 255) / 256)), dim3(256), 0, st, a);
 }
-
-}  // namespace
 
 int launch_route(const moe_config_t& c, int C, const float* logits, const float* u,
                  const moe_route_out_t& out, char* ws, const WsLayout& L, cudaStream_t st,

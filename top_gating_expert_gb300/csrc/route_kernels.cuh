@@ -68,6 +68,13 @@ struct FusedRouterArgs {
   int stages;
 };
 
+// route.cu: the argument block of a call, and the two launches after the per-chunk kernel
+// (with d, the finalize step also dispatches)
+RouteArgs route_args(const moe_config_t& c, int C, const float* logits, const float* u,
+                     const moe_route_out_t& out, char* ws, const WsLayout& L);
+int launch_scan_finalize(const moe_config_t& c, const RouteArgs& a, const DispatchFuse* d,
+                         cudaStream_t st);
+
 // entry points of the four kernel translation units (route_topk*.cu, route_fused*.cu)
 int launch_topk_chunks(const RouteArgs& a, int n_chunks, cudaStream_t st);
 int launch_topk_chunks_variants(const RouteArgs& a, int n_chunks, cudaStream_t st);

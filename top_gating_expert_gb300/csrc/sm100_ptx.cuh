@@ -141,6 +141,19 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
   return d;
 }
 
+// Shared-memory descriptor of an MN-major operand staged as 64-column TMA boxes (128-byte
+// rows, one K index a row, 128-byte swizzle): the swizzle atom is 8 K rows of 64 MN
+// elements; atoms follow each other along K every 1024 bytes (stride offset) and along MN
+// every 8 KB, the next box (leading offset).
+__device__ __forceinline__ uint64_t mn_sw128_desc(uint32_t saddr) {
+  uint64_t d = uint64_t((saddr & 0x3FFFFu) >> 4);
+  d |= uint64_t(8192 >> 4) << 16;  // leading-dimension offset: next 64 MN elements
+  d |= uint64_t(1024 >> 4) << 32;  // stride-dimension offset: next 8 K rows
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;
+  return d;
+}
+
 // Instruction descriptor, kind::f16: bf16 A and B (K-major), fp32 D, M = m, N = n.
 __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);

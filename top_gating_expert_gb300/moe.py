@@ -182,6 +182,49 @@ def route_noalloc(cfg, logits, u, out: RouteOutputs, device_status=None, stream=
                                      _ptr(device_status), _stream(stream)), "moe_route_noalloc")
 
 
+def make_score(score) -> N.MoeScore:
+    """A moe_score_t from a dict: score "sigmoid" or "softmax", group_top 1 or 2 (how many of a
+    group's best experts its score sums), renorm (weights sum to scale over the choices),
+    scale."""
+    if isinstance(score, N.MoeScore):
+        return score
+    return N.MoeScore(score=N.SCORES[score.get("score", "sigmoid")], group_top=int(score.get("group_top", 1)),
+                      renorm=int(score.get("renorm", 1)), scale=float(score.get("scale", 1.0)))
+
+
+def _check_f32(t, name: str, shape, where: str):
+    if t is None:
+        return
+    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{where}: {name} must be a contiguous float32 CUDA tensor of shape {tuple(shape)}")
+
+
+def route_scored(cfg, score, logits, select_bias, out: RouteOutputs, ws, stream=None):
+    """Routing from expert scores (see make_score) with a selection bias (float32 [E] or None):
+    the bias takes part in the choice of the experts only, not in their weights."""
+    c = _cfg(cfg)
+    _check_f32(logits, "logits", (c.S, c.E), "route_scored")
+    _check_f32(select_bias, "select_bias", (c.E,), "route_scored")
+    s = out.struct()
+    _check(N.lib().moe_route_scored(ctypes.byref(c), ctypes.byref(make_score(score)), _ptr(logits),
+                                    _ptr(select_bias), ctypes.byref(s), _ptr(ws), ws.numel(),
+                                    _stream(stream)), "moe_route_scored")
+
+
+def route_scored_backward(cfg, score, logits, out: RouteOutputs, dgate, dlogits, aux_coef=0.0,
+                          z_coef=0.0, stream=None):
+    """dlogits (float32 [S, E], written whole) from the gradient dgate [S, k] of the routing
+    weights and the coefficients of the two losses; out holds the forward's routing."""
+    c = _cfg(cfg)
+    _check_f32(logits, "logits", (c.S, c.E), "route_scored_backward")
+    _check_f32(dgate, "dgate", (c.S, c.k), "route_scored_backward")
+    _check_f32(dlogits, "dlogits", (c.S, c.E), "route_scored_backward")
+    s = out.struct()
+    _check(N.lib().moe_route_scored_backward(
+        ctypes.byref(c), ctypes.byref(make_score(score)), _ptr(logits), ctypes.byref(s), _ptr(dgate),
+        float(aux_coef), float(z_coef), _ptr(dlogits), _stream(stream)), "moe_route_scored_backward")
+
+
 def dispatch(cfg, x, out: RouteOutputs, x_perm, stream=None):
     s = out.struct()
     _check(N.lib().moe_dispatch(ctypes.byref(_cfg(cfg)), _ptr(x), ctypes.byref(s), _ptr(x_perm),
@@ -228,6 +271,17 @@ def layer_forward(cfg, x, W_g, bias, W_in_packed, W_out_packed, Ws_in_packed, Ws
         ctypes.byref(_cfg(cfg)), _ptr(x), _ptr(W_g), _ptr(bias), _ptr(W_in_packed), _ptr(W_out_packed),
         _ptr(Ws_in_packed), _ptr(Ws_out_packed), _ptr(u), _ptr(residual), _ptr(y), _ptr(logits_out),
         ctypes.byref(s), _ptr(ws), ws.numel(), _stream(stream)), "moe_layer_forward")
+
+
+def layer_forward_scored(cfg, score, x, W_g, bias, select_bias, W_in_packed, W_out_packed, Ws_in_packed,
+                         Ws_out_packed, residual, y, logits_out, out: RouteOutputs, ws, stream=None):
+    """layer_forward with route_scored as the routing."""
+    s = out.struct()
+    _check(N.lib().moe_layer_forward_scored(
+        ctypes.byref(_cfg(cfg)), ctypes.byref(make_score(score)), _ptr(x), _ptr(W_g), _ptr(bias),
+        _ptr(select_bias), _ptr(W_in_packed), _ptr(W_out_packed), _ptr(Ws_in_packed), _ptr(Ws_out_packed),
+        _ptr(residual), _ptr(y), _ptr(logits_out), ctypes.byref(s), _ptr(ws), ws.numel(),
+        _stream(stream)), "moe_layer_forward_scored")
 
 
 def pack_weights_backward(cfg, W_in, W_up, W_out, stream=None):
@@ -290,6 +344,20 @@ def layer_backward(cfg, x, dy, W_g, W_in_packed, Wt_in_packed, Wt_out_packed, Ws
         "moe_layer_backward")
 
 
+def layer_backward_scored(cfg, score, x, dy, W_g, W_in_packed, Wt_in_packed, Wt_out_packed, Ws_in_packed,
+                          Wst_in_packed, Wst_out_packed, logits, out: RouteOutputs, fwd_ws, residual,
+                          aux_coef, z_coef, grads: Grads, ws, stream=None):
+    """layer_backward of layer_forward_scored."""
+    s = out.struct()
+    g = grads.struct()
+    _check(N.lib().moe_layer_backward_scored(
+        ctypes.byref(_cfg(cfg)), ctypes.byref(make_score(score)), _ptr(x), _ptr(dy), _ptr(W_g),
+        _ptr(W_in_packed), _ptr(Wt_in_packed), _ptr(Wt_out_packed), _ptr(Ws_in_packed),
+        _ptr(Wst_in_packed), _ptr(Wst_out_packed), _ptr(logits), ctypes.byref(s), _ptr(fwd_ws),
+        fwd_ws.numel(), int(bool(residual)), float(aux_coef), float(z_coef), ctypes.byref(g), _ptr(ws),
+        ws.numel(), _stream(stream)), "moe_layer_backward_scored")
+
+
 def device_status(ws, stream=None) -> int:
     """Synchronises the stream; returns (and clears) the device status recorded in ws."""
     return N.lib().moe_get_device_status(_ptr(ws), _stream(stream))
@@ -310,12 +378,15 @@ class MoeLayer:
     the step's inputs from (pinned) host tensors, runs the layer and copies y and the two
     losses back."""
 
-    def __init__(self, cfg: dict, weights: dict, device="cuda", keep_logits: bool = True):
+    def __init__(self, cfg: dict, weights: dict, device="cuda", keep_logits: bool = True, score=None):
         """keep_logits: also store the router logits in ``self.logits`` on every forward
-        (for inspection and tests); without it the bf16 path never writes them."""
+        (for inspection and tests); without it the bf16 path never writes them.
+        score: a dict as make_score takes it routes by expert scores (route_scored), with
+        weights["select_bias"] (float32 [E], optional) as the selection bias."""
         self.cfg_dict = cfg
         self.cfg = make_config(cfg)
         _check(validate(self.cfg), "moe_validate_config")
+        self.score = None if score is None else make_score(score)
         dt = torch_dtype(self.cfg)
         dev = torch.device(device)
         to = lambda t: None if t is None else t.to(device=dev, dtype=dt).contiguous()
@@ -324,6 +395,9 @@ class MoeLayer:
         self.W_in_packed, self.W_out_packed = pack_weights(self.cfg, W_in, W_up, W_out)
         del W_in, W_up, W_out
         self.bias = None if weights.get("bias") is None else weights["bias"].to(dev, torch.float32)
+        self.select_bias = None
+        if score is not None and weights.get("select_bias") is not None:
+            self.select_bias = weights["select_bias"].to(dev, torch.float32).contiguous()
         self.Ws_in_packed = self.Ws_out_packed = None
         if self.cfg.n_shared > 0:
             self.Ws_in_packed, self.Ws_out_packed = pack_shared_weights(
@@ -339,6 +413,14 @@ class MoeLayer:
         """y (self.y unless `out` is given); the routing outputs go to self.route_out unless
         `route_out` (a RouteOutputs of this config) is given."""
         y = self.y if out is None else out
+        if self.score is not None:
+            if u is not None:
+                raise ValueError("scored routing takes no random-routing draws")
+            layer_forward_scored(self.cfg, self.score, x, self.W_g, self.bias, self.select_bias,
+                                 self.W_in_packed, self.W_out_packed, self.Ws_in_packed,
+                                 self.Ws_out_packed, residual, y, self.logits,
+                                 self.route_out if route_out is None else route_out, self.ws, stream)
+            return y
         layer_forward(self.cfg, x, self.W_g, self.bias, self.W_in_packed, self.W_out_packed,
                       self.Ws_in_packed, self.Ws_out_packed, u, residual, y, self.logits,
                       self.route_out if route_out is None else route_out, self.ws, stream)
@@ -363,6 +445,13 @@ class MoeLayer:
         (which must have kept its logits), into self.grads."""
         if self.logits is None:
             raise RuntimeError("the backward needs the forward's logits (keep_logits=True)")
+        if self.score is not None:
+            layer_backward_scored(self.cfg, self.score, x, dy, self.W_g, self.W_in_packed,
+                                  self.Wt_in_packed, self.Wt_out_packed, self.Ws_in_packed,
+                                  self.Wst_in_packed, self.Wst_out_packed, self.logits,
+                                  self.route_out, self.ws, residual, aux_coef, z_coef, self.grads,
+                                  self.ws_bwd, stream)
+            return self.grads
         layer_backward(self.cfg, x, dy, self.W_g, self.W_in_packed, self.Wt_in_packed,
                        self.Wt_out_packed, self.Ws_in_packed, self.Wst_in_packed,
                        self.Wst_out_packed, self.logits, self.route_out, self.ws, residual,
