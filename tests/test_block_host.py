@@ -1,0 +1,146 @@
+"""Refusals of the norm, linear and scored-routing entry points, before anything is launched:
+the C ABI's checks on made-up pointers and the Python binding's on CPU tensors."""
+
+import ctypes
+
+import pytest
+import torch
+
+from top_gating_expert_gb300 import _native as N
+from top_gating_expert_gb300 import block, moe
+from top_gating_expert_gb300.inputs import preset
+
+P = ctypes.c_void_p(1 << 20)
+REF = ctypes.byref
+
+
+def norm(**kw):
+    d = dict(rows=4, cols=64, dtype=1, eps=1e-5, ldx=64, ldr=64, ldh=64, ldy=64)
+    d.update(kw)
+    return N.MoeNorm(**d)
+
+
+def lin(**kw):
+    d = dict(T=4, N=64, K=32, act=0, dtype=1)
+    d.update(kw)
+    return N.MoeLinear(**d)
+
+
+@pytest.mark.parametrize("bad", [dict(rows=-1), dict(cols=0), dict(dtype=2), dict(eps=-1.0), dict(eps=float("nan")),
+                                 dict(eps=float("inf")), dict(ldx=63), dict(ldr=1), dict(ldh=0), dict(ldy=-64)])
+def test_norm_refuses(native_lib, bad):
+    n = norm(**bad)
+    b = N.c_size_t()
+    assert native_lib.moe_norm_forward(REF(n), P, None, P, None, None, P, None, None, None) == -1
+    assert native_lib.moe_norm_backward(REF(n), P, P, P, P, P, None, P, P, P, P, 1 << 30, None) == -1
+    assert native_lib.moe_norm_workspace_bytes(REF(n), REF(b)) == -1
+
+
+def test_norm_pointers_and_workspace(native_lib):
+    n, b = norm(), N.c_size_t()
+    L = native_lib
+    assert L.moe_norm_forward(None, P, None, P, None, None, P, None, None, None) == -1
+    assert L.moe_norm_forward(REF(n), None, None, P, None, None, P, None, None, None) == -1
+    assert L.moe_norm_forward(REF(n), P, None, None, None, None, P, None, None, None) == -1
+    assert L.moe_norm_forward(REF(n), P, None, P, None, None, None, None, None, None) == -1
+    assert L.moe_norm_forward(REF(n), P, None, P, None, P, P, None, None, None) == -1  # h is y
+    assert L.moe_norm_workspace_bytes(REF(n), REF(b)) == 0 and b.value > 256
+    assert L.moe_norm_workspace_bytes(REF(n), None) == -1
+    args = [P, P, P, P, P, None, P, P, P]
+    for i in (0, 1, 2, 3, 4, 6):
+        a = list(args)
+        a[i] = None
+        assert L.moe_norm_backward(REF(n), *a, P, b.value, None) == -1
+    assert L.moe_norm_backward(REF(n), *args, P, b.value - 1, None) == -3
+    assert L.moe_norm_backward(REF(n), *args, None, b.value, None) == -3
+    assert L.moe_norm_backward(REF(n), *args, ctypes.c_void_p((1 << 20) + 16), b.value, None) == -3
+    zero = norm(rows=0)
+    assert L.moe_norm_forward(REF(zero), None, None, None, None, None, None, None, None, None) == 0
+
+
+@pytest.mark.parametrize("bad", [dict(T=-1), dict(N=0), dict(K=0), dict(act=5), dict(act=-1), dict(dtype=7),
+                                 dict(ldx=31), dict(ldw=8), dict(ldy=63), dict(ldr=1), dict(ldp=63), dict(lddx=31),
+                                 dict(lddw=31)])
+def test_linear_refuses(native_lib, bad):
+    p, b = lin(**bad), N.c_size_t()
+    assert native_lib.moe_linear_workspace_bytes(REF(p), 1, 1, REF(b)) == -1
+    assert native_lib.moe_linear_forward(REF(p), P, P, None, None, P, None, P, 1 << 40, None) == -1
+    assert native_lib.moe_linear_backward(REF(p), P, P, P, P, P, P, P, P, 1 << 40, None) == -1
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_linear_pointers_and_workspace(native_lib, dtype):
+    L, p = native_lib, lin(dtype=dtype, act=2)
+    sizes = {}
+    for back in (0, 1):
+        for un in (0, 1):
+            b = N.c_size_t()
+            assert L.moe_linear_workspace_bytes(REF(p), back, un, REF(b)) == 0
+            sizes[back, un] = b.value
+    assert sizes[0, 0] <= sizes[0, 1] <= sizes[1, 1] and sizes[0, 0] <= sizes[1, 0] <= sizes[1, 1]
+    assert L.moe_linear_workspace_bytes(REF(p), 1, 1, None) == -1
+    fwd = sizes[0, 0]
+    assert L.moe_linear_forward(REF(p), None, P, None, None, P, None, P, fwd, None) == -1
+    assert L.moe_linear_forward(REF(p), P, None, None, None, P, None, P, fwd, None) == -1
+    assert L.moe_linear_forward(REF(p), P, P, None, None, None, None, P, fwd, None) == -1
+    assert L.moe_linear_forward(REF(p), P, P, None, None, P, P, P, fwd, None) == -1  # pre is y
+    assert L.moe_linear_forward(REF(p), P, P, None, None, P, None, P, fwd - 1, None) == -3
+    assert L.moe_linear_forward(REF(p), P, P, None, None, P, None, None, fwd, None) == -3
+    if dtype == 1:  # an operand off its 16-byte boundary needs room for its copy
+        off = ctypes.c_void_p((1 << 20) + 2)
+        assert L.moe_linear_forward(REF(p), off, P, None, None, P, None, P, fwd, None) == -3
+    bwd = sizes[1, 0]
+    assert L.moe_linear_backward(REF(p), P, P, P, None, P, P, P, P, bwd, None) == -1   # no pre
+    assert L.moe_linear_backward(REF(p), None, P, P, P, P, P, P, P, bwd, None) == -1
+    assert L.moe_linear_backward(REF(p), P, None, P, P, P, P, P, P, bwd, None) == -1   # dW needs x
+    assert L.moe_linear_backward(REF(p), P, P, None, P, P, P, P, P, bwd, None) == -1   # dx needs W
+    assert L.moe_linear_backward(REF(p), P, P, P, P, P, P, P, P, bwd - 1, None) == -3
+    zero = lin(T=0, dtype=dtype)
+    assert L.moe_linear_forward(REF(zero), None, None, None, None, None, None, None, 0, None) == 0
+
+
+def test_scored_routing_refuses(native_lib):
+    L = native_lib
+    c = moe.make_config(preset(2, random_routing=0))
+    need = moe.workspace_bytes(c, N.MOE_WS_STEP)
+    out = N.MoeRouteOut(**{f: (1 << 20) for f in N.ROUTE_FIELDS})
+    good = dict(score=0, group_top=1, renorm=1, scale=1.0)
+    call = lambda cfg, s, lg=P, o=out, ws=P, n=need: L.moe_route_scored(REF(cfg), REF(s) if s else None, lg, None,
+                                                                       REF(o), ws, n, None)
+    back = lambda cfg, s, lg=P, dg=P, dl=P, o=out: L.moe_route_scored_backward(REF(cfg), REF(s), lg, REF(o), dg, 0.0,
+                                                                              0.0, dl, None)
+    for bad in (dict(score=2), dict(score=-1), dict(group_top=0), dict(group_top=3), dict(renorm=2),
+                dict(scale=float("nan")), dict(scale=float("inf"))):
+        s = N.MoeScore(**dict(good, **bad))
+        assert call(c, s) == -1 and back(c, s) == -1
+    s = N.MoeScore(**good)
+    assert call(c, None) == -1 and call(c, s, lg=None) == -1
+    assert call(c, s, n=need - 1) == -3 and call(c, s, ws=None) == -3
+    holes = N.MoeRouteOut(**{f: (1 << 20) for f in N.ROUTE_FIELDS if f != "row"})
+    assert call(c, s, o=holes) == -1 and back(c, s, o=holes) == -1
+    assert back(c, s, lg=None) == -1 and back(c, s, dg=None) == -1 and back(c, s, dl=None) == -1
+    for over in (dict(random_routing=1), dict(uniform_assignment=1, random_routing=0),
+                 dict(gate_norm="none", random_routing=0)):
+        assert call(moe.make_config(preset(2, **over)), s) == -2
+    assert call(moe.make_config(preset(2, random_routing=0, k=9)), s) == -1
+    lay = moe.workspace_bytes(c, N.MOE_WS_LAYER)
+    assert L.moe_layer_forward_scored(REF(c), None, P, P, None, None, P, P, None, None, None, P, None, REF(out), P,
+                                      lay, None) == -1
+    assert L.moe_layer_forward_scored(REF(c), REF(s), P, P, None, None, P, P, None, None, None, P, None, REF(out), P,
+                                      16, None) == -3
+
+
+def test_binding_refuses_before_the_library(native_lib):
+    cpu = torch.zeros(4, 8)
+    for call in (lambda: block.layer_norm(cpu, torch.ones(8)),
+                 lambda: block.layer_norm_backward(cpu, cpu, torch.ones(8), torch.ones(4), torch.ones(4)),
+                 lambda: block.linear(cpu, cpu), lambda: block.linear_backward(cpu, cpu, cpu),
+                 lambda: block.linear(cpu, cpu, act="tanh"), lambda: block.linear_backward(cpu, cpu, cpu, act="x"),
+                 lambda: block.layer_norm(cpu[0], torch.ones(8))):
+        with pytest.raises(ValueError):
+            call()
+    cfg = preset(2, random_routing=0)
+    with pytest.raises(ValueError):
+        moe.route_scored(cfg, dict(score="sigmoid"), torch.zeros(4, 4), None, None, None)
+    with pytest.raises(KeyError):
+        moe.make_score(dict(score="tanh"))

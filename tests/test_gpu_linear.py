@@ -1,0 +1,270 @@
+"""The linear layer on the GPU against a 64-bit evaluation: every size class (one token, few,
+many; sizes that no tile divides; rows on no 16-byte boundary), activations, residual, stored
+pre-activations, gradients, in place, zero tokens, non-finite values, another stream, a graph.
+
+Tolerance of a product of K terms: the products are exact in fp32 for bf16 inputs (and off by u
+for fp32); summed in any order, by an accumulator that may truncate (2u a step), the sum is off
+by at most 2 (K + 2) u sum|a||b|. An activation with slope at most 1.2 and an evaluation error of
+16 u (|v| + 1) follows. bf16 gradients through an activation carry the rounding of d, 2^-8
+relative a term."""
+
+import pytest
+import torch
+
+from block_util import U, assert_within, generator, half_step, strided
+from top_gating_expert_gb300 import block
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
+
+
+def act64(name, v):
+    F = torch.nn.functional
+    return {"none": lambda z: z, "relu": F.relu, "gelu": F.gelu,
+            "gelu_tanh": lambda z: F.gelu(z, approximate="tanh"), "silu": F.silu}[name](v)
+
+
+def act_slope64(name, v):
+    if name == "none":
+        return torch.ones_like(v)
+    p = v.detach().clone().requires_grad_(True)
+    return torch.autograd.grad(act64(name, p).sum(), p)[0]
+
+
+def check_forward(x, W, bias, act, res, got, dt):
+    y, pre = got
+    K = x.shape[1]
+    xd, wd = x.double(), W.double()
+    v = xd @ wd.t()
+    s = xd.abs() @ wd.abs().t()
+    if bias is not None:
+        v = v + bias.double()
+        s = s + bias.double().abs()
+    tv = 2 * (K + 3) * U * s
+    if pre is not None:
+        assert_within(pre, v, tv * (1 + half_step(dt)) + half_step(dt) * v.abs() + 1e-38, "pre")
+    r = act64(act, v)
+    ty = 1.2 * tv + (0 if act in ("none", "relu") else 16 * U * (v.abs() + 1))
+    if res is not None:
+        r = r + res.double()
+        ty = ty + U * (r.abs() + res.double().abs())
+    assert_within(y, r, ty * (1 + half_step(dt)) + half_step(dt) * r.abs() + 1e-38, "y")
+
+
+def make(T, N, K, dtype, pad, off, seed, has_bias=True):
+    gen, dt = generator(seed), DT[dtype]
+    x = strided(T, K, pad, off, dt, gen)
+    W = strided(N, K, pad, off, dt, gen, scale=K ** -0.5)
+    bias = torch.randn(N, generator=gen, device="cuda") if has_bias else None
+    return gen, dt, x, W, bias
+
+
+SHAPES = [(1, 1, 1), (1, 64, 64), (1, 5000, 264), (2, 128, 8), (3, 7, 5), (16, 256, 512), (17, 130, 72),
+          (33, 200, 1000), (64, 1408, 2048), (65, 128, 64), (100, 100, 100), (128, 256, 192),
+          (129, 257, 321), (256, 256, 256), (300, 520, 640), (777, 141, 2049), (513, 2000, 136),
+          (2048, 1024, 512), (1000, 4104, 328), (1, 129, 20000), (40, 16, 9000)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("layout", [(0, 0), (3, 1), (8, 8)])
+def test_forward(native_lib, dtype, shape, layout):
+    (T, N, K), (pad, off) = shape, layout
+    gen, dt, x, W, bias = make(T, N, K, dtype, pad, off, T + N + K)
+    act = ACTS[(T + N + K + pad) % 5]
+    res = strided(T, N, pad, off, dt, gen)
+    out = strided(T, N, pad, off, dt, gen)
+    pre = strided(T, N, pad, off, dt, gen)
+    got = block.linear(x, W, bias, act=act, residual=res, out=out, pre=pre)
+    check_forward(x, W, bias, act, res, got, dt)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("shape", [(1, 512, 256), (48, 512, 256), (600, 512, 256)])
+def test_epilogue_parts(native_lib, dtype, act, shape):
+    """Every activation with each of bias, residual and stored pre-activation left out in turn."""
+    T, N, K = shape
+    gen, dt, x, W, bias = make(T, N, K, dtype, 0, 0, 3)
+    res = strided(T, N, 0, 0, dt, gen)
+    for b, r, p in ((bias, res, True), (None, res, False), (bias, None, True), (None, None, False)):
+        got = block.linear(x, W, b, act=act, residual=r, save_pre=p)
+        assert (got[1] is not None) == p
+        check_forward(x, W, b, act, r, got, dt)
+
+
+def check_backward(dy, x, W, act, pre, got, dt, has_bias):
+    dx, dW, db = got
+    T, N = dy.shape
+    d = dy.double()
+    if act != "none":
+        d = d * act_slope64(act, pre.double())
+    rel = half_step(torch.bfloat16) if (dt == torch.bfloat16 and act != "none") else 0.0
+    # of d itself: slopes within 16 u (|pre| + 1) (their terms reach |pre|), then the rounding
+    ed = (0 if act in ("none", "relu") else 16 * U * (pre.double().abs() + 1) * dy.double().abs()) + U * d.abs()
+    ed = ed + rel * d.abs() * (1 + 2 * U)
+    for name, r, mag, n, err, out in (
+            ("dx", d @ W.double(), d.abs() @ W.double().abs(), N, ed @ W.double().abs()
+             if torch.is_tensor(ed) else 0, dx),
+            ("dW", d.t() @ x.double(), d.abs().t() @ x.double().abs(), T, ed.t() @ x.double().abs(), dW)):
+        t = 2 * (n + 3) * U * mag * (1 + rel) + err
+        assert_within(out, r, t * (1 + half_step(dt)) + half_step(dt) * r.abs() + 1e-38, name)
+    if has_bias:
+        edb = (0 if act in ("none", "relu") else 16 * U * (pre.double().abs() + 1) * dy.double().abs()) + U * d.abs()
+        assert_within(db, d.sum(0), (T / 8 + 512) * U * d.abs().sum(0) + edb.sum(0) + 1e-38, "dbias")
+    else:
+        assert db is None
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("layout", [(0, 0), (3, 1)])
+def test_backward(native_lib, dtype, shape, layout):
+    (T, N, K), (pad, off) = shape, layout
+    gen, dt, x, W, _ = make(T, N, K, dtype, pad, off, T + N + K + 1)
+    act = ACTS[(T + N + K + pad + 2) % 5]
+    dy = strided(T, N, pad, off, dt, gen)
+    pre = None if act == "none" else strided(T, N, pad, off, dt, gen, scale=1.5)
+    dx, dW = strided(T, K, pad, off, dt, gen), strided(N, K, pad, off, dt, gen)
+    got = block.linear_backward(dy, x, W, act=act, pre=pre, need_bias=(T % 2 == 1), dx=dx, dW=dW)
+    check_backward(dy, x, W, act, pre, got, dt, T % 2 == 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ACTS)
+def test_backward_parts(native_lib, dtype, act):
+    """Each gradient alone equals the one of the whole call, bit for bit."""
+    gen, dt, x, W, _ = make(500, 384, 320, dtype, 0, 0, 9)
+    dy = strided(500, 384, 0, 0, dt, gen)
+    pre = strided(500, 384, 0, 0, dt, gen)
+    whole = block.linear_backward(dy, x, W, act=act, pre=pre)
+    check_backward(dy, x, W, act, pre, whole, dt, True)
+    for i, need in enumerate(("need_x", "need_W", "need_bias")):
+        flags = dict(need_x=False, need_W=False, need_bias=False)
+        flags[need] = True
+        part = block.linear_backward(dy, x, W, act=act, pre=pre, **flags)
+        assert torch.equal(part[i], whole[i])
+        assert [p is None for p in part] == [j != i for j in range(3)]
+
+
+def test_slopes_far_out(native_lib):
+    """Activations and their slopes at large arguments, at zero and at the infinities of plain
+    relu; the tanh form's cube does not spoil finite arguments."""
+    v = torch.tensor([[-3e38, -1e20, -100.0, -20.0, -5.0, -0.0, 0.0, 5.0, 20.0, 100.0, 1e20, 3e38]], device="cuda")
+    eye = torch.ones(1, 1, device="cuda")
+    for act in ("relu", "gelu", "gelu_tanh", "silu"):
+        y, _ = block.linear(v.t().contiguous(), eye, act=act)
+        ref = act64(act, v.t().double())
+        assert_within(y, ref, 32 * U * (ref.abs() + 1), act)
+        dx, _, _ = block.linear_backward(torch.ones_like(y), v.t().contiguous(), eye, act=act,
+                                         pre=v.t().contiguous())
+        far = v.t().abs() > 50
+        slope = torch.where(v.t() > 0, 1.0, 0.0)
+        assert torch.equal(dx[far], slope[far]), act
+    pre = torch.tensor([[0.0, -0.0, float("nan")]], device="cuda")
+    dx, _, _ = block.linear_backward(torch.ones(1, 3, device="cuda"), torch.ones(1, 1, device="cuda"),
+                                     torch.eye(3, device="cuda")[:, :1].contiguous(), act="relu", pre=pre)
+    assert dx.item() == 0.0  # relu'(0) = 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [2, 40, 300])
+def test_non_finite_rows_stay_in_their_rows(native_lib, dtype, T):
+    gen, dt, x, W, bias = make(T, 260, 200, dtype, 0, 0, 5)
+    clean, _ = block.linear(x, W, bias)
+    x[T // 2, 3] = float("nan")
+    x[0, 5] = float("inf")
+    y, _ = block.linear(x, W, bias)
+    assert torch.isnan(y[T // 2]).all()
+    assert torch.equal(y[0], (clean[0] * 0 + float("inf")) * torch.sign(W[:, 5])) or T // 2 == 0
+    rest = [t for t in range(T) if t not in (0, T // 2)]
+    assert torch.equal(y[rest], clean[rest])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_zero_tokens(native_lib, dtype):
+    dt = DT[dtype]
+    x, W = torch.empty(0, 64, device="cuda", dtype=dt), torch.randn(32, 64, device="cuda").to(dt)
+    y, pre = block.linear(x, W, act="gelu", save_pre=True)
+    assert y.shape == pre.shape == (0, 32)
+    dW = torch.full((32, 64), 3.0, device="cuda", dtype=dt)
+    dx, dW2, db = block.linear_backward(y, x, W, act="gelu", pre=pre, dW=dW)
+    assert dx.shape == (0, 64) and not dW2.any() and not db.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 20, 257, 1024])
+def test_residual_in_place(native_lib, dtype, T):
+    gen, dt, x, W, bias = make(T, 264, 320, dtype, 0, 0, 6)
+    res = strided(T, 264, 0, 0, dt, gen)
+    y, _ = block.linear(x, W, bias, act="silu", residual=res)
+    y2, _ = block.linear(x, W, bias, act="silu", residual=res, out=res)
+    assert y2 is res and torch.equal(y, y2)
+
+
+def test_aligned_workspace(native_lib):
+    """A workspace without room for copies serves aligned operands and refuses others."""
+    from top_gating_expert_gb300 import moe
+    gen, dt, x, W, bias = make(100, 256, 128, "bf16", 0, 0, 7)
+    ws = block.linear_workspace(100, 256, 128, aligned=True, backward=False)
+    y, _ = block.linear(x, W, bias, ws=ws)
+    assert torch.equal(y, block.linear(x, W, bias)[0])
+    xo = strided(100, 128, 0, 1, dt, gen)
+    with pytest.raises(moe.MoeError):
+        block.linear(xo, W, bias, ws=ws)
+    assert moe.device_status(ws) == 0
+
+
+def test_repeatable_on_another_stream_and_in_a_graph(native_lib):
+    gen, dt, x, W, bias = make(1500, 768, 513, "bf16", 0, 0, 10)
+    dy = strided(1500, 768, 0, 0, dt, gen)
+    ws = block.linear_workspace(1500, 768, 513)
+
+    def step(**kw):
+        y, pre = block.linear(x, W, bias, act="gelu", save_pre=True, ws=ws, **kw)
+        return (y, pre) + block.linear_backward(dy, x, W, act="gelu", pre=pre, ws=ws, **kw)
+
+    first = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    second = step(stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        third = step()
+    for _ in range(2):
+        graph.replay()
+    for a, b, c in zip(first, second, third):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_large_offsets(native_lib):
+    """Rows more than 2^31 elements into their buffers."""
+    T, N, K = 9, 64, 64
+    ld = 1 << 28
+    big = torch.empty(8 * ld + 64, dtype=torch.bfloat16, device="cuda")
+    x = big.as_strided((T, K), (ld, 1))
+    x.copy_(torch.randn(T, K, generator=generator(1), device="cuda"))
+    W = (torch.randn(N, K, generator=generator(2), device="cuda") / 8).to(torch.bfloat16)
+    y, _ = block.linear(x, W)
+    check_forward(x, W, None, "none", None, (y, None), torch.bfloat16)
+    gamma = torch.ones(K, device="cuda")
+    n = block.layer_norm(x, gamma)[0]
+    assert torch.equal(n, block.layer_norm(x.contiguous(), gamma)[0])
+
+
+def test_stalled_pipeline_reports_a_timeout(native_lib):
+    """A wait limit of 1 ns: the kernel gives up (or finishes at once), frees what it holds and
+    the next call with the default limit is right."""
+    from top_gating_expert_gb300 import moe
+    gen, dt, x, W, bias = make(600, 1024, 2048, "bf16", 0, 0, 12)
+    good, _ = block.linear(x, W, bias)
+    ws = block.linear_workspace(600, 1024, 2048)
+    moe.set_wait_limit(ws, 1)
+    block.linear(x, W, bias, ws=ws)
+    assert moe.device_status(ws) in (0, -5)
+    moe.set_wait_limit(ws, 0)
+    y, _ = block.linear(x, W, bias, ws=ws)
+    assert moe.device_status(ws) == 0 and torch.equal(y, good)

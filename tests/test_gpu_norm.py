@@ -1,0 +1,241 @@
+"""Layer norm on the GPU against a 64-bit evaluation: sizes from one row and one column to long
+and odd rows, strides and offsets that no 16-byte access fits, offsets large against the
+spread, NaN and infinity, empty inputs, in-place outputs, another stream, a CUDA graph.
+
+Tolerances: chains of d = M / 32 + 32 additions cover every summation tree used (at least 32
+threads a row and a tree over them), d_T = rows / 8 + 512 the column sums."""
+
+import pytest
+import torch
+
+from block_util import U, assert_within, generator, half_step, strided
+from top_gating_expert_gb300 import block
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+SHAPES = [(1, 1), (1, 7), (3, 2), (2, 8), (5, 33), (1, 4096), (4, 1000), (7, 1003), (130, 64), (33, 1024),
+          (300, 257), (17, 8192), (3, 16384), (2, 20001), (2000, 129), (641, 512), (9, 2056)]
+
+
+def ref_forward(x, res, gamma, beta, eps):
+    h = x.double() if res is None else x.double() + res.double()
+    mean = h.mean(1)
+    var = (h - mean[:, None]).square().mean(1)
+    rstd = 1.0 / torch.sqrt(var + eps)
+    xh = (h - mean[:, None]) * rstd[:, None]
+    y = xh * gamma.double() + (0 if beta is None else beta.double())
+    return h, mean, rstd, xh, y
+
+
+def check_forward(x, res, gamma, beta, eps, got, dt):
+    y, h, mean, rstd = got
+    rh, rmean, rrstd, xh, ry = ref_forward(x, res, gamma, beta, eps)
+    M = x.shape[1]
+    d = M / 32 + 32
+    habs = rh.abs()
+    dmean = (d + 3) * U * habs.mean(1) + U * rmean.abs()
+    assert_within(mean, rmean, dmean + 1e-40, "mean")
+    # of the variance: the chain, 4 u a term, and the mean's error (its square only, and the
+    # rounding of h itself)
+    dev = (rh - rmean[:, None]).abs()
+    dterm = 2 * dev * (U * (habs + rmean.abs()[:, None]) + dmean[:, None]) + dmean[:, None] ** 2
+    dvar = (dev ** 2).mean(1) * (d + 8) * U + dterm.mean(1)
+    drstd = rrstd * (0.5 * dvar * rrstd ** 2 + 4 * U)
+    small = dvar * rrstd ** 2 < 0.1  # first order holds
+    assert_within(rstd[small], rrstd[small], drstd[small], "rstd")
+    ab = 0 if beta is None else beta.double().abs()
+    g = gamma.double().abs()
+    ty = g * rrstd[:, None] * (dmean[:, None] + 3 * U * (habs + rmean.abs()[:, None])) \
+        + g * xh.abs() * (drstd / rrstd + 4 * U)[:, None] + 2 * U * ab
+    ty = ty * (1 + half_step(dt)) + half_step(dt) * ry.abs() + 1e-38
+    assert_within(y[small], ry[small], ty[small], "y")
+    if res is not None:
+        assert_within(h, rh, (U + half_step(dt)) * habs + 1e-40, "h")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("variant", [(0, 0, 0, 0), (1, 1, 0, 0), (1, 0, 3, 1), (0, 1, 8, 8)])
+def test_forward(native_lib, dtype, shape, variant):
+    (T, M), (has_res, has_beta, pad, off), dt = shape, variant, DT[dtype]
+    gen = generator(T * 31 + M)
+    x = strided(T, M, pad, off, dt, gen)
+    x.copy_(x.float() * 0.5 + 3.0)  # an offset against which E[x^2] - mean^2 would cancel
+    res = strided(T, M, pad, off, dt, gen) if has_res else None
+    gamma = 1 + 0.3 * torch.randn(M, generator=gen, device="cuda")
+    beta = torch.randn(M, generator=gen, device="cuda") if has_beta else None
+    out = strided(T, M, pad, off, dt, gen)
+    got = block.layer_norm(x, gamma, beta, 1e-5, residual=res, out=out)
+    assert got[0] is out
+    check_forward(x, res, gamma, beta, 1e-5, got, dt)
+
+
+def ref_backward(dy, h, gamma, mean, rstd, dh):
+    mean, rstd = mean.double()[:, None], rstd.double()[:, None]
+    h, dy, gamma = h.double(), dy.double(), gamma.double()
+    xh = (h - mean) * rstd
+    g = dy * gamma
+    dx = rstd * (g - g.mean(1, keepdim=True) - xh * (g * xh).mean(1, keepdim=True))
+    if dh is not None:
+        dx = dx + dh.double()
+    return dx, (dy * xh).sum(0), dy.sum(0), xh, g
+
+
+def check_backward(dy, h, gamma, mean, rstd, dh, got, dt):
+    dx, dgamma, dbeta = got
+    rdx, rdg, rdb, xh, g = ref_backward(dy, h, gamma, mean, rstd, dh)
+    T, M = h.shape
+    d, dT = M / 32 + 32, T / 8 + 512
+    ed = rstd.double()[:, None] * 3 * U * (h.double().abs() + mean.double().abs()[:, None]) + 2 * U * xh.abs()
+    e1 = (d + 3) * U * g.abs().mean(1, keepdim=True)
+    e2 = (d + 4) * U * (g * xh).abs().mean(1, keepdim=True) + (g.abs() * ed).mean(1, keepdim=True)
+    s2 = (g * xh).mean(1, keepdim=True)
+    s1 = g.mean(1, keepdim=True)
+    t = rstd.double()[:, None] * (e1 + xh.abs() * e2 + ed * s2.abs()
+                                  + 5 * U * (g.abs() + s1.abs() + (xh * s2).abs()))
+    if dh is not None:
+        t = t + U * (dh.double().abs() + rdx.abs())
+    t = t * (1 + half_step(dt)) + half_step(dt) * rdx.abs() + 1e-38
+    assert_within(dx, rdx, t, "dx")
+    tg = (dT + 2) * U * (dy.double() * xh).abs().sum(0) + (dy.double().abs() * ed).sum(0) + 1e-38
+    assert_within(dgamma, rdg, tg, "dgamma")
+    if dbeta is not None:
+        assert_within(dbeta, rdb, dT * U * dy.double().abs().sum(0) + 1e-38, "dbeta")
+
+
+def stats(h, eps=1e-5):
+    hf = h.double()
+    mean = hf.mean(1)
+    return mean.float(), (1 / torch.sqrt((hf - mean[:, None]).square().mean(1) + eps)).float()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("variant", [(0, 1, 0, 0), (1, 1, 0, 0), (1, 0, 3, 1)])
+def test_backward(native_lib, dtype, shape, variant):
+    (T, M), (has_dh, need_beta, pad, off), dt = shape, variant, DT[dtype]
+    gen = generator(T * 17 + M)
+    h = strided(T, M, pad, off, dt, gen)
+    h.copy_(h.float() * 0.7 - 2.0)
+    dy = strided(T, M, pad, off, dt, gen)
+    dh = strided(T, M, pad, off, dt, gen) if has_dh else None
+    gamma = 1 + 0.3 * torch.randn(M, generator=gen, device="cuda")
+    mean, rstd = stats(h)
+    dx = strided(T, M, pad, off, dt, gen)
+    got = block.layer_norm_backward(dy, h, gamma, mean, rstd, dh, need_beta=bool(need_beta), dx=dx)
+    assert got[0] is dx and (got[2] is not None) == bool(need_beta)
+    check_backward(dy, h, gamma, mean, rstd, dh, got, dt)
+
+
+def test_one_column_has_no_gradient(native_lib):
+    """With one column h equals its mean and g its own, so dx is zero exactly."""
+    gen = generator(2)
+    h = strided(100, 1, 0, 0, torch.bfloat16, gen)
+    dy = strided(100, 1, 0, 0, torch.bfloat16, gen)
+    mean, rstd = stats(h)
+    dx, dgamma, _ = block.layer_norm_backward(dy, h, torch.full((1,), 1.1, device="cuda"), mean, rstd)
+    assert not dx.any() and not dgamma.any()
+
+
+def test_gradient_against_differences(native_lib):
+    """d loss / d x in 64 bits of the forward's formula by central differences (step 1e-4, error
+    O(step^2) + O(2^-53 / step)) against the kernel's fp32 dx."""
+    gen = generator(4)
+    x = torch.randn(3, 24, generator=gen, device="cuda")
+    gamma = torch.randn(24, generator=gen, device="cuda")
+    dy = torch.randn(3, 24, generator=gen, device="cuda")
+    _, _, mean, rstd = block.layer_norm(x, gamma)
+    dx, _, _ = block.layer_norm_backward(dy, x, gamma, mean, rstd)
+    f = lambda z: (ref_forward(z, None, gamma, None, 1e-5)[4] * dy.double()).sum().item()
+    for r in range(3):
+        for c in range(24):
+            up, dn = x.double().clone(), x.double().clone()
+            up[r, c] += 1e-4
+            dn[r, c] -= 1e-4
+            num = (f(up) - f(dn)) / 2e-4
+            assert abs(num - dx[r, c].item()) < 1e-5
+
+
+def test_zero_rows(native_lib):
+    x = torch.empty(0, 64, device="cuda", dtype=torch.bfloat16)
+    gamma = torch.ones(64, device="cuda")
+    y, _, mean, rstd = block.layer_norm(x, gamma)
+    assert y.shape == (0, 64) and mean.shape == (0,)
+    dg = torch.full((64,), 7.0, device="cuda")
+    dx, dgamma, dbeta = block.layer_norm_backward(x, x, gamma, mean, rstd, dgamma=dg)
+    assert dx.shape == (0, 64) and not dgamma.any() and not dbeta.any()
+
+
+@pytest.mark.parametrize("M", [64, 1003, 4096, 20001])
+def test_constant_rows_and_non_finite_values(native_lib, M):
+    """A constant row has variance 0; a NaN or an infinity spoils its own row only."""
+    x = torch.randn(6, M, generator=generator(M), device="cuda")
+    x[1] = 2.5
+    x[3, M // 2] = float("nan")
+    x[4, 0] = float("inf")
+    gamma, beta = torch.ones(M, device="cuda"), torch.full((M,), 0.25, device="cuda")
+    y, _, mean, rstd = block.layer_norm(x, gamma, beta)
+    assert torch.equal(y[1], beta) and abs(rstd[1].item() - 1e-5 ** -0.5) < 1e-4 * 1e-5 ** -0.5
+    assert torch.isnan(y[3]).all() and torch.isnan(y[4]).all()
+    ok = [0, 2, 5]
+    check_forward(x[ok], None, gamma, beta, 1e-5, (y[ok], None, mean[ok], rstd[ok]), torch.float32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [1003, 1024, 4096])
+def test_in_place(native_lib, dtype, M):
+    """y written over x and h over the residual, dx over dy: the results of separate buffers."""
+    gen, dt = generator(M), DT[dtype]
+    x, res = strided(50, M, 0, 0, dt, gen), strided(50, M, 0, 0, dt, gen)
+    gamma = torch.randn(M, generator=gen, device="cuda")
+    y, h, mean, rstd = block.layer_norm(x, gamma, residual=res)
+    x2, res2 = x.clone(), res.clone()
+    y2, h2, _, _ = block.layer_norm(x2, gamma, residual=res2, out=x2, h=res2)
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+    dy = strided(50, M, 0, 0, dt, gen)
+    dx, dg, db = block.layer_norm_backward(dy, h, gamma, mean, rstd, dh=y)
+    dx2, dg2, db2 = block.layer_norm_backward(dy, h, gamma, mean, rstd, dh=y, dx=dy)
+    assert torch.equal(dx, dx2) and torch.equal(dg, dg2) and torch.equal(db, db2)
+
+
+def test_repeatable_on_another_stream_and_in_a_graph(native_lib):
+    gen = generator(8)
+    x = strided(3000, 1024, 0, 0, torch.bfloat16, gen)
+    dy = strided(3000, 1024, 0, 0, torch.bfloat16, gen)
+    gamma = torch.randn(1024, generator=gen, device="cuda")
+    y, _, mean, rstd = block.layer_norm(x, gamma)
+    dx, dg, db = block.layer_norm_backward(dy, x, gamma, mean, rstd)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y2, _, m2, r2 = block.layer_norm(x, gamma, stream=side)
+    dx2, dg2, db2 = block.layer_norm_backward(dy, x, gamma, m2, r2, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in ((y, y2), (dx, dx2), (dg, dg2), (db, db2)):
+        assert torch.equal(a, b)
+    ws = block.layer_norm_workspace(3000, 1024)
+    bufs = [torch.zeros_like(t) for t in (y, mean, rstd, dx, dg, db)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        block.layer_norm(x, gamma, out=bufs[0], mean=bufs[1], rstd=bufs[2])
+        block.layer_norm_backward(dy, x, gamma, bufs[1], bufs[2], dx=bufs[3], dgamma=bufs[4], dbeta=bufs[5],
+                                  ws=ws)
+    for _ in range(2):
+        graph.replay()
+    for a, b in zip((y, mean, rstd, dx, dg, db), bufs):
+        assert torch.equal(a, b)
+
+
+def test_refusals(native_lib):
+    x = torch.zeros(4, 64, device="cuda", dtype=torch.bfloat16)
+    g = torch.ones(64, device="cuda")
+    bad = [lambda: block.layer_norm(x.half(), g), lambda: block.layer_norm(x, g.bfloat16()),
+           lambda: block.layer_norm(x, g[:32]), lambda: block.layer_norm(x.t(), torch.ones(4, device="cuda")),
+           lambda: block.layer_norm(x[:1].expand(4, 64), g), lambda: block.layer_norm(x, g, residual=x[:2]),
+           lambda: block.layer_norm(x, g, residual=x.float()), lambda: block.layer_norm(x, g, out=x.float()),
+           lambda: block.layer_norm(x, g.cpu()), lambda: block.layer_norm(x, g, mean=g),
+           lambda: block.layer_norm_backward(x, x, g, g, g),
+           lambda: block.layer_norm_backward(x, x, g, g[:4], g[:4], ws=g)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()

@@ -54,6 +54,11 @@ __global__ void __launch_bounds__(kThreadsN)
   }
 }
 
+// g = dy gamma, rounded: contracted into the sum and into g - mean(g) as multiply-adds, the two
+// uses would see different values, and a difference that is exactly zero (one column) would
+// leave a rounding error times rstd.
+__device__ __forceinline__ float product(float a, float b) { return __fmul_rn(a, b); }
+
 // One CTA a row: the two row sums, then dx.
 template <typename T>
 __global__ void __launch_bounds__(kThreadsN)
@@ -70,14 +75,14 @@ __global__ void __launch_bounds__(kThreadsN)
   const float mu = mean[r], rs = rstd[r];
   float s1 = 0.f, s2 = 0.f;
   for (int i = threadIdx.x; i < M; i += kThreadsN) {
-    const float g = to_f32(dr[i]) * gamma[i];
+    const float g = product(to_f32(dr[i]), gamma[i]);
     s1 += g;
     s2 = fmaf(g, (to_f32(hr[i]) - mu) * rs, s2);
   }
   s1 = block_sum_all<kWarpsN>(s1, s_red) / float(M);
   s2 = block_sum_all<kWarpsN>(s2, s_red + kWarpsN) / float(M);
   for (int i = threadIdx.x; i < M; i += kThreadsN) {
-    const float g = to_f32(dr[i]) * gamma[i];
+    const float g = product(to_f32(dr[i]), gamma[i]);
     const float xh = (to_f32(hr[i]) - mu) * rs;
     float o = rs * (g - s1 - xh * s2);
     if (dh) o += to_f32(dh[r * n.ldr + i]);
