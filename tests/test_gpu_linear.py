@@ -268,3 +268,19 @@ def test_stalled_pipeline_reports_a_timeout(native_lib):
     moe.set_wait_limit(ws, 0)
     y, _ = block.linear(x, W, bias, ws=ws)
     assert moe.device_status(ws) == 0 and torch.equal(y, good)
+
+
+@pytest.mark.parametrize("shape", [(2600, 1800, 1912), (2511, 1803, 1901), (4096, 2304, 1280), (20000, 136, 2056)])
+@pytest.mark.parametrize("act", ["none", "gelu", "silu"])
+def test_many_tiles(native_lib, shape, act):
+    """Products whose 256 x 256 tiles fill the GPU, in both directions; ragged last tiles."""
+    T, N, K = shape
+    gen, dt, x, W, bias = make(T, N, K, "bf16", 0, 0, 21)
+    res = strided(T, N, 0, 0, dt, gen)
+    y, pre = block.linear(x, W, bias, act=act, residual=res, save_pre=True)
+    check_forward(x, W, bias, act, res, (y, pre), dt)
+    y2, _ = block.linear(x, W, bias, act=act, residual=res, out=res)
+    assert torch.equal(y, y2)
+    dy = strided(T, N, 0, 0, dt, gen)
+    got = block.linear_backward(dy, x, W, act=act, pre=pre)
+    check_backward(dy, x, W, act, pre, got, dt, True)

@@ -1553,6 +1553,10 @@ int make_tma_map_strided(CUtensorMap* m, const void* base, int64_t rows, int64_t
   return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
 }
 
+int make_tma_map_out32(CUtensorMap* m, void* base, int64_t rows, int cols, int64_t ld) {
+  return make_map_bf16_out(m, base, rows, cols, ld, 32);
+}
+
 int make_tma_map_rows(CUtensorMap* m, const void* base, int64_t rows, int K, int box_rows) {
   return make_map(m, base, rows, K, box_rows);
 }

@@ -260,6 +260,9 @@ int make_tma_map_rows(CUtensorMap* m, const void* base, int64_t rows, int K, int
 // past cols and rows past rows read as zeros
 int make_tma_map_strided(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld,
                          int box_rows);
+// over a bf16 output [rows, cols >= 32] with row stride ld (a multiple of 8): boxes of 32 x 32
+// for TMA stores, 64-byte swizzle; a store clips at the ends
+int make_tma_map_out32(CUtensorMap* m, void* base, int64_t rows, int cols, int64_t ld);
 
 // simt_f32.cu : plain-FMA fp32 path for small layers.
 int launch_router_f32(const moe_config_t& c, const float* x, const float* W_g, const float* bias,

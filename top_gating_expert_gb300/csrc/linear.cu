@@ -53,7 +53,8 @@ __global__ void __launch_bounds__(kColThreads * kRowLanes)
 #pragma unroll
       for (int q = 0; q < VEC; ++q) {
         float v = to_f32(g.v[q]);
-        if constexpr (ACT != MOE_LIN_NONE) v *= act_slope<ACT>(to_f32(w.v[q]));
+        if constexpr (ACT != MOE_LIN_NONE)
+          v *= sizeof(T) == 2 ? slope_fast<ACT>(to_f32(w.v[q])) : act_slope<ACT>(to_f32(w.v[q]));
         acc[q] += v;
         o.v[q] = from_f32<T>(v);
       }

@@ -74,8 +74,7 @@ __device__ __forceinline__ void emit4(const LinearEpi& e, int64_t r, int64_t c, 
       if (q < n) v[q] += __ldg(e.bias + c + q);
   }
   if (e.pre) store4(e.pre, r * e.ldp + c, v, n);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) v[q] = act_any(e.act, v[q]);
+  act_fast_all(e.act, v);
   if (e.res) {
     const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(e.res) + r * e.ldr + c;
     if (n == 4 && aligned8(p)) {
@@ -325,6 +324,341 @@ int run_tile(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
   return MOE_OK;
 }
 
+// ------------------------------------------------------------------ large products
+// linear_pair_kernel: persistent, one cluster of two CTAs per pair of SMs, each walking output
+// tiles of 256 x BN (cta_group::2 MMAs: every CTA stages its 128 rows of A and its half of B's
+// BN rows, so an SM pulls 32 KB per 64-wide k-block for 128 x 256 outputs).
+//   warp 0      TMA producer; both CTAs' loads complete on the even CTA's `full` barrier
+//   warp 1      TMEM owner; the even CTA's issues the MMAs into one of two accumulators
+//   warps 2..9  epilogue, two warps per 32 TMEM lanes, each half of the columns: 32 columns at
+//               a time from TMEM through bias, activation and residual into a swizzled 32 x 32
+//               box in shared memory and out by a TMA store (two boxes a warp in turn). The
+//               next tile's MMAs run meanwhile.
+// Tiles are walked in bands of kBand tile rows, column by column, so that the tiles in
+// flight share their operands through L2.
+constexpr int kBand = 16;
+constexpr int kPairThreads = 64 + 32 * 8;
+
+struct PairArgs {
+  int rows, cols, nkb, tiles_m, tiles_n;
+  int a_mn, b_mn, res_vec;
+  LinearEpi e;
+  unsigned* status;
+};
+
+template <int BN>
+struct PairCfg {
+  static constexpr int A_BYTES = BM * BK * 2;
+  static constexpr int B_BYTES = BN / 2 * BK * 2;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int BOXES = 8 * 2 * 2048;  // 8 warps x 2 boxes of 32 x 32 bf16
+  static constexpr int STAGES = (232448 - 1024 - BOXES - 256) / STAGE > 8 ? 8 : (232448 - 1024 - BOXES - 256) / STAGE;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + BOXES + 256;
+  static constexpr int TMEM_COLS = 2 * BN;
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmP,
+                       const PairArgs p) {
+  using C = PairCfg<BN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + C::STAGES * C::A_BYTES;
+  uint8_t* sBox = sB + C::STAGES * C::B_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sBox + C::BOXES);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 5);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::STAGES;
+  const uint32_t tfull0 = empty0 + 8 * C::STAGES, tempty0 = tfull0 + 16, drain_bar = tempty0 + 16;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int unit = int(blockIdx.x >> 1), units = int(gridDim.x >> 1);
+  const int total = p.tiles_m * p.tiles_n;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull0 + 8 * a, 1);
+      mbar_init(tempty0 + 8 * a, 8 * 2);
+    }
+    mbar_init(drain_bar, 1);
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_map(&tmA);
+    tma_prefetch_map(&tmB);
+    tma_prefetch_map(&tmY);
+  }
+  if (warp == 1) tmem_alloc_pair(smem_u32(s_tmem), C::TMEM_COLS);
+  pdl_wait();
+  pdl_trigger();
+  const uint64_t wlimit = wait_limit_ns(p.status);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // barriers initialised in both CTAs
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  auto decode = [&](int t, int& m, int& n) {
+    const int per = kBand * p.tiles_n, band = t / per, r = t - band * per;
+    const int gm = min(kBand, p.tiles_m - band * kBand);
+    n = r / gm;
+    m = band * kBand + r - n * gm;
+  };
+
+  uint32_t issued = 0, issued_par = 0;
+  bool mma_any = false, mma_drained = false;
+  if (warp == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = unit; t < total && ok; t += units) {
+      int m, n;
+      decode(t, m, n);
+      const int arow = m * 2 * BM + int(rank) * BM, brow = n * BN + int(rank) * (BN / 2);
+      for (int kb = 0; kb < p.nkb; ++kb) {
+        ok = __all_sync(0xffffffffu, wait_bounded(empty0 + 8 * stage, phase ^ 1u, s_abort, p.status, wlimit));
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t fb = full0 + 8 * stage, bar = cluster_addr(fb, 0);
+          const uint32_t dA = smem_u32(sA + stage * C::A_BYTES), dB = smem_u32(sB + stage * C::B_BYTES);
+          if (leader) mbar_expect_tx(fb, 2 * C::STAGE);
+          if (p.a_mn) {
+            tma_load_2d_pair(dA, &tmA, arow, kb * BK, bar);
+            tma_load_2d_pair(dA + 8192, &tmA, arow + 64, kb * BK, bar);
+          } else {
+            tma_load_2d_pair(dA, &tmA, kb * BK, arow, bar);
+          }
+          if (p.b_mn) {
+#pragma unroll
+            for (int b = 0; b < BN / 128; ++b)
+              tma_load_2d_pair(dB + b * 8192, &tmB, brow + 64 * b, kb * BK, bar);
+          } else {
+            tma_load_2d_pair(dB, &tmB, kb * BK, brow, bar);
+          }
+        }
+        __syncwarp();
+        issued |= 1u << stage;
+        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (leader) {
+      const uint32_t idesc = idesc_bf16(2 * BM, BN) | (p.a_mn ? 1u << 15 : 0u) | (p.b_mn ? 1u << 16 : 0u);
+      // descriptors of stage 0; a stage and a K step of 16 advance the address field (16-byte
+      // units): 32 bytes along a swizzled row (K-major), 16 K rows of 128 bytes (MN-major)
+      const uint64_t ad0 = p.a_mn ? mn_sw128_desc(smem_u32(sA)) : sw128_desc(smem_u32(sA));
+      const uint64_t bd0 = p.b_mn ? mn_sw128_desc(smem_u32(sB)) : sw128_desc(smem_u32(sB));
+      const uint32_t astep = p.a_mn ? 128 : 2, bstep = p.b_mn ? 128 : 2;
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int i = 0;
+      for (int t = unit; t < total && ok; t += units, ++i) {
+        const int acc = i & 1;
+        const uint32_t use = uint32_t(i >> 1) & 1u;
+        ok = __all_sync(0xffffffffu, wait_bounded(tempty0 + 8 * acc, use ^ 1u, s_abort, p.status, wlimit));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + uint32_t(acc * BN);
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          ok = __all_sync(0xffffffffu, wait_bounded(full0 + 8 * stage, phase, s_abort, p.status, wlimit));
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t ad = ad0 + uint64_t(stage * (C::A_BYTES >> 4));
+            const uint64_t bd = bd0 + uint64_t(stage * (C::B_BYTES >> 4));
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk)
+              mma_bf16_pair(d, ad + kk * astep, bd + kk * bstep, idesc, (kb | kk) != 0 ? 1u : 0u);
+            mma_commit_pair(empty0 + 8 * stage, uint16_t(3));
+          }
+          __syncwarp();
+          mma_any = true;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok && lane == 0) mma_commit_pair(tfull0 + 8 * acc, uint16_t(3));
+        __syncwarp();
+      }
+      if (!ok && mma_any && lane == 0) {  // every MMA issued must finish before TMEM is freed
+        mma_commit_pair(drain_bar, uint16_t(1));
+        wait_drain(drain_bar, 0u);
+      }
+      mma_drained = !ok && mma_any;
+      __syncwarp();
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tempty_leader = cluster_addr(tempty0, 0);
+    uint8_t* box = sBox + (warp - 2) * 4096;
+    int nb = 0;
+    int i = 0;
+    auto put = [&](const CUtensorMap* map, const float (&v)[32], int col, int row) {
+      if (lane == 0) bulk_wait_read<1>();  // the store that last used this box has read it
+      __syncwarp();
+      uint8_t* b = box + nb * 2048;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4*>(b + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(pack_bf16x2(v[8 * c], v[8 * c + 1]), pack_bf16x2(v[8 * c + 2], v[8 * c + 3]),
+                       pack_bf16x2(v[8 * c + 4], v[8 * c + 5]), pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(map, col, row, smem_u32(b));
+        bulk_commit();
+      }
+      nb ^= 1;
+    };
+    for (int t = unit; t < total; t += units, ++i) {
+      const int acc = i & 1;
+      const uint32_t use = uint32_t(i >> 1) & 1u;
+      int m, n;
+      decode(t, m, n);
+      const bool ok = __all_sync(0xffffffffu, wait_bounded(tfull0 + 8 * acc, use, s_abort, p.status, wlimit));
+      if (!ok) break;
+      tc_fence_after();
+      const int row0 = m * 2 * BM + int(rank) * BM + 32 * q, row = row0 + lane;
+      const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
+      const int cb = half * (BN / 2);
+#pragma unroll 1
+      for (int c0 = cb; c0 < cb + BN / 2; c0 += 32) {
+        const int col = n * BN + c0;
+        if (row0 >= p.rows || col >= p.cols) break;  // warp-uniform: nothing of this part exists
+        uint32_t acc32[32];
+        tmem_ld16(tbase + c0, *reinterpret_cast<uint32_t(*)[16]>(acc32));
+        tmem_ld16(tbase + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(acc32 + 16));
+        const __nv_bfloat16* rp = static_cast<const __nv_bfloat16*>(p.e.res);
+        uint4 rv[4];
+        const bool rvec = p.res_vec && row < p.rows && col + 32 <= p.cols;
+        if (rvec) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) rv[c] = *reinterpret_cast<const uint4*>(rp + row * p.e.ldr + col + 8 * c);
+        }
+        const float bias = p.e.bias && col + lane < p.cols ? __ldg(p.e.bias + col + lane) : 0.f;
+        tmem_ld_wait();
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(acc32[j]);
+        if (p.e.bias) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, bias, j);
+        }
+        if (p.e.pre) put(&tmP, v, col, row0);
+        act_fast_all(p.e.act, v);
+        if (rvec) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t w[4] = {rv[c].x, rv[c].y, rv[c].z, rv[c].w};
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[h]));
+              v[8 * c + 2 * h] += f.x;
+              v[8 * c + 2 * h + 1] += f.y;
+            }
+          }
+        } else if (rp && row < p.rows) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (col + j < p.cols) v[j] += __bfloat162float(rp[row * p.e.ldr + col + j]);
+        }
+        put(&tmY, v, col, row0);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * acc);
+    }
+    if (lane == 0) bulk_wait_all();  // the boxes are read before shared memory goes away
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*s_abort) {
+    // loads issued land and MMAs issued finish before shared and tensor memory go away
+    if (warp == 0 && leader && lane == 0)
+      for (int s = 0; s < C::STAGES; ++s)
+        if ((issued >> s) & 1u) wait_drain(full0 + 8 * s, (issued_par >> s) & 1u);
+    if (warp == 1 && leader && lane == 0 && mma_any && !mma_drained) {
+      mma_commit_pair(drain_bar, uint16_t(1));
+      wait_drain(drain_bar, 0u);
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  cluster_sync_all();  // both CTAs done with TMEM and each other's barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, C::TMEM_COLS);
+  }
+}
+
+bool out_aligned(const void* p, int64_t ld) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0);
+}
+
+template <int BN>
+int run_pair(const LinearOperand& A, const LinearOperand& B, int rows, int cols, int K, const LinearEpi& e,
+             unsigned* status, cudaStream_t st) {
+  using C = PairCfg<BN>;
+  CUtensorMap ta, tb, ty, tp;
+  int rc;
+  if ((rc = map_operand(&ta, A, rows, K, BM)) != MOE_OK) return rc;
+  if ((rc = map_operand(&tb, B, cols, K, BN / 2)) != MOE_OK) return rc;
+  if ((rc = make_tma_map_out32(&ty, e.out, rows, cols, e.ldo)) != MOE_OK) return rc;
+  tp = ty;
+  if (e.pre && (rc = make_tma_map_out32(&tp, e.pre, rows, cols, e.ldp)) != MOE_OK) return rc;
+  PairArgs p;
+  p.rows = rows; p.cols = cols;
+  p.nkb = (K + BK - 1) / BK;
+  p.tiles_m = (rows + 2 * BM - 1) / (2 * BM);
+  p.tiles_n = (cols + BN - 1) / BN;
+  if (int64_t(p.tiles_m) * p.tiles_n > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+  p.a_mn = A.mn; p.b_mn = B.mn;
+  p.res_vec = e.res && out_aligned(e.res, e.ldr);
+  p.e = e;
+  p.status = status;
+  auto kern = linear_pair_kernel<BN>;
+  MOE_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+  cudaLaunchConfig_t lc = {};
+  lc.blockDim = dim3(kPairThreads);
+  lc.dynamicSmemBytes = C::SMEM;
+  lc.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  lc.gridDim = dim3(2);
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, kern, &lc) != cudaSuccess || clusters < 1)
+    clusters = num_sms() / 2;
+  lc.gridDim = dim3(unsigned(2 * std::min(clusters, p.tiles_m * p.tiles_n)));
+  if (pdl_enabled()) {
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.numAttrs = 2;
+  }
+  MOE_CUDA_CHECK(cudaLaunchKernelEx(&lc, kern, ta, tb, ty, tp, p));
+  return MOE_OK;
+}
+
 // K splits for `tiles` tiles: the power of two (at most 8, the portable cluster) that brings
 // the CTAs closest to one wave, with at least four k-blocks each.
 int pick_splits(int64_t tiles, int K) {
@@ -345,6 +679,11 @@ int launch_linear_bf16(const LinearOperand& A, const LinearOperand& B, int rows,
     if (rows <= 32) return run_tile<32, true>(B, A, cols, rows, K, s, e, status, st);
     return run_tile<64, true>(B, A, cols, rows, K, s, e, status, st);
   }
+  // 256-wide pair tiles once they fill the SM pairs; their outputs leave by TMA stores, which
+  // need 16-byte rows
+  const int64_t pairs = ((int64_t(rows) + 255) / 256) * ((int64_t(cols) + 255) / 256);
+  if (pairs * 2 >= num_sms() / 2 && cols >= 128 && out_aligned(e.out, e.ldo) && out_aligned(e.pre, e.ldp))
+    return run_pair<256>(A, B, rows, cols, K, e, status, st);
   const int64_t tiles = wide * ((int64_t(rows) + BM - 1) / BM);
   return run_tile<128, false>(A, B, rows, cols, K, pick_splits(tiles, K), e, status, st);
 }
