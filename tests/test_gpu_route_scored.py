@@ -175,3 +175,33 @@ def test_repeatable_in_a_graph_and_on_another_stream(native_lib):
         n = R if f in ("token_of", "w_perm") else None
         np.testing.assert_array_equal(a[f][:n], b[f][:n])
         np.testing.assert_array_equal(a[f][:n], c[f][:n])
+
+
+@pytest.mark.parametrize("kind", range(len(KINDS)))
+def test_chosen_by_bias_alone(native_lib, kind):
+    """Biases that put experts of vanishing score in front: their renormalised weights are still
+    the ratios of those scores."""
+    rng = np.random.default_rng(kind)
+    cfg = _cfg(70, E=64, k=4)
+    logits = rng.standard_normal((70, 64)).astype(np.float32)
+    logits[:, 10:20] = -95.0 - rng.random((70, 10))
+    bias = np.where((np.arange(64) >= 10) & (np.arange(64) < 20), 3.0 + np.arange(64) / 64, 0.0).astype(np.float32)
+    score = KINDS[kind]
+    out, status, _ = gpu(cfg, score, logits, bias)
+    o = SC.route(logits, bias, cfg, score)
+    r = route_np(out)
+    np.testing.assert_array_equal(r["expert_id"], o["expert_id"])
+    # un-normalised, these scores lie below the smallest normal fp32 (2^-126)
+    np.testing.assert_allclose(r["gate"], o["gate"], rtol=400 * U, atol=2.0 ** -126)
+
+
+@pytest.mark.parametrize("E,k,ng,tg", [(256, 8, 8, 4), (64, 2, 0, 0), (200, 8, 8, 3), (32, 4, 0, 0)])
+def test_wide_range_of_biases(native_lib, E, k, ng, tg):
+    """Large, small and negative biases; scores far apart and close together in one batch."""
+    rng = np.random.default_rng(E)
+    cfg = _cfg(500, E=E, k=k, ng=ng, tg=tg)
+    for scale in (1e-6, 1.0, 300.0):
+        for shift in (-5.0, 0.0, 5.0):
+            logits = rng.standard_normal((500, E)) * 2 + shift
+            bias = (scale * rng.standard_normal(E)).astype(np.float32)
+            check(cfg, KINDS[2], logits, bias, f"{scale} {shift}")

@@ -57,6 +57,7 @@ struct RouteArgs {
   float gate_p;
   int ng, tg, gsz;  // expert groups (ng > 1: group-limited), groups kept, experts a group
   int uniform;      // ids replaced by (t*k + j) mod E
+  unsigned gm24 = 0;  // scored routing: expert e's group is (e * gm24) >> 24 (0: no groups)
 };
 
 // Arguments of the fused router kernel beyond RouteArgs.

@@ -7,13 +7,18 @@
 //
 // The choices are those of the scores evaluated in fp64: sigmoid and softmax scores lie close
 // together where they saturate, and an order decided in fp32 would depend on the last bits
-// of an exponential. Equal fp64 scores rank the lower expert (or group).
+// of an exponential. Equal fp64 scores rank the lower expert (or group). fp64 runs at 1/64 of
+// the fp32 rate, so a token's scores are first formed in fp32 with a bound on their error; only
+// when two values that decide (neighbours among the k + 1 best, the last group kept and the
+// first one not) lie within that bound is the token taken again in fp64 (choose_fp64). All
+// tokens in fp64 took 1640 us for 16384 tokens of 256 experts, top-8 in 4 of 8 groups.
 //
 // One CTA per chunk of 128 tokens of one group, a warp per token, lane l holding the experts
-// l, l + 32, .. (at most 8). The CTA then ranks its choices per (choice rank, expert) with warp
-// matches and a scan over warps, and writes the chunk's histograms, routed counts and loss
-// sums in the form that the scan and finalize kernels of the default routing take
-// (route.cu). Every sum has a fixed order.
+// l, l + 32, .. (Q = 1, 2, 4 or 8 of them). The CTA then ranks its choices per (choice rank,
+// expert) with warp matches and a scan over warps, and writes the chunk's histograms, routed
+// counts and loss sums in the form that the scan and finalize kernels of the default routing
+// take (route.cu). A batch of one chunk (a serving step) is finished by the same CTA: one
+// launch instead of three. Every sum has a fixed order.
 #include <algorithm>
 
 #include "route_kernels.cuh"
@@ -21,7 +26,7 @@
 namespace moe {
 namespace {
 
-constexpr int kTokWarps = 8;
+constexpr int kTokWarps = 16;
 constexpr int kTokThreads = 32 * kTokWarps;
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -53,30 +58,31 @@ __device__ __forceinline__ float sigmoid_shifted(float l, float m) {
 // A token's choices by the fp64 scores: lane j < k gets the j-th one's index. l: the lane's
 // logits (-inf where the expert is out), own: its experts that exist, row: E doubles of this
 // warp in shared memory.
-__device__ __noinline__ int choose_fp64(const float (&l)[8], const RouteArgs& a, const ScoreArgs& sc,
+template <int Q>
+__device__ __noinline__ int choose_fp64(const float (&l)[Q], const RouteArgs& a, const ScoreArgs& sc,
                                         double* row) {
   const int lane = threadIdx.x & 31, E = a.E;
-  double c[8];
+  double c[Q];
   if (sc.sigmoid) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) c[q] = 1.0 / (1.0 + exp(-double(l[q])));
+    for (int q = 0; q < Q; ++q) c[q] = 1.0 / (1.0 + exp(-double(l[q])));
   } else {
     float mf = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) mf = fmaxf(mf, l[q]);
+    for (int q = 0; q < Q; ++q) mf = fmaxf(mf, l[q]);
     const double m = double(warp_max(mf));
     double s = 0.0;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < Q; ++q) {
       c[q] = l[q] > -INFINITY ? exp(double(l[q]) - m) : 0.0;
       s += c[q];
     }
     s = warp_sum(s);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) c[q] = c[q] / s;
+    for (int q = 0; q < Q; ++q) c[q] = c[q] / s;
   }
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
+  for (int q = 0; q < Q; ++q) {
     const int e = lane + 32 * q;
     const float b = sc.bias && e < E ? __ldg(sc.bias + e) : 0.f;
     c[q] = l[q] > -INFINITY && isfinite(b) ? c[q] + double(b) : -INFINITY;
@@ -84,7 +90,7 @@ __device__ __noinline__ int choose_fp64(const float (&l)[8], const RouteArgs& a,
   unsigned groups = kFull;
   if (a.ng > 1) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
+    for (int q = 0; q < Q; ++q)
       if (lane + 32 * q < E) row[lane + 32 * q] = c[q];
     __syncwarp();
     double gs = -INFINITY;
@@ -111,7 +117,7 @@ __device__ __noinline__ int choose_fp64(const float (&l)[8], const RouteArgs& a,
   }
   unsigned open = 0u;  // bit q: expert lane + 32 q may still be chosen
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
+  for (int q = 0; q < Q; ++q) {
     const int e = lane + 32 * q;
     if (e < E && (a.ng <= 1 || ((groups >> (e / a.gsz)) & 1u))) open |= 1u << q;
   }
@@ -120,7 +126,7 @@ __device__ __noinline__ int choose_fp64(const float (&l)[8], const RouteArgs& a,
     double bv = -INFINITY;
     int bi = 0x7fffffff;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < Q; ++q) {
       const int e = lane + 32 * q;
       if (((open >> q) & 1u) && (c[q] > bv || (c[q] == bv && e < bi))) {
         bv = c[q];
@@ -161,9 +167,217 @@ __device__ __forceinline__ float choice_weight(float lsel, bool on, const ScoreA
   return w * sc.scale;
 }
 
-__global__ void __launch_bounds__(kTokThreads) route_scored_kernel(RouteArgs a, ScoreArgs sc) {
-  extern __shared__ double s_dyn[];  // [8 warps][E] group scratch, then the counts [k][4][E]
-  __shared__ float s_pp[kTokWarps][kMaxE];
+// Order-preserving map of a float to unsigned and back (finite values).
+__device__ __forceinline__ unsigned order_key(float v) {
+  const unsigned b = __float_as_uint(v);
+  return b ^ (unsigned(int(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(unsigned k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+// The loss terms and choice of one token in the general form: any finite logits, -inf where an
+// expert is out. q: the normalised scores.
+template <int Q>
+__device__ __noinline__ int token_general(const float (&l)[Q], const float* lr, const RouteArgs& a,
+                                          const ScoreArgs& sc, double* row, float (&q)[Q], float& lse,
+                                          float& w) {
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) m = fmaxf(m, l[i]);
+  m = warp_max(m);
+  const bool any = m > -INFINITY;
+  if (!any) m = 0.f;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    q[i] = expf(l[i] - m);
+    s += q[i];
+  }
+  s = warp_sum(s);
+  lse = any ? m + logf(s) : 0.f;
+  const float inv = s > 0.f ? 1.f / s : 0.f;
+  float ti = inv;
+  if (sc.sigmoid) {
+    const float top = fminf(m, 0.f);
+    float tot = 0.f;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      q[i] = sigmoid_shifted(l[i], top);
+      tot += q[i];
+    }
+    tot = warp_sum(tot);
+    ti = tot > 0.f ? 1.f / tot : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < Q; ++i) q[i] *= ti;
+  const int id = choose_fp64<Q>(l, a, sc, row);
+  float lsel = -INFINITY;
+  if (lane < a.k) {
+    lsel = __ldg(lr + id);
+    if (!isfinite(lsel) || (sc.bias && !isfinite(__ldg(sc.bias + id)))) lsel = -INFINITY;
+  }
+  w = choice_weight(lsel, lane < a.k, sc, m, inv);
+  return id;
+}
+
+// The two best keys of every group of 32 m experts (lane-strided experts: slots m g .. of all
+// lanes), summed (or the best alone), left in lane g. Equal best keys count twice, as they
+// should.
+template <int Q>
+__device__ __forceinline__ float group_scores_wide(const unsigned (&key)[Q], const RouteArgs& a,
+                                                   const ScoreArgs& sc) {
+  const int lane = threadIdx.x & 31, per = a.gsz >> 5;
+  float gs = -INFINITY;
+  for (int g = 0; g < a.ng; ++g) {
+    unsigned b1 = 0u, b2 = 0u;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      if (i / per != g) continue;
+      const unsigned v = key[i];
+      b2 = max(b2, min(b1, v));
+      b1 = max(b1, v);
+    }
+    const unsigned m1 = __reduce_max_sync(kFull, b1);
+    float v = order_value(m1 & ~7u);
+    if (sc.gtop == 2) {
+      const unsigned own = __ballot_sync(kFull, b1 == m1);
+      const unsigned second = lane == __ffs(own) - 1 ? b2 : b1;
+      v += order_value(__reduce_max_sync(kFull, second) & ~7u);
+    }
+    if (lane == g) gs = v;
+  }
+  return gs;
+}
+
+// The same for any group size, through this warp's row of shared memory: lane g walks its group
+// from a rotated start (the lanes then fall on different banks).
+template <int Q>
+__device__ __forceinline__ float group_scores_any(const float (&c)[Q], const RouteArgs& a,
+                                                  const ScoreArgs& sc, float* row) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < Q; ++i)
+    if (lane + 32 * i < a.E) row[lane + 32 * i] = c[i];
+  __syncwarp();
+  float b1 = -INFINITY, b2 = -INFINITY;
+  if (lane < a.ng) {
+    int r = lane % a.gsz;
+    for (int i = 0; i < a.gsz; ++i) {
+      const float v = row[lane * a.gsz + r];
+      b2 = fmaxf(b2, fminf(b1, v));
+      b1 = fmaxf(b1, v);
+      r = r + 1 == a.gsz ? 0 : r + 1;
+    }
+  }
+  __syncwarp();
+  return sc.gtop == 2 && a.gsz > 1 ? b1 + b2 : b1;
+}
+
+// A token in fp32: false when a decision lies within the error bound (or the values leave the
+// range the bound holds for), and the caller takes token_general. With x = __expf(l) (relative
+// error (2 + 1.2 |l|) 2^-23), s = sum x in (e^-20, e^20):
+//   sigmoid x / (1 + x): |l| sigma (1 - sigma) <= 0.224 and 2 ulp of the division bound the
+//     error by 2.5 * 2^-23, and by 27 * 2^-23 of the score where all are small (|l| < 20);
+//   softmax x / s: by (13 + 3 * 20) * 2^-23 of the score.
+// The bias adds half an ulp, and the keys drop 3 bits for the slot number: at most 2^-20 of the
+// largest selection value in all.
+template <int Q>
+__device__ __forceinline__ bool token_fast(const float (&l)[Q], const float (&b)[Q], float bmax,
+                                           const RouteArgs& a, const ScoreArgs& sc, float* row,
+                                           float (&q)[Q], float& lse, int& id) {
+  const int lane = threadIdx.x & 31;
+  constexpr float kU = 1.1920929e-7f;  // 2^-23
+  float s = 0.f, tot = 0.f, qm = 0.f;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const float x = __expf(l[i]);  // -inf (no expert): 0
+    s += x;
+    q[i] = sc.sigmoid ? __fdividef(x, 1.f + x) : x;
+    tot += q[i];
+    qm = fmaxf(qm, q[i]);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    s += __shfl_xor_sync(kFull, s, off);
+    tot += __shfl_xor_sync(kFull, tot, off);
+  }
+  if (!(s > 2.1e-9f && s < 4.8e8f)) return false;
+  lse = logf(s);
+  const float ti = __fdividef(1.f, tot);
+  qm = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(qm)));  // >= 0
+  float err;
+  if (sc.sigmoid) {
+    err = fminf(2.5f, 27.f * qm) * kU;
+  } else {
+    qm *= ti;
+    err = 73.f * qm * kU;
+  }
+  const float cmax = qm + bmax;
+  const float gap = 2.f * err + 1.1f * 8.f * kU * cmax;  // 2^-20 and the rounding of c
+
+  float c[Q];
+  unsigned key[Q];
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const float sv = sc.sigmoid ? q[i] : q[i] * ti;
+    q[i] *= ti;
+    c[i] = sv + b[i];
+    key[i] = lane + 32 * i < a.E ? ((order_key(c[i]) & ~7u) | unsigned(i)) : 0u;
+  }
+  if (a.ng > 1) {
+    const float gs = (a.gsz & 31) == 0 ? group_scores_wide<Q>(key, a, sc) : group_scores_any<Q>(c, a, sc, row);
+    int before = 0;
+    for (int h = 0; h < a.ng; ++h) {
+      const float vh = __shfl_sync(kFull, gs, h);
+      if (vh > gs || (vh == gs && h < lane)) ++before;
+    }
+    const bool mine = lane < a.ng, kept = mine && before < a.tg;
+    if (a.tg < a.ng) {  // the last group kept and the first one not, 2 err each way apart
+      const unsigned lo = __reduce_min_sync(kFull, kept ? order_key(gs) : 0xffffffffu);
+      const unsigned hi = __reduce_max_sync(kFull, mine && !kept ? order_key(gs) : 0u);
+      if (!(order_value(lo) - order_value(hi) > 2.f * gap + 4.f * kU * cmax)) return false;
+    }
+    const unsigned groups = __ballot_sync(kFull, kept);
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      const int e = lane + 32 * i;
+      const int g = int((unsigned(e) * a.gm24) >> 24);
+      if (!((groups >> g) & 1u)) key[i] = 0u;
+    }
+  }
+  unsigned lk = 0u;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) lk = max(lk, key[i]);
+  float prev = INFINITY;
+  id = 0;
+  for (int j = 0; j <= a.k; ++j) {
+    const unsigned top = __reduce_max_sync(kFull, lk);
+    if (top == 0u) break;  // j == k: no expert is left
+    const unsigned own = __ballot_sync(kFull, lk == top);
+    const float v = order_value(top & ~7u);
+    if (!(prev - v > gap) || (own & (own - 1u))) return false;
+    prev = v;
+    if (j == a.k) break;
+    const int owner = __ffs(own) - 1;
+    if (lane == j) id = owner + 32 * int(top & 7u);
+    const bool pop = lane == owner;
+    lk = 0u;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      if (pop && key[i] == top) key[i] = 0u;
+      lk = max(lk, key[i]);
+    }
+  }
+  return true;
+}
+
+template <int Q, bool ONE>
+__global__ void __launch_bounds__(kTokThreads, 1) route_scored_kernel(RouteArgs a, ScoreArgs sc) {
+  // [warps][E] doubles of group scratch, then [warps][E] probability sums, then the counts
+  // [k][4][E]
+  extern __shared__ double s_dyn[];
   __shared__ float s_z[kTokWarps];
   __shared__ uint8_t s_id[kThreads * kMaxK];
   __shared__ uint8_t s_rk[kThreads * kMaxK];
@@ -177,87 +391,99 @@ __global__ void __launch_bounds__(kTokThreads) route_scored_kernel(RouteArgs a, 
   pdl_trigger();
   if (c == 0 && tid == 0) *a.done = 0u;  // ticket counter of route_scan_kernel
 
-  if (sc.bias && tid < E && !isfinite(__ldg(sc.bias + tid))) atomicOr(a.status, kStatusNonfinite);
-  float pp[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float b[Q];
+  float bmax = 0.f;
+  bool bias_bad = false;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int e = lane + 32 * i;
+    b[i] = sc.bias && e < E ? __ldg(sc.bias + e) : 0.f;
+    if (!isfinite(b[i])) bias_bad = true;
+    bmax = fmaxf(bmax, fabsf(b[i]));
+  }
+  bias_bad = __any_sync(kFull, bias_bad);
+  bmax = warp_max(bmax);
+  if (bias_bad && tid == 0) atomicOr(a.status, kStatusNonfinite);
+  double* scratch = s_dyn + size_t(warp) * E;
+  float pp[Q];
+#pragma unroll
+  for (int i = 0; i < Q; ++i) pp[i] = 0.f;
   float zacc = 0.f;
+  float next[Q];
+  auto fetch = [&](int i) {
+#pragma unroll
+    for (int x = 0; x < Q; ++x) {
+      const int e = lane + 32 * x;
+      next[x] = (i < nt && e < E) ? __ldg(a.logits + int64_t(t0 + i) * E + e) : -INFINITY;
+    }
+  };
+  fetch(warp);
   for (int i = warp; i < nt; i += kTokWarps) {
     const int64_t t = t0 + i;
-    const float* lr = a.logits + t * E;
-    float l[8];
+    float l[Q], q[Q];
     bool bad = false;
-    float m = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int e = lane + 32 * q;
-      l[q] = -INFINITY;
-      if (e < E) {
-        const float v = __ldg(lr + e);
-        if (isfinite(v)) l[q] = v;
-        else bad = true;
+    for (int x = 0; x < Q; ++x) {
+      l[x] = next[x];
+      if (lane + 32 * x < E && !isfinite(l[x])) {
+        bad = true;
+        l[x] = -INFINITY;
       }
-      m = fmaxf(m, l[q]);
     }
-    if (bad) atomicOr(a.status, kStatusNonfinite);
-    m = warp_max(m);
-    const bool any = m > -INFINITY;
-    if (!any) m = 0.f;
-    // logsumexp, and the normalised scores for the balance loss
-    float x[8], s = 0.f;
+    fetch(i + kTokWarps);  // the warp's next token, while this one is worked on
+    bad = __any_sync(kFull, bad);
+    float lse, w;
+    int id;
+    const float* lr = a.logits + t * E;
+    bool fast = !bad && !bias_bad &&
+                token_fast<Q>(l, b, bmax, a, sc, reinterpret_cast<float*>(scratch), q, lse, id);
+    if (fast) {  // the weights, from accurate exponentials of the choices' logits (lanes j < k)
+      const float ls = lane < k ? __ldg(lr + id) : 0.f;
+      if (sc.renorm) {
+        w = lane < k ? (sc.sigmoid ? sigmoid_shifted(ls, 0.f) : expf(ls)) : 0.f;
+        float tot = w;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      x[q] = expf(l[q] - m);
-      s += x[q];
-    }
-    s = warp_sum(s);
-    const float lse = any ? m + logf(s) : 0.f;
-    const float inv = s > 0.f ? 1.f / s : 0.f;
-    if (sc.sigmoid) {
-      const float top = fminf(m, 0.f);
-      float tot = 0.f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        x[q] = sigmoid_shifted(l[q], top);
-        tot += x[q];
+        for (int off = 4; off > 0; off >>= 1) tot += __shfl_xor_sync(kFull, tot, off);
+        tot = __shfl_sync(kFull, tot, 0);
+        fast = tot > 1e-30f;  // else chosen by their biases, with scores that underflow
+        w = w / tot;
+      } else {
+        w = sc.sigmoid ? sigmoid_shifted(ls, 0.f) : expf(ls - lse);
       }
-      tot = warp_sum(tot);
-      const float ti = tot > 0.f ? 1.f / tot : 0.f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) pp[q] += x[q] * ti;
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) pp[q] += x[q] * inv;
+      w *= sc.scale;
     }
+    if (!fast) {
+      if (bad && lane == 0) atomicOr(a.status, kStatusNonfinite);
+      id = token_general<Q>(l, lr, a, sc, scratch, q, lse, w);
+    }
+#pragma unroll
+    for (int x = 0; x < Q; ++x) pp[x] += q[x];
     zacc += lse * lse;
-    const int id = choose_fp64(l, a, sc, s_dyn + size_t(warp) * E);
-    // lane j's logit of choice j
-    float lsel = -INFINITY;
-    if (lane < k) {
-      lsel = __ldg(lr + id);
-      if (!isfinite(lsel) || (sc.bias && !isfinite(__ldg(sc.bias + id)))) lsel = -INFINITY;
-    }
-    const float w = choice_weight(lsel, lane < k, sc, m, inv);
     if (lane < k) {
       a.expert_id[t * k + lane] = id;
       a.gate[t * k + lane] = w;
       s_id[i * kMaxK + lane] = uint8_t(id);
     }
   }
+  __syncthreads();  // the group scratch is free
+  float* s_pp = reinterpret_cast<float*>(s_dyn);
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
-    if (lane + 32 * q < E) s_pp[warp][lane + 32 * q] = pp[q];
+  for (int i = 0; i < Q; ++i)
+    if (lane + 32 * i < E) s_pp[warp * E + lane + 32 * i] = pp[i];
   if (lane == 0) s_z[warp] = zacc;
   __syncthreads();
-  for (int e = tid; e < E; e += kTokThreads) {
-    float sum = 0.f;
+  float psum = 0.f;  // of expert tid
+  if (tid < E) {
 #pragma unroll
-    for (int w = 0; w < kTokWarps; ++w) sum += s_pp[w][e];
-    a.ppart[size_t(c) * E + e] = sum;
+    for (int w = 0; w < kTokWarps; ++w) psum += s_pp[w * E + tid];
+    if (!ONE) a.ppart[size_t(c) * E + tid] = psum;
   }
+  float sz = 0.f;
   if (tid == 0) {
-    float sz = 0.f;
     for (int w = 0; w < kTokWarps; ++w) sz += s_z[w];
-    a.zpart[c] = sz;
+    if (!ONE) a.zpart[c] = sz;
   }
+  __syncthreads();
 
   // rank of each choice among the chunk's earlier ones of the same (j, e): the first
   // kThreads threads hold a token each; counts per (j, warp, e), one scan over the warps
@@ -276,29 +502,92 @@ __global__ void __launch_bounds__(kTokThreads) route_scored_kernel(RouteArgs a, 
     }
   }
   __syncthreads();
-  for (int x = tid; x < k * E; x += kTokThreads) {
-    const int j = x / E, e = x - j * E;
-    int run = 0;
+  if constexpr (!ONE) {
+    for (int x = tid; x < E; x += kTokThreads) {  // choice ranks in order: expert x's columns
+      int all = 0;
+      for (int j = 0; j < k; ++j) {
+        int run = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      int* cw = s_cnt + (j * kWarps + w) * E + e;
-      const int v = *cw;
-      *cw = run;
-      run += v;
+        for (int w = 0; w < kWarps; ++w) {
+          int* cw = s_cnt + (j * kWarps + w) * E + x;
+          const int v = *cw;
+          *cw = run;
+          run += v;
+        }
+        a.hist[(size_t(c) * k + j) * E + x] = run;
+        all += run;
+      }
+      a.hroute[size_t(c) * E + x] = all;  // every choice is a candidate
     }
-    a.hist[(size_t(c) * k + j) * E + e] = run;
-  }
-  __syncthreads();
-  if (tid < nt) {
-    for (int j = 0; j < k; ++j) {
-      const int e = int(s_id[tid * kMaxK + j]);
-      a.rank[size_t(t0 + tid) * k + j] = s_cnt[(j * kWarps + warp) * E + e] + int(s_rk[tid * kMaxK + j]);
+    __syncthreads();
+    for (int x = tid; x < nt * k; x += kTokThreads) {
+      const int i = x / k, j = x - i * k;
+      const int e = int(s_id[i * kMaxK + j]);
+      a.rank[size_t(t0) * k + x] = s_cnt[(j * kWarps + (i >> 5)) * E + e] + int(s_rk[i * kMaxK + j]);
     }
-  }
-  for (int e = tid; e < E; e += kTokThreads) {
-    int run = 0;  // every choice is a candidate: the routed counts are the histograms' sums
-    for (int j = 0; j < k; ++j) run += a.hist[(size_t(c) * k + j) * E + e];
-    a.hroute[size_t(c) * E + e] = run;
+  } else {
+    // the whole batch is here: slots, offsets, rows and losses as the scan and finalize
+    // kernels form them
+    __shared__ int s_first[kMaxE], s_wsum[kMaxE / 32];
+    __shared__ float s_aux[kMaxE / 32];
+    int all = 0, kept = 0;
+    if (tid < E) {
+      for (int j = 0; j < k; ++j)
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          int* cw = s_cnt + (j * kWarps + w) * E + tid;
+          const int v = *cw;
+          *cw = all;
+          all += v;
+        }
+      kept = a.C >= 0 && all > a.C ? a.C : all;
+      a.counts[tid] = kept;
+      a.counts_routed[tid] = all;
+    }
+    int inc = kept;
+    float aux = tid < E ? float(all) * psum : 0.f;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(kFull, inc, off);
+      if (lane >= off) inc += v;
+    }
+    aux = warp_sum(aux);
+    if (warp < kMaxE / 32) {
+      if (lane == 31) s_wsum[warp] = inc;
+      if (lane == 0) s_aux[warp] = aux;
+    }
+    __syncthreads();
+    if (tid < E) {
+      int base = 0;
+      for (int w = 0; w < warp; ++w) base += s_wsum[w];
+      s_first[tid] = base + inc - kept;
+      a.offsets[tid] = base + inc - kept;
+      if (tid == E - 1) a.offsets[E] = base + inc;
+    }
+    if (tid == 0) {
+      float t = 0.f;
+      for (int w = 0; w < (E + 31) / 32; ++w) t += s_aux[w];
+      *a.aux = float(double(t) * (double(E) / (double(a.Sg) * k * double(a.Sg))));
+      *a.z = sz / float(a.S);
+    }
+    __syncthreads();
+    for (int x = tid; x < nt * k; x += kTokThreads) {
+      const int i = x / k, j = x - i * k;
+      const int e = int(s_id[i * kMaxK + j]);
+      const int slot = s_cnt[(j * kWarps + (i >> 5)) * E + e] + int(s_rk[i * kMaxK + j]);
+      const bool in = a.C < 0 || slot < a.C;
+      const int row = in ? s_first[e] + slot : -1;
+      const float w = a.gate[x];
+      a.pos[x] = in ? slot : -1;
+      a.row[x] = row;
+      a.drop[x] = in ? MOE_KEPT : MOE_DROP_CAPACITY;
+      if (in) {
+        a.token_of[row] = i;
+        a.w_perm[row] = w;
+      } else {
+        a.gate[x] = 0.f;
+      }
+    }
   }
 }
 
@@ -438,11 +727,20 @@ ScoreArgs score_args(const moe_score_t& sc, const float* bias) {
 int launch_route_scored(const moe_config_t& c, const moe_score_t& sc, int C, const float* logits,
                         const float* select_bias, const moe_route_out_t& out, char* ws,
                         const WsLayout& L, cudaStream_t st, const DispatchFuse* d) {
-  const RouteArgs a = route_args(c, C, logits, nullptr, out, ws, L);
+  RouteArgs a = route_args(c, C, logits, nullptr, out, ws, L);
+  a.gm24 = a.ng > 1 ? ((1u << 24) + unsigned(a.gsz) - 1u) / unsigned(a.gsz) : 0u;
   const size_t dyn = std::max(size_t(kTokWarps) * c.E * sizeof(double), size_t(c.k) * kWarps * c.E * 4);
-  const int rc = launch_kernel(route_scored_kernel, dim3(unsigned(L.n_chunks)), dim3(kTokThreads), dyn,
-                               st, a, score_args(sc, select_bias));
-  if (rc != MOE_OK) return rc;
+  const bool one = L.n_chunks == 1 && !d;
+  auto go = [&](auto kern) {
+    return launch_kernel(kern, dim3(unsigned(L.n_chunks)), dim3(kTokThreads), dyn, st, a,
+                         score_args(sc, select_bias));
+  };
+  int rc;
+  if (c.E <= 32) rc = one ? go(route_scored_kernel<1, true>) : go(route_scored_kernel<1, false>);
+  else if (c.E <= 64) rc = one ? go(route_scored_kernel<2, true>) : go(route_scored_kernel<2, false>);
+  else if (c.E <= 128) rc = one ? go(route_scored_kernel<4, true>) : go(route_scored_kernel<4, false>);
+  else rc = one ? go(route_scored_kernel<8, true>) : go(route_scored_kernel<8, false>);
+  if (rc != MOE_OK || one) return rc;
   return launch_scan_finalize(c, a, d, st);
 }
 

@@ -127,7 +127,15 @@ class RouteOutputs:
                    z_loss=z((1,), torch.float32))
 
     def struct(self) -> N.MoeRouteOut:
-        return N.MoeRouteOut(**{f: getattr(self, f).data_ptr() for f in N.ROUTE_FIELDS})
+        s = self.__dict__.get("_struct")
+        if s is None:
+            s = N.MoeRouteOut(**{f: getattr(self, f).data_ptr() for f in N.ROUTE_FIELDS})
+            self.__dict__["_struct"] = s
+        return s
+
+    def __setattr__(self, name, value):  # another tensor in a field: the pointers are taken anew
+        self.__dict__[name] = value
+        self.__dict__.pop("_struct", None)
 
 
 # ------------------------------------------------------------------ weight packing
