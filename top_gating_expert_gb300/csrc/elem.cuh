@@ -15,6 +15,34 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// VEC elements as one access: 16 bytes, or a single element.
+template <typename T, int VEC>
+struct Vec {
+  T v[VEC];
+};
+template <typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> load_vec(const T* p) {
+  Vec<T, VEC> r;
+  if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<uint4*>(r.v) = *reinterpret_cast<const uint4*>(p);
+  else r.v[0] = *p;
+  return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T* p, const Vec<T, VEC>& r) {
+  if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(r.v);
+  else *p = r.v[0];
+}
+// VEC floats from a 16-byte aligned address (VEC 4 or 8), or one
+template <int VEC>
+__device__ __forceinline__ void load_floats(const float* p, float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    f[0] = __ldg(p);
+  } else {
+#pragma unroll
+    for (int q = 0; q < VEC / 4; ++q) reinterpret_cast<float4*>(f)[q] = __ldg(reinterpret_cast<const float4*>(p) + q);
+  }
+}
+
 // Sum over the block of NW warps of one float per thread, valid in every thread; the order
 // is a fixed tree. s_red: NW floats that no thread uses until the next barrier.
 template <int NW>

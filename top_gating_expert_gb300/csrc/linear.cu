@@ -11,23 +11,6 @@ namespace {
 
 constexpr int kColThreads = 32, kRowLanes = 8;
 
-template <typename T, int VEC>
-struct Vec {
-  T v[VEC];
-};
-template <typename T, int VEC>
-__device__ __forceinline__ Vec<T, VEC> load_vec(const T* p) {
-  Vec<T, VEC> r;
-  if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<uint4*>(r.v) = *reinterpret_cast<const uint4*>(p);
-  else r.v[0] = *p;
-  return r;
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const Vec<T, VEC>& r) {
-  if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(r.v);
-  else *p = r.v[0];
-}
-
 // d = dy act'(pre) (written to d when it is given) and the partial column sums of the
 // unrounded d over a slice of rows: part[slice][N]. CTA: 32 threads of VEC columns by 8 row
 // lanes; the lanes' sums are added in order.

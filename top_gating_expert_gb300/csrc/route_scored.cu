@@ -20,14 +20,17 @@
 // take (route.cu). A batch of one chunk (a serving step) is finished by the same CTA: one
 // launch instead of three. Every sum has a fixed order.
 #include <algorithm>
+#include <type_traits>
 
 #include "route_kernels.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTokWarps = 16;
-constexpr int kTokThreads = 32 * kTokWarps;
+// The chunk kernel: 16 warps; two CTAs an SM with at most 2 experts a lane (64 registers a
+// thread), so that one's last steps run beside the other's tokens. 32 warps with 8 experts a lane
+// (64 registers, spills) took the same time.
+constexpr int kTokWarps = 16, kTokThreads = 32 * kTokWarps;
 constexpr unsigned kFull = 0xffffffffu;
 
 struct ScoreArgs {
@@ -55,95 +58,96 @@ __device__ __forceinline__ float sigmoid_shifted(float l, float m) {
   return l > -INFINITY ? expf(fminf(l, 0.f) - m) / (1.f + expf(-fabsf(l))) : 0.f;
 }
 
+// Order-preserving map of a double to unsigned (integer comparisons; fp64 ones run on the slow
+// pipe): larger value, larger key; -inf is not 0. Back: order_double.
+__device__ __forceinline__ unsigned long long order_key(double v) {
+  const long long b = __double_as_longlong(v + 0.0);  // -0 and 0 are equal
+  return static_cast<unsigned long long>(b) ^ (static_cast<unsigned long long>(b >> 63) | (1ull << 63));
+}
+__device__ __forceinline__ double order_double(unsigned long long k) {
+  return __longlong_as_double(static_cast<long long>(k ^ ((k >> 63) ? (1ull << 63) : ~0ull)));
+}
+
+// The token's fp64 sum of exp(l - m) over all experts, m its largest logit (softmax scores).
+template <int Q>
+__device__ __forceinline__ double softmax_sum(const float (&l)[Q], double m) {
+  double s = 0.0;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) s += l[q] > -1e30f ? exp(double(l[q]) - m) : 0.0;
+  return warp_sum(s);
+}
+
 // A token's choices by the fp64 scores: lane j < k gets the j-th one's index. l: the lane's
-// logits (-inf where the expert is out), own: its experts that exist, row: E doubles of this
-// warp in shared memory.
+// logits (-inf where the expert is out), row: E doubles of this warp in shared memory.
 template <int Q>
 __device__ __noinline__ int choose_fp64(const float (&l)[Q], const RouteArgs& a, const ScoreArgs& sc,
                                         double* row) {
   const int lane = threadIdx.x & 31, E = a.E;
-  double c[Q];
-  if (sc.sigmoid) {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) c[q] = 1.0 / (1.0 + exp(-double(l[q])));
-  } else {
+  double m = 0.0, z = 1.0;
+  if (!sc.sigmoid) {
     float mf = -INFINITY;
 #pragma unroll
     for (int q = 0; q < Q; ++q) mf = fmaxf(mf, l[q]);
-    const double m = double(warp_max(mf));
-    double s = 0.0;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      c[q] = l[q] > -INFINITY ? exp(double(l[q]) - m) : 0.0;
-      s += c[q];
-    }
-    s = warp_sum(s);
-#pragma unroll
-    for (int q = 0; q < Q; ++q) c[q] = c[q] / s;
+    m = double(warp_max(mf));
+    z = softmax_sum<Q>(l, m);
   }
+  unsigned long long key[Q];
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     const int e = lane + 32 * q;
+    double c = sc.sigmoid ? 1.0 / (1.0 + exp(-double(l[q]))) : exp(double(l[q]) - m) / z;
     const float b = sc.bias && e < E ? __ldg(sc.bias + e) : 0.f;
-    c[q] = l[q] > -INFINITY && isfinite(b) ? c[q] + double(b) : -INFINITY;
+    c = l[q] > -INFINITY && isfinite(b) ? c + double(b) : -INFINITY;
+    key[q] = order_key(c);
   }
   unsigned groups = kFull;
   if (a.ng > 1) {
+    unsigned long long* keys = reinterpret_cast<unsigned long long*>(row);
 #pragma unroll
     for (int q = 0; q < Q; ++q)
-      if (lane + 32 * q < E) row[lane + 32 * q] = c[q];
+      if (lane + 32 * q < E) keys[lane + 32 * q] = key[q];
     __syncwarp();
-    double gs = -INFINITY;
+    unsigned long long gs = 0;
     if (lane < a.ng) {
-      double b1 = -INFINITY, b2 = -INFINITY;
+      unsigned long long b1 = 0, b2 = 0;
       for (int i = 0; i < a.gsz; ++i) {
-        const double v = row[lane * a.gsz + i];
-        if (v > b1) {
-          b2 = b1;
-          b1 = v;
-        } else if (v > b2) {
-          b2 = v;
-        }
+        const unsigned long long v = keys[lane * a.gsz + i];
+        b2 = max(b2, min(b1, v));
+        b1 = max(b1, v);
       }
-      gs = (sc.gtop == 2 && a.gsz > 1) ? b1 + b2 : b1;
+      gs = (sc.gtop == 2 && a.gsz > 1) ? order_key(order_double(b1) + order_double(b2)) : b1;
     }
     int before = 0;
     for (int h = 0; h < a.ng; ++h) {
-      const double vh = __shfl_sync(kFull, gs, h);
+      const unsigned long long vh = __shfl_sync(kFull, gs, h);
       if (vh > gs || (vh == gs && h < lane)) ++before;
     }
     groups = __ballot_sync(kFull, lane < a.ng && before < a.tg);
     __syncwarp();
   }
-  unsigned open = 0u;  // bit q: expert lane + 32 q may still be chosen
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
+  for (int q = 0; q < Q; ++q) {  // 0: not to be chosen
     const int e = lane + 32 * q;
-    if (e < E && (a.ng <= 1 || ((groups >> (e / a.gsz)) & 1u))) open |= 1u << q;
+    if (e >= E || (a.ng > 1 && !((groups >> (e / a.gsz)) & 1u))) key[q] = 0;
   }
   int mine = 0;
   for (int j = 0; j < a.k; ++j) {
-    double bv = -INFINITY;
-    int bi = 0x7fffffff;
+    unsigned long long best = 0;
+    int e = 0x7fffffff;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int e = lane + 32 * q;
-      if (((open >> q) & 1u) && (c[q] > bv || (c[q] == bv && e < bi))) {
-        bv = c[q];
-        bi = e;
+    for (int q = 0; q < Q; ++q)
+      if (key[q] > best) {  // equal keys: the lower q first
+        best = key[q];
+        e = lane + 32 * q;
       }
-    }
+    const unsigned hi = __reduce_max_sync(kFull, unsigned(best >> 32));
+    const bool top = unsigned(best >> 32) == hi;
+    const unsigned lo = __reduce_max_sync(kFull, top ? unsigned(best) : 0u);
+    const int id = __reduce_min_sync(kFull, top && unsigned(best) == lo ? e : 0x7fffffff);
+    if (lane == j) mine = id;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const double ov = __shfl_xor_sync(kFull, bv, off);
-      const int oi = __shfl_xor_sync(kFull, bi, off);
-      if (ov > bv || (ov == bv && oi < bi)) {
-        bv = ov;
-        bi = oi;
-      }
-    }
-    if ((bi & 31) == lane) open &= ~(1u << (bi >> 5));
-    if (lane == j) mine = bi;
+    for (int q = 0; q < Q; ++q)
+      if (lane + 32 * q == id) key[q] = 0;
   }
   return mine;
 }
@@ -167,22 +171,11 @@ __device__ __forceinline__ float choice_weight(float lsel, bool on, const ScoreA
   return w * sc.scale;
 }
 
-// Order-preserving map of a float to unsigned and back (finite values).
-__device__ __forceinline__ unsigned order_key(float v) {
-  const unsigned b = __float_as_uint(v);
-  return b ^ (unsigned(int(b) >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float order_value(unsigned k) {
-  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
-}
-
 // The loss terms and choice of one token in the general form: any finite logits, -inf where an
-// expert is out. q: the normalised scores.
+// expert is out. q: the normalised scores. Lane j < k returns choice j.
 template <int Q>
-__device__ __noinline__ int token_general(const float (&l)[Q], const float* lr, const RouteArgs& a,
-                                          const ScoreArgs& sc, double* row, float (&q)[Q], float& lse,
-                                          float& w) {
-  const int lane = threadIdx.x & 31;
+__device__ __noinline__ int token_general(const float (&l)[Q], const RouteArgs& a, const ScoreArgs& sc,
+                                          double* row, float (&q)[Q], float& lse) {
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < Q; ++i) m = fmaxf(m, l[i]);
@@ -197,8 +190,7 @@ __device__ __noinline__ int token_general(const float (&l)[Q], const float* lr, 
   }
   s = warp_sum(s);
   lse = any ? m + logf(s) : 0.f;
-  const float inv = s > 0.f ? 1.f / s : 0.f;
-  float ti = inv;
+  float ti = s > 0.f ? 1.f / s : 0.f;
   if (sc.sigmoid) {
     const float top = fminf(m, 0.f);
     float tot = 0.f;
@@ -212,43 +204,51 @@ __device__ __noinline__ int token_general(const float (&l)[Q], const float* lr, 
   }
 #pragma unroll
   for (int i = 0; i < Q; ++i) q[i] *= ti;
-  const int id = choose_fp64<Q>(l, a, sc, row);
-  float lsel = -INFINITY;
-  if (lane < a.k) {
-    lsel = __ldg(lr + id);
-    if (!isfinite(lsel) || (sc.bias && !isfinite(__ldg(sc.bias + id)))) lsel = -INFINITY;
-  }
-  w = choice_weight(lsel, lane < a.k, sc, m, inv);
-  return id;
+  return choose_fp64<Q>(l, a, sc, row);
 }
 
-// The two best keys of every group of 32 m experts (lane-strided experts: slots m g .. of all
-// lanes), summed (or the best alone), left in lane g. Equal best keys count twice, as they
-// should.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Group scores from keys (bits of non-negative floats, low 3 bits the slot number), lane g
+// getting group g's; groups of 32 m experts, i.e. slots m g .. m g + m - 1 of every lane. Equal
+// best keys count twice, as they should.
 template <int Q>
 __device__ __forceinline__ float group_scores_wide(const unsigned (&key)[Q], const RouteArgs& a,
                                                    const ScoreArgs& sc) {
   const int lane = threadIdx.x & 31, per = a.gsz >> 5;
-  float gs = -INFINITY;
-  for (int g = 0; g < a.ng; ++g) {
-    unsigned b1 = 0u, b2 = 0u;
+  unsigned b1 = 0u, b2 = 0u, g1 = 0u, g2 = 0u;
+  int g = 0, have = 0;
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
-      if (i / per != g) continue;
-      const unsigned v = key[i];
-      b2 = max(b2, min(b1, v));
-      b1 = max(b1, v);
+  for (int i = 0; i < Q; ++i) {
+    const unsigned v = key[i];
+    b2 = max(b2, min(b1, v));
+    b1 = max(b1, v);
+    if (++have == per) {  // slots g per .. g per + per - 1 are in
+      const unsigned m1 = __reduce_max_sync(kFull, b1);
+      unsigned m2 = 0u;
+      if (sc.gtop == 2) {
+        const int owner = __ffs(__ballot_sync(kFull, b1 == m1)) - 1;
+        m2 = __reduce_max_sync(kFull, lane == owner ? b2 : b1);
+      }
+      if (lane == g) {
+        g1 = m1;
+        g2 = m2;
+      }
+      ++g;
+      have = 0;
+      b1 = b2 = 0u;
     }
-    const unsigned m1 = __reduce_max_sync(kFull, b1);
-    float v = order_value(m1 & ~7u);
-    if (sc.gtop == 2) {
-      const unsigned own = __ballot_sync(kFull, b1 == m1);
-      const unsigned second = lane == __ffs(own) - 1 ? b2 : b1;
-      v += order_value(__reduce_max_sync(kFull, second) & ~7u);
-    }
-    if (lane == g) gs = v;
   }
-  return gs;
+  return __uint_as_float(g1 & ~7u) + __uint_as_float(g2 & ~7u);
 }
 
 // The same for any group size, through this warp's row of shared memory: lane g walks its group
@@ -261,7 +261,7 @@ __device__ __forceinline__ float group_scores_any(const float (&c)[Q], const Rou
   for (int i = 0; i < Q; ++i)
     if (lane + 32 * i < a.E) row[lane + 32 * i] = c[i];
   __syncwarp();
-  float b1 = -INFINITY, b2 = -INFINITY;
+  float b1 = 0.f, b2 = 0.f;
   if (lane < a.ng) {
     int r = lane % a.gsz;
     for (int i = 0; i < a.gsz; ++i) {
@@ -275,111 +275,256 @@ __device__ __forceinline__ float group_scores_any(const float (&c)[Q], const Rou
   return sc.gtop == 2 && a.gsz > 1 ? b1 + b2 : b1;
 }
 
-// A token in fp32: false when a decision lies within the error bound (or the values leave the
-// range the bound holds for), and the caller takes token_general. With x = __expf(l) (relative
-// error (2 + 1.2 |l|) 2^-23), s = sum x in (e^-20, e^20):
-//   sigmoid x / (1 + x): |l| sigma (1 - sigma) <= 0.224 and 2 ulp of the division bound the
-//     error by 2.5 * 2^-23, and by 27 * 2^-23 of the score where all are small (|l| < 20);
-//   softmax x / s: by (13 + 3 * 20) * 2^-23 of the score.
-// The bias adds half an ulp, and the keys drop 3 bits for the slot number: at most 2^-20 of the
-// largest selection value in all.
+// Groups of 32, the lanes' slot g being group g.
 template <int Q>
-__device__ __forceinline__ bool token_fast(const float (&l)[Q], const float (&b)[Q], float bmax,
-                                           const RouteArgs& a, const ScoreArgs& sc, float* row,
-                                           float (&q)[Q], float& lse, int& id) {
+__device__ __forceinline__ float group_scores_32(const unsigned (&key)[Q], const ScoreArgs& sc) {
   const int lane = threadIdx.x & 31;
-  constexpr float kU = 1.1920929e-7f;  // 2^-23
-  float s = 0.f, tot = 0.f, qm = 0.f;
+  unsigned g1 = 0u, g2 = 0u;
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
-    const float x = __expf(l[i]);  // -inf (no expert): 0
+    const unsigned m1 = __reduce_max_sync(kFull, key[i]);
+    unsigned m2 = 0u;
+    if (sc.gtop == 2) {
+      const bool at = key[i] == m1;
+      const unsigned own = __ballot_sync(kFull, at);
+      m2 = __reduce_max_sync(kFull, at ? 0u : key[i]);
+      if (own & (own - 1u)) m2 = m1;  // two experts share the best key
+    }
+    if (lane == i) {
+      g1 = m1;
+      g2 = m2;
+    }
+  }
+  return __uint_as_float(g1 & ~7u) + __uint_as_float(g2 & ~7u);
+}
+
+// Group g's score by the fp64 sigmoids, as an ordered key; the group's experts a lane each (or
+// every 32nd), their logits read again.
+__device__ __noinline__ unsigned long long group_score_fp64(const float* lr, const float* bias, int g,
+                                                            int gsz, int gtop) {
+  const int lane = threadIdx.x & 31;
+  unsigned long long b1 = 0, b2 = 0;
+  for (int i = lane; i < gsz; i += 32) {
+    const int e = g * gsz + i;
+    const unsigned long long v =
+        order_key(1.0 / (1.0 + exp(-double(__ldg(lr + e)))) + (bias ? double(__ldg(bias + e)) : 0.0));
+    b2 = max(b2, min(b1, v));
+    b1 = max(b1, v);
+  }
+  auto top = [&](unsigned long long v) {
+    const unsigned hi = __reduce_max_sync(kFull, unsigned(v >> 32));
+    const unsigned lo = __reduce_max_sync(kFull, unsigned(v >> 32) == hi ? unsigned(v) : 0u);
+    return (static_cast<unsigned long long>(hi) << 32) | lo;
+  };
+  const unsigned long long m1 = top(b1);
+  if (gtop != 2 || gsz == 1) return m1;
+  const int owner = __ffs(__ballot_sync(kFull, b1 == m1)) - 1;
+  return order_key(order_double(m1) + order_double(top(lane == owner ? b2 : b1)));
+}
+
+// How many groups rank before this lane's (lane g < ng holds group g's score).
+__device__ __forceinline__ int groups_before(float gs, int ng) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  if (ng <= 8) {  // lane (g, h): group g = lane & 7 against h = lane / 8 and h + 4
+    const int g = lane & 7, h = lane >> 3;
+    const float vg = __shfl_sync(kFull, gs, g);
+    const float v0 = __shfl_sync(kFull, gs, h), v1 = __shfl_sync(kFull, gs, h + 4);
+    if (h < ng && (v0 > vg || (v0 == vg && h < g))) ++before;
+    if (h + 4 < ng && (v1 > vg || (v1 == vg && h + 4 < g))) ++before;
+    before += __shfl_xor_sync(kFull, before, 8);
+    before += __shfl_xor_sync(kFull, before, 16);
+    return before;
+  }
+  for (int h = 0; h < ng; ++h) {
+    const float vh = __shfl_sync(kFull, gs, h);
+    if (vh > gs || (vh == gs && h < lane)) ++before;
+  }
+  return before;
+}
+
+// Of n candidates, a lane each (l its logit, b its bias, id its index): how many rank before this
+// lane's by sigmoid(l) + b in fp64, equal ones by index.
+__device__ __noinline__ int rank_fp64(float l, float b, int id, int n) {
+  const unsigned long long key = order_key(1.0 / (1.0 + exp(-double(l))) + double(b));
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const unsigned long long o = __shfl_sync(kFull, key, i);
+    const int oid = __shfl_sync(kFull, id, i);
+    if (o > key || (o == key && oid < id)) ++rank;
+  }
+  return rank;
+}
+
+// A token in fp32. Sigmoid scores that decide and lie within the error bound of each other (the
+// groups at the border of the kept ones, neighbours among the choices) are evaluated in fp64, a
+// lane each. False where softmax scores, whose sum all experts enter, lie that close, or the
+// values leave the range the bound holds for: the caller then takes token_general.
+// l: the lane's finite logits (-1e30 where there is no expert), b: the biases less the smallest
+// one, so that every selection value c = s + b is >= 0 and its bits order as an integer. The low
+// 3 bits of a key give way to the lane's slot number, so one warp maximum finds the value and
+// its expert; a key below 8 is no expert.
+// With x = exp2(l log2 e) (relative error (2 + 1.2 |l|) 2^-23), s = sum x in (e^-20, e^20):
+//   sigmoid x / (1 + x): |l| sigma (1 - sigma) <= 0.224 and 2 ulp of the reciprocal bound the
+//     error by 2.5 * 2^-23, and by 27 * 2^-23 of the score where all are small (|l| < 20);
+//   softmax x / s: by (13 + 3 * 20) * 2^-23 of the score.
+// The shifted bias and the sum c add an ulp (2^-23 of the largest value), the dropped bits 7.
+// Writes the choices to ids, and s.
+template <int Q, bool SIG>
+__device__ __forceinline__ bool token_fast(const float (&l)[Q], const float (&b)[Q], float brange,
+                                           const float* lr, const RouteArgs& a, const ScoreArgs& sc,
+                                           float* row, float (&pp)[Q], uint8_t* ids, float& s_out) {
+  const int lane = threadIdx.x & 31;
+  constexpr float kU = 1.1920929e-7f;  // 2^-23
+  float q[Q];
+  float s = 0.f, tot = 0.f, wild = 0.f;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const float x = exp2_approx(l[i] * 1.44269504088896341f);
+    wild = fmaf(l[i], 0.f, wild);  // NaN when a logit is not finite
     s += x;
-    q[i] = sc.sigmoid ? __fdividef(x, 1.f + x) : x;
-    tot += q[i];
-    qm = fmaxf(qm, q[i]);
+    if constexpr (SIG) {
+      q[i] = x * rcp_approx(1.f + x);
+      tot += q[i];
+    } else {
+      q[i] = x;
+    }
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     s += __shfl_xor_sync(kFull, s, off);
-    tot += __shfl_xor_sync(kFull, tot, off);
+    if constexpr (SIG) tot += __shfl_xor_sync(kFull, tot, off);
   }
-  if (!(s > 2.1e-9f && s < 4.8e8f)) return false;
-  lse = logf(s);
-  const float ti = __fdividef(1.f, tot);
-  qm = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(qm)));  // >= 0
-  float err;
-  if (sc.sigmoid) {
+  if (__any_sync(kFull, !(wild == 0.f)) || !(s > 2.1e-9f && s < 4.8e8f)) return false;
+  s_out = s;
+  const float ti = rcp_approx(SIG ? tot : s);
+  float err, qm;  // qm: at least the largest score
+  if constexpr (SIG) {
+    qm = fminf(tot, 1.f);
     err = fminf(2.5f, 27.f * qm) * kU;
   } else {
-    qm *= ti;
+    qm = q[0];
+#pragma unroll
+    for (int i = 1; i < Q; ++i) qm = fmaxf(qm, q[i]);
+    qm = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(qm))) * ti;
     err = 73.f * qm * kU;
   }
-  const float cmax = qm + bmax;
-  const float gap = 2.f * err + 1.1f * 8.f * kU * cmax;  // 2^-20 and the rounding of c
+  const float cmax = qm + brange;
+  const float gap = 2.f * err + 10.f * kU * cmax;
 
   float c[Q];
   unsigned key[Q];
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
-    const float sv = sc.sigmoid ? q[i] : q[i] * ti;
-    q[i] *= ti;
-    c[i] = sv + b[i];
-    key[i] = lane + 32 * i < a.E ? ((order_key(c[i]) & ~7u) | unsigned(i)) : 0u;
+    c[i] = SIG ? q[i] + b[i] : fmaf(q[i], ti, b[i]);
+    key[i] = (__float_as_uint(c[i]) & ~7u) | unsigned(i);
   }
   if (a.ng > 1) {
-    const float gs = (a.gsz & 31) == 0 ? group_scores_wide<Q>(key, a, sc) : group_scores_any<Q>(c, a, sc, row);
-    int before = 0;
-    for (int h = 0; h < a.ng; ++h) {
-      const float vh = __shfl_sync(kFull, gs, h);
-      if (vh > gs || (vh == gs && h < lane)) ++before;
-    }
-    const bool mine = lane < a.ng, kept = mine && before < a.tg;
-    if (a.tg < a.ng) {  // the last group kept and the first one not, 2 err each way apart
-      const unsigned lo = __reduce_min_sync(kFull, kept ? order_key(gs) : 0xffffffffu);
-      const unsigned hi = __reduce_max_sync(kFull, mine && !kept ? order_key(gs) : 0u);
-      if (!(order_value(lo) - order_value(hi) > 2.f * gap + 4.f * kU * cmax)) return false;
+    const float gs = a.gsz == 32          ? group_scores_32<Q>(key, sc)
+                     : (a.gsz & 31) == 0 ? group_scores_wide<Q>(key, a, sc)
+                                         : group_scores_any<Q>(c, a, sc, row);
+    const int before = groups_before(gs, a.ng);  // every lane: it shuffles
+    const bool mine = lane < a.ng;
+    bool kept = mine && before < a.tg;
+    if (a.tg < a.ng) {  // the last group kept and the first one not
+      const float lo = __uint_as_float(__reduce_min_sync(kFull, kept ? __float_as_uint(gs) : 0x7f800000u));
+      const float hi = __uint_as_float(__reduce_max_sync(kFull, mine && !kept ? __float_as_uint(gs) : 0u));
+      const float margin = 2.f * gap + 4.f * kU * cmax;
+      if (!(lo - hi > margin)) {
+        if constexpr (!SIG) return false;
+        // the groups within the bound of the border: the best of them by their fp64 scores
+        const bool near = mine && (kept ? !(gs - hi > margin) : !(lo - gs > margin));
+        const unsigned close = __ballot_sync(kFull, near);
+        const int seats = a.tg - __popc(__ballot_sync(kFull, kept && !near));
+        unsigned long long score = 0;
+        for (unsigned todo = close; todo; todo &= todo - 1u) {
+          const int g = __ffs(todo) - 1;
+          const unsigned long long v = group_score_fp64(lr, sc.bias, g, a.gsz, sc.gtop);
+          if (lane == g) score = v;
+        }
+        int rank = 0;
+        for (unsigned todo = close; todo; todo &= todo - 1u) {
+          const int g = __ffs(todo) - 1;
+          const unsigned long long o = __shfl_sync(kFull, score, g);
+          if (o > score || (o == score && g < lane)) ++rank;
+        }
+        if (near) kept = rank < seats;
+      }
     }
     const unsigned groups = __ballot_sync(kFull, kept);
+    if (a.gsz == 32) {
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
-      const int e = lane + 32 * i;
-      const int g = int((unsigned(e) * a.gm24) >> 24);
-      if (!((groups >> g) & 1u)) key[i] = 0u;
+      for (int i = 0; i < Q; ++i) key[i] = (groups >> i) & 1u ? key[i] : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        const int g = int((unsigned(lane + 32 * i) * a.gm24) >> 24);
+        if (!((groups >> g) & 1u)) key[i] = 0u;
+      }
     }
   }
-  unsigned lk = 0u;
+  // each lane's keys in falling order (odd-even transposition), so that taking one shifts them
 #pragma unroll
-  for (int i = 0; i < Q; ++i) lk = max(lk, key[i]);
-  float prev = INFINITY;
-  id = 0;
-  for (int j = 0; j <= a.k; ++j) {
-    const unsigned top = __reduce_max_sync(kFull, lk);
-    if (top == 0u) break;  // j == k: no expert is left
-    const unsigned own = __ballot_sync(kFull, lk == top);
-    const float v = order_value(top & ~7u);
-    if (!(prev - v > gap) || (own & (own - 1u))) return false;
-    prev = v;
-    if (j == a.k) break;
-    const int owner = __ffs(own) - 1;
-    if (lane == j) id = owner + 32 * int(top & 7u);
+  for (int r = 0; r < Q; ++r)
+#pragma unroll
+    for (int i = r & 1; i + 1 < Q; i += 2) {
+      const unsigned hi = max(key[i], key[i + 1]);
+      key[i + 1] = min(key[i], key[i + 1]);
+      key[i] = hi;
+    }
+  unsigned mine = 0u;  // lane j: the j-th largest key, and its lane
+  int from = 0;
+  auto take = [&](int j, unsigned top) {
+    const int owner = __ffs(__ballot_sync(kFull, key[0] == top)) - 1;
+    if (lane == j) {
+      mine = top;
+      from = owner;
+    }
     const bool pop = lane == owner;
-    lk = 0u;
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
-      if (pop && key[i] == top) key[i] = 0u;
-      lk = max(lk, key[i]);
-    }
+    for (int i = 0; i < Q; ++i) key[i] = pop ? (i + 1 < Q ? key[i + 1 < Q ? i + 1 : 0] : 0u) : key[i];
+  };
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    if (j == a.k) break;
+    take(j, __reduce_max_sync(kFull, key[0]));
   }
+  unsigned last = __reduce_max_sync(kFull, key[0]);  // the best one not chosen
+  const float v = __uint_as_float((lane == a.k ? last : mine) & ~7u);
+  const float above = __shfl_up_sync(kFull, v, 1);
+  const bool close = lane > 0 && (lane < a.k || (lane == a.k && last >= 8u)) && !(above - v > gap);
+  int id = from + 32 * int(mine & 7u);
+  if (__any_sync(kFull, close)) {
+    if constexpr (!SIG) return false;
+    // contested: the k best and all within the bound of the k-th (at most 32) in fp64, a lane each
+    const float floor_v = __shfl_sync(kFull, v, a.k - 1) - gap;
+    int n = a.k;
+    while (last >= 8u && __uint_as_float(last & ~7u) >= floor_v) {
+      if (n == 32) return false;
+      take(n++, last);
+      last = __reduce_max_sync(kFull, key[0]);
+    }
+    id = from + 32 * int(mine & 7u);
+    const int rank = rank_fp64(lane < n ? __ldg(lr + id) : 0.f, sc.bias && lane < n ? __ldg(sc.bias + id) : 0.f,
+                               id, n);
+    if (lane < n && rank < a.k) ids[rank] = uint8_t(id);
+  } else if (lane < a.k) {
+    ids[lane] = uint8_t(id);
+  }
+#pragma unroll
+  for (int i = 0; i < Q; ++i) pp[i] = fmaf(q[i], ti, pp[i]);
   return true;
 }
 
-template <int Q, bool ONE>
-__global__ void __launch_bounds__(kTokThreads, 1) route_scored_kernel(RouteArgs a, ScoreArgs sc) {
+template <int Q, bool SIG, bool ONE>
+__global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kernel(RouteArgs a, ScoreArgs sc) {
   // [warps][E] doubles of group scratch, then [warps][E] probability sums, then the counts
   // [k][4][E]
   extern __shared__ double s_dyn[];
-  __shared__ float s_z[kTokWarps];
-  __shared__ uint8_t s_id[kThreads * kMaxK];
+  __shared__ float s_z[kWarps];
+  __shared__ float s_lse[kThreads];   // sum of exponentials, or (general tokens) its logarithm
+  __shared__ uint8_t s_gen[kThreads];
+  __shared__ __align__(8) uint8_t s_id[kThreads * kMaxK];
   __shared__ uint8_t s_rk[kThreads * kMaxK];
   const int c = blockIdx.x;
   const int g = c / a.n_cpg, cc = c % a.n_cpg;
@@ -392,85 +537,110 @@ __global__ void __launch_bounds__(kTokThreads, 1) route_scored_kernel(RouteArgs 
   if (c == 0 && tid == 0) *a.done = 0u;  // ticket counter of route_scan_kernel
 
   float b[Q];
-  float bmax = 0.f;
+  float bmin = INFINITY, bmax = -INFINITY;
   bool bias_bad = false;
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
     const int e = lane + 32 * i;
-    b[i] = sc.bias && e < E ? __ldg(sc.bias + e) : 0.f;
-    if (!isfinite(b[i])) bias_bad = true;
-    bmax = fmaxf(bmax, fabsf(b[i]));
+    b[i] = 0.f;
+    if (e < E) {
+      if (sc.bias) b[i] = __ldg(sc.bias + e);
+      if (!isfinite(b[i])) bias_bad = true;
+      bmin = fminf(bmin, b[i]);
+      bmax = fmaxf(bmax, b[i]);
+    }
   }
   bias_bad = __any_sync(kFull, bias_bad);
+  bmin = -warp_max(-bmin);
   bmax = warp_max(bmax);
-  if (bias_bad && tid == 0) atomicOr(a.status, kStatusNonfinite);
+#pragma unroll
+  for (int i = 0; i < Q; ++i)  // an expert's key is never below 8, no expert's is its slot
+    b[i] = lane + 32 * i < E ? (b[i] - bmin) + 1e-30f : 0.f;
+  const float brange = bmax - bmin;
+  if (!(brange < 1e30f)) bias_bad = true;  // the shifted biases could overflow
+  if (bias_bad && tid == 0 && !(isfinite(bmin) && isfinite(bmax))) atomicOr(a.status, kStatusNonfinite);
   double* scratch = s_dyn + size_t(warp) * E;
   float pp[Q];
 #pragma unroll
   for (int i = 0; i < Q; ++i) pp[i] = 0.f;
-  float zacc = 0.f;
-  float next[Q];
-  auto fetch = [&](int i) {
-#pragma unroll
-    for (int x = 0; x < Q; ++x) {
-      const int e = lane + 32 * x;
-      next[x] = (i < nt && e < E) ? __ldg(a.logits + int64_t(t0 + i) * E + e) : -INFINITY;
-    }
-  };
-  fetch(warp);
   for (int i = warp; i < nt; i += kTokWarps) {
-    const int64_t t = t0 + i;
-    float l[Q], q[Q];
-    bool bad = false;
+    const float* lr = a.logits + int64_t(t0 + i) * E;
+    float l[Q];
 #pragma unroll
-    for (int x = 0; x < Q; ++x) {
-      l[x] = next[x];
-      if (lane + 32 * x < E && !isfinite(l[x])) {
-        bad = true;
-        l[x] = -INFINITY;
+    for (int x = 0; x < Q; ++x) l[x] = lane + 32 * x < E ? __ldg(lr + lane + 32 * x) : -1e30f;
+    float s;
+    if (!bias_bad && token_fast<Q, SIG>(l, b, brange, lr, a, sc, reinterpret_cast<float*>(scratch), pp,
+                                        s_id + i * kMaxK, s)) {
+      if (lane == 0) {
+        s_lse[i] = s;
+        s_gen[i] = 0;
+      }
+    } else {
+      float q[Q];
+      bool bad = false;
+#pragma unroll
+      for (int x = 0; x < Q; ++x) {
+        const bool in = lane + 32 * x < E;
+        if (in && !isfinite(l[x])) bad = true;
+        if (!in || !isfinite(l[x])) l[x] = -INFINITY;
+      }
+      if (bad) atomicOr(a.status, kStatusNonfinite);
+      __syncwarp();
+      const int id = token_general<Q>(l, a, sc, scratch, q, s);
+#pragma unroll
+      for (int x = 0; x < Q; ++x) pp[x] += q[x];
+      if (lane < k) s_id[i * kMaxK + lane] = uint8_t(id);
+      if (lane == 0) {
+        s_lse[i] = s;
+        s_gen[i] = 1;
       }
     }
-    fetch(i + kTokWarps);  // the warp's next token, while this one is worked on
-    bad = __any_sync(kFull, bad);
-    float lse, w;
-    int id;
-    const float* lr = a.logits + t * E;
-    bool fast = !bad && !bias_bad &&
-                token_fast<Q>(l, b, bmax, a, sc, reinterpret_cast<float*>(scratch), q, lse, id);
-    if (fast) {  // the weights, from accurate exponentials of the choices' logits (lanes j < k)
-      const float ls = lane < k ? __ldg(lr + id) : 0.f;
-      if (sc.renorm) {
-        w = lane < k ? (sc.sigmoid ? sigmoid_shifted(ls, 0.f) : expf(ls)) : 0.f;
-        float tot = w;
+  }
+  __syncthreads();
+  // the weights: 8 lanes a token, lane j < k its choice j, from accurate exponentials of the
+  // choices' logits shifted by the largest (they cannot all underflow)
+  for (int x = tid; x < kThreads * kMaxK; x += kTokThreads) {
+    const int i = x >> 3, j = x & 7;
+    const bool on = i < nt && j < k;
+    float ls = -INFINITY, lse = 0.f;
+    int id = 0;
+    if (i < nt) lse = s_gen[i] ? s_lse[i] : logf(s_lse[i]);
+    if (on) {
+      id = int(s_id[i * kMaxK + j]);
+      ls = __ldg(a.logits + int64_t(t0 + i) * E + id);
+      if (!isfinite(ls) || (sc.bias && !isfinite(__ldg(sc.bias + id)))) ls = -INFINITY;
+    }
+    float w;
+    if (sc.renorm) {
+      float top = SIG ? fminf(ls, 0.f) : ls;
 #pragma unroll
-        for (int off = 4; off > 0; off >>= 1) tot += __shfl_xor_sync(kFull, tot, off);
-        tot = __shfl_sync(kFull, tot, 0);
-        fast = tot > 1e-30f;  // else chosen by their biases, with scores that underflow
-        w = w / tot;
-      } else {
-        w = sc.sigmoid ? sigmoid_shifted(ls, 0.f) : expf(ls - lse);
-      }
-      w *= sc.scale;
-    }
-    if (!fast) {
-      if (bad && lane == 0) atomicOr(a.status, kStatusNonfinite);
-      id = token_general<Q>(l, lr, a, sc, scratch, q, lse, w);
-    }
+      for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+      if (!(top > -INFINITY)) top = 0.f;
+      w = SIG ? sigmoid_shifted(ls, top) : (ls > -INFINITY ? expf(ls - top) : 0.f);
+      float tot = w;
 #pragma unroll
-    for (int x = 0; x < Q; ++x) pp[x] += q[x];
-    zacc += lse * lse;
-    if (lane < k) {
-      a.expert_id[t * k + lane] = id;
-      a.gate[t * k + lane] = w;
-      s_id[i * kMaxK + lane] = uint8_t(id);
+      for (int off = 4; off > 0; off >>= 1) tot += __shfl_xor_sync(kFull, tot, off);
+      w = tot > 0.f ? w / tot : 0.f;
+    } else {
+      w = SIG ? sigmoid_shifted(ls, 0.f) : (ls > -INFINITY ? expf(ls - lse) : 0.f);
     }
+    if (on) {
+      a.expert_id[int64_t(t0 + i) * k + j] = id;
+      a.gate[int64_t(t0 + i) * k + j] = w * sc.scale;
+    }
+    // the token's logsumexp^2, kept for the sum below
+    __syncwarp();
+    if (i < nt && j == 0) s_lse[i] = lse * lse;
   }
   __syncthreads();  // the group scratch is free
   float* s_pp = reinterpret_cast<float*>(s_dyn);
 #pragma unroll
   for (int i = 0; i < Q; ++i)
     if (lane + 32 * i < E) s_pp[warp * E + lane + 32 * i] = pp[i];
-  if (lane == 0) s_z[warp] = zacc;
+  if (tid < kThreads) {
+    const float z = warp_sum(tid < nt ? s_lse[tid] : 0.f);
+    if (lane == 0) s_z[warp] = z;
+  }
   __syncthreads();
   float psum = 0.f;  // of expert tid
   if (tid < E) {
@@ -480,7 +650,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) route_scored_kernel(RouteArgs 
   }
   float sz = 0.f;
   if (tid == 0) {
-    for (int w = 0; w < kTokWarps; ++w) sz += s_z[w];
+    for (int w = 0; w < kWarps; ++w) sz += s_z[w];
     if (!ONE) a.zpart[c] = sz;
   }
   __syncthreads();
@@ -488,17 +658,18 @@ __global__ void __launch_bounds__(kTokThreads, 1) route_scored_kernel(RouteArgs 
   // rank of each choice among the chunk's earlier ones of the same (j, e): the first
   // kThreads threads hold a token each; counts per (j, warp, e), one scan over the warps
   int* s_cnt = reinterpret_cast<int*>(s_dyn);
-  for (int x = tid; x < k * kWarps * E; x += kTokThreads) s_cnt[x] = 0;
+  const int nw = (nt + 31) >> 5;  // of the kWarps groups of 32 tokens, those that hold any
+  for (int x = tid; x < k * nw * E; x += kTokThreads) s_cnt[x] = 0;
   __syncthreads();
   const unsigned lt_mask = (1u << lane) - 1u;
-  if (tid < kThreads) {
+  if (warp < nw) {
     for (int j = 0; j < k; ++j) {
       const bool on = tid < nt;
       const int e = on ? int(s_id[tid * kMaxK + j]) : -1;
       const unsigned peers = __match_any_sync(kFull, on ? e : 1024 + lane);
       const int rk = __popc(peers & lt_mask);
       s_rk[tid * kMaxK + j] = uint8_t(rk);
-      if (on && rk == 0) s_cnt[(j * kWarps + warp) * E + e] = __popc(peers);
+      if (on && rk == 0) s_cnt[(j * nw + warp) * E + e] = __popc(peers);
     }
   }
   __syncthreads();
@@ -507,9 +678,8 @@ __global__ void __launch_bounds__(kTokThreads, 1) route_scored_kernel(RouteArgs 
       int all = 0;
       for (int j = 0; j < k; ++j) {
         int run = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          int* cw = s_cnt + (j * kWarps + w) * E + x;
+        for (int w = 0; w < nw; ++w) {
+          int* cw = s_cnt + (j * nw + w) * E + x;
           const int v = *cw;
           *cw = run;
           run += v;
@@ -523,7 +693,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) route_scored_kernel(RouteArgs 
     for (int x = tid; x < nt * k; x += kTokThreads) {
       const int i = x / k, j = x - i * k;
       const int e = int(s_id[i * kMaxK + j]);
-      a.rank[size_t(t0) * k + x] = s_cnt[(j * kWarps + (i >> 5)) * E + e] + int(s_rk[i * kMaxK + j]);
+      a.rank[size_t(t0) * k + x] = s_cnt[(j * nw + (i >> 5)) * E + e] + int(s_rk[i * kMaxK + j]);
     }
   } else {
     // the whole batch is here: slots, offsets, rows and losses as the scan and finalize
@@ -533,9 +703,8 @@ __global__ void __launch_bounds__(kTokThreads, 1) route_scored_kernel(RouteArgs 
     int all = 0, kept = 0;
     if (tid < E) {
       for (int j = 0; j < k; ++j)
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          int* cw = s_cnt + (j * kWarps + w) * E + tid;
+        for (int w = 0; w < nw; ++w) {
+          int* cw = s_cnt + (j * nw + w) * E + tid;
           const int v = *cw;
           *cw = all;
           all += v;
@@ -574,7 +743,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) route_scored_kernel(RouteArgs 
     for (int x = tid; x < nt * k; x += kTokThreads) {
       const int i = x / k, j = x - i * k;
       const int e = int(s_id[i * kMaxK + j]);
-      const int slot = s_cnt[(j * kWarps + (i >> 5)) * E + e] + int(s_rk[i * kMaxK + j]);
+      const int slot = s_cnt[(j * nw + (i >> 5)) * E + e] + int(s_rk[i * kMaxK + j]);
       const bool in = a.C < 0 || slot < a.C;
       const int row = in ? s_first[e] + slot : -1;
       const float w = a.gate[x];
@@ -729,17 +898,22 @@ int launch_route_scored(const moe_config_t& c, const moe_score_t& sc, int C, con
                         const WsLayout& L, cudaStream_t st, const DispatchFuse* d) {
   RouteArgs a = route_args(c, C, logits, nullptr, out, ws, L);
   a.gm24 = a.ng > 1 ? ((1u << 24) + unsigned(a.gsz) - 1u) / unsigned(a.gsz) : 0u;
-  const size_t dyn = std::max(size_t(kTokWarps) * c.E * sizeof(double), size_t(c.k) * kWarps * c.E * 4);
-  const bool one = L.n_chunks == 1 && !d;
-  auto go = [&](auto kern) {
+  const bool one = L.n_chunks == 1 && !d, sig = sc.score == MOE_SCORE_SIGMOID;
+  auto launch = [&](auto kern) -> int {
+    const size_t dyn = std::max(size_t(kTokWarps) * c.E * sizeof(double), size_t(c.k) * kWarps * c.E * 4);
+    MOE_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(dyn)));
     return launch_kernel(kern, dim3(unsigned(L.n_chunks)), dim3(kTokThreads), dyn, st, a,
                          score_args(sc, select_bias));
   };
-  int rc;
-  if (c.E <= 32) rc = one ? go(route_scored_kernel<1, true>) : go(route_scored_kernel<1, false>);
-  else if (c.E <= 64) rc = one ? go(route_scored_kernel<2, true>) : go(route_scored_kernel<2, false>);
-  else if (c.E <= 128) rc = one ? go(route_scored_kernel<4, true>) : go(route_scored_kernel<4, false>);
-  else rc = one ? go(route_scored_kernel<8, true>) : go(route_scored_kernel<8, false>);
+  auto go = [&](auto q) -> int {
+    constexpr int Q = decltype(q)::value;
+    if (sig) return one ? launch(route_scored_kernel<Q, true, true>) : launch(route_scored_kernel<Q, true, false>);
+    return one ? launch(route_scored_kernel<Q, false, true>) : launch(route_scored_kernel<Q, false, false>);
+  };
+  const int rc = c.E <= 32    ? go(std::integral_constant<int, 1>{})
+                 : c.E <= 64  ? go(std::integral_constant<int, 2>{})
+                 : c.E <= 128 ? go(std::integral_constant<int, 4>{})
+                              : go(std::integral_constant<int, 8>{});
   if (rc != MOE_OK || one) return rc;
   return launch_scan_finalize(c, a, d, st);
 }
