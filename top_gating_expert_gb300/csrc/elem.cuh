@@ -32,6 +32,11 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, VEC>& r) {
   if constexpr (VEC * sizeof(T) == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(r.v);
   else *p = r.v[0];
 }
+// the same from shared memory, where a piece is 16 or 4 bytes
+template <typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> load_piece(const void* p) {
+  return load_vec<T, VEC>(static_cast<const T*>(p));
+}
 // VEC floats from a 16-byte aligned address (VEC 4 or 8), or one
 template <int VEC>
 __device__ __forceinline__ void load_floats(const float* p, float (&f)[VEC]) {

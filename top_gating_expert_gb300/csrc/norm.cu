@@ -9,14 +9,18 @@
 // E[h^2] - mean^2, which cancels when a channel's offset is large against its spread). Both
 // directions are bound by memory: every input is read once and every output written once.
 //
-// norm_fwd_kernel, norm_bwd_kernel: G warps a row (G = 1 .. 16, by the row's length), each lane NV
-// 16-byte vectors of it, held in registers from the one load to the store; the two row sums of
-// each direction cross the warps through shared memory. The backward's CTAs walk rows and keep
-// the column sums of dgamma and dbeta in registers, a column belonging to the same lane in
-// every row, so dy and h are read once for all three results; the CTAs' partial sums are
-// added by norm_bwd_sum_kernel in CTA order. Rows that no 16-byte access fits take the same
-// kernels with one element a vector. Rows too long for the registers take the *_any kernels,
-// which walk a row again from cache.
+// Ring kernels (norm_fwd_ring_kernel, norm_bwd_ring_kernel), for many rows: CTAs of 16 warps, one an
+// SM, G warps a row (by its length) and 16 / G rows at a time, each group of warps walking rows of
+// its own. A lane copies its own pieces of the rows to come into its own shared memory with
+// cp.async and reads only those back, so the copies need no barrier; 64 to 128 KB an SM are
+// then in flight whatever the registers hold. The two row sums of each direction cross the
+// group's warps under a barrier of their own. gamma and beta stay in registers; the backward
+// keeps the column sums of dgamma and dbeta there too (a column belongs to the same lane in
+// every row), so dy and h are read once for all three results. The CTAs' partial sums are added
+// by norm_bwd_sum_kernel in CTA order.
+// Register kernels (norm_fwd_kernel, norm_bwd_kernel): the same without the ring, for few rows
+// (one vector a lane, more warps a row: latency) and for rows that no cp.async fits. Rows too long
+// for either take the *_any kernels, which walk a row again from cache.
 #include <algorithm>
 
 #include "elem.cuh"
@@ -168,9 +172,8 @@ __device__ __forceinline__ float row_sum(float v, int G, float* s_red) {
   const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) s_red[warp] = v;
   __syncthreads();
-  const float* r = s_red + warp / G * G;
-  float t = 0.f;
-  for (int w = 0; w < G; ++w) t += r[w];
+  float t = s_red[warp / G * G + (threadIdx.x & (G - 1))];
+  for (int off = G >> 1; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
   return t;
 }
 
@@ -322,10 +325,11 @@ __global__ void __launch_bounds__(512)
         s_red[buf + 1][warp] = s2;
       }
       __syncthreads();
-      s1 = s2 = 0.f;
-      for (int w = 0; w < G; ++w) {
-        s1 += s_red[buf][slot * G + w];
-        s2 += s_red[buf + 1][slot * G + w];
+      s1 = s_red[buf][slot * G + (lane & (G - 1))];
+      s2 = s_red[buf + 1][slot * G + (lane & (G - 1))];
+      for (int off = G >> 1; off > 0; off >>= 1) {
+        s1 += __shfl_xor_sync(0xffffffffu, s1, off);
+        s2 += __shfl_xor_sync(0xffffffffu, s2, off);
       }
     }
     s1 *= inv_m;
@@ -365,6 +369,270 @@ __global__ void __launch_bounds__(512)
   }
 }
 
+// ------------------------------------------------------------------ ring kernels
+constexpr int kRingWarps = 16;
+
+// BYTES (16 or 4) of this lane, global to shared, and the groups of such copies.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Sum of v over the G warps of a row's group (s_red: one float a warp of the group, free until
+// the group's next barrier but one); a fixed tree, every lane gets it.
+__device__ __forceinline__ float group_sum(float v, int G, int slot, float* s_red) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if (G == 1) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) s_red[(threadIdx.x >> 5) & (G - 1)] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(G * 32) : "memory");
+  v = s_red[lane & (G - 1)];
+  for (int off = G >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+constexpr int kFwdStages = 3;
+
+template <typename T, int VEC, int NV>
+__global__ void __launch_bounds__(32 * kRingWarps, 1)
+    norm_fwd_ring_kernel(const T* x, const T* res, const float* __restrict__ gamma,
+                         const float* __restrict__ beta, T* h, T* y, float* mean, float* rstd, int G,
+                         moe_norm_t n) {
+  constexpr int BYTES = VEC * int(sizeof(T));
+  extern __shared__ __align__(16) uint8_t s_ring[];  // [stage][stream][NV][thread] pieces
+  __shared__ float s_red[kRingWarps][2][kRingWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slots = kRingWarps / G, slot = warp / G;
+  const int M = n.cols, step = G * 32 * VEC, c0 = ((warp & (G - 1)) * 32 + lane) * VEC;
+  const int streams = res ? 2 : 1;
+  auto piece = [&](int stage, int stream, int i) {
+    return s_ring + size_t(((stage * streams + stream) * NV + i) * (32 * kRingWarps) + tid) * BYTES;
+  };
+  float g[NV][VEC], b[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) g[i][q] = b[i][q] = 0.f;
+    if (c0 + i * step < M) {
+      load_floats<VEC>(gamma + c0 + i * step, g[i]);
+      if (beta) load_floats<VEC>(beta + c0 + i * step, b[i]);
+    }
+  }
+  const int64_t stride = int64_t(gridDim.x) * slots;
+  auto fetch = [&](int64_t r, int stage) {
+    if (r < n.rows) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = c0 + i * step;
+        if (c < M) {
+          copy_async<BYTES>(piece(stage, 0, i), x + r * n.ldx + c);
+          if (res) copy_async<BYTES>(piece(stage, 1, i), res + r * n.ldr + c);
+        }
+      }
+    }
+    copy_commit();  // an empty group at the end: the waits count groups
+  };
+  int64_t r = int64_t(blockIdx.x) * slots + slot;
+#pragma unroll
+  for (int s = 0; s < kFwdStages - 1; ++s) fetch(r + s * stride, s);
+  int stage = 0;
+  for (; r < n.rows; r += stride) {
+    fetch(r + (kFwdStages - 1) * stride, stage == 0 ? kFwdStages - 1 : stage - 1);
+    copy_wait<kFwdStages - 1>();
+    float v[NV][VEC], s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = c0 + i * step;
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) v[i][q] = 0.f;
+      if (c < M) {
+        const Vec<T, VEC> xv = load_piece<T, VEC>(piece(stage, 0, i));
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) v[i][q] = to_f32(xv.v[q]);
+        if (res) {
+          const Vec<T, VEC> rv = load_piece<T, VEC>(piece(stage, 1, i));
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) v[i][q] += to_f32(rv.v[q]);
+        }
+        if (h) {
+          Vec<T, VEC> o;
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) o.v[q] = from_f32<T>(v[i][q]);
+          store_vec<T, VEC>(h + r * n.ldh + c, o);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) s += v[i][q];
+    }
+    stage = stage + 1 == kFwdStages ? 0 : stage + 1;
+    const float mu = group_sum(s, G, slot, s_red[slot][0]) / float(M);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (c0 + i * step < M) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) {
+          v[i][q] -= mu;
+          ss = fmaf(v[i][q], v[i][q], ss);
+        }
+      }
+    const float rs = 1.f / sqrtf(group_sum(ss, G, slot, s_red[slot][1]) / float(M) + n.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = c0 + i * step;
+      if (c >= M) continue;
+      Vec<T, VEC> o;
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) o.v[q] = from_f32<T>(fmaf(v[i][q] * rs, g[i][q], b[i][q]));
+      store_vec<T, VEC>(y + r * n.ldy + c, o);
+    }
+    if (lane == 0 && (warp & (G - 1)) == 0) {
+      if (mean) mean[r] = mu;
+      if (rstd) rstd[r] = rs;
+    }
+  }
+}
+
+// part: [gridDim.x][2][cols], null when neither dgamma nor dbeta is wanted.
+template <typename T, int VEC, int NV, int STAGES>
+__global__ void __launch_bounds__(32 * kRingWarps, 1)
+    norm_bwd_ring_kernel(const T* dy, const T* h, const float* __restrict__ gamma,
+                         const float* __restrict__ mean, const float* __restrict__ rstd, const T* dh, T* dx,
+                         float* __restrict__ part, int G, moe_norm_t n) {
+  constexpr int BYTES = VEC * int(sizeof(T));
+  extern __shared__ __align__(16) uint8_t s_ring[];  // [stage][stream][NV][thread] pieces, then
+                                                     // the slots' column sums
+  __shared__ float s_red[kRingWarps][4][kRingWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slots = kRingWarps / G, slot = warp / G;
+  const int M = n.cols, step = G * 32 * VEC, c0 = ((warp & (G - 1)) * 32 + lane) * VEC;
+  const int streams = dh ? 3 : 2;
+  const float inv_m = 1.f / float(M);
+  auto piece = [&](int stage, int stream, int i) {
+    return s_ring + size_t(((stage * streams + stream) * NV + i) * (32 * kRingWarps) + tid) * BYTES;
+  };
+  float g[NV][VEC], sg[NV][VEC], sb[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) g[i][q] = sg[i][q] = sb[i][q] = 0.f;
+    if (c0 + i * step < M) load_floats<VEC>(gamma + c0 + i * step, g[i]);
+  }
+  const int64_t stride = int64_t(gridDim.x) * slots;
+  auto fetch = [&](int64_t r, int stage) {
+    if (r < n.rows) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = c0 + i * step;
+        if (c < M) {
+          copy_async<BYTES>(piece(stage, 0, i), h + r * n.ldx + c);
+          copy_async<BYTES>(piece(stage, 1, i), dy + r * n.ldy + c);
+          if (dh) copy_async<BYTES>(piece(stage, 2, i), dh + r * n.ldr + c);
+        }
+      }
+    }
+    copy_commit();
+  };
+  int64_t r = int64_t(blockIdx.x) * slots + slot;
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) fetch(r + s * stride, s);
+  float mu = r < n.rows ? __ldg(mean + r) : 0.f, rs = r < n.rows ? __ldg(rstd + r) : 0.f;
+  int stage = 0, odd = 0;
+  for (; r < n.rows; r += stride) {
+    fetch(r + (STAGES - 1) * stride, stage == 0 ? STAGES - 1 : stage - 1);
+    const float mu_r = mu, rs_r = rs;
+    if (r + stride < n.rows) {
+      mu = __ldg(mean + r + stride);
+      rs = __ldg(rstd + r + stride);
+    }
+    copy_wait<STAGES - 1>();
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (c0 + i * step >= M) continue;
+      const Vec<T, VEC> hv = load_piece<T, VEC>(piece(stage, 0, i)), dv = load_piece<T, VEC>(piece(stage, 1, i));
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) {
+        const float d = to_f32(dv.v[q]), xh = __fmul_rn(to_f32(hv.v[q]) - mu_r, rs_r);
+        const float gd = product(d, g[i][q]);
+        sg[i][q] = fmaf(d, xh, sg[i][q]);
+        sb[i][q] += d;
+        s1 += gd;
+        s2 = fmaf(gd, xh, s2);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      s1 += __shfl_xor_sync(0xffffffffu, s1, off);
+      s2 += __shfl_xor_sync(0xffffffffu, s2, off);
+    }
+    if (G > 1) {
+      float* red = s_red[slot][2 * odd];  // two places in turn: one barrier a row
+      if (lane == 0) {
+        red[warp & (G - 1)] = s1;
+        red[kRingWarps + (warp & (G - 1))] = s2;
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(G * 32) : "memory");
+      s1 = red[lane & (G - 1)];
+      s2 = red[kRingWarps + (lane & (G - 1))];
+      for (int off = G >> 1; off > 0; off >>= 1) {
+        s1 += __shfl_xor_sync(0xffffffffu, s1, off);
+        s2 += __shfl_xor_sync(0xffffffffu, s2, off);
+      }
+    }
+    s1 *= inv_m;
+    s2 *= inv_m;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = c0 + i * step;
+      if (c >= M) continue;
+      const Vec<T, VEC> hv = load_piece<T, VEC>(piece(stage, 0, i)), dv = load_piece<T, VEC>(piece(stage, 1, i));
+      Vec<T, VEC> ev, o;
+      if (dh) ev = load_piece<T, VEC>(piece(stage, 2, i));
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) {
+        const float xh = __fmul_rn(to_f32(hv.v[q]) - mu_r, rs_r);
+        float v = rs_r * (product(to_f32(dv.v[q]), g[i][q]) - s1 - xh * s2);
+        if (dh) v += to_f32(ev.v[q]);
+        o.v[q] = from_f32<T>(v);
+      }
+      store_vec<T, VEC>(dx + r * n.ldh + c, o);
+    }
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    odd ^= 1;
+  }
+  if (!part) return;
+  // the slots' column sums, added in slot order
+  copy_wait<0>();
+  float* s_cols = reinterpret_cast<float*>(s_ring);
+  const int width = step * NV;
+  float* out = part + int64_t(blockIdx.x) * 2 * M;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) s_cols[slot * width + c0 + i * step + q] = which ? sb[i][q] : sg[i][q];
+    __syncthreads();
+    for (int c = tid; c < M; c += 32 * kRingWarps) {
+      float t = 0.f;
+      for (int w = 0; w < slots; ++w) t += s_cols[w * width + c];
+      out[which * M + c] = t;
+    }
+  }
+}
+
 constexpr int kMaxSlices = 608;  // four CTAs an SM
 
 int check_norm(const moe_norm_t* n) {
@@ -375,10 +643,11 @@ int check_norm(const moe_norm_t* n) {
   return MOE_OK;
 }
 
-// Rows held in registers are at most 8192 long; the slices of longer ones share 2048 CTAs.
+// The slices of rows that are not held whole share 2048 CTAs; the ring and register kernels write
+// at most kMaxSlices, one an SM (ring) where rows are longer than 8192.
 int any_slices(int cols) { return std::max(1, std::min(kMaxSlices, 2048 / ((cols + kSliceCols - 1) / kSliceCols))); }
 size_t norm_ws_bytes(const moe_norm_t& n) {
-  const int slices = n.cols <= 8192 ? kMaxSlices : any_slices(n.cols);
+  const int slices = n.cols <= 8192 ? kMaxSlices : std::max(any_slices(n.cols), 160);
   return 256 + align256(size_t(slices) * 2 * size_t(n.cols) * 4);
 }
 
@@ -386,20 +655,42 @@ bool vec_ok(const void* p, int64_t ld, int vec, size_t eb) {
   return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % vec == 0 && eb * vec == 16);
 }
 
-// Warps a row (a power of two up to 16) so that NV vectors a lane hold it; 0: too long.
-int row_warps(int cols, int vec, int nv) {
+// Warps a row (a power of two up to most) so that NV vectors a lane hold it; 0: too long.
+int row_warps(int cols, int vec, int nv, int most = 16) {
   int G = 1;
-  while (G <= 16 && int64_t(G) * 32 * vec * nv < cols) G *= 2;
-  return G <= 16 ? G : 0;
+  while (G <= most && int64_t(G) * 32 * vec * nv < cols) G *= 2;
+  return G <= most ? G : 0;
 }
 
 template <typename T, int VEC>
 int norm_forward_v(const moe_norm_t& n, const T* x, const T* res, const float* gamma, const float* beta,
                    T* h, T* y, float* mean, float* rstd, cudaStream_t st) {
-  // vectors a lane: one while the rows are few (more warps share a row's latency), else 32
-  // floats a lane, which keeps more loads in flight per warp
+  // vectors a lane: one while the rows are few (more warps share a row's latency), else up to
+  // 32 floats a lane
   constexpr int kMost = VEC == 8 ? 4 : 8;
   const bool few = n.rows <= 2 * num_sms();
+  if constexpr (VEC * sizeof(T) >= 4) {
+    constexpr int kRing = VEC == 1 ? 8 : 4;  // what shared memory holds
+    int nv = 1;
+    int G = row_warps(n.cols, VEC, nv, 1);
+    while (G == 0 && nv < kRing) G = row_warps(n.cols, VEC, nv *= 2, nv == kRing ? 16 : 1);
+    if (!few && G) {
+      const int slots = kRingWarps / G;
+      const unsigned grid = unsigned(std::min<int64_t>((n.rows + slots - 1) / slots, num_sms()));
+      const size_t smem = size_t(kFwdStages) * (res ? 2 : 1) * nv * 32 * kRingWarps * VEC * sizeof(T);
+      auto go = [&](auto kern) -> int {
+        MOE_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+        return launch_kernel(kern, dim3(grid), dim3(32 * kRingWarps), smem, st, x, res, gamma, beta, h, y, mean,
+                             rstd, G, n);
+      };
+      switch (nv) {
+        case 1: return go(norm_fwd_ring_kernel<T, VEC, 1>);
+        case 2: return go(norm_fwd_ring_kernel<T, VEC, 2>);
+        case 4: return go(norm_fwd_ring_kernel<T, VEC, 4>);
+      }
+      if constexpr (kRing == 8) return go(norm_fwd_ring_kernel<T, VEC, 8>);
+    }
+  }
   int nv = few ? 1 : kMost;
   if (!few)  // no more than the row needs
     while (nv > 1 && 32 * VEC * (nv / 2) >= n.cols) nv /= 2;
@@ -444,8 +735,37 @@ int norm_backward_v(const moe_norm_t& n, const T* dy, const T* h, const float* g
                     cudaStream_t st) {
   int rc;
   const bool sums = dgamma || dbeta;
+  if constexpr (VEC * sizeof(T) >= 4) {
+    // more vectors a lane before more warps a row, up to 16 columns a lane (32 column sums and
+    // 16 of gamma: no spills); twice that for the longest bf16 rows and for single elements (for
+    // fp32 vectors shared memory does not hold it). Three stages, two where they would not fit
+    constexpr int kMore = VEC == 8 ? 2 : 4, kRing = VEC == 4 ? 4 : 2 * kMore;
+    int nv = 1;
+    int G = row_warps(n.cols, VEC, nv, 1);
+    while (G == 0 && nv < kRing) G = row_warps(n.cols, VEC, nv *= 2, nv >= kMore ? 16 : 1);
+    if (G) {
+      const int slots = kRingWarps / G;
+      const int grid = int(std::min<int64_t>((n.rows + slots - 1) / slots, std::min(num_sms(), 160)));
+      auto go = [&](auto kern, int stages) -> int {
+        const size_t ring = size_t(stages) * (dh ? 3 : 2) * nv * 32 * kRingWarps * VEC * sizeof(T);
+        const size_t smem = std::max(ring, sums ? size_t(kRingWarps) * 32 * VEC * nv * 4 : size_t(0));
+        MOE_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+        return launch_kernel(kern, dim3(unsigned(grid)), dim3(32 * kRingWarps), smem, st, dy, h, gamma, mean, rstd,
+                             dh, dx, sums ? part : nullptr, G, n);
+      };
+      rc = MOE_ERR_UNSUPPORTED;
+      if (nv == 1) rc = go(norm_bwd_ring_kernel<T, VEC, 1, 3>, 3);
+      if (nv == 2) rc = go(norm_bwd_ring_kernel<T, VEC, 2, 3>, 3);
+      if (nv == 4) rc = go(norm_bwd_ring_kernel<T, VEC, 4, VEC == 1 ? 3 : 2>, VEC == 1 ? 3 : 2);
+      if constexpr (kRing == 8) {
+        if (nv == 8) rc = go(norm_bwd_ring_kernel<T, VEC, 8, 2>, 2);
+      }
+      if (rc != MOE_OK || !sums) return rc;
+      return launch_norm_sum(part, grid, n.cols, dgamma, dbeta, st);
+    }
+  }
   int nv = 1;
-  constexpr int kMost = VEC == 1 ? 8 : 2;
+  constexpr int kMost = VEC == 1 ? 8 : 1;
   int G = row_warps(n.cols, VEC, nv);
   while (G == 0 && nv < kMost) G = row_warps(n.cols, VEC, nv *= 2);
   if (G == 0) {  // too long for the registers: the column sums first (dx may be written over dy)
@@ -474,8 +794,8 @@ int norm_backward_v(const moe_norm_t& n, const T* dy, const T* h, const float* g
   };
   rc = MOE_ERR_UNSUPPORTED;
   if (nv == 1) rc = go(norm_bwd_kernel<T, VEC, 1>);
-  if (nv == 2) rc = go(norm_bwd_kernel<T, VEC, 2>);
   if constexpr (kMost == 8) {
+    if (nv == 2) rc = go(norm_bwd_kernel<T, VEC, 2>);
     if (nv == 4) rc = go(norm_bwd_kernel<T, VEC, 4>);
     if (nv == 8) rc = go(norm_bwd_kernel<T, VEC, 8>);
   }
