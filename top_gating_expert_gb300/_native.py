@@ -138,6 +138,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """The loaded library. Raises if it has not been built: there is no fallback."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.library_path()

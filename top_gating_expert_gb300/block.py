@@ -15,49 +15,102 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+from functools import lru_cache
 
 import torch
 
 from . import _native as N
 from . import moe
-from .moe import _check, _ptr, _stream
+from .moe import _check, _raw_stream
 
 _DTYPES = {torch.float32: N.MOE_F32, torch.bfloat16: N.MOE_BF16}
+_F32 = torch.float32
 
 
-def _matrix(t, name, where, rows=None, cols=None, dtype=None, device=None):
-    """Checks one matrix; returns its row stride in elements."""
+@lru_cache(maxsize=None)
+def _entry(name):
+    return getattr(N.lib(), name)
+
+
+# The checks run on every call of a serving loop: attributes that cost little (shape, dtype, device
+# number, strides), and the message only when one fails.
+def _first(t, name, where):
+    """Checks the matrix that the others are compared with: (shape, dtype, device number, ld)."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{where}: {name} must be a 2-D tensor")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{where}: {name} must be on {device or 'a CUDA device'}")
-    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{where}: {name} must be {dtype or 'float32 or bfloat16'}, not {t.dtype}")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{where}: {name} must be float32 or bfloat16, not {t.dtype}")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{where}: {name} must be on a CUDA device")
+    if t.shape[1] < 1:
+        raise ValueError(f"{where}: {name} has no columns")
+    return t.shape, t.dtype, dev, _ld(t, name, where)
+
+
+def _ld(t, name, where):
+    """The row stride in elements."""
     r, c = t.shape
-    if c < 1 or (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected "
-                         f"({'any' if rows is None else rows}, {'any >= 1' if cols is None else cols})")
-    if c > 1 and t.stride(1) != 1:
+    s0, s1 = t.stride()
+    if s1 == 1 and s0 >= c:
+        return s0
+    if c > 1 and s1 != 1:
         raise ValueError(f"{where}: the columns of {name} must be contiguous")
-    if r > 1 and t.stride(0) < c:
-        raise ValueError(f"{where}: the rows of {name} overlap (row stride {t.stride(0)})")
-    return max(t.stride(0), c) if r > 1 else c
+    if r > 1 and s0 < c:
+        raise ValueError(f"{where}: the rows of {name} overlap (row stride {s0})")
+    return max(s0, c) if r > 1 else c
 
 
-def _vector(t, name, where, n, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != (n,) \
-            or t.device != device or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{where}: {name} must be a contiguous float32 tensor of {n} elements on {device}")
+def _matrix(t, name, where, shape, dt, dev):
+    """Checks another matrix against a shape, type and device; returns its row stride."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dt or t.get_device() != dev:
+        raise ValueError(f"{where}: {name} must be a {dt} tensor of shape {tuple(shape)} on CUDA device {dev}, "
+                         f"got {getattr(t, 'dtype', type(t))} {tuple(getattr(t, 'shape', ()))}")
+    return _ld(t, name, where)
 
 
-def _workspace_ok(ws, where, device):
-    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
-        raise ValueError(f"{where}: ws must be a contiguous uint8 tensor on {device}")
+def _vector(t, name, where, n, dev):
+    if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or t.shape != (n,) or t.get_device() != dev \
+            or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be a contiguous float32 tensor of {n} elements on CUDA device {dev}")
+
+
+def _workspace_ok(ws, where, dev):
+    if not isinstance(ws, torch.Tensor) or ws.dtype is not torch.uint8 or not ws.is_contiguous() \
+            or ws.get_device() != dev:
+        raise ValueError(f"{where}: ws must be a contiguous uint8 tensor on CUDA device {dev}")
 
 
 def _on(stream):
     """Allocations made for a call belong to the stream that the call runs on."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+@lru_cache(maxsize=None)
+def _device(dev):
+    return torch.device("cuda", dev)
+
+
+def _new(shape, dtype, dev, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=_device(dev))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=_device(dev))
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+# Argument structs by their values; the library reads them during a call only.
+@lru_cache(maxsize=512)
+def _norm_args(*fields):
+    return ctypes.byref(N.MoeNorm(*fields))
+
+
+@lru_cache(maxsize=512)
+def _linear_args(*fields):
+    return ctypes.byref(N.MoeLinear(*fields))
 
 
 # ------------------------------------------------------------------ layer norm
@@ -66,38 +119,37 @@ def layer_norm(x, gamma, beta=None, eps=1e-5, residual=None, *, out=None, h=None
     """(y, h, mean, rstd): h = x (+ residual) and y = (h - mean) * rstd * gamma (+ beta), row by
     row, rstd = 1 / sqrt(var + eps). Without a residual h is x itself, and nothing is stored."""
     w = "layer_norm"
-    ldx = _matrix(x, "x", w)
-    T, M = x.shape
-    dev, dt = x.device, x.dtype
-    ldr = M if residual is None else _matrix(residual, "residual", w, T, M, dt, dev)
+    shape, dt, dev, ldx = _first(x, "x", w)
+    T, M = shape
+    ldr = M if residual is None else _matrix(residual, "residual", w, shape, dt, dev)
     _vector(gamma, "gamma", w, M, dev)
     if beta is not None:
         _vector(beta, "beta", w, M, dev)
-    with _on(stream):
-        if out is None:
-            out = torch.empty((T, M), dtype=dt, device=dev)
-        if residual is not None and h is None:
-            h = torch.empty((T, M), dtype=dt, device=dev)
-        if mean is None:
-            mean = torch.empty(T, dtype=torch.float32, device=dev)
-        if rstd is None:
-            rstd = torch.empty(T, dtype=torch.float32, device=dev)
-    ldy = _matrix(out, "out", w, T, M, dt, dev)
-    ldh = M if h is None else _matrix(h, "h", w, T, M, dt, dev)
+    if out is None:
+        out = _new(shape, dt, dev, stream)
+    if residual is not None and h is None:
+        h = _new(shape, dt, dev, stream)
+    if mean is None:
+        mean = _new((T,), _F32, dev, stream)
+    if rstd is None:
+        rstd = _new((T,), _F32, dev, stream)
+    ldy = _matrix(out, "out", w, shape, dt, dev)
+    ldh = M if h is None else _matrix(h, "h", w, shape, dt, dev)
     _vector(mean, "mean", w, T, dev)
     _vector(rstd, "rstd", w, T, dev)
-    n = N.MoeNorm(rows=T, cols=M, dtype=_DTYPES[dt], eps=float(eps), ldx=ldx, ldr=ldr, ldh=ldh, ldy=ldy)
-    _check(N.lib().moe_norm_forward(ctypes.byref(n), _ptr(x), _ptr(residual), _ptr(gamma), _ptr(beta),
-                                    _ptr(h), _ptr(out), _ptr(mean), _ptr(rstd), _stream(stream)),
-           "moe_norm_forward")
+    rc = _entry("moe_norm_forward")(_norm_args(T, M, _DTYPES[dt], eps, ldx, ldr, ldh, ldy), x.data_ptr(),
+                                    _p(residual), gamma.data_ptr(), _p(beta), _p(h), out.data_ptr(),
+                                    mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_norm_forward")
     return out, (x if h is None else h), mean, rstd
 
 
 def layer_norm_workspace(T, M, dtype=torch.bfloat16, device="cuda"):
     """A zero-filled workspace for layer_norm_backward on [T, M] matrices."""
-    n = N.MoeNorm(rows=T, cols=M, dtype=_DTYPES[dtype], eps=0.0, ldx=M, ldr=M, ldh=M, ldy=M)
     b = N.c_size_t()
-    _check(N.lib().moe_norm_workspace_bytes(ctypes.byref(n), ctypes.byref(b)), "moe_norm_workspace_bytes")
+    _check(N.lib().moe_norm_workspace_bytes(_norm_args(T, M, _DTYPES[dtype], 0.0, M, M, M, M), ctypes.byref(b)),
+           "moe_norm_workspace_bytes")
     return torch.zeros(b.value, dtype=torch.uint8, device=device)
 
 
@@ -107,32 +159,33 @@ def layer_norm_backward(dy, h, gamma, mean, rstd, dh=None, *, need_beta=True, dx
     dh that reaches h on its other path; dx is the gradient of x and of the residual alike.
     dbeta is None unless need_beta."""
     w = "layer_norm_backward"
-    ldy = _matrix(dy, "dy", w)
-    T, M = dy.shape
-    dev, dt = dy.device, dy.dtype
-    ldx = _matrix(h, "h", w, T, M, dt, dev)
-    ldr = M if dh is None else _matrix(dh, "dh", w, T, M, dt, dev)
+    shape, dt, dev, ldy = _first(dy, "dy", w)
+    T, M = shape
+    ldx = _matrix(h, "h", w, shape, dt, dev)
+    ldr = M if dh is None else _matrix(dh, "dh", w, shape, dt, dev)
     _vector(gamma, "gamma", w, M, dev)
     _vector(mean, "mean", w, T, dev)
     _vector(rstd, "rstd", w, T, dev)
-    with _on(stream):
-        if dx is None:
-            dx = torch.empty((T, M), dtype=dt, device=dev)
-        if dgamma is None:
-            dgamma = torch.empty(M, dtype=torch.float32, device=dev)
-        if need_beta and dbeta is None:
-            dbeta = torch.empty(M, dtype=torch.float32, device=dev)
-        if ws is None:
-            ws = layer_norm_workspace(T, M, dt, dev)
-    ldh = _matrix(dx, "dx", w, T, M, dt, dev)
+    if dx is None:
+        dx = _new(shape, dt, dev, stream)
+    if dgamma is None:
+        dgamma = _new((M,), _F32, dev, stream)
+    if need_beta and dbeta is None:
+        dbeta = _new((M,), _F32, dev, stream)
+    if ws is None:
+        with _on(stream):
+            ws = layer_norm_workspace(T, M, dt, dy.device)
+    ldh = _matrix(dx, "dx", w, shape, dt, dev)
     _vector(dgamma, "dgamma", w, M, dev)
     if dbeta is not None:
         _vector(dbeta, "dbeta", w, M, dev)
     _workspace_ok(ws, w, dev)
-    n = N.MoeNorm(rows=T, cols=M, dtype=_DTYPES[dt], eps=0.0, ldx=ldx, ldr=ldr, ldh=ldh, ldy=ldy)
-    _check(N.lib().moe_norm_backward(ctypes.byref(n), _ptr(dy), _ptr(h), _ptr(gamma), _ptr(mean),
-                                     _ptr(rstd), _ptr(dh), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
-                                     _ptr(ws), ws.numel(), _stream(stream)), "moe_norm_backward")
+    rc = _entry("moe_norm_backward")(_norm_args(T, M, _DTYPES[dt], 0.0, ldx, ldr, ldh, ldy), dy.data_ptr(),
+                                     h.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _p(dh),
+                                     dx.data_ptr(), dgamma.data_ptr(), _p(dbeta), ws.data_ptr(), ws.numel(),
+                                     _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_norm_backward")
     return dx, dgamma, dbeta
 
 
@@ -155,33 +208,32 @@ def linear(x, W, bias=None, *, act="none", residual=None, save_pre=False, out=No
     for linear_backward, and None otherwise. act: "none", "relu", "gelu", "gelu_tanh", "silu".
     """
     w = "linear"
-    if act not in N.LIN_ACTS:
+    code = N.LIN_ACTS.get(act)
+    if code is None:
         raise ValueError(f"{w}: act must be one of {sorted(N.LIN_ACTS)}, not {act!r}")
-    ldx = _matrix(x, "x", w)
-    T, K = x.shape
-    dev, dt = x.device, x.dtype
-    ldw = _matrix(W, "W", w, None, K, dt, dev)
-    n_out = W.shape[0]
-    if n_out < 1:
-        raise ValueError(f"{w}: W has no rows")
+    (T, K), dt, dev, ldx = _first(x, "x", w)
+    (n_out, kw), dtw, devw, ldw = _first(W, "W", w)
+    if kw != K or dtw is not dt or devw != dev or n_out < 1:
+        raise ValueError(f"{w}: W must be a {dt} tensor of shape (any >= 1, {K}) on CUDA device {dev}")
+    shape = (T, n_out)
     if bias is not None:
         _vector(bias, "bias", w, n_out, dev)
-    ldr = n_out if residual is None else _matrix(residual, "residual", w, T, n_out, dt, dev)
-    with _on(stream):
-        if out is None:
-            out = torch.empty((T, n_out), dtype=dt, device=dev)
-        if save_pre and pre is None:
-            pre = torch.empty((T, n_out), dtype=dt, device=dev)
-        if ws is None:
-            ws = linear_workspace(T, n_out, K, dt, dev, backward=False)
-    ldy = _matrix(out, "out", w, T, n_out, dt, dev)
-    ldp = n_out if pre is None else _matrix(pre, "pre", w, T, n_out, dt, dev)
+    ldr = n_out if residual is None else _matrix(residual, "residual", w, shape, dt, dev)
+    if out is None:
+        out = _new(shape, dt, dev, stream)
+    if save_pre and pre is None:
+        pre = _new(shape, dt, dev, stream)
+    if ws is None:
+        with _on(stream):
+            ws = linear_workspace(T, n_out, K, dt, x.device, backward=False)
+    ldy = _matrix(out, "out", w, shape, dt, dev)
+    ldp = n_out if pre is None else _matrix(pre, "pre", w, shape, dt, dev)
     _workspace_ok(ws, w, dev)
-    p = N.MoeLinear(T=T, N=n_out, K=K, act=N.LIN_ACTS[act], dtype=_DTYPES[dt], ldx=ldx, ldw=ldw, ldy=ldy,
-                    ldr=ldr, ldp=ldp)
-    _check(N.lib().moe_linear_forward(ctypes.byref(p), _ptr(x), _ptr(W), _ptr(bias), _ptr(residual),
-                                      _ptr(out), _ptr(pre), _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_linear_forward")
+    rc = _entry("moe_linear_forward")(_linear_args(T, n_out, K, code, _DTYPES[dt], ldx, ldw, ldy, ldr, ldp),
+                                      x.data_ptr(), W.data_ptr(), _p(bias), _p(residual), out.data_ptr(),
+                                      _p(pre), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_linear_forward")
     return out, pre
 
 
@@ -191,36 +243,37 @@ def linear_backward(dy, x, W, *, act="none", pre=None, need_x=True, need_W=True,
     dx and dW in the element type, dbias float32; None for what is not needed. The gradient
     of the residual is dy itself."""
     w = "linear_backward"
-    if act not in N.LIN_ACTS:
+    code = N.LIN_ACTS.get(act)
+    if code is None:
         raise ValueError(f"{w}: act must be one of {sorted(N.LIN_ACTS)}, not {act!r}")
-    ldy = _matrix(dy, "dy", w)
-    T, n_out = dy.shape
-    dev, dt = dy.device, dy.dtype
-    ldx = _matrix(x, "x", w, T, None, dt, dev)
-    K = x.shape[1]
-    ldw = _matrix(W, "W", w, n_out, K, dt, dev)
-    if act != "none" and pre is None:
+    (T, n_out), dt, dev, ldy = _first(dy, "dy", w)
+    (tx, K), dtx, devx, ldx = _first(x, "x", w)
+    if tx != T or dtx is not dt or devx != dev:
+        raise ValueError(f"{w}: x must be a {dt} tensor of {T} rows on CUDA device {dev}")
+    ldw = _matrix(W, "W", w, (n_out, K), dt, dev)
+    if code and pre is None:
         raise ValueError(f"{w}: act {act!r} needs the forward's pre")
-    ldp = n_out if pre is None else _matrix(pre, "pre", w, T, n_out, dt, dev)
-    with _on(stream):
-        if need_x and dx is None:
-            dx = torch.empty((T, K), dtype=dt, device=dev)
-        if need_W and dW is None:
-            dW = torch.empty((n_out, K), dtype=dt, device=dev)
-        if need_bias and dbias is None:
-            dbias = torch.empty(n_out, dtype=torch.float32, device=dev)
-        if ws is None:
-            ws = linear_workspace(T, n_out, K, dt, dev)
-    lddx = K if dx is None else _matrix(dx, "dx", w, T, K, dt, dev)
-    lddw = K if dW is None else _matrix(dW, "dW", w, n_out, K, dt, dev)
+    ldp = n_out if pre is None else _matrix(pre, "pre", w, (T, n_out), dt, dev)
+    if need_x and dx is None:
+        dx = _new((T, K), dt, dev, stream)
+    if need_W and dW is None:
+        dW = _new((n_out, K), dt, dev, stream)
+    if need_bias and dbias is None:
+        dbias = _new((n_out,), _F32, dev, stream)
+    if ws is None:
+        with _on(stream):
+            ws = linear_workspace(T, n_out, K, dt, dy.device)
+    lddx = K if dx is None else _matrix(dx, "dx", w, (T, K), dt, dev)
+    lddw = K if dW is None else _matrix(dW, "dW", w, (n_out, K), dt, dev)
     if dbias is not None:
         _vector(dbias, "dbias", w, n_out, dev)
     _workspace_ok(ws, w, dev)
-    p = N.MoeLinear(T=T, N=n_out, K=K, act=N.LIN_ACTS[act], dtype=_DTYPES[dt], ldx=ldx, ldw=ldw, ldy=ldy,
-                    ldp=ldp, lddx=lddx, lddw=lddw)
-    _check(N.lib().moe_linear_backward(ctypes.byref(p), _ptr(dy), _ptr(x), _ptr(W), _ptr(pre), _ptr(dx),
-                                       _ptr(dW), _ptr(dbias), _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_linear_backward")
+    rc = _entry("moe_linear_backward")(
+        _linear_args(T, n_out, K, code, _DTYPES[dt], ldx, ldw, ldy, n_out, ldp, lddx, lddw), dy.data_ptr(),
+        x.data_ptr(), W.data_ptr(), _p(pre), _p(dx), _p(dW), _p(dbias), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_linear_backward")
     return dx, dW, dbias
 
 

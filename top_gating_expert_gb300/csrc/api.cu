@@ -24,6 +24,16 @@ int num_sms() {
   return n;
 }
 
+int allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& seen) {
+  int dev = 0;
+  MOE_CUDA_CHECK(cudaGetDevice(&dev));
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (seen.load(std::memory_order_acquire) & bit)) return MOE_OK;
+  MOE_CUDA_CHECK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  seen.fetch_or(bit, std::memory_order_release);
+  return MOE_OK;
+}
+
 namespace {
 
 int validate(const moe_config_t* c) {

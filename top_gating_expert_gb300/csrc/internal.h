@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "moe.h"
 
 namespace moe {
@@ -341,6 +343,11 @@ int launch_pack_transposed_f32(int mode, int swiglu, int groups, int N, int K, i
                                cudaStream_t st);
 
 int num_sms();
+
+// A kernel's opt-in to `bytes` of dynamic shared memory, once per device (`seen`: a static of the
+// caller, one per kernel): the attribute call would otherwise cost every launch about a
+// microsecond on the host.
+int allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& seen);
 
 // Programmatic dependent launch: every kernel of the library is launched with programmatic
 // stream serialisation (unless the environment sets MOE_PDL=0), so that it may start while

@@ -297,7 +297,8 @@ int run_tile(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
   const int smem = 1024 + p.stages * C::STAGE;
   if (p.stages * C::STAGE < C::DUMP) return MOE_ERR_UNSUPPORTED;
   auto kern = linear_tile_kernel<BN, TRANS>;
-  MOE_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  static std::atomic<unsigned long long> seen{0};
+  if ((rc = allow_smem(reinterpret_cast<const void*>(kern), smem, seen)) != MOE_OK) return rc;
   cudaLaunchConfig_t lc = {};
   const int64_t tj = (int64_t(cols) + BN - 1) / BN;
   if (tj > 65535) return MOE_ERR_UNSUPPORTED;
@@ -633,7 +634,8 @@ int run_pair(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
   p.e = e;
   p.status = status;
   auto kern = linear_pair_kernel<BN>;
-  MOE_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+  static std::atomic<unsigned long long> seen{0};
+  if ((rc = allow_smem(reinterpret_cast<const void*>(kern), C::SMEM, seen)) != MOE_OK) return rc;
   cudaLaunchConfig_t lc = {};
   lc.blockDim = dim3(kPairThreads);
   lc.dynamicSmemBytes = C::SMEM;
@@ -646,9 +648,13 @@ int run_pair(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
   lc.attrs = attr;
   lc.numAttrs = 1;
   lc.gridDim = dim3(2);
-  int clusters = 0;
-  if (cudaOccupancyMaxActiveClusters(&clusters, kern, &lc) != cudaSuccess || clusters < 1)
-    clusters = num_sms() / 2;
+  static std::atomic<int> resident{0};  // clusters the GPU holds at once (one kind of GPU)
+  int clusters = resident.load(std::memory_order_relaxed);
+  if (clusters == 0) {
+    if (cudaOccupancyMaxActiveClusters(&clusters, kern, &lc) != cudaSuccess || clusters < 1)
+      clusters = num_sms() / 2;
+    resident.store(clusters, std::memory_order_relaxed);
+  }
   lc.gridDim = dim3(unsigned(2 * std::min(clusters, p.tiles_m * p.tiles_n)));
   if (pdl_enabled()) {
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;

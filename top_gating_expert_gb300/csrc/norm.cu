@@ -29,6 +29,10 @@
 namespace moe {
 namespace {
 
+// makes a generic lambda's statics one per kernel
+template <int N>
+struct Tag {};
+
 constexpr int kThreadsN = 256;
 constexpr int kWarpsN = kThreadsN / 32;
 
@@ -678,17 +682,19 @@ int norm_forward_v(const moe_norm_t& n, const T* x, const T* res, const float* g
       const int slots = kRingWarps / G;
       const unsigned grid = unsigned(std::min<int64_t>((n.rows + slots - 1) / slots, num_sms()));
       const size_t smem = size_t(kFwdStages) * (res ? 2 : 1) * nv * 32 * kRingWarps * VEC * sizeof(T);
-      auto go = [&](auto kern) -> int {
-        MOE_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+      const size_t most = size_t(kFwdStages) * 2 * nv * 32 * kRingWarps * VEC * sizeof(T);
+      auto go = [&](auto kern, auto) -> int {
+        static std::atomic<unsigned long long> seen{0};
+        if (const int rc = allow_smem(reinterpret_cast<const void*>(kern), int(most), seen)) return rc;
         return launch_kernel(kern, dim3(grid), dim3(32 * kRingWarps), smem, st, x, res, gamma, beta, h, y, mean,
                              rstd, G, n);
       };
       switch (nv) {
-        case 1: return go(norm_fwd_ring_kernel<T, VEC, 1>);
-        case 2: return go(norm_fwd_ring_kernel<T, VEC, 2>);
-        case 4: return go(norm_fwd_ring_kernel<T, VEC, 4>);
+        case 1: return go(norm_fwd_ring_kernel<T, VEC, 1>, Tag<1>{});
+        case 2: return go(norm_fwd_ring_kernel<T, VEC, 2>, Tag<2>{});
+        case 4: return go(norm_fwd_ring_kernel<T, VEC, 4>, Tag<4>{});
       }
-      if constexpr (kRing == 8) return go(norm_fwd_ring_kernel<T, VEC, 8>);
+      if constexpr (kRing == 8) return go(norm_fwd_ring_kernel<T, VEC, 8>, Tag<8>{});
     }
   }
   int nv = few ? 1 : kMost;
@@ -746,19 +752,22 @@ int norm_backward_v(const moe_norm_t& n, const T* dy, const T* h, const float* g
     if (G) {
       const int slots = kRingWarps / G;
       const int grid = int(std::min<int64_t>((n.rows + slots - 1) / slots, std::min(num_sms(), 160)));
-      auto go = [&](auto kern, int stages) -> int {
+      auto go = [&](auto kern, int stages, auto) -> int {
         const size_t ring = size_t(stages) * (dh ? 3 : 2) * nv * 32 * kRingWarps * VEC * sizeof(T);
-        const size_t smem = std::max(ring, sums ? size_t(kRingWarps) * 32 * VEC * nv * 4 : size_t(0));
-        MOE_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+        const size_t cols = size_t(kRingWarps) * 32 * VEC * nv * 4;
+        const size_t smem = std::max(ring, sums ? cols : size_t(0));
+        const size_t most = std::max(size_t(stages) * 3 * nv * 32 * kRingWarps * VEC * sizeof(T), cols);
+        static std::atomic<unsigned long long> seen{0};
+        if (const int rc = allow_smem(reinterpret_cast<const void*>(kern), int(most), seen)) return rc;
         return launch_kernel(kern, dim3(unsigned(grid)), dim3(32 * kRingWarps), smem, st, dy, h, gamma, mean, rstd,
                              dh, dx, sums ? part : nullptr, G, n);
       };
       rc = MOE_ERR_UNSUPPORTED;
-      if (nv == 1) rc = go(norm_bwd_ring_kernel<T, VEC, 1, 3>, 3);
-      if (nv == 2) rc = go(norm_bwd_ring_kernel<T, VEC, 2, 3>, 3);
-      if (nv == 4) rc = go(norm_bwd_ring_kernel<T, VEC, 4, VEC == 1 ? 3 : 2>, VEC == 1 ? 3 : 2);
+      if (nv == 1) rc = go(norm_bwd_ring_kernel<T, VEC, 1, 3>, 3, Tag<1>{});
+      if (nv == 2) rc = go(norm_bwd_ring_kernel<T, VEC, 2, 3>, 3, Tag<2>{});
+      if (nv == 4) rc = go(norm_bwd_ring_kernel<T, VEC, 4, VEC == 1 ? 3 : 2>, VEC == 1 ? 3 : 2, Tag<4>{});
       if constexpr (kRing == 8) {
-        if (nv == 8) rc = go(norm_bwd_ring_kernel<T, VEC, 8, 2>, 2);
+        if (nv == 8) rc = go(norm_bwd_ring_kernel<T, VEC, 8, 2>, 2, Tag<8>{});
       }
       if (rc != MOE_OK || !sums) return rc;
       return launch_norm_sum(part, grid, n.cols, dgamma, dbeta, st);
@@ -787,8 +796,7 @@ int norm_backward_v(const moe_norm_t& n, const T* dy, const T* h, const float* g
   const int64_t need = (int64_t(n.rows) + slots - 1) / slots;
   const int grid = int(std::min<int64_t>(need, std::min(kMaxSlices, per_sm * num_sms())));
   const size_t smem = sums ? size_t(warps) * 32 * VEC * nv * 4 : 0;
-  auto go = [&](auto kern) -> int {
-    MOE_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+  auto go = [&](auto kern) -> int {  // at most 16 KB
     return launch_kernel(kern, dim3(unsigned(grid)), dim3(unsigned(32 * warps)), smem, st, dy, h, gamma, mean, rstd,
                          dh, dx, sums ? part : nullptr, G, n);
   };

@@ -900,8 +900,8 @@ int launch_route_scored(const moe_config_t& c, const moe_score_t& sc, int C, con
   a.gm24 = a.ng > 1 ? ((1u << 24) + unsigned(a.gsz) - 1u) / unsigned(a.gsz) : 0u;
   const bool one = L.n_chunks == 1 && !d, sig = sc.score == MOE_SCORE_SIGMOID;
   auto launch = [&](auto kern) -> int {
+    // at most 32 KB (E <= 256, k <= 8)
     const size_t dyn = std::max(size_t(kTokWarps) * c.E * sizeof(double), size_t(c.k) * kWarps * c.E * 4);
-    MOE_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(dyn)));
     return launch_kernel(kern, dim3(unsigned(L.n_chunks)), dim3(kTokThreads), dyn, st, a,
                          score_args(sc, select_bias));
   };

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
@@ -53,6 +54,11 @@ def torch_dtype(cfg) -> torch.dtype:
 
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _raw_stream(stream, dev: int):
+    """The cudaStream_t of a stream, or of the current one of CUDA device dev."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _stream(stream=None):
@@ -196,14 +202,18 @@ def make_score(score) -> N.MoeScore:
     scale."""
     if isinstance(score, N.MoeScore):
         return score
-    return N.MoeScore(score=N.SCORES[score.get("score", "sigmoid")], group_top=int(score.get("group_top", 1)),
-                      renorm=int(score.get("renorm", 1)), scale=float(score.get("scale", 1.0)))
+    return _score(N.SCORES[score.get("score", "sigmoid")], int(score.get("group_top", 1)),
+                  int(score.get("renorm", 1)), float(score.get("scale", 1.0)))
+
+
+@lru_cache(maxsize=64)
+def _score(*fields) -> N.MoeScore:  # by value; the library reads it during a call only
+    return N.MoeScore(*fields)
 
 
 def _check_f32(t, name: str, shape, where: str):
-    if t is None:
-        return
-    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != shape \
+            or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{where}: {name} must be a contiguous float32 CUDA tensor of shape {tuple(shape)}")
 
 
@@ -212,11 +222,14 @@ def route_scored(cfg, score, logits, select_bias, out: RouteOutputs, ws, stream=
     the bias takes part in the choice of the experts only, not in their weights."""
     c = _cfg(cfg)
     _check_f32(logits, "logits", (c.S, c.E), "route_scored")
-    _check_f32(select_bias, "select_bias", (c.E,), "route_scored")
-    s = out.struct()
-    _check(N.lib().moe_route_scored(ctypes.byref(c), ctypes.byref(make_score(score)), _ptr(logits),
-                                    _ptr(select_bias), ctypes.byref(s), _ptr(ws), ws.numel(),
-                                    _stream(stream)), "moe_route_scored")
+    bias = None
+    if select_bias is not None:
+        _check_f32(select_bias, "select_bias", (c.E,), "route_scored")
+        bias = select_bias.data_ptr()
+    rc = N.lib().moe_route_scored(ctypes.byref(c), ctypes.byref(make_score(score)), logits.data_ptr(), bias,
+                                  ctypes.byref(out.struct()), ws.data_ptr(), ws.numel(),
+                                  _raw_stream(stream, logits.get_device()))
+    _check(rc, "moe_route_scored")
 
 
 def route_scored_backward(cfg, score, logits, out: RouteOutputs, dgate, dlogits, aux_coef=0.0,
@@ -227,10 +240,10 @@ def route_scored_backward(cfg, score, logits, out: RouteOutputs, dgate, dlogits,
     _check_f32(logits, "logits", (c.S, c.E), "route_scored_backward")
     _check_f32(dgate, "dgate", (c.S, c.k), "route_scored_backward")
     _check_f32(dlogits, "dlogits", (c.S, c.E), "route_scored_backward")
-    s = out.struct()
-    _check(N.lib().moe_route_scored_backward(
-        ctypes.byref(c), ctypes.byref(make_score(score)), _ptr(logits), ctypes.byref(s), _ptr(dgate),
-        float(aux_coef), float(z_coef), _ptr(dlogits), _stream(stream)), "moe_route_scored_backward")
+    rc = N.lib().moe_route_scored_backward(
+        ctypes.byref(c), ctypes.byref(make_score(score)), logits.data_ptr(), ctypes.byref(out.struct()),
+        dgate.data_ptr(), aux_coef, z_coef, dlogits.data_ptr(), _raw_stream(stream, logits.get_device()))
+    _check(rc, "moe_route_scored_backward")
 
 
 def dispatch(cfg, x, out: RouteOutputs, x_perm, stream=None):
