@@ -71,21 +71,39 @@ __global__ void __launch_bounds__(256)
   out[c] = s;
 }
 
-// dst [rows][ldd] (16-byte rows) = src [rows][cols] of any alignment
-__global__ void __launch_bounds__(256)
-    linear_align_kernel(const __nv_bfloat16* __restrict__ src, int64_t ld, int64_t rows, int cols,
-                        __nv_bfloat16* __restrict__ dst, int64_t ldd) {
+// Copies of up to two operands to 16-byte rows: dst [rows][ldd] = src [rows][cols], src on any
+// element boundary. Eight elements a thread, read as the 4-byte words that hold them (five when
+// the row starts inside a word) and shifted into place.
+struct AlignJob {
+  const __nv_bfloat16* src;
+  int64_t ld, rows;
+  int cols;
+  __nv_bfloat16* dst;
+  int64_t ldd;
+};
+
+__global__ void __launch_bounds__(256) linear_align_kernel(AlignJob j0, AlignJob j1) {
   pdl_wait();
   pdl_trigger();
-  const int64_t per = ldd / 8, n = rows * per;
+  const AlignJob j = blockIdx.y ? j1 : j0;
+  const int per = int(j.ldd / 8);
+  const int64_t n = j.rows * per;
   for (int64_t x = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; x < n; x += int64_t(gridDim.x) * blockDim.x) {
     const int64_t r = x / per;
-    const int c = int(x % per) * 8;
-    const __nv_bfloat16* s = src + r * ld + c;
-    Vec<__nv_bfloat16, 8> v;
+    const int c = int(x - r * per) * 8, left = j.cols - c;  // >= 1
+    const uintptr_t at = reinterpret_cast<uintptr_t>(j.src + r * j.ld + c);
+    const int odd = int(at >> 1) & 1;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(at & ~uintptr_t(3));
+    uint32_t v[5];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v.v[q] = c + q < cols ? s[q] : __float2bfloat16_rn(0.f);
-    store_vec<__nv_bfloat16, 8>(dst + r * ldd + c, v);
+    for (int q = 0; q < 5; ++q) v[q] = 2 * q - odd < left && (q < 4 || odd) ? __ldg(w + q) : 0u;
+    uint32_t o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      o[q] = odd ? __funnelshift_r(v[q], v[q + 1], 16) : v[q];
+      if (2 * q + 1 >= left) o[q] &= 2 * q < left ? 0xffffu : 0u;  // past the row's end
+    }
+    *reinterpret_cast<uint4*>(j.dst + r * j.ldd + c) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -142,21 +160,29 @@ size_t ws_need(const moe_linear_t& p, bool backward, bool all) {
 
 bool in_place(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
 
-// The operand [rows, cols] as TMA can read it: in place, or copied to 16-byte rows.
+// The operand [rows, cols] as TMA can read it: in place, or in a copy with 16-byte rows that the
+// job describes (src null: none).
 int align_operand(const void* src, int64_t ld, int64_t rows, int cols, Carver& c, size_t ws_bytes,
-                  const void** out, int64_t* ldo, bool launch, cudaStream_t st) {
-  *out = src;
-  *ldo = ld;
+                  LinearOperand* o, AlignJob* job) {
+  o->p = src;
+  o->ld = ld;
+  *job = AlignJob{nullptr, 0, 0, 1, nullptr, 8};
   if (in_place(src, ld)) return MOE_OK;
-  *ldo = up8(cols);
-  void* dst = c.take(size_t(rows) * *ldo * 2);
-  *out = dst;
-  if (c.at > ws_bytes) return MOE_ERR_WORKSPACE;
-  if (!launch) return MOE_OK;
-  const int64_t n = rows * (*ldo / 8);
-  return launch_kernel(linear_align_kernel, dim3(unsigned(std::min<int64_t>((n + 255) / 256, 16 * num_sms()))),
-                       dim3(256), 0, st, static_cast<const __nv_bfloat16*>(src), ld, rows, cols,
-                       static_cast<__nv_bfloat16*>(dst), *ldo);
+  o->ld = up8(cols);
+  void* dst = c.take(size_t(rows) * o->ld * 2);
+  o->p = dst;
+  *job = AlignJob{static_cast<const __nv_bfloat16*>(src), ld, rows, cols, static_cast<__nv_bfloat16*>(dst), o->ld};
+  return c.at > ws_bytes ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+int launch_align(const AlignJob& a, const AlignJob& b, cudaStream_t st) {
+  const bool two = a.src && b.src;
+  if (!a.src && !b.src) return MOE_OK;
+  const AlignJob& one = a.src ? a : b;
+  const int64_t n = std::max(one.rows * (one.ldd / 8), two ? b.rows * (b.ldd / 8) : 0);
+  return launch_kernel(linear_align_kernel,
+                       dim3(unsigned(std::min<int64_t>((n + 255) / 256, 16 * num_sms())), two ? 2 : 1), dim3(256),
+                       0, st, one, b);
 }
 
 template <typename T>
@@ -215,12 +241,11 @@ int moe_linear_forward(const moe_linear_t* p, const void* x, const void* W, cons
                              1, q.T, q.N, q.K, e, part, stream);
   }
   LinearOperand a{nullptr, 0, false}, b{nullptr, 0, false};
-  for (int launch = 0; launch < 2; ++launch) {  // room first: nothing is launched without it
-    c.at = 256;
-    if ((rc = align_operand(x, q.ldx, q.T, q.K, c, ws_bytes, &a.p, &a.ld, launch, stream)) != MOE_OK ||
-        (rc = align_operand(W, q.ldw, q.N, q.K, c, ws_bytes, &b.p, &b.ld, launch, stream)) != MOE_OK)
-      return rc;
-  }
+  AlignJob ja, jb;
+  if ((rc = align_operand(x, q.ldx, q.T, q.K, c, ws_bytes, &a, &ja)) != MOE_OK ||
+      (rc = align_operand(W, q.ldw, q.N, q.K, c, ws_bytes, &b, &jb)) != MOE_OK ||
+      (rc = launch_align(ja, jb, stream)) != MOE_OK)
+    return rc;
   return launch_linear_bf16(a, b, q.T, q.N, q.K, e, static_cast<unsigned*>(ws), stream);
 }
 
@@ -273,16 +298,13 @@ int moe_linear_backward(const moe_linear_t* p, const void* dy, const void* x, co
   LinearOperand xo{nullptr, 0, true}, wo{nullptr, 0, true};
   void* d = nullptr;
   float* dbp = nullptr;
-  for (int launch = 0; launch < 2; ++launch) {
-    c.at = 256;
-    if (dW && (rc = align_operand(x, q.ldx, q.T, q.K, c, ws_bytes, &xo.p, &xo.ld, launch, stream)) != MOE_OK)
-      return rc;
-    if (dx && (rc = align_operand(W, q.ldw, q.N, q.K, c, ws_bytes, &wo.p, &wo.ld, launch, stream)) != MOE_OK)
-      return rc;
-    if (make_d) d = c.take(size_t(q.T) * Np * 2);
-    dbp = static_cast<float*>(c.take(size_t(bias_slices(q.T, q.N)) * q.N * 4));
-    if (c.at > ws_bytes) return MOE_ERR_WORKSPACE;
-  }
+  AlignJob jx{nullptr, 0, 0, 1, nullptr, 8}, jw = jx;
+  if (dW && (rc = align_operand(x, q.ldx, q.T, q.K, c, ws_bytes, &xo, &jx)) != MOE_OK) return rc;
+  if (dx && (rc = align_operand(W, q.ldw, q.N, q.K, c, ws_bytes, &wo, &jw)) != MOE_OK) return rc;
+  if (make_d) d = c.take(size_t(q.T) * Np * 2);
+  dbp = static_cast<float*>(c.take(size_t(bias_slices(q.T, q.N)) * q.N * 4));
+  if (c.at > ws_bytes) return MOE_ERR_WORKSPACE;
+  if ((rc = launch_align(jx, jw, stream)) != MOE_OK) return rc;
   if ((make_d || dbias) &&
       (rc = launch_dact<__nv_bfloat16>(q, dy, pre, d, Np, dbias ? dbp : nullptr, stream)) != MOE_OK)
     return rc;

@@ -81,35 +81,36 @@ __device__ __forceinline__ float act_slope(float v) {
 // with R a polynomial of degree 7 without constant term fitted to exp(x^2) erfc(x) by linear
 // programming on the relative error over 0 <= x <= 10 (1.0e-6; the tail keeps its relative
 // precision). erff's two branches and 1 + erf's cancellation cost about twice the instructions.
+// tail = Phi(-|v|), e = exp(-v^2 / 2)
 __device__ __forceinline__ void normal_parts(float v, float& tail, float& e) {
-  const float x = fabsf(v) * 0.70710678118654752f;
-  e = __expf(-x * x);
-  const float t = __fdividef(1.f, fmaf(0.38f, x, 1.f));
-  float r = -0.125161275f;
-  r = fmaf(r, t, 0.335073888f);
-  r = fmaf(r, t, -0.0684575289f);
-  r = fmaf(r, t, 0.24670291f);
-  r = fmaf(r, t, 0.181069434f);
-  r = fmaf(r, t, 0.216475591f);
-  r = fmaf(r, t, 0.214295983f);
-  tail = 0.5f * e * (r * t);
+  e = exp2_approx(v * v * -0.72134752044448170f);
+  const float t = rcp_approx(fmaf(0.26870057685f, fabsf(v), 1.f));
+  float r = -0.0625806375f;  // R's coefficients, halved
+  r = fmaf(r, t, 0.167536944f);
+  r = fmaf(r, t, -0.03422876445f);
+  r = fmaf(r, t, 0.123351455f);
+  r = fmaf(r, t, 0.0905347165f);
+  r = fmaf(r, t, 0.108237808f);
+  r = fmaf(r, t, 0.1071479915f);
+  tail = e * (r * t);
 }
 template <int ACT>
 __device__ __forceinline__ float act_fast(float v) {
+  constexpr float kL2e = 1.44269504088896341f;
   if constexpr (ACT == MOE_LIN_GELU) {
     float tail, e;
     normal_parts(v, tail, e);
     return v * (v < 0.f ? tail : 1.f - tail);
   }
-  if constexpr (ACT == MOE_LIN_GELU_TANH) {
-    const float u2 = v * fmaf(0.0713548162726f, v * v, 1.59576912160573f);
-    return __fdividef(v, 1.f + __expf(-u2));
+  if constexpr (ACT == MOE_LIN_GELU_TANH) {  // v / (1 + exp(-2u))
+    return v * rcp_approx(1.f + exp2_approx(v * fmaf(-0.0713548162726f * kL2e, v * v, -1.59576912160573f * kL2e)));
   }
-  if constexpr (ACT == MOE_LIN_SILU) return __fdividef(v, 1.f + __expf(-v));
+  if constexpr (ACT == MOE_LIN_SILU) return v * rcp_approx(1.f + exp2_approx(v * -kL2e));
   return act_value<ACT>(v);
 }
 template <int ACT>
 __device__ __forceinline__ float slope_fast(float v) {
+  constexpr float kL2e = 1.44269504088896341f;
   if constexpr (ACT == MOE_LIN_GELU) {
     float tail, e;
     normal_parts(v, tail, e);
@@ -117,13 +118,13 @@ __device__ __forceinline__ float slope_fast(float v) {
   }
   if constexpr (ACT == MOE_LIN_GELU_TANH) {
     if (fabsf(v) > 16.f) return v > 0.f ? 1.f : 0.f;
-    const float v2 = v * v;
-    const float e = __expf(fminf(-v * fmaf(0.0713548162726f, v2, 1.59576912160573f), 80.f));
-    const float s = __fdividef(1.f, 1.f + e);
+    const float v2 = v * v;  // the exponent capped at 2^115: the reciprocal stays normal
+    const float e = exp2_approx(fminf(v * fmaf(-0.0713548162726f * kL2e, v2, -1.59576912160573f * kL2e), 115.f));
+    const float s = rcp_approx(1.f + e);
     return fmaf(v * fmaf(0.214064448818f, v2, 1.59576912160573f), s * (e * s), s);
   }
   if constexpr (ACT == MOE_LIN_SILU) {
-    const float e = __expf(fminf(-v, 80.f)), s = __fdividef(1.f, 1.f + e);
+    const float e = exp2_approx(fminf(v * -kL2e, 115.f)), s = rcp_approx(1.f + e);
     return s * fmaf(v, e * s, 1.f);
   }
   return act_slope<ACT>(v);

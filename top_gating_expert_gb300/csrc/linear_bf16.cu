@@ -23,6 +23,7 @@
 // Every wait is bounded, as in the grouped GEMM: a role that gives up sets the status word
 // and the CTA's abort flag, the loads and MMAs in flight are drained, TMEM is freed.
 #include <algorithm>
+#include <type_traits>
 
 #include "linear.cuh"
 #include "sm100_ptx.cuh"
@@ -40,10 +41,16 @@ constexpr int kMaxStages = 8;
 struct TileArgs {
   int rows, cols, nkb, splits, stages;
   int a_mn, b_mn;
+  int vec;  // 8-byte accesses to bias, residual, pre and out rows
   LinearEpi e;
   unsigned* status;
 };
 
+__device__ __forceinline__ float ld_cluster_f(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
@@ -53,42 +60,83 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+// Epilogue: a warp takes whole rows of the tile, a lane 4 consecutive columns (VEC: 8-byte
+// accesses, when every row of every operand allows them) or every 32nd column. The residual's
+// loads of several rows are issued before the first is used.
+__device__ __forceinline__ float2 bf16x2_floats(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
 
-__device__ __forceinline__ void store4(void* base, int64_t at, const float (&v)[4], int n) {
+// Column of this lane's q-th value.
+template <bool VEC>
+__device__ __forceinline__ int lane_col(int lane, int q) {
+  return VEC ? (q >> 2) * 128 + lane * 4 + (q & 3) : lane + 32 * q;
+}
+
+// Stores the valid ones of a row's values, 4 at a time when VEC.
+template <int NC, bool VEC>
+__device__ __forceinline__ void store_row(void* base, int64_t at, const float (&v)[NC], int lane, int nc) {
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(base) + at;
-  if (n == 4 && aligned8(o)) {
-    *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  if constexpr (VEC) {
+#pragma unroll
+    for (int q = 0; q < NC; q += 4)
+      if (lane_col<true>(lane, q) < nc)  // 4 divides nc
+        *reinterpret_cast<uint2*>(o + lane_col<true>(lane, q)) =
+            make_uint2(pack_bf16x2(v[q], v[q + 1]), pack_bf16x2(v[q + 2], v[q + 3]));
   } else {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (q < n) o[q] = __float2bfloat16_rn(v[q]);
+    for (int q = 0; q < NC; ++q)
+      if (lane + 32 * q < nc) o[lane + 32 * q] = __float2bfloat16_rn(v[q]);
   }
 }
 
-// The epilogue of 4 consecutive columns c .. of output row r, the first n of them valid.
-__device__ __forceinline__ void emit4(const LinearEpi& e, int64_t r, int64_t c, float (&v)[4], int n) {
-  if (e.bias) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (q < n) v[q] += __ldg(e.bias + c + q);
-  }
-  if (e.pre) store4(e.pre, r * e.ldp + c, v, n);
-  act_fast_all(e.act, v);
+// The epilogue of output rows r, r + step, .. (those below r_end, at most ROWS of them), columns
+// c0 .. c0 + nc - 1; get(row, column of the tile) reads the summed accumulator.
+template <int NC, int ROWS, bool VEC, typename Get>
+__device__ __forceinline__ void emit_rows(const LinearEpi& e, int r, int step, int r_end, int64_t row0, int64_t c0,
+                                          int nc, int lane, const float (&bias)[NC], Get&& get) {
+  float v[ROWS][NC];
+  uint2 rv[ROWS][VEC ? NC / 4 : 1];
+  __nv_bfloat16 rs[ROWS][VEC ? 1 : NC];
   if (e.res) {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(e.res) + r * e.ldr + c;
-    if (n == 4 && aligned8(p)) {
-      const uint2 w = *reinterpret_cast<const uint2*>(p);
-      const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
-      const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
-      v[0] += a.x; v[1] += a.y; v[2] += b.x; v[3] += b.y;
-    } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q < n) v[q] += __bfloat162float(p[q]);
+    for (int k = 0; k < ROWS; ++k) {
+      if (r + k * step >= r_end) break;
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(e.res) + (row0 + r + k * step) * e.ldr + c0;
+      if constexpr (VEC) {
+#pragma unroll
+        for (int q = 0; q < NC; q += 4)
+          if (lane_col<true>(lane, q) < nc) rv[k][q / 4] = *reinterpret_cast<const uint2*>(p + lane_col<true>(lane, q));
+      } else {
+#pragma unroll
+        for (int q = 0; q < NC; ++q)
+          if (lane + 32 * q < nc) rs[k][q] = p[lane + 32 * q];
+      }
     }
   }
-  store4(e.out, r * e.ldo + c, v, n);
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    if (r + k * step >= r_end) break;
+    get(r + k * step, v[k]);
+#pragma unroll
+    for (int q = 0; q < NC; ++q) v[k][q] += bias[q];
+    const int64_t row = row0 + r + k * step;
+    if (e.pre) store_row<NC, VEC>(e.pre, row * e.ldp + c0, v[k], lane, nc);
+    act_fast_all(e.act, v[k]);
+    if (e.res) {
+#pragma unroll
+      for (int q = 0; q < NC; ++q) {
+        if (lane_col<VEC>(lane, q) >= nc) continue;
+        if constexpr (VEC) {
+          const float2 f = bf16x2_floats((q & 2) ? rv[k][q / 4].y : rv[k][q / 4].x);
+          v[k][q] += (q & 1) ? f.y : f.x;
+        } else {
+          v[k][q] += __bfloat162float(rs[k][q]);
+        }
+      }
+    }
+    store_row<NC, VEC>(e.out, row * e.ldo + c0, v[k], lane, nc);
+  }
 }
 
 template <int BN, bool TRANS>
@@ -102,7 +150,7 @@ struct TileCfg {
 };
 
 template <int BN, bool TRANS>
-__global__ void __launch_bounds__(kThreadsT)
+__global__ void __launch_bounds__(kThreadsT, 3)
     linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const TileArgs p) {
   using C = TileCfg<BN, TRANS>;
@@ -133,6 +181,18 @@ __global__ void __launch_bounds__(kThreadsT)
     tma_prefetch_map(&tmB);
   }
   if (warp == 1) tmem_alloc(smem_u32(&s_tmem), C::TMEM_COLS);
+  // this split's k-blocks
+  const int kb0 = int(int64_t(p.nkb) * split / p.splits);
+  const int kb1 = int(int64_t(p.nkb) * (split + 1) / p.splits);
+  if (TRANS && warp == 2 && lane == 0)  // few rows: the weights into L2 while the previous kernel ends
+    for (int kb = kb0; kb < min(kb1, kb0 + NS); ++kb) {
+      if (p.a_mn) {
+        tma_prefetch_2d(&tmA, i0, kb * BK);
+        if (i0 + 64 < p.rows) tma_prefetch_2d(&tmA, i0 + 64, kb * BK);
+      } else {
+        tma_prefetch_2d(&tmA, kb * BK, i0);
+      }
+    }
   pdl_wait();
   pdl_trigger();
   const uint64_t wlimit = wait_limit_ns(p.status);
@@ -140,9 +200,6 @@ __global__ void __launch_bounds__(kThreadsT)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  // this split's k-blocks
-  const int kb0 = int(int64_t(p.nkb) * split / p.splits);
-  const int kb1 = int(int64_t(p.nkb) * (split + 1) / p.splits);
   bool any = false;  // warp 0: loads issued; warp 1: MMAs issued
   int stage = 0;
   uint32_t phase = 0;
@@ -248,26 +305,48 @@ __global__ void __launch_bounds__(kThreadsT)
   if (p.splits > 1) cluster_sync_all();  // every split's tile is in its shared memory
 
   // epilogue: this CTA's share of the output rows of the tile
-  constexpr int OR = TRANS ? BN : BM, OC = TRANS ? BM : BN;
-  const int or0 = OR * split / p.splits, or1 = OR * (split + 1) / p.splits;
+  constexpr int OR = TRANS ? BN : BM, OC = 128, NC = OC / 32;
+  const int or0 = OR * split / p.splits;
   const int r0 = TRANS ? j0 : i0, c0 = TRANS ? i0 : j0;
-  const int nr = TRANS ? p.cols : p.rows, nc = TRANS ? p.rows : p.cols;
+  const int nr = TRANS ? p.cols : p.rows, nc = min(OC, (TRANS ? p.rows : p.cols) - c0);
+  const int or1 = min(OR * (split + 1) / p.splits, nr - r0);
   const uint32_t base = smem_u32(smem);
-  for (int x = threadIdx.x; x < (or1 - or0) * (OC / 4); x += kThreadsT) {
-    const int r = or0 + x / (OC / 4), c = (x % (OC / 4)) * 4;
-    if (r0 + r >= nr || c0 + c >= nc) continue;
-    const uint32_t off = base + uint32_t(r * C::PITCH + c) * 4;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (p.splits > 1) {
-      for (int s = 0; s < p.splits; ++s) {
-        const float4 f = ld_cluster_f4(cluster_addr(off, uint32_t(s)));
-        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+  auto run = [&](auto vec) {
+    constexpr bool VEC = decltype(vec)::value;
+    float bias[NC];
+#pragma unroll
+    for (int q = 0; q < NC; ++q)
+      bias[q] = p.e.bias && lane_col<VEC>(lane, q) < nc ? __ldg(p.e.bias + c0 + lane_col<VEC>(lane, q)) : 0.f;
+    auto get = [&](int r, float (&v)[NC]) {
+#pragma unroll
+      for (int q = 0; q < NC; q += VEC ? 4 : 1) {
+        const uint32_t off = uint32_t(r * C::PITCH + lane_col<VEC>(lane, q)) * 4;
+        if (p.splits > 1) {
+#pragma unroll
+          for (int x = 0; x < (VEC ? 4 : 1); ++x) v[q + x] = 0.f;
+          for (int s = 0; s < p.splits; ++s) {
+            const uint32_t at = cluster_addr(base + off, uint32_t(s));
+            if constexpr (VEC) {
+              const float4 f = ld_cluster_f4(at);
+              v[q] += f.x; v[q + 1] += f.y; v[q + 2] += f.z; v[q + 3] += f.w;
+            } else {
+              v[q] += ld_cluster_f(at);
+            }
+          }
+        } else if constexpr (VEC) {
+          const float4 f = *reinterpret_cast<const float4*>(smem + off);
+          v[q] = f.x; v[q + 1] = f.y; v[q + 2] = f.z; v[q + 3] = f.w;
+        } else {
+          v[q] = *reinterpret_cast<const float*>(smem + off);
+        }
       }
-    } else {
-      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(smem + (off - base));
-    }
-    emit4(p.e, r0 + r, c0 + c, v, min(4, nc - (c0 + c)));
-  }
+    };
+    constexpr int ROWS = 4, W = kThreadsT / 32;
+    for (int r = or0 + warp; r < or1; r += ROWS * W)
+      emit_rows<NC, ROWS, VEC>(p.e, r, W, or1, r0, c0, nc, lane, bias, get);
+  };
+  if (p.vec) run(std::true_type{});
+  else run(std::false_type{});
   __syncwarp();
   if (p.splits > 1) cluster_sync_all();  // no CTA leaves while another reads its tile
 }
@@ -293,12 +372,22 @@ int run_tile(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
   p.a_mn = A.mn; p.b_mn = B.mn;
   p.e = e;
   p.status = status;
-  p.stages = std::min(kMaxStages, (232448 - 2048) / C::STAGE);
+  // CTAs an SM: as many as the grid brings, while each still has three stages and room for the
+  // staged tile (the stages in flight of all of them are what hides the memory's latency)
+  const int64_t ctas = int64_t((rows + BM - 1) / BM) * ((cols + BN - 1) / BN) * splits;
+  int per_sm = int(std::min<int64_t>(3, (ctas + num_sms() - 1) / num_sms()));
+  auto stages_at = [](int n) { return std::min(kMaxStages, (233472 / n - 1024 - 1024 - 512) / C::STAGE); };
+  while (per_sm > 1 && (stages_at(per_sm) < 3 || stages_at(per_sm) * C::STAGE < C::DUMP)) --per_sm;
+  p.stages = stages_at(per_sm);
   const int smem = 1024 + p.stages * C::STAGE;
   if (p.stages * C::STAGE < C::DUMP) return MOE_ERR_UNSUPPORTED;
+  const int64_t oc = TRANS ? rows : cols;
+  auto vec8 = [](const void* q, int64_t ld) { return !q || (reinterpret_cast<uintptr_t>(q) % 8 == 0 && ld % 4 == 0); };
+  p.vec = oc % 4 == 0 && vec8(e.out, e.ldo) && vec8(e.pre, e.ldp) && vec8(e.res, e.ldr);
   auto kern = linear_tile_kernel<BN, TRANS>;
   static std::atomic<unsigned long long> seen{0};
-  if ((rc = allow_smem(reinterpret_cast<const void*>(kern), smem, seen)) != MOE_OK) return rc;
+  if ((rc = allow_smem(reinterpret_cast<const void*>(kern), 1024 + stages_at(1) * C::STAGE, seen)) != MOE_OK)
+    return rc;
   cudaLaunchConfig_t lc = {};
   const int64_t tj = (int64_t(cols) + BN - 1) / BN;
   if (tj > 65535) return MOE_ERR_UNSUPPORTED;
@@ -665,13 +754,21 @@ int run_pair(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
   return MOE_OK;
 }
 
-// K splits for `tiles` tiles: the power of two (at most 8, the portable cluster) that brings
-// the CTAs closest to one wave, with at least four k-blocks each.
+// K splits for `tiles` tiles over nkb k-blocks: the power of two (at most 8, the portable
+// cluster) with the fewest k-blocks on the busiest SM, a split's join counted as three of them.
+// One token through 14336 x 4096: 4 splits, 48 k-blocks an SM instead of 64.
 int pick_splits(int64_t tiles, int K) {
-  const int nkb = (K + BK - 1) / BK;
-  int s = 1;
-  while (s < 8 && tiles * s * 2 <= num_sms() && nkb >= s * 8) s *= 2;
-  return s;
+  const int nkb = (K + BK - 1) / BK, sms = num_sms();
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int s = 1; s <= 8 && nkb >= 2 * s; s *= 2) {
+    const int64_t cost = (tiles * s + sms - 1) / sms * ((nkb + s - 1) / s) + (s > 1 ? 3 : 0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
 }  // namespace

@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "elem.cuh"
 #include "route_kernels.cuh"
 
 namespace moe {
@@ -207,16 +208,6 @@ __device__ __noinline__ int token_general(const float (&l)[Q], const RouteArgs& 
   return choose_fp64<Q>(l, a, sc, row);
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 // Group scores from keys (bits of non-negative floats, low 3 bits the slot number), lane g
 // getting group g's; groups of 32 m experts, i.e. slots m g .. m g + m - 1 of every lane. Equal
@@ -770,120 +761,138 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
 //             else:    dl_j  = scale p_j d_j, dl_e -= scale p_e sum_i d_i p_i
 //             aux:     dl_e += ca p_e (f_e - sum f p)
 //   z         dl_e += 2 cz / S lse p_e
-// with ca = aux_coef E / (G S_g). 1 - s is evaluated as sigmoid(-l), so it keeps its precision
-// where s is close to 1.
-__global__ void __launch_bounds__(256)
+// with ca = aux_coef E / (G S_g). 1 - s = 1 / (1 + exp(l)), so it keeps its precision where s is
+// close to 1. One exponential an expert serves all of it: x = exp(l) where the logits lie within
+// +-80 (their sum then neither overflows nor vanishes), s = x / (1 + x); else exp(l - max) for the
+// softmax and shifted sigmoids apart. Bound by the instructions; by memory (8 S E bytes) it
+// would take a fifth of the time.
+constexpr int kBwdWarps = 8, kBwdTokens = 4;  // warps a CTA, consecutive tokens a warp
+
+template <int Q, bool SIG>
+__global__ void __launch_bounds__(32 * kBwdWarps)
     route_scored_bwd_kernel(const float* __restrict__ logits, const int32_t* __restrict__ expert_id,
                             const int32_t* __restrict__ row, const int32_t* __restrict__ counts_routed,
                             const float* __restrict__ dgate, const float* __restrict__ gpart,
                             int n_tiles, int S, int G, int E, int k, ScoreArgs sc, float aux_coef,
                             float z_coef, float* __restrict__ dlogits,
                             __nv_bfloat16* __restrict__ dlb, int Ep) {
+  __shared__ float s_dl[kBwdWarps][32 * Q];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (t >= S) return;
-  const float* lr = logits + t * E;
-  float l[8], p[8], dl[8];
-  float m = -INFINITY;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t first = (int64_t(blockIdx.x) * kBwdWarps + warp) * kBwdTokens;
+  const int Sg = S / G;
+  const float ca = aux_coef * float(E) / (float(G) * float(Sg)) / (float(Sg) * float(k));
+  const float cz = z_coef * 2.f / float(S);
+  float* sd = s_dl[warp];
+  float f[Q];  // ca times the routed counts of the token's group
+  int group = -1;
+  for (int64_t t = first; t < first + kBwdTokens && t < S; ++t) {
+    const float* lr = logits + t * E;
+    float l[Q], p[Q], q[Q], om[Q];  // p: softmax; q: normalised scores; om: 1 - s
+    bool plain = true;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int e = lane + 32 * q;
-    l[q] = e < E ? __ldg(lr + e) : -INFINITY;
-    if (!isfinite(l[q])) l[q] = -INFINITY;
-    m = fmaxf(m, l[q]);
-    dl[q] = 0.f;
-  }
-  m = warp_max(m);
-  const bool any = m > -INFINITY;
-  if (!any) m = 0.f;
-  float s = 0.f;
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    p[q] = expf(l[q] - m);
-    s += p[q];
-  }
-  s = warp_sum(s);
-  const float inv = s > 0.f ? 1.f / s : 0.f, lse = any ? m + logf(s) : 0.f;
-#pragma unroll
-  for (int q = 0; q < 8; ++q) p[q] *= inv;
-
-  // the choices, lane j < k: expert, logit, gradient of its weight
-  int id = -1;
-  float lsel = -INFINITY, dg = 0.f;
-  if (lane < k) {
-    id = expert_id[t * k + lane];
-    if (id < 0 || id >= E) id = -1;
-    if (id >= 0) lsel = __ldg(lr + id);
-    if (!isfinite(lsel)) lsel = -INFINITY;
-    const int r = row[t * k + lane];
-    if (r >= 0) {
-      if (dgate) dg = dgate[t * k + lane];
-      else
-        for (int nt = 0; nt < n_tiles; ++nt) dg += gpart[int64_t(r) * n_tiles + nt];
+    for (int i = 0; i < Q; ++i) {
+      const int e = lane + 32 * i;
+      l[i] = e < E ? __ldg(lr + e) : 0.f;
+      plain = plain && fabsf(l[i]) <= 80.f;  // false for NaN too
     }
-  }
-  ScoreArgs unit = sc;
-  unit.scale = 1.f;
-  const float w = choice_weight(lsel, lane < k, unit, m, inv);
-  const float inner = (sc.renorm || !sc.sigmoid) ? warp_sum(w * dg) : 0.f;
-  float dsel = sc.scale * w * ((sc.renorm ? dg - inner : dg) *
-                               (sc.sigmoid ? sigmoid_shifted(-lsel, 0.f) : 1.f));
-  if (!(lsel > -INFINITY)) dsel = 0.f;
-  for (int j = 0; j < k; ++j) {
-    const int idj = __shfl_sync(kFull, id, j);
-    const float dj = __shfl_sync(kFull, dsel, j);
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (idj == lane + 32 * q) dl[q] += dj;
-  }
-  if (!sc.sigmoid && !sc.renorm) {
-    const float ci = sc.scale * inner;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) dl[q] -= p[q] * ci;
-  }
-  if (aux_coef != 0.f) {
-    const int Sg = S / G;
-    const int32_t* cr = counts_routed + (t / Sg) * E;
-    const float fs = 1.f / (float(Sg) * float(k));
-    const float ca = aux_coef * float(E) / (float(G) * float(Sg));
-    float f[8], x[8], fq = 0.f, ti = 1.f;
-    if (sc.sigmoid) {
-      const float top = fminf(m, 0.f);
-      float tot = 0.f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        x[q] = sigmoid_shifted(l[q], top);
-        tot += x[q];
+    // the choices, lane j < k: expert, logit, gradient of its weight
+    int id = -1;
+    float lsel = -INFINITY, dg = 0.f;
+    if (lane < k) {
+      id = expert_id[t * k + lane];
+      if (id < 0 || id >= E) id = -1;
+      if (id >= 0) lsel = __ldg(lr + id);
+      if (!isfinite(lsel)) lsel = -INFINITY;
+      const int r = row[t * k + lane];
+      if (r >= 0) {
+        if (dgate) dg = dgate[t * k + lane];
+        else
+          for (int nt = 0; nt < n_tiles; ++nt) dg += gpart[int64_t(r) * n_tiles + nt];
       }
-      tot = warp_sum(tot);
-      ti = tot > 0.f ? 1.f / tot : 0.f;
+    }
+    if (aux_coef != 0.f && int(t / Sg) != group) {
+      group = int(t / Sg);
+#pragma unroll
+      for (int i = 0; i < Q; ++i)
+        f[i] = lane + 32 * i < E ? ca * float(counts_routed[int64_t(group) * E + lane + 32 * i]) : 0.f;
+    }
+    float s = 0.f, tot = 0.f, m = 0.f, lse;
+    if (__all_sync(kFull, plain)) {
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        const float x = lane + 32 * i < E ? expf(l[i]) : 0.f;
+        p[i] = x;
+        s += x;
+        if constexpr (SIG) {
+          om[i] = rcp_approx(1.f + x);
+          q[i] = x * om[i];
+          tot += q[i];
+        }
+      }
+      s = warp_sum(s);
+      lse = logf(s);
+    } else {
+      m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        if (lane + 32 * i >= E || !isfinite(l[i])) l[i] = -INFINITY;
+        m = fmaxf(m, l[i]);
+      }
+      m = warp_max(m);
+      const bool any = m > -INFINITY;
+      if (!any) m = 0.f;
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        p[i] = expf(l[i] - m);
+        s += p[i];
+        if constexpr (SIG) {
+          om[i] = l[i] > -INFINITY ? sigmoid_shifted(-l[i], 0.f) : 1.f;
+          q[i] = sigmoid_shifted(l[i], fminf(m, 0.f));
+          tot += q[i];
+        }
+      }
+      s = warp_sum(s);
+      lse = any ? m + logf(s) : 0.f;
+    }
+    const float inv = s > 0.f ? 1.f / s : 0.f;
+    if constexpr (SIG) tot = warp_sum(tot);
+    const float ti = SIG ? (tot > 0.f ? 1.f / tot : 0.f) : inv;
+    ScoreArgs unit = sc;
+    unit.scale = 1.f;
+    const float w = choice_weight(lsel, lane < k, unit, m, inv);
+    const float inner = (sc.renorm || !SIG) ? warp_sum(w * dg) : 0.f;
+    float dsel = sc.scale * w * ((sc.renorm ? dg - inner : dg) * (SIG ? sigmoid_shifted(-lsel, 0.f) : 1.f));
+    if (!(lsel > -INFINITY)) dsel = 0.f;
+    // the dense part: the losses' gradients (and the un-normalised softmax weights' common one)
+    const float cp = cz * lse * inv - (!SIG && !sc.renorm ? sc.scale * inner * inv : 0.f);
+    float fq = 0.f;
+    if (aux_coef != 0.f) {
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        q[i] = (SIG ? q[i] : p[i]) * ti;
+        fq = fmaf(f[i], q[i], fq);
+      }
+      fq = warp_sum(fq);
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int e = lane + 32 * q;
-      x[q] = sc.sigmoid ? x[q] * ti : p[q];
-      f[q] = e < E ? float(cr[e]) * fs : 0.f;
-      fq += f[q] * x[q];
+    for (int i = 0; i < Q; ++i) {
+      float d = p[i] * cp;
+      if (aux_coef != 0.f) d = fmaf(SIG ? q[i] * om[i] : q[i], f[i] - fq, d);
+      sd[lane + 32 * i] = d;
     }
-    fq = warp_sum(fq);
+    __syncwarp();
+    if (id >= 0) sd[id] += dsel;  // the choices are distinct experts
+    __syncwarp();
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const float one_s = sc.sigmoid && l[q] > -INFINITY ? sigmoid_shifted(-l[q], 0.f) : 1.f;
-      dl[q] += ca * x[q] * one_s * (f[q] - fq);
+    for (int i = 0; i < Q; ++i) {
+      const int e = lane + 32 * i;
+      const float d = sd[e];
+      if (e < E) dlogits[t * E + e] = d;
+      if (dlb && e < Ep) dlb[t * Ep + e] = __float2bfloat16_rn(e < E ? d : 0.f);
     }
-  }
-  if (z_coef != 0.f) {
-    const float cz = z_coef * 2.f / float(S) * lse;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) dl[q] += cz * p[q];
-  }
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const int e = lane + 32 * q;
-    if (e < E) dlogits[t * E + e] = dl[q];
-    if (dlb && e < Ep) dlb[t * Ep + e] = __float2bfloat16_rn(e < E ? dl[q] : 0.f);
+    __syncwarp();
   }
 }
 
@@ -922,12 +931,24 @@ int launch_route_scored_backward(const moe_config_t& c, const moe_score_t& sc, c
                                  const moe_route_out_t& r, const float* dgate, const float* gpart,
                                  int n_tiles, float aux_coef, float z_coef, float* dlogits, void* dlb,
                                  int Ep, cudaStream_t st) {
-  const unsigned blocks = unsigned((int64_t(c.S) * 32 + 255) / 256);
-  return launch_kernel(route_scored_bwd_kernel, dim3(blocks), dim3(256), 0, st, logits,
-                       static_cast<const int32_t*>(r.expert_id), static_cast<const int32_t*>(r.row),
-                       static_cast<const int32_t*>(r.counts_routed), dgate, gpart, n_tiles, c.S, c.G,
-                       c.E, c.k, score_args(sc, nullptr), aux_coef, z_coef, dlogits,
-                       static_cast<__nv_bfloat16*>(dlb), Ep);
+  const int64_t per = kBwdWarps * kBwdTokens;
+  auto launch = [&](auto kern) -> int {
+    return launch_kernel(kern, dim3(unsigned((c.S + per - 1) / per)), dim3(32 * kBwdWarps), 0, st, logits,
+                         static_cast<const int32_t*>(r.expert_id), static_cast<const int32_t*>(r.row),
+                         static_cast<const int32_t*>(r.counts_routed), dgate, gpart, n_tiles, c.S, c.G, c.E, c.k,
+                         score_args(sc, nullptr), aux_coef, z_coef, dlogits, static_cast<__nv_bfloat16*>(dlb), Ep);
+  };
+  auto go = [&](auto q) -> int {
+    constexpr int Q = decltype(q)::value;
+    return sc.score == MOE_SCORE_SIGMOID ? launch(route_scored_bwd_kernel<Q, true>)
+                                         : launch(route_scored_bwd_kernel<Q, false>);
+  };
+  // (dlb's columns go up to E rounded up to 64)
+  const int cols = dlb ? Ep : c.E;
+  return cols <= 32    ? go(std::integral_constant<int, 1>{})
+         : cols <= 64  ? go(std::integral_constant<int, 2>{})
+         : cols <= 128 ? go(std::integral_constant<int, 4>{})
+                       : go(std::integral_constant<int, 8>{});
 }
 
 }  // namespace moe
