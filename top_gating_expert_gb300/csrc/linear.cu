@@ -234,6 +234,8 @@ int moe_linear_forward(const moe_linear_t* p, const void* x, const void* W, cons
   e.bias = bias; e.res = residual; e.out = y; e.pre = pre;
   e.ldo = q.ldy; e.ldr = q.ldr; e.ldp = q.ldp;
   e.act = q.act;
+  if (q.T <= (q.dtype == MOE_BF16 ? 1 : 8))  // few tokens: W streamed row by row, nothing copied
+    return launch_linear_few(q.dtype == MOE_BF16, x, q.ldx, W, q.ldw, q.T, q.N, q.K, e, stream);
   Carver c{static_cast<char*>(ws)};
   if (q.dtype == MOE_F32) {
     float* part = static_cast<float*>(c.take(kPartBytes));

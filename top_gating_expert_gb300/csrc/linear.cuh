@@ -42,6 +42,10 @@ struct LinearOperand {
 int launch_linear_bf16(const LinearOperand& A, const LinearOperand& B, int rows, int cols, int K,
                        const LinearEpi& e, unsigned* status, cudaStream_t st);
 
+// The forward for one bf16 or up to eight fp32 tokens, operands on any boundary.
+int launch_linear_few(int bf16, const void* x, int64_t ldx, const void* W, int64_t ldw, int T, int N, int K,
+                      const LinearEpi& e, cudaStream_t st);
+
 #ifdef __CUDACC__
 template <int ACT>
 __device__ __forceinline__ float act_value(float v) {
@@ -128,6 +132,15 @@ __device__ __forceinline__ float slope_fast(float v) {
     return s * fmaf(v, e * s, 1.f);
   }
   return act_slope<ACT>(v);
+}
+__device__ __forceinline__ float act_any(int act, float v) {
+  switch (act) {
+    case MOE_LIN_RELU: return act_value<MOE_LIN_RELU>(v);
+    case MOE_LIN_GELU: return act_value<MOE_LIN_GELU>(v);
+    case MOE_LIN_GELU_TANH: return act_value<MOE_LIN_GELU_TANH>(v);
+    case MOE_LIN_SILU: return act_value<MOE_LIN_SILU>(v);
+  }
+  return v;
 }
 // n values at once, the activation chosen outside the loop
 template <int N>

@@ -35,7 +35,6 @@ using namespace sm100;
 
 constexpr int BM = 128;
 constexpr int BK = 64;  // bf16 elements of a 128-byte swizzled row
-constexpr int kThreadsT = 192;
 constexpr int kMaxStages = 8;
 
 struct TileArgs {
@@ -147,10 +146,12 @@ struct TileCfg {
   static constexpr int PITCH = (TRANS ? BM : BN) + 4;  // floats of a staged output row
   static constexpr int DUMP = (TRANS ? BN : BM) * PITCH * 4;
   static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
+  // six more warps for the epilogue of 128 rows (a tile's epilogue is bound by latency)
+  static constexpr int THREADS = TRANS ? 192 : 384;
 };
 
 template <int BN, bool TRANS>
-__global__ void __launch_bounds__(kThreadsT, 3)
+__global__ void __launch_bounds__(TileCfg<BN, TRANS>::THREADS, TRANS ? 3 : 1)
     linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const TileArgs p) {
   using C = TileCfg<BN, TRANS>;
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kThreadsT, 3)
     }
     if (lane == 0 && any) mma_commit(done_bar);  // on a failure too: what was issued finishes
     __syncwarp();
-  } else {
+  } else if (warp < 6) {
     const bool ok = __all_sync(0xffffffffu, wait_bounded(done_bar, 0u, &s_abort, p.status, wlimit));
     tc_fence_after();
     if (ok) {
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(kThreadsT, 3)
         }
       }
     };
-    constexpr int ROWS = 4, W = kThreadsT / 32;
+    constexpr int ROWS = 4, W = C::THREADS / 32;
     for (int r = or0 + warp; r < or1; r += ROWS * W)
       emit_rows<NC, ROWS, VEC>(p.e, r, W, or1, r0, c0, nc, lane, bias, get);
   };
@@ -392,7 +393,7 @@ int run_tile(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
   const int64_t tj = (int64_t(cols) + BN - 1) / BN;
   if (tj > 65535) return MOE_ERR_UNSUPPORTED;
   lc.gridDim = dim3(unsigned((rows + BM - 1) / BM), unsigned(tj), unsigned(splits));
-  lc.blockDim = dim3(kThreadsT);
+  lc.blockDim = dim3(C::THREADS);
   lc.dynamicSmemBytes = smem;
   lc.stream = st;
   cudaLaunchAttribute attr[2];
@@ -754,21 +755,15 @@ int run_pair(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
   return MOE_OK;
 }
 
-// K splits for `tiles` tiles over nkb k-blocks: the power of two (at most 8, the portable
-// cluster) with the fewest k-blocks on the busiest SM, a split's join counted as three of them.
-// One token through 14336 x 4096: 4 splits, 48 k-blocks an SM instead of 64.
+// K splits for `tiles` tiles: the largest power of two (at most 8, the portable cluster) whose
+// CTAs all run at once, one an SM, with four k-blocks each at least. Clusters of 8 find room on 16 of
+// the 18 to 20 SMs of a GPC; a second wave of clusters costs more than it saves (777 x 1408 x 1024:
+// 84 tiles in 8 splits 24 us, unsplit 14 us).
 int pick_splits(int64_t tiles, int K) {
-  const int nkb = (K + BK - 1) / BK, sms = num_sms();
-  int best = 1;
-  int64_t best_cost = INT64_MAX;
-  for (int s = 1; s <= 8 && nkb >= 2 * s; s *= 2) {
-    const int64_t cost = (tiles * s + sms - 1) / sms * ((nkb + s - 1) / s) + (s > 1 ? 3 : 0);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = s;
-    }
-  }
-  return best;
+  const int nkb = (K + BK - 1) / BK, room = num_sms() * 7 / 8;
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= room && nkb >= 8 * s) s *= 2;
+  return s;
 }
 
 }  // namespace
