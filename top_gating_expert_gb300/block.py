@@ -168,12 +168,12 @@ def layer_norm_backward(dy, h, gamma, mean, rstd, dh=None, *, need_beta=True, dx
     _vector(rstd, "rstd", w, T, dev)
     if dx is None:
         dx = _new(shape, dt, dev, stream)
-    if dgamma is None:
-        dgamma = _new((M,), _F32, dev, stream)
-    if need_beta and dbeta is None:
-        dbeta = _new((M,), _F32, dev, stream)
-    if ws is None:
-        with _on(stream):
+    with _on(stream):
+        if dgamma is None:
+            dgamma = torch.empty_like(gamma)
+        if need_beta and dbeta is None:
+            dbeta = torch.empty_like(gamma)
+        if ws is None:
             ws = layer_norm_workspace(T, M, dt, dy.device)
     ldh = _matrix(dx, "dx", w, shape, dt, dev)
     _vector(dgamma, "dgamma", w, M, dev)

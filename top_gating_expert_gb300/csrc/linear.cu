@@ -58,17 +58,26 @@ __global__ void __launch_bounds__(kColThreads * kRowLanes)
   }
 }
 
-// out[c] = sum over the slices, in order, of part[s][c]
+// out[c] = sum over the slices of part[s][c]: a CTA takes 32 columns, each of its eight warps every
+// eighth slice, then the warps' sums in order.
 __global__ void __launch_bounds__(256)
     linear_dbias_kernel(const float* __restrict__ part, int slices, int N, float* __restrict__ out) {
+  __shared__ float s_part[8][32];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= N) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
+  if (c < N) {
 #pragma unroll 8
-  for (int i = 0; i < slices; ++i) s += part[int64_t(i) * N + c];
-  out[c] = s;
+    for (int i = warp; i < slices; i += 8) s += part[int64_t(i) * N + c];
+  }
+  s_part[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < N) {
+    for (int w = 1; w < 8; ++w) s += s_part[w][lane];
+    out[c] = s;
+  }
 }
 
 // Copies of up to two operands to 16-byte rows: dst [rows][ldd] = src [rows][cols], src on any
@@ -113,7 +122,7 @@ int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
 int bias_slices(int T, int N) {
   const int cblocks = (N + 255) / 256;
   const int s = std::max(1, std::min(256, 1216 / cblocks));
-  return std::max(1, std::min(s, (T + kRowLanes - 1) / kRowLanes));
+  return std::max(1, std::min(s, (T + 4 * kRowLanes - 1) / (4 * kRowLanes)));  // four rows a lane
 }
 
 int check_linear(const moe_linear_t* p, moe_linear_t* q) {
@@ -185,23 +194,29 @@ int launch_align(const AlignJob& a, const AlignJob& b, cudaStream_t st) {
                        0, st, one, b);
 }
 
+// d (when it is given) and dbias (when it is given; part: its slices' partial sums)
 template <typename T>
 int launch_dact(const moe_linear_t& p, const void* dy, const void* pre, void* d, int64_t ldd, float* part,
-                cudaStream_t st) {
+                float* dbias, cudaStream_t st) {
+  if (!d && !dbias) return MOE_OK;
   constexpr int V = 16 / int(sizeof(T));
   auto ok = [](const void* q, int64_t ld) {
     return !q || (reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % V == 0);
   };
   const bool vec = p.N % V == 0 && ok(dy, p.ldy) && ok(pre, p.ldp) && ok(d, ldd);
   const int slices = bias_slices(p.T, p.N), slice = (p.T + slices - 1) / slices;
-  return with_act(p.act, [&](auto tag) {
+  float* sums = dbias ? (slices == 1 ? dbias : part) : nullptr;  // one slice: the sum itself
+  const int rc = with_act(p.act, [&](auto tag) {
     constexpr int ACT = decltype(tag)::value;
     const int cols = kColThreads * (vec ? V : 1);
     auto kern = vec ? linear_dact_kernel<T, V, ACT> : linear_dact_kernel<T, 1, ACT>;
     return launch_kernel(kern, dim3(unsigned((p.N + cols - 1) / cols), unsigned(slices)),
                          dim3(kColThreads * kRowLanes), 0, st, static_cast<const T*>(dy), p.ldy,
-                         static_cast<const T*>(pre), p.ldp, static_cast<T*>(d), ldd, p.T, p.N, slice, part);
+                         static_cast<const T*>(pre), p.ldp, static_cast<T*>(d), ldd, p.T, p.N, slice, sums);
   });
+  if (rc != MOE_OK || !dbias || slices == 1) return rc;
+  return launch_kernel(linear_dbias_kernel, dim3(unsigned((p.N + 31) / 32)), dim3(256), 0, st,
+                       static_cast<const float*>(part), slices, p.N, dbias);
 }
 
 }  // namespace
@@ -273,13 +288,7 @@ int moe_linear_backward(const moe_linear_t* p, const void* dy, const void* x, co
     float* part = static_cast<float*>(c.take(kPartBytes));
     void* d = pre ? c.take(size_t(q.T) * Np * 4) : nullptr;
     float* dbp = static_cast<float*>(c.take(size_t(bias_slices(q.T, q.N)) * q.N * 4));
-    if ((pre || dbias) &&
-        (rc = launch_dact<float>(q, dy, pre, d, Np, dbias ? dbp : nullptr, stream)) != MOE_OK)
-      return rc;
-    if (dbias && (rc = launch_kernel(linear_dbias_kernel, dim3(unsigned((q.N + 255) / 256)), dim3(256), 0,
-                                     stream, static_cast<const float*>(dbp), bias_slices(q.T, q.N), q.N,
-                                     dbias)) != MOE_OK)
-      return rc;
+    if ((rc = launch_dact<float>(q, dy, pre, d, Np, dbp, dbias, stream)) != MOE_OK) return rc;
     const float* df = static_cast<const float*>(pre ? d : dy);
     const int64_t ldd = pre ? Np : q.ldy;
     LinearEpi e;
@@ -307,13 +316,7 @@ int moe_linear_backward(const moe_linear_t* p, const void* dy, const void* x, co
   dbp = static_cast<float*>(c.take(size_t(bias_slices(q.T, q.N)) * q.N * 4));
   if (c.at > ws_bytes) return MOE_ERR_WORKSPACE;
   if ((rc = launch_align(jx, jw, stream)) != MOE_OK) return rc;
-  if ((make_d || dbias) &&
-      (rc = launch_dact<__nv_bfloat16>(q, dy, pre, d, Np, dbias ? dbp : nullptr, stream)) != MOE_OK)
-    return rc;
-  if (dbias && (rc = launch_kernel(linear_dbias_kernel, dim3(unsigned((q.N + 255) / 256)), dim3(256), 0,
-                                   stream, static_cast<const float*>(dbp), bias_slices(q.T, q.N), q.N,
-                                   dbias)) != MOE_OK)
-    return rc;
+  if ((rc = launch_dact<__nv_bfloat16>(q, dy, pre, d, Np, dbp, dbias, stream)) != MOE_OK) return rc;
   LinearOperand dk{make_d ? d : dy, make_d ? Np : q.ldy, false};
   unsigned* status = static_cast<unsigned*>(ws);
   LinearEpi e;

@@ -743,9 +743,9 @@ int norm_backward_v(const moe_norm_t& n, const T* dy, const T* h, const float* g
   const bool sums = dgamma || dbeta;
   if constexpr (VEC * sizeof(T) >= 4) {
     // more vectors a lane before more warps a row, up to 16 columns a lane (32 column sums and
-    // 16 of gamma: no spills); twice that for the longest bf16 rows and for single elements (for
-    // fp32 vectors shared memory does not hold it). Three stages, two where they would not fit
-    constexpr int kMore = VEC == 8 ? 2 : 4, kRing = VEC == 4 ? 4 : 2 * kMore;
+    // 16 of gamma: no spills); twice that for the longest bf16 rows (for fp32 vectors shared memory
+    // does not hold it). Three stages, two where they would not fit
+    constexpr int kMore = VEC == 8 ? 2 : (VEC == 4 ? 4 : 8), kRing = VEC == 8 ? 4 : kMore;
     int nv = 1;
     int G = row_warps(n.cols, VEC, nv, 1);
     while (G == 0 && nv < kRing) G = row_warps(n.cols, VEC, nv *= 2, nv >= kMore ? 16 : 1);

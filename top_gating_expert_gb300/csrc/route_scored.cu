@@ -153,25 +153,6 @@ __device__ __noinline__ int choose_fp64(const float (&l)[Q], const RouteArgs& a,
   return mine;
 }
 
-// The weight of this lane's choice (lanes j < k; lsel its logit, -inf when it is out), from
-// the scores of the k choices; m, inv: the token's largest logit and 1 / sum exp(l - m)
-// (softmax).
-__device__ __forceinline__ float choice_weight(float lsel, bool on, const ScoreArgs& sc, float m,
-                                               float inv) {
-  if (!on) lsel = -INFINITY;
-  float w;
-  if (sc.renorm) {
-    float top = warp_max(sc.sigmoid ? fminf(lsel, 0.f) : lsel);
-    if (!(top > -INFINITY)) top = 0.f;
-    w = sc.sigmoid ? sigmoid_shifted(lsel, top) : (lsel > -INFINITY ? expf(lsel - top) : 0.f);
-    const float tot = warp_sum(w);
-    w = tot > 0.f ? w / tot : 0.f;
-  } else {
-    w = sc.sigmoid ? sigmoid_shifted(lsel, 0.f) : (lsel > -INFINITY ? expf(lsel - m) * inv : 0.f);
-  }
-  return w * sc.scale;
-}
-
 // The loss terms and choice of one token in the general form: any finite logits, -inf where an
 // expert is out. q: the normalised scores. Lane j < k returns choice j.
 template <int Q>
@@ -527,6 +508,13 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
   pdl_trigger();
   if (c == 0 && tid == 0) *a.done = 0u;  // ticket counter of route_scan_kernel
 
+  float l[Q];
+  auto fetch = [&](int i) {
+    const float* lr = a.logits + int64_t(t0 + i) * E;
+#pragma unroll
+    for (int x = 0; x < Q; ++x) l[x] = lane + 32 * x < E ? __ldg(lr + lane + 32 * x) : -1e30f;
+  };
+  if (warp < nt) fetch(warp);  // the first token, beside the biases
   float b[Q];
   float bmin = INFINITY, bmax = -INFINITY;
   bool bias_bad = false;
@@ -556,9 +544,7 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
   for (int i = 0; i < Q; ++i) pp[i] = 0.f;
   for (int i = warp; i < nt; i += kTokWarps) {
     const float* lr = a.logits + int64_t(t0 + i) * E;
-    float l[Q];
-#pragma unroll
-    for (int x = 0; x < Q; ++x) l[x] = lane + 32 * x < E ? __ldg(lr + lane + 32 * x) : -1e30f;
+    if (i != warp) fetch(i);
     float s;
     if (!bias_bad && token_fast<Q, SIG>(l, b, brange, lr, a, sc, reinterpret_cast<float*>(scratch), pp,
                                         s_id + i * kMaxK, s)) {
@@ -766,10 +752,10 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
 // +-80 (their sum then neither overflows nor vanishes), s = x / (1 + x); else exp(l - max) for the
 // softmax and shifted sigmoids apart. Bound by the instructions; by memory (8 S E bytes) it
 // would take a fifth of the time.
-constexpr int kBwdWarps = 8, kBwdTokens = 4;  // warps a CTA, consecutive tokens a warp
+constexpr int kBwdWarps = 8, kBwdTokens = 2;  // warps a CTA, consecutive tokens a warp
 
 template <int Q, bool SIG>
-__global__ void __launch_bounds__(32 * kBwdWarps)
+__global__ void __launch_bounds__(32 * kBwdWarps, 4)
     route_scored_bwd_kernel(const float* __restrict__ logits, const int32_t* __restrict__ expert_id,
                             const int32_t* __restrict__ row, const int32_t* __restrict__ counts_routed,
                             const float* __restrict__ dgate, const float* __restrict__ gpart,
@@ -794,7 +780,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps)
 #pragma unroll
     for (int i = 0; i < Q; ++i) {
       const int e = lane + 32 * i;
-      l[i] = e < E ? __ldg(lr + e) : 0.f;
+      l[i] = e < E ? __ldg(lr + e) : -80.f;  // no expert: exp(-80) of a score, and f = 0
       plain = plain && fabsf(l[i]) <= 80.f;  // false for NaN too
     }
     // the choices, lane j < k: expert, logit, gradient of its weight
@@ -822,7 +808,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps)
     if (__all_sync(kFull, plain)) {
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
-        const float x = lane + 32 * i < E ? expf(l[i]) : 0.f;
+        const float x = expf(l[i]);
         p[i] = x;
         s += x;
         if constexpr (SIG) {
@@ -856,13 +842,30 @@ __global__ void __launch_bounds__(32 * kBwdWarps)
       s = warp_sum(s);
       lse = any ? m + logf(s) : 0.f;
     }
-    const float inv = s > 0.f ? 1.f / s : 0.f;
+    const float inv = s > 0.f ? rcp_approx(s) : 0.f;
     if constexpr (SIG) tot = warp_sum(tot);
-    const float ti = SIG ? (tot > 0.f ? 1.f / tot : 0.f) : inv;
-    ScoreArgs unit = sc;
-    unit.scale = 1.f;
-    const float w = choice_weight(lsel, lane < k, unit, m, inv);
-    const float inner = (sc.renorm || !SIG) ? warp_sum(w * dg) : 0.f;
+    const float ti = SIG ? (tot > 0.f ? rcp_approx(tot) : 0.f) : inv;
+    // the weights of the choices (unscaled; lanes j < 8, the others idle along)
+    float w, inner = 0.f;
+    if (sc.renorm) {
+      float top = SIG ? fminf(lsel, 0.f) : lsel;
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+      if (!(top > -INFINITY)) top = 0.f;
+      w = SIG ? sigmoid_shifted(lsel, top) : (lsel > -INFINITY ? expf(lsel - top) : 0.f);
+      float all = w;
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) all += __shfl_xor_sync(kFull, all, off);
+      w = all > 0.f ? w / all : 0.f;
+    } else {
+      w = SIG ? sigmoid_shifted(lsel, 0.f) : (lsel > -INFINITY ? expf(lsel - m) * inv : 0.f);
+    }
+    if (sc.renorm || !SIG) {
+      inner = w * dg;
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) inner += __shfl_xor_sync(kFull, inner, off);
+      inner = __shfl_sync(kFull, inner, 0);
+    }
     float dsel = sc.scale * w * ((sc.renorm ? dg - inner : dg) * (SIG ? sigmoid_shifted(-lsel, 0.f) : 1.f));
     if (!(lsel > -INFINITY)) dsel = 0.f;
     // the dense part: the losses' gradients (and the un-normalised softmax weights' common one)
