@@ -5,8 +5,10 @@
 //
 // for the forward (A = x, B = W), dx (A = d, B = W^T) and dW (A = d^T, B = x^T): the operands
 // come with two strides, one of them 1, and are transposed on their way into shared memory.
-// A CTA of 256 threads computes a 128 x 128 tile, 8 x 8 outputs a thread, over 16-deep slices
-// of K, the next slice's loads in registers while the present one is multiplied. When the
+// A CTA of 256 threads computes a 128 x 128 tile (64 x 128 for up to 64 rows), 8 x 8 outputs a
+// thread as pairs of columns (two multiply-adds an instruction: with single ones the issue slots
+// of shared-memory loads and multiply-adds together bound it), over 16-deep slices of K, the
+// next slice's loads in registers while the present one is multiplied; two CTAs an SM. When the
 // tiles are fewer than the SMs the K range is split over grid.z; the partial tiles are then
 // added in split order by a second kernel, which applies the epilogue.
 #include <algorithm>
@@ -17,7 +19,6 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 128, kDepth = 16, kThreadsF = 256;
-constexpr int kPitch = kTile + 4;
 
 struct Operand {
   const float* p;
@@ -26,45 +27,50 @@ struct Operand {
   int vec;  // 16-byte loads along the unit stride are possible
 };
 
-// This thread's 8 values of the 128 x 16 slice: along k (unit sk) row tid / 2, k 8 (tid & 1)
-// ..; along the rows (unit si) k tid / 16, rows 8 (tid & 15) ..
-__device__ __forceinline__ void load_slice(const Operand& o, int r0, int64_t k0, int64_t k1, float (&v)[8]) {
+// This thread's VALS = ROWS / 16 values of a ROWS x 16 slice: along k (unit sk) a row's consecutive
+// k; along the rows (unit si) one k's consecutive rows.
+template <int ROWS>
+__device__ __forceinline__ void load_slice(const Operand& o, int r0, int64_t k0, int64_t k1,
+                                           float (&v)[ROWS / 16]) {
+  constexpr int VALS = ROWS / 16, PER = 16 / VALS;  // threads along k of a row
   const int tid = threadIdx.x;
-  if (o.sk == 1) {
-    const int r = r0 + (tid >> 1);
-    const int64_t k = k0 + 8 * (tid & 1);
-    const float* p = o.p + r * o.si + k;
-    if (r < o.rows && o.vec && k + 8 <= k1) {
-      *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(p));
-      *reinterpret_cast<float4*>(v + 4) = __ldg(reinterpret_cast<const float4*>(p + 4));
-    } else {
+  const bool along_k = o.sk == 1;
+  const int r = r0 + (along_k ? tid / PER : VALS * (tid & 15));
+  const int64_t k = k0 + (along_k ? VALS * (tid % PER) : (tid >> 4));
+  const float* p = o.p + r * o.si + k * o.sk;
+  const bool whole = along_k ? (r < o.rows && k + VALS <= k1) : (k < k1 && r + VALS <= o.rows);
+  if (whole && o.vec) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = (r < o.rows && k + q < k1) ? __ldg(p + q) : 0.f;
-    }
+    for (int q = 0; q < VALS; q += 4) *reinterpret_cast<float4*>(v + q) = __ldg(reinterpret_cast<const float4*>(p + q));
   } else {
-    const int r = r0 + 8 * (tid & 15);
-    const int64_t k = k0 + (tid >> 4);
-    const float* p = o.p + r + k * o.sk;
-    if (k < k1 && o.vec && r + 8 <= o.rows) {
-      *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(p));
-      *reinterpret_cast<float4*>(v + 4) = __ldg(reinterpret_cast<const float4*>(p + 4));
-    } else {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = (k < k1 && r + q < o.rows) ? __ldg(p + q) : 0.f;
-    }
+    for (int q = 0; q < VALS; ++q)
+      v[q] = (along_k ? (r < o.rows && k + q < k1) : (k < k1 && r + q < o.rows)) ? __ldg(p + q) : 0.f;
   }
 }
-__device__ __forceinline__ void store_slice(const Operand& o, float* s, const float (&v)[8]) {
+template <int ROWS>
+__device__ __forceinline__ void store_slice(const Operand& o, float* s, const float (&v)[ROWS / 16]) {
+  constexpr int VALS = ROWS / 16, PER = 16 / VALS, PITCH = ROWS + 4;
   const int tid = threadIdx.x;
   if (o.sk == 1) {
-    const int r = tid >> 1, k = 8 * (tid & 1);
+    const int r = tid / PER, k = VALS * (tid % PER);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s[(k + q) * kPitch + r] = v[q];
+    for (int q = 0; q < VALS; ++q) s[(k + q) * PITCH + r] = v[q];
   } else {
-    float* d = s + (tid >> 4) * kPitch + 8 * (tid & 15);
-    *reinterpret_cast<float4*>(d) = *reinterpret_cast<const float4*>(v);
-    *reinterpret_cast<float4*>(d + 4) = *reinterpret_cast<const float4*>(v + 4);
+    float* d = s + (tid >> 4) * PITCH + VALS * (tid & 15);
+#pragma unroll
+    for (int q = 0; q < VALS; q += 4) *reinterpret_cast<float4*>(d + q) = *reinterpret_cast<const float4*>(v + q);
   }
+}
+
+// Two fp32 multiply-adds in one instruction (each rounded as fmaf).
+__device__ __forceinline__ void fma2(unsigned long long& c, unsigned long long a, unsigned long long b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ unsigned long long both(float a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(a));
+  return r;
 }
 
 template <int ACT>
@@ -76,66 +82,73 @@ __device__ __forceinline__ void emit(const LinearEpi& e, int64_t i, int64_t j, f
   static_cast<float*>(e.out)[i * e.ldo + j] = v;
 }
 
-template <int ACT>
-__global__ void __launch_bounds__(kThreadsF)
+template <int ACT, int ROWS>
+__global__ void __launch_bounds__(kThreadsF, 2)
     linear_f32_kernel(Operand A, Operand B, int K, int kchunk, float* part, LinearEpi e) {
-  __shared__ __align__(16) float sA[2][kDepth * kPitch], sB[2][kDepth * kPitch];
+  constexpr int RT = ROWS / 16, PA = ROWS + 4, PB = kTile + 4;  // rows a thread, pitches
+  __shared__ __align__(16) float sA[2][kDepth * PA], sB[2][kDepth * PB];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile;
+  const int i0 = blockIdx.y * ROWS, j0 = blockIdx.x * kTile;
   const int64_t k0 = int64_t(blockIdx.z) * kchunk, k1 = min(int64_t(K), k0 + kchunk);
-  float acc[8][8];
+  unsigned long long acc[RT][4];  // row r, column pairs
 #pragma unroll
-  for (int a = 0; a < 8; ++a)
+  for (int a = 0; a < RT; ++a)
 #pragma unroll
-    for (int b = 0; b < 8; ++b) acc[a][b] = 0.f;
-  float va[8], vb[8];
-  load_slice(A, i0, k0, k1, va);
-  load_slice(B, j0, k0, k1, vb);
-  store_slice(A, sA[0], va);
-  store_slice(B, sB[0], vb);
+    for (int b = 0; b < 4; ++b) acc[a][b] = 0ull;
+  float va[RT], vb[8];
+  load_slice<ROWS>(A, i0, k0, k1, va);
+  load_slice<kTile>(B, j0, k0, k1, vb);
+  store_slice<ROWS>(A, sA[0], va);
+  store_slice<kTile>(B, sB[0], vb);
   __syncthreads();
   int buf = 0;
   for (int64_t k = k0; k < k1; k += kDepth) {
     const bool more = k + kDepth < k1;
     if (more) {
-      load_slice(A, i0, k + kDepth, k1, va);
-      load_slice(B, j0, k + kDepth, k1, vb);
+      load_slice<ROWS>(A, i0, k + kDepth, k1, va);
+      load_slice<kTile>(B, j0, k + kDepth, k1, vb);
     }
     const float* pa = sA[buf] + ty * 4;
     const float* pb = sB[buf] + tx * 4;
 #pragma unroll
     for (int q = 0; q < kDepth; ++q) {
-      float a[8], b[8];
-      *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(pa + q * kPitch);
-      *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(pa + q * kPitch + 64);
-      *reinterpret_cast<float4*>(b) = *reinterpret_cast<const float4*>(pb + q * kPitch);
-      *reinterpret_cast<float4*>(b + 4) = *reinterpret_cast<const float4*>(pb + q * kPitch + 64);
+      float a[RT];
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
+      for (int h = 0; h < RT / 4; ++h)
+        *reinterpret_cast<float4*>(a + 4 * h) = *reinterpret_cast<const float4*>(pa + q * PA + 64 * h);
+      const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(pb + q * PB);
+      const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(pb + q * PB + 64);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) acc[r][c] = fmaf(a[r], b[c], acc[r][c]);
+      for (int r = 0; r < RT; ++r) {
+        const unsigned long long aa = both(a[r]);
+        fma2(acc[r][0], aa, b0.x);
+        fma2(acc[r][1], aa, b0.y);
+        fma2(acc[r][2], aa, b1.x);
+        fma2(acc[r][3], aa, b1.y);
+      }
     }
     if (more) {
-      store_slice(A, sA[buf ^ 1], va);
-      store_slice(B, sB[buf ^ 1], vb);
+      store_slice<ROWS>(A, sA[buf ^ 1], va);
+      store_slice<kTile>(B, sB[buf ^ 1], vb);
     }
     __syncthreads();
     buf ^= 1;
   }
-  // thread (ty, tx): rows 4 ty .. + 3 and 64 + 4 ty .., columns likewise
+  // thread (ty, tx): rows 4 ty .. + 3 (and 64 + 4 ty ..), columns 4 tx .. and 64 + 4 tx ..
   float* pt = part ? part + int64_t(blockIdx.z) * A.rows * B.rows : nullptr;
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
+  for (int r = 0; r < RT; ++r) {
     const int64_t i = i0 + (r >> 2) * 64 + ty * 4 + (r & 3);
     if (i >= A.rows) continue;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       const int64_t j = j0 + (c >> 2) * 64 + tx * 4 + (c & 3);
       if (j >= B.rows) continue;
-      if (pt) pt[i * B.rows + j] = acc[r][c];
-      else emit<ACT>(e, i, j, acc[r][c]);
+      const float v = __uint_as_float(unsigned(acc[r][c >> 1] >> (32 * (c & 1))));
+      if (pt) pt[i * B.rows + j] = v;
+      else emit<ACT>(e, i, j, v);
     }
   }
 }
@@ -166,7 +179,8 @@ int launch_linear_f32(const float* A, int64_t a_i, int64_t a_k, const float* B, 
                       int64_t b_k, int rows, int cols, int K, const LinearEpi& e, float* part,
                       cudaStream_t st) {
   const Operand oa = operand(A, a_i, a_k, rows), ob = operand(B, b_j, b_k, cols);
-  const int64_t ty = (rows + kTile - 1) / kTile, tx = (cols + kTile - 1) / kTile;
+  const int tile_rows = rows <= 64 ? 64 : kTile;
+  const int64_t ty = (rows + tile_rows - 1) / tile_rows, tx = (cols + kTile - 1) / kTile;
   if (ty > 65535) return MOE_ERR_UNSUPPORTED;
   // splits: about two tiles an SM, at least 64 deep each, within the scratch
   int splits = 1;
@@ -178,7 +192,8 @@ int launch_linear_f32(const float* A, int64_t a_i, int64_t a_k, const float* B, 
   splits = (K + kchunk - 1) / kchunk;
   return with_act(e.act, [&](auto tag) {
     constexpr int ACT = decltype(tag)::value;
-    int rc = launch_kernel(linear_f32_kernel<ACT>, dim3(unsigned(tx), unsigned(ty), unsigned(splits)),
+    auto kern = tile_rows == 64 ? linear_f32_kernel<ACT, 64> : linear_f32_kernel<ACT, kTile>;
+    int rc = launch_kernel(kern, dim3(unsigned(tx), unsigned(ty), unsigned(splits)),
                            dim3(kThreadsF), 0, st, oa, ob, K, kchunk, splits > 1 ? part : nullptr, e);
     if (rc != MOE_OK || splits == 1) return rc;
     const int64_t n = int64_t(rows) * cols;
