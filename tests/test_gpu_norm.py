@@ -15,7 +15,8 @@ pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 SHAPES = [(1, 1), (1, 7), (3, 2), (2, 8), (5, 33), (1, 4096), (4, 1000), (7, 1003), (130, 64), (33, 1024),
-          (300, 257), (17, 8192), (3, 16384), (2, 20001), (2000, 129), (641, 512), (9, 2056), (700, 8200), (400, 16384), (400, 4100)]
+          (300, 257), (17, 8192), (3, 16384), (2, 20001), (2000, 129), (641, 512), (9, 2056), (700, 8200), (400, 16384), (400, 4100),
+          (5000, 8), (3001, 16), (2500, 24), (1777, 40), (1000, 100), (999, 3), (611, 5)]
 
 
 def ref_forward(x, res, gamma, beta, eps):

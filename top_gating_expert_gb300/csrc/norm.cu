@@ -10,8 +10,8 @@
 // directions are bound by memory: every input is read once and every output written once.
 //
 // Ring kernels (norm_fwd_ring_kernel, norm_bwd_ring_kernel), for many rows: CTAs of 16 warps, one an
-// SM, G warps a row (by its length) and 16 / G rows at a time, each group of warps walking rows of
-// its own. A lane copies its own pieces of the rows to come into its own shared memory with
+// SM, L lanes a row (by its length, from one lane to 16 warps) and 512 / L rows at a time, each
+// group of lanes walking rows of its own. A lane copies its own pieces of the rows to come into its own shared memory with
 // cp.async and reads only those back, so the copies need no barrier; 64 to 128 KB an SM are
 // then in flight whatever the registers hold. The two row sums of each direction cross the
 // group's warps under a barrier of their own. gamma and beta stay in registers; the backward
@@ -387,35 +387,44 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Sum of v over the G warps of a row's group (s_red: one float a warp of the group, free until
-// the group's next barrier but one); a fixed tree, every lane gets it.
-__device__ __forceinline__ float group_sum(float v, int G, int slot, float* s_red) {
+// Sum of v over the L lanes of a row (a power of two: lanes of one warp, or L / 32 whole warps,
+// which then meet at a barrier of their slot's own; s_red: one float a warp of the row, free until
+// its next barrier but one). A fixed tree, every lane gets it; all lanes of a warp take part.
+template <bool SUB>  // SUB: L < 32
+__device__ __forceinline__ float row_lanes_sum(float v, int L, int slot, float* s_red) {
+  if constexpr (SUB) {
+    for (int off = L >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+  } else {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  if (G == 1) return v;
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) s_red[(threadIdx.x >> 5) & (G - 1)] = v;
-  asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(G * 32) : "memory");
-  v = s_red[lane & (G - 1)];
-  for (int off = G >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    const int G = L >> 5;
+    if (G == 1) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) s_red[(threadIdx.x >> 5) & (G - 1)] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(L) : "memory");
+    v = s_red[lane & (G - 1)];
+    for (int off = G >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+  }
 }
 
 constexpr int kFwdStages = 3;
 
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, int NV, bool SUB = false>
 __global__ void __launch_bounds__(32 * kRingWarps, 1)
     norm_fwd_ring_kernel(const T* x, const T* res, const float* __restrict__ gamma,
-                         const float* __restrict__ beta, T* h, T* y, float* mean, float* rstd, int G,
+                         const float* __restrict__ beta, T* h, T* y, float* mean, float* rstd, int L,
                          moe_norm_t n) {
   constexpr int BYTES = VEC * int(sizeof(T));
   extern __shared__ __align__(16) uint8_t s_ring[];  // [stage][stream][NV][thread] pieces
-  __shared__ float s_red[kRingWarps][2][kRingWarps];
+  __shared__ float s_red[kRingWarps / 2][2][kRingWarps];  // rows of two warps or more
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slots = kRingWarps / G, slot = warp / G;
-  const int M = n.cols, step = G * 32 * VEC, c0 = ((warp & (G - 1)) * 32 + lane) * VEC;
+  const int tid = threadIdx.x;
+  const int slots = 32 * kRingWarps / L, slot = tid / L, rl = tid & (L - 1);
+  const int M = n.cols, step = L * VEC, c0 = rl * VEC;
+  float(*red)[kRingWarps] = s_red[L > 32 ? slot : 0];
   const int streams = res ? 2 : 1;
   auto piece = [&](int stage, int stream, int i) {
     return s_ring + size_t(((stage * streams + stream) * NV + i) * (32 * kRingWarps) + tid) * BYTES;
@@ -448,7 +457,10 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
 #pragma unroll
   for (int s = 0; s < kFwdStages - 1; ++s) fetch(r + s * stride, s);
   int stage = 0;
-  for (; r < n.rows; r += stride) {
+  // (a warp of several rows goes on while any of them exists; first: its lowest)
+  const int first = SUB ? (tid & 31) / L : 0;
+  for (; r - first < n.rows; r += stride) {
+    const bool on = !SUB || r < n.rows;
     fetch(r + (kFwdStages - 1) * stride, stage == 0 ? kFwdStages - 1 : stage - 1);
     copy_wait<kFwdStages - 1>();
     float v[NV][VEC], s = 0.f;
@@ -457,7 +469,7 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
       const int c = c0 + i * step;
 #pragma unroll
       for (int q = 0; q < VEC; ++q) v[i][q] = 0.f;
-      if (c < M) {
+      if (on && c < M) {
         const Vec<T, VEC> xv = load_piece<T, VEC>(piece(stage, 0, i));
 #pragma unroll
         for (int q = 0; q < VEC; ++q) v[i][q] = to_f32(xv.v[q]);
@@ -477,7 +489,7 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
       for (int q = 0; q < VEC; ++q) s += v[i][q];
     }
     stage = stage + 1 == kFwdStages ? 0 : stage + 1;
-    const float mu = group_sum(s, G, slot, s_red[slot][0]) / float(M);
+    const float mu = row_lanes_sum<SUB>(s, L, slot, red[0]) / float(M);
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -488,17 +500,17 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
           ss = fmaf(v[i][q], v[i][q], ss);
         }
       }
-    const float rs = 1.f / sqrtf(group_sum(ss, G, slot, s_red[slot][1]) / float(M) + n.eps);
+    const float rs = 1.f / sqrtf(row_lanes_sum<SUB>(ss, L, slot, red[1]) / float(M) + n.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = c0 + i * step;
-      if (c >= M) continue;
+      if (!on || c >= M) continue;
       Vec<T, VEC> o;
 #pragma unroll
       for (int q = 0; q < VEC; ++q) o.v[q] = from_f32<T>(fmaf(v[i][q] * rs, g[i][q], b[i][q]));
       store_vec<T, VEC>(y + r * n.ldy + c, o);
     }
-    if (lane == 0 && (warp & (G - 1)) == 0) {
+    if (on && rl == 0) {
       if (mean) mean[r] = mu;
       if (rstd) rstd[r] = rs;
     }
@@ -506,20 +518,20 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
 }
 
 // part: [gridDim.x][2][cols], null when neither dgamma nor dbeta is wanted.
-template <typename T, int VEC, int NV, int STAGES>
+template <typename T, int VEC, int NV, int STAGES, bool SUB = false>
 __global__ void __launch_bounds__(32 * kRingWarps, 1)
     norm_bwd_ring_kernel(const T* dy, const T* h, const float* __restrict__ gamma,
                          const float* __restrict__ mean, const float* __restrict__ rstd, const T* dh, T* dx,
-                         float* __restrict__ part, int G, moe_norm_t n) {
+                         float* __restrict__ part, int L, moe_norm_t n) {
   constexpr int BYTES = VEC * int(sizeof(T));
   extern __shared__ __align__(16) uint8_t s_ring[];  // [stage][stream][NV][thread] pieces, then
                                                      // the slots' column sums
-  __shared__ float s_red[kRingWarps][4][kRingWarps];
+  __shared__ float s_red[kRingWarps / 2][4][kRingWarps];  // rows of two warps or more
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slots = kRingWarps / G, slot = warp / G;
-  const int M = n.cols, step = G * 32 * VEC, c0 = ((warp & (G - 1)) * 32 + lane) * VEC;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int slots = 32 * kRingWarps / L, slot = tid / L;
+  const int M = n.cols, step = L * VEC, c0 = (tid & (L - 1)) * VEC, G = L >> 5;
   const int streams = dh ? 3 : 2;
   const float inv_m = 1.f / float(M);
   auto piece = [&](int stage, int stream, int i) {
@@ -552,7 +564,9 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
   for (int s = 0; s < STAGES - 1; ++s) fetch(r + s * stride, s);
   float mu = r < n.rows ? __ldg(mean + r) : 0.f, rs = r < n.rows ? __ldg(rstd + r) : 0.f;
   int stage = 0, odd = 0;
-  for (; r < n.rows; r += stride) {
+  const int first = SUB ? lane / L : 0;  // (as in the forward)
+  for (; r - first < n.rows; r += stride) {
+    const bool on = !SUB || r < n.rows;
     fetch(r + (STAGES - 1) * stride, stage == 0 ? STAGES - 1 : stage - 1);
     const float mu_r = mu, rs_r = rs;
     if (r + stride < n.rows) {
@@ -563,7 +577,7 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (c0 + i * step >= M) continue;
+      if (!on || c0 + i * step >= M) continue;
       const Vec<T, VEC> hv = load_piece<T, VEC>(piece(stage, 0, i)), dv = load_piece<T, VEC>(piece(stage, 1, i));
 #pragma unroll
       for (int q = 0; q < VEC; ++q) {
@@ -577,16 +591,17 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
+      if (SUB && off >= L) continue;
       s1 += __shfl_xor_sync(0xffffffffu, s1, off);
       s2 += __shfl_xor_sync(0xffffffffu, s2, off);
     }
-    if (G > 1) {
+    if (!SUB && G > 1) {
       float* red = s_red[slot][2 * odd];  // two places in turn: one barrier a row
       if (lane == 0) {
-        red[warp & (G - 1)] = s1;
-        red[kRingWarps + (warp & (G - 1))] = s2;
+        red[(tid >> 5) & (G - 1)] = s1;
+        red[kRingWarps + ((tid >> 5) & (G - 1))] = s2;
       }
-      asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(G * 32) : "memory");
+      asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(L) : "memory");
       s1 = red[lane & (G - 1)];
       s2 = red[kRingWarps + (lane & (G - 1))];
       for (int off = G >> 1; off > 0; off >>= 1) {
@@ -599,7 +614,7 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = c0 + i * step;
-      if (c >= M) continue;
+      if (!on || c >= M) continue;
       const Vec<T, VEC> hv = load_piece<T, VEC>(piece(stage, 0, i)), dv = load_piece<T, VEC>(piece(stage, 1, i));
       Vec<T, VEC> ev, o;
       if (dh) ev = load_piece<T, VEC>(piece(stage, 2, i));
@@ -616,22 +631,34 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
     odd ^= 1;
   }
   if (!part) return;
-  // the slots' column sums, added in slot order
+  // the slots' column sums, added in slot order (several rows a warp: first across the warp)
   copy_wait<0>();
+  if constexpr (SUB) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int q = 0; q < VEC; ++q)
+        for (int off = 16; off >= L; off >>= 1) {
+          sg[i][q] += __shfl_xor_sync(0xffffffffu, sg[i][q], off);
+          sb[i][q] += __shfl_xor_sync(0xffffffffu, sb[i][q], off);
+        }
+  }
   float* s_cols = reinterpret_cast<float*>(s_ring);
-  const int width = step * NV;
+  const int width = step * NV, parts = min(slots, kRingWarps), mine = SUB ? tid >> 5 : slot;
   float* out = part + int64_t(blockIdx.x) * 2 * M;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     __syncthreads();
+    if (!SUB || lane < L) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int q = 0; q < VEC; ++q) s_cols[slot * width + c0 + i * step + q] = which ? sb[i][q] : sg[i][q];
+        for (int q = 0; q < VEC; ++q) s_cols[mine * width + c0 + i * step + q] = which ? sb[i][q] : sg[i][q];
+    }
     __syncthreads();
     for (int c = tid; c < M; c += 32 * kRingWarps) {
       float t = 0.f;
-      for (int w = 0; w < slots; ++w) t += s_cols[w * width + c];
+      for (int w = 0; w < parts; ++w) t += s_cols[w * width + c];
       out[which * M + c] = t;
     }
   }
@@ -666,6 +693,14 @@ int row_warps(int cols, int vec, int nv, int most = 16) {
   return G <= most ? G : 0;
 }
 
+// Lanes a row: 32 G, or a part of a warp for short rows (several rows a warp).
+int row_lanes(int cols, int vec, int nv, int G) {
+  int L = 32 * G;
+  if (G == 1 && nv == 1)
+    while (L > 1 && (L / 2) * vec >= cols) L /= 2;
+  return L;
+}
+
 template <typename T, int VEC>
 int norm_forward_v(const moe_norm_t& n, const T* x, const T* res, const float* gamma, const float* beta,
                    T* h, T* y, float* mean, float* rstd, cudaStream_t st) {
@@ -679,7 +714,7 @@ int norm_forward_v(const moe_norm_t& n, const T* x, const T* res, const float* g
     int G = row_warps(n.cols, VEC, nv, 1);
     while (G == 0 && nv < kRing) G = row_warps(n.cols, VEC, nv *= 2, nv == kRing ? 16 : 1);
     if (!few && G) {
-      const int slots = kRingWarps / G;
+      const int L = row_lanes(n.cols, VEC, nv, G), slots = 32 * kRingWarps / L;
       const unsigned grid = unsigned(std::min<int64_t>((n.rows + slots - 1) / slots, num_sms()));
       const size_t smem = size_t(kFwdStages) * (res ? 2 : 1) * nv * 32 * kRingWarps * VEC * sizeof(T);
       const size_t most = size_t(kFwdStages) * 2 * nv * 32 * kRingWarps * VEC * sizeof(T);
@@ -687,10 +722,11 @@ int norm_forward_v(const moe_norm_t& n, const T* x, const T* res, const float* g
         static std::atomic<unsigned long long> seen{0};
         if (const int rc = allow_smem(reinterpret_cast<const void*>(kern), int(most), seen)) return rc;
         return launch_kernel(kern, dim3(grid), dim3(32 * kRingWarps), smem, st, x, res, gamma, beta, h, y, mean,
-                             rstd, G, n);
+                             rstd, L, n);
       };
       switch (nv) {
-        case 1: return go(norm_fwd_ring_kernel<T, VEC, 1>, Tag<1>{});
+        case 1: return L < 32 ? go(norm_fwd_ring_kernel<T, VEC, 1, true>, Tag<0>{})
+                              : go(norm_fwd_ring_kernel<T, VEC, 1>, Tag<1>{});
         case 2: return go(norm_fwd_ring_kernel<T, VEC, 2>, Tag<2>{});
         case 4: return go(norm_fwd_ring_kernel<T, VEC, 4>, Tag<4>{});
       }
@@ -750,7 +786,7 @@ int norm_backward_v(const moe_norm_t& n, const T* dy, const T* h, const float* g
     int G = row_warps(n.cols, VEC, nv, 1);
     while (G == 0 && nv < kRing) G = row_warps(n.cols, VEC, nv *= 2, nv >= kMore ? 16 : 1);
     if (G) {
-      const int slots = kRingWarps / G;
+      const int L = row_lanes(n.cols, VEC, nv, G), slots = 32 * kRingWarps / L;
       const int grid = int(std::min<int64_t>((n.rows + slots - 1) / slots, std::min(num_sms(), 160)));
       auto go = [&](auto kern, int stages, auto) -> int {
         const size_t ring = size_t(stages) * (dh ? 3 : 2) * nv * 32 * kRingWarps * VEC * sizeof(T);
@@ -760,10 +796,12 @@ int norm_backward_v(const moe_norm_t& n, const T* dy, const T* h, const float* g
         static std::atomic<unsigned long long> seen{0};
         if (const int rc = allow_smem(reinterpret_cast<const void*>(kern), int(most), seen)) return rc;
         return launch_kernel(kern, dim3(unsigned(grid)), dim3(32 * kRingWarps), smem, st, dy, h, gamma, mean, rstd,
-                             dh, dx, sums ? part : nullptr, G, n);
+                             dh, dx, sums ? part : nullptr, L, n);
       };
       rc = MOE_ERR_UNSUPPORTED;
-      if (nv == 1) rc = go(norm_bwd_ring_kernel<T, VEC, 1, 3>, 3, Tag<1>{});
+      if (nv == 1)
+        rc = L < 32 ? go(norm_bwd_ring_kernel<T, VEC, 1, 3, true>, 3, Tag<0>{})
+                    : go(norm_bwd_ring_kernel<T, VEC, 1, 3>, 3, Tag<1>{});
       if (nv == 2) rc = go(norm_bwd_ring_kernel<T, VEC, 2, 3>, 3, Tag<2>{});
       if (nv == 4) rc = go(norm_bwd_ring_kernel<T, VEC, 4, VEC == 1 ? 3 : 2>, VEC == 1 ? 3 : 2, Tag<4>{});
       if constexpr (kRing == 8) {
