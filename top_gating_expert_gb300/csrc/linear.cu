@@ -33,13 +33,28 @@ __global__ void __launch_bounds__(kColThreads * kRowLanes)
       const Vec<T, VEC> g = load_vec<T, VEC>(dy + r * ldy + c);
       Vec<T, VEC> o, w;
       if constexpr (ACT != MOE_LIN_NONE) w = load_vec<T, VEC>(pre + r * ldp + c);
+      if constexpr (sizeof(T) == 2 && VEC > 1 && ACT != MOE_LIN_NONE) {
 #pragma unroll
-      for (int q = 0; q < VEC; ++q) {
-        float v = to_f32(g.v[q]);
-        if constexpr (ACT != MOE_LIN_NONE)
-          v *= sizeof(T) == 2 ? slope_fast<ACT>(to_f32(w.v[q])) : act_slope<ACT>(to_f32(w.v[q]));
-        acc[q] += v;
-        o.v[q] = from_f32<T>(v);
+        for (int q = 0; q < VEC; q += 2) {
+          const f32x2 sl = slope_fast2<ACT>(pack2(to_f32(w.v[q]), to_f32(w.v[q + 1])));
+          const f32x2 v = mul2(pack2(to_f32(g.v[q]), to_f32(g.v[q + 1])), sl);
+          const float2 f = unpack2(v);
+          acc[q] += f.x;
+          acc[q + 1] += f.y;
+          o.v[q] = from_f32<T>(f.x);
+          o.v[q + 1] = from_f32<T>(f.y);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) {
+          float v = to_f32(g.v[q]);
+          if constexpr (ACT != MOE_LIN_NONE) {
+            const float p = to_f32(w.v[q]);
+            v *= sizeof(T) == 2 ? unpack2(slope_fast2<ACT>(pack2(p, p))).x : act_slope<ACT>(p);
+          }
+          acc[q] += v;
+          o.v[q] = from_f32<T>(v);
+        }
       }
       if (d) store_vec<T, VEC>(d + r * ldd + c, o);
     }

@@ -84,54 +84,74 @@ __device__ __forceinline__ float act_slope(float v) {
 //   Phi(-|v|) = erfc(x) / 2, x = |v| / sqrt(2), erfc(x) = exp(-x^2) R(t), t = 1 / (1 + 0.38 x),
 // with R a polynomial of degree 7 without constant term fitted to exp(x^2) erfc(x) by linear
 // programming on the relative error over 0 <= x <= 10 (1.0e-6; the tail keeps its relative
-// precision). erff's two branches and 1 + erf's cancellation cost about twice the instructions.
-// tail = Phi(-|v|), e = exp(-v^2 / 2)
-__device__ __forceinline__ void normal_parts(float v, float& tail, float& e) {
-  e = exp2_approx(v * v * -0.72134752044448170f);
-  const float t = rcp_approx(fmaf(0.26870057685f, fabsf(v), 1.f));
-  float r = -0.0625806375f;  // R's coefficients, halved
-  r = fmaf(r, t, 0.167536944f);
-  r = fmaf(r, t, -0.03422876445f);
-  r = fmaf(r, t, 0.123351455f);
-  r = fmaf(r, t, 0.0905347165f);
-  r = fmaf(r, t, 0.108237808f);
-  r = fmaf(r, t, 0.1071479915f);
-  tail = e * (r * t);
+// precision). erff's two branches and 1 + erf's cancellation cost about twice the instructions, and
+// pairs in one instruction halve what is left (the 8192 x 14336 epilogue and the backward's pass
+// over dy and pre are bound by issue).
+// All on pairs. e = exp(-v^2 / 2), and Phi(v): the tail below zero, one less it above
+__device__ __forceinline__ f32x2 exp2_2(f32x2 x) {
+  const float2 f = unpack2(x);
+  return pack2(exp2_approx(f.x), exp2_approx(f.y));
+}
+__device__ __forceinline__ f32x2 rcp_2(f32x2 x) {
+  const float2 f = unpack2(x);
+  return pack2(rcp_approx(f.x), rcp_approx(f.y));
+}
+__device__ __forceinline__ f32x2 normal_cdf2(f32x2 v, f32x2& e) {
+  const float2 f = unpack2(v);
+  e = exp2_2(mul2(mul2(v, v), set2(-0.72134752044448170f)));
+  const f32x2 t = rcp_2(fma2(pack2(fabsf(f.x), fabsf(f.y)), set2(0.26870057685f), set2(1.f)));
+  f32x2 r = set2(-0.0625806375f);  // R's coefficients, halved
+  r = fma2(r, t, set2(0.167536944f));
+  r = fma2(r, t, set2(-0.03422876445f));
+  r = fma2(r, t, set2(0.123351455f));
+  r = fma2(r, t, set2(0.0905347165f));
+  r = fma2(r, t, set2(0.108237808f));
+  r = fma2(r, t, set2(0.1071479915f));
+  const f32x2 tail = mul2(e, mul2(r, t));
+  const float2 lo = unpack2(tail), hi = unpack2(fma2(tail, set2(-1.f), set2(1.f)));
+  return pack2(f.x < 0.f ? lo.x : hi.x, f.y < 0.f ? lo.y : hi.y);
 }
 template <int ACT>
-__device__ __forceinline__ float act_fast(float v) {
+__device__ __forceinline__ f32x2 act_fast2(f32x2 v) {
   constexpr float kL2e = 1.44269504088896341f;
   if constexpr (ACT == MOE_LIN_GELU) {
-    float tail, e;
-    normal_parts(v, tail, e);
-    return v * (v < 0.f ? tail : 1.f - tail);
+    f32x2 e;
+    return mul2(v, normal_cdf2(v, e));
+  } else if constexpr (ACT == MOE_LIN_GELU_TANH) {  // v / (1 + exp(-2u))
+    const f32x2 u = mul2(v, fma2(mul2(v, v), set2(-0.0713548162726f * kL2e), set2(-1.59576912160573f * kL2e)));
+    return mul2(v, rcp_2(add2(exp2_2(u), set2(1.f))));
+  } else if constexpr (ACT == MOE_LIN_SILU) {
+    return mul2(v, rcp_2(add2(exp2_2(mul2(v, set2(-kL2e))), set2(1.f))));
+  } else {
+    const float2 f = unpack2(v);
+    return pack2(act_value<ACT>(f.x), act_value<ACT>(f.y));
   }
-  if constexpr (ACT == MOE_LIN_GELU_TANH) {  // v / (1 + exp(-2u))
-    return v * rcp_approx(1.f + exp2_approx(v * fmaf(-0.0713548162726f * kL2e, v * v, -1.59576912160573f * kL2e)));
-  }
-  if constexpr (ACT == MOE_LIN_SILU) return v * rcp_approx(1.f + exp2_approx(v * -kL2e));
-  return act_value<ACT>(v);
 }
 template <int ACT>
-__device__ __forceinline__ float slope_fast(float v) {
+__device__ __forceinline__ f32x2 slope_fast2(f32x2 v) {
   constexpr float kL2e = 1.44269504088896341f;
+  const float2 f = unpack2(v);
   if constexpr (ACT == MOE_LIN_GELU) {
-    float tail, e;
-    normal_parts(v, tail, e);
-    return fmaf(v * 0.39894228040143268f, e, v < 0.f ? tail : 1.f - tail);
+    f32x2 e;
+    const f32x2 phi = normal_cdf2(v, e);
+    return fma2(mul2(v, set2(0.39894228040143268f)), e, phi);
+  } else if constexpr (ACT == MOE_LIN_GELU_TANH) {
+    const f32x2 v2 = mul2(v, v);  // the exponent capped at 2^115: the reciprocal stays normal
+    const float2 u = unpack2(mul2(v, fma2(v2, set2(-0.0713548162726f * kL2e), set2(-1.59576912160573f * kL2e))));
+    const f32x2 e = pack2(exp2_approx(fminf(u.x, 115.f)), exp2_approx(fminf(u.y, 115.f)));
+    const f32x2 s = rcp_2(add2(e, set2(1.f)));
+    const float2 d = unpack2(
+        fma2(mul2(v, fma2(v2, set2(0.214064448818f), set2(1.59576912160573f))), mul2(s, mul2(e, s)), s));
+    // far out v^3 may overflow; the slope is 0 or 1 there
+    return pack2(fabsf(f.x) > 16.f ? (f.x > 0.f ? 1.f : 0.f) : d.x, fabsf(f.y) > 16.f ? (f.y > 0.f ? 1.f : 0.f) : d.y);
+  } else if constexpr (ACT == MOE_LIN_SILU) {
+    const float2 u = unpack2(mul2(v, set2(-kL2e)));
+    const f32x2 e = pack2(exp2_approx(fminf(u.x, 115.f)), exp2_approx(fminf(u.y, 115.f)));
+    const f32x2 s = rcp_2(add2(e, set2(1.f)));
+    return mul2(s, fma2(v, mul2(e, s), set2(1.f)));
+  } else {
+    return pack2(act_slope<ACT>(f.x), act_slope<ACT>(f.y));
   }
-  if constexpr (ACT == MOE_LIN_GELU_TANH) {
-    if (fabsf(v) > 16.f) return v > 0.f ? 1.f : 0.f;
-    const float v2 = v * v;  // the exponent capped at 2^115: the reciprocal stays normal
-    const float e = exp2_approx(fminf(v * fmaf(-0.0713548162726f * kL2e, v2, -1.59576912160573f * kL2e), 115.f));
-    const float s = rcp_approx(1.f + e);
-    return fmaf(v * fmaf(0.214064448818f, v2, 1.59576912160573f), s * (e * s), s);
-  }
-  if constexpr (ACT == MOE_LIN_SILU) {
-    const float e = exp2_approx(fminf(v * -kL2e, 115.f)), s = rcp_approx(1.f + e);
-    return s * fmaf(v, e * s, 1.f);
-  }
-  return act_slope<ACT>(v);
 }
 __device__ __forceinline__ float act_any(int act, float v) {
   switch (act) {
@@ -142,26 +162,23 @@ __device__ __forceinline__ float act_any(int act, float v) {
   }
   return v;
 }
-// n values at once, the activation chosen outside the loop
+// N values at once, the activation chosen outside the loop
+template <int ACT, int N>
+__device__ __forceinline__ void act_pairs(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 f = unpack2(act_fast2<ACT>(pack2(v[i], v[i + 1])));
+    v[i] = f.x;
+    v[i + 1] = f.y;
+  }
+}
 template <int N>
 __device__ __forceinline__ void act_fast_all(int act, float (&v)[N]) {
   switch (act) {
-    case MOE_LIN_RELU:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = act_fast<MOE_LIN_RELU>(v[i]);
-      break;
-    case MOE_LIN_GELU:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = act_fast<MOE_LIN_GELU>(v[i]);
-      break;
-    case MOE_LIN_GELU_TANH:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = act_fast<MOE_LIN_GELU_TANH>(v[i]);
-      break;
-    case MOE_LIN_SILU:
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = act_fast<MOE_LIN_SILU>(v[i]);
-      break;
+    case MOE_LIN_RELU: act_pairs<MOE_LIN_RELU>(v); break;
+    case MOE_LIN_GELU: act_pairs<MOE_LIN_GELU>(v); break;
+    case MOE_LIN_GELU_TANH: act_pairs<MOE_LIN_GELU_TANH>(v); break;
+    case MOE_LIN_SILU: act_pairs<MOE_LIN_SILU>(v); break;
   }
 }
 

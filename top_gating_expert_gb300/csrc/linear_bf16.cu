@@ -432,7 +432,8 @@ constexpr int kPairThreads = 64 + 32 * 8;
 
 struct PairArgs {
   int rows, cols, nkb, tiles_m, tiles_n;
-  int a_mn, b_mn, res_vec;
+  int a_mn, b_mn, res_vec, bias_vec;
+  int stream;  // outputs too large to be found in L2 again: stores marked evict-first
   LinearEpi e;
   unsigned* status;
 };
@@ -611,7 +612,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tma_store_2d(map, col, row, smem_u32(b));
+        if (p.stream) tma_store_2d_hint(map, col, row, smem_u32(b), policy_evict_first());
+        else tma_store_2d(map, col, row, smem_u32(b));
         bulk_commit();
       }
       nb ^= 1;
@@ -641,12 +643,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) rv[c] = *reinterpret_cast<const uint4*>(rp + row * p.e.ldr + col + 8 * c);
         }
-        const float bias = p.e.bias && col + lane < p.cols ? __ldg(p.e.bias + col + lane) : 0.f;
+        float4 bv[8];  // the columns' biases, one address for the whole warp
+        const bool bvec = p.bias_vec && col + 32 <= p.cols;
+        if (bvec) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) bv[j] = __ldg(reinterpret_cast<const float4*>(p.e.bias + col) + j);
+        }
         tmem_ld_wait();
         float v[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(acc32[j]);
-        if (p.e.bias) {
+        if (bvec) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 lo = unpack2(add2(pack2(v[4 * j], v[4 * j + 1]), pack2(bv[j].x, bv[j].y)));
+            const float2 hi = unpack2(add2(pack2(v[4 * j + 2], v[4 * j + 3]), pack2(bv[j].z, bv[j].w)));
+            v[4 * j] = lo.x; v[4 * j + 1] = lo.y; v[4 * j + 2] = hi.x; v[4 * j + 3] = hi.y;
+          }
+        } else if (p.e.bias) {
+          const float bias = col + lane < p.cols ? __ldg(p.e.bias + col + lane) : 0.f;
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, bias, j);
         }
@@ -721,6 +736,8 @@ int run_pair(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
   if (int64_t(p.tiles_m) * p.tiles_n > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
   p.a_mn = A.mn; p.b_mn = B.mn;
   p.res_vec = e.res && out_aligned(e.res, e.ldr);
+  p.bias_vec = e.bias && reinterpret_cast<uintptr_t>(e.bias) % 16 == 0;
+  p.stream = int64_t(rows) * cols * 2 * (e.pre ? 2 : 1) > (int64_t(96) << 20);
   p.e = e;
   p.status = status;
   auto kern = linear_pair_kernel<BN>;

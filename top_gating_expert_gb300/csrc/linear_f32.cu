@@ -63,16 +63,6 @@ __device__ __forceinline__ void store_slice(const Operand& o, float* s, const fl
   }
 }
 
-// Two fp32 multiply-adds in one instruction (each rounded as fmaf).
-__device__ __forceinline__ void fma2(unsigned long long& c, unsigned long long a, unsigned long long b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ unsigned long long both(float a) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(a));
-  return r;
-}
-
 template <int ACT>
 __device__ __forceinline__ void emit(const LinearEpi& e, int64_t i, int64_t j, float v) {
   if (e.bias) v += e.bias[j];
@@ -92,7 +82,7 @@ __global__ void __launch_bounds__(kThreadsF, 2)
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int i0 = blockIdx.y * ROWS, j0 = blockIdx.x * kTile;
   const int64_t k0 = int64_t(blockIdx.z) * kchunk, k1 = min(int64_t(K), k0 + kchunk);
-  unsigned long long acc[RT][4];  // row r, column pairs
+  f32x2 acc[RT][4];  // row r, column pairs
 #pragma unroll
   for (int a = 0; a < RT; ++a)
 #pragma unroll
@@ -122,11 +112,11 @@ __global__ void __launch_bounds__(kThreadsF, 2)
       const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(pb + q * PB + 64);
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const unsigned long long aa = both(a[r]);
-        fma2(acc[r][0], aa, b0.x);
-        fma2(acc[r][1], aa, b0.y);
-        fma2(acc[r][2], aa, b1.x);
-        fma2(acc[r][3], aa, b1.y);
+        const f32x2 aa = set2(a[r]);
+        acc[r][0] = fma2(aa, b0.x, acc[r][0]);
+        acc[r][1] = fma2(aa, b0.y, acc[r][1]);
+        acc[r][2] = fma2(aa, b1.x, acc[r][2]);
+        acc[r][3] = fma2(aa, b1.y, acc[r][3]);
       }
     }
     if (more) {
@@ -146,7 +136,8 @@ __global__ void __launch_bounds__(kThreadsF, 2)
     for (int c = 0; c < 8; ++c) {
       const int64_t j = j0 + (c >> 2) * 64 + tx * 4 + (c & 3);
       if (j >= B.rows) continue;
-      const float v = __uint_as_float(unsigned(acc[r][c >> 1] >> (32 * (c & 1))));
+      const float2 f = unpack2(acc[r][c >> 1]);
+      const float v = c & 1 ? f.y : f.x;
       if (pt) pt[i * B.rows + j] = v;
       else emit<ACT>(e, i, j, v);
     }
