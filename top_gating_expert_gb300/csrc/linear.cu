@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(256)
 
 // Copies of up to two operands to 16-byte rows: dst [rows][ldd] = src [rows][cols], src on any
 // element boundary. Eight elements a thread, read as the 4-byte words that hold them (five when
-// the row starts inside a word) and shifted into place.
+// the row starts inside a word) and shifted into place; a warp takes 256 columns of a row.
 struct AlignJob {
   const __nv_bfloat16* src;
   int64_t ld, rows;
@@ -110,24 +110,25 @@ __global__ void __launch_bounds__(256) linear_align_kernel(AlignJob j0, AlignJob
   pdl_wait();
   pdl_trigger();
   const AlignJob j = blockIdx.y ? j1 : j0;
-  const int per = int(j.ldd / 8);
-  const int64_t n = j.rows * per;
-  for (int64_t x = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; x < n; x += int64_t(gridDim.x) * blockDim.x) {
-    const int64_t r = x / per;
-    const int c = int(x - r * per) * 8, left = j.cols - c;  // >= 1
-    const uintptr_t at = reinterpret_cast<uintptr_t>(j.src + r * j.ld + c);
-    const int odd = int(at >> 1) & 1;
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(at & ~uintptr_t(3));
-    uint32_t v[5];
+  const int per = int(j.ldd / 8), lane = threadIdx.x & 31;
+  for (int64_t r = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); r < j.rows; r += int64_t(gridDim.x) * 8) {
+    const uintptr_t row = reinterpret_cast<uintptr_t>(j.src + r * j.ld);
+    const int odd = int(row >> 1) & 1;
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(row & ~uintptr_t(3));
+    for (int p = blockIdx.z * 32 + lane; p < per; p += gridDim.z * 32) {
+      const int left = j.cols - 8 * p;  // >= 1
+      const uint32_t* w = words + 4 * p;
+      uint32_t v[5];
 #pragma unroll
-    for (int q = 0; q < 5; ++q) v[q] = 2 * q - odd < left && (q < 4 || odd) ? __ldg(w + q) : 0u;
-    uint32_t o[4];
+      for (int q = 0; q < 5; ++q) v[q] = 2 * q - odd < left && (q < 4 || odd) ? __ldg(w + q) : 0u;
+      uint32_t o[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      o[q] = odd ? __funnelshift_r(v[q], v[q + 1], 16) : v[q];
-      if (2 * q + 1 >= left) o[q] &= 2 * q < left ? 0xffffu : 0u;  // past the row's end
+      for (int q = 0; q < 4; ++q) {
+        o[q] = odd ? __funnelshift_r(v[q], v[q + 1], 16) : v[q];
+        if (2 * q + 1 >= left) o[q] &= 2 * q < left ? 0xffffu : 0u;  // past the row's end
+      }
+      *reinterpret_cast<uint4*>(j.dst + r * j.ldd + 8 * p) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    *reinterpret_cast<uint4*>(j.dst + r * j.ldd + c) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -203,10 +204,10 @@ int launch_align(const AlignJob& a, const AlignJob& b, cudaStream_t st) {
   const bool two = a.src && b.src;
   if (!a.src && !b.src) return MOE_OK;
   const AlignJob& one = a.src ? a : b;
-  const int64_t n = std::max(one.rows * (one.ldd / 8), two ? b.rows * (b.ldd / 8) : 0);
-  return launch_kernel(linear_align_kernel,
-                       dim3(unsigned(std::min<int64_t>((n + 255) / 256, 16 * num_sms())), two ? 2 : 1), dim3(256),
-                       0, st, one, b);
+  const int64_t rows = std::max(one.rows, two ? b.rows : 0), per = std::max(one.ldd, two ? b.ldd : 0) / 8;
+  const dim3 grid(unsigned(std::min<int64_t>((rows + 7) / 8, 1 << 20)), two ? 2 : 1,
+                  unsigned(std::min<int64_t>((per + 31) / 32, 64)));
+  return launch_kernel(linear_align_kernel, grid, dim3(256), 0, st, one, b);
 }
 
 // d (when it is given) and dbias (when it is given; part: its slices' partial sums)

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreadsG) linear_few_kernel(FewArgs p) {
     if (n < p.N) {
       const uintptr_t a = (reinterpret_cast<uintptr_t>(W + n * p.ldw) + 15) & ~uintptr_t(15);
       const uintptr_t b = reinterpret_cast<uintptr_t>(W + n * p.ldw + p.K) & ~uintptr_t(15);
-      if (a < b) prefetch_l2_bulk(reinterpret_cast<const void*>(a), uint32_t(b - a));
+      if (a < b) prefetch_l2_bulk(reinterpret_cast<const void*>(a), uint32_t(min(b - a, uintptr_t(32768))));
     }
   }
   pdl_wait();

@@ -498,6 +498,7 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
   __shared__ uint8_t s_gen[kThreads];
   __shared__ __align__(8) uint8_t s_id[kThreads * kMaxK];
   __shared__ uint8_t s_rk[kThreads * kMaxK];
+  __shared__ float s_w[ONE ? kThreads * kMaxK : 1];  // the choices' weights
   const int c = blockIdx.x;
   const int g = c / a.n_cpg, cc = c % a.n_cpg;
   const int t0 = g * a.Sg + cc * kThreads;
@@ -603,7 +604,8 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
     }
     if (on) {
       a.expert_id[int64_t(t0 + i) * k + j] = id;
-      a.gate[int64_t(t0 + i) * k + j] = w * sc.scale;
+      if (ONE) s_w[i * kMaxK + j] = w * sc.scale;
+      else a.gate[int64_t(t0 + i) * k + j] = w * sc.scale;
     }
     // the token's logsumexp^2, kept for the sum below
     __syncwarp();
@@ -723,16 +725,15 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
       const int slot = s_cnt[(j * nw + (i >> 5)) * E + e] + int(s_rk[i * kMaxK + j]);
       const bool in = a.C < 0 || slot < a.C;
       const int row = in ? s_first[e] + slot : -1;
-      const float w = a.gate[x];
+      const float w = s_w[i * kMaxK + j];
       a.pos[x] = in ? slot : -1;
       a.row[x] = row;
       a.drop[x] = in ? MOE_KEPT : MOE_DROP_CAPACITY;
       if (in) {
         a.token_of[row] = i;
         a.w_perm[row] = w;
-      } else {
-        a.gate[x] = 0.f;
       }
+      a.gate[x] = in ? w : 0.f;
     }
   }
 }
