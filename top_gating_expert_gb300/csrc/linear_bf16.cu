@@ -433,6 +433,7 @@ constexpr int kPairThreads = 64 + 32 * 8;
 struct PairArgs {
   int rows, cols, nkb, tiles_m, tiles_n;
   int a_mn, b_mn, res_vec, bias_vec;
+  int res_tma;  // the residual comes by TMA (16-byte rows; not beside a stored pre, which takes the boxes)
   int stream;  // outputs too large to be found in L2 again: stores marked evict-first
   LinearEpi e;
   unsigned* status;
@@ -444,8 +445,9 @@ struct PairCfg {
   static constexpr int B_BYTES = BN / 2 * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int BOXES = 8 * 2 * 2048;  // 8 warps x 2 boxes of 32 x 32 bf16
-  static constexpr int STAGES = (232448 - 1024 - BOXES - 256) / STAGE > 8 ? 8 : (232448 - 1024 - BOXES - 256) / STAGE;
-  static constexpr int SMEM = 1024 + STAGES * STAGE + BOXES + 256;
+  static constexpr int BARS = 512;
+  static constexpr int STAGES = (232448 - 1024 - BOXES - BARS) / STAGE > 8 ? 8 : (232448 - 1024 - BOXES - BARS) / STAGE;
+  static constexpr int SMEM = 1024 + STAGES * STAGE + BOXES + BARS;
   static constexpr int TMEM_COLS = 2 * BN;
 };
 
@@ -453,7 +455,7 @@ template <int BN>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmP,
-                       const PairArgs p) {
+                       const __grid_constant__ CUtensorMap tmR, const PairArgs p) {
   using C = PairCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -462,11 +464,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint8_t* sB = smem + C::STAGES * C::A_BYTES;
   uint8_t* sBox = sB + C::STAGES * C::B_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sBox + C::BOXES);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 5);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 5 + 16);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::STAGES;
   const uint32_t tfull0 = empty0 + 8 * C::STAGES, tempty0 = tfull0 + 16, drain_bar = tempty0 + 16;
+  const uint32_t res0 = drain_bar + 8;  // [8 warps][2 boxes]: a residual box has landed
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int unit = int(blockIdx.x >> 1), units = int(gridDim.x >> 1);
@@ -482,6 +485,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(tempty0 + 8 * a, 8 * 2);
     }
     mbar_init(drain_bar, 1);
+    for (int b = 0; b < 16; ++b) mbar_init(res0 + 8 * b, 1);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&tmA);
@@ -598,11 +602,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tempty_leader = cluster_addr(tempty0, 0);
     uint8_t* box = sBox + (warp - 2) * 4096;
-    int nb = 0;
+    int nb = 0;  // the box of the next 32 columns
     int i = 0;
-    auto put = [&](const CUtensorMap* map, const float (&v)[32], int col, int row) {
-      if (lane == 0) bulk_wait_read<1>();  // the store that last used this box has read it
-      __syncwarp();
+    // v (this lane's row, 32 columns) into box nb and out; the box's last store has been read
+    auto write_box = [&](const CUtensorMap* map, const float (&v)[32], int col, int row) {
       uint8_t* b = box + nb * 2048;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -618,30 +621,66 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       nb ^= 1;
     };
+    auto put = [&](const CUtensorMap* map, const float (&v)[32], int col, int row) {
+      if (lane == 0) bulk_wait_read<1>();  // the store that last used this box has read it
+      __syncwarp();
+      write_box(map, v, col, row);
+    };
+    // res_tma: the residual's 32 x 32 box is brought into the box that the sum will leave from, a
+    // step ahead (into box `b`, once every store so far has been read)
+    const uint32_t res_bar = res0 + 16 * uint32_t(warp - 2);
+    uint32_t res_phase = 0;  // bit b: phase of box b's barrier
+    bool res_open = false;   // a box has been asked for and not waited for
+    auto fetch_res = [&](int b, int col, int row) {
+      if (lane == 0) {
+        bulk_wait_read<0>();
+        mbar_expect_tx(res_bar + 8 * b, 2048);
+        tma_load_2d(smem_u32(box + b * 2048), &tmR, col, row, res_bar + 8 * b);
+      }
+      __syncwarp();
+      res_open = true;
+    };
     for (int t = unit; t < total; t += units, ++i) {
       const int acc = i & 1;
       const uint32_t use = uint32_t(i >> 1) & 1u;
       int m, n;
       decode(t, m, n);
+      const int row0 = m * 2 * BM + int(rank) * BM + 32 * q, row = row0 + lane;
+      const int cb = half * (BN / 2);
+      const bool rows_here = row0 < p.rows;
+      const int tile_col = n * BN;
+      const __nv_bfloat16* rp = static_cast<const __nv_bfloat16*>(p.e.res) + row * p.e.ldr;
+      if (p.res_tma && rows_here && tile_col + cb < p.cols) fetch_res(nb, tile_col + cb, row0);
       const bool ok = __all_sync(0xffffffffu, wait_bounded(tfull0 + 8 * acc, use, s_abort, p.status, wlimit));
       if (!ok) break;
       tc_fence_after();
-      const int row0 = m * 2 * BM + int(rank) * BM + 32 * q, row = row0 + lane;
       const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
-      const int cb = half * (BN / 2);
+      bool landed = true;
 #pragma unroll 1
       for (int c0 = cb; c0 < cb + BN / 2; c0 += 32) {
-        const int col = n * BN + c0;
-        if (row0 >= p.rows || col >= p.cols) break;  // warp-uniform: nothing of this part exists
+        const int col = tile_col + c0;
+        if (!rows_here || col >= p.cols) break;  // warp-uniform: nothing of this part exists
         uint32_t acc32[32];
         tmem_ld16(tbase + c0, *reinterpret_cast<uint32_t(*)[16]>(acc32));
         tmem_ld16(tbase + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(acc32 + 16));
-        const __nv_bfloat16* rp = static_cast<const __nv_bfloat16*>(p.e.res);
         uint4 rv[4];
-        const bool rvec = p.res_vec && row < p.rows && col + 32 <= p.cols;
-        if (rvec) {
+        const bool rvec = !p.res_tma && p.res_vec && row < p.rows && col + 32 <= p.cols;
+        if (p.res_tma) {
+          landed = __all_sync(0xffffffffu, wait_bounded(res_bar + 8 * nb, (res_phase >> nb) & 1u, s_abort,
+                                                        p.status, wlimit));
+          if (!landed) {
+            tmem_ld_wait();
+            break;
+          }
+          res_phase ^= 1u << nb;
+          res_open = false;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) rv[c] = *reinterpret_cast<const uint4*>(rp + row * p.e.ldr + col + 8 * c);
+          for (int c = 0; c < 4; ++c)
+            rv[c] = *reinterpret_cast<const uint4*>(box + nb * 2048 + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+          if (c0 + 32 < cb + BN / 2 && col + 32 < p.cols) fetch_res(nb ^ 1, col + 32, row0);
+        } else if (rvec) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) rv[c] = *reinterpret_cast<const uint4*>(rp + col + 8 * c);
         }
         float4 bv[8];  // the columns' biases, one address for the whole warp
         const bool bvec = p.bias_vec && col + 32 <= p.cols;
@@ -667,7 +706,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (p.e.pre) put(&tmP, v, col, row0);
         act_fast_all(p.e.act, v);
-        if (rvec) {
+        if (rvec || p.res_tma) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t w[4] = {rv[c].x, rv[c].y, rv[c].z, rv[c].w};
@@ -678,18 +717,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               v[8 * c + 2 * h + 1] += f.y;
             }
           }
-        } else if (rp && row < p.rows) {
+        } else if (p.e.res && row < p.rows) {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (col + j < p.cols) v[j] += __bfloat162float(rp[row * p.e.ldr + col + j]);
+            if (col + j < p.cols) v[j] += __bfloat162float(rp[col + j]);
         }
-        put(&tmY, v, col, row0);
+        if (p.res_tma) write_box(&tmY, v, col, row0);
+        else put(&tmY, v, col, row0);
       }
+      if (!landed) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8 * acc);
     }
-    if (lane == 0) bulk_wait_all();  // the boxes are read before shared memory goes away
+    if (lane == 0) {  // the boxes are read, and a box asked for has landed, before they go away
+      bulk_wait_all();
+      if (res_open) {
+        const int b = nb;  // before a tile: this box; inside one: the next
+        wait_drain(res_bar + 8 * b, (res_phase >> b) & 1u);
+      }
+    }
   }
 
   tc_fence_before();
@@ -721,12 +768,14 @@ template <int BN>
 int run_pair(const LinearOperand& A, const LinearOperand& B, int rows, int cols, int K, const LinearEpi& e,
              unsigned* status, cudaStream_t st) {
   using C = PairCfg<BN>;
-  CUtensorMap ta, tb, ty, tp;
+  CUtensorMap ta, tb, ty, tp, tr;
   int rc;
   if ((rc = map_operand(&ta, A, rows, K, BM)) != MOE_OK) return rc;
   if ((rc = map_operand(&tb, B, cols, K, BN / 2)) != MOE_OK) return rc;
   if ((rc = make_tma_map_out32(&ty, e.out, rows, cols, e.ldo)) != MOE_OK) return rc;
-  tp = ty;
+  tp = tr = ty;
+  const bool res_tma = e.res && !e.pre && out_aligned(e.res, e.ldr);
+  if (res_tma && (rc = make_tma_map_out32(&tr, const_cast<void*>(e.res), rows, cols, e.ldr)) != MOE_OK) return rc;
   if (e.pre && (rc = make_tma_map_out32(&tp, e.pre, rows, cols, e.ldp)) != MOE_OK) return rc;
   PairArgs p;
   p.rows = rows; p.cols = cols;
@@ -736,6 +785,7 @@ int run_pair(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
   if (int64_t(p.tiles_m) * p.tiles_n > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
   p.a_mn = A.mn; p.b_mn = B.mn;
   p.res_vec = e.res && out_aligned(e.res, e.ldr);
+  p.res_tma = res_tma;
   p.bias_vec = e.bias && reinterpret_cast<uintptr_t>(e.bias) % 16 == 0;
   p.stream = int64_t(rows) * cols * 2 * (e.pre ? 2 : 1) > (int64_t(96) << 20);
   p.e = e;
@@ -768,7 +818,7 @@ int run_pair(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     lc.numAttrs = 2;
   }
-  MOE_CUDA_CHECK(cudaLaunchKernelEx(&lc, kern, ta, tb, ty, tp, p));
+  MOE_CUDA_CHECK(cudaLaunchKernelEx(&lc, kern, ta, tb, ty, tp, tr, p));
   return MOE_OK;
 }
 
