@@ -104,4 +104,25 @@ __device__ __forceinline__ float block_sum_all(float v, float* s_red) {
   return r;
 }
 
+
+// Column sums of partial results: value(s, c) over s < n, for 32 columns from c0 on, by a CTA of 32
+// warps: each warp every 32nd s (a lane a column), then warp w joins column w's 32 sums. The order
+// depends on n alone. (Eight warps took twice the time: the loads of one warp are one chain.)
+template <typename Value, typename Store>
+__device__ __forceinline__ void column_sums(int n, int c0, int cols, float (*s_part)[33], Value&& value,
+                                            Store&& store) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float t = 0.f;
+  if (c0 + lane < cols) {
+#pragma unroll 8
+    for (int s = warp; s < n; s += 32) t += value(s, c0 + lane);
+  }
+  s_part[warp][lane] = t;
+  __syncthreads();
+  t = s_part[lane][warp];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+  if (lane == 0 && c0 + warp < cols) store(c0 + warp, t);
+}
+
 }  // namespace moe

@@ -73,26 +73,14 @@ __global__ void __launch_bounds__(kColThreads * kRowLanes)
   }
 }
 
-// out[c] = sum over the slices of part[s][c]: a CTA takes 32 columns, each of its eight warps every
-// eighth slice, then the warps' sums in order.
-__global__ void __launch_bounds__(256)
+// out[c] = sum over the slices of part[s][c]
+__global__ void __launch_bounds__(1024)
     linear_dbias_kernel(const float* __restrict__ part, int slices, int N, float* __restrict__ out) {
-  __shared__ float s_part[8][32];
+  __shared__ float s_part[32][33];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float s = 0.f;
-  if (c < N) {
-#pragma unroll 8
-    for (int i = warp; i < slices; i += 8) s += part[int64_t(i) * N + c];
-  }
-  s_part[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < N) {
-    for (int w = 1; w < 8; ++w) s += s_part[w][lane];
-    out[c] = s;
-  }
+  column_sums(slices, blockIdx.x * 32, N, s_part, [&](int s, int c) { return part[int64_t(s) * N + c]; },
+              [&](int c, float t) { out[c] = t; });
 }
 
 // Copies of up to two operands to 16-byte rows: dst [rows][ldd] = src [rows][cols], src on any
@@ -231,7 +219,7 @@ int launch_dact(const moe_linear_t& p, const void* dy, const void* pre, void* d,
                          static_cast<const T*>(pre), p.ldp, static_cast<T*>(d), ldd, p.T, p.N, slice, sums);
   });
   if (rc != MOE_OK || !dbias || slices == 1) return rc;
-  return launch_kernel(linear_dbias_kernel, dim3(unsigned((p.N + 31) / 32)), dim3(256), 0, st,
+  return launch_kernel(linear_dbias_kernel, dim3(unsigned((p.N + 31) / 32)), dim3(1024), 0, st,
                        static_cast<const float*>(part), slices, p.N, dbias);
 }
 

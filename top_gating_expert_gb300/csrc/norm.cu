@@ -142,29 +142,18 @@ __global__ void __launch_bounds__(kThreadsN)
   }
 }
 
-// dgamma and dbeta from the slices' partials [slices][2][cols]: a CTA takes 32 columns of one of
-// the two, each of its eight warps every eighth slice, then the warps' sums in order.
-__global__ void __launch_bounds__(kThreadsN)
+// dgamma (blockIdx.y 0) and dbeta (1) from the slices' partials [slices][2][cols].
+__global__ void __launch_bounds__(1024)
     norm_bwd_sum_kernel(const float* __restrict__ part, int slices, int cols, float* dgamma,
                         float* dbeta) {
-  __shared__ float s_part[kWarpsN][32];
+  __shared__ float s_part[32][33];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
   float* out = blockIdx.y ? dbeta : dgamma;
   if (!out) return;
-  float t = 0.f;
-  if (c < cols) {
-#pragma unroll 8
-    for (int s = warp; s < slices; s += kWarpsN) t += part[(int64_t(s) * 2 + blockIdx.y) * cols + c];
-  }
-  s_part[warp][lane] = t;
-  __syncthreads();
-  if (warp == 0 && c < cols) {
-    for (int w = 1; w < kWarpsN; ++w) t += s_part[w][lane];
-    out[c] = t;
-  }
+  column_sums(slices, blockIdx.x * 32, cols, s_part,
+              [&](int s, int c) { return part[(int64_t(s) * 2 + blockIdx.y) * cols + c]; },
+              [&](int c, float t) { out[c] = t; });
 }
 
 // Sum over the G warps of each row (warp = slot * G + wi), a fixed tree; every lane gets it.
@@ -767,7 +756,7 @@ int norm_forward_t(const moe_norm_t& n, const void* x, const void* residual, con
 }
 
 int launch_norm_sum(const float* part, int slices, int cols, float* dgamma, float* dbeta, cudaStream_t st) {
-  return launch_kernel(norm_bwd_sum_kernel, dim3(unsigned((cols + 31) / 32), 2), dim3(kThreadsN), 0, st, part,
+  return launch_kernel(norm_bwd_sum_kernel, dim3(unsigned((cols + 31) / 32), 2), dim3(1024), 0, st, part,
                        slices, cols, dgamma, dbeta);
 }
 
