@@ -5,7 +5,10 @@
  *   router projection -> softmax / top-k gates -> random 2nd-expert dispatch ->
  *   per-(group, expert) capacity slots -> expert-contiguous rows -> gather ->
  *   grouped expert FFN (GEMM1 + activation, GEMM2 + gate) -> combine back to token order,
- * plus the load-balancing (aux) loss and the router z-loss.
+ * plus the load-balancing (aux) loss and the router z-loss; its backward pass; and the
+ * operators around it in a Transformer block: routing by expert scores with a selection bias
+ * (moe_route_scored, moe_layer_*_scored), layer norm (moe_norm_*) and dense layers with bias,
+ * activation and residual (moe_linear_*), each with its gradient.
  *
  * Sources, by page title and section:
  *   GShard summary page ("GShard: Scaling Giant Models with Conditional Computation and
@@ -538,10 +541,11 @@ enum { MOE_LIN_NONE = 0, MOE_LIN_RELU = 1, MOE_LIN_GELU = 2, MOE_LIN_GELU_TANH =
  * layers, GShard "MoE Transformer"; Lec16 "DeepSeek V3 MoE": the first layers are dense):
  *     pre = x W^T (+ bias),  y = act(pre) (+ residual)
  * x [T, K], W [N, K], residual, y and pre [T, N] in the element type, bias float [N];
- * T >= 0, N >= 1, K >= 1, any size. Products are summed in fp32 and each output rounded once.
- * ld*: elements between rows (0: the row's length). bf16 runs on the tensor cores; operands
- * whose rows are not on 16-byte boundaries are copied into the workspace first. fp32 (the
- * plain-FMA path, meant for small layers).
+ * T >= 0, N >= 1, K >= 1, any size (MOE_ERR_UNSUPPORTED beyond T = 2^30, N or K = 2^22).
+ * Products are summed in fp32 and each output rounded once. ld*: elements between rows (0: the
+ * row's length). bf16 runs on the tensor cores (one token: plain FMA at the rate of memory);
+ * operands whose rows are not on 16-byte boundaries are copied into the workspace first, except
+ * for one token. fp32 is the plain-FMA path, meant for small layers.
  */
 typedef struct {
   int32_t T, N, K;

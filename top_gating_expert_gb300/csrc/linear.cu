@@ -13,7 +13,8 @@ constexpr int kColThreads = 32, kRowLanes = 8;
 
 // d = dy act'(pre) (written to d when it is given) and the partial column sums of the
 // unrounded d over a slice of rows: part[slice][N]. CTA: 32 threads of VEC columns by 8 row
-// lanes; the lanes' sums are added in order.
+// lanes; the lanes' sums are added in order. 16384 x 4096 bf16, gelu: 76 us for 403 MB (0.78 of the
+// copy rate); four rows in flight a lane instead of two cost registers and 15 us.
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kColThreads * kRowLanes)
     linear_dact_kernel(const T* __restrict__ dy, int64_t ldy, const T* __restrict__ pre, int64_t ldp,

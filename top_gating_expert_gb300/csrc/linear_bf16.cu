@@ -15,10 +15,12 @@
 //   warps 2..5  move the finished accumulator into shared memory (over the drained ring)
 //   all warps   epilogue: contiguous runs of an output row, 4 columns a thread
 // With few rows (a serving step) the roles are exchanged (TRANS): the 128-row side is W and
-// the narrow side the tokens, so the MMA's M is full and the kernel streams W at the rate of
-// memory. When the tiles are fewer than the SMs, K is split over the CTAs of a cluster;
+// the narrow side the tokens, so the MMA's M is full and the kernel streams W. When the tiles are fewer than the SMs, K is split over the CTAs of a cluster;
 // each then sums its share of the tile over the cluster's shared memories in split order, so
 // the result does not depend on timing and no scratch in memory is needed.
+// 777 x 1408 x 2048 (77 tiles, 32 k-blocks): 16 us, a k-block 0.28 us where the MMAs would take
+// 0.16: bound by the operands' way from L2 (32 KB a k-block for 128 x 128 outputs). 64 x 14336 x
+// 4096: 27 us, W at 4.3 TB/s on 112 of the 152 SMs.
 //
 // Every wait is bounded, as in the grouped GEMM: a role that gives up sets the status word
 // and the CTA's abort flag, the loads and MMAs in flight are drained, TMEM is freed.
@@ -426,7 +428,12 @@ int run_tile(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
 //               box in shared memory and out by a TMA store (two boxes a warp in turn). The
 //               next tile's MMAs run meanwhile.
 // Tiles are walked in bands of kBand tile rows, column by column, so that the tiles in
-// flight share their operands through L2.
+// flight share their operands through L2 (bands of 8 the same, 4 and 32 slower by 3 and 11 %).
+//
+// Measured: 8192 x 14336 x 4096 without epilogue 550 us (1.75 PFLOP/s, the library's product 542; 1.01
+// of the sustained rate); bias adds 9 us, gelu 19 and the stored pre 21 (235 MB more), 607 us
+// in all (0.92 of the sustained rate, the tensor pipe 84 % active in a capture). The backward's
+// products at 16384 x 4096 x 1024 take 87 us each: 256 and 64 tiles fill 76 pairs to 84 %.
 constexpr int kBand = 16;
 constexpr int kPairThreads = 64 + 32 * 8;
 

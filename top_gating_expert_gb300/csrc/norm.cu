@@ -21,6 +21,12 @@
 // Register kernels (norm_fwd_kernel, norm_bwd_kernel): the same without the ring, for few rows
 // (one vector a lane, more warps a row: latency) and for rows that no cp.async fits. Rows too long
 // for either take the *_any kernels, which walk a row again from cache.
+//
+// Measured (copy rate 6778 GB/s): 65536 x 1024 bf16 with residual and the sum stored, 537 MB, 95 us
+// (0.83 of it; without the ring 109 us); 16384 x 4096 bf16 backward with dh, 537 MB, 101 us (0.78;
+// 250 us in registers alone, one row of 16 warps at a time, bound by its latency; now 72 % of the
+// issue slots are taken); 65536 x 64 forward 6.6 us, backward 10 us (21 and 24 with a warp a row).
+// bf16 rows on no 4-byte boundary run at a sixth of the copy rate (2-byte loads).
 #include <algorithm>
 
 #include "elem.cuh"
