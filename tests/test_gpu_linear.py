@@ -255,19 +255,22 @@ def test_large_offsets(native_lib):
     assert torch.equal(n, block.layer_norm(x.contiguous(), gamma)[0])
 
 
-def test_stalled_pipeline_reports_a_timeout(native_lib):
+@pytest.mark.parametrize("T,N,K,residual", [(600, 1024, 2048, False), (20, 4096, 2048, True), (2600, 1800, 1912, True)])
+def test_stalled_pipeline_reports_a_timeout(native_lib, T, N, K, residual):
     """A wait limit of 1 ns: the kernel gives up (or finishes at once), frees what it holds and
     the next call with the default limit is right."""
     from top_gating_expert_gb300 import moe
-    gen, dt, x, W, bias = make(600, 1024, 2048, "bf16", 0, 0, 12)
-    good, _ = block.linear(x, W, bias)
-    ws = block.linear_workspace(600, 1024, 2048)
-    moe.set_wait_limit(ws, 1)
-    block.linear(x, W, bias, ws=ws)
-    assert moe.device_status(ws) in (0, -5)
-    moe.set_wait_limit(ws, 0)
-    y, _ = block.linear(x, W, bias, ws=ws)
-    assert moe.device_status(ws) == 0 and torch.equal(y, good)
+    gen, dt, x, W, bias = make(T, N, K, "bf16", 0, 0, 12)
+    res = strided(T, N, 0, 0, dt, gen) if residual else None
+    good, _ = block.linear(x, W, bias, residual=res)
+    ws = block.linear_workspace(T, N, K)
+    for _ in range(3):
+        moe.set_wait_limit(ws, 1)
+        block.linear(x, W, bias, residual=res, ws=ws)
+        assert moe.device_status(ws) in (0, -5)
+        moe.set_wait_limit(ws, 0)
+        y, _ = block.linear(x, W, bias, residual=res, ws=ws)
+        assert moe.device_status(ws) == 0 and torch.equal(y, good)
 
 
 @pytest.mark.parametrize("shape", [(2600, 1800, 1912), (2511, 1803, 1901), (4096, 2304, 1280), (20000, 136, 2056)])

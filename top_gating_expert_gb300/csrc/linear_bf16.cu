@@ -473,6 +473,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sBox + C::BOXES);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 5 + 16);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  volatile uint32_t* s_peer = s_tmem + 2;  // written by the other CTA at its end: k-blocks loaded, gave up
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::STAGES;
   const uint32_t tfull0 = empty0 + 8 * C::STAGES, tempty0 = tfull0 + 16, drain_bar = tempty0 + 16;
@@ -516,7 +517,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     m = band * kBand + r - n * gm;
   };
 
-  uint32_t issued = 0, issued_par = 0;
+  uint32_t issued = 0;  // warp 0: k-blocks loaded
   bool mma_any = false, mma_drained = false;
   if (warp == 0) {
     int stage = 0;
@@ -548,8 +549,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         }
         __syncwarp();
-        issued |= 1u << stage;
-        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        ++issued;
         if (++stage == C::STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -748,19 +748,36 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (*s_abort) {
-    // loads issued land and MMAs issued finish before shared and tensor memory go away
-    if (warp == 0 && leader && lane == 0)
-      for (int s = 0; s < C::STAGES; ++s)
-        if ((issued >> s) & 1u) wait_drain(full0 + 8 * s, (issued_par >> s) & 1u);
+  if (warp == 0 && lane == 0) {
+    const uint32_t peer = cluster_addr(smem_u32(const_cast<uint32_t*>(s_peer)), rank ^ 1u);
+    st_cluster_u32(peer, issued);
+    st_cluster_u32(peer + 4, uint32_t(*s_abort));
+  }
+  __syncwarp();
+  cluster_sync_all();  // both CTAs done with TMEM and each other's barriers
+  if (*s_abort || s_peer[1]) {
+    // One CTA gave up: loads issued land and MMAs issued finish before shared and tensor memory
+    // go away. The CTAs' producers are at most a use of each stage apart; the even CTA's full
+    // barriers count both CTAs' bytes, so for a k-block that only one of them loaded the other's
+    // part is settled first (its bytes taken as come, or the arrival that it would have made).
+    if (warp == 0 && leader && lane == 0) {
+      const uint32_t theirs = s_peer[0], lo = min(issued, theirs), hi = max(issued, theirs);
+      for (uint32_t j = lo; j < hi; ++j) {
+        const uint32_t fb = full0 + 8 * (j % C::STAGES);
+        if (issued > theirs) mbar_complete_tx(fb, C::STAGE);
+        else mbar_expect_tx(fb, C::STAGE);
+      }
+      for (uint32_t j = hi > C::STAGES ? hi - C::STAGES : 0; j < hi; ++j)
+        wait_drain(full0 + 8 * (j % C::STAGES), (j / C::STAGES) & 1u);
+    }
     if (warp == 1 && leader && lane == 0 && mma_any && !mma_drained) {
       mma_commit_pair(drain_bar, uint16_t(1));
       wait_drain(drain_bar, 0u);
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();
   }
-  cluster_sync_all();  // both CTAs done with TMEM and each other's barriers
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, C::TMEM_COLS);
