@@ -183,6 +183,37 @@ def test_constant_rows_and_non_finite_values(native_lib, M):
     check_forward(x[ok], None, gamma, beta, 1e-5, (y[ok], None, mean[ok], rstd[ok]), torch.float32)
 
 
+def among(rows, cols, pad, offset, dtype, gen, fill):
+    """(whole buffer, [rows, cols] view of normal values) with `fill` everywhere between the rows."""
+    full = torch.full((offset + rows * (cols + pad) + 8,), fill, dtype=dtype, device="cuda")
+    view = full[offset:].as_strided((rows, cols), (cols + pad, 1))
+    view.copy_(torch.randn((rows, cols), generator=gen, device="cuda"))
+    return full, view
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(700, 3), (700, 37), (700, 300), (500, 1003), (400, 2051), (320, 4100), (310, 9001)])
+@pytest.mark.parametrize("where", [(5, 1, 2, 3), (1, 0, 3, 7), (2, 6, 0, 1), (0, 5, 4, 0)])
+def test_nothing_beside_the_rows_is_used_or_written(native_lib, dtype, shape, where):
+    """Every operand on a boundary of its own, NaN between the rows and around them: the results are
+    those of operands by themselves, and what lies beside the outputs' rows keeps its value."""
+    (T, M), (pad, ox, orr, oy), dt = shape, where, DT[dtype]
+    gen, nan = generator(T + M), float("nan")
+    x, res = among(T, M, pad, ox, dt, gen, nan)[1], among(T, M, pad, orr, dt, gen, nan)[1]
+    (ybuf, y), (hbuf, h) = among(T, M, pad, oy, dt, gen, 7.0), among(T, M, pad, ox, dt, gen, 7.0)
+    gamma, beta = 1 + 0.3 * torch.randn(M, generator=gen, device="cuda"), torch.randn(M, generator=gen, device="cuda")
+    got = block.layer_norm(x, gamma, beta, residual=res, out=y, h=h)
+    check_forward(x, res, gamma, beta, 1e-5, got, dt)
+    dy = among(T, M, pad, orr, dt, gen, nan)[1]
+    mean, rstd = stats(x)
+    dbuf, dx = among(T, M, pad, oy, dt, gen, 7.0)
+    back = block.layer_norm_backward(dy, x, gamma, mean, rstd, res, dx=dx)
+    check_backward(dy, x, gamma, mean, rstd, res, back, dt)
+    for buf, view, off in ((ybuf, y, oy), (hbuf, h, ox), (dbuf, dx, oy)):
+        view.fill_(7.0)
+        assert (buf == 7.0).all(), f"written beside the rows (offset {off})"
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("M", [1003, 1024, 4096])
 def test_in_place(native_lib, dtype, M):

@@ -18,26 +18,20 @@
 // keeps the column sums of dgamma and dbeta there too (a column belongs to the same lane in
 // every row), so dy and h are read once for all three results. The CTAs' partial sums are added
 // by norm_bwd_sum_kernel in CTA order.
-// Register kernels (norm_fwd_kernel, norm_bwd_kernel): the same without the ring, for few rows
-// (one vector a lane, more warps a row: latency) and for rows that no cp.async fits. Rows too long
-// for either take the *_any kernels, which walk a row again from cache.
+// Rows on no 16-byte boundary: norm_odd.cu. norm_fwd_kernel, in registers without the ring, is for few
+// rows (one vector a lane, more warps a row: latency). Rows too long for any of these take the *_any
+// kernels, which walk a row again from cache.
 //
 // Measured (copy rate 6778 GB/s): 65536 x 1024 bf16 with residual and the sum stored, 537 MB, 95 us
 // (0.83 of it; without the ring 109 us); 16384 x 4096 bf16 backward with dh, 537 MB, 101 us (0.78;
 // 250 us in registers alone, one row of 16 warps at a time, bound by its latency; now 72 % of the
 // issue slots are taken); 65536 x 64 forward 6.6 us, backward 10 us (21 and 24 with a warp a row).
-// bf16 rows on no 4-byte boundary run at a sixth of the copy rate (2-byte loads).
 #include <algorithm>
 
-#include "elem.cuh"
-#include "internal.h"
+#include "norm_ring.cuh"
 
 namespace moe {
 namespace {
-
-// makes a generic lambda's statics one per kernel
-template <int N>
-struct Tag {};
 
 constexpr int kThreadsN = 256;
 constexpr int kWarpsN = kThreadsN / 32;
@@ -76,11 +70,6 @@ __global__ void __launch_bounds__(kThreadsN)
     if (rstd) rstd[r] = rs;
   }
 }
-
-// g = dy gamma, rounded: contracted into the sum and into g - mean(g) as multiply-adds, the two
-// uses would see different values, and a difference that is exactly zero (one column) would
-// leave a rounding error times rstd.
-__device__ __forceinline__ float product(float a, float b) { return __fmul_rn(a, b); }
 
 // One CTA a row: the two row sums, then dx.
 template <typename T>
@@ -248,164 +237,7 @@ __global__ void __launch_bounds__(512)
   }
 }
 
-// part: [gridDim.x][2][cols], null when neither dgamma nor dbeta is wanted.
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(512)
-    norm_bwd_kernel(const T* dy, const T* __restrict__ h, const float* __restrict__ gamma,
-                    const float* __restrict__ mean, const float* __restrict__ rstd, const T* dh, T* dx,
-                    float* __restrict__ part, int G, moe_norm_t n) {
-  __shared__ float s_red[4][16];
-  extern __shared__ float s_cols[];  // [slots][G * 32 * VEC * NV], one of the two sums at a time
-  pdl_wait();
-  pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slots = (blockDim.x >> 5) / G, slot = warp / G;
-  const int M = n.cols, step = G * 32 * VEC;
-  const int c0 = (warp % G * 32 + lane) * VEC;
-  const float inv_m = 1.f / float(M);
-  float g[NV][VEC], sg[NV][VEC], sb[NV][VEC];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) g[i][q] = sg[i][q] = sb[i][q] = 0.f;
-    if (c0 + i * step < M) load_floats<VEC>(gamma + c0 + i * step, g[i]);
-  }
-  Vec<T, VEC> hv[NV], dv[NV];
-  float mu = 0.f, rs = 0.f;
-  auto fetch = [&](int64_t r) {
-    if (r >= n.rows) return;
-    mu = __ldg(mean + r);
-    rs = __ldg(rstd + r);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = c0 + i * step;
-      if (c < M) {
-        hv[i] = load_vec<T, VEC>(h + r * n.ldx + c);
-        dv[i] = load_vec<T, VEC>(dy + r * n.ldy + c);
-      }
-    }
-  };
-  const int64_t stride = int64_t(gridDim.x) * slots;
-  int64_t r = int64_t(blockIdx.x) * slots + slot;
-  fetch(r);
-  int buf = 0;
-  for (int64_t r0 = int64_t(blockIdx.x) * slots; r0 < n.rows; r0 += stride, r += stride, buf ^= 2) {
-    const bool on = r < n.rows;
-    const float rstd_r = rs;
-    float xh[NV][VEC], gd[NV][VEC];
-    Vec<T, VEC> ev[NV];
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = c0 + i * step;
-      if (on && c < M) {
-        if (dh) ev[i] = load_vec<T, VEC>(dh + r * n.ldr + c);
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-          const float d = to_f32(dv[i].v[q]);
-          xh[i][q] = (to_f32(hv[i].v[q]) - mu) * rs;
-          gd[i][q] = product(d, g[i][q]);
-          sg[i][q] = fmaf(d, xh[i][q], sg[i][q]);
-          sb[i][q] += d;
-          s1 += gd[i][q];
-          s2 = fmaf(gd[i][q], xh[i][q], s2);
-        }
-      }
-    }
-    fetch(r + stride);  // the next row, while this one's sums cross the warps
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      s1 += __shfl_xor_sync(0xffffffffu, s1, off);
-      s2 += __shfl_xor_sync(0xffffffffu, s2, off);
-    }
-    if (G > 1) {
-      if (lane == 0) {
-        s_red[buf][warp] = s1;
-        s_red[buf + 1][warp] = s2;
-      }
-      __syncthreads();
-      s1 = s_red[buf][slot * G + (lane & (G - 1))];
-      s2 = s_red[buf + 1][slot * G + (lane & (G - 1))];
-      for (int off = G >> 1; off > 0; off >>= 1) {
-        s1 += __shfl_xor_sync(0xffffffffu, s1, off);
-        s2 += __shfl_xor_sync(0xffffffffu, s2, off);
-      }
-    }
-    s1 *= inv_m;
-    s2 *= inv_m;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = c0 + i * step;
-      if (on && c < M) {
-        Vec<T, VEC> o;
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-          float v = rstd_r * (gd[i][q] - s1 - xh[i][q] * s2);
-          if (dh) v += to_f32(ev[i].v[q]);
-          o.v[q] = from_f32<T>(v);
-        }
-        store_vec<T, VEC>(dx + r * n.ldh + c, o);
-      }
-    }
-  }
-  if (!part) return;
-  // the slots' column sums, added in slot order
-  const int width = step * NV;
-  float* out = part + int64_t(blockIdx.x) * 2 * M;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) s_cols[slot * width + c0 + i * step + q] = which ? sb[i][q] : sg[i][q];
-    __syncthreads();
-    for (int c = threadIdx.x; c < M; c += blockDim.x) {
-      float t = 0.f;
-      for (int w = 0; w < slots; ++w) t += s_cols[w * width + c];
-      out[which * M + c] = t;
-    }
-  }
-}
-
 // ------------------------------------------------------------------ ring kernels
-constexpr int kRingWarps = 16;
-
-// BYTES (16 or 4) of this lane, global to shared, and the groups of such copies.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* dst, const void* src) {
-  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// Sum of v over the L lanes of a row (a power of two: lanes of one warp, or L / 32 whole warps,
-// which then meet at a barrier of their slot's own; s_red: one float a warp of the row, free until
-// its next barrier but one). A fixed tree, every lane gets it; all lanes of a warp take part.
-template <bool SUB>  // SUB: L < 32
-__device__ __forceinline__ float row_lanes_sum(float v, int L, int slot, float* s_red) {
-  if constexpr (SUB) {
-    for (int off = L >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
-  } else {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    const int G = L >> 5;
-    if (G == 1) return v;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) s_red[(threadIdx.x >> 5) & (G - 1)] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(L) : "memory");
-    v = s_red[lane & (G - 1)];
-    for (int off = G >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
-  }
-}
-
-constexpr int kFwdStages = 3;
-
 template <typename T, int VEC, int NV, bool SUB = false>
 __global__ void __launch_bounds__(32 * kRingWarps, 1)
     norm_fwd_ring_kernel(const T* x, const T* res, const float* __restrict__ gamma,
@@ -441,8 +273,8 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
       for (int i = 0; i < NV; ++i) {
         const int c = c0 + i * step;
         if (c < M) {
-          copy_async<BYTES>(piece(stage, 0, i), x + r * n.ldx + c);
-          if (res) copy_async<BYTES>(piece(stage, 1, i), res + r * n.ldr + c);
+          copy_async(piece(stage, 0, i), x + r * n.ldx + c);
+          if (res) copy_async(piece(stage, 1, i), res + r * n.ldr + c);
         }
       }
     }
@@ -546,9 +378,9 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
       for (int i = 0; i < NV; ++i) {
         const int c = c0 + i * step;
         if (c < M) {
-          copy_async<BYTES>(piece(stage, 0, i), h + r * n.ldx + c);
-          copy_async<BYTES>(piece(stage, 1, i), dy + r * n.ldy + c);
-          if (dh) copy_async<BYTES>(piece(stage, 2, i), dh + r * n.ldr + c);
+          copy_async(piece(stage, 0, i), h + r * n.ldx + c);
+          copy_async(piece(stage, 1, i), dy + r * n.ldy + c);
+          if (dh) copy_async(piece(stage, 2, i), dh + r * n.ldr + c);
         }
       }
     }
@@ -669,8 +501,7 @@ int check_norm(const moe_norm_t* n) {
   return MOE_OK;
 }
 
-// The slices of rows that are not held whole share 2048 CTAs; the ring and register kernels write
-// at most kMaxSlices, one an SM (ring) where rows are longer than 8192.
+// The slices of rows that are not held whole share 2048 CTAs; the ring kernels write one an SM.
 int any_slices(int cols) { return std::max(1, std::min(kMaxSlices, 2048 / ((cols + kSliceCols - 1) / kSliceCols))); }
 size_t norm_ws_bytes(const moe_norm_t& n) {
   const int slices = n.cols <= 8192 ? kMaxSlices : std::max(any_slices(n.cols), 160);
@@ -681,21 +512,6 @@ bool vec_ok(const void* p, int64_t ld, int vec, size_t eb) {
   return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % vec == 0 && eb * vec == 16);
 }
 
-// Warps a row (a power of two up to most) so that NV vectors a lane hold it; 0: too long.
-int row_warps(int cols, int vec, int nv, int most = 16) {
-  int G = 1;
-  while (G <= most && int64_t(G) * 32 * vec * nv < cols) G *= 2;
-  return G <= most ? G : 0;
-}
-
-// Lanes a row: 32 G, or a part of a warp for short rows (several rows a warp).
-int row_lanes(int cols, int vec, int nv, int G) {
-  int L = 32 * G;
-  if (G == 1 && nv == 1)
-    while (L > 1 && (L / 2) * vec >= cols) L /= 2;
-  return L;
-}
-
 template <typename T, int VEC>
 int norm_forward_v(const moe_norm_t& n, const T* x, const T* res, const float* gamma, const float* beta,
                    T* h, T* y, float* mean, float* rstd, cudaStream_t st) {
@@ -703,11 +519,15 @@ int norm_forward_v(const moe_norm_t& n, const T* x, const T* res, const float* g
   // 32 floats a lane
   constexpr int kMost = VEC == 8 ? 4 : 8;
   const bool few = n.rows <= 2 * num_sms();
-  if constexpr (VEC * sizeof(T) >= 4) {
-    constexpr int kRing = VEC == 1 ? 8 : 4;  // what shared memory holds
+  if constexpr (VEC == 1) {
+    if ((!few || !row_warps(n.cols, VEC, kMost)) && norm_odd_fits<T>(n.cols))
+      return norm_forward_odd<T>(n, x, res, gamma, beta, h, y, mean, rstd, st);
+  } else {
+    constexpr int kRing = 4;  // what shared memory holds
     int nv = 1;
     int G = row_warps(n.cols, VEC, nv, 1);
     while (G == 0 && nv < kRing) G = row_warps(n.cols, VEC, nv *= 2, nv == kRing ? 16 : 1);
+    if (G) spread_rows(n.rows, nv, G);
     if (!few && G) {
       const int L = row_lanes(n.cols, VEC, nv, G), slots = 32 * kRingWarps / L;
       const unsigned grid = unsigned(std::min<int64_t>((n.rows + slots - 1) / slots, num_sms()));
@@ -725,7 +545,6 @@ int norm_forward_v(const moe_norm_t& n, const T* x, const T* res, const float* g
         case 2: return go(norm_fwd_ring_kernel<T, VEC, 2>, Tag<2>{});
         case 4: return go(norm_fwd_ring_kernel<T, VEC, 4>, Tag<4>{});
       }
-      if constexpr (kRing == 8) return go(norm_fwd_ring_kernel<T, VEC, 8>, Tag<8>{});
     }
   }
   int nv = few ? 1 : kMost;
@@ -766,82 +585,69 @@ int launch_norm_sum(const float* part, int slices, int cols, float* dgamma, floa
                        slices, cols, dgamma, dbeta);
 }
 
-template <typename T, int VEC>
+// CTAs that wrote a partial to part: *slices
+template <typename T>
+int norm_backward_ring(const moe_norm_t& n, const T* dy, const T* h, const float* gamma, const float* mean,
+                       const float* rstd, const T* dh, T* dx, float* part, int nv, int G, int* slices,
+                       cudaStream_t st) {
+  constexpr int VEC = 16 / int(sizeof(T));
+  const int L = row_lanes(n.cols, VEC, nv, G), slots = 32 * kRingWarps / L;
+  const int grid = int(std::min<int64_t>((n.rows + slots - 1) / slots, std::min(num_sms(), 160)));
+  *slices = grid;
+  auto go = [&](auto kern, int stages, auto) -> int {
+    const size_t ring = size_t(stages) * (dh ? 3 : 2) * nv * 32 * kRingWarps * VEC * sizeof(T);
+    const size_t cols = size_t(kRingWarps) * 32 * VEC * nv * 4;
+    const size_t smem = std::max(ring, part ? cols : size_t(0));
+    const size_t most = std::max(size_t(stages) * 3 * nv * 32 * kRingWarps * VEC * sizeof(T), cols);
+    static std::atomic<unsigned long long> seen{0};
+    if (const int rc = allow_smem(reinterpret_cast<const void*>(kern), int(most), seen)) return rc;
+    return launch_kernel(kern, dim3(unsigned(grid)), dim3(32 * kRingWarps), smem, st, dy, h, gamma, mean, rstd,
+                         dh, dx, part, L, n);
+  };
+  switch (nv) {
+    case 1: return L < 32 ? go(norm_bwd_ring_kernel<T, VEC, 1, 3, true>, 3, Tag<0>{})
+                          : go(norm_bwd_ring_kernel<T, VEC, 1, 3>, 3, Tag<1>{});
+    case 2: return go(norm_bwd_ring_kernel<T, VEC, 2, 3>, 3, Tag<2>{});
+  }
+  return go(norm_bwd_ring_kernel<T, VEC, 4, 2>, 2, Tag<4>{});
+}
+
+template <typename T, bool ALIGNED>
 int norm_backward_v(const moe_norm_t& n, const T* dy, const T* h, const float* gamma, const float* mean,
                     const float* rstd, const T* dh, T* dx, float* dgamma, float* dbeta, float* part,
                     cudaStream_t st) {
-  int rc;
+  constexpr int VEC = 16 / int(sizeof(T));
+  int rc, slices = 0;
   const bool sums = dgamma || dbeta;
-  if constexpr (VEC * sizeof(T) >= 4) {
-    // more vectors a lane before more warps a row, up to 16 columns a lane (32 column sums and
-    // 16 of gamma: no spills); twice that for the longest bf16 rows (for fp32 vectors shared memory
-    // does not hold it). Three stages, two where they would not fit
-    constexpr int kMore = VEC == 8 ? 2 : (VEC == 4 ? 4 : 8), kRing = VEC == 8 ? 4 : kMore;
-    int nv = 1;
-    int G = row_warps(n.cols, VEC, nv, 1);
-    while (G == 0 && nv < kRing) G = row_warps(n.cols, VEC, nv *= 2, nv >= kMore ? 16 : 1);
-    if (G) {
-      const int L = row_lanes(n.cols, VEC, nv, G), slots = 32 * kRingWarps / L;
-      const int grid = int(std::min<int64_t>((n.rows + slots - 1) / slots, std::min(num_sms(), 160)));
-      auto go = [&](auto kern, int stages, auto) -> int {
-        const size_t ring = size_t(stages) * (dh ? 3 : 2) * nv * 32 * kRingWarps * VEC * sizeof(T);
-        const size_t cols = size_t(kRingWarps) * 32 * VEC * nv * 4;
-        const size_t smem = std::max(ring, sums ? cols : size_t(0));
-        const size_t most = std::max(size_t(stages) * 3 * nv * 32 * kRingWarps * VEC * sizeof(T), cols);
-        static std::atomic<unsigned long long> seen{0};
-        if (const int rc = allow_smem(reinterpret_cast<const void*>(kern), int(most), seen)) return rc;
-        return launch_kernel(kern, dim3(unsigned(grid)), dim3(32 * kRingWarps), smem, st, dy, h, gamma, mean, rstd,
-                             dh, dx, sums ? part : nullptr, L, n);
-      };
-      rc = MOE_ERR_UNSUPPORTED;
-      if (nv == 1)
-        rc = L < 32 ? go(norm_bwd_ring_kernel<T, VEC, 1, 3, true>, 3, Tag<0>{})
-                    : go(norm_bwd_ring_kernel<T, VEC, 1, 3>, 3, Tag<1>{});
-      if (nv == 2) rc = go(norm_bwd_ring_kernel<T, VEC, 2, 3>, 3, Tag<2>{});
-      if (nv == 4) rc = go(norm_bwd_ring_kernel<T, VEC, 4, VEC == 1 ? 3 : 2>, VEC == 1 ? 3 : 2, Tag<4>{});
-      if constexpr (kRing == 8) {
-        if (nv == 8) rc = go(norm_bwd_ring_kernel<T, VEC, 8, 2>, 2, Tag<8>{});
-      }
-      if (rc != MOE_OK || !sums) return rc;
-      return launch_norm_sum(part, grid, n.cols, dgamma, dbeta, st);
-    }
-  }
+  // more vectors a lane before more warps a row, up to 16 columns a lane (32 column sums and 16 of
+  // gamma: no spills); twice that for the longest bf16 rows (for fp32 vectors shared memory does not
+  // hold it). Three stages, two where they would not fit
+  constexpr int kMore = VEC == 8 ? 2 : 4;
   int nv = 1;
-  constexpr int kMost = VEC == 1 ? 8 : 1;
-  int G = row_warps(n.cols, VEC, nv);
-  while (G == 0 && nv < kMost) G = row_warps(n.cols, VEC, nv *= 2);
-  if (G == 0) {  // too long for the registers: the column sums first (dx may be written over dy)
-    if (sums) {
-      const int cblocks = (n.cols + kSliceCols - 1) / kSliceCols;
-      int slices = std::min(any_slices(n.cols), (n.rows + kWarpsN - 1) / kWarpsN);
-      const int slice = (n.rows + slices - 1) / slices;
-      slices = (n.rows + slice - 1) / slice;
-      if ((rc = launch_kernel(norm_bwd_cols_any_kernel<T>, dim3(unsigned(cblocks), unsigned(slices)),
-                              dim3(kThreadsN), 0, st, dy, h, mean, rstd, part, slice, n)) != MOE_OK)
-        return rc;
-      if ((rc = launch_norm_sum(part, slices, n.cols, dgamma, dbeta, st)) != MOE_OK) return rc;
-    }
-    return launch_kernel(norm_bwd_dx_any_kernel<T>, dim3(unsigned(n.rows)), dim3(kThreadsN), 0, st, dy, h,
-                         gamma, mean, rstd, dh, dx, n);
+  int G = row_warps(n.cols, VEC, nv, 1);
+  while (G == 0 && nv < 4) G = row_warps(n.cols, VEC, nv *= 2, nv >= kMore ? 16 : 1);
+  if (G) {
+    float* const to = sums ? part : nullptr;
+    if constexpr (ALIGNED)
+      rc = norm_backward_ring<T>(n, dy, h, gamma, mean, rstd, dh, dx, to, nv, G, &slices, st);
+    else
+      rc = norm_backward_odd<T>(n, dy, h, gamma, mean, rstd, dh, dx, to, nv, G, &slices, st);
+    if (rc != MOE_OK || !sums) return rc;
+    return launch_norm_sum(part, slices, n.cols, dgamma, dbeta, st);
   }
-  const int warps = std::max(G, 8), slots = warps / G;
-  const int per_sm = 64 / warps > 4 ? 4 : (64 / warps > 2 ? 64 / warps : 2);
-  const int64_t need = (int64_t(n.rows) + slots - 1) / slots;
-  const int grid = int(std::min<int64_t>(need, std::min(kMaxSlices, per_sm * num_sms())));
-  const size_t smem = sums ? size_t(warps) * 32 * VEC * nv * 4 : 0;
-  auto go = [&](auto kern) -> int {  // at most 16 KB
-    return launch_kernel(kern, dim3(unsigned(grid)), dim3(unsigned(32 * warps)), smem, st, dy, h, gamma, mean, rstd,
-                         dh, dx, sums ? part : nullptr, G, n);
-  };
-  rc = MOE_ERR_UNSUPPORTED;
-  if (nv == 1) rc = go(norm_bwd_kernel<T, VEC, 1>);
-  if constexpr (kMost == 8) {
-    if (nv == 2) rc = go(norm_bwd_kernel<T, VEC, 2>);
-    if (nv == 4) rc = go(norm_bwd_kernel<T, VEC, 4>);
-    if (nv == 8) rc = go(norm_bwd_kernel<T, VEC, 8>);
+  // too long for the registers: the column sums first (dx may be written over dy)
+  if (sums) {
+    const int cblocks = (n.cols + kSliceCols - 1) / kSliceCols;
+    slices = std::min(any_slices(n.cols), (n.rows + kWarpsN - 1) / kWarpsN);
+    const int slice = (n.rows + slices - 1) / slices;
+    slices = (n.rows + slice - 1) / slice;
+    if ((rc = launch_kernel(norm_bwd_cols_any_kernel<T>, dim3(unsigned(cblocks), unsigned(slices)),
+                            dim3(kThreadsN), 0, st, dy, h, mean, rstd, part, slice, n)) != MOE_OK)
+      return rc;
+    if ((rc = launch_norm_sum(part, slices, n.cols, dgamma, dbeta, st)) != MOE_OK) return rc;
   }
-  if (rc != MOE_OK || !sums) return rc;
-  return launch_norm_sum(part, grid, n.cols, dgamma, dbeta, st);
+  return launch_kernel(norm_bwd_dx_any_kernel<T>, dim3(unsigned(n.rows)), dim3(kThreadsN), 0, st, dy, h, gamma,
+                       mean, rstd, dh, dx, n);
 }
 
 template <typename T>
@@ -855,8 +661,8 @@ int norm_backward_t(const moe_norm_t& n, const void* dy, const void* h, const fl
   const T *dyt = static_cast<const T*>(dy), *ht = static_cast<const T*>(h), *dht = static_cast<const T*>(dh);
   T* dxt = static_cast<T*>(dx);
   float* part = reinterpret_cast<float*>(ws + 256);
-  return vec ? norm_backward_v<T, V>(n, dyt, ht, gamma, mean, rstd, dht, dxt, dgamma, dbeta, part, st)
-             : norm_backward_v<T, 1>(n, dyt, ht, gamma, mean, rstd, dht, dxt, dgamma, dbeta, part, st);
+  return vec ? norm_backward_v<T, true>(n, dyt, ht, gamma, mean, rstd, dht, dxt, dgamma, dbeta, part, st)
+             : norm_backward_v<T, false>(n, dyt, ht, gamma, mean, rstd, dht, dxt, dgamma, dbeta, part, st);
 }
 
 }  // namespace
