@@ -22,7 +22,7 @@ struct LinearEpi {
 };
 
 // Partial sums of a split product: at most kPartTiles output tiles of 128 x 128 fp32, by the
-// rule that picks the splits (tiles x splits <= kPartTiles when splits > 1).
+// rule that picks the splits (tiles x splits <= kPartTiles when splits > 1; more of smaller tiles).
 constexpr int kPartTiles = 304;
 constexpr size_t kPartBytes = size_t(kPartTiles) * 128 * 128 * 4;
 

@@ -4,15 +4,21 @@
 //   out(i, j) = act(sum_k A(i, k) B(j, k) + bias[j]) + residual(i, j)
 //
 // for the forward (A = x, B = W), dx (A = d, B = W^T) and dW (A = d^T, B = x^T): the operands
-// come with two strides, one of them 1, and are transposed on their way into shared memory.
-// A CTA of 256 threads computes a 128 x 128 tile (64 x 128 for up to 64 rows), 8 x 8 outputs a
-// thread as pairs of columns (two multiply-adds an instruction: with single ones the issue slots
-// of shared-memory loads and multiply-adds together bound it), over 16-deep slices of K, the
-// next slice's loads in registers while the present one is multiplied; two CTAs an SM. When the
-// tiles are fewer than the SMs the K range is split over grid.z; the partial tiles are then
-// added in split order by a second kernel, which applies the epilogue. 2048^3: 372 us, 46 TFLOP/s
-// (the library's product 293): shared memory's rate and the 1.7 waves of 256 tiles bound it.
+// come with two strides, one of them 1 (a template argument each: 3 % over reading them at run time),
+// and are transposed on their way into shared memory, 64 bytes of a row by neighbouring lanes.
+// A CTA of 256 threads computes a 128 x 128 tile, 8 x 8 outputs a thread as pairs of columns (two
+// multiply-adds an instruction: with single ones the issue slots of shared-memory loads and
+// multiply-adds together bound it), over 16-deep slices of K, the next slice's loads in registers while
+// the present one is multiplied; two CTAs an SM. An output with a side of at most 64, 32 or 16 takes
+// tiles of 64, 32 or 16 x 128 along it, rows and columns changing places where the columns are the
+// short side (16384 x 16 x 4096 forward 365 -> 195 us, 16384 x 64 x 8192 718 -> 455). When the
+// tiles are fewer than half of what the SMs hold, the K range is split over grid.z; the partial tiles
+// are then added in split order by a second kernel, which applies the epilogue. 2048^3: 364 us, 47
+// TFLOP/s (the library's product 293): the multiply-adds' rate (213 us), 256 tiles on 304 places, and
+// the waits on shared memory of four warps a scheduler bound it. (8 x 16 outputs a thread with half
+// the threads: 388 us.)
 #include <algorithm>
+#include <type_traits>
 
 #include "linear.cuh"
 
@@ -20,6 +26,8 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 128, kDepth = 16, kThreadsF = 256;
+// CTAs of ROWS x 128 tiles that an SM is to hold (their registers allow it)
+constexpr int ctas_per_sm(int rows) { return rows > 32 ? 2 : (rows > 16 ? 3 : 4); }
 
 struct Operand {
   const float* p;
@@ -28,39 +36,68 @@ struct Operand {
   int vec;  // 16-byte loads along the unit stride are possible
 };
 
-// This thread's VALS = ROWS / 16 values of a ROWS x 16 slice: along k (unit sk) a row's consecutive
-// k; along the rows (unit si) one k's consecutive rows.
+// This thread's VALS = ROWS / 16 values of a ROWS x 16 slice: along k (unit sk) W consecutive k of a row
+// (and of the row 64 on); along the rows (unit si) one k's consecutive rows.
 template <int ROWS>
+struct Slice {
+  static constexpr int VALS = ROWS / 16, W = VALS < 4 ? VALS : 4, PER = 16 / W, PITCH = ROWS + 4;
+};
+template <int W>
+__device__ __forceinline__ void load_whole(float* v, const float* p) {
+  if constexpr (W == 4) *reinterpret_cast<float4*>(v) = __ldg(reinterpret_cast<const float4*>(p));
+  else if constexpr (W == 2) *reinterpret_cast<float2*>(v) = __ldg(reinterpret_cast<const float2*>(p));
+  else v[0] = __ldg(p);
+}
+template <int ROWS, bool ALONG_K>
 __device__ __forceinline__ void load_slice(const Operand& o, int r0, int64_t k0, int64_t k1,
                                            float (&v)[ROWS / 16]) {
-  constexpr int VALS = ROWS / 16, PER = 16 / VALS;  // threads along k of a row
+  using S = Slice<ROWS>;
   const int tid = threadIdx.x;
-  const bool along_k = o.sk == 1;
-  const int r = r0 + (along_k ? tid / PER : VALS * (tid & 15));
-  const int64_t k = k0 + (along_k ? VALS * (tid % PER) : (tid >> 4));
-  const float* p = o.p + r * o.si + k * o.sk;
-  const bool whole = along_k ? (r < o.rows && k + VALS <= k1) : (k < k1 && r + VALS <= o.rows);
-  if (whole && o.vec) {
+  if constexpr (ALONG_K) {
+    const int64_t k = k0 + S::W * (tid % S::PER);
 #pragma unroll
-    for (int q = 0; q < VALS; q += 4) *reinterpret_cast<float4*>(v + q) = __ldg(reinterpret_cast<const float4*>(p + q));
+    for (int m = 0; m < S::VALS; m += S::W) {
+      const int r = r0 + tid / S::PER + 16 * m;
+      const float* p = o.p + r * o.si + k;
+      if (r < o.rows && k + S::W <= k1 && o.vec) {
+        load_whole<S::W>(v + m, p);
+      } else {
+#pragma unroll
+        for (int q = 0; q < S::W; ++q) v[m + q] = r < o.rows && k + q < k1 ? __ldg(p + q) : 0.f;
+      }
+    }
   } else {
+    const int r = r0 + S::VALS * (tid & 15);
+    const int64_t k = k0 + (tid >> 4);
+    const float* p = o.p + k * o.sk + r;
+    if (k < k1 && r + S::VALS <= o.rows && o.vec) {
 #pragma unroll
-    for (int q = 0; q < VALS; ++q)
-      v[q] = (along_k ? (r < o.rows && k + q < k1) : (k < k1 && r + q < o.rows)) ? __ldg(p + q) : 0.f;
+      for (int m = 0; m < S::VALS; m += S::W) load_whole<S::W>(v + m, p + m);
+    } else {
+#pragma unroll
+      for (int q = 0; q < S::VALS; ++q) v[q] = k < k1 && r + q < o.rows ? __ldg(p + q) : 0.f;
+    }
   }
 }
-template <int ROWS>
-__device__ __forceinline__ void store_slice(const Operand& o, float* s, const float (&v)[ROWS / 16]) {
-  constexpr int VALS = ROWS / 16, PER = 16 / VALS, PITCH = ROWS + 4;
+template <int ROWS, bool ALONG_K>
+__device__ __forceinline__ void store_slice(float* s, const float (&v)[ROWS / 16]) {
+  using S = Slice<ROWS>;
   const int tid = threadIdx.x;
-  if (o.sk == 1) {
-    const int r = tid / PER, k = VALS * (tid % PER);
+  if constexpr (ALONG_K) {
+    float* d = s + S::W * (tid % S::PER) * S::PITCH + tid / S::PER;
 #pragma unroll
-    for (int q = 0; q < VALS; ++q) s[(k + q) * PITCH + r] = v[q];
+    for (int m = 0; m < S::VALS; m += S::W)
+#pragma unroll
+      for (int q = 0; q < S::W; ++q) d[q * S::PITCH + 16 * m] = v[m + q];
   } else {
-    float* d = s + (tid >> 4) * PITCH + VALS * (tid & 15);
+    float* d = s + (tid >> 4) * S::PITCH + S::VALS * (tid & 15);
+    if constexpr (S::VALS >= 4) {
 #pragma unroll
-    for (int q = 0; q < VALS; q += 4) *reinterpret_cast<float4*>(d + q) = *reinterpret_cast<const float4*>(v + q);
+      for (int q = 0; q < S::VALS; q += 4) *reinterpret_cast<float4*>(d + q) = *reinterpret_cast<const float4*>(v + q);
+    } else {
+#pragma unroll
+      for (int q = 0; q < S::VALS; ++q) d[q] = v[q];
+    }
   }
 }
 
@@ -73,10 +110,11 @@ __device__ __forceinline__ void emit(const LinearEpi& e, int64_t i, int64_t j, f
   static_cast<float*>(e.out)[i * e.ldo + j] = v;
 }
 
-template <int ACT, int ROWS>
-__global__ void __launch_bounds__(kThreadsF, 2)
-    linear_f32_kernel(Operand A, Operand B, int K, int kchunk, float* part, LinearEpi e) {
+template <int ACT, int ROWS, bool AK, bool BK>  // AK, BK: the operand's unit stride is k's
+__global__ void __launch_bounds__(kThreadsF, ctas_per_sm(ROWS))
+    linear_f32_kernel(Operand A, Operand B, int K, int kchunk, float* part, int swap, LinearEpi e) {
   constexpr int RT = ROWS / 16, PA = ROWS + 4, PB = kTile + 4;  // rows a thread, pitches
+  constexpr int RV = RT < 4 ? RT : 4;                           // consecutive ones of them
   __shared__ __align__(16) float sA[2][kDepth * PA], sB[2][kDepth * PB];
   pdl_wait();
   pdl_trigger();
@@ -89,26 +127,32 @@ __global__ void __launch_bounds__(kThreadsF, 2)
 #pragma unroll
     for (int b = 0; b < 4; ++b) acc[a][b] = 0ull;
   float va[RT], vb[8];
-  load_slice<ROWS>(A, i0, k0, k1, va);
-  load_slice<kTile>(B, j0, k0, k1, vb);
-  store_slice<ROWS>(A, sA[0], va);
-  store_slice<kTile>(B, sB[0], vb);
+  load_slice<ROWS, AK>(A, i0, k0, k1, va);
+  load_slice<kTile, BK>(B, j0, k0, k1, vb);
+  store_slice<ROWS, AK>(sA[0], va);
+  store_slice<kTile, BK>(sB[0], vb);
   __syncthreads();
   int buf = 0;
   for (int64_t k = k0; k < k1; k += kDepth) {
     const bool more = k + kDepth < k1;
     if (more) {
-      load_slice<ROWS>(A, i0, k + kDepth, k1, va);
-      load_slice<kTile>(B, j0, k + kDepth, k1, vb);
+      load_slice<ROWS, AK>(A, i0, k + kDepth, k1, va);
+      load_slice<kTile, BK>(B, j0, k + kDepth, k1, vb);
     }
-    const float* pa = sA[buf] + ty * 4;
+    const float* pa = sA[buf] + ty * RV;
     const float* pb = sB[buf] + tx * 4;
 #pragma unroll
     for (int q = 0; q < kDepth; ++q) {
       float a[RT];
+      if constexpr (RT >= 4) {
 #pragma unroll
-      for (int h = 0; h < RT / 4; ++h)
-        *reinterpret_cast<float4*>(a + 4 * h) = *reinterpret_cast<const float4*>(pa + q * PA + 64 * h);
+        for (int h = 0; h < RT / 4; ++h)
+          *reinterpret_cast<float4*>(a + 4 * h) = *reinterpret_cast<const float4*>(pa + q * PA + 64 * h);
+      } else if constexpr (RT == 2) {
+        *reinterpret_cast<float2*>(a) = *reinterpret_cast<const float2*>(pa + q * PA);
+      } else {
+        a[0] = pa[q * PA];
+      }
       const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(pb + q * PB);
       const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(pb + q * PB + 64);
 #pragma unroll
@@ -121,40 +165,48 @@ __global__ void __launch_bounds__(kThreadsF, 2)
       }
     }
     if (more) {
-      store_slice<ROWS>(A, sA[buf ^ 1], va);
-      store_slice<kTile>(B, sB[buf ^ 1], vb);
+      store_slice<ROWS, AK>(sA[buf ^ 1], va);
+      store_slice<kTile, BK>(sB[buf ^ 1], vb);
     }
     __syncthreads();
     buf ^= 1;
   }
   // thread (ty, tx): rows 4 ty .. + 3 (and 64 + 4 ty ..), columns 4 tx .. and 64 + 4 tx ..
   float* pt = part ? part + int64_t(blockIdx.z) * A.rows * B.rows : nullptr;
+  auto leave = [&](auto swapped) {
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int64_t i = i0 + (r >> 2) * 64 + ty * 4 + (r & 3);
-    if (i >= A.rows) continue;
+    for (int r = 0; r < RT; ++r) {
+      const int64_t i = i0 + r / RV * 64 + ty * RV + r % RV;
+      if (i >= A.rows) continue;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int64_t j = j0 + (c >> 2) * 64 + tx * 4 + (c & 3);
-      if (j >= B.rows) continue;
-      const float2 f = unpack2(acc[r][c >> 1]);
-      const float v = c & 1 ? f.y : f.x;
-      if (pt) pt[i * B.rows + j] = v;
-      else emit<ACT>(e, i, j, v);
+      for (int c = 0; c < 8; ++c) {
+        const int64_t j = j0 + (c >> 2) * 64 + tx * 4 + (c & 3);
+        if (j >= B.rows) continue;
+        const float2 f = unpack2(acc[r][c >> 1]);
+        const float v = c & 1 ? f.y : f.x;
+        if (pt) pt[i * B.rows + j] = v;
+        else if (decltype(swapped)::value) emit<ACT>(e, j, i, v);
+        else emit<ACT>(e, i, j, v);
+      }
     }
+  };
+  if constexpr (ROWS < kTile) {
+    if (swap) return leave(std::bool_constant<true>{});
   }
+  leave(std::bool_constant<false>{});
 }
 
 template <int ACT>
 __global__ void __launch_bounds__(256)
-    linear_f32_join_kernel(const float* __restrict__ part, int splits, int rows, int cols, LinearEpi e) {
+    linear_f32_join_kernel(const float* __restrict__ part, int splits, int rows, int cols, int swap, LinearEpi e) {
   pdl_wait();
   pdl_trigger();
   const int64_t n = int64_t(rows) * cols;
   for (int64_t x = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; x < n; x += int64_t(gridDim.x) * blockDim.x) {
     float v = 0.f;
     for (int s = 0; s < splits; ++s) v += part[s * n + x];
-    emit<ACT>(e, x / cols, x % cols, v);
+    const int64_t i = x / cols, j = x - i * cols;
+    emit<ACT>(e, swap ? j : i, swap ? i : j, v);
   }
 }
 
@@ -170,28 +222,47 @@ Operand operand(const float* p, int64_t si, int64_t sk, int rows) {
 int launch_linear_f32(const float* A, int64_t a_i, int64_t a_k, const float* B, int64_t b_j,
                       int64_t b_k, int rows, int cols, int K, const LinearEpi& e, float* part,
                       cudaStream_t st) {
-  const Operand oa = operand(A, a_i, a_k, rows), ob = operand(B, b_j, b_k, cols);
-  const int tile_rows = rows <= 64 ? 64 : kTile;
-  const int64_t ty = (rows + tile_rows - 1) / tile_rows, tx = (cols + kTile - 1) / kTile;
+  // the shorter side of the output along the tiles' rows, in the smallest tile that holds it
+  const int swap = cols < rows && cols <= 64;
+  Operand oa = operand(A, a_i, a_k, rows), ob = operand(B, b_j, b_k, cols);
+  if (swap) std::swap(oa, ob);
+  const int tile_rows = oa.rows <= 16 ? 16 : (oa.rows <= 32 ? 32 : (oa.rows <= 64 ? 64 : kTile));
+  const int64_t ty = (oa.rows + tile_rows - 1) / tile_rows, tx = (ob.rows + kTile - 1) / kTile;
   if (ty > 65535) return MOE_ERR_UNSUPPORTED;
-  // splits: about two tiles an SM, at least 64 deep each, within the scratch
+  // splits: about as many tiles as the SMs hold, at least 64 deep each, within the scratch
   int splits = 1;
-  if (tx * ty < num_sms()) {
-    splits = int(std::min<int64_t>(std::min<int64_t>(2 * num_sms(), kPartTiles) / (tx * ty), (K + 63) / 64));
+  const int64_t room = ctas_per_sm(tile_rows) * num_sms();
+  if (tx * ty <= room / 2) {
+    splits = int(std::min<int64_t>(std::min<int64_t>(room, kPartTiles * (128 / tile_rows)) / (tx * ty), (K + 63) / 64));
     if (splits < 1) splits = 1;
   }
   const int kchunk = int(((K + splits - 1) / splits + kDepth - 1) / kDepth * kDepth);
   splits = (K + kchunk - 1) / kchunk;
+  int rc;
+  auto go = [&](auto act, auto ak, auto bk) {
+    constexpr int ACT = decltype(act)::value;
+    constexpr bool AK = decltype(ak)::value, BK = decltype(bk)::value;
+    auto kern = tile_rows == 16   ? linear_f32_kernel<ACT, 16, AK, BK>
+                : tile_rows == 32 ? linear_f32_kernel<ACT, 32, AK, BK>
+                : tile_rows == 64 ? linear_f32_kernel<ACT, 64, AK, BK>
+                                  : linear_f32_kernel<ACT, kTile, AK, BK>;
+    return launch_kernel(kern, dim3(unsigned(tx), unsigned(ty), unsigned(splits)), dim3(kThreadsF), 0, st, oa, ob, K,
+                         kchunk, splits > 1 ? part : nullptr, swap, e);
+  };
+  const bool ak = oa.sk == 1, bk = ob.sk == 1;
+  constexpr std::bool_constant<true> yes{};
+  constexpr std::bool_constant<false> no{};
+  constexpr std::integral_constant<int, MOE_LIN_NONE> none{};  // the backward's products: no activation
+  if (ak && bk) rc = with_act(e.act, [&](auto tag) { return go(tag, yes, yes); });
+  else if (ak) rc = go(none, yes, no);
+  else if (bk) rc = go(none, no, yes);
+  else rc = go(none, no, no);
+  if (rc != MOE_OK || splits == 1) return rc;
+  const int64_t n = int64_t(rows) * cols;
+  const unsigned grid = unsigned(std::min<int64_t>((n + 255) / 256, 8 * num_sms()));
   return with_act(e.act, [&](auto tag) {
-    constexpr int ACT = decltype(tag)::value;
-    auto kern = tile_rows == 64 ? linear_f32_kernel<ACT, 64> : linear_f32_kernel<ACT, kTile>;
-    int rc = launch_kernel(kern, dim3(unsigned(tx), unsigned(ty), unsigned(splits)),
-                           dim3(kThreadsF), 0, st, oa, ob, K, kchunk, splits > 1 ? part : nullptr, e);
-    if (rc != MOE_OK || splits == 1) return rc;
-    const int64_t n = int64_t(rows) * cols;
-    const unsigned grid = unsigned(std::min<int64_t>((n + 255) / 256, 8 * num_sms()));
-    return launch_kernel(linear_f32_join_kernel<ACT>, dim3(grid), dim3(256), 0, st,
-                         static_cast<const float*>(part), splits, rows, cols, e);
+    return launch_kernel(linear_f32_join_kernel<decltype(tag)::value>, dim3(grid), dim3(256), 0, st,
+                         static_cast<const float*>(part), splits, oa.rows, ob.rows, swap, e);
   });
 }
 
