@@ -10,10 +10,11 @@
 // multiply-adds an instruction: with single ones the issue slots of shared-memory loads and
 // multiply-adds together bound it), over 16-deep slices of K, the next slice's loads in registers while
 // the present one is multiplied; two CTAs an SM. An output with a side of at most 64, 32 or 16 takes
-// tiles of 64, 32 or 16 x 128 along it, rows and columns changing places where the columns are the
-// short side (16384 x 16 x 4096 forward 365 -> 195 us, 16384 x 64 x 8192 718 -> 455). When the
+// tiles of 64, 32 or 16 x 128 along it (linear_f32_narrow_kernel), rows and columns changing places where the
+// columns are the short side: 16384 x 16 x 4096 forward 96 us (365 in whole tiles; 268 MB of x, 40 us),
+// 16384 x 64 x 8192 420 (718), 16 x 4096 x 4096 25 us (61). When the
 // tiles are fewer than half of what the SMs hold, the K range is split over grid.z; the partial tiles
-// are then added in split order by a second kernel, which applies the epilogue. 2048^3: 364 us, 47
+// are then added in split order by a second kernel, which applies the epilogue. 2048^3: 349 us, 49
 // TFLOP/s (the library's product 293): the multiply-adds' rate (213 us), 256 tiles on 304 places, and
 // the waits on shared memory of four warps a scheduler bound it. (8 x 16 outputs a thread with half
 // the threads: 388 us.)
@@ -27,7 +28,9 @@ namespace {
 
 constexpr int kTile = 128, kDepth = 16, kThreadsF = 256;
 // CTAs of ROWS x 128 tiles that an SM is to hold (their registers allow it)
-constexpr int ctas_per_sm(int rows) { return rows > 32 ? 2 : (rows > 16 ? 3 : 4); }
+// (16384 x 16 x 4096 with four, at 64 registers a thread, 106 us, with three 96; 2000 x 50 x 5000 with
+// three 37.5, with two 33.4)
+constexpr int ctas_per_sm(int rows) { return rows > 32 ? 2 : 3; }
 
 struct Operand {
   const float* p;
@@ -110,51 +113,43 @@ __device__ __forceinline__ void emit(const LinearEpi& e, int64_t i, int64_t j, f
   static_cast<float*>(e.out)[i * e.ldo + j] = v;
 }
 
-template <int ACT, int ROWS, bool AK, bool BK>  // AK, BK: the operand's unit stride is k's
-__global__ void __launch_bounds__(kThreadsF, ctas_per_sm(ROWS))
-    linear_f32_kernel(Operand A, Operand B, int K, int kchunk, float* part, int swap, LinearEpi e) {
-  constexpr int RT = ROWS / 16, PA = ROWS + 4, PB = kTile + 4;  // rows a thread, pitches
-  constexpr int RV = RT < 4 ? RT : 4;                           // consecutive ones of them
-  __shared__ __align__(16) float sA[2][kDepth * PA], sB[2][kDepth * PB];
+template <int ACT, bool AK, bool BK>  // AK, BK: the operand's unit stride is k's
+__global__ void __launch_bounds__(kThreadsF, ctas_per_sm(kTile))
+    linear_f32_kernel(Operand A, Operand B, int K, int kchunk, float* part, LinearEpi e) {
+  constexpr int RT = 8, P = kTile + 4;  // rows a thread, pitch
+  __shared__ __align__(16) float sA[2][kDepth * P], sB[2][kDepth * P];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int i0 = blockIdx.y * ROWS, j0 = blockIdx.x * kTile;
+  const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile;
   const int64_t k0 = int64_t(blockIdx.z) * kchunk, k1 = min(int64_t(K), k0 + kchunk);
   f32x2 acc[RT][4];  // row r, column pairs
 #pragma unroll
   for (int a = 0; a < RT; ++a)
 #pragma unroll
     for (int b = 0; b < 4; ++b) acc[a][b] = 0ull;
-  float va[RT], vb[8];
-  load_slice<ROWS, AK>(A, i0, k0, k1, va);
+  float va[8], vb[8];
+  load_slice<kTile, AK>(A, i0, k0, k1, va);
   load_slice<kTile, BK>(B, j0, k0, k1, vb);
-  store_slice<ROWS, AK>(sA[0], va);
+  store_slice<kTile, AK>(sA[0], va);
   store_slice<kTile, BK>(sB[0], vb);
   __syncthreads();
   int buf = 0;
   for (int64_t k = k0; k < k1; k += kDepth) {
     const bool more = k + kDepth < k1;
     if (more) {
-      load_slice<ROWS, AK>(A, i0, k + kDepth, k1, va);
+      load_slice<kTile, AK>(A, i0, k + kDepth, k1, va);
       load_slice<kTile, BK>(B, j0, k + kDepth, k1, vb);
     }
-    const float* pa = sA[buf] + ty * RV;
+    const float* pa = sA[buf] + ty * 4;
     const float* pb = sB[buf] + tx * 4;
 #pragma unroll
     for (int q = 0; q < kDepth; ++q) {
       float a[RT];
-      if constexpr (RT >= 4) {
-#pragma unroll
-        for (int h = 0; h < RT / 4; ++h)
-          *reinterpret_cast<float4*>(a + 4 * h) = *reinterpret_cast<const float4*>(pa + q * PA + 64 * h);
-      } else if constexpr (RT == 2) {
-        *reinterpret_cast<float2*>(a) = *reinterpret_cast<const float2*>(pa + q * PA);
-      } else {
-        a[0] = pa[q * PA];
-      }
-      const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(pb + q * PB);
-      const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(pb + q * PB + 64);
+      *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(pa + q * P);
+      *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(pa + q * P + 64);
+      const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(pb + q * P);
+      const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(pb + q * P + 64);
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         const f32x2 aa = set2(a[r]);
@@ -165,7 +160,7 @@ __global__ void __launch_bounds__(kThreadsF, ctas_per_sm(ROWS))
       }
     }
     if (more) {
-      store_slice<ROWS, AK>(sA[buf ^ 1], va);
+      store_slice<kTile, AK>(sA[buf ^ 1], va);
       store_slice<kTile, BK>(sB[buf ^ 1], vb);
     }
     __syncthreads();
@@ -173,27 +168,113 @@ __global__ void __launch_bounds__(kThreadsF, ctas_per_sm(ROWS))
   }
   // thread (ty, tx): rows 4 ty .. + 3 (and 64 + 4 ty ..), columns 4 tx .. and 64 + 4 tx ..
   float* pt = part ? part + int64_t(blockIdx.z) * A.rows * B.rows : nullptr;
-  auto leave = [&](auto swapped) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int64_t i = i0 + r / RV * 64 + ty * RV + r % RV;
-      if (i >= A.rows) continue;
+  for (int r = 0; r < RT; ++r) {
+    const int64_t i = i0 + (r >> 2) * 64 + ty * 4 + (r & 3);
+    if (i >= A.rows) continue;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int64_t j = j0 + (c >> 2) * 64 + tx * 4 + (c & 3);
-        if (j >= B.rows) continue;
-        const float2 f = unpack2(acc[r][c >> 1]);
-        const float v = c & 1 ? f.y : f.x;
-        if (pt) pt[i * B.rows + j] = v;
-        else if (decltype(swapped)::value) emit<ACT>(e, j, i, v);
-        else emit<ACT>(e, i, j, v);
+    for (int c = 0; c < 8; ++c) {
+      const int64_t j = j0 + (c >> 2) * 64 + tx * 4 + (c & 3);
+      if (j >= B.rows) continue;
+      const float2 f = unpack2(acc[r][c >> 1]);
+      const float v = c & 1 ? f.y : f.x;
+      if (pt) pt[i * B.rows + j] = v;
+      else emit<ACT>(e, i, j, v);
+    }
+  }
+}
+
+// ROWS (16, 32 or 64) x 128 tiles, of the output's transpose with swap: 8 x 4 outputs a thread, so that
+// 12 floats from shared memory feed 32 multiply-adds; the threads that this leaves over share a slice's
+// k (64 / ROWS groups of them), and the groups' sums are added through shared memory in group order.
+template <int ACT, int ROWS, bool AK, bool BK>
+__global__ void __launch_bounds__(kThreadsF, ctas_per_sm(ROWS))
+    linear_f32_narrow_kernel(Operand A, Operand B, int K, int kchunk, float* part, int swap, LinearEpi e) {
+  constexpr int GROUPS = 64 / ROWS, DEPTH = kDepth / GROUPS, PA = ROWS + 4, PB = kTile + 4;
+  constexpr int SLICE = kDepth * (PA + PB), SUMS = GROUPS * ROWS * PB;
+  __shared__ __align__(16) float s_all[2 * SLICE > SUMS ? 2 * SLICE : SUMS];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, tx = tid & 31, ty = (tid >> 5) % (ROWS / 8), grp = tid / (4 * ROWS);
+  const int i0 = blockIdx.y * ROWS, j0 = blockIdx.x * kTile;
+  const int64_t k0 = int64_t(blockIdx.z) * kchunk, k1 = min(int64_t(K), k0 + kchunk);
+  f32x2 acc[8][2];
+#pragma unroll
+  for (int a = 0; a < 8; ++a) acc[a][0] = acc[a][1] = 0ull;
+  float va[ROWS / 16], vb[8];
+  load_slice<ROWS, AK>(A, i0, k0, k1, va);
+  load_slice<kTile, BK>(B, j0, k0, k1, vb);
+  store_slice<ROWS, AK>(s_all, va);
+  store_slice<kTile, BK>(s_all + kDepth * PA, vb);
+  __syncthreads();
+  int buf = 0;
+  for (int64_t k = k0; k < k1; k += kDepth) {
+    const bool more = k + kDepth < k1;
+    if (more) {
+      load_slice<ROWS, AK>(A, i0, k + kDepth, k1, va);
+      load_slice<kTile, BK>(B, j0, k + kDepth, k1, vb);
+    }
+    const float* pa = s_all + buf * SLICE + grp * DEPTH * PA + ty * 8;
+    const float* pb = s_all + buf * SLICE + kDepth * PA + grp * DEPTH * PB + tx * 4;
+#pragma unroll
+    for (int q = 0; q < DEPTH; ++q) {
+      float a[8];
+      *reinterpret_cast<float4*>(a) = *reinterpret_cast<const float4*>(pa + q * PA);
+      *reinterpret_cast<float4*>(a + 4) = *reinterpret_cast<const float4*>(pa + q * PA + 4);
+      const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(pb + q * PB);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const f32x2 aa = set2(a[r]);
+        acc[r][0] = fma2(aa, b.x, acc[r][0]);
+        acc[r][1] = fma2(aa, b.y, acc[r][1]);
       }
     }
-  };
-  if constexpr (ROWS < kTile) {
-    if (swap) return leave(std::bool_constant<true>{});
+    if (more) {
+      store_slice<ROWS, AK>(s_all + (buf ^ 1) * SLICE, va);
+      store_slice<kTile, BK>(s_all + (buf ^ 1) * SLICE + kDepth * PA, vb);
+    }
+    __syncthreads();
+    buf ^= 1;
   }
-  leave(std::bool_constant<false>{});
+  float* pt = part ? part + int64_t(blockIdx.z) * A.rows * B.rows : nullptr;
+  if constexpr (GROUPS == 1) {
+    auto leave = [&](auto swapped) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const int64_t i = i0 + ty * 8 + r;
+        if (i >= A.rows) continue;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int64_t j = j0 + tx * 4 + c;
+          if (j >= B.rows) continue;
+          const float2 f = unpack2(acc[r][c >> 1]);
+          const float v = c & 1 ? f.y : f.x;
+          if (pt) pt[i * B.rows + j] = v;
+          else if (decltype(swapped)::value) emit<ACT>(e, j, i, v);
+          else emit<ACT>(e, i, j, v);
+        }
+      }
+    };
+    return swap ? leave(std::bool_constant<true>{}) : leave(std::bool_constant<false>{});
+  }
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    *reinterpret_cast<ulonglong2*>(s_all + (grp * ROWS + ty * 8 + r) * PB + tx * 4) =
+        make_ulonglong2(acc[r][0], acc[r][1]);
+  __syncthreads();
+  const bool across = swap && !pt;  // consecutive threads along what is contiguous in the output
+#pragma unroll
+  for (int x = tid; x < ROWS * kTile; x += kThreadsF) {
+    const int r = across ? x % ROWS : x / kTile, c = across ? x / ROWS : x % kTile;
+    const int64_t i = i0 + r, j = j0 + c;
+    if (i >= A.rows || j >= B.rows) continue;
+    float v = s_all[r * PB + c];
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) v += s_all[(g * ROWS + r) * PB + c];
+    if (pt) pt[i * B.rows + j] = v;
+    else if (swap) emit<ACT>(e, j, i, v);
+    else emit<ACT>(e, i, j, v);
+  }
 }
 
 template <int ACT>
@@ -233,7 +314,8 @@ int launch_linear_f32(const float* A, int64_t a_i, int64_t a_k, const float* B, 
   int splits = 1;
   const int64_t room = ctas_per_sm(tile_rows) * num_sms();
   if (tx * ty <= room / 2) {
-    splits = int(std::min<int64_t>(std::min<int64_t>(room, kPartTiles * (128 / tile_rows)) / (tx * ty), (K + 63) / 64));
+    const int64_t most = std::min<int64_t>(room, kPartTiles * (kTile / tile_rows));
+    splits = int(std::min<int64_t>(most / (tx * ty), (K + 63) / 64));
     if (splits < 1) splits = 1;
   }
   const int kchunk = int(((K + splits - 1) / splits + kDepth - 1) / kDepth * kDepth);
@@ -242,12 +324,15 @@ int launch_linear_f32(const float* A, int64_t a_i, int64_t a_k, const float* B, 
   auto go = [&](auto act, auto ak, auto bk) {
     constexpr int ACT = decltype(act)::value;
     constexpr bool AK = decltype(ak)::value, BK = decltype(bk)::value;
-    auto kern = tile_rows == 16   ? linear_f32_kernel<ACT, 16, AK, BK>
-                : tile_rows == 32 ? linear_f32_kernel<ACT, 32, AK, BK>
-                : tile_rows == 64 ? linear_f32_kernel<ACT, 64, AK, BK>
-                                  : linear_f32_kernel<ACT, kTile, AK, BK>;
-    return launch_kernel(kern, dim3(unsigned(tx), unsigned(ty), unsigned(splits)), dim3(kThreadsF), 0, st, oa, ob, K,
-                         kchunk, splits > 1 ? part : nullptr, swap, e);
+    const dim3 grid = dim3(unsigned(tx), unsigned(ty), unsigned(splits));
+    float* const to = splits > 1 ? part : nullptr;
+    auto narrow = [&](auto kern) {
+      return launch_kernel(kern, grid, dim3(kThreadsF), 0, st, oa, ob, K, kchunk, to, swap, e);
+    };
+    if (tile_rows == 16) return narrow(linear_f32_narrow_kernel<ACT, 16, AK, BK>);
+    if (tile_rows == 32) return narrow(linear_f32_narrow_kernel<ACT, 32, AK, BK>);
+    if (tile_rows == 64) return narrow(linear_f32_narrow_kernel<ACT, 64, AK, BK>);
+    return launch_kernel(linear_f32_kernel<ACT, AK, BK>, grid, dim3(kThreadsF), 0, st, oa, ob, K, kchunk, to, e);
   };
   const bool ak = oa.sk == 1, bk = ob.sk == 1;
   constexpr std::bool_constant<true> yes{};
