@@ -133,6 +133,26 @@ def test_backward(native_lib, dtype, shape, layout):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("side", [1, 9, 16, 17, 32, 33, 64, 65])
+@pytest.mark.parametrize("K", [20, 1001, 9000])
+@pytest.mark.parametrize("layout", [(0, 0), (3, 1), (8, 8)])
+def test_short_sides(native_lib, dtype, side, K, layout):
+    """Few tokens or few outputs (and, in the backward, few inputs) against a long other side: the
+    tiles along a short side, transposed or not, with K split and not."""
+    pad, off = layout
+    for T, N in ((side, 700), (700, side)):
+        act = ACTS[(side + K + T) % 5]
+        gen, dt, x, W, bias = make(T, N, K, dtype, pad, off, side + K)
+        res, out, pre = (strided(T, N, pad, off, dt, gen) for _ in range(3))
+        got = block.linear(x, W, bias, act=act, residual=res, out=out, pre=pre)
+        check_forward(x, W, bias, act, res, got, dt)
+        dy = strided(T, N, pad, off, dt, gen)
+        p = None if act == "none" else got[1]
+        back = block.linear_backward(dy, x, W, act=act, pre=p, need_bias=True)
+        check_backward(dy, x, W, act, p, back, dt, True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("act", ACTS)
 def test_backward_parts(native_lib, dtype, act):
     """Each gradient alone equals the one of the whole call, bit for bit."""
