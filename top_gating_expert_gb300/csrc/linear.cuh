@@ -68,9 +68,9 @@ __device__ __forceinline__ float act_slope(float v) {
   if constexpr (ACT == MOE_LIN_GELU_TANH) {
     // with s = sigmoid(2u): s + v 2u' s (1 - s)
     if (fabsf(v) > 16.f) return v > 0.f ? 1.f : 0.f;  // s (1 - s) is 0 and v^3 may overflow
-    const float u2 = 1.59576912160573072f * (v + 0.044715f * v * v * v);
+    const float u2 = 1.5957691216f * (v + 0.044715f * v * v * v);
     const float s = 1.f / (1.f + expf(-u2)), t = 1.f / (1.f + expf(u2));
-    return s + v * (1.59576912160573072f * (1.f + 0.134145f * v * v)) * s * t;
+    return s + v * (1.5957691216f * (1.f + 0.134145f * v * v)) * s * t;
   }
   if constexpr (ACT == MOE_LIN_SILU) {
     const float s = 1.f / (1.f + expf(-v)), t = 1.f / (1.f + expf(v));
