@@ -126,6 +126,54 @@ def test_moe_block(native_lib, name):
             assert_close(to_np(a), b.numpy(), rtol, f"d{key}[{e}]")
 
 
+@pytest.mark.parametrize("pad,offset", [(8, 0), (3, 0), (0, 1), (5, 3)])
+@pytest.mark.parametrize("name", ["softmax_ragged", "fp32", "one_token"])
+def test_moe_block_on_strided_rows(native_lib, name, pad, offset):
+    """x and dy whose rows lie apart or start off a 16-byte boundary: what the layer gives for
+    contiguous ones, bit for bit, on the current stream and on another."""
+    cfg, score = CASES[name]
+    w = weights_of(cfg, 7)
+    dt, (S, M) = moe.torch_dtype(cfg), (cfg["S"], cfg["M"])
+    g = torch.Generator().manual_seed(11)
+    x, dy = (torch.randn((S, M), generator=g).to(dt).cuda() for _ in range(2))
+
+    def apart(t):
+        full = torch.full((S * (M + pad) + offset,), 1e3, dtype=dt, device="cuda")
+        return full[offset:].as_strided((S, M), (M + pad, 1)).copy_(t)
+
+    xs, dys = apart(x), apart(dy)
+    for stream in (None, torch.cuda.Stream()):
+        blk, layer = block.MoeBlock(cfg, w, score=score), moe.MoeLayer(cfg, w, score=score)
+        blk.enable_backward(w)
+        layer.enable_backward(w)
+        torch.cuda.synchronize()
+        y = blk.forward(xs, stream=stream)
+        dx, dgamma, dbeta, got = blk.backward(xs, dys, aux_coef=AUX, z_coef=Z, stream=stream)
+        torch.cuda.synchronize()
+        assert moe.device_status(blk.layer.ws) == 0 and moe.device_status(blk.layer.ws_bwd) == 0
+        assert torch.equal(y, layer.forward(blk.n, residual=x))
+        want = layer.backward(blk.n, dy, aux_coef=AUX, z_coef=Z)
+        for k in ("dx", "dW_g", "dW_in", "dW_out"):
+            assert torch.equal(getattr(got, k), getattr(want, k)), k
+        norm = block.layer_norm_backward(want.dx, xs, blk.gamma, blk.mean, blk.rstd, dh=dy)
+        for a, b in zip((dx, dgamma, dbeta), norm):
+            assert torch.equal(a, b)
+
+
+def test_moe_block_backward_refuses_other_shapes(native_lib):
+    cfg, score = CASES["softmax_ragged"]
+    w = weights_of(cfg, 7)
+    blk = block.MoeBlock(cfg, w, score=score)
+    blk.enable_backward(w)
+    x = w["x"].to(torch.bfloat16).cuda()
+    blk.forward(x)
+    for bad in (x[:-1], x[:, :-8], x.float(), x.cpu()):
+        with pytest.raises(ValueError):
+            blk.backward(x, bad)
+        with pytest.raises(ValueError):
+            blk.backward(bad, x)
+
+
 def test_scored_layer_equals_step_calls(native_lib):
     """moe_layer_forward_scored against the separate calls, bit for bit."""
     cfg, score = CASES["groups_shared_dropless"]

@@ -278,6 +278,15 @@ def linear_backward(dy, x, W, *, act="none", pre=None, need_x=True, need_W=True,
 
 
 # ------------------------------------------------------------------ blocks
+def _whole_rows(t, stream):
+    """t as the MoE layer reads it (by its address alone: contiguous, on a 16-byte boundary), or
+    a copy of it made on the stream."""
+    if t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return t
+    with _on(stream):
+        return t.clone(memory_format=torch.contiguous_format)
+
+
 class MoeBlock:
     """out = x + MoE(norm(x)): the pre-norm MoE half of a Transformer block, with the routing
     by expert scores when `score` is given (see moe.make_score). weights: those of MoeLayer,
@@ -296,7 +305,7 @@ class MoeBlock:
     def forward(self, x, u=None, stream=None):
         layer_norm(x, self.gamma, self.beta, self.eps, out=self.n, mean=self.mean, rstd=self.rstd,
                    stream=stream)
-        return self.layer.forward(self.n, u, residual=x, stream=stream, out=self.y)
+        return self.layer.forward(self.n, u, residual=_whole_rows(x, stream), stream=stream, out=self.y)
 
     def enable_backward(self, weights: dict):
         self.layer.enable_backward(weights)
@@ -306,7 +315,11 @@ class MoeBlock:
     def backward(self, x, dy, aux_coef=0.0, z_coef=0.0, stream=None):
         """(dx, dgamma, dbeta, grads) for the last forward on x; grads holds the layer's weight
         gradients (its dx is the normalised input's)."""
-        g = self.layer.backward(self.n, dy, residual=False, aux_coef=aux_coef, z_coef=z_coef, stream=stream)
+        n = self.n
+        for t, name in ((x, "x"), (dy, "dy")):  # the layer itself checks no shapes
+            _matrix(t, name, "MoeBlock.backward", n.shape, n.dtype, n.get_device())
+        dy = _whole_rows(dy, stream)
+        g = self.layer.backward(n, dy, residual=False, aux_coef=aux_coef, z_coef=z_coef, stream=stream)
         dx, dgamma, dbeta = layer_norm_backward(g.dx, x, self.gamma, self.mean, self.rstd, dh=dy,
                                                 ws=self.norm_ws, stream=stream)
         return dx, dgamma, dbeta, g
