@@ -113,6 +113,28 @@ def test_non_finite(native_lib, kind):
         np.testing.assert_allclose([r["aux_loss"][0], r["z_loss"][0]], [o["aux_loss"], o["z_loss"]], rtol=LOSS_RTOL)
 
 
+@pytest.mark.parametrize("kind", range(len(KINDS)))
+@pytest.mark.parametrize("shift", [-1e5, -1e3, -70.0, 70.0, 1e3, 1e5])
+def test_offset_of_the_logits(native_lib, kind, shift):
+    """A common offset costs the weights nothing (the spread in their tolerance is the token's own)."""
+    for cfg in (_cfg(200, E=64, k=4), _cfg(150, E=256, k=8, ng=8, tg=4), _cfg(1, E=5, k=2)):
+        rng = np.random.default_rng(kind)
+        logits = (rng.standard_normal((cfg["S"], cfg["E"])) + shift).astype(np.float32)
+        check(cfg, KINDS[kind], logits, None)
+
+
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("value", [-1e20, -1e9, 1e9, 1e20])
+def test_equal_logits_of_any_size(native_lib, value, renorm):
+    """Equal logits: equal softmax weights, 1 / E (or 1 / k), whatever the logits are."""
+    for E, k in ((7, 3), (64, 2), (200, 8)):
+        cfg, score = _cfg(33, E=E, k=k), dict(score="softmax", group_top=1, renorm=renorm, scale=1.0)
+        out, status, _ = gpu(cfg, score, np.full((33, E), value), None)
+        assert status == 0
+        np.testing.assert_array_equal(route_np(out)["expert_id"], np.tile(np.arange(k), (33, 1)))
+        np.testing.assert_allclose(route_np(out)["gate"], 1.0 / (k if renorm else E), rtol=(E + 64) * U)
+
+
 @pytest.mark.parametrize("case", range(len(CASES)))
 @pytest.mark.parametrize("kind", range(len(KINDS)))
 def test_backward(native_lib, case, kind):

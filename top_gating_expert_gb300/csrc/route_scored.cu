@@ -158,24 +158,23 @@ __device__ __noinline__ int choose_fp64(const float (&l)[Q], const RouteArgs& a,
 }
 
 // The loss terms and choice of one token in the general form: any finite logits, -inf where an
-// expert is out. q: the normalised scores. Lane j < k returns choice j.
+// expert is out. q: the normalised scores; the logits' largest m and s = sum exp(l - m) (0 and 0
+// where no expert is in). Lane j < k returns choice j.
 template <int Q>
 __device__ __noinline__ int token_general(const float (&l)[Q], const RouteArgs& a, const ScoreArgs& sc,
-                                          double* row, float (&q)[Q], float& lse) {
-  float m = -INFINITY;
+                                          double* row, float (&q)[Q], float& m, float& s) {
+  m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < Q; ++i) m = fmaxf(m, l[i]);
   m = warp_max(m);
-  const bool any = m > -INFINITY;
-  if (!any) m = 0.f;
-  float s = 0.f;
+  if (!(m > -INFINITY)) m = 0.f;
+  s = 0.f;
 #pragma unroll
   for (int i = 0; i < Q; ++i) {
     q[i] = expf(l[i] - m);
     s += q[i];
   }
   s = warp_sum(s);
-  lse = any ? m + logf(s) : 0.f;
   float ti = s > 0.f ? 1.f / s : 0.f;
   if (sc.sigmoid) {
     const float top = fminf(m, 0.f);
@@ -498,8 +497,8 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
   // [k][4][E]
   extern __shared__ double s_dyn[];
   __shared__ float s_z[kWarps];
-  __shared__ float s_lse[kThreads];   // sum of exponentials, or (general tokens) its logarithm
-  __shared__ uint8_t s_gen[kThreads];
+  __shared__ float s_sum[kThreads];  // sum of exp(l - top), later logsumexp^2
+  __shared__ float s_top[kThreads];  // the largest logit of general tokens, 0 of the others
   __shared__ __align__(8) uint8_t s_id[kThreads * kMaxK];
   __shared__ uint8_t s_rk[kThreads * kMaxK];
   __shared__ float s_w[ONE ? kThreads * kMaxK : 1];  // the choices' weights
@@ -554,8 +553,8 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
     if (!bias_bad && token_fast<Q, SIG>(l, b, brange, lr, a, sc, reinterpret_cast<float*>(scratch), pp,
                                         s_id + i * kMaxK, s)) {
       if (lane == 0) {
-        s_lse[i] = s;
-        s_gen[i] = 0;
+        s_sum[i] = s;
+        s_top[i] = 0.f;
       }
     } else {
       float q[Q];
@@ -568,25 +567,31 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
       }
       if (bad) atomicOr(a.status, kStatusNonfinite);
       __syncwarp();
-      const int id = token_general<Q>(l, a, sc, scratch, q, s);
+      float m;
+      const int id = token_general<Q>(l, a, sc, scratch, q, m, s);
 #pragma unroll
       for (int x = 0; x < Q; ++x) pp[x] += q[x];
       if (lane < k) s_id[i * kMaxK + lane] = uint8_t(id);
       if (lane == 0) {
-        s_lse[i] = s;
-        s_gen[i] = 1;
+        s_sum[i] = s;
+        s_top[i] = m;
       }
     }
   }
   __syncthreads();
-  // the weights: 8 lanes a token, lane j < k its choice j, from accurate exponentials of the
-  // choices' logits shifted by the largest (they cannot all underflow)
+  // the weights: 8 lanes a token, lane j < k its choice j, from accurate exponentials: renormalised
+  // ones of the choices' logits less their largest (they cannot all underflow), softmax ones of
+  // l - top - log(sum), the largest logit taken off first (l less the rounded logsumexp would carry
+  // half a step of it, 4e-3 of the weight at an offset of 1e5)
   for (int x = tid; x < kThreads * kMaxK; x += kTokThreads) {
     const int i = x >> 3, j = x & 7;
     const bool on = i < nt && j < k;
-    float ls = -INFINITY, lse = 0.f;
+    float ls = -INFINITY, top = 0.f, log_sum = 0.f;
     int id = 0;
-    if (i < nt) lse = s_gen[i] ? s_lse[i] : logf(s_lse[i]);
+    if (i < nt) {
+      top = s_top[i];
+      log_sum = s_sum[i] > 0.f ? logf(s_sum[i]) : 0.f;
+    }
     if (on) {
       id = int(s_id[i * kMaxK + j]);
       ls = __ldg(a.logits + int64_t(t0 + i) * E + id);
@@ -594,17 +599,17 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
     }
     float w;
     if (sc.renorm) {
-      float top = SIG ? fminf(ls, 0.f) : ls;
+      float most = SIG ? fminf(ls, 0.f) : ls;
 #pragma unroll
-      for (int off = 4; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-      if (!(top > -INFINITY)) top = 0.f;
-      w = SIG ? sigmoid_shifted(ls, top) : (ls > -INFINITY ? expf(ls - top) : 0.f);
+      for (int off = 4; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, off));
+      if (!(most > -INFINITY)) most = 0.f;
+      w = SIG ? sigmoid_shifted(ls, most) : (ls > -INFINITY ? expf(ls - most) : 0.f);
       float tot = w;
 #pragma unroll
       for (int off = 4; off > 0; off >>= 1) tot += __shfl_xor_sync(kFull, tot, off);
       w = tot > 0.f ? w / tot : 0.f;
     } else {
-      w = SIG ? sigmoid_shifted(ls, 0.f) : (ls > -INFINITY ? expf(ls - lse) : 0.f);
+      w = SIG ? sigmoid_shifted(ls, 0.f) : (ls > -INFINITY ? expf((ls - top) - log_sum) : 0.f);
     }
     if (on) {
       a.expert_id[int64_t(t0 + i) * k + j] = id;
@@ -613,7 +618,7 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
     }
     // the token's logsumexp^2, kept for the sum below
     __syncwarp();
-    if (i < nt && j == 0) s_lse[i] = lse * lse;
+    if (i < nt && j == 0) s_sum[i] = (top + log_sum) * (top + log_sum);
   }
   __syncthreads();  // the group scratch is free
   float* s_pp = reinterpret_cast<float*>(s_dyn);
@@ -621,7 +626,7 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
   for (int i = 0; i < Q; ++i)
     if (lane + 32 * i < E) s_pp[warp * E + lane + 32 * i] = pp[i];
   if (tid < kThreads) {
-    const float z = warp_sum(tid < nt ? s_lse[tid] : 0.f);
+    const float z = warp_sum(tid < nt ? s_sum[tid] : 0.f);
     if (lane == 0) s_z[warp] = z;
   }
   __syncthreads();
