@@ -174,6 +174,33 @@ def test_moe_block_backward_refuses_other_shapes(native_lib):
             blk.backward(bad, x)
 
 
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layer_of_shifted_logits(native_lib, dtype, renorm):
+    """Softmax scores do not know a common offset: with every logit 78 lower (exactly: x and W_g on
+    coarse grids) the layer of 8 experts routes the same, and its gradients are the same but for
+    roundings."""
+    cfg = _cfg(S=300, E=8, k=2, act="relu", dtype=dtype, M=256 if dtype == "bf16" else 64)
+    score = dict(score="softmax", group_top=1, renorm=renorm, scale=1.5)
+    w = weights_of(cfg, 8)
+    w["W_g"] = (w["W_g"].float() * 64).round().div(64).to(w["W_g"].dtype)
+    x = (w["x"].float() * 4).round().div(4).to(w["x"].dtype).cuda()
+    dy = torch.randn((cfg["S"], cfg["M"]), generator=torch.Generator().manual_seed(3)).to(x.dtype).cuda()
+    results = []
+    for shift in (0.0, -78.0):
+        layer = moe.MoeLayer(cfg, dict(w, bias=torch.full((8,), shift)), score=score)
+        layer.enable_backward(w)
+        y = layer.forward(x)
+        g = layer.backward(x, dy, aux_coef=AUX)
+        results.append([layer.route_out.expert_id, layer.logits - shift, layer.route_out.gate, y, g.dx, g.dW_g,
+                        g.dbias, g.dW_in, g.dW_out])
+    a, b = results
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # dbias sums over all tokens to (nearly) nothing: its row rms is that of its own terms
+    for name, u, v in zip(("gate", "y", "dx", "dW_g", "dbias", "dW_in", "dW_out"), a[2:], b[2:]):
+        assert_close(to_np(v), to_np(u), RTOL[dtype], name)
+
+
 def test_scored_layer_equals_step_calls(native_lib):
     """moe_layer_forward_scored against the separate calls, bit for bit."""
     cfg, score = CASES["groups_shared_dropless"]

@@ -173,6 +173,43 @@ def test_backward(native_lib, case, kind):
         assert not dl.cpu().numpy()[~chosen].any()
 
 
+@pytest.mark.parametrize("E", [5, 8, 40, 100, 160])
+@pytest.mark.parametrize("kind", range(len(KINDS)))
+@pytest.mark.parametrize("shift", [-60.0, -70.0, -74.0, -78.0, -81.0, -500.0, 70.0, 90.0])
+def test_backward_of_shifted_logits(native_lib, E, kind, shift):
+    """Tokens whose logits all lie far from 0, experts that fill no warp: only the experts count in
+    the sums. Tolerance as above, and a step of the logsumexp more (half of one, |lse| u, is in the
+    z term's own magnitude)."""
+    cfg, score = _cfg(90, E=E, k=min(4, E)), KINDS[kind]
+    rng = np.random.default_rng(E + kind)
+    S, k = cfg["S"], cfg["k"]
+    logits = (rng.standard_normal((S, E)) + shift).astype(np.float32)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    out, status, lg = gpu(cfg, score, logits, bias)
+    assert status == 0
+    o = SC.route(logits, bias, cfg, score)
+    np.testing.assert_array_equal(route_np(out)["expert_id"], o["expert_id"])
+    dgate = rng.standard_normal((S, k)).astype(np.float32)
+    dl = torch.full((S, E), float("nan"), device="cuda")
+    moe.route_scored_backward(cfg, score, lg, out, torch.from_numpy(dgate).cuda(), dl, 0.7, 0.3)
+    ref = SC.logit_grad(logits, cfg, score, o, dgate, 0.7, 0.3)
+    q = SC.normalised(logits, score["score"])
+    lse = SC.losses(logits, o["counts_routed"], cfg, score)[2]
+    f = np.repeat(o["counts_routed"] / (S * k), S, axis=0)
+    p = np.exp(logits - lse[:, None])
+    w = np.abs(o["gate_raw"])
+    mag = 0.7 * E / S * q * (f + (f * q).sum(1, keepdims=True)) + 0.6 / S * np.abs(lse)[:, None] * p
+    dabs = np.abs(dgate) + (np.abs(dgate) * w).sum(1, keepdims=True)
+    at = np.zeros((S, E))
+    np.add.at(at, (np.repeat(np.arange(S), k), o["expert_id"].ravel()), (w * dabs).ravel())
+    if score["score"] == "softmax" and not score["renorm"]:
+        at += p * (np.abs(dgate) * w).sum(1, keepdims=True)
+    spread = float((logits.max(1) - logits.min(1)).max())
+    tol = (E + 66 + spread) * U * (mag + at) + 1e-30
+    err = np.abs(dl.cpu().numpy().astype(np.float64) - ref)
+    assert (err <= tol).all(), (err / tol).max()
+
+
 def test_repeatable_in_a_graph_and_on_another_stream(native_lib):
     cfg, score = _cfg(1500, E=256, k=8, ng=8, tg=4, cf=1.0), KINDS[2]
     rng = np.random.default_rng(3)

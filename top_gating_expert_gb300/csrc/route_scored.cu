@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4)
 #pragma unroll
     for (int i = 0; i < Q; ++i) {
       const int e = lane + 32 * i;
-      l[i] = e < E ? __ldg(lr + e) : -80.f;  // no expert: exp(-80) of a score, and f = 0
+      l[i] = e < E ? __ldg(lr + e) : 0.f;  // no expert: left out of the sums below, and f = 0
       plain = plain && fabsf(l[i]) <= 80.f;  // false for NaN too
     }
     // the choices, lane j < k: expert, logit, gradient of its weight
@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4)
     if (__all_sync(kFull, plain)) {
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
-        const float x = expf(l[i]);
+        const float x = lane + 32 * i < E ? expf(l[i]) : 0.f;
         p[i] = x;
         s += x;
         if constexpr (SIG) {
