@@ -135,6 +135,33 @@ def test_equal_logits_of_any_size(native_lib, value, renorm):
         np.testing.assert_allclose(route_np(out)["gate"], 1.0 / (k if renorm else E), rtol=(E + 64) * U)
 
 
+@pytest.mark.parametrize("kind", range(len(KINDS)))
+def test_logits_of_the_lowest_values(native_lib, kind):
+    """Tokens of which every logit is hugely negative but finite (masked with the type's lowest
+    value, say), between ordinary ones: no status, choices and weights of the 64-bit scores."""
+    rng = np.random.default_rng(kind)
+    lowest = float(np.finfo(np.float32).min)
+    for cfg in (_cfg(40, E=4, k=2), _cfg(40, E=64, k=4, ng=8, tg=3), _cfg(40, E=200, k=8)):
+        E = cfg["E"]
+        logits = rng.standard_normal((40, E)).astype(np.float32)
+        logits[0] = lowest
+        logits[1] = np.resize(np.float32([-2e30, -1.5e30, -3e30, -1.5e30]), E)
+        logits[2] = -1e30
+        logits[3] = -1e30 * (1 + rng.random(E))
+        logits[4] = lowest
+        logits[4, E // 2] = -1e30
+        logits[5, 1:] = lowest
+        logits[6] = -2e30
+        logits[6, :3] = 0.5
+        for bias in (None, (0.1 * rng.standard_normal(E)).astype(np.float32)):
+            out, status, _ = gpu(cfg, KINDS[kind], logits, bias)
+            assert status == 0
+            o, r = SC.route(logits, bias, cfg, KINDS[kind]), route_np(out)
+            for key in ("expert_id", "pos", "row", "counts", "expert_offsets"):
+                np.testing.assert_array_equal(r[key], o[key], err_msg=key)
+            np.testing.assert_allclose(r["gate"], o["gate"], rtol=(E + 80) * U, atol=2.0 ** -126)
+
+
 @pytest.mark.parametrize("case", range(len(CASES)))
 @pytest.mark.parametrize("kind", range(len(KINDS)))
 def test_backward(native_lib, case, kind):

@@ -78,7 +78,7 @@ template <int Q>
 __device__ __forceinline__ double softmax_sum(const float (&l)[Q], double m) {
   double s = 0.0;
 #pragma unroll
-  for (int q = 0; q < Q; ++q) s += l[q] > -1e30f ? exp(double(l[q]) - m) : 0.0;
+  for (int q = 0; q < Q; ++q) s += l[q] > -INFINITY ? exp(double(l[q]) - m) : 0.0;  // -inf: out
   return warp_sum(s);
 }
 
