@@ -162,6 +162,27 @@ def test_logits_of_the_lowest_values(native_lib, kind):
             np.testing.assert_allclose(r["gate"], o["gate"], rtol=(E + 80) * U, atol=2.0 ** -126)
 
 
+@pytest.mark.parametrize("kind", range(len(KINDS)))
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("at", [0, 6, 31])
+def test_non_finite_bias_alone(native_lib, kind, bad, at):
+    """A bias that is not finite beside finite logits is reported and takes its expert out; biases
+    of any finite size are not reported."""
+    rng = np.random.default_rng(kind)
+    for cfg in (_cfg(1, E=32, k=4, ng=4, tg=2), _cfg(260, E=32, k=4), _cfg(200, E=160, k=8, ng=8, tg=3)):
+        logits = rng.standard_normal((cfg["S"], cfg["E"])).astype(np.float32)
+        bias = (0.1 * rng.standard_normal(cfg["E"])).astype(np.float32)
+        bias[at] = bad
+        out, status, _ = gpu(cfg, KINDS[kind], logits, bias)
+        assert status == -6
+        o, r = SC.route(logits, bias, cfg, KINDS[kind]), route_np(out)
+        for key in ("expert_id", "pos", "row", "counts", "expert_offsets"):
+            np.testing.assert_array_equal(r[key], o[key])
+        np.testing.assert_allclose(r["gate"], o["gate"], rtol=(cfg["E"] + 80) * U, atol=1e-30)
+        bias[at] = 3e38 if bad > 0 else -3e38
+        assert gpu(cfg, KINDS[kind], logits, bias)[1] == 0
+
+
 @pytest.mark.parametrize("case", range(len(CASES)))
 @pytest.mark.parametrize("kind", range(len(KINDS)))
 def test_backward(native_lib, case, kind):

@@ -534,14 +534,14 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
     }
   }
   bias_bad = __any_sync(kFull, bias_bad);
+  if (bias_bad && tid == 0) atomicOr(a.status, kStatusNonfinite);
   bmin = -warp_max(-bmin);
   bmax = warp_max(bmax);
 #pragma unroll
   for (int i = 0; i < Q; ++i)  // an expert's key is never below 8, no expert's is its slot
     b[i] = lane + 32 * i < E ? (b[i] - bmin) + 1e-30f : 0.f;
   const float brange = bmax - bmin;
-  if (!(brange < 1e30f)) bias_bad = true;  // the shifted biases could overflow
-  if (bias_bad && tid == 0 && !(isfinite(bmin) && isfinite(bmax))) atomicOr(a.status, kStatusNonfinite);
+  if (!(brange < 1e30f)) bias_bad = true;  // the shifted biases could overflow (no error)
   double* scratch = s_dyn + size_t(warp) * E;
   float pp[Q];
 #pragma unroll
