@@ -144,3 +144,12 @@ def test_binding_refuses_before_the_library(native_lib):
         moe.route_scored(cfg, dict(score="sigmoid"), torch.zeros(4, 4), None, None, None)
     with pytest.raises(KeyError):
         moe.make_score(dict(score="tanh"))
+
+
+def test_scored_layer_refuses_other_selection_biases(native_lib):
+    """The kernel reads E floats at the bias's address: other shapes, types and devices stop here."""
+    c = preset(2, random_routing=0)
+    call = lambda b: moe.layer_forward_scored(c, dict(score="sigmoid"), *[None] * 3, b, *[None] * 7, None, None)
+    for bad in (torch.zeros(c["E"]), torch.zeros(c["E"] - 1), torch.zeros(1, c["E"]), torch.zeros(c["E"]).double(), [0.0]):
+        with pytest.raises(ValueError, match="select_bias"):
+            call(bad)

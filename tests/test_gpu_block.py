@@ -201,6 +201,14 @@ def test_layer_of_shifted_logits(native_lib, dtype, renorm):
         assert_close(to_np(v), to_np(u), RTOL[dtype], name)
 
 
+def test_layer_refuses_a_selection_bias_of_another_length(native_lib):
+    cfg, score = CASES["capacity_relu"]
+    w = weights_of(cfg, 6)
+    for n in (cfg["E"] - 1, cfg["E"] + 1):
+        with pytest.raises(ValueError, match="select_bias"):
+            moe.MoeLayer(cfg, dict(w, select_bias=torch.zeros(n)), score=score)
+
+
 def test_scored_layer_equals_step_calls(native_lib):
     """moe_layer_forward_scored against the separate calls, bit for bit."""
     cfg, score = CASES["groups_shared_dropless"]

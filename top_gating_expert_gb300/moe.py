@@ -297,9 +297,12 @@ def layer_forward(cfg, x, W_g, bias, W_in_packed, W_out_packed, Ws_in_packed, Ws
 def layer_forward_scored(cfg, score, x, W_g, bias, select_bias, W_in_packed, W_out_packed, Ws_in_packed,
                          Ws_out_packed, residual, y, logits_out, out: RouteOutputs, ws, stream=None):
     """layer_forward with route_scored as the routing."""
+    c = _cfg(cfg)
+    if select_bias is not None:
+        _check_f32(select_bias, "select_bias", (c.E,), "layer_forward_scored")
     s = out.struct()
     _check(N.lib().moe_layer_forward_scored(
-        ctypes.byref(_cfg(cfg)), ctypes.byref(make_score(score)), _ptr(x), _ptr(W_g), _ptr(bias),
+        ctypes.byref(c), ctypes.byref(make_score(score)), _ptr(x), _ptr(W_g), _ptr(bias),
         _ptr(select_bias), _ptr(W_in_packed), _ptr(W_out_packed), _ptr(Ws_in_packed), _ptr(Ws_out_packed),
         _ptr(residual), _ptr(y), _ptr(logits_out), ctypes.byref(s), _ptr(ws), ws.numel(),
         _stream(stream)), "moe_layer_forward_scored")
@@ -419,6 +422,7 @@ class MoeLayer:
         self.select_bias = None
         if score is not None and weights.get("select_bias") is not None:
             self.select_bias = weights["select_bias"].to(dev, torch.float32).contiguous()
+            _check_f32(self.select_bias, "select_bias", (self.cfg.E,), "MoeLayer")
         self.Ws_in_packed = self.Ws_out_packed = None
         if self.cfg.n_shared > 0:
             self.Ws_in_packed, self.Ws_out_packed = pack_shared_weights(
