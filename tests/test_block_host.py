@@ -153,3 +153,51 @@ def test_scored_layer_refuses_other_selection_biases(native_lib):
     for bad in (torch.zeros(c["E"]), torch.zeros(c["E"] - 1), torch.zeros(1, c["E"]), torch.zeros(c["E"]).double(), [0.0]):
         with pytest.raises(ValueError, match="select_bias"):
             call(bad)
+
+
+class OnDevice1(torch.Tensor):
+    """A CPU tensor that says that it is on CUDA device 1 (nothing is launched on it)."""
+    is_cuda = True
+
+    def get_device(self):
+        return 1
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_launches_on_the_tensors_device(native_lib, monkeypatch, current):
+    """Every call makes the tensors' device the current one around the library's call, and takes
+    that device's stream."""
+    at, seen = [current], []
+    make = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype).as_subclass(OnDevice1)
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            at.append(self.dev)
+
+        def __exit__(self, *exc):
+            at.pop()
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: at[-1], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 100 + dev, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(moe, "_entry", lambda name: lambda *a: seen.append((name, at[-1], a[-1])) or 0)
+    x, v, t = make(4, 8), make(8), make(4)
+    W, b, ws = make(6, 8), make(6), make(1 << 16, dtype=torch.uint8)
+    block.layer_norm(x, v, v, out=make(4, 8), mean=t, rstd=t)
+    block.layer_norm_backward(x, x, v, t, t, dx=make(4, 8), dgamma=v, dbeta=v, ws=ws)
+    block.linear(x, W, b, out=make(4, 6), ws=ws)
+    block.linear_backward(make(4, 6), x, W, dx=make(4, 8), dW=make(6, 8), dbias=b, ws=ws)
+    c = preset(1, random_routing=0, S=4, E=8)
+    out = moe.RouteOutputs(*[make(1) for _ in N.ROUTE_FIELDS])
+    moe.route_scored(c, dict(score="sigmoid"), x, v, out, ws)
+    moe.route_scored_backward(c, dict(score="sigmoid"), x, out, make(4, 2), make(4, 8))
+    moe.route(c, x, None, out, ws)
+    moe.layer_forward_scored(c, dict(score="sigmoid"), x, x, None, v, x, x, None, None, x, x, None, out, ws)
+    moe.layer_backward(c, x, x, x, x, x, x, None, None, None, x, out, ws, 0, 0.0, 0.0, moe.Grads(c, "cpu"), ws)
+    moe.set_wait_limit(ws, 0)
+    assert moe.device_status(ws) == 0
+    assert len(seen) == 11 and {s[1:] for s in seen} == {(1, 101)}, seen
+    assert at == [current]

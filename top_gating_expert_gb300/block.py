@@ -21,15 +21,10 @@ import torch
 
 from . import _native as N
 from . import moe
-from .moe import _check, _raw_stream
+from .moe import _check, _launch
 
 _DTYPES = {torch.float32: N.MOE_F32, torch.bfloat16: N.MOE_BF16}
 _F32 = torch.float32
-
-
-@lru_cache(maxsize=None)
-def _entry(name):
-    return getattr(N.lib(), name)
 
 
 # The checks run on every call of a serving loop: attributes that cost little (shape, dtype, device
@@ -137,11 +132,8 @@ def layer_norm(x, gamma, beta=None, eps=1e-5, residual=None, *, out=None, h=None
     ldh = M if h is None else _matrix(h, "h", w, shape, dt, dev)
     _vector(mean, "mean", w, T, dev)
     _vector(rstd, "rstd", w, T, dev)
-    rc = _entry("moe_norm_forward")(_norm_args(T, M, _DTYPES[dt], eps, ldx, ldr, ldh, ldy), x.data_ptr(),
-                                    _p(residual), gamma.data_ptr(), _p(beta), _p(h), out.data_ptr(),
-                                    mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, dev))
-    if rc:
-        _check(rc, "moe_norm_forward")
+    _launch("moe_norm_forward", x, stream, _norm_args(T, M, _DTYPES[dt], eps, ldx, ldr, ldh, ldy), x.data_ptr(),
+            _p(residual), gamma.data_ptr(), _p(beta), _p(h), out.data_ptr(), mean.data_ptr(), rstd.data_ptr())
     return out, (x if h is None else h), mean, rstd
 
 
@@ -180,12 +172,9 @@ def layer_norm_backward(dy, h, gamma, mean, rstd, dh=None, *, need_beta=True, dx
     if dbeta is not None:
         _vector(dbeta, "dbeta", w, M, dev)
     _workspace_ok(ws, w, dev)
-    rc = _entry("moe_norm_backward")(_norm_args(T, M, _DTYPES[dt], 0.0, ldx, ldr, ldh, ldy), dy.data_ptr(),
-                                     h.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _p(dh),
-                                     dx.data_ptr(), dgamma.data_ptr(), _p(dbeta), ws.data_ptr(), ws.numel(),
-                                     _raw_stream(stream, dev))
-    if rc:
-        _check(rc, "moe_norm_backward")
+    _launch("moe_norm_backward", dy, stream, _norm_args(T, M, _DTYPES[dt], 0.0, ldx, ldr, ldh, ldy),
+            dy.data_ptr(), h.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _p(dh), dx.data_ptr(),
+            dgamma.data_ptr(), _p(dbeta), ws.data_ptr(), ws.numel())
     return dx, dgamma, dbeta
 
 
@@ -229,11 +218,8 @@ def linear(x, W, bias=None, *, act="none", residual=None, save_pre=False, out=No
     ldy = _matrix(out, "out", w, shape, dt, dev)
     ldp = n_out if pre is None else _matrix(pre, "pre", w, shape, dt, dev)
     _workspace_ok(ws, w, dev)
-    rc = _entry("moe_linear_forward")(_linear_args(T, n_out, K, code, _DTYPES[dt], ldx, ldw, ldy, ldr, ldp),
-                                      x.data_ptr(), W.data_ptr(), _p(bias), _p(residual), out.data_ptr(),
-                                      _p(pre), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
-    if rc:
-        _check(rc, "moe_linear_forward")
+    _launch("moe_linear_forward", x, stream, _linear_args(T, n_out, K, code, _DTYPES[dt], ldx, ldw, ldy, ldr, ldp),
+            x.data_ptr(), W.data_ptr(), _p(bias), _p(residual), out.data_ptr(), _p(pre), ws.data_ptr(), ws.numel())
     return out, pre
 
 
@@ -268,12 +254,9 @@ def linear_backward(dy, x, W, *, act="none", pre=None, need_x=True, need_W=True,
     if dbias is not None:
         _vector(dbias, "dbias", w, n_out, dev)
     _workspace_ok(ws, w, dev)
-    rc = _entry("moe_linear_backward")(
-        _linear_args(T, n_out, K, code, _DTYPES[dt], ldx, ldw, ldy, n_out, ldp, lddx, lddw), dy.data_ptr(),
-        x.data_ptr(), W.data_ptr(), _p(pre), _p(dx), _p(dW), _p(dbias), ws.data_ptr(), ws.numel(),
-        _raw_stream(stream, dev))
-    if rc:
-        _check(rc, "moe_linear_backward")
+    _launch("moe_linear_backward", dy, stream,
+            _linear_args(T, n_out, K, code, _DTYPES[dt], ldx, ldw, ldy, n_out, ldp, lddx, lddw), dy.data_ptr(),
+            x.data_ptr(), W.data_ptr(), _p(pre), _p(dx), _p(dW), _p(dbias), ws.data_ptr(), ws.numel())
     return dx, dW, dbias
 
 

@@ -61,9 +61,24 @@ def _raw_stream(stream, dev: int):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+@lru_cache(maxsize=None)
+def _entry(name: str):
+    return getattr(N.lib(), name)
+
+
+def _launch(name: str, t: torch.Tensor, stream, *args):
+    """Calls a launching entry point on the stream (None: the current one of t's device), with
+    t's device as the current one: the library launches there, and a default stream's handle
+    names no device."""
+    dev = t.get_device()
+    raw = _raw_stream(stream, dev)
+    if dev == torch._C._cuda_getDevice():
+        rc = _entry(name)(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = _entry(name)(*args, raw)
+    if rc:
+        _check(rc, name)
 
 
 # ------------------------------------------------------------------ host-only queries
@@ -151,8 +166,8 @@ def pack_weights(cfg, W_in, W_up, W_out, stream=None):
     n_in, n_out, _, _ = packed_sizes(c)
     p_in = torch.empty(n_in, dtype=W_in.dtype, device=W_in.device)
     p_out = torch.empty(n_out, dtype=W_in.dtype, device=W_in.device)
-    _check(N.lib().moe_pack_weights(ctypes.byref(c), _ptr(W_in), _ptr(W_up), _ptr(W_out),
-                                    _ptr(p_in), _ptr(p_out), _stream(stream)), "moe_pack_weights")
+    _launch("moe_pack_weights", W_in, stream, ctypes.byref(c), _ptr(W_in), _ptr(W_up), _ptr(W_out),
+            _ptr(p_in), _ptr(p_out))
     return p_in, p_out
 
 
@@ -161,39 +176,37 @@ def pack_shared_weights(cfg, Ws_in, Ws_up, Ws_out, stream=None):
     _, _, n_in, n_out = packed_sizes(c)
     p_in = torch.empty(n_in, dtype=Ws_in.dtype, device=Ws_in.device)
     p_out = torch.empty(n_out, dtype=Ws_in.dtype, device=Ws_in.device)
-    _check(N.lib().moe_pack_shared_weights(ctypes.byref(c), _ptr(Ws_in), _ptr(Ws_up), _ptr(Ws_out),
-                                           _ptr(p_in), _ptr(p_out), _stream(stream)),
-           "moe_pack_shared_weights")
+    _launch("moe_pack_shared_weights", Ws_in, stream, ctypes.byref(c), _ptr(Ws_in), _ptr(Ws_up),
+            _ptr(Ws_out), _ptr(p_in), _ptr(p_out))
     return p_in, p_out
 
 
 # ------------------------------------------------------------------ forward steps
 def router(cfg, x, W_g, bias, logits, ws, stream=None):
-    _check(N.lib().moe_router(ctypes.byref(_cfg(cfg)), _ptr(x), _ptr(W_g), _ptr(bias), _ptr(logits),
-                              _ptr(ws), ws.numel(), _stream(stream)), "moe_router")
+    _launch("moe_router", ws, stream, ctypes.byref(_cfg(cfg)), _ptr(x), _ptr(W_g), _ptr(bias),
+            _ptr(logits), _ptr(ws), ws.numel())
 
 
 def route(cfg, logits, u, out: RouteOutputs, ws, stream=None):
     s = out.struct()
-    _check(N.lib().moe_route(ctypes.byref(_cfg(cfg)), _ptr(logits), _ptr(u), ctypes.byref(s),
-                             _ptr(ws), ws.numel(), _stream(stream)), "moe_route")
+    _launch("moe_route", ws, stream, ctypes.byref(_cfg(cfg)), _ptr(logits), _ptr(u),
+            ctypes.byref(s), _ptr(ws), ws.numel())
 
 
 def router_route(cfg, x, W_g, bias, u, logits_out, out: RouteOutputs, ws, stream=None):
     """moe_router + moe_route in one pass (bf16: the logits stay on chip unless logits_out
     is given; fp32 needs logits_out)."""
     s = out.struct()
-    _check(N.lib().moe_router_route(ctypes.byref(_cfg(cfg)), _ptr(x), _ptr(W_g), _ptr(bias), _ptr(u),
-                                    _ptr(logits_out), ctypes.byref(s), _ptr(ws), ws.numel(),
-                                    _stream(stream)), "moe_router_route")
+    _launch("moe_router_route", ws, stream, ctypes.byref(_cfg(cfg)), _ptr(x), _ptr(W_g), _ptr(bias),
+            _ptr(u), _ptr(logits_out), ctypes.byref(s), _ptr(ws), ws.numel())
 
 
 def route_noalloc(cfg, logits, u, out: RouteOutputs, device_status=None, stream=None):
     """moe_route without a workspace (scratch in the library's fixed 4 MiB device array),
     for callers that cannot allocate device memory; see include/moe.h."""
     s = out.struct()
-    _check(N.lib().moe_route_noalloc(ctypes.byref(_cfg(cfg)), _ptr(logits), _ptr(u), ctypes.byref(s),
-                                     _ptr(device_status), _stream(stream)), "moe_route_noalloc")
+    _launch("moe_route_noalloc", logits, stream, ctypes.byref(_cfg(cfg)), _ptr(logits), _ptr(u),
+            ctypes.byref(s), _ptr(device_status))
 
 
 def make_score(score) -> N.MoeScore:
@@ -226,10 +239,8 @@ def route_scored(cfg, score, logits, select_bias, out: RouteOutputs, ws, stream=
     if select_bias is not None:
         _check_f32(select_bias, "select_bias", (c.E,), "route_scored")
         bias = select_bias.data_ptr()
-    rc = N.lib().moe_route_scored(ctypes.byref(c), ctypes.byref(make_score(score)), logits.data_ptr(), bias,
-                                  ctypes.byref(out.struct()), ws.data_ptr(), ws.numel(),
-                                  _raw_stream(stream, logits.get_device()))
-    _check(rc, "moe_route_scored")
+    _launch("moe_route_scored", logits, stream, ctypes.byref(c), ctypes.byref(make_score(score)),
+            logits.data_ptr(), bias, ctypes.byref(out.struct()), ws.data_ptr(), ws.numel())
 
 
 def route_scored_backward(cfg, score, logits, out: RouteOutputs, dgate, dlogits, aux_coef=0.0,
@@ -240,58 +251,53 @@ def route_scored_backward(cfg, score, logits, out: RouteOutputs, dgate, dlogits,
     _check_f32(logits, "logits", (c.S, c.E), "route_scored_backward")
     _check_f32(dgate, "dgate", (c.S, c.k), "route_scored_backward")
     _check_f32(dlogits, "dlogits", (c.S, c.E), "route_scored_backward")
-    rc = N.lib().moe_route_scored_backward(
-        ctypes.byref(c), ctypes.byref(make_score(score)), logits.data_ptr(), ctypes.byref(out.struct()),
-        dgate.data_ptr(), aux_coef, z_coef, dlogits.data_ptr(), _raw_stream(stream, logits.get_device()))
-    _check(rc, "moe_route_scored_backward")
+    _launch("moe_route_scored_backward", logits, stream, ctypes.byref(c), ctypes.byref(make_score(score)),
+            logits.data_ptr(), ctypes.byref(out.struct()), dgate.data_ptr(), aux_coef, z_coef,
+            dlogits.data_ptr())
 
 
 def dispatch(cfg, x, out: RouteOutputs, x_perm, stream=None):
     s = out.struct()
-    _check(N.lib().moe_dispatch(ctypes.byref(_cfg(cfg)), _ptr(x), ctypes.byref(s), _ptr(x_perm),
-                                _stream(stream)), "moe_dispatch")
+    _launch("moe_dispatch", x, stream, ctypes.byref(_cfg(cfg)), _ptr(x), ctypes.byref(s),
+            _ptr(x_perm))
 
 
 def expert_up(cfg, x_perm, expert_offsets, W_in_packed, h_perm, ws, stream=None):
-    _check(N.lib().moe_expert_up(ctypes.byref(_cfg(cfg)), _ptr(x_perm), _ptr(expert_offsets),
-                                 _ptr(W_in_packed), _ptr(h_perm), _ptr(ws), ws.numel(),
-                                 _stream(stream)), "moe_expert_up")
+    _launch("moe_expert_up", ws, stream, ctypes.byref(_cfg(cfg)), _ptr(x_perm),
+            _ptr(expert_offsets), _ptr(W_in_packed), _ptr(h_perm), _ptr(ws), ws.numel())
 
 
 def expert_down(cfg, h_perm, expert_offsets, w_perm, W_out_packed, y_perm, ws, stream=None):
-    _check(N.lib().moe_expert_down(ctypes.byref(_cfg(cfg)), _ptr(h_perm), _ptr(expert_offsets),
-                                   _ptr(w_perm), _ptr(W_out_packed), _ptr(y_perm), _ptr(ws),
-                                   ws.numel(), _stream(stream)), "moe_expert_down")
+    _launch("moe_expert_down", ws, stream, ctypes.byref(_cfg(cfg)), _ptr(h_perm),
+            _ptr(expert_offsets), _ptr(w_perm), _ptr(W_out_packed), _ptr(y_perm), _ptr(ws),
+            ws.numel())
 
 
 def expert_ffn(cfg, x_perm, expert_offsets, w_perm, W_in_packed, W_out_packed, h_perm, y_perm, ws,
                stream=None):
-    _check(N.lib().moe_expert_ffn(ctypes.byref(_cfg(cfg)), _ptr(x_perm), _ptr(expert_offsets),
-                                  _ptr(w_perm), _ptr(W_in_packed), _ptr(W_out_packed), _ptr(h_perm),
-                                  _ptr(y_perm), _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_expert_ffn")
+    _launch("moe_expert_ffn", ws, stream, ctypes.byref(_cfg(cfg)), _ptr(x_perm),
+            _ptr(expert_offsets), _ptr(w_perm), _ptr(W_in_packed), _ptr(W_out_packed), _ptr(h_perm),
+            _ptr(y_perm), _ptr(ws), ws.numel())
 
 
 def shared_ffn(cfg, x, Ws_in_packed, Ws_out_packed, h_shared, shared_out, ws, stream=None):
-    _check(N.lib().moe_shared_ffn(ctypes.byref(_cfg(cfg)), _ptr(x), _ptr(Ws_in_packed),
-                                  _ptr(Ws_out_packed), _ptr(h_shared), _ptr(shared_out), _ptr(ws),
-                                  ws.numel(), _stream(stream)), "moe_shared_ffn")
+    _launch("moe_shared_ffn", ws, stream, ctypes.byref(_cfg(cfg)), _ptr(x), _ptr(Ws_in_packed),
+            _ptr(Ws_out_packed), _ptr(h_shared), _ptr(shared_out), _ptr(ws), ws.numel())
 
 
 def combine(cfg, y_perm, out: RouteOutputs, shared_out, residual, y, stream=None):
     s = out.struct()
-    _check(N.lib().moe_combine(ctypes.byref(_cfg(cfg)), _ptr(y_perm), ctypes.byref(s),
-                               _ptr(shared_out), _ptr(residual), _ptr(y), _stream(stream)),
-           "moe_combine")
+    _launch("moe_combine", y_perm, stream, ctypes.byref(_cfg(cfg)), _ptr(y_perm), ctypes.byref(s),
+            _ptr(shared_out), _ptr(residual), _ptr(y))
 
 
 def layer_forward(cfg, x, W_g, bias, W_in_packed, W_out_packed, Ws_in_packed, Ws_out_packed, u,
                   residual, y, logits_out, out: RouteOutputs, ws, stream=None):
     s = out.struct()
-    _check(N.lib().moe_layer_forward(
-        ctypes.byref(_cfg(cfg)), _ptr(x), _ptr(W_g), _ptr(bias), _ptr(W_in_packed), _ptr(W_out_packed),
-        _ptr(Ws_in_packed), _ptr(Ws_out_packed), _ptr(u), _ptr(residual), _ptr(y), _ptr(logits_out),
-        ctypes.byref(s), _ptr(ws), ws.numel(), _stream(stream)), "moe_layer_forward")
+    _launch("moe_layer_forward", ws, stream, ctypes.byref(_cfg(cfg)), _ptr(x), _ptr(W_g),
+            _ptr(bias), _ptr(W_in_packed), _ptr(W_out_packed), _ptr(Ws_in_packed),
+            _ptr(Ws_out_packed), _ptr(u), _ptr(residual), _ptr(y), _ptr(logits_out),
+            ctypes.byref(s), _ptr(ws), ws.numel())
 
 
 def layer_forward_scored(cfg, score, x, W_g, bias, select_bias, W_in_packed, W_out_packed, Ws_in_packed,
@@ -301,11 +307,10 @@ def layer_forward_scored(cfg, score, x, W_g, bias, select_bias, W_in_packed, W_o
     if select_bias is not None:
         _check_f32(select_bias, "select_bias", (c.E,), "layer_forward_scored")
     s = out.struct()
-    _check(N.lib().moe_layer_forward_scored(
-        ctypes.byref(c), ctypes.byref(make_score(score)), _ptr(x), _ptr(W_g), _ptr(bias),
-        _ptr(select_bias), _ptr(W_in_packed), _ptr(W_out_packed), _ptr(Ws_in_packed), _ptr(Ws_out_packed),
-        _ptr(residual), _ptr(y), _ptr(logits_out), ctypes.byref(s), _ptr(ws), ws.numel(),
-        _stream(stream)), "moe_layer_forward_scored")
+    _launch("moe_layer_forward_scored", ws, stream, ctypes.byref(c),
+            ctypes.byref(make_score(score)), _ptr(x), _ptr(W_g), _ptr(bias), _ptr(select_bias),
+            _ptr(W_in_packed), _ptr(W_out_packed), _ptr(Ws_in_packed), _ptr(Ws_out_packed),
+            _ptr(residual), _ptr(y), _ptr(logits_out), ctypes.byref(s), _ptr(ws), ws.numel())
 
 
 def pack_weights_backward(cfg, W_in, W_up, W_out, stream=None):
@@ -314,9 +319,8 @@ def pack_weights_backward(cfg, W_in, W_up, W_out, stream=None):
     n_in, n_out, _, _ = packed_sizes(c)
     p_in = torch.empty(n_in, dtype=W_in.dtype, device=W_in.device)
     p_out = torch.empty(n_out, dtype=W_in.dtype, device=W_in.device)
-    _check(N.lib().moe_pack_weights_backward(ctypes.byref(c), _ptr(W_in), _ptr(W_up), _ptr(W_out),
-                                             _ptr(p_in), _ptr(p_out), _stream(stream)),
-           "moe_pack_weights_backward")
+    _launch("moe_pack_weights_backward", W_in, stream, ctypes.byref(c), _ptr(W_in), _ptr(W_up),
+            _ptr(W_out), _ptr(p_in), _ptr(p_out))
     return p_in, p_out
 
 
@@ -325,10 +329,8 @@ def pack_shared_weights_backward(cfg, Ws_in, Ws_up, Ws_out, stream=None):
     _, _, n_in, n_out = packed_sizes(c)
     p_in = torch.empty(n_in, dtype=Ws_in.dtype, device=Ws_in.device)
     p_out = torch.empty(n_out, dtype=Ws_in.dtype, device=Ws_in.device)
-    _check(N.lib().moe_pack_shared_weights_backward(ctypes.byref(c), _ptr(Ws_in), _ptr(Ws_up),
-                                                    _ptr(Ws_out), _ptr(p_in), _ptr(p_out),
-                                                    _stream(stream)),
-           "moe_pack_shared_weights_backward")
+    _launch("moe_pack_shared_weights_backward", Ws_in, stream, ctypes.byref(c), _ptr(Ws_in),
+            _ptr(Ws_up), _ptr(Ws_out), _ptr(p_in), _ptr(p_out))
     return p_in, p_out
 
 
@@ -360,12 +362,11 @@ def layer_backward(cfg, x, dy, W_g, W_in_packed, Wt_in_packed, Wt_out_packed, Ws
                    aux_coef, z_coef, grads: Grads, ws, stream=None):
     s = out.struct()
     g = grads.struct()
-    _check(N.lib().moe_layer_backward(
-        ctypes.byref(_cfg(cfg)), _ptr(x), _ptr(dy), _ptr(W_g), _ptr(W_in_packed), _ptr(Wt_in_packed),
-        _ptr(Wt_out_packed), _ptr(Ws_in_packed), _ptr(Wst_in_packed), _ptr(Wst_out_packed),
-        _ptr(logits), ctypes.byref(s), _ptr(fwd_ws), fwd_ws.numel(), int(bool(residual)),
-        float(aux_coef), float(z_coef), ctypes.byref(g), _ptr(ws), ws.numel(), _stream(stream)),
-        "moe_layer_backward")
+    _launch("moe_layer_backward", ws, stream, ctypes.byref(_cfg(cfg)), _ptr(x), _ptr(dy), _ptr(W_g),
+            _ptr(W_in_packed), _ptr(Wt_in_packed), _ptr(Wt_out_packed), _ptr(Ws_in_packed),
+            _ptr(Wst_in_packed), _ptr(Wst_out_packed), _ptr(logits), ctypes.byref(s), _ptr(fwd_ws),
+            fwd_ws.numel(), int(bool(residual)), float(aux_coef), float(z_coef), ctypes.byref(g),
+            _ptr(ws), ws.numel())
 
 
 def layer_backward_scored(cfg, score, x, dy, W_g, W_in_packed, Wt_in_packed, Wt_out_packed, Ws_in_packed,
@@ -374,24 +375,25 @@ def layer_backward_scored(cfg, score, x, dy, W_g, W_in_packed, Wt_in_packed, Wt_
     """layer_backward of layer_forward_scored."""
     s = out.struct()
     g = grads.struct()
-    _check(N.lib().moe_layer_backward_scored(
-        ctypes.byref(_cfg(cfg)), ctypes.byref(make_score(score)), _ptr(x), _ptr(dy), _ptr(W_g),
-        _ptr(W_in_packed), _ptr(Wt_in_packed), _ptr(Wt_out_packed), _ptr(Ws_in_packed),
-        _ptr(Wst_in_packed), _ptr(Wst_out_packed), _ptr(logits), ctypes.byref(s), _ptr(fwd_ws),
-        fwd_ws.numel(), int(bool(residual)), float(aux_coef), float(z_coef), ctypes.byref(g), _ptr(ws),
-        ws.numel(), _stream(stream)), "moe_layer_backward_scored")
+    _launch("moe_layer_backward_scored", ws, stream, ctypes.byref(_cfg(cfg)),
+            ctypes.byref(make_score(score)), _ptr(x), _ptr(dy), _ptr(W_g), _ptr(W_in_packed),
+            _ptr(Wt_in_packed), _ptr(Wt_out_packed), _ptr(Ws_in_packed), _ptr(Wst_in_packed),
+            _ptr(Wst_out_packed), _ptr(logits), ctypes.byref(s), _ptr(fwd_ws), fwd_ws.numel(),
+            int(bool(residual)), float(aux_coef), float(z_coef), ctypes.byref(g), _ptr(ws),
+            ws.numel())
 
 
 def device_status(ws, stream=None) -> int:
     """Synchronises the stream; returns (and clears) the device status recorded in ws."""
-    return N.lib().moe_get_device_status(_ptr(ws), _stream(stream))
+    dev = ws.get_device()
+    with torch.cuda.device(dev):
+        return _entry("moe_get_device_status")(_ptr(ws), _raw_stream(stream, dev))
 
 
 def set_wait_limit(ws, limit_ns: int, stream=None):
     """How long the kernels using workspace ws wait on their own pipeline before giving up
     (0 = the default of 2 s)."""
-    _check(N.lib().moe_set_wait_limit(_ptr(ws), int(limit_ns), _stream(stream)),
-           "moe_set_wait_limit")
+    _launch("moe_set_wait_limit", ws, stream, _ptr(ws), int(limit_ns))
 
 
 # ------------------------------------------------------------------ a layer object
