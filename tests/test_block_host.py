@@ -1,7 +1,9 @@
 """Refusals of the norm, linear and scored-routing entry points, before anything is launched:
 the C ABI's checks on made-up pointers and the Python binding's on CPU tensors."""
 
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -201,3 +203,25 @@ def test_launches_on_the_tensors_device(native_lib, monkeypatch, current):
     assert moe.device_status(ws) == 0
     assert len(seen) == 11 and {s[1:] for s in seen} == {(1, 101)}, seen
     assert at == [current]
+
+
+def test_route_outputs_follow_their_tensors():
+    """The struct of pointers after a field was set, resized or swapped in place; copies and pickles
+    of outputs that were in use."""
+    out = moe.RouteOutputs(*[torch.zeros(4) for _ in N.ROUTE_FIELDS])
+    now = lambda o: [getattr(o, f).data_ptr() for f in N.ROUTE_FIELDS]
+    held = lambda o: [getattr(o.struct(), f) for f in N.ROUTE_FIELDS]
+    assert held(out) == now(out)
+    assert out.struct() is out.struct()
+    keep = out.gate
+    out.gate = torch.ones(4)
+    assert held(out) == now(out) and keep.data_ptr() not in held(out)
+    out.row.set_(torch.ones(9))
+    assert held(out) == now(out)
+    out.pos.resize_(1 << 16)
+    assert held(out) == now(out)
+    for other in (copy.deepcopy(out), pickle.loads(pickle.dumps(out))):
+        assert held(other) == now(other) and not set(now(other)) & set(now(out))
+        assert torch.equal(other.gate, out.gate)
+    assert held(copy.copy(out)) == now(out)
+    assert held(out) == now(out)

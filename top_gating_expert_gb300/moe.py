@@ -148,15 +148,14 @@ class RouteOutputs:
                    z_loss=z((1,), torch.float32))
 
     def struct(self) -> N.MoeRouteOut:
-        s = self.__dict__.get("_struct")
-        if s is None:
-            s = N.MoeRouteOut(**{f: getattr(self, f).data_ptr() for f in N.ROUTE_FIELDS})
-            self.__dict__["_struct"] = s
-        return s
+        at = tuple([getattr(self, f).data_ptr() for f in N.ROUTE_FIELDS])
+        held = self.__dict__.get("_struct")  # made anew when any field's memory is another
+        if held is None or held[0] != at:
+            held = self.__dict__["_struct"] = (at, N.MoeRouteOut(*at))
+        return held[1]
 
-    def __setattr__(self, name, value):  # another tensor in a field: the pointers are taken anew
-        self.__dict__[name] = value
-        self.__dict__.pop("_struct", None)
+    def __getstate__(self):  # copies and pickles take the tensors, not their addresses
+        return {k: v for k, v in self.__dict__.items() if k != "_struct"}
 
 
 # ------------------------------------------------------------------ weight packing
