@@ -225,3 +225,13 @@ def test_route_outputs_follow_their_tensors():
         assert torch.equal(other.gate, out.gate)
     assert held(copy.copy(out)) == now(out)
     assert held(out) == now(out)
+
+
+def test_scores_are_not_shared(native_lib):
+    """A score made from a dict is the caller's: changing it changes no other one and no later call."""
+    d = dict(score="softmax", group_top=2, renorm=0, scale=2.5)
+    a, b = moe.make_score(d), moe.make_score(d)
+    a.scale = 7.0
+    held = moe._score(d)._obj
+    assert b.scale == 2.5 and moe.make_score(d).scale == 2.5 and held.scale == 2.5 and held.score == 1
+    assert moe.make_score(a) is a and moe._score(a)._obj is a

@@ -211,16 +211,25 @@ def route_noalloc(cfg, logits, u, out: RouteOutputs, device_status=None, stream=
 def make_score(score) -> N.MoeScore:
     """A moe_score_t from a dict: score "sigmoid" or "softmax", group_top 1 or 2 (how many of a
     group's best experts its score sums), renorm (weights sum to scale over the choices),
-    scale."""
+    scale. The caller's own: a struct as given, a new one for every dict."""
     if isinstance(score, N.MoeScore):
         return score
-    return _score(N.SCORES[score.get("score", "sigmoid")], int(score.get("group_top", 1)),
-                  int(score.get("renorm", 1)), float(score.get("scale", 1.0)))
+    return N.MoeScore(*_score_fields(score))
+
+
+def _score_fields(score: dict):
+    return (N.SCORES[score.get("score", "sigmoid")], int(score.get("group_top", 1)),
+            int(score.get("renorm", 1)), float(score.get("scale", 1.0)))
 
 
 @lru_cache(maxsize=64)
-def _score(*fields) -> N.MoeScore:  # by value; the library reads it during a call only
-    return N.MoeScore(*fields)
+def _held_score(*fields):
+    return ctypes.byref(N.MoeScore(*fields))
+
+
+def _score(score):
+    """The argument of a call: dicts by value, from structs that no caller sees."""
+    return ctypes.byref(score) if isinstance(score, N.MoeScore) else _held_score(*_score_fields(score))
 
 
 def _check_f32(t, name: str, shape, where: str):
@@ -238,7 +247,7 @@ def route_scored(cfg, score, logits, select_bias, out: RouteOutputs, ws, stream=
     if select_bias is not None:
         _check_f32(select_bias, "select_bias", (c.E,), "route_scored")
         bias = select_bias.data_ptr()
-    _launch("moe_route_scored", logits, stream, ctypes.byref(c), ctypes.byref(make_score(score)),
+    _launch("moe_route_scored", logits, stream, ctypes.byref(c), _score(score),
             logits.data_ptr(), bias, ctypes.byref(out.struct()), ws.data_ptr(), ws.numel())
 
 
@@ -250,7 +259,7 @@ def route_scored_backward(cfg, score, logits, out: RouteOutputs, dgate, dlogits,
     _check_f32(logits, "logits", (c.S, c.E), "route_scored_backward")
     _check_f32(dgate, "dgate", (c.S, c.k), "route_scored_backward")
     _check_f32(dlogits, "dlogits", (c.S, c.E), "route_scored_backward")
-    _launch("moe_route_scored_backward", logits, stream, ctypes.byref(c), ctypes.byref(make_score(score)),
+    _launch("moe_route_scored_backward", logits, stream, ctypes.byref(c), _score(score),
             logits.data_ptr(), ctypes.byref(out.struct()), dgate.data_ptr(), aux_coef, z_coef,
             dlogits.data_ptr())
 
@@ -307,7 +316,7 @@ def layer_forward_scored(cfg, score, x, W_g, bias, select_bias, W_in_packed, W_o
         _check_f32(select_bias, "select_bias", (c.E,), "layer_forward_scored")
     s = out.struct()
     _launch("moe_layer_forward_scored", ws, stream, ctypes.byref(c),
-            ctypes.byref(make_score(score)), _ptr(x), _ptr(W_g), _ptr(bias), _ptr(select_bias),
+            _score(score), _ptr(x), _ptr(W_g), _ptr(bias), _ptr(select_bias),
             _ptr(W_in_packed), _ptr(W_out_packed), _ptr(Ws_in_packed), _ptr(Ws_out_packed),
             _ptr(residual), _ptr(y), _ptr(logits_out), ctypes.byref(s), _ptr(ws), ws.numel())
 
@@ -375,7 +384,7 @@ def layer_backward_scored(cfg, score, x, dy, W_g, W_in_packed, Wt_in_packed, Wt_
     s = out.struct()
     g = grads.struct()
     _launch("moe_layer_backward_scored", ws, stream, ctypes.byref(_cfg(cfg)),
-            ctypes.byref(make_score(score)), _ptr(x), _ptr(dy), _ptr(W_g), _ptr(W_in_packed),
+            _score(score), _ptr(x), _ptr(dy), _ptr(W_g), _ptr(W_in_packed),
             _ptr(Wt_in_packed), _ptr(Wt_out_packed), _ptr(Ws_in_packed), _ptr(Wst_in_packed),
             _ptr(Wst_out_packed), _ptr(logits), ctypes.byref(s), _ptr(fwd_ws), fwd_ws.numel(),
             int(bool(residual)), float(aux_coef), float(z_coef), ctypes.byref(g), _ptr(ws),
