@@ -307,3 +307,28 @@ def test_many_tiles(native_lib, shape, act):
     dy = strided(T, N, 0, 0, dt, gen)
     got = block.linear_backward(dy, x, W, act=act, pre=pre)
     check_backward(dy, x, W, act, pre, got, dt, True)
+
+
+@pytest.mark.parametrize("T", [2, 70])
+@pytest.mark.parametrize("off", [0, 1])
+def test_copied_operands_end_with_their_rows(native_lib, T, off):
+    """bf16 rows of every length up to three pieces, even and odd starts, between NaNs: the copies
+    hold the rows and zeros, whatever lies beside them."""
+    gen = generator(T + off)
+
+    def between_nans(rows, cols, pad):
+        full = torch.full((rows * (cols + pad) + off + 9,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        v = full[off:].as_strided((rows, cols), (cols + pad, 1))
+        return v.copy_(torch.randn((rows, cols), generator=gen, device="cuda"))
+
+    for K in range(1, 26):
+        for pad in (1, 2, 5):
+            x, W = between_nans(T, K, pad), between_nans(9, K, pad)
+            got = block.linear(x, W, save_pre=True)
+            check_forward(x, W, None, "none", None, got, torch.bfloat16)
+            dy = between_nans(T, 9, pad)
+            dx, dW, _ = block.linear_backward(dy, x, W, need_bias=False)
+            dd, xd, wd = dy.double(), x.double(), W.double()
+            h = half_step(torch.bfloat16)
+            for g, ref, s, n in ((dx, dd @ wd, dd.abs() @ wd.abs(), 9), (dW, dd.t() @ xd, dd.abs().t() @ xd.abs(), T)):
+                assert_within(g, ref, 2 * (n + 3) * U * s * (1 + h) + h * ref.abs() + 1e-38)

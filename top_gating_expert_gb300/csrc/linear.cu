@@ -86,7 +86,8 @@ __global__ void __launch_bounds__(1024)
 
 // Copies of up to two operands to 16-byte rows: dst [rows][ldd] = src [rows][cols], src on any
 // element boundary. Eight elements a thread, read as the 4-byte words that hold them (five when
-// the row starts inside a word) and shifted into place; a warp takes 256 columns of a row.
+// the row starts inside a word) and shifted into place; a word that the row only half fills is read
+// as its one element, so nothing outside of the row is read. A warp takes 256 columns of a row.
 struct AlignJob {
   const __nv_bfloat16* src;
   int64_t ld, rows;
@@ -109,13 +110,20 @@ __global__ void __launch_bounds__(256) linear_align_kernel(AlignJob j0, AlignJob
       const uint32_t* w = words + 4 * p;
       uint32_t v[5];
 #pragma unroll
-      for (int q = 0; q < 5; ++q) v[q] = 2 * q - odd < left && (q < 4 || odd) ? __ldg(w + q) : 0u;
+      for (int q = 0; q < 5; ++q) {
+        const int at = 2 * q - odd;  // the word's first element, from this thread's first one on
+        const bool head = at < 0 && p == 0, tail = at + 1 >= left;
+        const uint16_t* one = reinterpret_cast<const uint16_t*>(w + q);
+        v[q] = 0u;
+        if (at < left && (q < 4 || odd)) {
+          if (head) v[q] = uint32_t(__ldg(one + 1)) << 16;
+          else if (tail) v[q] = __ldg(one);
+          else v[q] = __ldg(w + q);
+        }
+      }
       uint32_t o[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        o[q] = odd ? __funnelshift_r(v[q], v[q + 1], 16) : v[q];
-        if (2 * q + 1 >= left) o[q] &= 2 * q < left ? 0xffffu : 0u;  // past the row's end
-      }
+      for (int q = 0; q < 4; ++q) o[q] = odd ? __funnelshift_r(v[q], v[q + 1], 16) : v[q];
       *reinterpret_cast<uint4*>(j.dst + r * j.ldd + 8 * p) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
