@@ -332,3 +332,23 @@ def test_copied_operands_end_with_their_rows(native_lib, T, off):
             h = half_step(torch.bfloat16)
             for g, ref, s, n in ((dx, dd @ wd, dd.abs() @ wd.abs(), 9), (dW, dd.t() @ xd, dd.abs().t() @ xd.abs(), T)):
                 assert_within(g, ref, 2 * (n + 3) * U * s * (1 + h) + h * ref.abs() + 1e-38)
+
+
+@pytest.mark.parametrize("dtype,N", [("f32", 66), ("f32", 130), ("f32", 20), ("bf16", 66)])
+def test_more_rows_than_a_grid_axis_has_tiles(native_lib, dtype, N):
+    """65536 tiles of 128 rows and one row more, either side of the output the long one."""
+    T, K = 65536 * 128 + 1, 3
+    gen, dt = generator(N), DT[dtype]
+    x = torch.randn((T, K), generator=gen, device="cuda").to(dt)
+    W, b = torch.randn((N, K), generator=gen, device="cuda").to(dt), torch.randn(N, generator=gen, device="cuda")
+    out = torch.full((T, N), float("nan"), dtype=dt, device="cuda")
+    block.linear(x, W, b, act="relu", out=out)
+    assert not torch.isnan(out).any()
+    for at in (slice(0, 700), slice(65535 * 128 - 300, 65535 * 128 + 300), slice(T - 300, T)):
+        check_forward(x[at], W, b, "relu", None, (out[at], None), dt)
+    if dtype == "f32":  # dx's rows are the tokens too
+        wide = torch.randn((2, N), generator=gen, device="cuda")
+        dx, _, _ = block.linear_backward(x[:, :2], out, wide, need_W=False, need_bias=False, dx=out)
+        for at in (slice(0, 700), slice(65535 * 128 - 300, 65535 * 128 + 300), slice(T - 300, T)):
+            ref, s = x[at, :2].double() @ wide.double(), x[at, :2].double().abs() @ wide.double().abs()
+            assert_within(dx[at], ref, 2 * 5 * U * s + U * ref.abs() + 1e-38)
