@@ -515,7 +515,8 @@ int moe_norm_forward(const moe_norm_t* n, const void* x, const void* residual, c
                      const float* beta, void* h, void* y, float* mean, float* rstd,
                      moe_stream_t stream);
 
-/* Workspace of moe_norm_backward: a zero-filled header and partial sums (256-byte aligned). */
+/* Workspace of moe_norm_backward (256-byte aligned): a zero-filled header of 256 bytes, and partial
+ * sums that may hold anything. */
 int moe_norm_workspace_bytes(const moe_norm_t* n, size_t* bytes);
 
 /*

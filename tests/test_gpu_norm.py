@@ -271,3 +271,31 @@ def test_refusals(native_lib):
     for call in bad:
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,pad,off", [(1, 64, 0, 0), (5000, 64, 0, 0), (5000, 1003, 3, 1), (3000, 4096, 0, 0),
+                                               (700, 8192, 0, 0), (700, 8191, 0, 0), (400, 16384, 0, 0),
+                                               (300, 20001, 0, 1), (9000, 20000, 0, 0)])
+def test_backward_workspace_holds_all_that_is_written(native_lib, dtype, rows, cols, pad, off):
+    """A workspace of exactly the bytes asked for, arbitrary beyond its header; the call's own one is
+    no larger: 160 partials of two column sums."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    gen = generator(rows + cols)
+    h, dy = (strided(rows, cols, pad, off, dt, gen) for _ in range(2))
+    gamma = torch.randn(cols, generator=gen, device="cuda")
+    mean, rstd = torch.randn(rows, generator=gen, device="cuda"), torch.rand(rows, generator=gen, device="cuda")
+    dx, dg, db = torch.empty((rows, cols), dtype=dt, device="cuda"), torch.empty_like(gamma), torch.empty_like(gamma)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    block.layer_norm_backward(dy, h, gamma, mean, rstd, dx=dx, dgamma=dg, dbeta=db)
+    assert torch.cuda.max_memory_allocated() - before <= 160 * 2 * cols * 4 + 1024
+    want = [t.clone() for t in (dx, dg, db)]
+    n = block.layer_norm_workspace(rows, cols, dt).numel()
+    ws = torch.full((n + 65536,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    block.layer_norm_backward(dy, h, gamma, mean, rstd, dx=dx, dgamma=dg, dbeta=db, ws=ws[:n])
+    assert bool((ws[n:] == 0xFF).all())
+    for a, b in zip((dx, dg, db), want):
+        assert torch.equal(a, b)

@@ -491,8 +491,6 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
   }
 }
 
-constexpr int kMaxSlices = 608;  // four CTAs an SM
-
 int check_norm(const moe_norm_t* n) {
   if (!n || n->rows < 0 || n->cols < 1 || !(n->eps >= 0.f) || n->eps > 3.0e38f) return MOE_ERR_INVALID_ARG;
   if (n->dtype != MOE_F32 && n->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
@@ -501,11 +499,12 @@ int check_norm(const moe_norm_t* n) {
   return MOE_OK;
 }
 
-// The slices of rows that are not held whole share 2048 CTAs; the ring kernels write one an SM.
-int any_slices(int cols) { return std::max(1, std::min(kMaxSlices, 2048 / ((cols + kSliceCols - 1) / kSliceCols))); }
+// The ring kernels write a partial a CTA; the slices of rows that are not held whole share 2048 CTAs.
+int any_slices(int cols) {
+  return std::max(1, std::min(kMaxPartials, 2048 / ((cols + kSliceCols - 1) / kSliceCols)));
+}
 size_t norm_ws_bytes(const moe_norm_t& n) {
-  const int slices = n.cols <= 8192 ? kMaxSlices : std::max(any_slices(n.cols), 160);
-  return 256 + align256(size_t(slices) * 2 * size_t(n.cols) * 4);
+  return 256 + align256(size_t(kMaxPartials) * 2 * size_t(n.cols) * 4);
 }
 
 bool vec_ok(const void* p, int64_t ld, int vec, size_t eb) {
@@ -592,7 +591,7 @@ int norm_backward_ring(const moe_norm_t& n, const T* dy, const T* h, const float
                        cudaStream_t st) {
   constexpr int VEC = 16 / int(sizeof(T));
   const int L = row_lanes(n.cols, VEC, nv, G), slots = 32 * kRingWarps / L;
-  const int grid = int(std::min<int64_t>((n.rows + slots - 1) / slots, std::min(num_sms(), 160)));
+  const int grid = int(std::min<int64_t>((n.rows + slots - 1) / slots, std::min(num_sms(), kMaxPartials)));
   *slices = grid;
   auto go = [&](auto kern, int stages, auto) -> int {
     const size_t ring = size_t(stages) * (dh ? 3 : 2) * nv * 32 * kRingWarps * VEC * sizeof(T);

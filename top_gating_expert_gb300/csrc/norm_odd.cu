@@ -412,7 +412,7 @@ int norm_backward_odd(const moe_norm_t& n, const T* dy, const T* h, const float*
                       cudaStream_t st) {
   constexpr int VEC = 16 / int(sizeof(T));
   const int L = row_lanes(n.cols, VEC, nv, G), slots = 32 * kRingWarps / L;
-  const int grid = int(std::min<int64_t>((n.rows + slots - 1) / slots, std::min(num_sms(), 160)));
+  const int grid = int(std::min<int64_t>((n.rows + slots - 1) / slots, std::min(num_sms(), kMaxPartials)));
   *slices = grid;
   auto go = [&](auto kern, int stages, auto) -> int {
     const size_t cols = size_t(kRingWarps) * 32 * VEC * nv * 4;

@@ -15,6 +15,7 @@ struct Tag {};
 __device__ __forceinline__ float product(float a, float b) { return __fmul_rn(a, b); }
 
 constexpr int kRingWarps = 16;
+constexpr int kMaxPartials = 160;  // partial column sums of a backward: the workspace holds as many
 
 // 16 bytes of this lane, global to shared, and the groups of such copies.
 __device__ __forceinline__ void copy_async(void* dst, const void* src) {
