@@ -561,7 +561,8 @@ typedef struct {
  * wait limit as every workspace's). backward: 1 for both directions, 0 for the forward
  * alone. unaligned: 1 makes room for the copies of every bf16 operand; 0 for those that the
  * strides call for (an operand that does not start on a 16-byte boundary then gives
- * MOE_ERR_WORKSPACE).
+ * MOE_ERR_WORKSPACE). The forward of one bf16 or up to eight fp32 tokens needs the 256 bytes
+ * alone. Nothing beyond them has to hold any value.
  */
 int moe_linear_workspace_bytes(const moe_linear_t* p, int backward, int unaligned, size_t* bytes);
 

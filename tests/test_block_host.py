@@ -235,3 +235,22 @@ def test_scores_are_not_shared(native_lib):
     held = moe._score(d)._obj
     assert b.scale == 2.5 and moe.make_score(d).scale == 2.5 and held.scale == 2.5 and held.score == 1
     assert moe.make_score(a) is a and moe._score(a)._obj is a
+
+
+def test_workspace_sizes(native_lib):
+    """The header alone where nothing is copied or split; the norm's partials at most one an SM."""
+    def linear_bytes(back, un, **kw):
+        b = N.c_size_t()
+        assert native_lib.moe_linear_workspace_bytes(REF(lin(**kw)), back, un, REF(b)) == 0
+        return b.value
+
+    for un in (0, 1):
+        assert linear_bytes(0, un, T=1, N=14336, K=4097) == 256
+        assert linear_bytes(0, un, T=8, N=14336, K=4097, dtype=0) == 256
+    assert linear_bytes(0, 0, T=8192, N=14336, K=4096) == 256
+    assert linear_bytes(0, 1, T=8192, N=14336, K=4096) >= 256 + 2 * 4096 * (8192 + 14336)
+    b = N.c_size_t()
+    for cols in (1, 64, 8192, 20000):
+        n = norm(rows=1 << 20, cols=cols, ldx=cols, ldr=cols, ldh=cols, ldy=cols)
+        assert native_lib.moe_norm_workspace_bytes(REF(n), REF(b)) == 0
+        assert b.value <= 256 + 160 * 2 * cols * 4 + 255

@@ -352,3 +352,47 @@ def test_more_rows_than_a_grid_axis_has_tiles(native_lib, dtype, N):
         for at in (slice(0, 700), slice(65535 * 128 - 300, 65535 * 128 + 300), slice(T - 300, T)):
             ref, s = x[at, :2].double() @ wide.double(), x[at, :2].double().abs() @ wide.double().abs()
             assert_within(dx[at], ref, 2 * 5 * U * s + U * ref.abs() + 1e-38)
+
+
+@pytest.mark.parametrize("T,N,K,dtype,pad,off,room", [
+    (1, 512, 256, "bf16", 0, 0, 0), (1, 511, 257, "bf16", 3, 1, 0), (8, 100, 300, "f32", 3, 1, 0),
+    (300, 512, 256, "bf16", 0, 0, 0), (300, 512, 256, "bf16", 8, 8, 0), (300, 100, 257, "bf16", 0, 0, 400 * 264 * 2)])
+def test_forward_without_a_workspace_allocates_little(native_lib, T, N, K, dtype, pad, off, room):
+    """Operands on 16-byte rows, and few tokens, need the header alone; others room for their copies."""
+    gen, dt, x, W, bias = make(T, N, K, dtype, pad, off, T + N)
+    out = torch.empty((T, N), dtype=dt, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    got = block.linear(x, W, bias, out=out)
+    assert torch.cuda.max_memory_allocated() - before <= 512 + room + 1024 * bool(room)
+    check_forward(x, W, bias, "none", None, got, dt)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,K,pad,off", [(1, 70, 129, 3, 1), (200, 256, 512, 0, 0), (333, 130, 257, 3, 1),
+                                           (64, 1408, 2048, 8, 0), (1500, 768, 513, 0, 0)])
+def test_workspaces_hold_all_that_is_written(native_lib, dtype, T, N, K, pad, off):
+    """A workspace of exactly the bytes asked for, arbitrary beyond its header: the bytes after it stay
+    as they are and the results do not change."""
+    gen, dt, x, W, bias = make(T, N, K, dtype, pad, off, T + K)
+    dy, pre = strided(T, N, pad, off, dt, gen), strided(T, N, pad, off, dt, gen)
+
+    def results(ws_of):
+        y, p = block.linear(x, W, bias, act="silu", save_pre=True, ws=ws_of(0))
+        return (y, p, *block.linear_backward(dy, x, W, act="silu", pre=pre, ws=ws_of(1)))
+
+    want = results(lambda back: None)
+    for stale in (0xFF, 0x3C):
+        whole = []
+
+        def ws_of(back):
+            n = block.linear_workspace(T, N, K, dt, backward=bool(back)).numel()
+            whole.append((torch.full((n + 8192,), stale, dtype=torch.uint8, device="cuda"), n))
+            whole[-1][0][:256] = 0
+            return whole[-1][0][:n]
+
+        for a, b in zip(results(ws_of), want):
+            assert torch.equal(a, b)
+        for t, n in whole:
+            assert bool((t[n:] == stale).all())

@@ -97,6 +97,14 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _scratch(nbytes, dev, stream):
+    """A workspace for one call: zeros in its header, the rest as the allocator left it."""
+    ws = _new((nbytes,), torch.uint8, dev, stream)
+    with _on(stream):
+        ws[:256].zero_()
+    return ws
+
+
 # Argument structs by their values; the library reads them during a call only.
 @lru_cache(maxsize=512)
 def _norm_args(*fields):
@@ -137,12 +145,17 @@ def layer_norm(x, gamma, beta=None, eps=1e-5, residual=None, *, out=None, h=None
     return out, (x if h is None else h), mean, rstd
 
 
+@lru_cache(maxsize=512)
+def _norm_ws_bytes(T, M, dtype):
+    b = N.c_size_t()
+    _check(N.lib().moe_norm_workspace_bytes(_norm_args(T, M, dtype, 0.0, M, M, M, M), ctypes.byref(b)),
+           "moe_norm_workspace_bytes")
+    return b.value
+
+
 def layer_norm_workspace(T, M, dtype=torch.bfloat16, device="cuda"):
     """A zero-filled workspace for layer_norm_backward on [T, M] matrices."""
-    b = N.c_size_t()
-    _check(N.lib().moe_norm_workspace_bytes(_norm_args(T, M, _DTYPES[dtype], 0.0, M, M, M, M), ctypes.byref(b)),
-           "moe_norm_workspace_bytes")
-    return torch.zeros(b.value, dtype=torch.uint8, device=device)
+    return torch.zeros(_norm_ws_bytes(T, M, _DTYPES[dtype]), dtype=torch.uint8, device=device)
 
 
 def layer_norm_backward(dy, h, gamma, mean, rstd, dh=None, *, need_beta=True, dx=None, dgamma=None,
@@ -165,8 +178,8 @@ def layer_norm_backward(dy, h, gamma, mean, rstd, dh=None, *, need_beta=True, dx
             dgamma = torch.empty_like(gamma)
         if need_beta and dbeta is None:
             dbeta = torch.empty_like(gamma)
-        if ws is None:
-            ws = layer_norm_workspace(T, M, dt, dy.device)
+    if ws is None:
+        ws = _scratch(_norm_ws_bytes(T, M, _DTYPES[dt]), dev, stream)
     ldh = _matrix(dx, "dx", w, shape, dt, dev)
     _vector(dgamma, "dgamma", w, M, dev)
     if dbeta is not None:
@@ -179,15 +192,25 @@ def layer_norm_backward(dy, h, gamma, mean, rstd, dh=None, *, need_beta=True, dx
 
 
 # ------------------------------------------------------------------ linear layer
+@lru_cache(maxsize=512)
+def _linear_ws_bytes(backward, unaligned, *fields):
+    b = N.c_size_t()
+    _check(N.lib().moe_linear_workspace_bytes(_linear_args(*fields), backward, unaligned, ctypes.byref(b)),
+           "moe_linear_workspace_bytes")
+    return b.value
+
+
 def linear_workspace(T, N_out, K, dtype=torch.bfloat16, device="cuda", *, backward=True, aligned=False):
     """A zero-filled workspace for linear (and linear_backward, unless backward is False) with
     x [T, K] and W [N_out, K]. aligned: every matrix starts on a 16-byte boundary and has rows
     of a multiple of 16 bytes, so that no room is needed for copies of them."""
-    p = N.MoeLinear(T=T, N=N_out, K=K, act=N.LIN_ACTS["silu"], dtype=_DTYPES[dtype])
-    b = N.c_size_t()
-    _check(N.lib().moe_linear_workspace_bytes(ctypes.byref(p), int(bool(backward)), int(not aligned),
-                                              ctypes.byref(b)), "moe_linear_workspace_bytes")
-    return torch.zeros(b.value, dtype=torch.uint8, device=device)
+    n = _linear_ws_bytes(int(bool(backward)), int(not aligned), T, N_out, K, N.LIN_ACTS["silu"], _DTYPES[dtype])
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _unaligned(*ts):
+    """Whether a matrix starts off a 16-byte boundary: it is copied whatever its stride."""
+    return int(any(t.data_ptr() % 16 for t in ts))
 
 
 def linear(x, W, bias=None, *, act="none", residual=None, save_pre=False, out=None, pre=None, ws=None,
@@ -195,7 +218,9 @@ def linear(x, W, bias=None, *, act="none", residual=None, save_pre=False, out=No
     """(y, pre): y = act(x W^T + bias) + residual for x [T, K], W [N, K], bias float32 [N],
     residual [T, N]; pre = x W^T + bias is stored when save_pre (or a buffer for it) is given,
     for linear_backward, and None otherwise. act: "none", "relu", "gelu", "gelu_tanh", "silu".
-    """
+    Without ws the call allocates what it needs (256 bytes, and room for copies of bf16 operands
+    on no 16-byte rows); the status word goes with it, so who wants to ask moe.device_status
+    whether a wait ran out keeps a workspace of their own."""
     w = "linear"
     code = N.LIN_ACTS.get(act)
     if code is None:
@@ -213,8 +238,7 @@ def linear(x, W, bias=None, *, act="none", residual=None, save_pre=False, out=No
     if save_pre and pre is None:
         pre = _new(shape, dt, dev, stream)
     if ws is None:
-        with _on(stream):
-            ws = linear_workspace(T, n_out, K, dt, x.device, backward=False)
+        ws = _scratch(_linear_ws_bytes(0, _unaligned(x, W), T, n_out, K, code, _DTYPES[dt], ldx, ldw), dev, stream)
     ldy = _matrix(out, "out", w, shape, dt, dev)
     ldp = n_out if pre is None else _matrix(pre, "pre", w, shape, dt, dev)
     _workspace_ok(ws, w, dev)
@@ -227,7 +251,7 @@ def linear_backward(dy, x, W, *, act="none", pre=None, need_x=True, need_W=True,
                     dW=None, dbias=None, ws=None, stream=None):
     """(dx, dW, dbias) of linear from dy [T, N] and the stored pre (not needed for act "none");
     dx and dW in the element type, dbias float32; None for what is not needed. The gradient
-    of the residual is dy itself."""
+    of the residual is dy itself. ws as in linear."""
     w = "linear_backward"
     code = N.LIN_ACTS.get(act)
     if code is None:
@@ -247,8 +271,8 @@ def linear_backward(dy, x, W, *, act="none", pre=None, need_x=True, need_W=True,
     if need_bias and dbias is None:
         dbias = _new((n_out,), _F32, dev, stream)
     if ws is None:
-        with _on(stream):
-            ws = linear_workspace(T, n_out, K, dt, dy.device)
+        ws = _scratch(_linear_ws_bytes(1, _unaligned(dy, x, W), T, n_out, K, code, _DTYPES[dt], ldx, ldw, ldy), dev,
+                      stream)
     lddx = K if dx is None else _matrix(dx, "dx", w, (T, K), dt, dev)
     lddw = K if dW is None else _matrix(dW, "dW", w, (n_out, K), dt, dev)
     if dbias is not None:

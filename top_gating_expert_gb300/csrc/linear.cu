@@ -165,8 +165,12 @@ struct Carver {
   }
 };
 
+// Few tokens forward: W is streamed row by row, nothing copied and no partial sums.
+bool few_tokens(const moe_linear_t& p) { return p.T <= (p.dtype == MOE_BF16 ? 1 : 8); }
+
 size_t ws_need(const moe_linear_t& p, bool backward, bool all) {
   Carver c{nullptr};
+  if (!backward && few_tokens(p)) return c.at;
   const int64_t Kp = up8(p.K), Np = up8(p.N);
   if (p.dtype == MOE_F32) {
     c.take(kPartBytes);
@@ -262,7 +266,7 @@ int moe_linear_forward(const moe_linear_t* p, const void* x, const void* W, cons
   e.bias = bias; e.res = residual; e.out = y; e.pre = pre;
   e.ldo = q.ldy; e.ldr = q.ldr; e.ldp = q.ldp;
   e.act = q.act;
-  if (q.T <= (q.dtype == MOE_BF16 ? 1 : 8))  // few tokens: W streamed row by row, nothing copied
+  if (few_tokens(q))
     return launch_linear_few(q.dtype == MOE_BF16, x, q.ldx, W, q.ldw, q.T, q.N, q.K, e, stream);
   Carver c{static_cast<char*>(ws)};
   if (q.dtype == MOE_F32) {
