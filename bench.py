@@ -32,6 +32,7 @@ import statistics
 import subprocess
 import sys
 import tempfile
+import threading
 import time
 
 ROOT = os.path.dirname(os.path.abspath(__file__))
@@ -63,6 +64,35 @@ _T0 = time.perf_counter()
 def log(msg: str):
     """A progress line on stderr (the JSON line alone goes to stdout)."""
     print(f"[bench {time.perf_counter() - _T0:7.1f} s] {msg}", file=sys.stderr, flush=True)
+
+
+class GpuStalled(RuntimeError):
+    """The GPU did not finish the work enqueued so far within the limit of a wait."""
+
+
+def bounded(wait, limit_s: float, what: str):
+    """wait() (a blocking call that releases the interpreter) on a thread of its own: its result
+    within limit_s seconds, or GpuStalled; the thread stays behind then."""
+    done, failed = threading.Event(), []
+
+    def run():
+        try:
+            wait()
+        except BaseException as exc:  # noqa: BLE001 (handed on below)
+            failed.append(exc)
+        done.set()
+
+    threading.Thread(target=run, daemon=True).start()
+    if not done.wait(limit_s):
+        raise GpuStalled(f"{what}: the GPU did not finish within {limit_s:.0f} s")
+    if failed:
+        raise failed[0]
+
+
+def stall_limit_s(args) -> float:
+    """No step of any preset takes 20 ms, and no phase enqueues more than the steps (warm-ups
+    among them) twice: a second for each, and what a first launch may take."""
+    return 120.0 + 2.0 * (args.steps + args.warmup)
 
 
 def parse(argv=None):
@@ -484,6 +514,7 @@ def run_preset(args, n, cfg, rank, world, dev, flush, barrier, *, headline: bool
     for _ in range(args.warmup):
         flush()
         step()
+    barrier()
     check("after warm-up")
 
     # ---- the whole forward (moe_layer_forward) captured once as a CUDA graph
@@ -498,6 +529,7 @@ def run_preset(args, n, cfg, rank, world, dev, flush, barrier, *, headline: bool
         graph_ok = False
         print(f"preset {n}: graph capture failed ({exc}); timing eager moe_layer_forward",
               file=sys.stderr)
+    barrier()
     check("after graph warm-up")
     clocks = ClockSampler(dev.index or 0)
     time.sleep(0.3)
@@ -670,7 +702,22 @@ def run_preset(args, n, cfg, rank, world, dev, flush, barrier, *, headline: bool
     return res
 
 
+def measure_others(args, measure):
+    """({preset: measure(preset)}, stalled): after a preset whose work the GPU did not finish, none
+    is measured, and what there is (the headline among it) is still reported."""
+    others = {}
+    for m in other_presets(args):
+        try:
+            others[m] = measure(m)
+        except GpuStalled as exc:
+            log(f"preset {m}: {exc}; not measured, nor are those after it")
+            others[m] = {"stalled": str(exc)}
+            return others, True
+    return others, False
+
+
 def run_ours(args, rank, world, local_rank):
+    """(the line, or None off rank 0; whether the GPU stalled in one of the other presets)"""
     import torch
     import torch.distributed as dist
 
@@ -678,21 +725,24 @@ def run_ours(args, rank, world, local_rank):
     dev = torch.device("cuda", local_rank)
     flush = Flush(dev)
 
-    def barrier():
+    def finish():
         if world > 1:
+            torch.cuda.set_device(local_rank)
             dist.barrier()
-        torch.cuda.synchronize()
+        torch.cuda.synchronize(dev)
+
+    def barrier():
+        bounded(finish, stall_limit_s(args), "barrier")
 
     n = args.config
     cfg = preset_for(args)
     head = run_preset(args, n, cfg, rank, world, dev, flush, barrier, headline=True,
                       variants=(args.variants_preset == n))
-    others = {}
-    for m in other_presets(args):
-        others[m] = run_preset(args, m, preset_for(args, m), rank, world, dev, flush, barrier,
-                               headline=False, variants=(args.variants_preset == m))
+    others, stalled = measure_others(
+        args, lambda m: run_preset(args, m, preset_for(args, m), rank, world, dev, flush, barrier,
+                                   headline=False, variants=(args.variants_preset == m)))
     if rank != 0:
-        return None
+        return None, stalled
 
     line = {
         "metric": METRIC, "value": head["value"], "unit": UNIT, "n_gpus": world,
@@ -721,7 +771,7 @@ def run_ours(args, rank, world, local_rank):
         line["presets"] = presets
     if var is not None:
         line["variants"] = var
-    return line
+    return line, stalled
 
 
 # ------------------------------------------------------------------ routing variants
@@ -924,6 +974,7 @@ def main():
     rank = int(os.environ.get("RANK", "0"))
     world = int(os.environ.get("WORLD_SIZE", "1"))
     local_rank = int(os.environ.get("LOCAL_RANK", "0"))
+    stalled = False
     if args.impl == "reference":
         line = run_reference(args, rank, world)
     else:
@@ -932,12 +983,20 @@ def main():
             import torch.distributed as dist
             torch.cuda.set_device(local_rank)
             dist.init_process_group("nccl", device_id=torch.device("cuda", local_rank))
-        line = run_ours(args, rank, world, local_rank)
-        if world > 1:
+        try:
+            line, stalled = run_ours(args, rank, world, local_rank)
+        except GpuStalled as exc:  # in the headline workload: there is nothing to report
+            log(f"{exc}; no result")
+            sys.stderr.flush()
+            os._exit(1)
+        if world > 1 and not stalled:
             import torch.distributed as dist
             dist.destroy_process_group()
     if line is not None:
         print(json.dumps(line), flush=True)
+    if stalled:  # the interpreter's own exit would wait for the GPU's work
+        sys.stdout.flush()
+        os._exit(0)
 
 
 if __name__ == "__main__":

@@ -142,3 +142,30 @@ def test_backward_summary_bounds():
     b1 = bench.backward_summary(PRESETS[1], 512, 256, 1, 0.05, 0.1, P)
     assert b1["bound"] == "latency" and b1["roofline_frac"] is None
     assert b1["train_tokens_per_s"] == round(256 / 0.15e-3, 1)
+
+
+def test_a_stalled_preset_does_not_take_the_others_along():
+    """What was measured before it (and its own message) is reported; those after it are not run."""
+    import threading
+    import time
+    never, ran = threading.Event(), []
+
+    def measure(m):
+        ran.append(m)
+        if m == 4:
+            bench.bounded(never.wait, 0.05, "barrier")
+        return {"value": m}
+
+    args = _args()
+    t = time.perf_counter()
+    others, stalled = bench.measure_others(args, measure)
+    assert stalled and ran == [1, 2, 4] and time.perf_counter() - t < 10
+    assert others[1] == {"value": 1} and others[2] == {"value": 2} and "did not finish" in others[4]["stalled"]
+    never.set()
+    assert bench.measure_others(args, lambda m: {"value": m}) == ({m: {"value": m} for m in (1, 2, 4, 5)}, False)
+    bench.bounded(lambda: None, 5.0, "barrier")
+    with pytest.raises(ZeroDivisionError):
+        bench.bounded(lambda: 1 // 0, 5.0, "barrier")
+    # room for the work itself: the largest step takes 13 ms
+    assert bench.stall_limit_s(args) > 100 + 0.02 * (args.steps + args.warmup)
+    assert bench.stall_limit_s(_args("--steps", "100000")) > 0.02 * 100000
