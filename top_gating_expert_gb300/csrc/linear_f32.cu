@@ -13,7 +13,7 @@
 // tiles of 64, 32 or 16 x 128 along it (linear_f32_narrow_kernel), rows and columns changing places where the
 // columns are the short side: 16384 x 16 x 4096 forward 96 us (365 in whole tiles; 268 MB of x, 40 us),
 // 16384 x 64 x 8192 420 (718), 16 x 4096 x 4096 25 us (61). When the
-// tiles are fewer than half of what the SMs hold, the K range is split over grid.y; the partial tiles
+// tiles are fewer than half of what the SMs hold, the K range is split over grid.z; the partial tiles
 // are then added in split order by a second kernel, which applies the epilogue. 2048^3: 349 us, 49
 // TFLOP/s (the library's product 293): the multiply-adds' rate (213 us), 256 tiles on 304 places, and
 // the waits on shared memory of four warps a scheduler bound it. (8 x 16 outputs a thread with half
@@ -31,6 +31,8 @@ constexpr int kTile = 128, kDepth = 16, kThreadsF = 256;
 // (16384 x 16 x 4096 with four, at 64 registers a thread, 106 us, with three 96; 2000 x 50 x 5000 with
 // three 37.5, with two 33.4)
 constexpr int ctas_per_sm(int rows) { return rows > 32 ? 2 : 3; }
+
+constexpr int64_t kGridY = 65535;  // rows of tiles that one launch takes
 
 struct Operand {
   const float* p;
@@ -115,14 +117,14 @@ __device__ __forceinline__ void emit(const LinearEpi& e, int64_t i, int64_t j, f
 
 template <int ACT, bool AK, bool BK>  // AK, BK: the operand's unit stride is k's
 __global__ void __launch_bounds__(kThreadsF, ctas_per_sm(kTile))
-    linear_f32_kernel(Operand A, Operand B, int tiles_x, int K, int kchunk, float* part, LinearEpi e) {
+    linear_f32_kernel(Operand A, Operand B, int K, int kchunk, float* part, LinearEpi e) {
   constexpr int RT = 8, P = kTile + 4;  // rows a thread, pitch
   __shared__ __align__(16) float sA[2][kDepth * P], sB[2][kDepth * P];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int i0 = int(blockIdx.x / tiles_x) * kTile, j0 = int(blockIdx.x % tiles_x) * kTile;
-  const int64_t k0 = int64_t(blockIdx.y) * kchunk, k1 = min(int64_t(K), k0 + kchunk);
+  const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile;
+  const int64_t k0 = int64_t(blockIdx.z) * kchunk, k1 = min(int64_t(K), k0 + kchunk);
   f32x2 acc[RT][4];  // row r, column pairs
 #pragma unroll
   for (int a = 0; a < RT; ++a)
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(kThreadsF, ctas_per_sm(kTile))
     buf ^= 1;
   }
   // thread (ty, tx): rows 4 ty .. + 3 (and 64 + 4 ty ..), columns 4 tx .. and 64 + 4 tx ..
-  float* pt = part ? part + int64_t(blockIdx.y) * A.rows * B.rows : nullptr;
+  float* pt = part ? part + int64_t(blockIdx.z) * A.rows * B.rows : nullptr;
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     const int64_t i = i0 + (r >> 2) * 64 + ty * 4 + (r & 3);
@@ -189,16 +191,15 @@ __global__ void __launch_bounds__(kThreadsF, ctas_per_sm(kTile))
 // k (64 / ROWS groups of them), and the groups' sums are added through shared memory in group order.
 template <int ACT, int ROWS, bool AK, bool BK>
 __global__ void __launch_bounds__(kThreadsF, ctas_per_sm(ROWS))
-    linear_f32_narrow_kernel(Operand A, Operand B, int tiles_x, int K, int kchunk, float* part, int swap,
-                             LinearEpi e) {
+    linear_f32_narrow_kernel(Operand A, Operand B, int K, int kchunk, float* part, int swap, LinearEpi e) {
   constexpr int GROUPS = 64 / ROWS, DEPTH = kDepth / GROUPS, PA = ROWS + 4, PB = kTile + 4;
   constexpr int SLICE = kDepth * (PA + PB), SUMS = GROUPS * ROWS * PB;
   __shared__ __align__(16) float s_all[2 * SLICE > SUMS ? 2 * SLICE : SUMS];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, tx = tid & 31, ty = (tid >> 5) % (ROWS / 8), grp = tid / (4 * ROWS);
-  const int i0 = int(blockIdx.x / tiles_x) * ROWS, j0 = int(blockIdx.x % tiles_x) * kTile;
-  const int64_t k0 = int64_t(blockIdx.y) * kchunk, k1 = min(int64_t(K), k0 + kchunk);
+  const int i0 = blockIdx.y * ROWS, j0 = blockIdx.x * kTile;
+  const int64_t k0 = int64_t(blockIdx.z) * kchunk, k1 = min(int64_t(K), k0 + kchunk);
   f32x2 acc[8][2];
 #pragma unroll
   for (int a = 0; a < 8; ++a) acc[a][0] = acc[a][1] = 0ull;
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kThreadsF, ctas_per_sm(ROWS))
     __syncthreads();
     buf ^= 1;
   }
-  float* pt = part ? part + int64_t(blockIdx.y) * A.rows * B.rows : nullptr;
+  float* pt = part ? part + int64_t(blockIdx.z) * A.rows * B.rows : nullptr;
   if constexpr (GROUPS == 1) {
     auto leave = [&](auto swapped) {
 #pragma unroll
@@ -310,7 +311,19 @@ int launch_linear_f32(const float* A, int64_t a_i, int64_t a_k, const float* B, 
   if (swap) std::swap(oa, ob);
   const int tile_rows = oa.rows <= 16 ? 16 : (oa.rows <= 32 ? 32 : (oa.rows <= 64 ? 64 : kTile));
   const int64_t ty = (oa.rows + tile_rows - 1) / tile_rows, tx = (ob.rows + kTile - 1) / kTile;
-  if (tx * ty > INT32_MAX) return MOE_ERR_UNSUPPORTED;  // (140 TB of output)
+  if (ty > kGridY) {  // (not swapped: a swapped side has 64 rows at most)
+    const int most = int(kGridY) * kTile;
+    for (int r = 0; r < rows; r += most) {
+      LinearEpi part_e = e;
+      part_e.out = static_cast<float*>(e.out) + r * e.ldo;
+      if (e.pre) part_e.pre = static_cast<float*>(e.pre) + r * e.ldp;
+      if (e.res) part_e.res = static_cast<const float*>(e.res) + r * e.ldr;
+      const int rc = launch_linear_f32(A + r * a_i, a_i, a_k, B, b_j, b_k, std::min(most, rows - r), cols, K, part_e,
+                                       part, st);
+      if (rc != MOE_OK) return rc;
+    }
+    return MOE_OK;
+  }
   // splits: about as many tiles as the SMs hold, at least 64 deep each, within the scratch
   int splits = 1;
   const int64_t room = ctas_per_sm(tile_rows) * num_sms();
@@ -325,15 +338,15 @@ int launch_linear_f32(const float* A, int64_t a_i, int64_t a_k, const float* B, 
   auto go = [&](auto act, auto ak, auto bk) {
     constexpr int ACT = decltype(act)::value;
     constexpr bool AK = decltype(ak)::value, BK = decltype(bk)::value;
-    const dim3 grid = dim3(unsigned(tx * ty), unsigned(splits));  // tiles along one axis: it holds 2^31
+    const dim3 grid = dim3(unsigned(tx), unsigned(ty), unsigned(splits));
     float* const to = splits > 1 ? part : nullptr;
     auto narrow = [&](auto kern) {
-      return launch_kernel(kern, grid, dim3(kThreadsF), 0, st, oa, ob, int(tx), K, kchunk, to, swap, e);
+      return launch_kernel(kern, grid, dim3(kThreadsF), 0, st, oa, ob, K, kchunk, to, swap, e);
     };
     if (tile_rows == 16) return narrow(linear_f32_narrow_kernel<ACT, 16, AK, BK>);
     if (tile_rows == 32) return narrow(linear_f32_narrow_kernel<ACT, 32, AK, BK>);
     if (tile_rows == 64) return narrow(linear_f32_narrow_kernel<ACT, 64, AK, BK>);
-    return launch_kernel(linear_f32_kernel<ACT, AK, BK>, grid, dim3(kThreadsF), 0, st, oa, ob, int(tx), K, kchunk, to, e);
+    return launch_kernel(linear_f32_kernel<ACT, AK, BK>, grid, dim3(kThreadsF), 0, st, oa, ob, K, kchunk, to, e);
   };
   const bool ak = oa.sk == 1, bk = ob.sk == 1;
   constexpr std::bool_constant<true> yes{};
