@@ -48,3 +48,49 @@ def test_wait_limit_times_out_then_recovers(native_lib):
     ref = O.router_logits(inp.np["x"][rows], inp.np["W_g"])
     assert_close(got[rows], ref, LOGIT_RTOL["bf16"], "logits after the timeout")
     assert np.isfinite(got).all()
+
+
+@pytest.mark.parametrize("act", ["relu", "swiglu"])
+@pytest.mark.parametrize("limit_ns", [1, 1000, 5000])
+def test_pairs_that_give_up_leave_nothing_behind(native_lib, act, limit_ns):
+    """The expert GEMMs' CTA pairs and the backward's GEMMs with limits that stop the two CTAs of a
+    pair at k-blocks of their own: a status, and with the default limit the very next calls, on the
+    same SMs and shared memory, give what they gave before, bit for bit."""
+    cfg = dict(S=3000, G=1, E=6, M=4096, H=4096, k=2, capacity_factor=0.0, random_routing=0, n_shared=1,
+               H_shared=512, act=act, dtype="bf16", bias=False)
+    inp = make_inputs(cfg, seed=9)
+    layer = moe.MoeLayer(cfg, inp.host)
+    layer.enable_backward(inp.host)
+    c, out = layer.cfg, layer.route_out
+    x = inp.host["x"].cuda()
+    dy = torch.randn((c.S, c.M), generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    names = ["dx", "dW_g", "dW_in", "dW_out", "dWs_in", "dWs_out"] + (["dW_up", "dWs_up"] if act == "swiglu" else [])
+
+    def step():
+        y = layer.forward(x, residual=x).clone()
+        g = layer.backward(x, dy, residual=True, aux_coef=0.1)
+        got = [y] + [getattr(g, n).clone() for n in names]
+        assert moe.device_status(layer.ws) == 0 and moe.device_status(layer.ws_bwd) == 0
+        return got
+
+    want = step()
+    R = moe.rows_max(c)
+    x_perm, h, y_perm = (torch.zeros((R, n), dtype=torch.bfloat16, device="cuda") for n in (c.M, c.H, c.M))
+    hs, so = (torch.zeros((c.S, n), dtype=torch.bfloat16, device="cuda") for n in (c.n_shared * c.H_shared, c.M))
+    moe.dispatch(c, x, out, x_perm)
+    for _ in range(4):
+        moe.set_wait_limit(layer.ws, limit_ns)
+        moe.expert_ffn(c, x_perm, out.expert_offsets, out.w_perm, layer.W_in_packed, layer.W_out_packed, h, y_perm,
+                       layer.ws)
+        moe.shared_ffn(c, x, layer.Ws_in_packed, layer.Ws_out_packed, hs, so, layer.ws)
+        moe.set_wait_limit(layer.ws, 0)
+        gave_up = moe.device_status(layer.ws)
+        assert gave_up in ((MOE_ERR_TIMEOUT,) if limit_ns == 1 else (0, MOE_ERR_TIMEOUT))
+        for a, b in zip(step(), want):
+            assert torch.equal(a, b)
+        moe.set_wait_limit(layer.ws_bwd, limit_ns)
+        layer.backward(x, dy, residual=True, aux_coef=0.1)
+        moe.set_wait_limit(layer.ws_bwd, 0)
+        assert moe.device_status(layer.ws_bwd) in (0, MOE_ERR_TIMEOUT)
+        for a, b in zip(step(), want):
+            assert torch.equal(a, b)

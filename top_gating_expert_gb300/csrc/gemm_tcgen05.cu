@@ -36,7 +36,7 @@
 // Tiles are ordered group by group, then by N tile, then by M tile, so the CTAs that run
 // at the same time share each weight tile through L2.
 //
-// Every wait is bounded: after the wait limit (2 s unless set in the workspace header) a
+// Every mbarrier wait is bounded: after the wait limit (2 s unless set in the workspace header) a
 // waiting thread sets the status word's timeout bit and a CTA-wide abort flag; every role
 // then stops and, after a CTA barrier, the producer waits for its loads in flight and the
 // MMA thread for its MMAs, whichever role gave up; TMEM is freed before the CTA exits.
@@ -657,6 +657,8 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps<EPI, KRAG>(), 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 5);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_total = reinterpret_cast<int*>(s_tmem + 2);
+  // pairs: written by the other CTA at its end, the k-blocks it loaded and (top bit) that it gave up
+  volatile uint32_t* s_peer = s_tmem + 3;
   int* s_tstart = reinterpret_cast<int*>(s_tmem + 4);  // [groups+1] first m-tile of each group
   int* s_off = s_tstart + (kMaxGroups + 1);            // [groups+1] first row of each group
   int* s_koff = s_off + (kMaxGroups + 1);              // K-ragged: [groups+1] K offsets
@@ -780,8 +782,8 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps<EPI, KRAG>(), 1)
   };
 
   // what each role has in flight, for the drain after an abort: the stages whose last load
-  // the producer issued (and that load's phase), whether the MMA thread issued MMAs and
-  // has already waited for them
+  // the producer issued (and that load's phase; pairs: the k-blocks it loaded), whether the MMA
+  // thread issued MMAs and has already waited for them
   uint32_t issued = 0, issued_par = 0;
   bool mma_any = false, mma_drained = false;
   if (warp == 0) {
@@ -834,8 +836,12 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps<EPI, KRAG>(), 1)
           }
         }
         __syncwarp();
-        issued |= 1u << stage;
-        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if constexpr (PAIR) {
+          ++issued;
+        } else {
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        }
         if (++stage == C::STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -967,14 +973,37 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps<EPI, KRAG>(), 1)
 
   tc_fence_before();
   __syncthreads();
-  if (*s_abort) {
+  bool gave_up = *s_abort != 0;  // (read after the barrier: the whole CTA takes the same branch)
+  if constexpr (PAIR) {
+    if (warp == 0 && lane == 0)
+      st_cluster_u32(cluster_addr(smem_u32(const_cast<uint32_t*>(s_peer)), rank ^ 1u),
+                     (issued & 0x7fffffffu) | (gave_up ? 0x80000000u : 0u));
+    __syncwarp();
+    cluster_sync_all();  // both CTAs done with TMEM and each other's barriers
+    gave_up = gave_up || (*s_peer >> 31) != 0u;
+  }
+  if (gave_up) {
     // A role may have finished its own loop before another gave up, with loads or MMAs still
-    // in flight: every load issued lands (the even CTA's full barriers also count the odd
-    // CTA's bytes) and every MMA issued finishes before shared and tensor memory go away.
-    // The flag is read after the barrier, so every thread of the CTA takes this branch.
+    // in flight: every load issued lands and every MMA issued finishes before shared and tensor
+    // memory go away. A pair's producers are at most a use of each stage apart, and the even
+    // CTA's full barriers count both CTAs' bytes: for a k-block that only one of them loaded the
+    // other's part is settled first (its bytes taken as come, or the arrival that it would have
+    // made).
     if (warp == 0 && leader && lane == 0) {
-      for (int s = 0; s < C::STAGES; ++s)
-        if ((issued >> s) & 1u) wait_drain(full0 + 8 * s, (issued_par >> s) & 1u);
+      if constexpr (PAIR) {
+        const uint32_t mine = issued & 0x7fffffffu, theirs = *s_peer & 0x7fffffffu;
+        const uint32_t lo = min(mine, theirs), hi = max(mine, theirs);
+        for (uint32_t j = lo; j < hi; ++j) {
+          const uint32_t fb = full0 + 8 * (j % C::STAGES);
+          if (mine > theirs) mbar_complete_tx(fb, C::STAGE_BYTES);
+          else mbar_expect_tx(fb, C::STAGE_BYTES);
+        }
+        for (uint32_t j = hi > uint32_t(C::STAGES) ? hi - C::STAGES : 0u; j < hi; ++j)
+          wait_drain(full0 + 8 * (j % C::STAGES), (j / C::STAGES) & 1u);
+      } else {
+        for (int s = 0; s < C::STAGES; ++s)
+          if ((issued >> s) & 1u) wait_drain(full0 + 8 * s, (issued_par >> s) & 1u);
+      }
     }
     if (warp == 1 && leader && lane == 0 && mma_any && !mma_drained) {
       if constexpr (PAIR) mma_commit_pair(drain_bar, uint16_t(1));
@@ -983,8 +1012,8 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps<EPI, KRAG>(), 1)
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();  // the odd CTA's shared memory is read until here
   }
-  if constexpr (PAIR) cluster_sync_all();  // both CTAs done with TMEM and each other's smem
   if (warp == 1) {
     tc_fence_after();
     if constexpr (PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);

@@ -22,7 +22,7 @@
 // 0.16: bound by the operands' way from L2 (32 KB a k-block for 128 x 128 outputs). 64 x 14336 x
 // 4096: 27 us, W at 4.3 TB/s on 112 of the 152 SMs.
 //
-// Every wait is bounded, as in the grouped GEMM: a role that gives up sets the status word
+// Every mbarrier wait is bounded, as in the grouped GEMM: a role that gives up sets the status word
 // and the CTA's abort flag, the loads and MMAs in flight are drained, TMEM is freed.
 #include <algorithm>
 #include <type_traits>

@@ -1,6 +1,9 @@
 // Inline-PTX wrappers for sm_100-family (sm_103a) kernels: mbarriers, TMA (cp.async.bulk.tensor),
 // tcgen05 tensor-memory allocation, MMA, commit and loads, cluster addressing. Shared by the
-// GEMM and routing translation units; every wait is bounded (wait_limit_ns, kWaitLimitNs).
+// GEMM and routing translation units. Every wait on an mbarrier is bounded (wait_limit_ns,
+// kWaitLimitNs). What has no limit of its own (there is no such form): tcgen05.alloc, the CTA's and
+// the cluster's barriers, the wait on the previous kernel and on bulk stores; each waits for
+// threads whose own waits are bounded, or for the hardware.
 #pragma once
 
 #include <cuda.h>
