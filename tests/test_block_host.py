@@ -182,6 +182,7 @@ def test_launches_on_the_tensors_device(native_lib, monkeypatch, current):
         def __exit__(self, *exc):
             at.pop()
 
+    monkeypatch.setattr(moe, "_one_device", lambda: False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: at[-1], raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 100 + dev, raising=False)
     monkeypatch.setattr(torch.cuda, "device", Device)

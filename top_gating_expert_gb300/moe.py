@@ -66,13 +66,18 @@ def _entry(name: str):
     return getattr(N.lib(), name)
 
 
+@lru_cache(maxsize=None)
+def _one_device() -> bool:
+    return torch.cuda.device_count() == 1
+
+
 def _launch(name: str, t: torch.Tensor, stream, *args):
     """Calls a launching entry point on the stream (None: the current one of t's device), with
     t's device as the current one: the library launches there, and a default stream's handle
     names no device."""
     dev = t.get_device()
-    raw = _raw_stream(stream, dev)
-    if dev == torch._C._cuda_getDevice():
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if _one_device() or dev == torch._C._cuda_getDevice():
         rc = _entry(name)(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -148,7 +153,11 @@ class RouteOutputs:
                    z_loss=z((1,), torch.float32))
 
     def struct(self) -> N.MoeRouteOut:
-        at = tuple([getattr(self, f).data_ptr() for f in N.ROUTE_FIELDS])
+        # N.ROUTE_FIELDS one by one (this runs on every call of a serving loop)
+        at = (self.expert_id.data_ptr(), self.gate.data_ptr(), self.pos.data_ptr(), self.drop_reason.data_ptr(),
+              self.row.data_ptr(), self.counts.data_ptr(), self.counts_routed.data_ptr(),
+              self.expert_offsets.data_ptr(), self.token_of.data_ptr(), self.w_perm.data_ptr(),
+              self.aux_loss.data_ptr(), self.z_loss.data_ptr())
         held = self.__dict__.get("_struct")  # made anew when any field's memory is another
         if held is None or held[0] != at:
             held = self.__dict__["_struct"] = (at, N.MoeRouteOut(*at))
