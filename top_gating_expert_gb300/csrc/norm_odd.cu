@@ -14,7 +14,8 @@
 //
 // Measured (copy rate 6778 GB/s; in brackets one element a copy and a store): 65536 x 1003 fp32 forward
 // 92 us (215), with residual and the sum stored 178 us, 5.9 TB/s (263), backward with dh 167 us, 6.3 TB/s
-// (261); bf16 86 (162), 136 (204) and 146 us (277): half the bytes, bound by issue. Pieces shifted in
+// (261); bf16 86 (162), 136 (204) and 146 us (277): half the bytes, as many
+// instructions (64 and 72 % of the issue slots with four warps a scheduler). Pieces shifted in
 // registers to 16 bytes of consecutive columns a lane, the results turned to words in shared memory,
 // took 240 and 176 us for the two backwards.
 #include <algorithm>

@@ -12,10 +12,12 @@
 // when two values that decide (neighbours among the k + 1 best, the last group kept and the
 // first one not) lie within that bound are those evaluated in fp64, a lane each. All tokens in
 // fp64 took 1640 us for 16384 tokens of 256 experts, top-8 in 4 of 8 groups; now 45 us, of
-// which this kernel takes 27. It is bound by issue: about 860 instructions a token (an
-// exponential and a reciprocal an expert, two warp maxima a group, one a choice), 128 CTAs on
-// 152 SMs; memory (16.8 MB of logits) would take 3 us. 65536 tokens of 64 experts, top-2, softmax
-// scores, capacity: 39 us. One token: 10 us alone in a chain of launches.
+// which this kernel takes 27. It waits on latency: four warps a scheduler (128 CTAs of 16 on 152
+// SMs) take 45 % of the issue slots, each warp's 860 instructions a token (an exponential and a
+// reciprocal an expert, two warp maxima a group, one a choice) hang together, and a token's logits
+// are asked for when its turn comes; issue alone would take 13 us, memory (16.8 MB of logits) 3. 65536
+// tokens of 64 experts, top-2, softmax scores, capacity: 39 us, 22 here (52 % of the slots, 1.7 waves
+// of CTAs). One token: 10 us alone in a chain of launches.
 //
 // One CTA per chunk of 128 tokens of one group, a warp per token, lane l holding the experts
 // l, l + 32, .. (Q = 1, 2, 4 or 8 of them). The CTA then ranks its choices per (choice rank,
@@ -761,7 +763,7 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
 // close to 1. One exponential an expert serves all of it: x = exp(l) where the logits lie within
 // +-80 (their sum then neither overflows nor vanishes), s = x / (1 + x); else exp(l - max) for the
 // softmax and shifted sigmoids apart. 16384 x 256: 14 us (with three exponentials an expert 29);
-// bound by issue (62 % of the slots), by memory (8 S E bytes) 5 us.
+// 62 % of the issue slots are taken; memory (8 S E bytes) would take 5 us.
 constexpr int kBwdWarps = 8, kBwdTokens = 2;  // warps a CTA, consecutive tokens a warp
 
 template <int Q, bool SIG>
