@@ -762,9 +762,13 @@ __global__ void __launch_bounds__(kTokThreads, Q >= 4 ? 1 : 2) route_scored_kern
 // with ca = aux_coef E / (G S_g). 1 - s = 1 / (1 + exp(l)), so it keeps its precision where s is
 // close to 1. One exponential an expert serves all of it: x = exp(l) where the logits lie within
 // +-80 (their sum then neither overflows nor vanishes), s = x / (1 + x); else exp(l - max) for the
-// softmax and shifted sigmoids apart. 16384 x 256: 14 us (with three exponentials an expert 29);
+// softmax and shifted sigmoids apart. 16384 x 256: 15 us (with three exponentials an expert 29);
 // 62 % of the issue slots are taken; memory (8 S E bytes) would take 5 us.
 constexpr int kBwdWarps = 8, kBwdTokens = 2;  // warps a CTA, consecutive tokens a warp
+// A lane without an expert brings exp(-80) into the sums (a select an expert to leave it out took 1 us
+// more): of a sum of exponentials above this, all 255 of them together are less than 5e-9. Below it
+// the token takes the general form, whose sums hold experts alone.
+constexpr float kFewest = 1e-24f;
 
 template <int Q, bool SIG>
 __global__ void __launch_bounds__(32 * kBwdWarps, 4)
@@ -792,7 +796,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4)
 #pragma unroll
     for (int i = 0; i < Q; ++i) {
       const int e = lane + 32 * i;
-      l[i] = e < E ? __ldg(lr + e) : 0.f;  // no expert: left out of the sums below, and f = 0
+      l[i] = e < E ? __ldg(lr + e) : -80.f;  // no expert (f = 0): see kFewest
       plain = plain && fabsf(l[i]) <= 80.f;  // false for NaN too
     }
     // the choices, lane j < k: expert, logit, gradient of its weight
@@ -817,10 +821,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4)
         f[i] = lane + 32 * i < E ? ca * float(counts_routed[int64_t(group) * E + lane + 32 * i]) : 0.f;
     }
     float s = 0.f, tot = 0.f, m = 0.f, lse;
-    if (__all_sync(kFull, plain)) {
+    bool fast = __all_sync(kFull, plain);
+    if (fast) {
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
-        const float x = lane + 32 * i < E ? expf(l[i]) : 0.f;
+        const float x = expf(l[i]);
         p[i] = x;
         s += x;
         if constexpr (SIG) {
@@ -831,11 +836,15 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4)
       }
       s = warp_sum(s);
       lse = logf(s);
-    } else {
+      fast = s > kFewest;
+    }
+    if (!fast) {
       m = -INFINITY;
+      s = tot = 0.f;
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
-        if (lane + 32 * i >= E || !isfinite(l[i])) l[i] = -INFINITY;
+        l[i] = lane + 32 * i < E ? __ldg(lr + lane + 32 * i) : -INFINITY;
+        if (!isfinite(l[i])) l[i] = -INFINITY;
         m = fmaxf(m, l[i]);
       }
       m = warp_max(m);
