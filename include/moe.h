@@ -458,7 +458,8 @@ int moe_route_scored(const moe_config_t* cfg, const moe_score_t* score, const fl
  *                         + z_coef * z_loss ) / d logits
  * dgate float [S, k]; r: the forward's routing outputs, of which expert_id, row (-1 = not
  * kept, no gradient) and counts_routed are read. Every entry of dlogits is written. No
- * workspace.
+ * workspace. (The selection bias is not read: after a forward that reported a non-finite one, a
+ * token that had to take that bias's expert, weight 0, gets the gradient of its score's weight.)
  */
 int moe_route_scored_backward(const moe_config_t* cfg, const moe_score_t* score,
                               const float* logits, const moe_route_out_t* r, const float* dgate,

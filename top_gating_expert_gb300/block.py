@@ -291,7 +291,7 @@ def _whole_rows(t, stream):
     if t.is_contiguous() and t.data_ptr() % 16 == 0:
         return t
     with _on(stream):
-        return t.clone(memory_format=torch.contiguous_format)
+        return t.detach().clone(memory_format=torch.contiguous_format)
 
 
 class MoeBlock:
