@@ -59,10 +59,12 @@ CPU_FLOPS_REFERENCE_STEP = 0.8e12
 
 
 _T0 = time.perf_counter()
+_PHASE = ["start"]  # the last progress line: what a stalled wait was in
 
 
 def log(msg: str):
     """A progress line on stderr (the JSON line alone goes to stdout)."""
+    _PHASE[0] = msg
     print(f"[bench {time.perf_counter() - _T0:7.1f} s] {msg}", file=sys.stderr, flush=True)
 
 
@@ -732,7 +734,7 @@ def run_ours(args, rank, world, local_rank):
         torch.cuda.synchronize(dev)
 
     def barrier():
-        bounded(finish, stall_limit_s(args), "barrier")
+        bounded(finish, stall_limit_s(args), f"after '{_PHASE[0]}'")
 
     n = args.config
     cfg = preset_for(args)
