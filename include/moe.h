@@ -8,7 +8,9 @@
  * plus the load-balancing (aux) loss and the router z-loss; its backward pass; and the
  * operators around it in a Transformer block: routing by expert scores with a selection bias
  * (moe_route_scored, moe_layer_*_scored), layer norm (moe_norm_*) and dense layers with bias,
- * activation and residual (moe_linear_*), each with its gradient.
+ * activation and residual (moe_linear_*), each with its gradient; and what closes a training step:
+ * the cross entropy of a linear head over a large vocabulary (moe_xent_*), the global norm of many
+ * gradients (moe_grad_norm) and AdamW over many tensors (moe_adamw_*).
  *
  * Sources, by page title and section:
  *   GShard summary page ("GShard: Scaling Giant Models with Conditional Computation and
@@ -582,6 +584,118 @@ int moe_linear_forward(const moe_linear_t* p, const void* x, const void* W, cons
 int moe_linear_backward(const moe_linear_t* p, const void* dy, const void* x, const void* W,
                         const void* pre, void* dx, void* dW, float* dbias, void* ws,
                         size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- cross entropy of a linear head */
+
+/*
+ * The head of a model: logits l = x W^T over a vocabulary of V, and each token's cross entropy
+ * with its target, without storing the logits:
+ *     lse[t] = log sum_v exp(l[t, v])
+ *     loss[t] = lse[t] - l[t, target[t]] + z_coef lse[t]^2      (the z-loss: MegaBlocks router §2)
+ * x [T, K], W [V, K] in the element type, target int64 [T]. A token whose target is ignore_index
+ * has loss 0 and no gradient; any other target outside of 0 .. V - 1 sets MOE_ERR_DEVICE_DATA, has
+ * loss NaN and no gradient. T >= 0, V >= 1, K >= 1, any size (MOE_ERR_UNSUPPORTED beyond T = 2^30, V
+ * or K = 2^22). Logits and sums are fp32. ld*: elements between rows (0: the row's length). bf16 runs on
+ * the tensor cores, operands on no 16-byte rows from copies in the workspace; fp32 is the
+ * plain-FMA path, meant for small models.
+ *   z_coef: finite, >= 0.
+ *   piece:  the vocabulary entries that the backward (fp32: both) takes at a time: 0 = chosen so
+ *           that a piece of logits takes about 512 MB (512 entries at least).
+ */
+typedef struct {
+  int32_t T, V, K;
+  int32_t dtype; /* MOE_F32 / MOE_BF16 */
+  int64_t ldx, ldw, lddx, lddw;
+  int64_t ignore_index;
+  float z_coef;
+  int32_t piece;
+} moe_xent_t;
+
+/* Workspace (256-byte aligned, its first 256 bytes zero before first use). backward: 1 for both
+ * directions, 0 for the forward alone; unaligned: as in moe_linear_workspace_bytes. */
+int moe_xent_workspace_bytes(const moe_xent_t* p, int backward, int unaligned, size_t* bytes);
+
+/* loss, lse: float [T]. stats: float [2], the mean loss over the tokens with a target (0 if there
+ * are none) and their number. */
+int moe_xent_forward(const moe_xent_t* p, const void* x, const void* W, const int64_t* target,
+                     float* loss, float* lse, float* stats, void* ws, size_t ws_bytes,
+                     moe_stream_t stream);
+
+/*
+ * The gradients of sum over t of w[t] loss[t], with w[t] = dloss[t] (float [T]), or, when dloss is
+ * NULL, scale / max(1, stats[1]) (the gradient of scale times the mean loss):
+ *     d[t, v] = w[t] ((1 + 2 z_coef lse[t]) exp(l[t, v] - lse[t]) - [v = target[t]])
+ *     dx [T, K] = d W,  dW [V, K] = d^T x                            (element type)
+ * The logits are made again, a piece of the vocabulary at a time. bf16: d is rounded to bf16 for the
+ * two products (the tensor cores' operand type); dx is summed over the pieces in fp32 and rounded
+ * once. dx and dW may be NULL. lse (and stats) as the forward wrote them; with dloss, scale and stats
+ * are not read. ws may be the forward's.
+ */
+int moe_xent_backward(const moe_xent_t* p, const void* x, const void* W, const int64_t* target,
+                      const float* lse, const float* dloss, const float* stats, float scale,
+                      void* dx, void* dW, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- optimiser */
+
+/*
+ * A parameter tensor of an optimiser step: n contiguous elements of p and its gradient g (DEVICE
+ * pointers, no other alignment than the element's), copy (nullable, bf16 [n]) a rounded copy of p
+ * that is written with it. first: the place of its first element in the moment buffers, a multiple
+ * of 256, the tensors' places not overlapping (a tensor takes n rounded up to 256).
+ * The array itself is read on the host during the call; n may be 0.
+ */
+typedef struct {
+  void* p;
+  const void* g;
+  void* copy;
+  int64_t n, first;
+  double weight_decay; /* >= 0 */
+  int32_t p_dtype, g_dtype; /* MOE_F32 / MOE_BF16 */
+} moe_param_t;
+
+/*
+ * One AdamW step over n tensors (weight decay apart from the gradient), t counting the steps from 1:
+ *     g' = g min(1, max_norm / (norm[0] + 1e-6))                     (norm NULL: g' = g)
+ *     m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *     p = p (1 - lr weight_decay) - lr m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32, p rounded once to its type (and once more to bf16 in copy).
+ *   bits 32: m, v are float buffers. bits 8: m int8 and v uint8 codes in blocks of 256 elements with
+ *     a float each in m_scale, v_scale (index = place / 256): m = sign(c) (c / 127)^2 m_scale, v =
+ *     ((c / 255)^2 v_scale)^2. Codes are those of the nearest value (seed < 0), or of one of the two
+ *     around it at random, with the value as expectation, by a hash of seed, t and place. Only v = 0
+ *     has code 0. A value that is not finite makes its block's scale NaN.
+ *     Blocks whose largest |m| or sqrt(v) is below 2^-100 become 0.
+ *   Buffers: m, v 16-byte aligned; what lies behind a tensor's n elements up to its block's end must
+ *     be 0 at first and stays so.
+ *   clock: double [3] on the device: t, beta1^t, beta2^t of the steps made (0, 1, 1 at the start);
+ *     advanced by the call, so that a captured step counts at every replay.
+ *   lr: NULL (the struct's), or a float on the device that takes its place.
+ *   norm: NULL, or a float on the device (moe_grad_norm's); needs max_norm > 0.
+ *   ws: 256 bytes, zero before first use.
+ * Every result is a function of the inputs alone, whatever the order of execution.
+ */
+typedef struct {
+  double lr, beta1, beta2; /* 0 <= beta < 1 */
+  float eps, max_norm;
+  int32_t bits; /* 32 / 8 */
+  int64_t seed; /* 8 bits: < 0 rounds to the nearest */
+} moe_adamw_t;
+int moe_adamw_step(const moe_adamw_t* a, const moe_param_t* params, int n, void* m, void* v,
+                   float* m_scale, float* v_scale, double* clock, const float* lr, const float* norm,
+                   void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The values that n (a multiple of 256) 8-bit codes stand for: m_out, v_out float [n]. */
+int moe_adamw_values(const void* m, const void* v, const float* m_scale, const float* v_scale,
+                     int64_t n, float* m_out, float* v_out, moe_stream_t stream);
+
+/*
+ * out[0] = sqrt of the sum of squares of all elements of the tensors' g (of moe_param_t, g, n and
+ * g_dtype are read). Squares are summed in fp32 within a CTA's share and in fp64 over the shares, in
+ * an order fixed by the sizes: an element above 1.8e19 gives infinity.
+ */
+int moe_grad_norm_workspace_bytes(size_t* bytes);
+int moe_grad_norm(const moe_param_t* params, int n, float* out, void* ws, size_t ws_bytes,
+                  moe_stream_t stream);
 
 /*
  * Synchronises `stream`, reads the status word in ws, clears it, and returns MOE_OK or

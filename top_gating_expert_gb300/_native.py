@@ -56,6 +56,22 @@ class MoeLinear(ctypes.Structure):
                 ("lddx", c_int64), ("lddw", c_int64)]
 
 
+class MoeXent(ctypes.Structure):
+    _fields_ = [("T", c_int32), ("V", c_int32), ("K", c_int32), ("dtype", c_int32), ("ldx", c_int64),
+                ("ldw", c_int64), ("lddx", c_int64), ("lddw", c_int64), ("ignore_index", c_int64),
+                ("z_coef", c_float), ("piece", c_int32)]
+
+
+class MoeParam(ctypes.Structure):
+    _fields_ = [("p", c_void_p), ("g", c_void_p), ("copy", c_void_p), ("n", c_int64), ("first", c_int64),
+                ("weight_decay", ctypes.c_double), ("p_dtype", c_int32), ("g_dtype", c_int32)]
+
+
+class MoeAdamW(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", c_float), ("max_norm", c_float), ("bits", c_int32), ("seed", c_int64)]
+
+
 GRAD_FIELDS = ("dx", "dW_g", "dbias", "dW_in", "dW_up", "dW_out", "dWs_in", "dWs_up", "dWs_out")
 
 
@@ -126,6 +142,16 @@ _PROTOTYPES = {
                            c_void_p, c_size_t, c_void_p],
     "moe_linear_backward": [_P(MoeLinear), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                             c_void_p, c_void_p, c_size_t, c_void_p],
+    "moe_xent_workspace_bytes": [_P(MoeXent), ctypes.c_int, ctypes.c_int, _P(c_size_t)],
+    "moe_xent_forward": [_P(MoeXent), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                         c_void_p, c_size_t, c_void_p],
+    "moe_xent_backward": [_P(MoeXent), c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                          c_float, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p],
+    "moe_adamw_step": [_P(MoeAdamW), c_void_p, ctypes.c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                       c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p],
+    "moe_adamw_values": [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p],
+    "moe_grad_norm_workspace_bytes": [_P(c_size_t)],
+    "moe_grad_norm": [c_void_p, ctypes.c_int, c_void_p, c_void_p, c_size_t, c_void_p],
     "moe_get_device_status": [c_void_p, c_void_p],
     "moe_set_wait_limit": [c_void_p, ctypes.c_uint64, c_void_p],
 }

@@ -1,0 +1,508 @@
+// One AdamW step over many tensors, and the global norm of many gradients.
+//
+//   g' = g c                      c = min(1, max_norm / (norm + 1e-6)), or 1
+//   m  = b1 m + (1 - b1) g'       v = b2 v + (1 - b2) g'^2
+//   p  = p (1 - lr wd) - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// element by element, bound by memory: an fp32 parameter with fp32 moments moves 28 bytes (30 with
+// its bf16 copy), with 8-bit moments 16 (18). The tensors' table travels as a kernel argument (no
+// copy to the device, and a captured graph holds it), in the smallest of three sizes that takes it;
+// persistent CTAs walk chunks of 2048 elements over all tensors, a warp 256 of them, and find a
+// chunk's tensor by halving.
+//
+// The moments of all tensors lie in one buffer each, every tensor from a multiple of 256 on. In 8
+// bits, 256 elements share a scale s, their largest |m| (or sqrt(v)), and a code c stands for
+//   m ~ sign(c) (c / 127)^2 s,     sqrt(v) ~ (c / 255)^2 s:
+// quadratic steps, fine near zero. With y = 127^2 |m| / s the code is the k with k^2 <= y < (k + 1)^2,
+// or k + 1 where y - k^2 > r (2k + 1): r = 1/2 takes the nearer value, a random r of (0, 1) makes the
+// value's expectation y itself, so that changes much smaller than a step are not lost (b2 = 0.999
+// moves v by 0.1 % a step, codes are 0.8 % apart at best). r comes from a hash of seed, step and
+// place. No sqrt(v) above 0 goes to code 0: m / sqrt(v) would grow without bound.
+// The update takes the moments before they are rounded. Operations on the way to a code are
+// rounded one by one (no fused multiply-add), so the codes are a function of the formula alone.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "elem.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBlock = 256;                // elements that share a scale: a warp's, 8 a lane
+constexpr int kChunk = kWarps * kBlock;    // elements of a CTA's step
+constexpr int kNormSlots = 2048;           // partial sums of the norm: CTAs at most
+constexpr float kMLevels = 127.f * 127.f, kVLevels = 255.f * 255.f;
+
+struct Tensor {
+  void* p;
+  const void* g;
+  void* copy;
+  int64_t n, first, chunk0;  // elements, place in the moments, chunks before it
+  float decay, wd;           // 1 - lr wd (lr by value), wd (lr on the device)
+  int p_bf16, g_bf16, vec;   // vec: 4 elements an access everywhere
+};
+template <int CAP>
+struct Table {
+  Tensor t[CAP];
+};
+
+struct StepArgs {
+  int n, last;  // last: the launch that advances the clock
+  int64_t chunks;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  double* clock;  // t, b1^t, b2^t of the steps made
+  const float* lr_dev;
+  const float* norm;
+  unsigned* ticket;
+  double beta1, beta2;
+  float lr, b1, c1, b2, c2, eps, max_norm;
+  int64_t seed;  // < 0: codes of the nearest values
+};
+
+// The tensor of a chunk: the last one with chunk0 <= chunk.
+template <int CAP>
+__device__ __forceinline__ int tensor_of(const Table<CAP>& tab, int n, int64_t chunk) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tab.t[mid].chunk0 <= chunk) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Four elements i .. i + 3 of which `left` exist, as fp32 (0 where there is none)
+__device__ __forceinline__ float4 load4(const void* base, int bf16, int vec, int64_t i, int left) {
+  if (left >= 4 && vec) {
+    if (!bf16) return __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
+    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + i));
+    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
+    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+  float f[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    f[q] = 0.f;
+    if (q < left)
+      f[q] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i + q]) : static_cast<const float*>(base)[i + q];
+  }
+  return make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store4(void* base, int bf16, int vec, int64_t i, int left, const float (&f)[4]) {
+  if (left >= 4 && vec) {
+    if (!bf16) {
+      __stcs(reinterpret_cast<float4*>(static_cast<float*>(base) + i), make_float4(f[0], f[1], f[2], f[3]));
+    } else {
+      __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+      __stcs(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + i),
+             make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b)));
+    }
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (q < left) {
+      if (bf16) static_cast<__nv_bfloat16*>(base)[i + q] = __float2bfloat16_rn(f[q]);
+      else static_cast<float*>(base)[i + q] = f[q];
+    }
+}
+
+__device__ __forceinline__ uint32_t mix32(uint32_t h) {
+  h ^= h >> 16;
+  h *= 0x9E3779B1u;
+  h ^= h >> 15;
+  h *= 0x85157AF5u;
+  return h ^ (h >> 16);
+}
+
+// The code of y (in units of the scale, times the levels), r the share of the way above which the next one
+__device__ __forceinline__ float level(float y, float r, float most) {
+  const float k = floorf(__fsqrt_rn(y));
+  const float up = __fsub_rn(y, k * k) > __fmul_rn(r, 2.f * k + 1.f) ? 1.f : 0.f;
+  return fminf(k + up, most);
+}
+
+// A block's scale from the bits of its largest magnitude: NaN where one is not finite, 0 below 2^-100
+// (its values are then 0); and levels / scale.
+__device__ __forceinline__ void block_scale(uint32_t bits, float levels, float& s, float& inv) {
+  const float top = __uint_as_float(bits);
+  s = bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : (top >= 0x1p-100f ? top : 0.f);
+  inv = s == 0.f ? 0.f : __fdiv_rn(levels, s);
+}
+
+template <int BITS, int CAP>
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ Table<CAP> tab, const StepArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float lr = a.lr_dev ? __ldg(a.lr_dev) : a.lr;
+  const double t = a.clock[0] + 1.0, b1t = a.clock[1] * a.beta1, b2t = a.clock[2] * a.beta2;
+  const float size = __fdiv_rn(lr, float(1.0 - b1t)), rs = __fdiv_rn(1.f, __fsqrt_rn(float(1.0 - b2t)));
+  float coef = 1.f;
+  if (a.norm) {
+    coef = __fdiv_rn(a.max_norm, __fadd_rn(__ldg(a.norm), 1e-6f));
+    if (coef > 1.f) coef = 1.f;  // NaN stays
+  }
+  uint32_t key = 0;
+  if (BITS == 8 && a.seed >= 0) key = mix32(uint32_t(a.seed) + 0x632BE5ABu * uint32_t(int64_t(t)));
+
+  for (int64_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
+    const Tensor& x = tab.t[tensor_of(tab, a.n, chunk)];
+    const int64_t e0 = (chunk - x.chunk0) * kChunk + warp * kBlock;
+    if (e0 >= x.n) continue;  // the whole warp
+    const int64_t s0 = x.first + e0;
+    const int valid = int(min(int64_t(kBlock), x.n - e0));
+    const float decay = a.lr_dev ? fmaf(-lr, x.wd, 1.f) : x.decay;
+    float4 pv[2], gv[2], mv[2], vv[2];
+    uint32_t mc[2], vc[2];
+    float ms = 0.f, vs = 0.f;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int at = 128 * q + 4 * lane, left = valid - at;
+      gv[q] = load4(x.g, x.g_bf16, x.vec, e0 + at, left);
+      pv[q] = load4(x.p, x.p_bf16, x.vec, e0 + at, left);
+      if constexpr (BITS == 32) {
+        mv[q] = load4(a.m, 0, 1, s0 + at, left);
+        vv[q] = load4(a.v, 0, 1, s0 + at, left);
+      } else {  // whole words of codes: the buffer is padded to blocks
+        mc[q] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s0 + at));
+        vc[q] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s0 + at));
+      }
+    }
+    if constexpr (BITS == 8) {
+      ms = __fmul_rn(a.m_scale[s0 / kBlock], 1.f / kMLevels);
+      vs = __fmul_rn(a.v_scale[s0 / kBlock], 1.f / kVLevels);
+    }
+    float m[8], u[8], v[8];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float g4[4] = {gv[q].x, gv[q].y, gv[q].z, gv[q].w};
+      const float p4[4] = {pv[q].x, pv[q].y, pv[q].z, pv[q].w};
+      float m4[4], v4[4], out[4];
+      if constexpr (BITS == 32) {
+        m4[0] = mv[q].x; m4[1] = mv[q].y; m4[2] = mv[q].z; m4[3] = mv[q].w;
+        v4[0] = vv[q].x; v4[1] = vv[q].y; v4[2] = vv[q].z; v4[3] = vv[q].w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float cm = float(int8_t(mc[q] >> (8 * k))), cv = float((vc[q] >> (8 * k)) & 255u);
+          m4[k] = __fmul_rn(cm * fabsf(cm), ms);
+          const float uu = __fmul_rn(cv * cv, vs);
+          v4[k] = __fmul_rn(uu, uu);
+        }
+      }
+      const int at = 128 * q + 4 * lane, left = valid - at;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float g = __fmul_rn(g4[k], coef);
+        const float mn = __fadd_rn(__fmul_rn(m4[k], a.b1), __fmul_rn(g, a.c1));
+        const float vn = __fadd_rn(__fmul_rn(v4[k], a.b2), __fmul_rn(__fmul_rn(g, g), a.c2));
+        const float un = __fsqrt_rn(vn);
+        const float step = __fmul_rn(__fdiv_rn(mn, __fadd_rn(__fmul_rn(un, rs), a.eps)), size);
+        out[k] = __fsub_rn(__fmul_rn(p4[k], decay), step);
+        m[4 * q + k] = k < left ? mn : 0.f;
+        u[4 * q + k] = k < left ? un : 0.f;
+        v[4 * q + k] = vn;
+      }
+      store4(x.p, x.p_bf16, x.vec, e0 + at, left, out);
+      if (x.copy) store4(x.copy, 1, x.vec, e0 + at, left, out);
+      if constexpr (BITS == 32) {
+        store4(a.m, 0, 1, s0 + at, left, reinterpret_cast<const float(&)[4]>(m[4 * q]));
+        store4(a.v, 0, 1, s0 + at, left, reinterpret_cast<const float(&)[4]>(v[4 * q]));
+      }
+    }
+    if constexpr (BITS == 8) {
+      // magnitudes' bits compare as the magnitudes do, NaN above all
+      uint32_t mb = 0, ub = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        mb = max(mb, __float_as_uint(m[k]) & 0x7fffffffu);
+        ub = max(ub, __float_as_uint(u[k]) & 0x7fffffffu);
+      }
+      mb = __reduce_max_sync(0xffffffffu, mb);
+      ub = __reduce_max_sync(0xffffffffu, ub);
+      float sm, im, sv, iv;
+      block_scale(mb, kMLevels, sm, im);
+      block_scale(ub, kVLevels, sv, iv);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int at = 128 * q + 4 * lane;
+        uint32_t wm = 0, wv = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float rm = 0.5f, rv = 0.5f;
+          if (a.seed >= 0) {
+            const int64_t place = s0 + at + k;
+            const uint32_t h = mix32(uint32_t(place) ^ uint32_t(place >> 32) * 0x2545F491u ^ key);
+            rm = (float(h & 0xffffu) + 0.5f) * 0x1p-16f;
+            rv = (float(h >> 16) + 0.5f) * 0x1p-16f;
+          }
+          const float mk = m[4 * q + k];
+          const float cm = level(__fmul_rn(fabsf(mk), im), rm, 127.f);
+          const float yv = __fmul_rn(u[4 * q + k], iv);
+          const float cv = yv > 0.f ? fmaxf(level(yv, rv, 255.f), 1.f) : 0.f;
+          // a NaN scale: the codes do not matter, but are whole (float2int takes NaN to 0)
+          wm |= (uint32_t(__float2int_rz(copysignf(cm, mk))) & 255u) << (8 * k);
+          wv |= (uint32_t(__float2int_rz(cv)) & 255u) << (8 * k);
+        }
+        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s0 + at), wm);
+        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + s0 + at), wv);
+      }
+      if (lane == 0) {
+        a.m_scale[s0 / kBlock] = sm;
+        a.v_scale[s0 / kBlock] = sv;
+      }
+    }
+  }
+  if (!a.last) return;
+  // every CTA has read the clock by its turn here; the last one advances it
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    if (atomicAdd(a.ticket, 1u) == gridDim.x - 1) {
+      *a.ticket = 0u;
+      a.clock[0] = t;
+      a.clock[1] = b1t;
+      a.clock[2] = b2t;
+    }
+  }
+}
+
+// The moments' 32-bit values from their codes, blocks of 256.
+__global__ void __launch_bounds__(kThreads)
+    adamw_values_kernel(const int8_t* __restrict__ mc, const uint8_t* __restrict__ vc, const float* __restrict__ m_scale,
+                        const float* __restrict__ v_scale, int64_t n, float* __restrict__ m, float* __restrict__ v) {
+  pdl_wait();
+  pdl_trigger();
+  for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 4; i < n; i += int64_t(gridDim.x) * kThreads * 4) {
+    const uint32_t wm = *reinterpret_cast<const uint32_t*>(mc + i), wv = *reinterpret_cast<const uint32_t*>(vc + i);
+    const float ms = __fmul_rn(__ldg(m_scale + i / kBlock), 1.f / kMLevels);
+    const float vs = __fmul_rn(__ldg(v_scale + i / kBlock), 1.f / kVLevels);
+    float fm[4], fv[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = float(int8_t(wm >> (8 * k))), b = float((wv >> (8 * k)) & 255u);
+      fm[k] = __fmul_rn(a * fabsf(a), ms);
+      const float u = __fmul_rn(b * b, vs);
+      fv[k] = __fmul_rn(u, u);
+    }
+    __stcs(reinterpret_cast<float4*>(m + i), make_float4(fm[0], fm[1], fm[2], fm[3]));
+    __stcs(reinterpret_cast<float4*>(v + i), make_float4(fv[0], fv[1], fv[2], fv[3]));
+  }
+}
+
+struct NormArgs {
+  int n, first, last;  // first: the sum starts here; last: the norm is written
+  int64_t chunks;
+  float* out;
+  float* part;     // [kNormSlots]
+  double* total;
+  unsigned* ticket;
+};
+
+// Sum of squares of all elements: fp32 within a thread (a lane's elements of one chunk first), a fixed
+// tree over a CTA, fp64 over the CTAs in the last one to finish; launches add up in order.
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 4) grad_norm_kernel(const __grid_constant__ Table<CAP> tab, const NormArgs a) {
+  __shared__ float s_red[kWarps];
+  __shared__ double s_tot[kWarps];
+  __shared__ bool s_last;
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float sum = 0.f;
+  for (int64_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
+    const Tensor& x = tab.t[tensor_of(tab, a.n, chunk)];
+    const int64_t e0 = (chunk - x.chunk0) * kChunk + threadIdx.x * 4;
+    float4 v[kChunk / (kThreads * 4)];
+#pragma unroll
+    for (int q = 0; q < kChunk / (kThreads * 4); ++q) {
+      const int64_t i = e0 + q * kThreads * 4;
+      v[q] = load4(x.g, x.g_bf16, x.vec, i, int(max(int64_t(0), min(int64_t(4), x.n - i))));
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < kChunk / (kThreads * 4); ++q)
+      s += (v[q].x * v[q].x + v[q].y * v[q].y) + (v[q].z * v[q].z + v[q].w * v[q].w);
+    sum += s;
+  }
+  sum = block_sum_all<kWarps>(sum, s_red);
+  if (threadIdx.x == 0) {
+    a.part[blockIdx.x] = sum;
+    __threadfence();
+    s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  double d = 0.0;
+  for (int i = threadIdx.x; i < int(gridDim.x); i += kThreads) d += double(__ldcg(a.part + i));
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+  if (lane == 0) s_tot[warp] = d;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    d = a.first ? 0.0 : *a.total;
+    for (int w = 0; w < kWarps; ++w) d += s_tot[w];
+    *a.total = d;
+    *a.ticket = 0u;
+    if (a.last) *a.out = float(sqrt(d));
+  }
+}
+
+int check_params(const moe_param_t* t, int n, bool step) {
+  if (n < 0 || (n > 0 && !t)) return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i) {
+    const moe_param_t& x = t[i];
+    if (x.n < 0 || x.n > (int64_t(1) << 48)) return MOE_ERR_INVALID_ARG;
+    if (x.g_dtype != MOE_F32 && x.g_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (x.n > 0 && !x.g) return MOE_ERR_INVALID_ARG;
+    if (!step) continue;
+    if (x.p_dtype != MOE_F32 && x.p_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (x.n > 0 && !x.p) return MOE_ERR_INVALID_ARG;
+    if (x.first < 0 || x.first % kBlock != 0 || x.first > (int64_t(1) << 48)) return MOE_ERR_INVALID_ARG;
+    if (!(x.weight_decay >= 0.0) || !std::isfinite(x.weight_decay)) return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+bool on(const void* p, size_t b) { return reinterpret_cast<uintptr_t>(p) % b == 0; }
+
+constexpr int kMost = 448;  // tensors of a launch: 448 x 72 bytes of the 32 KB that arguments may have
+
+// Fills the table from t[at ..], skipping empty tensors; returns the next index.
+template <int CAP>
+int fill(Table<CAP>& tab, const moe_param_t* t, int n, int at, double lr, bool step, int* used, int64_t* chunks) {
+  *used = 0;
+  *chunks = 0;
+  for (; at < n && *used < CAP; ++at) {
+    const moe_param_t& x = t[at];
+    if (x.n == 0) continue;
+    Tensor& d = tab.t[(*used)++];
+    d.p = step ? x.p : nullptr;
+    d.g = x.g;
+    d.copy = step ? x.copy : nullptr;
+    d.n = x.n;
+    d.first = step ? x.first : 0;
+    d.chunk0 = *chunks;
+    d.wd = step ? float(x.weight_decay) : 0.f;
+    d.decay = step ? float(1.0 - lr * x.weight_decay) : 1.f;
+    d.p_bf16 = step && x.p_dtype == MOE_BF16;
+    d.g_bf16 = x.g_dtype == MOE_BF16;
+    d.vec = on(x.g, d.g_bf16 ? 8 : 16) && (!step || (on(x.p, d.p_bf16 ? 8 : 16) && on(x.copy, 8)));
+    *chunks += (x.n + kChunk - 1) / kChunk;
+  }
+  return at;
+}
+
+// f(table, used, chunks, last) for each launch's tensors, in the smallest table that takes them all
+template <int CAP, typename F>
+int launches(const moe_param_t* t, int n, double lr, bool step, F&& f) {
+  Table<CAP> tab;
+  int at = 0;
+  do {
+    int used;
+    int64_t chunks;
+    const int next = fill(tab, t, n, at, lr, step, &used, &chunks);
+    bool last = true;  // nothing but empty tensors follows
+    for (int i = next; i < n && last; ++i) last = t[i].n == 0;
+    const int rc = f(tab, used, chunks, at == 0, last);
+    if (rc != MOE_OK || last) return rc;
+    at = next;
+  } while (at < n);
+  return MOE_OK;
+}
+template <typename F>
+int with_table(const moe_param_t* t, int n, double lr, bool step, F&& f) {
+  if (n <= 16) return launches<16>(t, n, lr, step, f);
+  if (n <= 96) return launches<96>(t, n, lr, step, f);
+  return launches<kMost>(t, n, lr, step, f);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_adamw_step(const moe_adamw_t* a, const moe_param_t* params, int n, void* m, void* v, float* m_scale,
+                   float* v_scale, double* clock, const float* lr, const float* norm, void* ws, size_t ws_bytes,
+                   moe_stream_t stream) {
+  if (!a || (a->bits != 32 && a->bits != 8)) return MOE_ERR_INVALID_ARG;
+  if (!(a->beta1 >= 0.0 && a->beta1 < 1.0) || !(a->beta2 >= 0.0 && a->beta2 < 1.0) || !(a->eps >= 0.f) ||
+      !std::isfinite(a->eps) || !std::isfinite(a->lr))
+    return MOE_ERR_INVALID_ARG;
+  if (norm && !(a->max_norm > 0.f)) return MOE_ERR_INVALID_ARG;
+  const int rc = check_params(params, n, true);
+  if (rc != MOE_OK) return rc;
+  if (!clock || !on(clock, 8)) return MOE_ERR_INVALID_ARG;
+  bool any = false;
+  for (int i = 0; i < n && !any; ++i) any = params[i].n > 0;
+  if (any && (!m || !v || !on(m, 16) || !on(v, 16))) return MOE_ERR_INVALID_ARG;
+  if (any && a->bits == 8 && (!m_scale || !v_scale)) return MOE_ERR_INVALID_ARG;
+  if (!ws || !on(ws, 256) || ws_bytes < 256) return MOE_ERR_WORKSPACE;
+  StepArgs s;
+  s.m = m; s.v = v; s.m_scale = m_scale; s.v_scale = v_scale;
+  s.clock = clock; s.lr_dev = lr; s.norm = norm;
+  s.ticket = static_cast<unsigned*>(ws) + 1;
+  s.beta1 = a->beta1; s.beta2 = a->beta2;
+  s.lr = float(a->lr);
+  s.b1 = float(a->beta1); s.c1 = float(1.0 - a->beta1);
+  s.b2 = float(a->beta2); s.c2 = float(1.0 - a->beta2);
+  s.eps = a->eps; s.max_norm = a->max_norm;
+  s.seed = a->bits == 8 ? a->seed : -1;
+  return with_table(params, n, a->lr, true, [&](const auto& tab, int used, int64_t chunks, bool, bool last) {
+    constexpr int CAP = sizeof(tab.t) / sizeof(Tensor);
+    s.n = used; s.chunks = chunks; s.last = last;
+    const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(chunks, 4 * num_sms())));
+    auto kern = a->bits == 8 ? adamw_kernel<8, CAP> : adamw_kernel<32, CAP>;
+    return launch_kernel(kern, dim3(grid), dim3(kThreads), 0, stream, tab, s);
+  });
+}
+
+int moe_adamw_values(const void* m, const void* v, const float* m_scale, const float* v_scale, int64_t n, float* m_out,
+                     float* v_out, moe_stream_t stream) {
+  if (n < 0 || n % kBlock != 0) return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  if (!m || !v || !m_scale || !v_scale || !m_out || !v_out) return MOE_ERR_INVALID_ARG;
+  if (!on(m, 4) || !on(v, 4) || !on(m_out, 16) || !on(v_out, 16)) return MOE_ERR_INVALID_ARG;
+  const unsigned grid = unsigned(std::min<int64_t>((n / 4 + kThreads - 1) / kThreads, 16 * num_sms()));
+  return launch_kernel(adamw_values_kernel, dim3(grid), dim3(kThreads), 0, stream, static_cast<const int8_t*>(m),
+                       static_cast<const uint8_t*>(v), m_scale, v_scale, n, m_out, v_out);
+}
+
+int moe_grad_norm_workspace_bytes(size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = 256 + kNormSlots * sizeof(float);
+  return MOE_OK;
+}
+
+int moe_grad_norm(const moe_param_t* params, int n, float* out, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  const int rc = check_params(params, n, false);
+  if (rc != MOE_OK) return rc;
+  if (!out) return MOE_ERR_INVALID_ARG;
+  size_t need;
+  moe_grad_norm_workspace_bytes(&need);
+  if (!ws || !on(ws, 256) || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  NormArgs a;
+  a.out = out;
+  a.ticket = static_cast<unsigned*>(ws) + 1;
+  a.total = reinterpret_cast<double*>(static_cast<char*>(ws) + 64);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 256);
+  return with_table(params, n, 0.0, false, [&](const auto& tab, int used, int64_t chunks, bool first, bool last) {
+    constexpr int CAP = sizeof(tab.t) / sizeof(Tensor);
+    a.n = used; a.chunks = chunks; a.first = first; a.last = last;
+    const int64_t most = std::min<int64_t>(kNormSlots, 4 * num_sms());
+    const unsigned grid = unsigned(std::max<int64_t>(1, std::min(chunks, most)));
+    return launch_kernel(grad_norm_kernel<CAP>, dim3(grid), dim3(kThreads), 0, stream, tab, a);
+  });
+}
+
+}  // extern "C"

@@ -88,14 +88,6 @@ __global__ void __launch_bounds__(1024)
 // element boundary. Eight elements a thread, read as the 4-byte words that hold them (five when
 // the row starts inside a word) and shifted into place; a word that the row only half fills is read
 // as its one element, so nothing outside of the row is read. A warp takes 256 columns of a row.
-struct AlignJob {
-  const __nv_bfloat16* src;
-  int64_t ld, rows;
-  int cols;
-  __nv_bfloat16* dst;
-  int64_t ldd;
-};
-
 __global__ void __launch_bounds__(256) linear_align_kernel(AlignJob j0, AlignJob j1) {
   pdl_wait();
   pdl_trigger();
@@ -129,8 +121,6 @@ __global__ void __launch_bounds__(256) linear_align_kernel(AlignJob j0, AlignJob
   }
 }
 
-int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
-
 // slices of the bias's gradient: about 1216 CTAs of 256 columns (eight an SM) at most
 int bias_slices(int T, int N) {
   const int cblocks = (N + 255) / 256;
@@ -154,17 +144,6 @@ int check_linear(const moe_linear_t* p, moe_linear_t* q) {
   return MOE_OK;
 }
 
-// Carves the workspace: regions in a fixed order, their total compared with what there is.
-struct Carver {
-  char* base;
-  size_t at = 256;
-  void* take(size_t bytes) {
-    void* p = base ? base + at : nullptr;
-    at = align256(at + bytes);
-    return p;
-  }
-};
-
 // Few tokens forward: W is streamed row by row, nothing copied and no partial sums.
 bool few_tokens(const moe_linear_t& p) { return p.T <= (p.dtype == MOE_BF16 ? 1 : 8); }
 
@@ -185,31 +164,6 @@ size_t ws_need(const moe_linear_t& p, bool backward, bool all) {
 }
 
 bool in_place(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
-
-// The operand [rows, cols] as TMA can read it: in place, or in a copy with 16-byte rows that the
-// job describes (src null: none).
-int align_operand(const void* src, int64_t ld, int64_t rows, int cols, Carver& c, size_t ws_bytes,
-                  LinearOperand* o, AlignJob* job) {
-  o->p = src;
-  o->ld = ld;
-  *job = AlignJob{nullptr, 0, 0, 1, nullptr, 8};
-  if (in_place(src, ld)) return MOE_OK;
-  o->ld = up8(cols);
-  void* dst = c.take(size_t(rows) * o->ld * 2);
-  o->p = dst;
-  *job = AlignJob{static_cast<const __nv_bfloat16*>(src), ld, rows, cols, static_cast<__nv_bfloat16*>(dst), o->ld};
-  return c.at > ws_bytes ? MOE_ERR_WORKSPACE : MOE_OK;
-}
-
-int launch_align(const AlignJob& a, const AlignJob& b, cudaStream_t st) {
-  const bool two = a.src && b.src;
-  if (!a.src && !b.src) return MOE_OK;
-  const AlignJob& one = a.src ? a : b;
-  const int64_t rows = std::max(one.rows, two ? b.rows : 0), per = std::max(one.ldd, two ? b.ldd : 0) / 8;
-  const dim3 grid(unsigned(std::min<int64_t>((rows + 7) / 8, 1 << 20)), two ? 2 : 1,
-                  unsigned(std::min<int64_t>((per + 31) / 32, 64)));
-  return launch_kernel(linear_align_kernel, grid, dim3(256), 0, st, one, b);
-}
 
 // d (when it is given) and dbias (when it is given; part: its slices' partial sums)
 template <typename T>
@@ -237,6 +191,30 @@ int launch_dact(const moe_linear_t& p, const void* dy, const void* pre, void* d,
 }
 
 }  // namespace
+
+int align_operand(const void* src, int64_t ld, int64_t rows, int cols, Carver& c, size_t ws_bytes,
+                  LinearOperand* o, AlignJob* job) {
+  o->p = src;
+  o->ld = ld;
+  *job = AlignJob{nullptr, 0, 0, 1, nullptr, 8};
+  if (in_place(src, ld)) return MOE_OK;
+  o->ld = up8(cols);
+  void* dst = c.take(size_t(rows) * o->ld * 2);
+  o->p = dst;
+  *job = AlignJob{static_cast<const __nv_bfloat16*>(src), ld, rows, cols, static_cast<__nv_bfloat16*>(dst), o->ld};
+  return c.at > ws_bytes ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+int launch_align(const AlignJob& a, const AlignJob& b, cudaStream_t st) {
+  const bool two = a.src && b.src;
+  if (!a.src && !b.src) return MOE_OK;
+  const AlignJob& one = a.src ? a : b;
+  const int64_t rows = std::max(one.rows, two ? b.rows : 0), per = std::max(one.ldd, two ? b.ldd : 0) / 8;
+  const dim3 grid(unsigned(std::min<int64_t>((rows + 7) / 8, 1 << 20)), two ? 2 : 1,
+                  unsigned(std::min<int64_t>((per + 31) / 32, 64)));
+  return launch_kernel(linear_align_kernel, grid, dim3(256), 0, st, one, b);
+}
+
 }  // namespace moe
 
 using namespace moe;

@@ -26,6 +26,29 @@ struct LinearEpi {
 constexpr int kPartTiles = 304;
 constexpr size_t kPartBytes = size_t(kPartTiles) * 128 * 128 * 4;
 
+// A bf16 operand copied to 16-byte rows (src null: none): dst [rows][ldd] = src [rows][cols].
+struct AlignJob {
+  const __nv_bfloat16* src;
+  int64_t ld, rows;
+  int cols;
+  __nv_bfloat16* dst;
+  int64_t ldd;
+};
+int launch_align(const AlignJob& a, const AlignJob& b, cudaStream_t st);
+
+// Carves a workspace behind its header: regions in a fixed order, their total compared with what there is.
+struct Carver {
+  char* base;
+  size_t at = 256;
+  void* take(size_t bytes) {
+    void* p = base ? base + at : nullptr;
+    at = align256(at + bytes);
+    return p;
+  }
+};
+
+inline int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
+
 // out(i, j) over i < rows, j < cols from A(i, k) = A[i * a_i + k * a_k] and B likewise, one
 // stride of each operand being 1; part: kPartBytes of scratch.
 int launch_linear_f32(const float* A, int64_t a_i, int64_t a_k, const float* B, int64_t b_j,
@@ -39,8 +62,39 @@ struct LinearOperand {
   int64_t ld;
   bool mn;
 };
+// The operand [rows, cols] as TMA can read it: in place, or in a copy with 16-byte rows that the
+// job describes (src null: none).
+int align_operand(const void* src, int64_t ld, int64_t rows, int cols, Carver& c, size_t ws_bytes,
+                  LinearOperand* o, AlignJob* job);
 int launch_linear_bf16(const LinearOperand& A, const LinearOperand& B, int rows, int cols, int K,
                        const LinearEpi& e, unsigned* status, cudaStream_t st);
+
+// What becomes of a tensor-core product's accumulator.
+enum ProductMode {
+  kProduct,     // the linear layer's epilogue (LinearEpi)
+  kXentStats,   // logits: their largest and their sum of exponentials, 128 columns at a time
+  kXentGrad,    // logits: the gradient of the cross entropy to them, bf16
+  kProductSum,  // added to fp32 sums; bf16 at last
+};
+// What the modes other than kProduct take beside LinearEpi's out and ldo.
+struct XentEpi {
+  // kXentStats: part[column / 128][row] = (c, s): the sum of exp(l) over the 128 columns is 2^c s, c the
+  // largest l times log2(e); hit[row] = the logit of the row's target where it lies in the columns
+  float2* part = nullptr;
+  int64_t ldpart = 0;
+  float* hit = nullptr;
+  const int64_t* target = nullptr;
+  // kXentGrad: d = 2^(l log2(e) - x) y, less z at the target's column (bits of w) - v0; z = 0: d = 0
+  const float4* row = nullptr;
+  int v0 = 0;
+  // kProductSum: v + acc_in (null: v) to acc_out, or rounded to out where that is null; 16-byte
+  // aligned rows of ldacc floats, a multiple of 8
+  const float* acc_in = nullptr;
+  float* acc_out = nullptr;
+  int64_t ldacc = 0;
+};
+int launch_xent_bf16(ProductMode mode, const LinearOperand& A, const LinearOperand& B, int rows, int cols, int K,
+                     const LinearEpi& e, const XentEpi& x, unsigned* status, cudaStream_t st);
 
 // The forward for one bf16 or up to eight fp32 tokens, operands on any boundary.
 int launch_linear_few(int bf16, const void* x, int64_t ldx, const void* W, int64_t ldw, int T, int N, int K,

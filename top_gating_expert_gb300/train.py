@@ -1,0 +1,283 @@
+"""What closes a training step around the blocks: the loss of a linear head, the gradients' norm and
+the optimiser.
+
+``linear_cross_entropy`` and its backward are the C ABI's moe_xent_* on torch tensors (logits over a
+large vocabulary that are never stored), ``grad_norm`` is moe_grad_norm and ``AdamW`` holds the
+moments of a list of parameters and updates all of them in one launch (moe_adamw_*). Matrices, types,
+strides and streams as in `block`.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from functools import lru_cache
+
+import numpy as np
+import torch
+
+from . import _native as N
+from .block import _DTYPES, _F32, _device, _first, _matrix, _new, _on, _p, _scratch, _unaligned, _vector, \
+    _workspace_ok
+from .moe import _check, _launch
+
+
+# ------------------------------------------------------------------ cross entropy of a linear head
+@lru_cache(maxsize=512)
+def _xent_args(*fields):
+    return ctypes.byref(N.MoeXent(*fields))
+
+
+@lru_cache(maxsize=512)
+def _xent_ws_bytes(backward, unaligned, *fields):
+    b = N.c_size_t()
+    _check(N.lib().moe_xent_workspace_bytes(_xent_args(*fields), backward, unaligned, ctypes.byref(b)),
+           "moe_xent_workspace_bytes")
+    return b.value
+
+
+def linear_cross_entropy_workspace(T, V, K, dtype=torch.bfloat16, device="cuda", *, backward=True, aligned=False,
+                                   piece=0):
+    """A zero-filled workspace for linear_cross_entropy (and its backward, unless backward is False)
+    with x [T, K] and W [V, K]. aligned: x and W start on a 16-byte boundary and have rows of a
+    multiple of 16 bytes. piece: as the calls will be given it."""
+    n = _xent_ws_bytes(int(bool(backward)), int(not aligned), T, V, K, _DTYPES[dtype], 0, 0, 0, 0, 0, 0.0, piece)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _xent_checked(x, W, target, where):
+    (T, K), dt, dev, ldx = _first(x, "x", where)
+    (V, kw), dtw, devw, ldw = _first(W, "W", where)
+    if kw != K or dtw is not dt or devw != dev or V < 1:
+        raise ValueError(f"{where}: W must be a {dt} tensor of shape (any >= 1, {K}) on CUDA device {dev}")
+    if not isinstance(target, torch.Tensor) or target.dtype is not torch.int64 or target.shape != (T,) \
+            or target.get_device() != dev or not target.is_contiguous():
+        raise ValueError(f"{where}: target must be a contiguous int64 tensor of {T} elements on CUDA device {dev}")
+    return T, V, K, dt, dev, ldx, ldw
+
+
+def linear_cross_entropy(x, W, target, *, ignore_index=-100, z_coef=0.0, loss=None, lse=None, stats=None, piece=0,
+                         ws=None, stream=None):
+    """(loss, lse, stats) of the logits x W^T for x [T, K], W [V, K] and target int64 [T]: each
+    token's loss lse - logit of its target + z_coef lse^2 (0 where the target is ignore_index) and
+    the logsumexp lse of its logits, float32 [T], and stats, float32 [2]: the mean loss over the
+    tokens with a target, and their number. The logits are not stored. A target outside of the
+    vocabulary gives a NaN loss and, in ws, the status MOE_ERR_DEVICE_DATA. piece: vocabulary entries
+    at a time (0: chosen from the sizes)."""
+    w = "linear_cross_entropy"
+    T, V, K, dt, dev, ldx, ldw = _xent_checked(x, W, target, w)
+    if loss is None:
+        loss = _new((T,), _F32, dev, stream)
+    if lse is None:
+        lse = _new((T,), _F32, dev, stream)
+    if stats is None:
+        stats = _new((2,), _F32, dev, stream)
+    _vector(loss, "loss", w, T, dev)
+    _vector(lse, "lse", w, T, dev)
+    _vector(stats, "stats", w, 2, dev)
+    fields = (T, V, K, _DTYPES[dt], ldx, ldw, K, K, ignore_index, z_coef, piece)
+    if ws is None:
+        ws = _scratch(_xent_ws_bytes(0, _unaligned(x, W), *fields), dev, stream)
+    _workspace_ok(ws, w, dev)
+    _launch("moe_xent_forward", x, stream, _xent_args(*fields), x.data_ptr(), W.data_ptr(), target.data_ptr(),
+            loss.data_ptr(), lse.data_ptr(), stats.data_ptr(), ws.data_ptr(), ws.numel())
+    return loss, lse, stats
+
+
+def linear_cross_entropy_backward(x, W, target, lse, *, dloss=None, stats=None, scale=1.0, ignore_index=-100,
+                                  z_coef=0.0, need_x=True, need_W=True, dx=None, dW=None, piece=0, ws=None,
+                                  stream=None):
+    """(dx, dW) of linear_cross_entropy, in the element type: the gradient of sum(dloss * loss) for
+    dloss float32 [T], or without it of scale times the mean loss, from the forward's stats. lse,
+    ignore_index and z_coef as in the forward; None for what is not needed."""
+    w = "linear_cross_entropy_backward"
+    T, V, K, dt, dev, ldx, ldw = _xent_checked(x, W, target, w)
+    _vector(lse, "lse", w, T, dev)
+    if dloss is not None:
+        _vector(dloss, "dloss", w, T, dev)
+    elif stats is None:
+        raise ValueError(f"{w}: dloss or the forward's stats must be given")
+    else:
+        _vector(stats, "stats", w, 2, dev)
+    if need_x and dx is None:
+        dx = _new((T, K), dt, dev, stream)
+    if need_W and dW is None:
+        dW = _new((V, K), dt, dev, stream)
+    lddx = K if dx is None else _matrix(dx, "dx", w, (T, K), dt, dev)
+    lddw = K if dW is None else _matrix(dW, "dW", w, (V, K), dt, dev)
+    fields = (T, V, K, _DTYPES[dt], ldx, ldw, lddx, lddw, ignore_index, z_coef, piece)
+    if ws is None:
+        ws = _scratch(_xent_ws_bytes(1, _unaligned(x, W), *fields), dev, stream)
+    _workspace_ok(ws, w, dev)
+    _launch("moe_xent_backward", x, stream, _xent_args(*fields), x.data_ptr(), W.data_ptr(), target.data_ptr(),
+            lse.data_ptr(), _p(dloss), _p(stats), scale, _p(dx), _p(dW), ws.data_ptr(), ws.numel())
+    return dx, dW
+
+
+# ------------------------------------------------------------------ many tensors
+_PARAM = np.dtype([("p", np.uint64), ("g", np.uint64), ("copy", np.uint64), ("n", np.int64), ("first", np.int64),
+                   ("weight_decay", np.float64), ("p_dtype", np.int32), ("g_dtype", np.int32)])
+_BLOCK = 256  # elements that share a scale in 8 bits; every tensor's moments start at a multiple
+
+
+def _elements(t, name, where, dev):
+    """Checks a tensor of a list by its elements alone: its address."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be a contiguous float32 or bfloat16 tensor on CUDA device {dev}")
+    return t.data_ptr()
+
+
+@lru_cache(maxsize=1)
+def _grad_norm_ws_bytes():
+    b = N.c_size_t()
+    _check(N.lib().moe_grad_norm_workspace_bytes(ctypes.byref(b)), "moe_grad_norm_workspace_bytes")
+    return b.value
+
+
+def grad_norm_workspace(device="cuda"):
+    """A zero-filled workspace for grad_norm."""
+    return torch.zeros(_grad_norm_ws_bytes(), dtype=torch.uint8, device=device)
+
+
+def grad_norm(grads, *, out=None, ws=None, stream=None):
+    """float32 [1]: the 2-norm of all elements of the tensors (float32 or bfloat16, contiguous; None
+    is left out). Nothing is read back: AdamW.step takes it as it is."""
+    w = "grad_norm"
+    ts = [g for g in grads if g is not None]
+    if not ts:
+        raise ValueError(f"{w}: no gradients")
+    dev = ts[0].get_device() if isinstance(ts[0], torch.Tensor) else -1
+    if dev < 0:
+        raise ValueError(f"{w}: the gradients must be tensors on a CUDA device")
+    tab = np.zeros(len(ts), _PARAM)
+    tab["g"] = [_elements(g, "every gradient", w, dev) for g in ts]
+    tab["n"] = [g.numel() for g in ts]
+    tab["g_dtype"] = [_DTYPES[g.dtype] for g in ts]
+    if out is None:
+        out = _new((1,), _F32, dev, stream)
+    _vector(out, "out", w, 1, dev)
+    if ws is None:
+        ws = _scratch(_grad_norm_ws_bytes(), dev, stream)
+    _workspace_ok(ws, w, dev)
+    _launch("moe_grad_norm", out, stream, tab.ctypes.data, len(ts), out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+class AdamW:
+    """AdamW over a list of parameters (float32 or bfloat16, contiguous), updated in place.
+
+    bits 32 holds both moments as float32 (`m`, `v`), bits 8 as codes (int8, uint8) of blocks of 256
+    elements with a float32 scale each (`m_scale`, `v_scale`); seed: None rounds to the nearest code,
+    a number >= 0 at random around the value, the same way for the same seed. All parameters' moments
+    lie in one buffer, parameter i's from element first[i] on. weight_decay: one number or one for each
+    parameter. copies: bfloat16 tensors (or None) that receive the rounded parameters, for float32
+    master weights. max_norm: a step given the gradients' norm scales them to at most this norm.
+
+    `clock` (float64 [3]: the steps made, and both betas to that power) is on the device and advanced by
+    the step itself, so a captured step counts at every replay. A checkpoint is m, v, the scales and
+    clock. A parameter that gets no gradient keeps its moments; the bias corrections are those of the
+    common clock."""
+
+    def __init__(self, params, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32, seed=None,
+                 copies=None, max_norm=None):
+        w = "AdamW"
+        self.params = list(params)
+        if not self.params:
+            raise ValueError(f"{w}: no parameters")
+        t0 = self.params[0]
+        self.dev = t0.get_device() if isinstance(t0, torch.Tensor) else -1
+        if self.dev < 0:
+            raise ValueError(f"{w}: the parameters must be tensors on a CUDA device")
+        if bits not in (32, 8):
+            raise ValueError(f"{w}: bits must be 32 or 8, not {bits!r}")
+        if seed is not None and (bits != 8 or not 0 <= int(seed) < 1 << 63):
+            raise ValueError(f"{w}: seed must be >= 0 and belongs to bits 8")
+        if max_norm is not None and not max_norm > 0:
+            raise ValueError(f"{w}: max_norm must be positive")
+        n = len(self.params)
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        self.copies = [None] * n if copies is None else list(copies)
+        if len(decay) != n or len(self.copies) != n:
+            raise ValueError(f"{w}: weight_decay and copies must have an entry for each of the {n} parameters")
+        self.lr, self.betas, self.eps, self.max_norm = lr, betas, eps, max_norm
+        self.bits, self.seed = bits, -1 if seed is None else int(seed)
+        self._tab = np.zeros(n, _PARAM)
+        self._tab["weight_decay"] = decay
+        self._n = np.array([p.numel() if isinstance(p, torch.Tensor) else 0 for p in self.params], np.int64)
+        at = np.concatenate([[0], np.cumsum((self._n + _BLOCK - 1) // _BLOCK * _BLOCK)])
+        self._tab["first"] = at[:-1]
+        self.first, total = at[:-1].tolist(), int(at[-1])
+        self._addresses()
+        z = lambda k, dt: torch.zeros(k, dtype=dt, device=_device(self.dev))
+        if bits == 8:
+            self.m, self.v = z(total, torch.int8), z(total, torch.uint8)
+            self.m_scale, self.v_scale = z(total // _BLOCK, _F32), z(total // _BLOCK, _F32)
+        else:
+            self.m, self.v = z(total, _F32), z(total, _F32)
+            self.m_scale = self.v_scale = None
+        self.clock = torch.tensor([0.0, 1.0, 1.0], dtype=torch.float64, device=_device(self.dev))
+        self.ws = z(256, torch.uint8)
+
+    def _addresses(self):
+        """Reads the parameters' and copies' addresses and checks that no two overlap."""
+        w, dev, tab = "AdamW", self.dev, self._tab
+        tab["p"] = p = [_elements(t, "every parameter", w, dev) for t in self.params]
+        tab["p_dtype"] = [_DTYPES[t.dtype] for t in self.params]
+        spans = []
+        for i, (t, c) in enumerate(zip(self.params, self.copies)):
+            k = int(self._n[i])
+            if t.numel() != k:
+                raise ValueError(f"{w}: parameter {i} has {t.numel()} elements now and had {k}")
+            if c is not None:
+                if not isinstance(c, torch.Tensor) or c.dtype is not torch.bfloat16 or c.numel() != k \
+                        or c.get_device() != dev or not c.is_contiguous():
+                    raise ValueError(f"{w}: copy {i} must be a contiguous bfloat16 tensor of {k} elements on CUDA "
+                                     f"device {dev}")
+                spans.append((c.data_ptr(), 2 * k))
+            spans.append((p[i], t.element_size() * k))
+        tab["copy"] = [0 if c is None else c.data_ptr() for c in self.copies]
+        spans = sorted(s for s in spans if s[1])
+        if any(a + k > b for (a, k), (b, _) in zip(spans, spans[1:])):
+            raise ValueError(f"{w}: parameters or copies overlap in memory")
+
+    def step(self, grads, *, lr=None, norm=None, stream=None):
+        """One step with a gradient for each parameter (None: that parameter is left as it is). lr: a
+        number for this step, or a float32 CUDA tensor [1] that the device reads. norm: float32 [1], as
+        grad_norm gives it; with max_norm the gradients are scaled by min(1, max_norm / (norm + 1e-6))."""
+        w, dev, tab = "AdamW.step", self.dev, self._tab
+        if len(grads) != len(self.params):
+            raise ValueError(f"{w}: {len(grads)} gradients for {len(self.params)} parameters")
+        if [t.data_ptr() for t in self.params] != tab["p"].tolist() or \
+                any(c is not None and c.data_ptr() != a for c, a in zip(self.copies, tab["copy"].tolist())):
+            self._addresses()  # a parameter's memory is another one now
+        g, n, dt = [], [], []
+        for i, x in enumerate(grads):
+            if x is None:
+                g.append(0); n.append(0); dt.append(0)
+                continue
+            g.append(_elements(x, "every gradient", w, dev)); n.append(x.numel()); dt.append(_DTYPES[x.dtype])
+        tab["g"], tab["n"], tab["g_dtype"] = g, n, dt
+        if (tab["n"] != self._n).any() and any(x is not None and x.numel() != k for x, k in zip(grads, self._n)):
+            raise ValueError(f"{w}: a gradient and its parameter differ in size")
+        if norm is not None:
+            _vector(norm, "norm", w, 1, dev)
+            if self.max_norm is None:
+                raise ValueError(f"{w}: norm given, but no max_norm to scale to")
+        lr_dev = None
+        if isinstance(lr, torch.Tensor):
+            _vector(lr, "lr", w, 1, dev)
+            lr_dev, lr = lr, self.lr
+        lr = self.lr if lr is None else lr
+        a = N.MoeAdamW(lr, self.betas[0], self.betas[1], self.eps, self.max_norm or 0.0, self.bits, self.seed)
+        _launch("moe_adamw_step", self.m, stream, ctypes.byref(a), tab.ctypes.data, len(g), self.m.data_ptr(),
+                self.v.data_ptr(), _p(self.m_scale), _p(self.v_scale), self.clock.data_ptr(), _p(lr_dev), _p(norm),
+                self.ws.data_ptr(), self.ws.numel())
+
+    def moments(self, stream=None):
+        """(m, v) as float32 buffers: themselves with bits 32, what the codes stand for with bits 8."""
+        if self.bits == 32:
+            return self.m, self.v
+        with _on(stream):
+            m, v = torch.empty_like(self.m, dtype=_F32), torch.empty_like(self.v, dtype=_F32)
+        _launch("moe_adamw_values", m, stream, self.m.data_ptr(), self.v.data_ptr(), self.m_scale.data_ptr(),
+                self.v_scale.data_ptr(), m.numel(), m.data_ptr(), v.data_ptr())
+        return m, v
