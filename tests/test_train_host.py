@@ -3,6 +3,7 @@ host-only queries: the C ABI's checks on made-up pointers, the binding's on CPU 
 say that they lie on a GPU."""
 
 import ctypes
+from ctypes import c_void_p
 
 import pytest
 import torch
@@ -180,6 +181,7 @@ def test_calls_reach_the_library_on_the_tensors_device(native_lib, monkeypatch):
             table = None
             if name in ("moe_adamw_step", "moe_grad_norm"):
                 addr, n = (a[1], a[2]) if name == "moe_adamw_step" else (a[0], a[1])
+                addr = ctypes.cast(addr, c_void_p).value if isinstance(addr, bytes) else addr
                 table = [N.MoeParam.from_address(addr + i * ctypes.sizeof(N.MoeParam)) for i in range(n)]
                 table = [{f: getattr(t, f) for f, _ in N.MoeParam._fields_} for t in table]
             seen.append((name, at[-1], a[-1], table))

@@ -1,7 +1,8 @@
 """In-tree build of the CUDA library (sm_103a only).
 
 Each ``csrc/*.cu`` compiles to an object in parallel, then one shared library links them:
-``top_gating_expert_gb300/libmoe_gb300.so``. nvcc cross-compiles without a GPU.
+``top_gating_expert_gb300/libmoe_gb300.so``. nvcc cross-compiles without a GPU. Beside it,
+``csrc/lists.cpp`` becomes the extension module ``_lists.so``, which reads lists of torch tensors.
 """
 
 from __future__ import annotations
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -29,6 +31,10 @@ def library_path() -> str:
     return os.path.join(PKG, LIBNAME)
 
 
+def lists_path() -> str:
+    return os.path.join(PKG, "_lists.so")
+
+
 def _nvcc() -> str:
     for cand in (shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -41,12 +47,28 @@ def _sources():
 
 
 def _needs_rebuild(lib: str) -> bool:
-    if not os.path.exists(lib):
+    if not os.path.exists(lib) or not os.path.exists(lists_path()):
         return True
-    t = os.path.getmtime(lib)
-    deps = _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
+    t = min(os.path.getmtime(lib), os.path.getmtime(lists_path()))
+    deps = _sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
         + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _build_lists(verbose: bool) -> None:
+    import torch
+    base = os.path.dirname(torch.__file__)
+    tmp = lists_path() + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", f'-DBUILT_FOR="{torch.__version__}"',
+           "-I", INCLUDE, "-I", os.path.join(base, "include"), "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "lists.cpp"), "-o", tmp, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on lists.cpp")
+    os.replace(tmp, lists_path())
 
 
 def build_library(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -68,8 +90,10 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=()) ->
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
         return obj
 
-    with ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        lists = ex.submit(_build_lists, verbose)
         objs = list(ex.map(compile_one, srcs))
+        lists.result()
     tmp = lib + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -34,6 +34,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kBlock = 256;                // elements that share a scale: a warp's, 8 a lane
 constexpr int kChunk = kWarps * kBlock;    // elements of a CTA's step
+constexpr int kNormChunk = 8192;           // elements of a CTA's step of the norm
 constexpr int kNormSlots = 2048;           // partial sums of the norm: CTAs at most
 constexpr float kMLevels = 127.f * 127.f, kVLevels = 255.f * 255.f;
 
@@ -121,11 +122,42 @@ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
   return h ^ (h >> 16);
 }
 
-// The code of y (in units of the scale, times the levels), r the share of the way above which the next one
-__device__ __forceinline__ float level(float y, float r, float most) {
-  const float k = floorf(__fsqrt_rn(y));
-  const float up = __fsub_rn(y, k * k) > __fmul_rn(r, 2.f * k + 1.f) ? 1.f : 0.f;
-  return fminf(k + up, most);
+// Conversions between small whole numbers and fp32 by the number's place in a float's mantissa (a
+// conversion instruction takes the slow unit, which the square roots fill).
+__device__ __forceinline__ float byte_float(uint32_t w, int k) {  // byte k of w
+  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540u | k)) - 8388608.f;
+}
+__device__ __forceinline__ float signed_byte_float(uint32_t w, int k) {  // of w with every byte's top bit flipped
+  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540u | k)) - 8388736.f;
+}
+// the low bytes of four words
+__device__ __forceinline__ uint32_t pack_bytes(const uint32_t (&w)[4]) {
+  return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+}
+
+// The codes of y (in units of the scale, times the levels): k + 1 where y - k^2 > r (2k + 1), else k, for the
+// k with k^2 <= y < (k + 1)^2; f = 2^16 r. The hardware's root (within 2^-21 here) plus 2^-12 less 1/2, rounded,
+// is k or, next to the following square, k + 1; y - k^2 (exact product, rounded once) tells.
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void level2(float (&y)[2], const float (&f)[2], float (&code)[2]) {
+  const f32x2 magic = set2(12582912.f), y2 = pack2(y[0], y[1]);
+  const f32x2 k2 = add2(add2(add2(pack2(sqrt_approx(y[0]), sqrt_approx(y[1])), set2(-0.499755859375f)), magic),
+                        set2(-12582912.f));
+  const float2 kf = unpack2(k2), tf = unpack2(fma2(mul2(k2, set2(-1.f)), k2, y2));
+  float k[2] = {kf.x, kf.y}, t[2] = {tf.x, tf.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (t[i] < 0.f) {
+      k[i] -= 1.f;
+      t[i] = fmaf(-k[i], k[i], y[i]);
+    }
+  const float2 lim = unpack2(mul2(pack2(f[0], f[1]), fma2(pack2(k[0], k[1]), set2(0x1p-15f), set2(0x1p-16f))));
+  code[0] = t[0] > lim.x ? k[0] + 1.f : k[0];
+  code[1] = t[1] > lim.y ? k[1] + 1.f : k[1];
 }
 
 // A block's scale from the bits of its largest magnitude: NaN where one is not finite, 0 below 2^-100
@@ -179,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
       ms = __fmul_rn(a.m_scale[s0 / kBlock], 1.f / kMLevels);
       vs = __fmul_rn(a.v_scale[s0 / kBlock], 1.f / kVLevels);
     }
-    float m[8], u[8], v[8];
+    float m[8], u[8];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const float g4[4] = {gv[q].x, gv[q].y, gv[q].z, gv[q].w};
@@ -189,32 +221,54 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
         m4[0] = mv[q].x; m4[1] = mv[q].y; m4[2] = mv[q].z; m4[3] = mv[q].w;
         v4[0] = vv[q].x; v4[1] = vv[q].y; v4[2] = vv[q].z; v4[3] = vv[q].w;
       } else {
+        const uint32_t flip = mc[q] ^ 0x80808080u;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float cm = float(int8_t(mc[q] >> (8 * k))), cv = float((vc[q] >> (8 * k)) & 255u);
-          m4[k] = __fmul_rn(cm * fabsf(cm), ms);
-          const float uu = __fmul_rn(cv * cv, vs);
-          v4[k] = __fmul_rn(uu, uu);
+          m4[k] = signed_byte_float(flip, k);
+          v4[k] = byte_float(vc[q], k);
         }
       }
       const int at = 128 * q + 4 * lane, left = valid - at;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float g = __fmul_rn(g4[k], coef);
-        const float mn = __fadd_rn(__fmul_rn(m4[k], a.b1), __fmul_rn(g, a.c1));
-        const float vn = __fadd_rn(__fmul_rn(v4[k], a.b2), __fmul_rn(__fmul_rn(g, g), a.c2));
-        const float un = __fsqrt_rn(vn);
-        const float step = __fmul_rn(__fdiv_rn(mn, __fadd_rn(__fmul_rn(un, rs), a.eps)), size);
-        out[k] = __fsub_rn(__fmul_rn(p4[k], decay), step);
-        m[4 * q + k] = k < left ? mn : 0.f;
-        u[4 * q + k] = k < left ? un : 0.f;
-        v[4 * q + k] = vn;
+      for (int k = 0; k < 4; k += 2) {
+        f32x2 m2, v2;
+        if constexpr (BITS == 32) {
+          m2 = pack2(m4[k], m4[k + 1]);
+          v2 = pack2(v4[k], v4[k + 1]);
+        } else {
+          m2 = mul2(mul2(pack2(m4[k], m4[k + 1]), pack2(fabsf(m4[k]), fabsf(m4[k + 1]))), set2(ms));
+          const f32x2 c2 = pack2(v4[k], v4[k + 1]), u2 = mul2(mul2(c2, c2), set2(vs));
+          v2 = mul2(u2, u2);
+        }
+        // Every product and sum is rounded by itself: the sums one by one, since the assembler fuses a
+        // sum of pairs with a product of pairs in front of it
+        const f32x2 g2 = mul2(pack2(g4[k], g4[k + 1]), set2(coef));
+        const float2 bm = unpack2(mul2(m2, set2(a.b1))), gm = unpack2(mul2(g2, set2(a.c1)));
+        const float2 bv = unpack2(mul2(v2, set2(a.b2))), gg = unpack2(mul2(mul2(g2, g2), set2(a.c2)));
+        const float2 mf = make_float2(__fadd_rn(bm.x, gm.x), __fadd_rn(bm.y, gm.y));
+        const float2 vf = make_float2(__fadd_rn(bv.x, gg.x), __fadd_rn(bv.y, gg.y));
+        const float un[2] = {__fsqrt_rn(vf.x), __fsqrt_rn(vf.y)};
+        const float2 den = unpack2(add2(mul2(pack2(un[0], un[1]), set2(rs)), set2(a.eps)));
+        const f32x2 step = mul2(mul2(pack2(mf.x, mf.y), pack2(rcp_approx(den.x), rcp_approx(den.y))), set2(-size));
+        const float2 pn = unpack2(add2(mul2(pack2(p4[k], p4[k + 1]), set2(decay)), step));
+        out[k] = pn.x;
+        out[k + 1] = pn.y;
+        const int e = 4 * q + k;
+        m[e] = k < left ? mf.x : 0.f;
+        m[e + 1] = k + 1 < left ? mf.y : 0.f;
+        if constexpr (BITS == 32) {
+          u[e] = vf.x;
+          u[e + 1] = vf.y;
+        } else {
+          u[e] = k < left ? un[0] : 0.f;
+          u[e + 1] = k + 1 < left ? un[1] : 0.f;
+        }
       }
       store4(x.p, x.p_bf16, x.vec, e0 + at, left, out);
       if (x.copy) store4(x.copy, 1, x.vec, e0 + at, left, out);
       if constexpr (BITS == 32) {
         store4(a.m, 0, 1, s0 + at, left, reinterpret_cast<const float(&)[4]>(m[4 * q]));
-        store4(a.v, 0, 1, s0 + at, left, reinterpret_cast<const float(&)[4]>(v[4 * q]));
+        store4(a.v, 0, 1, s0 + at, left, reinterpret_cast<const float(&)[4]>(u[4 * q]));
       }
     }
     if constexpr (BITS == 8) {
@@ -223,36 +277,44 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         mb = max(mb, __float_as_uint(m[k]) & 0x7fffffffu);
-        ub = max(ub, __float_as_uint(u[k]) & 0x7fffffffu);
+        ub = max(ub, __float_as_uint(u[k]));
       }
       mb = __reduce_max_sync(0xffffffffu, mb);
-      ub = __reduce_max_sync(0xffffffffu, ub);
+      ub = __reduce_max_sync(0xffffffffu, ub & 0x7fffffffu);
       float sm, im, sv, iv;
       block_scale(mb, kMLevels, sm, im);
       block_scale(ub, kVLevels, sv, iv);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int at = 128 * q + 4 * lane;
-        uint32_t wm = 0, wv = 0;
+        uint32_t wm[4], wv[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float rm = 0.5f, rv = 0.5f;
+        for (int k = 0; k < 4; k += 2) {
+          float fm[2] = {32768.f, 32768.f}, fv[2] = {32768.f, 32768.f};
           if (a.seed >= 0) {
-            const int64_t place = s0 + at + k;
-            const uint32_t h = mix32(uint32_t(place) ^ uint32_t(place >> 32) * 0x2545F491u ^ key);
-            rm = (float(h & 0xffffu) + 0.5f) * 0x1p-16f;
-            rv = (float(h >> 16) + 0.5f) * 0x1p-16f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int64_t place = s0 + at + k + i;
+              const uint32_t h = mix32(uint32_t(place) ^ uint32_t(place >> 32) * 0x2545F491u ^ key);
+              fm[i] = __uint_as_float(__byte_perm(h, 0x4B000000u, 0x7610u)) - 8388607.5f;  // low half + 1/2
+              fv[i] = __uint_as_float(__byte_perm(h, 0x4B000000u, 0x7632u)) - 8388607.5f;
+            }
           }
-          const float mk = m[4 * q + k];
-          const float cm = level(__fmul_rn(fabsf(mk), im), rm, 127.f);
-          const float yv = __fmul_rn(u[4 * q + k], iv);
-          const float cv = yv > 0.f ? fmaxf(level(yv, rv, 255.f), 1.f) : 0.f;
-          // a NaN scale: the codes do not matter, but are whole (float2int takes NaN to 0)
-          wm |= (uint32_t(__float2int_rz(copysignf(cm, mk))) & 255u) << (8 * k);
-          wv |= (uint32_t(__float2int_rz(cv)) & 255u) << (8 * k);
+          const int e = 4 * q + k;
+          const float2 ym2 = unpack2(mul2(pack2(fabsf(m[e]), fabsf(m[e + 1])), set2(im)));
+          const float2 yv2 = unpack2(mul2(pack2(u[e], u[e + 1]), set2(iv)));
+          float ym[2] = {ym2.x, ym2.y}, yv[2] = {yv2.x, yv2.y}, cm[2], cv[2];
+          level2(ym, fm, cm);
+          level2(yv, fv, cv);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // whole numbers in the mantissa's low byte; after a NaN scale any
+            wm[k + i] = __float_as_uint(copysignf(fminf(cm[i], 127.f), m[e + i]) + 12582912.f);
+            wv[k + i] = __float_as_uint(fminf(yv[i] > 0.f ? fmaxf(cv[i], 1.f) : 0.f, 255.f) + 12582912.f);
+          }
         }
-        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s0 + at), wm);
-        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + s0 + at), wv);
+        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s0 + at), pack_bytes(wm));
+        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + s0 + at), pack_bytes(wv));
       }
       if (lane == 0) {
         a.m_scale[s0 / kBlock] = sm;
@@ -281,13 +343,14 @@ __global__ void __launch_bounds__(kThreads)
   pdl_wait();
   pdl_trigger();
   for (int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * 4; i < n; i += int64_t(gridDim.x) * kThreads * 4) {
-    const uint32_t wm = *reinterpret_cast<const uint32_t*>(mc + i), wv = *reinterpret_cast<const uint32_t*>(vc + i);
+    const uint32_t wm = __ldcs(reinterpret_cast<const uint32_t*>(mc + i)) ^ 0x80808080u;
+    const uint32_t wv = __ldcs(reinterpret_cast<const uint32_t*>(vc + i));
     const float ms = __fmul_rn(__ldg(m_scale + i / kBlock), 1.f / kMLevels);
     const float vs = __fmul_rn(__ldg(v_scale + i / kBlock), 1.f / kVLevels);
     float fm[4], fv[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float a = float(int8_t(wm >> (8 * k))), b = float((wv >> (8 * k)) & 255u);
+      const float a = signed_byte_float(wm, k), b = byte_float(wv, k);
       fm[k] = __fmul_rn(a * fabsf(a), ms);
       const float u = __fmul_rn(b * b, vs);
       fv[k] = __fmul_rn(u, u);
@@ -319,18 +382,44 @@ __global__ void __launch_bounds__(kThreads, 4) grad_norm_kernel(const __grid_con
   float sum = 0.f;
   for (int64_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
     const Tensor& x = tab.t[tensor_of(tab, a.n, chunk)];
-    const int64_t e0 = (chunk - x.chunk0) * kChunk + threadIdx.x * 4;
-    float4 v[kChunk / (kThreads * 4)];
+    const int64_t e0 = (chunk - x.chunk0) * kNormChunk, rest = x.n - e0;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (x.vec && rest >= kNormChunk) {  // all loads of the chunk in flight
+      if (!x.g_bf16) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x.g) + e0) + threadIdx.x;
+        float4 v[kNormChunk / (kThreads * 4)];
 #pragma unroll
-    for (int q = 0; q < kChunk / (kThreads * 4); ++q) {
-      const int64_t i = e0 + q * kThreads * 4;
-      v[q] = load4(x.g, x.g_bf16, x.vec, i, int(max(int64_t(0), min(int64_t(4), x.n - i))));
+        for (int q = 0; q < kNormChunk / (kThreads * 4); ++q) v[q] = __ldcs(p + q * kThreads);
+#pragma unroll
+        for (int q = 0; q < kNormChunk / (kThreads * 4); ++q) {
+          s[0] = fmaf(v[q].x, v[q].x, s[0]); s[1] = fmaf(v[q].y, v[q].y, s[1]);
+          s[2] = fmaf(v[q].z, v[q].z, s[2]); s[3] = fmaf(v[q].w, v[q].w, s[3]);
+        }
+      } else {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x.g) + e0) + threadIdx.x;
+        uint4 v[kNormChunk / (kThreads * 8)];
+#pragma unroll
+        for (int q = 0; q < kNormChunk / (kThreads * 8); ++q) v[q] = __ldcs(p + q * kThreads);
+#pragma unroll
+        for (int q = 0; q < kNormChunk / (kThreads * 8); ++q) {
+          const uint32_t w[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]));
+            s[k] = fmaf(f.x, f.x, s[k]);
+            s[k] = fmaf(f.y, f.y, s[k]);
+          }
+        }
+      }
+    } else {
+#pragma unroll 2
+      for (int q = threadIdx.x * 4; q < kNormChunk && q < rest; q += kThreads * 4) {
+        const float4 v = load4(x.g, x.g_bf16, x.vec, e0 + q, int(min(int64_t(4), rest - q)));
+        s[0] = fmaf(v.x, v.x, s[0]); s[1] = fmaf(v.y, v.y, s[1]);
+        s[2] = fmaf(v.z, v.z, s[2]); s[3] = fmaf(v.w, v.w, s[3]);
+      }
     }
-    float s = 0.f;
-#pragma unroll
-    for (int q = 0; q < kChunk / (kThreads * 4); ++q)
-      s += (v[q].x * v[q].x + v[q].y * v[q].y) + (v[q].z * v[q].z + v[q].w * v[q].w);
-    sum += s;
+    sum += (s[0] + s[1]) + (s[2] + s[3]);
   }
   sum = block_sum_all<kWarps>(sum, s_red);
   if (threadIdx.x == 0) {
@@ -395,8 +484,9 @@ int fill(Table<CAP>& tab, const moe_param_t* t, int n, int at, double lr, bool s
     d.decay = step ? float(1.0 - lr * x.weight_decay) : 1.f;
     d.p_bf16 = step && x.p_dtype == MOE_BF16;
     d.g_bf16 = x.g_dtype == MOE_BF16;
-    d.vec = on(x.g, d.g_bf16 ? 8 : 16) && (!step || (on(x.p, d.p_bf16 ? 8 : 16) && on(x.copy, 8)));
-    *chunks += (x.n + kChunk - 1) / kChunk;
+    d.vec = on(x.g, d.g_bf16 && step ? 8 : 16) && (!step || (on(x.p, d.p_bf16 ? 8 : 16) && on(x.copy, 8)));
+    const int64_t chunk = step ? kChunk : kNormChunk;
+    *chunks += (x.n + chunk - 1) / chunk;
   }
   return at;
 }

@@ -87,8 +87,9 @@ struct XentEpi {
   // kXentGrad: d = 2^(l log2(e) - x) y, less z at the target's column (bits of w) - v0; z = 0: d = 0
   const float4* row = nullptr;
   int v0 = 0;
-  // kProductSum: v + acc_in (null: v) to acc_out, or rounded to out where that is null; 16-byte
-  // aligned rows of ldacc floats, a multiple of 8
+  // kProductSum: v + acc_in (null: v) to acc_out, or times factor[0] (null: 1) and rounded to out where
+  // acc_out is null; 16-byte aligned rows of ldacc floats, a multiple of 8
+  const float* factor = nullptr;
   const float* acc_in = nullptr;
   float* acc_out = nullptr;
   int64_t ldacc = 0;

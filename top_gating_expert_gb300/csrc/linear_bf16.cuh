@@ -190,12 +190,14 @@ __device__ __forceinline__ void emit_row_mode(const LinearEpi& e, const XentEpi&
   } else {  // kProductSum: the accumulators' rows are padded to whole groups of 8 columns
     const float* in = x.acc_in ? x.acc_in + row * x.ldacc + c0 : nullptr;
     float* out = x.acc_out ? x.acc_out + row * x.ldacc + c0 : nullptr;
+    const float f = x.factor && !out ? __ldg(x.factor) : 1.f;
 #pragma unroll
     for (int q = 0; q < NC; ++q) {
       const int c = lane_col<VEC>(lane, q);
       if (c >= nc) continue;
       if (in) v[q] += in[c];
       if (out) out[c] = v[q];
+      v[q] *= f;
     }
     if (!out) store_row<NC, VEC>(e.out, row * e.ldo + c0, v, lane, nc);
   }
@@ -684,6 +686,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint8_t* box = sBox + (warp - 2) * 4096;
     int nb = 0;  // the box of the next 32 columns
     int i = 0;
+    float factor = 1.f;
+    if constexpr (MODE == kProductSum) factor = p.x.factor && !p.x.acc_out ? __ldg(p.x.factor) : 1.f;
     // v (this lane's row, 32 columns) into box nb and out; the box's last store has been read
     auto write_box = [&](const CUtensorMap* map, const float (&v)[32], int col, int row) {
       uint8_t* b = box + nb * 2048;
@@ -820,6 +824,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                   v[4 * j] += in[j].x; v[4 * j + 1] += in[j].y; v[4 * j + 2] += in[j].z; v[4 * j + 3] += in[j].w;
                 }
             }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= factor;
             if (p.x.acc_out) {
               if (aout) {
 #pragma unroll

@@ -119,6 +119,19 @@ _PARAM = np.dtype([("p", np.uint64), ("g", np.uint64), ("copy", np.uint64), ("n"
 _BLOCK = 256  # elements that share a scale in 8 bits; every tensor's moments start at a multiple
 
 
+@lru_cache(maxsize=1)
+def _lists():
+    """The extension that reads lists of tensors (built beside the library)."""
+    N.lib()
+    try:
+        from . import _lists as m
+    except ImportError as e:
+        raise RuntimeError("the extension _lists is not built; run `python -m top_gating_expert_gb300.build`") from e
+    if m.built_for != torch.__version__:
+        raise RuntimeError(f"_lists was built for torch {m.built_for}, not {torch.__version__}: build it again")
+    return m
+
+
 def _elements(t, name, where, dev):
     """Checks a tensor of a list by its elements alone: its address."""
     if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.get_device() != dev or not t.is_contiguous():
@@ -142,23 +155,19 @@ def grad_norm(grads, *, out=None, ws=None, stream=None):
     """float32 [1]: the 2-norm of all elements of the tensors (float32 or bfloat16, contiguous; None
     is left out). Nothing is read back: AdamW.step takes it as it is."""
     w = "grad_norm"
-    ts = [g for g in grads if g is not None]
-    if not ts:
-        raise ValueError(f"{w}: no gradients")
-    dev = ts[0].get_device() if isinstance(ts[0], torch.Tensor) else -1
+    grads = list(grads)
+    t = next((g for g in grads if g is not None), None)
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
     if dev < 0:
-        raise ValueError(f"{w}: the gradients must be tensors on a CUDA device")
-    tab = np.zeros(len(ts), _PARAM)
-    tab["g"] = [_elements(g, "every gradient", w, dev) for g in ts]
-    tab["n"] = [g.numel() for g in ts]
-    tab["g_dtype"] = [_DTYPES[g.dtype] for g in ts]
+        raise ValueError(f"{w}: there must be a gradient, and all of them on a CUDA device")
+    tab, n = _lists().gradients(grads, dev)
     if out is None:
         out = _new((1,), _F32, dev, stream)
     _vector(out, "out", w, 1, dev)
     if ws is None:
         ws = _scratch(_grad_norm_ws_bytes(), dev, stream)
     _workspace_ok(ws, w, dev)
-    _launch("moe_grad_norm", out, stream, tab.ctypes.data, len(ts), out.data_ptr(), ws.data_ptr(), ws.numel())
+    _launch("moe_grad_norm", out, stream, tab, n, out.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 
@@ -202,7 +211,9 @@ class AdamW:
         self.bits, self.seed = bits, -1 if seed is None else int(seed)
         self._tab = np.zeros(n, _PARAM)
         self._tab["weight_decay"] = decay
+        self._tab_at = self._tab.ctypes.data
         self._n = np.array([p.numel() if isinstance(p, torch.Tensor) else 0 for p in self.params], np.int64)
+        self._n_at = self._n.ctypes.data
         at = np.concatenate([[0], np.cumsum((self._n + _BLOCK - 1) // _BLOCK * _BLOCK)])
         self._tab["first"] = at[:-1]
         self.first, total = at[:-1].tolist(), int(at[-1])
@@ -243,21 +254,9 @@ class AdamW:
         """One step with a gradient for each parameter (None: that parameter is left as it is). lr: a
         number for this step, or a float32 CUDA tensor [1] that the device reads. norm: float32 [1], as
         grad_norm gives it; with max_norm the gradients are scaled by min(1, max_norm / (norm + 1e-6))."""
-        w, dev, tab = "AdamW.step", self.dev, self._tab
-        if len(grads) != len(self.params):
-            raise ValueError(f"{w}: {len(grads)} gradients for {len(self.params)} parameters")
-        if [t.data_ptr() for t in self.params] != tab["p"].tolist() or \
-                any(c is not None and c.data_ptr() != a for c, a in zip(self.copies, tab["copy"].tolist())):
+        w, dev = "AdamW.step", self.dev
+        if _lists().step(self._tab_at, self._n_at, grads, self.params, self.copies, dev):
             self._addresses()  # a parameter's memory is another one now
-        g, n, dt = [], [], []
-        for i, x in enumerate(grads):
-            if x is None:
-                g.append(0); n.append(0); dt.append(0)
-                continue
-            g.append(_elements(x, "every gradient", w, dev)); n.append(x.numel()); dt.append(_DTYPES[x.dtype])
-        tab["g"], tab["n"], tab["g_dtype"] = g, n, dt
-        if (tab["n"] != self._n).any() and any(x is not None and x.numel() != k for x, k in zip(grads, self._n)):
-            raise ValueError(f"{w}: a gradient and its parameter differ in size")
         if norm is not None:
             _vector(norm, "norm", w, 1, dev)
             if self.max_norm is None:
@@ -268,7 +267,7 @@ class AdamW:
             lr_dev, lr = lr, self.lr
         lr = self.lr if lr is None else lr
         a = N.MoeAdamW(lr, self.betas[0], self.betas[1], self.eps, self.max_norm or 0.0, self.bits, self.seed)
-        _launch("moe_adamw_step", self.m, stream, ctypes.byref(a), tab.ctypes.data, len(g), self.m.data_ptr(),
+        _launch("moe_adamw_step", self.m, stream, ctypes.byref(a), self._tab_at, len(self.params), self.m.data_ptr(),
                 self.v.data_ptr(), _p(self.m_scale), _p(self.v_scale), self.clock.data_ptr(), _p(lr_dev), _p(norm),
                 self.ws.data_ptr(), self.ws.numel())
 
