@@ -221,6 +221,29 @@ def test_tiny_and_zero_gradients(native_lib, bits):
     assert torch.isfinite(p).all()
 
 
+@pytest.mark.parametrize("seed", [None, 7])
+@pytest.mark.parametrize("scale", [1e-21, 1e-18, 1e-15, 1e-8, 1.0, 1e8, 1e14, 1e16, 1e18])
+def test_codes_at_every_magnitude(native_lib, scale, seed):
+    """Codes and scales bit for bit, and steps of the right size without eps, for gradients whose squares are
+    denormal, ordinary and near fp32's end; some 10^-6 of the others."""
+    n = 2048
+    g = torch.randn(n, generator=generator(1), device="cuda") * scale
+    g[::9] *= 1e-6
+    g[::50] = 0.0
+    p = torch.zeros(n, device="cuda")
+    opt = train.AdamW([p], lr=1.0, bits=8, seed=seed, eps=0.0, weight_decay=0.0, betas=(0.9, 0.95))
+    opt.step([g])
+    m, v = g * (1.0 - 0.9), g * g * (1.0 - 0.95)
+    rm, rv = plain._dither(dict(seed=-1 if seed is None else seed), n, 1)
+    for got, want in zip((opt.m, opt.m_scale, opt.v, opt.v_scale), plain._m_codes(m, rm) + plain._v_codes(v.sqrt(), rv)):
+        assert torch.equal(got, want)
+    some = (g != 0) & (v > 1e-37)
+    assert torch.isnan(p[g == 0]).all()  # 0 / 0 without eps
+    ref = -(m.double() / 0.1) / (v.double() / 0.05).sqrt()
+    assert ((p.double() - ref).abs() <= 64 * U)[some].all()
+    assert torch.isfinite(p[(g != 0) & (v > 0)]).all()
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_missing_gradients_and_lr(native_lib, bits):
     """A parameter without a gradient, its moments and its copy are left alone; lr by number, by call and

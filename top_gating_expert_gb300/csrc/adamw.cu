@@ -24,6 +24,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "elem.cuh"
 #include "internal.h"
@@ -124,40 +125,81 @@ __device__ __forceinline__ uint32_t mix32(uint32_t h) {
 
 // Conversions between small whole numbers and fp32 by the number's place in a float's mantissa (a
 // conversion instruction takes the slow unit, which the square roots fill).
-__device__ __forceinline__ float byte_float(uint32_t w, int k) {  // byte k of w
-  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540u | k)) - 8388608.f;
-}
-__device__ __forceinline__ float signed_byte_float(uint32_t w, int k) {  // of w with every byte's top bit flipped
-  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540u | k)) - 8388736.f;
+__device__ __forceinline__ float byte_bits(uint32_t w, int k) {  // 2^23 + byte k of w
+  return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540u | k));
 }
 // the low bytes of four words
 __device__ __forceinline__ uint32_t pack_bytes(const uint32_t (&w)[4]) {
   return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
 }
-
-// The codes of y (in units of the scale, times the levels): k + 1 where y - k^2 > r (2k + 1), else k, for the
-// k with k^2 <= y < (k + 1)^2; f = 2^16 r. The hardware's root (within 2^-21 here) plus 2^-12 less 1/2, rounded,
-// is k or, next to the following square, k + 1; y - k^2 (exact product, rounded once) tells.
+// the hardware's root (within 2^-21): with denormals, or with those taken as 0
 __device__ __forceinline__ float sqrt_approx(float x) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float sqrt_approx_ftz(float x) {
   float r;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ void level2(float (&y)[2], const float (&f)[2], float (&code)[2]) {
-  const f32x2 magic = set2(12582912.f), y2 = pack2(y[0], y[1]);
-  const f32x2 k2 = add2(add2(add2(pack2(sqrt_approx(y[0]), sqrt_approx(y[1])), set2(-0.499755859375f)), magic),
-                        set2(-12582912.f));
-  const float2 kf = unpack2(k2), tf = unpack2(fma2(mul2(k2, set2(-1.f)), k2, y2));
-  float k[2] = {kf.x, kf.y}, t[2] = {tf.x, tf.y};
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// the largest magnitude of three (NaN if one is)
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Codes. For y >= 0 (in units of the scale, times the levels) the code is k + 1 where t = y - k^2 > r (2k + 1),
+// else k, for the k with k^2 <= y < (k + 1)^2; f = 2^16 r. k comes from the hardware's root plus
+// 2^-14 less 1/2, rounded: it is never less (the root is within 2^-23, the sum within 2^-17), and next to the
+// following square k + 1 (t < 0).
+constexpr float kToFloor = -0.5f + 0x1p-14f, kMagic = 12582912.f;  // 1.5 * 2^23
+__device__ __forceinline__ f32x2 floor_root2(f32x2 y) {
+  const float2 f = unpack2(y);
+  return add2(add2(add2(pack2(sqrt_approx_ftz(f.x), sqrt_approx_ftz(f.y)), set2(kToFloor)), set2(kMagic)), set2(-kMagic));
+}
+__device__ __forceinline__ f32x2 limit2(const float (&f)[2], f32x2 k) {  // r (2k + 1), rounded once
+  return mul2(pack2(f[0], f[1]), fma2(k, set2(0x1p-15f), set2(0x1p-16f)));
+}
+// the codes of two exact y
+__device__ __forceinline__ void exact_codes(const float (&y)[2], const float (&f)[2], float (&code)[2]) {
+  const float2 k2 = unpack2(floor_root2(pack2(y[0], y[1])));
+  float k[2] = {k2.x, k2.y}, t[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 2; ++i) {
+    t[i] = fmaf(-k[i], k[i], y[i]);
     if (t[i] < 0.f) {
       k[i] -= 1.f;
       t[i] = fmaf(-k[i], k[i], y[i]);
     }
-  const float2 lim = unpack2(mul2(pack2(f[0], f[1]), fma2(pack2(k[0], k[1]), set2(0x1p-15f), set2(0x1p-16f))));
+  }
+  const float2 lim = unpack2(limit2(f, pack2(k[0], k[1])));
   code[0] = t[0] > lim.x ? k[0] + 1.f : k[0];
   code[1] = t[1] > lim.y ? k[1] + 1.f : k[1];
+}
+// The same without the correction of k and for y off by up to y 2^-21: `margin` becomes negative where a code may be
+// another one (t not safely above 0, where k and the limit may belong to the next square, or close to the limit).
+// Not for `top`, the block's largest value, whose code is the highest: its y is next to a square always.
+__device__ __forceinline__ void near_codes(f32x2 y, const float (&f)[2], float v0, float v1, float top, float (&code)[2],
+                                           float& margin) {
+  const f32x2 k2 = floor_root2(y);
+  const float2 yf = unpack2(y), k = unpack2(k2), lim = unpack2(limit2(f, k2));
+  const float t0 = fmaf(-k.x, k.x, yf.x), t1 = fmaf(-k.y, k.y, yf.y);
+  code[0] = k.x;
+  code[1] = k.y;
+  if (t0 > lim.x) code[0] += 1.f;
+  if (t1 > lim.y) code[1] += 1.f;
+  if (v0 != top) margin = min3(margin, fmaf(yf.x, -0x1p-21f, t0), fmaf(yf.x, -0x1p-21f, fabsf(t0 - lim.x)));
+  if (v1 != top) margin = min3(margin, fmaf(yf.y, -0x1p-21f, t1), fmaf(yf.y, -0x1p-21f, fabsf(t1 - lim.y)));
+}
+__device__ __forceinline__ float v_code(float c, float y) {  // 0 for 0 alone, 255 at most
+  return fminf(fmaxf(c, __saturatef(y * 0x1p126f)), 255.f);
 }
 
 // A block's scale from the bits of its largest magnitude: NaN where one is not finite, 0 below 2^-100
@@ -168,158 +210,220 @@ __device__ __forceinline__ void block_scale(uint32_t bits, float levels, float& 
   inv = s == 0.f ? 0.f : __fdiv_rn(levels, s);
 }
 
+// What all blocks of a step share.
+struct Shared {
+  float size, rs, coef;  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t), the clip factor
+  uint32_t key;
+};
+
+// A warp's 256 elements e0 .. of tensor x, places s0 .. of the moments. FULL: all of them exist, in whole
+// accesses; P16, G16: p and g in bf16 (without FULL x says so).
+template <int BITS, bool FULL, bool P16, bool G16>
+__device__ __forceinline__ void adamw_block(const Tensor& x, const StepArgs& a, const Shared& sh, float decay, int64_t e0,
+                                            int64_t s0, int valid_) {
+  const int lane = threadIdx.x & 31;
+  const int valid = FULL ? kBlock : valid_;
+  const int p16 = FULL ? P16 : x.p_bf16, g16 = FULL ? G16 : x.g_bf16, vec = FULL ? 1 : x.vec;
+  const float size = sh.size, rs = sh.rs, coef = sh.coef;
+  const uint32_t key = sh.key;
+  float4 pv[2], gv[2], mv[2], vv[2];
+  uint32_t mc[2], vc[2];
+  float ms = 0.f, vs = 0.f;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int at = 128 * q + 4 * lane, left = valid - at;
+    gv[q] = load4(x.g, g16, vec, e0 + at, left);
+    pv[q] = load4(x.p, p16, vec, e0 + at, left);
+    if constexpr (BITS == 32) {
+      mv[q] = load4(a.m, 0, 1, s0 + at, left);
+      vv[q] = load4(a.v, 0, 1, s0 + at, left);
+    } else {  // whole words of codes: the buffer is padded to blocks
+      mc[q] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s0 + at));
+      vc[q] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s0 + at));
+    }
+  }
+  if constexpr (BITS == 8) {
+    ms = __fmul_rn(a.m_scale[s0 / kBlock], 1.f / kMLevels);
+    vs = __fmul_rn(a.v_scale[s0 / kBlock], 1.f / kVLevels);
+  }
+  // What does not exist reads as 0 (the codes behind a tensor's end are), and its moments stay 0.
+  float m[8], v[8];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float g4[4] = {gv[q].x, gv[q].y, gv[q].z, gv[q].w};
+    const float p4[4] = {pv[q].x, pv[q].y, pv[q].z, pv[q].w};
+    float m4[4], v4[4], out[4];
+    if constexpr (BITS == 32) {
+      m4[0] = mv[q].x; m4[1] = mv[q].y; m4[2] = mv[q].z; m4[3] = mv[q].w;
+      v4[0] = vv[q].x; v4[1] = vv[q].y; v4[2] = vv[q].z; v4[3] = vv[q].w;
+    }
+    const uint32_t flip = BITS == 8 ? mc[q] ^ 0x80808080u : 0u;  // signed bytes from 0 on
+    const int at = 128 * q + 4 * lane, left = valid - at;
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      f32x2 m2, v2;
+      if constexpr (BITS == 32) {
+        m2 = pack2(m4[k], m4[k + 1]);
+        v2 = pack2(v4[k], v4[k + 1]);
+      } else {
+        const float2 cm = unpack2(add2(pack2(byte_bits(flip, k), byte_bits(flip, k + 1)), set2(-8388736.f)));
+        const f32x2 cv = add2(pack2(byte_bits(vc[q], k), byte_bits(vc[q], k + 1)), set2(-8388608.f));
+        m2 = mul2(pack2(cm.x * fabsf(cm.x), cm.y * fabsf(cm.y)), set2(ms));
+        const f32x2 u2 = mul2(mul2(cv, cv), set2(vs));
+        v2 = mul2(u2, u2);
+      }
+      // Every product and sum of the moments is rounded by itself: the sums one by one, since the
+      // assembler fuses a sum of pairs with a product of pairs in front of it
+      const f32x2 g2 = mul2(pack2(g4[k], g4[k + 1]), set2(coef));
+      const float2 bm = unpack2(mul2(m2, set2(a.b1))), gm = unpack2(mul2(g2, set2(a.c1)));
+      const float2 bv = unpack2(mul2(v2, set2(a.b2))), gg = unpack2(mul2(mul2(g2, g2), set2(a.c2)));
+      const float2 mf = make_float2(__fadd_rn(bm.x, gm.x), __fadd_rn(bm.y, gm.y));
+      const float2 vf = make_float2(__fadd_rn(bv.x, gg.x), __fadd_rn(bv.y, gg.y));
+      // the step takes the hardware's root and reciprocal: a few ulp of a step that is 10^-3 of p
+      const float2 den = unpack2(fma2(pack2(sqrt_approx(vf.x), sqrt_approx(vf.y)), set2(rs), set2(a.eps)));
+      const f32x2 step = mul2(mul2(pack2(mf.x, mf.y), pack2(rcp_approx(den.x), rcp_approx(den.y))), set2(-size));
+      const float2 pn = unpack2(fma2(pack2(p4[k], p4[k + 1]), set2(decay), step));
+      out[k] = pn.x;
+      out[k + 1] = pn.y;
+      const int e = 4 * q + k;
+      m[e] = mf.x;
+      m[e + 1] = mf.y;
+      v[e] = vf.x;
+      v[e + 1] = vf.y;
+    }
+    store4(x.p, p16, vec, e0 + at, left, out);
+    if (x.copy) store4(x.copy, 1, vec, e0 + at, left, out);
+    if constexpr (BITS == 32) {
+      store4(a.m, 0, 1, s0 + at, left, reinterpret_cast<const float(&)[4]>(m[4 * q]));
+      store4(a.v, 0, 1, s0 + at, left, reinterpret_cast<const float(&)[4]>(v[4 * q]));
+    }
+  }
+  if constexpr (BITS == 8) {
+    // bits of magnitudes compare as the magnitudes do, NaN above all; the root of the largest v is the
+    // largest root
+    float mt = max3_abs(m[0], m[1], m[2]), vt = max3_abs(v[0], v[1], v[2]);
+    mt = max3_abs(mt, m[3], m[4]);
+    vt = max3_abs(vt, v[3], v[4]);
+    mt = max3_abs(mt, m[5], max3_abs(m[6], m[7], 0.f));
+    vt = max3_abs(vt, v[5], max3_abs(v[6], v[7], 0.f));
+    const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mt));
+    const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(vt));
+    float sm, im, sv, iv;
+    block_scale(mb, kMLevels, sm, im);
+    block_scale(__float_as_uint(__fsqrt_rn(__uint_as_float(vb))), kVLevels, sv, iv);
+    // The thresholds of element e, times 2^16: the halves of mix32(place ^ key), plus 1/2. Of the place the bits of
+    // 128 (e / 4) + e % 4 are those of the element in the lane, so the hash's first step is shared.
+    const uint32_t x0 = uint32_t(s0 + 4 * lane) ^ (uint32_t(s0 >> 32) * 0x2545F491u) ^ key, x1 = x0 ^ (x0 >> 16);
+    auto thresholds = [&](int e, float& fm, float& fv) {
+      uint32_t h = (x1 ^ uint32_t(128 * (e / 4) + (e & 3))) * 0x9E3779B1u;
+      h = (h ^ (h >> 15)) * 0x85157AF5u;
+      fm = __uint_as_float(__byte_perm(h ^ (h >> 16), 0x4B000000u, 0x7610u));
+      fv = __uint_as_float(__byte_perm(h, 0x4B000000u, 0x7632u));
+    };
+    auto thresholds2 = [&](int e, float (&fm)[2], float (&fv)[2]) {
+      float m0, m1, v0, v1;
+      thresholds(e, m0, v0);
+      thresholds(e + 1, m1, v1);
+      const float2 a2 = unpack2(add2(pack2(m0, m1), set2(-8388607.5f))), b2 = unpack2(add2(pack2(v0, v1), set2(-8388607.5f)));
+      fm[0] = a2.x; fm[1] = a2.y;
+      fv[0] = b2.x; fv[1] = b2.y;
+    };
+    // roots of 2^24 v, which no denormal v is too small for; largest ones too large for it go the exact way
+    const float iv12 = iv * 0x1p-12f;
+    uint32_t wm[2], wv[2];
+    float margin = vb >= 0x71800000u ? -1.f : 0.f;  // 2^100
+    auto codes = [&](auto exact) {
+      constexpr bool EXACT = decltype(exact)::value;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t bm[4], bv[4];
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const int e = 4 * q + k;
+          float fm[2] = {32768.f, 32768.f}, fv[2] = {32768.f, 32768.f};
+          if (a.seed >= 0) thresholds2(e, fm, fv);
+          const float ym[2] = {__fmul_rn(fabsf(m[e]), im), __fmul_rn(fabsf(m[e + 1]), im)};
+          float cm[2], cv[2], yv[2];
+          if constexpr (!EXACT) exact_codes(ym, fm, cm);
+          if constexpr (EXACT) {
+            yv[0] = __fmul_rn(__fsqrt_rn(v[e]), iv);
+            yv[1] = __fmul_rn(__fsqrt_rn(v[e + 1]), iv);
+            exact_codes(yv, fv, cv);
+          } else {
+            const float2 up = unpack2(mul2(pack2(v[e], v[e + 1]), set2(0x1p24f)));
+            const f32x2 y2 = mul2(pack2(sqrt_approx_ftz(up.x), sqrt_approx_ftz(up.y)), set2(iv12));
+            const float2 f = unpack2(y2);
+            yv[0] = f.x;
+            yv[1] = f.y;
+            near_codes(y2, fv, v[e], v[e + 1], __uint_as_float(vb), cv, margin);
+          }
+          // whole numbers in the mantissa's low byte; after a NaN scale any
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (!EXACT) bm[k + i] = __float_as_uint(copysignf(fminf(cm[i], 127.f), m[e + i]) + kMagic);
+            bv[k + i] = __float_as_uint(v_code(cv[i], yv[i]) + kMagic);
+          }
+        }
+        if constexpr (!EXACT) wm[q] = pack_bytes(bm);
+        wv[q] = pack_bytes(bv);
+      }
+    };
+    codes(std::false_type{});
+    // some code of v is near a border (about one block of twenty): the block's from correctly rounded roots
+    if (__any_sync(0xffffffffu, margin < 0.f)) codes(std::true_type{});
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int64_t at = s0 + 128 * q + 4 * lane;
+      __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + at), wm[q]);
+      __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + at), wv[q]);
+    }
+    if (lane == 0) {
+      a.m_scale[s0 / kBlock] = sm;
+      a.v_scale[s0 / kBlock] = sv;
+    }
+  }
+}
+
 template <int BITS, int CAP>
 __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ Table<CAP> tab, const StepArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const float lr = a.lr_dev ? __ldg(a.lr_dev) : a.lr;
-  const double t = a.clock[0] + 1.0, b1t = a.clock[1] * a.beta1, b2t = a.clock[2] * a.beta2;
-  const float size = __fdiv_rn(lr, float(1.0 - b1t)), rs = __fdiv_rn(1.f, __fsqrt_rn(float(1.0 - b2t)));
-  float coef = 1.f;
+  Shared sh;
+  sh.size = __fdiv_rn(lr, float(1.0 - a.clock[1] * a.beta1));
+  sh.rs = __fdiv_rn(1.f, __fsqrt_rn(float(1.0 - a.clock[2] * a.beta2)));
+  sh.coef = 1.f;
   if (a.norm) {
-    coef = __fdiv_rn(a.max_norm, __fadd_rn(__ldg(a.norm), 1e-6f));
-    if (coef > 1.f) coef = 1.f;  // NaN stays
+    sh.coef = __fdiv_rn(a.max_norm, __fadd_rn(__ldg(a.norm), 1e-6f));
+    if (sh.coef > 1.f) sh.coef = 1.f;  // NaN stays
   }
-  uint32_t key = 0;
-  if (BITS == 8 && a.seed >= 0) key = mix32(uint32_t(a.seed) + 0x632BE5ABu * uint32_t(int64_t(t)));
+  sh.key = 0;
+  if (BITS == 8 && a.seed >= 0) sh.key = mix32(uint32_t(a.seed) + 0x632BE5ABu * uint32_t(int64_t(a.clock[0] + 1.0)));
 
+  int at = 0;
+  int64_t end = 0;  // the first chunk that is not tensor at's
   for (int64_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
-    const Tensor& x = tab.t[tensor_of(tab, a.n, chunk)];
+    if (chunk >= end) {
+      at = tensor_of(tab, a.n, chunk);
+      end = at + 1 < a.n ? tab.t[at + 1].chunk0 : a.chunks;
+    }
+    const Tensor& x = tab.t[at];
     const int64_t e0 = (chunk - x.chunk0) * kChunk + warp * kBlock;
     if (e0 >= x.n) continue;  // the whole warp
     const int64_t s0 = x.first + e0;
     const int valid = int(min(int64_t(kBlock), x.n - e0));
     const float decay = a.lr_dev ? fmaf(-lr, x.wd, 1.f) : x.decay;
-    float4 pv[2], gv[2], mv[2], vv[2];
-    uint32_t mc[2], vc[2];
-    float ms = 0.f, vs = 0.f;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int at = 128 * q + 4 * lane, left = valid - at;
-      gv[q] = load4(x.g, x.g_bf16, x.vec, e0 + at, left);
-      pv[q] = load4(x.p, x.p_bf16, x.vec, e0 + at, left);
-      if constexpr (BITS == 32) {
-        mv[q] = load4(a.m, 0, 1, s0 + at, left);
-        vv[q] = load4(a.v, 0, 1, s0 + at, left);
-      } else {  // whole words of codes: the buffer is padded to blocks
-        mc[q] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s0 + at));
-        vc[q] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s0 + at));
-      }
-    }
-    if constexpr (BITS == 8) {
-      ms = __fmul_rn(a.m_scale[s0 / kBlock], 1.f / kMLevels);
-      vs = __fmul_rn(a.v_scale[s0 / kBlock], 1.f / kVLevels);
-    }
-    float m[8], u[8];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float g4[4] = {gv[q].x, gv[q].y, gv[q].z, gv[q].w};
-      const float p4[4] = {pv[q].x, pv[q].y, pv[q].z, pv[q].w};
-      float m4[4], v4[4], out[4];
-      if constexpr (BITS == 32) {
-        m4[0] = mv[q].x; m4[1] = mv[q].y; m4[2] = mv[q].z; m4[3] = mv[q].w;
-        v4[0] = vv[q].x; v4[1] = vv[q].y; v4[2] = vv[q].z; v4[3] = vv[q].w;
+    if (valid == kBlock && x.vec) {
+      if (x.p_bf16) {
+        if (x.g_bf16) adamw_block<BITS, true, true, true>(x, a, sh, decay, e0, s0, valid);
+        else adamw_block<BITS, true, true, false>(x, a, sh, decay, e0, s0, valid);
       } else {
-        const uint32_t flip = mc[q] ^ 0x80808080u;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          m4[k] = signed_byte_float(flip, k);
-          v4[k] = byte_float(vc[q], k);
-        }
+        if (x.g_bf16) adamw_block<BITS, true, false, true>(x, a, sh, decay, e0, s0, valid);
+        else adamw_block<BITS, true, false, false>(x, a, sh, decay, e0, s0, valid);
       }
-      const int at = 128 * q + 4 * lane, left = valid - at;
-#pragma unroll
-      for (int k = 0; k < 4; k += 2) {
-        f32x2 m2, v2;
-        if constexpr (BITS == 32) {
-          m2 = pack2(m4[k], m4[k + 1]);
-          v2 = pack2(v4[k], v4[k + 1]);
-        } else {
-          m2 = mul2(mul2(pack2(m4[k], m4[k + 1]), pack2(fabsf(m4[k]), fabsf(m4[k + 1]))), set2(ms));
-          const f32x2 c2 = pack2(v4[k], v4[k + 1]), u2 = mul2(mul2(c2, c2), set2(vs));
-          v2 = mul2(u2, u2);
-        }
-        // Every product and sum is rounded by itself: the sums one by one, since the assembler fuses a
-        // sum of pairs with a product of pairs in front of it
-        const f32x2 g2 = mul2(pack2(g4[k], g4[k + 1]), set2(coef));
-        const float2 bm = unpack2(mul2(m2, set2(a.b1))), gm = unpack2(mul2(g2, set2(a.c1)));
-        const float2 bv = unpack2(mul2(v2, set2(a.b2))), gg = unpack2(mul2(mul2(g2, g2), set2(a.c2)));
-        const float2 mf = make_float2(__fadd_rn(bm.x, gm.x), __fadd_rn(bm.y, gm.y));
-        const float2 vf = make_float2(__fadd_rn(bv.x, gg.x), __fadd_rn(bv.y, gg.y));
-        const float un[2] = {__fsqrt_rn(vf.x), __fsqrt_rn(vf.y)};
-        const float2 den = unpack2(add2(mul2(pack2(un[0], un[1]), set2(rs)), set2(a.eps)));
-        const f32x2 step = mul2(mul2(pack2(mf.x, mf.y), pack2(rcp_approx(den.x), rcp_approx(den.y))), set2(-size));
-        const float2 pn = unpack2(add2(mul2(pack2(p4[k], p4[k + 1]), set2(decay)), step));
-        out[k] = pn.x;
-        out[k + 1] = pn.y;
-        const int e = 4 * q + k;
-        m[e] = k < left ? mf.x : 0.f;
-        m[e + 1] = k + 1 < left ? mf.y : 0.f;
-        if constexpr (BITS == 32) {
-          u[e] = vf.x;
-          u[e + 1] = vf.y;
-        } else {
-          u[e] = k < left ? un[0] : 0.f;
-          u[e + 1] = k + 1 < left ? un[1] : 0.f;
-        }
-      }
-      store4(x.p, x.p_bf16, x.vec, e0 + at, left, out);
-      if (x.copy) store4(x.copy, 1, x.vec, e0 + at, left, out);
-      if constexpr (BITS == 32) {
-        store4(a.m, 0, 1, s0 + at, left, reinterpret_cast<const float(&)[4]>(m[4 * q]));
-        store4(a.v, 0, 1, s0 + at, left, reinterpret_cast<const float(&)[4]>(u[4 * q]));
-      }
-    }
-    if constexpr (BITS == 8) {
-      // magnitudes' bits compare as the magnitudes do, NaN above all
-      uint32_t mb = 0, ub = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        mb = max(mb, __float_as_uint(m[k]) & 0x7fffffffu);
-        ub = max(ub, __float_as_uint(u[k]));
-      }
-      mb = __reduce_max_sync(0xffffffffu, mb);
-      ub = __reduce_max_sync(0xffffffffu, ub & 0x7fffffffu);
-      float sm, im, sv, iv;
-      block_scale(mb, kMLevels, sm, im);
-      block_scale(ub, kVLevels, sv, iv);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int at = 128 * q + 4 * lane;
-        uint32_t wm[4], wv[4];
-#pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          float fm[2] = {32768.f, 32768.f}, fv[2] = {32768.f, 32768.f};
-          if (a.seed >= 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int64_t place = s0 + at + k + i;
-              const uint32_t h = mix32(uint32_t(place) ^ uint32_t(place >> 32) * 0x2545F491u ^ key);
-              fm[i] = __uint_as_float(__byte_perm(h, 0x4B000000u, 0x7610u)) - 8388607.5f;  // low half + 1/2
-              fv[i] = __uint_as_float(__byte_perm(h, 0x4B000000u, 0x7632u)) - 8388607.5f;
-            }
-          }
-          const int e = 4 * q + k;
-          const float2 ym2 = unpack2(mul2(pack2(fabsf(m[e]), fabsf(m[e + 1])), set2(im)));
-          const float2 yv2 = unpack2(mul2(pack2(u[e], u[e + 1]), set2(iv)));
-          float ym[2] = {ym2.x, ym2.y}, yv[2] = {yv2.x, yv2.y}, cm[2], cv[2];
-          level2(ym, fm, cm);
-          level2(yv, fv, cv);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            // whole numbers in the mantissa's low byte; after a NaN scale any
-            wm[k + i] = __float_as_uint(copysignf(fminf(cm[i], 127.f), m[e + i]) + 12582912.f);
-            wv[k + i] = __float_as_uint(fminf(yv[i] > 0.f ? fmaxf(cv[i], 1.f) : 0.f, 255.f) + 12582912.f);
-          }
-        }
-        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + s0 + at), pack_bytes(wm));
-        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + s0 + at), pack_bytes(wv));
-      }
-      if (lane == 0) {
-        a.m_scale[s0 / kBlock] = sm;
-        a.v_scale[s0 / kBlock] = sv;
-      }
+    } else {
+      adamw_block<BITS, false, false, false>(x, a, sh, decay, e0, s0, valid);
     }
   }
   if (!a.last) return;
@@ -329,9 +433,9 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
     __threadfence();
     if (atomicAdd(a.ticket, 1u) == gridDim.x - 1) {
       *a.ticket = 0u;
-      a.clock[0] = t;
-      a.clock[1] = b1t;
-      a.clock[2] = b2t;
+      a.clock[0] += 1.0;
+      a.clock[1] *= a.beta1;
+      a.clock[2] *= a.beta2;
     }
   }
 }
@@ -350,7 +454,7 @@ __global__ void __launch_bounds__(kThreads)
     float fm[4], fv[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float a = signed_byte_float(wm, k), b = byte_float(wv, k);
+      const float a = byte_bits(wm, k) - 8388736.f, b = byte_bits(wv, k) - 8388608.f;
       fm[k] = __fmul_rn(a * fabsf(a), ms);
       const float u = __fmul_rn(b * b, vs);
       fv[k] = __fmul_rn(u, u);
@@ -380,8 +484,14 @@ __global__ void __launch_bounds__(kThreads, 4) grad_norm_kernel(const __grid_con
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float sum = 0.f;
+  int at = 0;
+  int64_t end = 0;
   for (int64_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
-    const Tensor& x = tab.t[tensor_of(tab, a.n, chunk)];
+    if (chunk >= end) {
+      at = tensor_of(tab, a.n, chunk);
+      end = at + 1 < a.n ? tab.t[at + 1].chunk0 : a.chunks;
+    }
+    const Tensor& x = tab.t[at];
     const int64_t e0 = (chunk - x.chunk0) * kNormChunk, rest = x.n - e0;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     if (x.vec && rest >= kNormChunk) {  // all loads of the chunk in flight
