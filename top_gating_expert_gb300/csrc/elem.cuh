@@ -27,6 +27,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
+// the largest of three in one instruction (a NaN is left out, as in fmaxf)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Pairs of fp32 in one 64-bit register: two operations an instruction, each rounded as alone.
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pack2(float lo, float hi) {

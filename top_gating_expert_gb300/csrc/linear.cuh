@@ -72,28 +72,39 @@ int launch_linear_bf16(const LinearOperand& A, const LinearOperand& B, int rows,
 // What becomes of a tensor-core product's accumulator.
 enum ProductMode {
   kProduct,     // the linear layer's epilogue (LinearEpi)
-  kXentStats,   // logits: their largest and their sum of exponentials, 128 columns at a time
+  kXentStats,   // logits: their largest and their sum of exponentials, 128 or 256 columns at a time
   kXentGrad,    // logits: the gradient of the cross entropy to them, bf16
   kProductSum,  // added to fp32 sums; bf16 at last
 };
 // What the modes other than kProduct take beside LinearEpi's out and ldo.
 struct XentEpi {
-  // kXentStats: part[column / 128][row] = (c, s): the sum of exp(l) over the 128 columns is 2^c s, c the
-  // largest l times log2(e); hit[row] = the logit of the row's target where it lies in the columns
+  // kXentStats: part[column / w][row] = (c, s): the sum of exp(l) over w columns is 2^c s, c the
+  // largest l times log2(e), w = xent_stats_cols; hit[row] = the logit of the row's target where it lies in the columns
   float2* part = nullptr;
   int64_t ldpart = 0;
   float* hit = nullptr;
   const int64_t* target = nullptr;
-  // kXentGrad: d = 2^(l log2(e) - x) y, less z at the target's column (bits of w) - v0; z = 0: d = 0
-  const float4* row = nullptr;
-  int v0 = 0;
-  // kProductSum: v + acc_in (null: v) to acc_out, or times factor[0] (null: 1) and rounded to out where
-  // acc_out is null; 16-byte aligned rows of ldacc floats, a multiple of 8
-  const float* factor = nullptr;
+  // kXentGrad (with target): columns v0 .. of the vocabulary V; lse [rows]; the tokens' weights dloss, or null: 1,
+  // the weight that they share being scale / max(1, stats[1]) and kept out of d
+  const float *lse = nullptr, *dloss = nullptr;
+  int64_t ignore = 0;
+  float z = 0.f;
+  int v0 = 0, V = 0;
+  // kProductSum: v + acc_in (null: v) to acc_out, or times scale / max(1, stats[1]) (stats null: 1) and rounded
+  // to out where acc_out is null; 16-byte aligned rows of ldacc floats, a multiple of 8
+  // splits > 1: the reduction in that many parts, each with its own sums part[split][row][ldacc]
+  const float* stats = nullptr;
+  float scale = 1.f;
+  int splits = 1;
+  float* sums = nullptr;
   const float* acc_in = nullptr;
   float* acc_out = nullptr;
   int64_t ldacc = 0;
 };
+int xent_stats_cols(int rows, int cols);  // 128 or 256
+// Parts of the reduction of a kProductSum product of these sizes (they take that many times rows * up8(cols) floats
+// in x.sums), by the sizes alone.
+int product_sum_splits(int rows, int cols, int K);
 int launch_xent_bf16(ProductMode mode, const LinearOperand& A, const LinearOperand& B, int rows, int cols, int K,
                      const LinearEpi& e, const XentEpi& x, unsigned* status, cudaStream_t st);
 
@@ -102,6 +113,24 @@ int launch_linear_few(int bf16, const void* x, int64_t ldx, const void* W, int64
                       const LinearEpi& e, cudaStream_t st);
 
 #ifdef __CUDACC__
+// What the gradient of a token's cross entropy takes: d = 2^(l log2(e) - x) y - z [column = w]. Tokens without one:
+// z = 0, for which d is 0 whatever the logits are.
+__device__ __forceinline__ float4 xent_row(const XentEpi& x, int64_t row) {
+  const int64_t y = __ldg(x.target + row);
+  float4 r = make_float4(INFINITY, 0.f, 0.f, __int_as_float(-1));
+  if (y == x.ignore || y < 0 || y >= x.V) return r;
+  const float l = __ldg(x.lse + row), w = x.dloss ? __ldg(x.dloss + row) : 1.f;
+  if (w != 0.f) r = make_float4(l * 1.44269504088896341f, w * (1.f + 2.f * x.z * l), w, __int_as_float(int(y)));
+  return r;
+}
+__device__ __forceinline__ bool xent_bad_target(const XentEpi& x, int64_t row) {
+  const int64_t y = __ldg(x.target + row);
+  return y != x.ignore && (y < 0 || y >= x.V);
+}
+__device__ __forceinline__ float xent_factor(const XentEpi& x) {
+  return x.stats ? x.scale / fmaxf(1.f, __ldg(x.stats + 1)) : 1.f;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float v) {
   if constexpr (ACT == MOE_LIN_RELU) return v < 0.f ? 0.f : v;  // NaN stays NaN

@@ -157,7 +157,7 @@ __device__ __forceinline__ void emit_rows(const LinearEpi& e, int r, int step, i
 // The other modes' epilogue of one output row: NC columns a lane, from column c0 on, nc of them there.
 template <int MODE, int NC, bool VEC>
 __device__ __forceinline__ void emit_row_mode(const LinearEpi& e, const XentEpi& x, int64_t row, int64_t c0, int nc,
-                                              int lane, float (&v)[NC]) {
+                                              int lane, unsigned* status, float (&v)[NC]) {
   if constexpr (MODE == kXentStats) {
     const int64_t at = __ldg(x.target + row) - c0;
     float mx = kNegInf;
@@ -178,8 +178,9 @@ __device__ __forceinline__ void emit_row_mode(const LinearEpi& e, const XentEpi&
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     if (lane == 0) x.part[(c0 / 128) * x.ldpart + row] = make_float2(c, s);
   } else if constexpr (MODE == kXentGrad) {
-    const float4 rw = __ldg(x.row + row);
+    const float4 rw = xent_row(x, row);
     const int at = __float_as_int(rw.w) - x.v0 - int(c0);
+    if (c0 == 0 && x.v0 == 0 && lane == 0 && xent_bad_target(x, row)) atomicOr(status, kStatusDeviceData);
 #pragma unroll
     for (int q = 0; q < NC; ++q) {
       v[q] = exp2_approx(fmaf(v[q], kLog2e, -rw.x)) * rw.y;
@@ -190,7 +191,7 @@ __device__ __forceinline__ void emit_row_mode(const LinearEpi& e, const XentEpi&
   } else {  // kProductSum: the accumulators' rows are padded to whole groups of 8 columns
     const float* in = x.acc_in ? x.acc_in + row * x.ldacc + c0 : nullptr;
     float* out = x.acc_out ? x.acc_out + row * x.ldacc + c0 : nullptr;
-    const float f = x.factor && !out ? __ldg(x.factor) : 1.f;
+    const float f = out ? 1.f : xent_factor(x);
 #pragma unroll
     for (int q = 0; q < NC; ++q) {
       const int c = lane_col<VEC>(lane, q);
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(TileCfg<BN, TRANS>::THREADS, TRANS ? 3 : 1)
       for (int r = or0 + warp; r < or1; r += W) {
         float v[NC];
         get(r, v);
-        emit_row_mode<MODE, NC, VEC>(p.e, p.x, r0 + int64_t(r), c0, nc, lane, v);
+        emit_row_mode<MODE, NC, VEC>(p.e, p.x, r0 + int64_t(r), c0, nc, lane, p.status, v);
       }
     }
   };
@@ -507,7 +508,12 @@ int run_tile(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
 // in all (0.92 of the sustained rate, the tensor pipe 84 % active in a capture). The backward's
 // products at 16384 x 4096 x 1024 take 87 us each: 256 and 64 tiles fill 76 pairs to 84 %.
 constexpr int kBand = 16;
-constexpr int kPairThreads = 64 + 32 * 8;
+// The epilogues that take an exponential of every logit have 16 warps: with 8 the latencies of two warps a
+// scheduler bound them (8192 x 131072 x 256 forward 500 us with 8 warps).
+template <int MODE>
+constexpr int kEpiWarps = MODE == kXentStats || MODE == kXentGrad ? 16 : 8;
+template <int MODE>
+constexpr int kPairThreads = 64 + 32 * kEpiWarps<MODE>;
 
 template <int MODE>
 struct PairArgs {
@@ -521,12 +527,13 @@ struct PairArgs {
   ExtraEpi<MODE> x;
 };
 
-template <int BN>
+template <int MODE, int BN>
 struct PairCfg {
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_BYTES = BN / 2 * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int BOXES = 8 * 2 * 2048;  // 8 warps x 2 boxes of 32 x 32 bf16
+  // 2 boxes of 32 x 32 bf16 a warp; kXentStats: the rows' (c, s) of four warps, for two tiles
+  static constexpr int BOXES = MODE == kXentStats ? 2 * 4 * BM * 8 : kEpiWarps<MODE> * 2 * 2048;
   static constexpr int BARS = 512;
   static constexpr int STAGES = (232448 - 1024 - BOXES - BARS) / STAGE > 8 ? 8 : (232448 - 1024 - BOXES - BARS) / STAGE;
   static constexpr int SMEM = 1024 + STAGES * STAGE + BOXES + BARS;
@@ -534,11 +541,11 @@ struct PairCfg {
 };
 
 template <int MODE, int BN>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kPairThreads<MODE>, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmP,
                        const __grid_constant__ CUtensorMap tmR, const PairArgs<MODE> p) {
-  using C = PairCfg<BN>;
+  using C = PairCfg<MODE, BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -556,7 +563,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int unit = int(blockIdx.x >> 1), units = int(gridDim.x >> 1);
-  const int total = p.tiles_m * p.tiles_n;
+  // work items: tiles, and in kProductSum splits of the reduction, the tiles of a split one after another
+  const int tiles = p.tiles_m * p.tiles_n;
+  int splits = 1;
+  if constexpr (MODE == kProductSum) splits = p.x.splits;
+  const int total = tiles * splits;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -565,10 +576,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
-      mbar_init(tempty0 + 8 * a, 8 * 2);
+      mbar_init(tempty0 + 8 * a, kEpiWarps<MODE> * 2);
     }
     mbar_init(drain_bar, 1);
-    for (int b = 0; b < 16; ++b) mbar_init(res0 + 8 * b, 1);
+    // (kXentStats: four of them, for the warps of 32 rows to hand their parts over)
+    for (int b = 0; b < 16; ++b) mbar_init(res0 + 8 * b, MODE == kXentStats ? kEpiWarps<MODE> / 4 : 1);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&tmA);
@@ -585,10 +597,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
+  auto k_blocks = [&](int t, int& kb0, int& kb1) {
+    kb0 = 0;
+    kb1 = p.nkb;
+    if constexpr (MODE == kProductSum) {
+      const int s = t / tiles;
+      kb0 = int(int64_t(p.nkb) * s / splits);
+      kb1 = int(int64_t(p.nkb) * (s + 1) / splits);
+    }
+  };
   auto decode = [&](int t, int& m, int& n) {
-    const int per = kBand * p.tiles_n, band = t / per, r = t - band * per;
+    if constexpr (MODE == kProductSum) t %= tiles;
+    const int per = kBand * p.tiles_n, band = p.tiles_m <= kBand ? 0 : t / per, r = t - band * per;
     const int gm = min(kBand, p.tiles_m - band * kBand);
-    n = r / gm;
+    n = gm == kBand ? r / kBand : r / gm;
     m = band * kBand + r - n * gm;
   };
 
@@ -599,10 +621,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int t = unit; t < total && ok; t += units) {
-      int m, n;
+      int m, n, kb0, kb1;
       decode(t, m, n);
+      k_blocks(t, kb0, kb1);
       const int arow = m * 2 * BM + int(rank) * BM, brow = n * BN + int(rank) * (BN / 2);
-      for (int kb = 0; kb < p.nkb; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         ok = __all_sync(0xffffffffu, wait_bounded(empty0 + 8 * stage, phase ^ 1u, s_abort, p.status, wlimit));
         if (!ok) break;
         if (lane == 0) {
@@ -651,7 +674,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(acc * BN);
-        for (int kb = 0; kb < p.nkb; ++kb) {
+        int kb0, kb1;
+        k_blocks(t, kb0, kb1);
+        for (int kb = kb0; kb < kb1; ++kb) {
           ok = __all_sync(0xffffffffu, wait_bounded(full0 + 8 * stage, phase, s_abort, p.status, wlimit));
           if (!ok) break;
           tc_fence_after();
@@ -660,7 +685,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint64_t bd = bd0 + uint64_t(stage * (C::B_BYTES >> 4));
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-              mma_bf16_pair(d, ad + kk * astep, bd + kk * bstep, idesc, (kb | kk) != 0 ? 1u : 0u);
+              mma_bf16_pair(d, ad + kk * astep, bd + kk * bstep, idesc, (kb != kb0 || kk != 0) ? 1u : 0u);
             mma_commit_pair(empty0 + 8 * stage, uint16_t(3));
           }
           __syncwarp();
@@ -681,21 +706,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       __syncwarp();
     }
   } else {
+    constexpr int COLS = BN * 4 / kEpiWarps<MODE>;  // a warp's columns of a tile
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tempty_leader = cluster_addr(tempty0, 0);
     uint8_t* box = sBox + (warp - 2) * 4096;
     int nb = 0;  // the box of the next 32 columns
     int i = 0;
     float factor = 1.f;
-    if constexpr (MODE == kProductSum) factor = p.x.factor && !p.x.acc_out ? __ldg(p.x.factor) : 1.f;
+    if constexpr (MODE == kProductSum) factor = p.x.acc_out || splits > 1 ? 1.f : xent_factor(p.x);
     // v (this lane's row, 32 columns) into box nb and out; the box's last store has been read
-    auto write_box = [&](const CUtensorMap* map, const float (&v)[32], int col, int row) {
+    auto fill_box = [&](const float (&v)[32]) {
       uint8_t* b = box + nb * 2048;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         *reinterpret_cast<uint4*>(b + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
             make_uint4(pack_bf16x2(v[8 * c], v[8 * c + 1]), pack_bf16x2(v[8 * c + 2], v[8 * c + 3]),
                        pack_bf16x2(v[8 * c + 4], v[8 * c + 5]), pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
+    };
+    auto send_box = [&](const CUtensorMap* map, int col, int row) {
+      uint8_t* b = box + nb * 2048;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -704,6 +733,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         bulk_commit();
       }
       nb ^= 1;
+    };
+    auto write_box = [&](const CUtensorMap* map, const float (&v)[32], int col, int row) {
+      fill_box(v);
+      send_box(map, col, row);
     };
     auto put = [&](const CUtensorMap* map, const float (&v)[32], int col, int row) {
       if (lane == 0) bulk_wait_read<1>();  // the store that last used this box has read it
@@ -730,7 +763,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int m, n;
       decode(t, m, n);
       const int row0 = m * 2 * BM + int(rank) * BM + 32 * q, row = row0 + lane;
-      const int cb = half * (BN / 2);
+      const int cb = half * COLS;
       const bool rows_here = row0 < p.rows;
       const int tile_col = n * BN;
       if constexpr (MODE != kProduct) {
@@ -743,17 +776,42 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           const int64_t y = row_here ? __ldg(p.x.target + row) - tile_col : -1;
           at = y >= 0 && y < BN && tile_col + y < p.cols ? int(y) : -1;
         } else if constexpr (MODE == kXentGrad) {
-          if (row_here) rw = __ldg(p.x.row + row);
+          if (row_here) rw = xent_row(p.x, row);
+          if (tile_col + cb == 0 && p.x.v0 == 0 && row_here && xent_bad_target(p.x, row))
+            atomicOr(p.status, kStatusDeviceData);
           at = row_here ? __float_as_int(rw.w) - p.x.v0 - tile_col : -1;
         }
         const bool ok = __all_sync(0xffffffffu, wait_bounded(tfull0 + 8 * acc, use, s_abort, p.status, wlimit));
         if (!ok) break;
         tc_fence_after();
         const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
+        // Rare things are kept out of the loops over 32 registers, where they would run as 32 predicated
+        // instructions each (60 of the 176 that 32 logits took): a column that one lane wants is read from
+        // tensor memory by itself.
+        float at_target = 0.f;  // this lane's target's logit, if it is among the warp's columns
+        const bool has_target = half_here && at >= cb && at < cb + COLS;
+        if constexpr (MODE == kXentStats || MODE == kXentGrad) {
+          for (unsigned want = __ballot_sync(0xffffffffu, has_target); want; want &= want - 1) {
+            const int l = __ffs(want) - 1;
+            const float f = tmem_ld_column(tbase + __shfl_sync(0xffffffffu, at, l));
+            if (lane == l) at_target = f;
+          }
+          if constexpr (MODE == kXentStats) {
+            if (has_target) p.x.hit[row] = at_target;
+          }
+        }
 #pragma unroll 1
-        for (int c0 = cb; c0 < cb + BN / 2; c0 += 32) {
+        for (int c0 = cb; c0 < cb + COLS; c0 += 32) {
           const int col = tile_col + c0;
           if (!half_here || col >= p.cols) break;  // warp-uniform
+          if (MODE == kXentStats && col + 32 > p.cols) {  // the vocabulary's last columns one by one
+            for (int j = c0; j < c0 + p.cols - col; ++j) {
+              const float l = tmem_ld_column(tbase + j) * kLog2e, cn = fmaxf(sc, l), base = cn == kNegInf ? 0.f : cn;
+              ss = ss * exp2_approx(sc - base) + exp2_approx(l - base);
+              sc = cn;
+            }
+            break;
+          }
           uint32_t acc32[32];
           tmem_ld16(tbase + c0, *reinterpret_cast<uint32_t(*)[16]>(acc32));
           tmem_ld16(tbase + c0 + 16, *reinterpret_cast<uint32_t(*)[16]>(acc32 + 16));
@@ -761,39 +819,39 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           const float* ain = nullptr;
           float* aout = nullptr;
           if constexpr (MODE == kProductSum) {  // rows of the accumulator: whole groups of 8 columns
-            if (p.x.acc_in && row_here) ain = p.x.acc_in + row * p.x.ldacc + col;
-            if (p.x.acc_out && row_here) aout = p.x.acc_out + row * p.x.ldacc + col;
+            if (splits > 1) {
+              if (row_here) aout = p.x.sums + (int64_t(t / tiles) * p.rows + row) * p.x.ldacc + col;
+            } else {
+              if (p.x.acc_in && row_here) ain = p.x.acc_in + row * p.x.ldacc + col;
+              if (p.x.acc_out && row_here) aout = p.x.acc_out + row * p.x.ldacc + col;
+            }
             if (ain) {
 #pragma unroll
               for (int j = 0; j < 8; ++j)
                 if (col + 4 * j < p.x.ldacc) in[j] = *reinterpret_cast<const float4*>(ain + 4 * j);
             }
           }
-          tmem_ld_wait();
+          tmem_ld_wait_for(acc32);
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(acc32[j]);
           if constexpr (MODE == kXentStats) {
-            if (__any_sync(0xffffffffu, at >= c0 && at < c0 + 32)) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (c0 + j == at) p.x.hit[row] = v[j];
-            }
-            if (col + 32 > p.cols) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (col + j >= p.cols) v[j] = kNegInf;
-            }
             float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-            for (int j = 4; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
-            const float cn = fmaxf(sc, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e);
+            for (int j = 4; j < 28; j += 8) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], v[j + i], v[j + 4 + i]);
+            }
+            const float hi = max3(max3(mx[0], mx[1], v[28]), max3(mx[2], mx[3], v[29]), fmaxf(v[30], v[31]));
+            const float cn = fmaxf(sc, hi * kLog2e);
             const float base = cn == kNegInf ? 0.f : cn;
             const f32x2 nb2 = set2(-base), l2 = set2(kLog2e);
             f32x2 sum[2] = {pack2(ss * exp2_approx(sc - base), 0.f), set2(0.f)};
 #pragma unroll
-            for (int j = 0; j < 32; j += 2)
-              sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], exp2_2(fma2(pack2(v[j], v[j + 1]), l2, nb2)));
+            for (int j = 0; j < 32; j += 2) {
+              const f32x2 x = fma2(pack2(v[j], v[j + 1]), l2, nb2);
+              sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], exp2_2(x));
+            }
             const float2 f = unpack2(add2(sum[0], sum[1]));
             ss = f.x + f.y;
             sc = cn;
@@ -801,21 +859,27 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const f32x2 nb2 = set2(-rw.x), l2 = set2(kLog2e), cp = set2(rw.y);
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
-              const float2 f = unpack2(mul2(exp2_2(fma2(pack2(v[j], v[j + 1]), l2, nb2)), cp));
+              const f32x2 x = fma2(pack2(v[j], v[j + 1]), l2, nb2);
+              const float2 f = unpack2(mul2(exp2_2(x), cp));
               v[j] = f.x;
               v[j + 1] = f.y;
             }
-            if (__any_sync(0xffffffffu, at >= c0 && at < c0 + 32)) {
+            // into the box, and there the lane's own: a row without a gradient (0, whatever its logits are), the
+            // target's entry
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
+            fill_box(v);
+            uint8_t* r = box + nb * 2048 + lane * 64;
+            if (rw.z == 0.f) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (c0 + j == at) v[j] -= rw.z;
+              for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(r + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+            } else if (has_target && at >= c0 && at < c0 + 32) {
+              const int j = at - c0;
+              const float d = fmaf(exp2_approx(fmaf(at_target, kLog2e, -rw.x)), rw.y, -rw.z);
+              *reinterpret_cast<__nv_bfloat16*>(r + (((j >> 3) ^ ((lane >> 1) & 3)) << 4) + (j & 7) * 2) =
+                  __float2bfloat16_rn(d);
             }
-            if (__any_sync(0xffffffffu, rw.z == 0.f)) {  // no gradient, whatever the logits are
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (rw.z == 0.f) v[j] = 0.f;
-            }
-            put(&tmY, v, col, row0);
+            send_box(&tmY, col, row0);
           } else {
             if (ain) {
 #pragma unroll
@@ -826,7 +890,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= factor;
-            if (p.x.acc_out) {
+            if (p.x.acc_out || splits > 1) {
               if (aout) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -858,8 +922,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         }
         if constexpr (MODE == kXentStats) {
-          if (half_here && row_here)
-            p.x.part[int64_t((tile_col + cb) / 128) * p.x.ldpart + row] = make_float2(sc, ss);
+          // the warps of these rows hand their columns' (c, s) to the first of them, which joins them. A buffer is
+          // used again two tiles on: its accumulator is free only when that warp has arrived below.
+          float2* join = reinterpret_cast<float2*>(sBox) + (i & 1) * 4 * BM;
+          const uint32_t bar = res0 + 8 * uint32_t(q);
+          join[half * BM + 32 * q + lane] = make_float2(sc, ss);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
+          if (half == 0) {
+            const bool all =
+                __all_sync(0xffffffffu, wait_bounded(bar, uint32_t(i) & 1u, s_abort, p.status, wlimit));
+            if (!all) break;
+            float2 o[3];
+#pragma unroll
+            for (int h = 0; h < 3; ++h) o[h] = join[(h + 1) * BM + 32 * q + lane];
+            const float cn = max3(max3(sc, o[0].x, o[1].x), o[2].x, kNegInf), base = cn == kNegInf ? 0.f : cn;
+            ss *= exp2_approx(sc - base);
+#pragma unroll
+            for (int h = 0; h < 3; ++h) ss = fmaf(o[h].y, exp2_approx(o[h].x - base), ss);
+            if (row_here) p.x.part[int64_t(n) * p.x.ldpart + row] = make_float2(cn, ss);
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -874,7 +956,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
       bool landed = true;
 #pragma unroll 1
-      for (int c0 = cb; c0 < cb + BN / 2; c0 += 32) {
+      for (int c0 = cb; c0 < cb + COLS; c0 += 32) {
         const int col = tile_col + c0;
         if (!rows_here || col >= p.cols) break;  // warp-uniform: nothing of this part exists
         uint32_t acc32[32];
@@ -894,7 +976,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             rv[c] = *reinterpret_cast<const uint4*>(box + nb * 2048 + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
-          if (c0 + 32 < cb + BN / 2 && col + 32 < p.cols) fetch_res(nb ^ 1, col + 32, row0);
+          if (c0 + 32 < cb + COLS && col + 32 < p.cols) fetch_res(nb ^ 1, col + 32, row0);
         } else if (rvec) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) rv[c] = *reinterpret_cast<const uint4*>(rp + col + 8 * c);
@@ -1001,7 +1083,7 @@ bool out_aligned(const void* p, int64_t ld) {
 template <int MODE, int BN>
 int run_pair(const LinearOperand& A, const LinearOperand& B, int rows, int cols, int K, const LinearEpi& e,
              const ExtraEpi<MODE>& x, unsigned* status, cudaStream_t st) {
-  using C = PairCfg<BN>;
+  using C = PairCfg<MODE, BN>;
   CUtensorMap ta, tb, ty, tp, tr;
   int rc;
   if ((rc = map_operand(&ta, A, rows, K, BM)) != MOE_OK) return rc;
@@ -1032,7 +1114,7 @@ int run_pair(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
   static std::atomic<unsigned long long> seen{0};
   if ((rc = allow_smem(reinterpret_cast<const void*>(kern), C::SMEM, seen)) != MOE_OK) return rc;
   cudaLaunchConfig_t lc = {};
-  lc.blockDim = dim3(kPairThreads);
+  lc.blockDim = dim3(kPairThreads<MODE>);
   lc.dynamicSmemBytes = C::SMEM;
   lc.stream = st;
   cudaLaunchAttribute attr[2];
@@ -1050,7 +1132,9 @@ int run_pair(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
       clusters = num_sms() / 2;
     resident.store(clusters, std::memory_order_relaxed);
   }
-  lc.gridDim = dim3(unsigned(2 * std::min(clusters, p.tiles_m * p.tiles_n)));
+  int items = p.tiles_m * p.tiles_n;
+  if constexpr (MODE == kProductSum) items *= x.splits;
+  lc.gridDim = dim3(unsigned(2 * std::min(clusters, items)));
   if (pdl_enabled()) {
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -1071,21 +1155,29 @@ int pick_splits(int64_t tiles, int K) {
   return s;
 }
 
+// Whether a product takes CTA pairs: 256-wide tiles once they fill the SM pairs.
+bool takes_pairs(int rows, int cols, bool a_mn) {
+  if (rows <= 64 && !a_mn) return false;  // few rows: the wide side becomes the MMA's 128 rows
+  const int64_t pairs = ((int64_t(rows) + 255) / 256) * ((int64_t(cols) + 255) / 256);
+  return pairs * 2 >= num_sms() / 2 && cols >= 128;
+}
+
 // The kernel for the sizes, by the same rules in every mode.
 template <int MODE>
 int run_product(const LinearOperand& A, const LinearOperand& B, int rows, int cols, int K, const LinearEpi& e,
                 const ExtraEpi<MODE>& x, unsigned* status, cudaStream_t st) {
+  if constexpr (MODE == kProductSum) {
+    if (x.splits > 1) return run_pair<MODE, 256>(A, B, rows, cols, K, e, x, status, st);
+  }
   const int64_t wide = (int64_t(cols) + BM - 1) / BM;
-  if (rows <= 64 && !A.mn) {  // few rows: the wide side becomes the MMA's 128 rows
+  if (rows <= 64 && !A.mn) {
     const int s = pick_splits(wide, K);
     if (rows <= 16) return run_tile<MODE, 16, true>(B, A, cols, rows, K, s, e, x, status, st);
     if (rows <= 32) return run_tile<MODE, 32, true>(B, A, cols, rows, K, s, e, x, status, st);
     return run_tile<MODE, 64, true>(B, A, cols, rows, K, s, e, x, status, st);
   }
-  // 256-wide pair tiles once they fill the SM pairs; a linear layer's outputs leave by TMA stores,
-  // which need 16-byte rows
-  const int64_t pairs = ((int64_t(rows) + 255) / 256) * ((int64_t(cols) + 255) / 256);
-  if (pairs * 2 >= num_sms() / 2 && cols >= 128 &&
+  // (a linear layer's outputs leave by TMA stores, which need 16-byte rows)
+  if (takes_pairs(rows, cols, A.mn) &&
       (MODE != kProduct || (out_aligned(e.out, e.ldo) && out_aligned(e.pre, e.ldp))))
     return run_pair<MODE, 256>(A, B, rows, cols, K, e, x, status, st);
   const int64_t tiles = wide * ((int64_t(rows) + BM - 1) / BM);

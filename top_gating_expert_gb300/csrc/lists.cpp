@@ -5,6 +5,7 @@
 #include <Python.h>
 
 #include <ATen/core/TensorBody.h>
+#include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -114,6 +115,34 @@ PyObject* step(PyObject*, PyObject* args) {
   return PyBool_FromLong(moved);
 }
 
+// vectors(device, n, ..) -> float32 tensors of n elements each on the CUDA device, from the current stream's pool
+PyObject* vectors(PyObject*, PyObject* args) {
+  const Py_ssize_t n = PyTuple_GET_SIZE(args) - 1;
+  if (n < 0) return PyErr_Format(PyExc_TypeError, "vectors: a device and sizes");
+  const long dev = PyLong_AsLong(PyTuple_GET_ITEM(args, 0));
+  if (dev == -1 && PyErr_Occurred()) return nullptr;
+  const auto options = at::TensorOptions().dtype(at::kFloat).device(at::Device(at::kCUDA, c10::DeviceIndex(dev)));
+  PyObject* out = PyTuple_New(n);
+  for (Py_ssize_t i = 0; out && i < n; ++i) {
+    const long long k = PyLong_AsLongLong(PyTuple_GET_ITEM(args, i + 1));
+    PyObject* t = nullptr;
+    if (!(k == -1 && PyErr_Occurred())) {
+      try {
+        t = THPVariable_Wrap(at::empty({k}, options));
+      } catch (...) {
+        Py_DECREF(out);
+        throw;
+      }
+    }
+    if (!t) {
+      Py_CLEAR(out);
+      break;
+    }
+    PyTuple_SET_ITEM(out, i, t);
+  }
+  return out;
+}
+
 // No C++ exception (a tensor without storage throws one) leaves the module.
 template <PyObject* (*F)(PyObject*, PyObject*)>
 PyObject* guarded(PyObject* self, PyObject* args) {
@@ -129,6 +158,7 @@ PyObject* guarded(PyObject* self, PyObject* args) {
 
 PyMethodDef methods[] = {{"gradients", guarded<gradients>, METH_VARARGS, nullptr},
                          {"step", guarded<step>, METH_VARARGS, nullptr},
+                         {"vectors", guarded<vectors>, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lists", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

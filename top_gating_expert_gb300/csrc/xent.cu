@@ -5,13 +5,17 @@
 //   loss = lse - l[target] + z lse^2,   d = w ((1 + 2 z lse) exp(l - lse) - [target]),
 //   dx = d W,   dW = d^T x
 //
-// Forward, bf16: one product whose epilogue keeps of 128 columns of a row their largest logit and sum
-// of exponentials (8 bytes for 128 logits) and the target's logit; xent_join_kernel joins them.
+// Forward, bf16: one product whose epilogue keeps of 128 or 256 columns of a row their largest logit and sum
+// of exponentials (8 bytes) and the target's logit; xent_join_kernel joins them.
 // Backward, bf16: a piece of the vocabulary at a time, the logits once more, d in bf16 into the
 // workspace, then its share of dx (fp32 sums over the pieces) and the rows of dW, which are whole. Pieces of
 // about 512 MB of d: small enough for memory (the logits of 8192 tokens and 131072 entries take 4.3 GB in
 // fp32), large enough that the sums' way through memory, 8 bytes an element of dx and piece, stays below
 // 2 % of the products.
+// d of the mean loss is kept without the weight that all tokens share, which the products' results take:
+// rounding to bf16 then leaves the target's entry, near -1, almost as it is, where w (p - 1) would be off by up to
+// 2^-8, the same way in every token (8192 x 65536 x 2048: gradients 3.1e-3 off in all with w in d, now 1.7e-3,
+// their own rounding).
 // fp32: the logits of a piece go through the workspace; the plain-FMA products are by far the longest part.
 #include <math.h>
 
@@ -24,7 +28,7 @@ namespace {
 
 constexpr float kL2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 constexpr size_t kPieceBytes = size_t(512) << 20;  // of d (bf16) or logits (fp32)
-constexpr size_t kStatBytes = size_t(256) << 20;   // of the forward's 8 bytes for 128 logits: tokens at a time
+constexpr size_t kStatBytes = size_t(256) << 20;   // of the forward's 8 bytes for 128 logits or more: tokens at a time
 constexpr int kLeastPiece = 512;
 
 // The join of n (c, s) pairs of 32 tokens: each of 32 warps every 32nd pair (a lane a token), then warp w joins
@@ -49,21 +53,45 @@ __device__ __forceinline__ void join_pair(float& c, float& s, float pc, float ps
   c = cn;
 }
 
+// sums over a warp, in every lane, in the order of a fixed tree
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
 __global__ void __launch_bounds__(1024) xent_join_kernel(const JoinArgs a) {
   __shared__ float2 s_part[32][33];
-  __shared__ float2 s_tok[32];
-  __shared__ double s_sum[32], s_cnt[32];
+  __shared__ float s_loss[32];
+  __shared__ int s_one[32];
+  __shared__ double s_sum[32];
   __shared__ bool s_last;
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 32 + lane;
+  const int t = blockIdx.x * 32 + lane, row = blockIdx.x * 32 + warp;
+  // for the end: this warp's token
+  int64_t y = a.ignore;
+  float hit = 0.f;
+  if (row < a.rows) {
+    y = __ldg(a.target + row);
+    hit = __ldg(a.hit + row);  // any, without a target among the logits
+  }
   float c = -INFINITY, s = 0.f;
   if (t < a.rows) {
-#pragma unroll 4
-    for (int i = warp; i < a.n; i += 32) {
-      const float2 p = __ldg(a.part + i * a.ldpart + t);
-      join_pair(c, s, p.x, p.y);
+    float2 p[8];  // eight pairs in flight
+    for (int i0 = warp; i0 < a.n; i0 += 256) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (i0 + 32 * q < a.n) p[q] = __ldg(a.part + (i0 + 32 * q) * a.ldpart + t);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (i0 + 32 * q < a.n) join_pair(c, s, p[q].x, p[q].y);
     }
   }
   s_part[warp][lane] = make_float2(c, s);
@@ -72,20 +100,14 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const JoinArgs a) {
   float top = p.x;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  s = p.y * exp2f(p.x - (top == -INFINITY ? 0.f : top));
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  const int row = blockIdx.x * 32 + warp;
+  s = warp_sum(p.y * exp2f(p.x - (top == -INFINITY ? 0.f : top)));
   if (lane == 0) {
-    float loss = 0.f, one = 0.f;
+    float loss = 0.f;
     if (row < a.rows) {
       const float lse = (top + log2f(s)) * kLn2;
-      const int64_t y = a.target[row];
       if (y != a.ignore) {
-        one = 1.f;
-        if (y >= 0 && y < a.V) {
-          loss = lse - a.hit[row] + a.z * lse * lse;
-        } else {
+        loss = lse - hit + a.z * lse * lse;
+        if (y < 0 || y >= a.V) {
           loss = __int_as_float(0x7fc00000);
           atomicOr(a.status, kStatusDeviceData);
         }
@@ -93,74 +115,45 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const JoinArgs a) {
       a.lse[row] = lse;
       a.loss[row] = loss;
     }
-    s_tok[warp] = make_float2(loss, one);
+    s_loss[warp] = loss;
+    s_one[warp] = y != a.ignore;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float2 b = s_tok[0];
-    for (int w = 1; w < 32; ++w) {
-      b.x += s_tok[w].x;
-      b.y += s_tok[w].y;
+  if (warp == 0) {
+    const float sum = warp_sum(s_loss[lane]);
+    const int cnt = __popc(__ballot_sync(0xffffffffu, s_one[lane] != 0));
+    if (lane == 0) {
+      a.sums[a.first + blockIdx.x] = make_float2(sum, float(cnt));
+      __threadfence();
+      s_last = atomicAdd(a.status + 1, 1u) == a.ctas - 1;
     }
-    a.sums[a.first + blockIdx.x] = b;
-    __threadfence();
-    s_last = atomicAdd(a.status + 1, 1u) == a.ctas - 1;
   }
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  double sum = 0.0, cnt = 0.0;
+  double sum = 0.0;
+  int cnt = 0;
   for (unsigned i = threadIdx.x; i < a.ctas; i += 1024) {
     const float2 b = __ldcg(a.sums + i);
     sum += double(b.x);
-    cnt += double(b.y);
+    cnt += int(b.y);
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    cnt += __shfl_xor_sync(0xffffffffu, cnt, off);
-  }
+  sum = warp_sum(sum);
+  cnt = __reduce_add_sync(0xffffffffu, cnt);
   if (lane == 0) {
     s_sum[warp] = sum;
-    s_cnt[warp] = cnt;
+    s_one[warp] = cnt;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    sum = cnt = 0.0;
-    for (int w = 0; w < 32; ++w) {
-      sum += s_sum[w];
-      cnt += s_cnt[w];
+  if (warp == 0) {
+    sum = warp_sum(s_sum[lane]);
+    cnt = __reduce_add_sync(0xffffffffu, s_one[lane]);
+    if (lane == 0) {
+      a.stats[0] = cnt > 0 ? float(sum) / float(cnt) : 0.f;
+      a.stats[1] = float(cnt);
+      a.status[1] = 0u;  // the ticket
     }
-    a.stats[0] = cnt > 0.0 ? float(sum / cnt) : 0.f;
-    a.stats[1] = float(cnt);
-    a.status[1] = 0u;  // the ticket
   }
-}
-
-// What the backward's epilogue needs of a token: d = 2^(l log2(e) - x) y - z [column = w]. Tokens
-// without a gradient: z = 0, for which d is 0. With factor, the weight that all tokens share is kept out of
-// d (z = 1) and written there, for the products' results: d's rounding to bf16 then leaves the target's
-// entry, near -1, almost as it is, where w (p - 1) would be off by up to 2^-8, the same way in every
-// token (8192 x 65536 x 2048: gradients 3.1e-3 off in all with w in d, 1.7e-3 of it their own rounding).
-__global__ void __launch_bounds__(256)
-    xent_rows_kernel(const int64_t* __restrict__ target, const float* __restrict__ lse, const float* __restrict__ dloss,
-                     const float* __restrict__ stats, float scale, float z, int64_t ignore, int V, int T,
-                     float4* __restrict__ row, float* factor, unsigned* status) {
-  pdl_wait();
-  pdl_trigger();
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t >= T) return;
-  const float all = dloss ? 1.f : scale / fmaxf(1.f, __ldg(stats + 1));
-  if (factor && t == 0) *factor = all;
-  const int64_t y = target[t];
-  const bool in = y >= 0 && y < V;
-  float4 r = make_float4(INFINITY, 0.f, 0.f, __int_as_float(-1));
-  if (y != ignore && !in) atomicOr(status, kStatusDeviceData);
-  if (y != ignore && in) {
-    const float l = lse[t], w = dloss ? dloss[t] : (factor ? 1.f : all);
-    if (w != 0.f) r = make_float4(l * kL2e, w * (1.f + 2.f * z * l), w, __int_as_float(int(y)));
-  }
-  row[t] = r;
 }
 
 // fp32 logits of a piece [rows, cols] (row stride ld): the row's (c, s) and its target's logit.
@@ -206,15 +199,20 @@ __global__ void __launch_bounds__(256)
 
 // d in place of the fp32 logits of a piece.
 __global__ void __launch_bounds__(256)
-    xent_grad_f32_kernel(float* __restrict__ l, int64_t ld, int cols, const float4* __restrict__ rows, int v0) {
+    xent_grad_f32_kernel(float* __restrict__ l, int64_t ld, int cols, const XentEpi x, unsigned* status) {
   pdl_wait();
   pdl_trigger();
   const int64_t row = blockIdx.x;
-  const float4 r = __ldg(rows + row);
-  const int at = __float_as_int(r.w) - v0;
+  float4 r = xent_row(x, row);
+  const float f = xent_factor(x);
+  if (x.v0 == 0 && blockIdx.y == 0 && threadIdx.x == 0 && xent_bad_target(x, row)) atomicOr(status, kStatusDeviceData);
+  const int at = __float_as_int(r.w) - x.v0;
+  const bool on = r.z != 0.f;
+  r.y *= f;
+  r.z *= f;
   for (int i = blockIdx.y * 256 + threadIdx.x; i < cols; i += gridDim.y * 256) {
     float d = 0.f;
-    if (r.z != 0.f) {
+    if (on) {
       d = exp2f(fmaf(l[row * ld + i], kL2e, -r.x)) * r.y;
       if (i == at) d -= r.z;
     }
@@ -252,14 +250,16 @@ int forward_rows(const moe_xent_t& p) {
   return int(std::min<int64_t>(std::max(1, p.T), most));
 }
 
+// parts of the reduction of dx over a piece (the last piece may be shorter: the same parts, if it has as many k-blocks)
+int dx_splits(const moe_xent_t& p) { return p.T ? product_sum_splits(p.T, p.K, p.piece) : 1; }
+
 // Regions behind the operands' copies; the forward's and the backward's share their room.
 struct Regions {
   float2 *part = nullptr, *sums = nullptr;
   float* hit = nullptr;
-  float4* row = nullptr;
   void* d = nullptr;  // [T][up8(piece)]: bf16 d, or fp32 logits
   float* acc = nullptr;
-  float* factor = nullptr;
+  float* split = nullptr;
   float* prod = nullptr;  // the fp32 products' partial sums
 };
 void carve(const moe_xent_t& p, bool backward, Carver& c, Regions* r) {
@@ -272,9 +272,9 @@ void carve(const moe_xent_t& p, bool backward, Carver& c, Regions* r) {
     r->hit = static_cast<float*>(c.take(size_t(forward_rows(p)) * 4));
     r->sums = static_cast<float2*>(c.take((T + 31) / 32 * 8 + size_t((p.T + forward_rows(p) - 1) / forward_rows(p)) * 8));
   } else {
-    r->row = static_cast<float4*>(c.take(T * 16));
-    if (!f32) r->factor = static_cast<float*>(c.take(4));
     if (!f32 && pieces(p) > 1) r->acc = static_cast<float*>(c.take(T * up8(p.K) * 4));
+    const int n = f32 ? 1 : dx_splits(p);
+    if (n > 1) r->split = static_cast<float*>(c.take(n * T * up8(p.K) * 4));
   }
 }
 
@@ -365,7 +365,8 @@ int forward(const moe_xent_t& p, const void* x, const void* W, const int64_t* ta
         return rc;
     }
     JoinArgs j;
-    j.part = r.part; j.ldpart = step; j.n = slots(p); j.rows = rows; j.V = p.V;
+    const int w = f32 ? p.piece : xent_stats_cols(rows, p.V);
+    j.part = r.part; j.ldpart = step; j.n = (p.V + w - 1) / w; j.rows = rows; j.V = p.V;
     j.hit = r.hit; j.target = target + t0; j.ignore = p.ignore_index; j.z = p.z_coef;
     j.loss = loss + t0; j.lse = lse + t0; j.stats = stats;
     j.sums = r.sums; j.first = first; j.ctas = ctas;
@@ -394,22 +395,22 @@ int backward(const moe_xent_t& p, const void* x, const void* W, const int64_t* t
   if ((rc = operands(p, x, W, c, ws_bytes, &a, &b, st)) != MOE_OK) return rc;
   carve(p, true, c, &r);
   unsigned* status = static_cast<unsigned*>(ws);
-  if ((rc = launch_kernel(xent_rows_kernel, dim3(unsigned((p.T + 255) / 256)), dim3(256), 0, st, target, lse, dloss,
-                          stats, scale, p.z_coef, p.ignore_index, p.V, p.T, r.row, dloss ? nullptr : r.factor,
-                          status)) != MOE_OK)
-    return rc;
   const int64_t ldd = up8(p.piece);
   const bool f32 = p.dtype == MOE_F32;
-  const float* factor = dloss ? nullptr : r.factor;
+  XentEpi g;  // what all pieces share
+  g.target = target; g.lse = lse; g.dloss = dloss; g.ignore = p.ignore_index; g.z = p.z_coef; g.V = p.V;
+  g.stats = dloss ? nullptr : stats;
+  g.scale = scale;
   for (int v0 = 0; v0 < p.V; v0 += p.piece) {
     const int nv = std::min(p.piece, p.V - v0);
     const bool first = v0 == 0, last = v0 + nv == p.V;
+    g.v0 = v0;
     if (f32) {
       if ((rc = logits_f32(p, a, b, v0, nv, r, st)) != MOE_OK) return rc;
       float* d = static_cast<float*>(r.d);
       const unsigned gy = unsigned(std::max(1, std::min(8, nv / 1024)));
       if ((rc = launch_kernel(xent_grad_f32_kernel, dim3(unsigned(p.T), gy), dim3(256), 0, st, d, ldd, nv,
-                              static_cast<const float4*>(r.row), v0)) != MOE_OK)
+                              g, status)) != MOE_OK)
         return rc;
       LinearEpi e;
       if (dx) {
@@ -428,17 +429,16 @@ int backward(const moe_xent_t& p, const void* x, const void* W, const int64_t* t
       }
       continue;
     }
-    XentEpi g;
-    g.row = r.row; g.v0 = v0;
     LinearEpi e;
     e.out = r.d; e.ldo = ldd;
     LinearOperand w = rows_from(b, v0, 2), d{r.d, ldd, false}, xt = a;
     if ((rc = launch_xent_bf16(kXentGrad, a, w, p.T, nv, p.K, e, g, status, st)) != MOE_OK) return rc;
     if (dx) {  // d W: W's rows run along the reduction, so it is read MN-major
-      XentEpi s;
+      XentEpi s = g;
       LinearEpi o;
       s.ldacc = up8(p.K);
-      s.factor = factor;
+      s.splits = std::min(dx_splits(p), (nv + 63) / 64);
+      s.sums = r.split;
       if (!first) s.acc_in = r.acc;
       if (!last) s.acc_out = r.acc;
       else { o.out = dx; o.ldo = p.lddx; }
@@ -447,12 +447,10 @@ int backward(const moe_xent_t& p, const void* x, const void* W, const int64_t* t
     }
     if (dW) {  // d^T x: both operands' rows run along the reduction
       LinearEpi o;
-      XentEpi s;
-      s.factor = factor;
       o.out = static_cast<__nv_bfloat16*>(dW) + v0 * p.lddw; o.ldo = p.lddw;
       d.mn = true;
       xt.mn = true;
-      if ((rc = launch_xent_bf16(kProductSum, d, xt, nv, p.K, p.T, o, s, status, st)) != MOE_OK) return rc;
+      if ((rc = launch_xent_bf16(kProductSum, d, xt, nv, p.K, p.T, o, g, status, st)) != MOE_OK) return rc;
     }
   }
   return MOE_OK;

@@ -65,6 +65,9 @@ def linear_cross_entropy(x, W, target, *, ignore_index=-100, z_coef=0.0, loss=No
     at a time (0: chosen from the sizes)."""
     w = "linear_cross_entropy"
     T, V, K, dt, dev, ldx, ldw = _xent_checked(x, W, target, w)
+    if loss is None and lse is None and stats is None:
+        with _on(stream):
+            loss, lse, stats = _lists().vectors(dev, T, T, 2)
     if loss is None:
         loss = _new((T,), _F32, dev, stream)
     if lse is None:
