@@ -154,53 +154,84 @@ __device__ __forceinline__ void emit_rows(const LinearEpi& e, int r, int step, i
   }
 }
 
-// The other modes' epilogue of one output row: NC columns a lane, from column c0 on, nc of them there.
-template <int MODE, int NC, bool VEC>
-__device__ __forceinline__ void emit_row_mode(const LinearEpi& e, const XentEpi& x, int64_t row, int64_t c0, int nc,
-                                              int lane, unsigned* status, float (&v)[NC]) {
+// The other modes' epilogue of output rows r, r + step, .. (those below r_end, at most 32): lane k fetches what the
+// k-th row needs before the first is worked on (one after another the loads' latencies took 6 us a tile).
+template <int MODE, int NC, bool VEC, typename Get>
+__device__ __forceinline__ void emit_rows_mode(const LinearEpi& e, const XentEpi& x, int r, int step, int r_end,
+                                               int64_t row0, int64_t c0, int nc, int lane, unsigned* status, Get&& get) {
+  const bool mine = r + lane * step < r_end;
+  const int64_t my_row = row0 + r + lane * step;
+  int at_l = -1;  // the row's target's column of the tile
+  float4 rw_l = make_float4(0.f, 0.f, 0.f, 0.f);
   if constexpr (MODE == kXentStats) {
-    const int64_t at = __ldg(x.target + row) - c0;
-    float mx = kNegInf;
-#pragma unroll
-    for (int q = 0; q < NC; ++q) {
-      const int c = lane_col<VEC>(lane, q);
-      if (c == at && c < nc) x.hit[row] = v[q];
-      if (c >= nc) v[q] = kNegInf;
-      mx = fmaxf(mx, v[q]);
+    if (mine) {
+      const int64_t y = __ldg(x.target + my_row) - c0;
+      at_l = y >= 0 && y < nc ? int(y) : -1;
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    const float c = mx * kLog2e, base = c == kNegInf ? 0.f : c;
-    float s = 0.f;
-#pragma unroll
-    for (int q = 0; q < NC; ++q) s += exp2_approx(fmaf(v[q], kLog2e, -base));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    if (lane == 0) x.part[(c0 / 128) * x.ldpart + row] = make_float2(c, s);
   } else if constexpr (MODE == kXentGrad) {
-    const float4 rw = xent_row(x, row);
-    const int at = __float_as_int(rw.w) - x.v0 - int(c0);
-    if (c0 == 0 && x.v0 == 0 && lane == 0 && xent_bad_target(x, row)) atomicOr(status, kStatusDeviceData);
-#pragma unroll
-    for (int q = 0; q < NC; ++q) {
-      v[q] = exp2_approx(fmaf(v[q], kLog2e, -rw.x)) * rw.y;
-      if (rw.z == 0.f) v[q] = 0.f;  // no gradient, whatever the logits are
-      else if (lane_col<VEC>(lane, q) == at) v[q] -= rw.z;
+    if (mine) {
+      rw_l = xent_row(x, my_row);
+      at_l = __float_as_int(rw_l.w) - x.v0 - int(c0);
+      if (c0 == 0 && x.v0 == 0 && xent_bad_target(x, my_row)) atomicOr(status, kStatusDeviceData);
     }
-    store_row<NC, VEC>(e.out, row * e.ldo + c0, v, lane, nc);
-  } else {  // kProductSum: the accumulators' rows are padded to whole groups of 8 columns
-    const float* in = x.acc_in ? x.acc_in + row * x.ldacc + c0 : nullptr;
-    float* out = x.acc_out ? x.acc_out + row * x.ldacc + c0 : nullptr;
-    const float f = out ? 1.f : xent_factor(x);
+  }
+  const float factor = MODE == kProductSum && !x.acc_out ? xent_factor(x) : 1.f;
+  __syncwarp();
+#pragma unroll 4
+  for (int k = 0; k < 32; ++k) {
+    if (r + k * step >= r_end) break;
+    const int64_t row = row0 + r + k * step;
+    float v[NC];
+    float add[NC];
+    if constexpr (MODE == kProductSum) {  // the accumulators' rows are padded to whole groups of 8 columns
 #pragma unroll
-    for (int q = 0; q < NC; ++q) {
-      const int c = lane_col<VEC>(lane, q);
-      if (c >= nc) continue;
-      if (in) v[q] += in[c];
-      if (out) out[c] = v[q];
-      v[q] *= f;
+      for (int q = 0; q < NC; ++q) {
+        const int c = lane_col<VEC>(lane, q);
+        add[q] = x.acc_in && c < nc ? x.acc_in[row * x.ldacc + c0 + c] : 0.f;
+      }
     }
-    if (!out) store_row<NC, VEC>(e.out, row * e.ldo + c0, v, lane, nc);
+    get(r + k * step, v);
+    if constexpr (MODE == kXentStats) {
+      const int at = __shfl_sync(0xffffffffu, at_l, k);
+      float mx = kNegInf;
+#pragma unroll
+      for (int q = 0; q < NC; ++q) {
+        const int c = lane_col<VEC>(lane, q);
+        if (c == at) x.hit[row] = v[q];
+        if (c >= nc) v[q] = kNegInf;
+        mx = fmaxf(mx, v[q]);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      const float c = mx * kLog2e, base = c == kNegInf ? 0.f : c;
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < NC; ++q) s += exp2_approx(fmaf(v[q], kLog2e, -base));
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      if (lane == 0) x.part[(c0 / 128) * x.ldpart + row] = make_float2(c, s);
+    } else if constexpr (MODE == kXentGrad) {
+      const int at = __shfl_sync(0xffffffffu, at_l, k);
+      const float lse2 = __shfl_sync(0xffffffffu, rw_l.x, k), cp = __shfl_sync(0xffffffffu, rw_l.y, k),
+                  w = __shfl_sync(0xffffffffu, rw_l.z, k);
+#pragma unroll
+      for (int q = 0; q < NC; ++q) {
+        v[q] = exp2_approx(fmaf(v[q], kLog2e, -lse2)) * cp;
+        if (w == 0.f) v[q] = 0.f;  // no gradient, whatever the logits are
+        else if (lane_col<VEC>(lane, q) == at) v[q] -= w;
+      }
+      store_row<NC, VEC>(e.out, row * e.ldo + c0, v, lane, nc);
+    } else {
+      float* out = x.acc_out ? x.acc_out + row * x.ldacc + c0 : nullptr;
+#pragma unroll
+      for (int q = 0; q < NC; ++q) {
+        const int c = lane_col<VEC>(lane, q);
+        v[q] += add[q];
+        if (out && c < nc) out[c] = v[q];
+        v[q] *= factor;
+      }
+      if (!out) store_row<NC, VEC>(e.out, row * e.ldo + c0, v, lane, nc);
+    }
   }
 }
 
@@ -413,11 +444,8 @@ __global__ void __launch_bounds__(TileCfg<BN, TRANS>::THREADS, TRANS ? 3 : 1)
       for (int r = or0 + warp; r < or1; r += ROWS * W)
         emit_rows<NC, ROWS, VEC>(p.e, r, W, or1, r0, c0, nc, lane, bias, get);
     } else {
-      for (int r = or0 + warp; r < or1; r += W) {
-        float v[NC];
-        get(r, v);
-        emit_row_mode<MODE, NC, VEC>(p.e, p.x, r0 + int64_t(r), c0, nc, lane, p.status, v);
-      }
+      static_assert(OR <= 32 * W, "a lane a row");
+      emit_rows_mode<MODE, NC, VEC>(p.e, p.x, or0 + warp, W, or1, r0, c0, nc, lane, p.status, get);
     }
   };
   if (p.vec) run(std::true_type{});

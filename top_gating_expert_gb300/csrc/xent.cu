@@ -122,7 +122,11 @@ __global__ void __launch_bounds__(1024) xent_join_kernel(const JoinArgs a) {
   if (warp == 0) {
     const float sum = warp_sum(s_loss[lane]);
     const int cnt = __popc(__ballot_sync(0xffffffffu, s_one[lane] != 0));
-    if (lane == 0) {
+    if (lane == 0 && a.ctas == 1) {
+      a.stats[0] = cnt > 0 ? sum / float(cnt) : 0.f;
+      a.stats[1] = float(cnt);
+      s_last = false;
+    } else if (lane == 0) {
       a.sums[a.first + blockIdx.x] = make_float2(sum, float(cnt));
       __threadfence();
       s_last = atomicAdd(a.status + 1, 1u) == a.ctas - 1;

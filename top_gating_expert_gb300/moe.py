@@ -7,6 +7,7 @@ compute function does, and raises if the library is missing.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 from functools import lru_cache
@@ -168,22 +169,29 @@ class RouteOutputs:
 
 
 # ------------------------------------------------------------------ weight packing
-def pack_weights(cfg, W_in, W_up, W_out, stream=None):
-    """Returns (W_in_packed, W_out_packed) in the layout the expert GEMMs stream."""
+def _packed(sizes, W, out):
+    """Buffers of the packed sizes in W's type, or those of an earlier call (out)."""
+    if out is None:
+        return tuple(torch.empty(n, dtype=W.dtype, device=W.device) for n in sizes)
+    for t, n in zip(out, sizes):
+        if t.numel() != n or t.dtype is not W.dtype or t.get_device() != W.get_device() or not t.is_contiguous():
+            raise ValueError("out must be the packed buffers of the same configuration")
+    return out
+
+
+def pack_weights(cfg, W_in, W_up, W_out, stream=None, out=None):
+    """Returns (W_in_packed, W_out_packed) in the layout the expert GEMMs stream; out: such a pair
+    to be written again."""
     c = _cfg(cfg)
-    n_in, n_out, _, _ = packed_sizes(c)
-    p_in = torch.empty(n_in, dtype=W_in.dtype, device=W_in.device)
-    p_out = torch.empty(n_out, dtype=W_in.dtype, device=W_in.device)
+    p_in, p_out = _packed(packed_sizes(c)[:2], W_in, out)
     _launch("moe_pack_weights", W_in, stream, ctypes.byref(c), _ptr(W_in), _ptr(W_up), _ptr(W_out),
             _ptr(p_in), _ptr(p_out))
     return p_in, p_out
 
 
-def pack_shared_weights(cfg, Ws_in, Ws_up, Ws_out, stream=None):
+def pack_shared_weights(cfg, Ws_in, Ws_up, Ws_out, stream=None, out=None):
     c = _cfg(cfg)
-    _, _, n_in, n_out = packed_sizes(c)
-    p_in = torch.empty(n_in, dtype=Ws_in.dtype, device=Ws_in.device)
-    p_out = torch.empty(n_out, dtype=Ws_in.dtype, device=Ws_in.device)
+    p_in, p_out = _packed(packed_sizes(c)[2:], Ws_in, out)
     _launch("moe_pack_shared_weights", Ws_in, stream, ctypes.byref(c), _ptr(Ws_in), _ptr(Ws_up),
             _ptr(Ws_out), _ptr(p_in), _ptr(p_out))
     return p_in, p_out
@@ -330,22 +338,18 @@ def layer_forward_scored(cfg, score, x, W_g, bias, select_bias, W_in_packed, W_o
             _ptr(residual), _ptr(y), _ptr(logits_out), ctypes.byref(s), _ptr(ws), ws.numel())
 
 
-def pack_weights_backward(cfg, W_in, W_up, W_out, stream=None):
+def pack_weights_backward(cfg, W_in, W_up, W_out, stream=None, out=None):
     """Transposed packs for the backward's data-gradient GEMMs: (Wt_in_packed, Wt_out_packed)."""
     c = _cfg(cfg)
-    n_in, n_out, _, _ = packed_sizes(c)
-    p_in = torch.empty(n_in, dtype=W_in.dtype, device=W_in.device)
-    p_out = torch.empty(n_out, dtype=W_in.dtype, device=W_in.device)
+    p_in, p_out = _packed(packed_sizes(c)[:2], W_in, out)
     _launch("moe_pack_weights_backward", W_in, stream, ctypes.byref(c), _ptr(W_in), _ptr(W_up),
             _ptr(W_out), _ptr(p_in), _ptr(p_out))
     return p_in, p_out
 
 
-def pack_shared_weights_backward(cfg, Ws_in, Ws_up, Ws_out, stream=None):
+def pack_shared_weights_backward(cfg, Ws_in, Ws_up, Ws_out, stream=None, out=None):
     c = _cfg(cfg)
-    _, _, n_in, n_out = packed_sizes(c)
-    p_in = torch.empty(n_in, dtype=Ws_in.dtype, device=Ws_in.device)
-    p_out = torch.empty(n_out, dtype=Ws_in.dtype, device=Ws_in.device)
+    p_in, p_out = _packed(packed_sizes(c)[2:], Ws_in, out)
     _launch("moe_pack_shared_weights_backward", Ws_in, stream, ctypes.byref(c), _ptr(Ws_in),
             _ptr(Ws_up), _ptr(Ws_out), _ptr(p_in), _ptr(p_out))
     return p_in, p_out
@@ -483,6 +487,48 @@ class MoeLayer:
                 self.cfg, to(weights["Ws_in"]), to(weights.get("Ws_up")), to(weights["Ws_out"]))
         self.ws_bwd = workspace(self.cfg, N.MOE_WS_BACKWARD, self.device)
         self.grads = Grads(self.cfg, self.device, bias=self.bias is not None)
+
+    def set_weights(self, weights: dict, stream=None):
+        """Takes new values of the weights (the dict of __init__, contiguous tensors of the element type on
+        the layer's device; the bias and select_bias float32) into the buffers that the layer holds, the
+        backward's too once it is enabled, so that captured forwards go on with them. (W_g and the biases
+        are held as __init__ was given them, where type and device allow it.)"""
+        c = self.cfg
+        dt, dev = torch_dtype(c), self.W_g.get_device()
+        sw, Hs = c.act == N.MOE_ACT_SWIGLU, c.H_shared
+        want = dict(W_g=(c.E, c.M), W_in=(c.E, c.H, c.M), W_out=(c.E, c.M, c.H))
+        if sw:
+            want["W_up"] = want["W_in"]
+        if c.n_shared > 0:
+            want.update(Ws_in=(c.n_shared, Hs, c.M), Ws_out=(c.n_shared, c.M, Hs))
+            if sw:
+                want["Ws_up"] = want["Ws_in"]
+        vectors = dict(bias=self.bias, select_bias=self.select_bias)
+        for name, shape in want.items():
+            t = weights.get(name)
+            if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dt or t.get_device() != dev \
+                    or not t.is_contiguous() or t.data_ptr() % 16:
+                raise ValueError(f"set_weights: {name} must be a contiguous {dt} tensor of shape {shape} on the "
+                                 f"layer's device, from a 16-byte boundary on")
+        for name, held in vectors.items():
+            if held is not None:
+                _check_f32(weights.get(name), name, held.shape, "set_weights")
+        get = weights.get
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            self.W_g.copy_(weights["W_g"])
+            for name, held in vectors.items():
+                if held is not None:
+                    held.copy_(weights[name])
+        pack_weights(c, weights["W_in"], get("W_up"), weights["W_out"], stream, (self.W_in_packed, self.W_out_packed))
+        if c.n_shared > 0:
+            pack_shared_weights(c, weights["Ws_in"], get("Ws_up"), weights["Ws_out"], stream,
+                                (self.Ws_in_packed, self.Ws_out_packed))
+        if hasattr(self, "grads"):
+            pack_weights_backward(c, weights["W_in"], get("W_up"), weights["W_out"], stream,
+                                  (self.Wt_in_packed, self.Wt_out_packed))
+            if c.n_shared > 0:
+                pack_shared_weights_backward(c, weights["Ws_in"], get("Ws_up"), weights["Ws_out"], stream,
+                                             (self.Wst_in_packed, self.Wst_out_packed))
 
     def backward(self, x, dy, residual=False, aux_coef=0.0, z_coef=0.0, stream=None):
         """Gradients of sum(dy * y) + aux_coef * aux + z_coef * z for the last forward on x

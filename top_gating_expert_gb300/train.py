@@ -3,7 +3,8 @@ the optimiser.
 
 ``linear_cross_entropy`` and its backward are the C ABI's moe_xent_* on torch tensors (logits over a
 large vocabulary that are never stored), ``grad_norm`` is moe_grad_norm and ``AdamW`` holds the
-moments of a list of parameters and updates all of them in one launch (moe_adamw_*). Matrices, types,
+moments of a list of parameters and updates all of them in one launch (moe_adamw_*). ``TrainStep`` runs
+them around a stack of blocks: one training step of a model made of this package. Matrices, types,
 strides and streams as in `block`.
 """
 
@@ -16,6 +17,7 @@ import numpy as np
 import torch
 
 from . import _native as N
+from . import block
 from .block import _DTYPES, _F32, _device, _first, _matrix, _new, _on, _p, _scratch, _unaligned, _vector, \
     _workspace_ok
 from .moe import _check, _launch
@@ -283,3 +285,109 @@ class AdamW:
         _launch("moe_adamw_values", m, stream, self.m.data_ptr(), self.v.data_ptr(), self.m_scale.data_ptr(),
                 self.v_scale.data_ptr(), m.numel(), m.data_ptr(), v.data_ptr())
         return m, v
+
+
+# ------------------------------------------------------------------ a training step
+_MOE_MATRICES = ("W_g", "W_in", "W_up", "W_out", "Ws_in", "Ws_up", "Ws_out")
+
+
+class TrainStep:
+    """One step of training a model x -> blocks -> logits over a vocabulary: forward, the mean cross entropy
+    of the head, the blocks' backward passes, clipping and AdamW.
+
+    blocks: MoeBlock and DenseBlock objects of one number of tokens and width, weights: the dicts that each
+    was made from; head: W [V, M] in the element type. bf16 matrices have float32 master weights (made from
+    the dicts and the head), and the optimiser writes the bf16 ones beside them; float32 weights are trained
+    where they lie. Experts' weights are packed again after every step (MoeLayer.set_weights). Matrices decay,
+    norm and bias vectors do not. aux_coef, router_z: the MoE layers' balance and z-loss; z_coef: the head's.
+    The other arguments are AdamW's. `masters` holds (name, tensor) of every trained weight, in the order of
+    the optimiser's parameters."""
+
+    def __init__(self, blocks, weights, head, *, aux_coef=0.0, router_z=0.0, z_coef=0.0, ignore_index=-100,
+                 weight_decay=0.01, **adamw):
+        if len(blocks) != len(weights):
+            raise ValueError("TrainStep: a dict of weights for each block")
+        self.blocks, self.head = list(blocks), head
+        self.aux_coef, self.router_z, self.z_coef, self.ignore = aux_coef, router_z, z_coef, ignore_index
+        self.masters, copies, decay = [], [], []
+
+        def train(name, value, held=None, vector=False):
+            """Adds a weight: `held` is what the forward reads (None: a tensor of its own); returns that."""
+            if vector or held is not None and held.dtype is _F32:
+                self.masters.append((name, held)); copies.append(None)
+            else:
+                t = value if held is None else held
+                master = value.to(t.device, _F32, copy=True).contiguous()
+                low = t.dtype is torch.bfloat16
+                if low and held is None:
+                    held = master.bfloat16()
+                self.masters.append((name, master)); copies.append(held if low else None)
+                held = held if low else master
+            decay.append(0.0 if vector else weight_decay)
+            return held
+
+        self._unpacked = []  # what set_weights takes, block by block (None: a dense one)
+        for i, (b, w) in enumerate(zip(self.blocks, weights)):
+            at = lambda n: f"{i}.{n}"
+            if isinstance(b, block.DenseBlock):
+                for n, t in (("W1", b.W1), ("W2", b.W2)):
+                    train(at(n), w[n], t)
+                for n, t in (("b1", b.b1), ("b2", b.b2)):
+                    train(at(n), None, t, vector=True)
+                self._unpacked.append(None)
+            else:
+                dev, dt = b.layer.device, b.n.dtype
+                if not hasattr(b, "norm_ws"):
+                    b.enable_backward(w)
+                u = {n: train(at(n), w[n].to(dev, dt)) for n in _MOE_MATRICES if w.get(n) is not None}
+                if b.layer.bias is not None:
+                    u["bias"] = train(at("bias"), None, b.layer.bias, vector=True)
+                if b.layer.select_bias is not None:
+                    u["select_bias"] = b.layer.select_bias
+                self._unpacked.append(u)
+            for n, t in (("norm_gamma", b.gamma), ("norm_beta", b.beta)):
+                train(at(n), None, t, vector=True)
+        train("head", head, head)
+        self.opt = AdamW([t for _, t in self.masters], weight_decay=decay, copies=copies, **adamw)
+        self.norm_ws = grad_norm_workspace(head.device)
+        T, M = self.blocks[0].n.shape if self.blocks else (0, head.shape[1])
+        self.ws = linear_cross_entropy_workspace(T, head.shape[0], M, head.dtype, head.device) if self.blocks else None
+
+    def gradients(self, x, target, u=None):
+        """(stats, gradients): the head's stats (see linear_cross_entropy) and a gradient for each of `masters`.
+        u: the draws for blocks with random routing."""
+        inputs = []
+        for b in self.blocks:
+            inputs.append(x)
+            if isinstance(b, block.DenseBlock):
+                x = b.forward(x)
+            else:
+                x = b.forward(x, u if b.layer.cfg.random_routing else None)
+        _, lse, stats = linear_cross_entropy(x, self.head, target, ignore_index=self.ignore, z_coef=self.z_coef,
+                                             ws=self.ws)
+        dx, dhead = linear_cross_entropy_backward(x, self.head, target, lse, stats=stats, ignore_index=self.ignore,
+                                                  z_coef=self.z_coef, ws=self.ws)
+        found = [[dhead]]
+        for b, x in zip(reversed(self.blocks), reversed(inputs)):
+            if isinstance(b, block.DenseBlock):
+                g = b.backward(x, dx)
+                dx = g["dx"]
+                found.append([g[n] for n in ("W1", "W2", "b1", "b2", "norm_gamma", "norm_beta")])
+                continue
+            dx, dgamma, dbeta, g = b.backward(x, dx, aux_coef=self.aux_coef, z_coef=self.router_z)
+            c = b.layer.cfg
+            got = [getattr(g, "d" + n) for n in _MOE_MATRICES]
+            if c.n_shared > 1:  # the shared experts' hidden units lie side by side
+                got[-1] = got[-1].view(c.M, c.n_shared, c.H_shared).transpose(0, 1).contiguous()
+            found.append([t for t in (*got, g.dbias) if t is not None] + [dgamma, dbeta])
+        return stats, [t for part in reversed(found) for t in part]
+
+    def step(self, x, target, u=None, lr=None):
+        """One step; returns the stats of its forward (float32 [2], on the device)."""
+        stats, grads = self.gradients(x, target, u)
+        norm = None if self.opt.max_norm is None else grad_norm(grads, ws=self.norm_ws)
+        self.opt.step(grads, lr=lr, norm=norm)
+        for b, w in zip(self.blocks, self._unpacked):
+            if w is not None:
+                b.layer.set_weights(w)
+        return stats
