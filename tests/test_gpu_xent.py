@@ -299,3 +299,28 @@ def test_workspace_is_what_is_asked_for(native_lib):
         with pytest.raises(moe.MoeError):  # the longer of the two needs all of it
             train.linear_cross_entropy(x, W, y, piece=512, ws=big[:n - 256])
             train.linear_cross_entropy_backward(x, W, y, lse, stats=stats, piece=512, ws=big[:n - 256])
+
+
+@pytest.mark.parametrize("T,V,K", [(600, 5000, 4096), (100, 3000, 8192), (1, 40000, 4096)])
+def test_waits_that_run_out(native_lib, T, V, K):
+    """With a wait limit of a nanosecond both directions report a timeout and return; with the default again the
+    next calls on the same workspace give what they gave before, bit for bit."""
+    x, W, y = make(T, V, K, "bf16")
+    ws = train.linear_cross_entropy_workspace(T, V, K)
+
+    def both():
+        got = train.linear_cross_entropy(x, W, y, ws=ws)
+        return [*got, *train.linear_cross_entropy_backward(x, W, y, got[1], stats=got[2], ws=ws)]
+
+    want = both()
+    assert moe.device_status(ws) == 0
+    for _ in range(3):
+        moe.set_wait_limit(ws, 1)
+        train.linear_cross_entropy(x, W, y, ws=ws)
+        assert moe.device_status(ws) == -5
+        train.linear_cross_entropy_backward(x, W, y, want[1], stats=want[2], ws=ws)
+        assert moe.device_status(ws) == -5
+        moe.set_wait_limit(ws, 0)
+        got = both()
+        assert moe.device_status(ws) == 0
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

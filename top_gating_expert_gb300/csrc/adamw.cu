@@ -308,9 +308,10 @@ __device__ __forceinline__ void adamw_block(const Tensor& x, const StepArgs& a, 
     vt = max3_abs(vt, v[5], max3_abs(v[6], v[7], 0.f));
     const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mt));
     const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(vt));
-    float sm, im, sv, iv;
-    block_scale(mb, kMLevels, sm, im);
-    block_scale(__float_as_uint(__fsqrt_rn(__uint_as_float(vb))), kVLevels, sv, iv);
+    // one division for both: the lower lanes m's, the upper ones v's
+    float s2, i2;
+    block_scale(lane < 16 ? mb : __float_as_uint(__fsqrt_rn(__uint_as_float(vb))), lane < 16 ? kMLevels : kVLevels, s2, i2);
+    const float im = __shfl_sync(0xffffffffu, i2, 0), iv = __shfl_sync(0xffffffffu, i2, 16);
     // The thresholds of element e, times 2^16: the halves of mix32(place ^ key), plus 1/2. Of the place the bits of
     // 128 (e / 4) + e % 4 are those of the element in the lane, so the hash's first step is shared.
     const uint32_t x0 = uint32_t(s0 + 4 * lane) ^ (uint32_t(s0 >> 32) * 0x2545F491u) ^ key, x1 = x0 ^ (x0 >> 16);
@@ -377,10 +378,7 @@ __device__ __forceinline__ void adamw_block(const Tensor& x, const StepArgs& a, 
       __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + at), wm[q]);
       __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + at), wv[q]);
     }
-    if (lane == 0) {
-      a.m_scale[s0 / kBlock] = sm;
-      a.v_scale[s0 / kBlock] = sv;
-    }
+    if ((lane & 15) == 0) (lane == 0 ? a.m_scale : a.v_scale)[s0 / kBlock] = s2;
   }
 }
 
