@@ -171,6 +171,27 @@ def test_random_codes_keep_the_mean(native_lib):
         assert ((got - want).abs() <= 5 * 0.5 * gap / seeds ** 0.5 + 16 * U * want[-1]).all()
 
 
+def test_codes_at_the_top(native_lib):
+    """Blocks whose largest element has the highest threshold (65535.5 / 65536): its y may come out a rounding below
+    the highest square, and its code is then the one below 255 or 127."""
+    n, seed = 1 << 24, 17
+    rm, rv = plain._dither(dict(seed=seed), n, 1)
+    gen = generator(3)
+    for r in (rm, rv):
+        g = torch.randn(n, generator=gen, device="cuda") * 1e-2
+        at = (r > 0.99999).nonzero()[:, 0]
+        assert at.numel() > 100
+        g[at] = 0.2 + 0.1 * torch.rand(at.numel(), generator=gen, device="cuda")
+        opt = train.AdamW([torch.zeros(n, device="cuda")], bits=8, seed=seed, betas=(0.9, 0.95))
+        opt.step([g])
+        want = plain._m_codes(g * (1.0 - 0.9), rm) + plain._v_codes((g * g * (1.0 - 0.95)).sqrt(), rv)
+        for got, w in zip((opt.m, opt.m_scale, opt.v, opt.v_scale), want):
+            assert torch.equal(got, w)
+        # met for v, where one rounding below 255^2 is 2^-8 of a gap of 509, more than 2^-17 of it; one below 127^2 is
+        # 2^-10 of 253, less
+        assert r is rm or (opt.v[at] == 254).any()
+
+
 def test_hash_is_spread(native_lib):
     """The two thresholds of neighbouring elements and successive steps: mean 1/2 and no correlation
     (within 5 standard errors of 2^18 draws)."""

@@ -185,7 +185,8 @@ __device__ __forceinline__ void exact_codes(const float (&y)[2], const float (&f
 }
 // The same without the correction of k and for y off by up to y 2^-21: `margin` becomes negative where a code may be
 // another one (t not safely above 0, where k and the limit may belong to the next square, or close to the limit).
-// Not for `top`, the block's largest value, whose code is the highest: its y is next to a square always.
+// Not for `top`, the block's largest value, whose y is next to a square always, as long as r does not come within 2^-17
+// of 1: its code is then the highest (y is at most two roundings, 2^-23, below the highest square).
 __device__ __forceinline__ void near_codes(f32x2 y, const float (&f)[2], float v0, float v1, float top, float (&code)[2],
                                            float& margin) {
   const f32x2 k2 = floor_root2(y);
@@ -195,8 +196,8 @@ __device__ __forceinline__ void near_codes(f32x2 y, const float (&f)[2], float v
   code[1] = k.y;
   if (t0 > lim.x) code[0] += 1.f;
   if (t1 > lim.y) code[1] += 1.f;
-  if (v0 != top) margin = min3(margin, fmaf(yf.x, -0x1p-21f, t0), fmaf(yf.x, -0x1p-21f, fabsf(t0 - lim.x)));
-  if (v1 != top) margin = min3(margin, fmaf(yf.y, -0x1p-21f, t1), fmaf(yf.y, -0x1p-21f, fabsf(t1 - lim.y)));
+  if (v0 != top || f[0] > 65535.f) margin = min3(margin, fmaf(yf.x, -0x1p-21f, t0), fmaf(yf.x, -0x1p-21f, fabsf(t0 - lim.x)));
+  if (v1 != top || f[1] > 65535.f) margin = min3(margin, fmaf(yf.y, -0x1p-21f, t1), fmaf(yf.y, -0x1p-21f, fabsf(t1 - lim.y)));
 }
 __device__ __forceinline__ float v_code(float c, float y) {  // 0 for 0 alone, 255 at most
   return fminf(fmaxf(c, __saturatef(y * 0x1p126f)), 255.f);
@@ -530,26 +531,33 @@ __global__ void __launch_bounds__(kThreads, 4) grad_norm_kernel(const __grid_con
     sum += (s[0] + s[1]) + (s[2] + s[3]);
   }
   sum = block_sum_all<kWarps>(sum, s_red);
-  if (threadIdx.x == 0) {
-    a.part[blockIdx.x] = sum;
-    __threadfence();
-    s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
   double d = 0.0;
-  for (int i = threadIdx.x; i < int(gridDim.x); i += kThreads) d += double(__ldcg(a.part + i));
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) {
+      a.part[blockIdx.x] = sum;
+      __threadfence();
+      s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    for (int i = threadIdx.x; i < int(gridDim.x); i += kThreads) d += double(__ldcg(a.part + i));
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-  if (lane == 0) s_tot[warp] = d;
-  __syncthreads();
+    for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    if (lane == 0) s_tot[warp] = d;
+    __syncthreads();
+    d = lane < kWarps ? s_tot[lane] : 0.0;
+#pragma unroll
+    for (int off = kWarps / 2; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    if (threadIdx.x == 0) *a.ticket = 0u;
+  } else {
+    d = double(sum);
+  }
   if (threadIdx.x == 0) {
-    d = a.first ? 0.0 : *a.total;
-    for (int w = 0; w < kWarps; ++w) d += s_tot[w];
-    *a.total = d;
-    *a.ticket = 0u;
-    if (a.last) *a.out = float(sqrt(d));
+    if (!a.first) d += *a.total;
+    if (!a.last) *a.total = d;
+    // the fp32 root where the sum is in its range (the fp64 one takes microseconds)
+    else *a.out = d > 1e-30 && d < 1e30 ? __fsqrt_rn(float(d)) : float(sqrt(d));
   }
 }
 

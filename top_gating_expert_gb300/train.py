@@ -70,15 +70,12 @@ def linear_cross_entropy(x, W, target, *, ignore_index=-100, z_coef=0.0, loss=No
     if loss is None and lse is None and stats is None:
         with _on(stream):
             loss, lse, stats = _lists().vectors(dev, T, T, 2)
-    if loss is None:
-        loss = _new((T,), _F32, dev, stream)
-    if lse is None:
-        lse = _new((T,), _F32, dev, stream)
-    if stats is None:
-        stats = _new((2,), _F32, dev, stream)
-    _vector(loss, "loss", w, T, dev)
-    _vector(lse, "lse", w, T, dev)
-    _vector(stats, "stats", w, 2, dev)
+    else:
+        loss, lse, stats = (_new((n,), _F32, dev, stream) if t is None else t
+                            for t, n in ((loss, T), (lse, T), (stats, 2)))
+        _vector(loss, "loss", w, T, dev)
+        _vector(lse, "lse", w, T, dev)
+        _vector(stats, "stats", w, 2, dev)
     fields = (T, V, K, _DTYPES[dt], ldx, ldw, K, K, ignore_index, z_coef, piece)
     if ws is None:
         ws = _scratch(_xent_ws_bytes(0, _unaligned(x, W), *fields), dev, stream)
@@ -167,8 +164,10 @@ def grad_norm(grads, *, out=None, ws=None, stream=None):
         raise ValueError(f"{w}: there must be a gradient, and all of them on a CUDA device")
     tab, n = _lists().gradients(grads, dev)
     if out is None:
-        out = _new((1,), _F32, dev, stream)
-    _vector(out, "out", w, 1, dev)
+        with _on(stream):
+            out, = _lists().vectors(dev, 1)
+    else:
+        _vector(out, "out", w, 1, dev)
     if ws is None:
         ws = _scratch(_grad_norm_ws_bytes(), dev, stream)
     _workspace_ok(ws, w, dev)
