@@ -69,7 +69,7 @@ def linear_cross_entropy(x, W, target, *, ignore_index=-100, z_coef=0.0, loss=No
     T, V, K, dt, dev, ldx, ldw = _xent_checked(x, W, target, w)
     if loss is None and lse is None and stats is None:
         with _on(stream):
-            loss, lse, stats = _lists().vectors(dev, T, T, 2)
+            loss, lse, stats = _lists().outputs(dev, N.MOE_F32, 0, T, T, 2)
     else:
         loss, lse, stats = (_new((n,), _F32, dev, stream) if t is None else t
                             for t, n in ((loss, T), (lse, T), (stats, 2)))
@@ -100,6 +100,9 @@ def linear_cross_entropy_backward(x, W, target, lse, *, dloss=None, stats=None, 
         raise ValueError(f"{w}: dloss or the forward's stats must be given")
     else:
         _vector(stats, "stats", w, 2, dev)
+    if need_x and need_W and dx is None and dW is None:
+        with _on(stream):
+            dx, dW = _lists().outputs(dev, _DTYPES[dt], K, T, V)
     if need_x and dx is None:
         dx = _new((T, K), dt, dev, stream)
     if need_W and dW is None:
@@ -165,7 +168,7 @@ def grad_norm(grads, *, out=None, ws=None, stream=None):
     tab, n = _lists().gradients(grads, dev)
     if out is None:
         with _on(stream):
-            out, = _lists().vectors(dev, 1)
+            out, = _lists().outputs(dev, N.MOE_F32, 0, 1)
     else:
         _vector(out, "out", w, 1, dev)
     if ws is None:
