@@ -628,8 +628,9 @@ int moe_xent_forward(const moe_xent_t* p, const void* x, const void* W, const in
  *     dx [T, K] = d W,  dW [V, K] = d^T x                            (element type)
  * The logits are made again, a piece of the vocabulary at a time. bf16: d is rounded to bf16 for the
  * two products (the tensor cores' operand type); dx is summed over the pieces in fp32 and rounded
- * once. dx and dW may be NULL. lse (and stats) as the forward wrote them; with dloss, scale and stats
- * are not read. ws may be the forward's.
+ * once. dx and dW may be NULL; they overlap no input, nor each other. lse (and stats) as the forward wrote
+ * them; with dloss, scale and stats are not read. ws may be the forward's. A token without a gradient adds
+ * nothing to dx; its row of x does take part in dW's sums, with weight 0 (it has to be finite).
  */
 int moe_xent_backward(const moe_xent_t* p, const void* x, const void* W, const int64_t* target,
                       const float* lse, const float* dloss, const float* stats, float scale,
@@ -662,7 +663,7 @@ typedef struct {
  *   bits 32: m, v are float buffers. bits 8: m int8 and v uint8 codes in blocks of 256 elements with
  *     a float each in m_scale, v_scale (index = place / 256): m = sign(c) (c / 127)^2 m_scale, v =
  *     ((c / 255)^2 v_scale)^2. Codes are those of the nearest value (seed < 0), or of one of the two
- *     around it at random, with the value as expectation, by a hash of seed, t and place. Only v = 0
+ *     around it at random, with the value as expectation, by a hash of seed (its low 32 bits), t and place. Only v = 0
  *     has code 0. A value that is not finite makes its block's scale NaN.
  *     Blocks whose largest |m| or sqrt(v) is below 2^-100 become 0.
  *   Buffers: m, v 16-byte aligned; what lies behind a tensor's n elements up to its block's end must

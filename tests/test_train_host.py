@@ -219,5 +219,12 @@ def test_calls_reach_the_library_on_the_tensors_device(native_lib, monkeypatch):
             opt.step(bad)
     with pytest.raises(ValueError):
         opt.step(g, norm=there(1))  # no max_norm
+    held, opt.params = opt.params, [a, 5, c]  # lists that were changed behind its back
+    with pytest.raises(ValueError):
+        opt.step(g)
+    opt.params = held + [a]
+    with pytest.raises(ValueError):
+        opt.step(g + [None])
+    opt.params = held
     with pytest.raises(ValueError):
         opt.step(g, lr=there(2))

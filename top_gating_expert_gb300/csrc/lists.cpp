@@ -76,13 +76,14 @@ PyObject* gradients(PyObject*, PyObject* args) {
                        Py_ssize_t(tab.size()));
 }
 
-// step(table's address, sizes' address, gradients, parameters, copies, device) -> whether a parameter or copy has
-// another address than the table. Writes g, n and g_dtype (no gradient: n = 0).
+// step(table's address, sizes' address, their length, gradients, parameters, copies, device) -> whether a parameter or
+// copy has another address than the table. Writes g, n and g_dtype (no gradient: n = 0).
 PyObject* step(PyObject*, PyObject* args) {
   unsigned long long table, sizes;
   PyObject *grads, *params, *copies;
+  Py_ssize_t held;
   long dev;
-  if (!PyArg_ParseTuple(args, "KKOOOl", &table, &sizes, &grads, &params, &copies, &dev)) return nullptr;
+  if (!PyArg_ParseTuple(args, "KKnOOOl", &table, &sizes, &held, &grads, &params, &copies, &dev)) return nullptr;
   Items g(grads, "AdamW.step: the gradients must be a sequence"), p(params, "parameters"), c(copies, "copies");
   if (!g.seq || !p.seq || !c.seq) return nullptr;
   if (g.size() != p.size()) {
@@ -91,9 +92,12 @@ PyObject* step(PyObject*, PyObject* args) {
   }
   moe_param_t* tab = reinterpret_cast<moe_param_t*>(table);
   const int64_t* n = reinterpret_cast<const int64_t*>(sizes);
+  if (p.size() != held || c.size() != held) return PyErr_Format(PyExc_ValueError, "AdamW.step: the lists of parameters or copies are not what they were");
   bool moved = false;
   for (Py_ssize_t i = 0; i < g.size(); ++i) {
     moe_param_t& e = tab[i];
+    if (!THPVariable_Check(p[i]) || (c[i] != Py_None && !THPVariable_Check(c[i])))
+      return PyErr_Format(PyExc_ValueError, "AdamW.step: parameter or copy %zd is no tensor", i);
     moved |= address(p[i]) != e.p || (c[i] != Py_None && address(c[i]) != e.copy);
     if (g[i] == Py_None) {
       e.g = nullptr;

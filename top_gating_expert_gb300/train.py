@@ -262,7 +262,7 @@ class AdamW:
         number for this step, or a float32 CUDA tensor [1] that the device reads. norm: float32 [1], as
         grad_norm gives it; with max_norm the gradients are scaled by min(1, max_norm / (norm + 1e-6))."""
         w, dev = "AdamW.step", self.dev
-        if _lists().step(self._tab_at, self._n_at, grads, self.params, self.copies, dev):
+        if _lists().step(self._tab_at, self._n_at, len(self._n), grads, self.params, self.copies, dev):
             self._addresses()  # a parameter's memory is another one now
         if norm is not None:
             _vector(norm, "norm", w, 1, dev)
@@ -274,7 +274,7 @@ class AdamW:
             lr_dev, lr = lr, self.lr
         lr = self.lr if lr is None else lr
         a = N.MoeAdamW(lr, self.betas[0], self.betas[1], self.eps, self.max_norm or 0.0, self.bits, self.seed)
-        _launch("moe_adamw_step", self.m, stream, ctypes.byref(a), self._tab_at, len(self.params), self.m.data_ptr(),
+        _launch("moe_adamw_step", self.m, stream, ctypes.byref(a), self._tab_at, len(self._n), self.m.data_ptr(),
                 self.v.data_ptr(), _p(self.m_scale), _p(self.v_scale), self.clock.data_ptr(), _p(lr_dev), _p(norm),
                 self.ws.data_ptr(), self.ws.numel())
 
