@@ -100,6 +100,7 @@ __device__ __forceinline__ uint4 align_piece(const char* piece, const char* row,
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+template <int N>  // groups of 31 pieces in flight
 __global__ void __launch_bounds__(256) linear_align_kernel(AlignJob j0, AlignJob j1) {
   pdl_wait();
   pdl_trigger();
@@ -111,7 +112,6 @@ __global__ void __launch_bounds__(256) linear_align_kernel(AlignJob j0, AlignJob
     const char* first = reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(row) & ~uintptr_t(15));
     const int shift = int(row - first), words = shift / 4;
     uint4* dst = reinterpret_cast<uint4*>(j.dst + r * j.ldd);
-    constexpr int N = 4;  // groups of 31 pieces in flight
     for (int p0 = blockIdx.z * 31 * N; p0 < per; p0 += gridDim.z * 31 * N) {
       uint4 own[N];
 #pragma unroll
@@ -229,9 +229,16 @@ int launch_align(const AlignJob& a, const AlignJob& b, cudaStream_t st) {
   if (!a.src && !b.src) return MOE_OK;
   const AlignJob& one = a.src ? a : b;
   const int64_t rows = std::max(one.rows, two ? b.rows : 0), per = std::max(one.ldd, two ? b.ldd : 0) / 8;
+  // as many groups a warp (2 to 5) as leave the fewest places empty: 1003 columns are 5 groups
+  const int64_t groups = (per + 30) / 31;
+  int n = 5;
+  for (int i = 4; i >= 2; --i)
+    if ((groups + i - 1) / i * i < (groups + n - 1) / n * n) n = i;
   const dim3 grid(unsigned(std::min<int64_t>((rows + 7) / 8, 1 << 20)), two ? 2 : 1,
-                  unsigned(std::min<int64_t>((per + 123) / 124, 64)));
-  return launch_kernel(linear_align_kernel, grid, dim3(256), 0, st, one, b);
+                  unsigned(std::min<int64_t>((groups + n - 1) / n, 64)));
+  auto kern = n == 5 ? linear_align_kernel<5>
+                     : (n == 4 ? linear_align_kernel<4> : (n == 3 ? linear_align_kernel<3> : linear_align_kernel<2>));
+  return launch_kernel(kern, grid, dim3(256), 0, st, one, b);
 }
 
 }  // namespace moe
