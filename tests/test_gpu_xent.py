@@ -242,6 +242,19 @@ def test_offsets_beyond_32_bits(native_lib):
                    (None, back))
 
 
+@pytest.mark.parametrize("T,V,K", [(8087, 20011, 64), (8087, 20011, 4), (6000, 30001, 8), (20000, 5121, 136)])
+def test_many_tiles(native_lib, T, V, K):
+    """Products of many tiles with few k-blocks, whose last columns (one by one, slower) are followed by other tiles:
+    warps of a tile that run ahead of one another. Every token, several times."""
+    x, W, y = make(T, V, K, "bf16")
+    for _ in range(3):
+        got = train.linear_cross_entropy(x, W, y, z_coef=1e-3)
+        check_forward(x, W, y, 1e-3, got)
+    dx, _ = train.linear_cross_entropy_backward(x, W, y, got[1], stats=got[2], z_coef=1e-3, need_W=False)
+    w = torch.full((T,), 1.0 / int((y != IGNORE).sum()), dtype=torch.float64, device="cuda")
+    check_backward(x, W, y, 1e-3, got[1], w, (dx, None))
+
+
 @pytest.mark.parametrize("dtype,T,V,K", [("bf16", 1, 4096, 256), ("bf16", 50, 3001, 128), ("bf16", 900, 5000, 256),
                                          ("f32", 60, 1500, 64)])
 def test_streams_graphs_and_repeats(native_lib, dtype, T, V, K):

@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kPairThreads<MODE>, 1)
       mbar_init(tempty0 + 8 * a, kEpiWarps<MODE> * 2);
     }
     mbar_init(drain_bar, 1);
-    // (kXentStats: four of them, for the warps of 32 rows to hand their parts over)
+    // (kXentStats: eight of them, for the warps of 32 rows to hand their parts over, two tiles in turn)
     for (int b = 0; b < 16; ++b) mbar_init(res0 + 8 * b, MODE == kXentStats ? kEpiWarps<MODE> / 4 : 1);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -950,16 +950,17 @@ __global__ void __launch_bounds__(kPairThreads<MODE>, 1)
           }
         }
         if constexpr (MODE == kXentStats) {
-          // the warps of these rows hand their columns' (c, s) to the first of them, which joins them. A buffer is
-          // used again two tiles on: its accumulator is free only when that warp has arrived below.
+          // The warps of these rows hand their columns' (c, s) to the first of them, which joins them. They may be a
+          // tile ahead of it, so buffers and barriers are two; two tiles ahead they cannot be: the tile's
+          // accumulator is free for the MMAs only when that warp has arrived below.
           float2* join = reinterpret_cast<float2*>(sBox) + (i & 1) * 4 * BM;
-          const uint32_t bar = res0 + 8 * uint32_t(q);
+          const uint32_t bar = res0 + 8 * uint32_t(2 * q + (i & 1));
           join[half * BM + 32 * q + lane] = make_float2(sc, ss);
           __syncwarp();
           if (lane == 0) mbar_arrive(bar);
           if (half == 0) {
             const bool all =
-                __all_sync(0xffffffffu, wait_bounded(bar, uint32_t(i) & 1u, s_abort, p.status, wlimit));
+                __all_sync(0xffffffffu, wait_bounded(bar, uint32_t(i >> 1) & 1u, s_abort, p.status, wlimit));
             if (!all) break;
             float2 o[3];
 #pragma unroll
