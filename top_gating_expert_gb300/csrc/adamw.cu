@@ -5,7 +5,10 @@
 //   p  = p (1 - lr wd) - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 //
 // element by element, bound by memory: an fp32 parameter with fp32 moments moves 28 bytes (30 with
-// its bf16 copy), with 8-bit moments 16 (18). The tensors' table travels as a kernel argument (no
+// its bf16 copy), with 8-bit moments 16 (18). 2^28 fp32 elements: 1147 us in 32 bits (6.55 TB/s, 0.98 of the
+// copy rate), 1245 with the copy; in 8 bits 809 (nearest codes; 5.3 TB/s) and 919 (random): 100 instructions an element,
+// 72 % of the issue slots, beside 61 % of DRAM's rate. The values of the codes: 444 us (6.0 TB/s); the norm 172 us
+// (bf16 92). The tensors' table travels as a kernel argument (no
 // copy to the device, and a captured graph holds it), in the smallest of three sizes that takes it;
 // persistent CTAs walk chunks of 2048 elements over all tensors, a warp 256 of them, and find a
 // chunk's tensor by halving.
@@ -78,41 +81,22 @@ __device__ __forceinline__ int tensor_of(const Table<CAP>& tab, int n, int64_t c
   return lo;
 }
 
-// Four elements i .. i + 3 of which `left` exist, as fp32 (0 where there is none)
-__device__ __forceinline__ float4 load4(const void* base, int bf16, int vec, int64_t i, int left) {
-  if (left >= 4 && vec) {
-    if (!bf16) return __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
-    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + i));
-    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
-    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-  }
-  float f[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    f[q] = 0.f;
-    if (q < left)
-      f[q] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i + q]) : static_cast<const float*>(base)[i + q];
-  }
-  return make_float4(f[0], f[1], f[2], f[3]);
+// Four elements i .. i + 3 as one access
+__device__ __forceinline__ float4 load4(const void* base, int bf16, int64_t i) {
+  if (!bf16) return __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
+  const uint2 w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + i));
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
+  return make_float4(a.x, a.y, b.x, b.y);
 }
-__device__ __forceinline__ void store4(void* base, int bf16, int vec, int64_t i, int left, const float (&f)[4]) {
-  if (left >= 4 && vec) {
-    if (!bf16) {
-      __stcs(reinterpret_cast<float4*>(static_cast<float*>(base) + i), make_float4(f[0], f[1], f[2], f[3]));
-    } else {
-      __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
-      __stcs(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + i),
-             make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b)));
-    }
-    return;
+__device__ __forceinline__ void store4(void* base, int bf16, int64_t i, const float (&f)[4]) {
+  if (!bf16) {
+    __stcs(reinterpret_cast<float4*>(static_cast<float*>(base) + i), make_float4(f[0], f[1], f[2], f[3]));
+  } else {
+    __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    __stcs(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + i),
+           make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b)));
   }
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    if (q < left) {
-      if (bf16) static_cast<__nv_bfloat16*>(base)[i + q] = __float2bfloat16_rn(f[q]);
-      else static_cast<float*>(base)[i + q] = f[q];
-    }
 }
 
 __device__ __forceinline__ uint32_t mix32(uint32_t h) {
@@ -217,14 +201,63 @@ struct Shared {
   uint32_t key;
 };
 
-// A warp's 256 elements e0 .. of tensor x, places s0 .. of the moments. FULL: all of them exist, in whole
-// accesses; P16, G16: p and g in bf16 (without FULL x says so).
+// A warp's 256 elements e0 .. of tensor x, places s0 .. of the moments, 8 a lane. FULL: all of them exist, in
+// accesses of four elements; else (a tensor's end, rows on no boundary) one by one, neighbouring lanes on
+// neighbouring elements (12.7 M bf16 parameters and gradients on no boundary: 56 us, with four in a row a
+// lane 80). P16, G16: p and g in
+// bf16.
 template <int BITS, bool FULL, bool P16, bool G16>
 __device__ __forceinline__ void adamw_block(const Tensor& x, const StepArgs& a, const Shared& sh, float decay, int64_t e0,
                                             int64_t s0, int valid_) {
   const int lane = threadIdx.x & 31;
   const int valid = FULL ? kBlock : valid_;
-  const int p16 = FULL ? P16 : x.p_bf16, g16 = FULL ? G16 : x.g_bf16, vec = FULL ? 1 : x.vec;
+  constexpr int p16 = P16, g16 = G16;
+  // the place of a lane's e-th element, and four of them (4 q ..) from and to memory
+  auto place_of = [&](int e) { return FULL ? 128 * (e / 4) + 4 * lane + (e & 3) : 32 * e + lane; };
+  auto load = [&](const void* base, int bf16, int64_t from, int q) {
+    if constexpr (FULL) return load4(base, bf16, from + place_of(4 * q));
+    float f[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = place_of(4 * q + k);
+      f[k] = 0.f;
+      if (i < valid)
+        f[k] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(base)[from + i])
+                    : static_cast<const float*>(base)[from + i];
+    }
+    return make_float4(f[0], f[1], f[2], f[3]);
+  };
+  auto store = [&](void* base, int bf16, int64_t from, int q, const float (&f)[4]) {
+    if constexpr (FULL) {
+      store4(base, bf16, from + place_of(4 * q), f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = place_of(4 * q + k);
+        if (i >= valid) continue;
+        if (bf16) static_cast<__nv_bfloat16*>(base)[from + i] = __float2bfloat16_rn(f[k]);
+        else static_cast<float*>(base)[from + i] = f[k];
+      }
+    }
+  };
+  // codes: every block of theirs is whole
+  auto load_codes = [&](const void* base, int q) {
+    const uint8_t* c = static_cast<const uint8_t*>(base) + s0;
+    if constexpr (FULL) return __ldcs(reinterpret_cast<const uint32_t*>(c + place_of(4 * q)));
+    uint32_t w = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w |= uint32_t(c[place_of(4 * q + k)]) << (8 * k);
+    return w;
+  };
+  auto store_codes = [&](void* base, int q, uint32_t w) {
+    uint8_t* c = static_cast<uint8_t*>(base) + s0;
+    if constexpr (FULL) {
+      __stcs(reinterpret_cast<uint32_t*>(c + place_of(4 * q)), w);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[place_of(4 * q + k)] = uint8_t(w >> (8 * k));
+    }
+  };
   const float size = sh.size, rs = sh.rs, coef = sh.coef;
   const uint32_t key = sh.key;
   float4 pv[2], gv[2], mv[2], vv[2];
@@ -232,15 +265,14 @@ __device__ __forceinline__ void adamw_block(const Tensor& x, const StepArgs& a, 
   float ms = 0.f, vs = 0.f;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int at = 128 * q + 4 * lane, left = valid - at;
-    gv[q] = load4(x.g, g16, vec, e0 + at, left);
-    pv[q] = load4(x.p, p16, vec, e0 + at, left);
+    gv[q] = load(x.g, g16, e0, q);
+    pv[q] = load(x.p, p16, e0, q);
     if constexpr (BITS == 32) {
-      mv[q] = load4(a.m, 0, 1, s0 + at, left);
-      vv[q] = load4(a.v, 0, 1, s0 + at, left);
-    } else {  // whole words of codes: the buffer is padded to blocks
-      mc[q] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + s0 + at));
-      vc[q] = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + s0 + at));
+      mv[q] = load(a.m, 0, s0, q);
+      vv[q] = load(a.v, 0, s0, q);
+    } else {
+      mc[q] = load_codes(a.m, q);
+      vc[q] = load_codes(a.v, q);
     }
   }
   if constexpr (BITS == 8) {
@@ -259,7 +291,6 @@ __device__ __forceinline__ void adamw_block(const Tensor& x, const StepArgs& a, 
       v4[0] = vv[q].x; v4[1] = vv[q].y; v4[2] = vv[q].z; v4[3] = vv[q].w;
     }
     const uint32_t flip = BITS == 8 ? mc[q] ^ 0x80808080u : 0u;  // signed bytes from 0 on
-    const int at = 128 * q + 4 * lane, left = valid - at;
 #pragma unroll
     for (int k = 0; k < 4; k += 2) {
       f32x2 m2, v2;
@@ -292,11 +323,11 @@ __device__ __forceinline__ void adamw_block(const Tensor& x, const StepArgs& a, 
       v[e] = vf.x;
       v[e + 1] = vf.y;
     }
-    store4(x.p, p16, vec, e0 + at, left, out);
-    if (x.copy) store4(x.copy, 1, vec, e0 + at, left, out);
+    store(x.p, p16, e0, q, out);
+    if (x.copy) store(x.copy, 1, e0, q, out);
     if constexpr (BITS == 32) {
-      store4(a.m, 0, 1, s0 + at, left, reinterpret_cast<const float(&)[4]>(m[4 * q]));
-      store4(a.v, 0, 1, s0 + at, left, reinterpret_cast<const float(&)[4]>(v[4 * q]));
+      store(a.m, 0, s0, q, reinterpret_cast<const float(&)[4]>(m[4 * q]));
+      store(a.v, 0, s0, q, reinterpret_cast<const float(&)[4]>(v[4 * q]));
     }
   }
   if constexpr (BITS == 8) {
@@ -313,11 +344,11 @@ __device__ __forceinline__ void adamw_block(const Tensor& x, const StepArgs& a, 
     float s2, i2;
     block_scale(lane < 16 ? mb : __float_as_uint(__fsqrt_rn(__uint_as_float(vb))), lane < 16 ? kMLevels : kVLevels, s2, i2);
     const float im = __shfl_sync(0xffffffffu, i2, 0), iv = __shfl_sync(0xffffffffu, i2, 16);
-    // The thresholds of element e, times 2^16: the halves of mix32(place ^ key), plus 1/2. Of the place the bits of
-    // 128 (e / 4) + e % 4 are those of the element in the lane, so the hash's first step is shared.
-    const uint32_t x0 = uint32_t(s0 + 4 * lane) ^ (uint32_t(s0 >> 32) * 0x2545F491u) ^ key, x1 = x0 ^ (x0 >> 16);
+    // The thresholds of element e, times 2^16: the halves of mix32(place ^ key), plus 1/2. In the place the bits of
+    // the element in the lane are apart from the lane's, so the hash's first step is shared.
+    const uint32_t x0 = uint32_t(s0 + place_of(0)) ^ (uint32_t(s0 >> 32) * 0x2545F491u) ^ key, x1 = x0 ^ (x0 >> 16);
     auto thresholds = [&](int e, float& fm, float& fv) {
-      uint32_t h = (x1 ^ uint32_t(128 * (e / 4) + (e & 3))) * 0x9E3779B1u;
+      uint32_t h = (x1 ^ uint32_t(FULL ? 128 * (e / 4) + (e & 3) : 32 * e)) * 0x9E3779B1u;
       h = (h ^ (h >> 15)) * 0x85157AF5u;
       fm = __uint_as_float(__byte_perm(h ^ (h >> 16), 0x4B000000u, 0x7610u));
       fv = __uint_as_float(__byte_perm(h, 0x4B000000u, 0x7632u));
@@ -375,9 +406,8 @@ __device__ __forceinline__ void adamw_block(const Tensor& x, const StepArgs& a, 
     if (__any_sync(0xffffffffu, margin < 0.f)) codes(std::true_type{});
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int64_t at = s0 + 128 * q + 4 * lane;
-      __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + at), wm[q]);
-      __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + at), wv[q]);
+      store_codes(a.m, q, wm[q]);
+      store_codes(a.v, q, wv[q]);
     }
     if ((lane & 15) == 0) (lane == 0 ? a.m_scale : a.v_scale)[s0 / kBlock] = s2;
   }
@@ -413,16 +443,16 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
     const int64_t s0 = x.first + e0;
     const int valid = int(min(int64_t(kBlock), x.n - e0));
     const float decay = a.lr_dev ? fmaf(-lr, x.wd, 1.f) : x.decay;
-    if (valid == kBlock && x.vec) {
-      if (x.p_bf16) {
-        if (x.g_bf16) adamw_block<BITS, true, true, true>(x, a, sh, decay, e0, s0, valid);
-        else adamw_block<BITS, true, true, false>(x, a, sh, decay, e0, s0, valid);
-      } else {
-        if (x.g_bf16) adamw_block<BITS, true, false, true>(x, a, sh, decay, e0, s0, valid);
-        else adamw_block<BITS, true, false, false>(x, a, sh, decay, e0, s0, valid);
-      }
-    } else {
-      adamw_block<BITS, false, false, false>(x, a, sh, decay, e0, s0, valid);
+    const bool full = valid == kBlock && x.vec;
+    switch ((full ? 4 : 0) + (x.p_bf16 ? 2 : 0) + (x.g_bf16 ? 1 : 0)) {  // the same for the whole warp
+      case 0: adamw_block<BITS, false, false, false>(x, a, sh, decay, e0, s0, valid); break;
+      case 1: adamw_block<BITS, false, false, true>(x, a, sh, decay, e0, s0, valid); break;
+      case 2: adamw_block<BITS, false, true, false>(x, a, sh, decay, e0, s0, valid); break;
+      case 3: adamw_block<BITS, false, true, true>(x, a, sh, decay, e0, s0, valid); break;
+      case 4: adamw_block<BITS, true, false, false>(x, a, sh, decay, e0, s0, valid); break;
+      case 5: adamw_block<BITS, true, false, true>(x, a, sh, decay, e0, s0, valid); break;
+      case 6: adamw_block<BITS, true, true, false>(x, a, sh, decay, e0, s0, valid); break;
+      case 7: adamw_block<BITS, true, true, true>(x, a, sh, decay, e0, s0, valid); break;
     }
   }
   if (!a.last) return;
@@ -521,12 +551,18 @@ __global__ void __launch_bounds__(kThreads, 4) grad_norm_kernel(const __grid_con
         }
       }
     } else {
-#pragma unroll 2
-      for (int q = threadIdx.x * 4; q < kNormChunk && q < rest; q += kThreads * 4) {
-        const float4 v = load4(x.g, x.g_bf16, x.vec, e0 + q, int(min(int64_t(4), rest - q)));
-        s[0] = fmaf(v.x, v.x, s[0]); s[1] = fmaf(v.y, v.y, s[1]);
-        s[2] = fmaf(v.z, v.z, s[2]); s[3] = fmaf(v.w, v.w, s[3]);
-      }
+      const int n = int(min(int64_t(kNormChunk), rest));
+      auto add = [&](const auto* p) {
+        for (int q0 = threadIdx.x; q0 < n; q0 += 8 * kThreads) {
+          float v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[q] = q0 + q * kThreads < n ? to_f32(p[q0 + q * kThreads]) : 0.f;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) s[q & 3] = fmaf(v[q], v[q], s[q & 3]);
+        }
+      };
+      if (x.g_bf16) add(static_cast<const __nv_bfloat16*>(x.g) + e0);
+      else add(static_cast<const float*>(x.g) + e0);
     }
     sum += (s[0] + s[1]) + (s[2] + s[3]);
   }

@@ -537,7 +537,9 @@ int run_tile(const LinearOperand& A, const LinearOperand& B, int rows, int cols,
 // products at 16384 x 4096 x 1024 take 87 us each: 256 and 64 tiles fill 76 pairs to 84 %.
 constexpr int kBand = 16;
 // The epilogues that take an exponential of every logit have 16 warps: with 8 the latencies of two warps a
-// scheduler bound them (8192 x 131072 x 256 forward 500 us with 8 warps).
+// scheduler bound them (8192 x 131072 x 64 forward 430 us with 8 warps, 355 with 16, 297 with the rare paths out
+// of the loops; a tile's hand-over between MMAs and epilogue then takes as long as its 64-deep product). A third of the
+// exponentials by a polynomial on the multiply-add pipe instead: slower (425), the issue slots are the scarcer.
 template <int MODE>
 constexpr int kEpiWarps = MODE == kXentStats || MODE == kXentGrad ? 16 : 8;
 template <int MODE>

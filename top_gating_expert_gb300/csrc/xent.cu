@@ -17,6 +17,9 @@
 // 2^-8, the same way in every token (8192 x 65536 x 2048: gradients 3.1e-3 off in all with w in d, now 1.7e-3,
 // their own rounding).
 // fp32: the logits of a piece go through the workspace; the plain-FMA products are by far the longest part.
+// Measured: 8192 x 65536 x 2048 forward 1.12 ms, backward 3.9 (tensor pipe 83 to 90 % active); 8192 x 32768 x 1024
+// forward 303 us, backward 962; 1 x 32768 x 1024 forward 26 us alone. The tensor cores' sums truncate: lse comes
+// out low by 3e-7 of itself for every 1024 of K.
 #include <math.h>
 
 #include <algorithm>
