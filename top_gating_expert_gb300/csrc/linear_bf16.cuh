@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kPairThreads<MODE>, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::STAGES;
   const uint32_t tfull0 = empty0 + 8 * C::STAGES, tempty0 = tfull0 + 16, drain_bar = tempty0 + 16;
-  const uint32_t res0 = drain_bar + 8;  // [8 warps][2 boxes]: a residual box has landed
+  const uint32_t res0 = drain_bar + 8;  // [8 warps][2 boxes]: a residual box has landed (kXentStats: see below)
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int unit = int(blockIdx.x >> 1), units = int(gridDim.x >> 1);
@@ -609,8 +609,9 @@ __global__ void __launch_bounds__(kPairThreads<MODE>, 1)
       mbar_init(tempty0 + 8 * a, kEpiWarps<MODE> * 2);
     }
     mbar_init(drain_bar, 1);
-    // (kXentStats: eight of them, for the warps of 32 rows to hand their parts over, two tiles in turn)
-    for (int b = 0; b < 16; ++b) mbar_init(res0 + 8 * b, MODE == kXentStats ? kEpiWarps<MODE> / 4 : 1);
+    // (kXentStats: for the warps of 32 rows to hand their parts over, two tiles in turn: eight for parts written, eight
+    // for parts read)
+    for (int b = 0; b < 16; ++b) mbar_init(res0 + 8 * b, MODE == kXentStats && b < 8 ? kEpiWarps<MODE> / 4 : 1);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&tmA);
@@ -953,11 +954,17 @@ __global__ void __launch_bounds__(kPairThreads<MODE>, 1)
         }
         if constexpr (MODE == kXentStats) {
           // The warps of these rows hand their columns' (c, s) to the first of them, which joins them. They may be a
-          // tile ahead of it, so buffers and barriers are two; two tiles ahead they cannot be: the tile's
-          // accumulator is free for the MMAs only when that warp has arrived below.
+          // tile ahead of it, so buffers and barriers are two. Two tiles ahead they are never (the tile's
+          // accumulator is free for the MMAs only when that warp has arrived below), but that arrival orders no
+          // accesses to shared memory: a buffer is written again once its reader has said so itself.
           float2* join = reinterpret_cast<float2*>(sBox) + (i & 1) * 4 * BM;
-          const uint32_t bar = res0 + 8 * uint32_t(2 * q + (i & 1));
-          join[half * BM + 32 * q + lane] = make_float2(sc, ss);
+          const uint32_t bar = res0 + 8 * uint32_t(2 * q + (i & 1)), read_bar = bar + 64;
+          if (half != 0) {
+            const bool empty = __all_sync(
+                0xffffffffu, wait_bounded(read_bar, (uint32_t(i >> 1) & 1u) ^ 1u, s_abort, p.status, wlimit));
+            if (!empty) break;
+            join[half * BM + 32 * q + lane] = make_float2(sc, ss);
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar);
           if (half == 0) {
@@ -967,6 +974,8 @@ __global__ void __launch_bounds__(kPairThreads<MODE>, 1)
             float2 o[3];
 #pragma unroll
             for (int h = 0; h < 3; ++h) o[h] = join[(h + 1) * BM + 32 * q + lane];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(read_bar);
             const float cn = max3(max3(sc, o[0].x, o[1].x), o[2].x, kNegInf), base = cn == kNegInf ? 0.f : cn;
             ss *= exp2_approx(sc - base);
 #pragma unroll
