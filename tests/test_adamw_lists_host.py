@@ -1,0 +1,57 @@
+"""What AdamW's step checks of its tensors before anything is launched, on CPU tensors that say that they lie on a
+GPU, the library's calls replaced by a record of them."""
+
+import pytest
+import torch
+
+from test_block_host import OnDevice1
+from top_gating_expert_gb300 import moe, train
+
+
+def there(*s, dtype=torch.float32):
+    return torch.zeros(s, dtype=dtype).as_subclass(OnDevice1)
+
+
+@pytest.fixture
+def calls(native_lib, monkeypatch):
+    """The names of the library's calls, in order."""
+    made = []
+
+    def entry(name):
+        def call(*a):
+            made.append(name)
+            return 0
+        return call
+
+    monkeypatch.setattr(moe, "_one_device", lambda: True)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 100 + dev, raising=False)
+    monkeypatch.setattr(train, "_device", lambda dev: torch.device("cpu"))
+    monkeypatch.setattr(moe, "_entry", entry)
+    monkeypatch.setattr(torch, "zeros", lambda *s, dtype=torch.float32, device=None, _z=torch.zeros:
+                        _z(*s, dtype=dtype).as_subclass(OnDevice1))
+    monkeypatch.setattr(torch, "tensor", lambda *s, device=None, _t=torch.tensor, **k: _t(*s, **k).as_subclass(OnDevice1))
+    return made
+
+
+def refused_twice(opt, grads, calls, **kw):
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            opt.step(grads, **kw)
+    assert "moe_adamw_step" not in calls
+
+
+@pytest.mark.parametrize("new", [lambda a, b: there(200), lambda a, b: there(300, dtype=torch.float16),
+                                 lambda a, b: there(20, 30)[:, ::2], lambda a, b: b[10:]],
+                         ids=["shorter", "type", "strided", "overlapping"])
+def test_a_refused_step_is_refused_again(calls, new):
+    """A parameter's memory replaced by one that cannot be updated: every step says so, none uses its address."""
+    a, b = there(300), there(310)
+    opt = train.AdamW([a, b])
+    opt.step([there(300), there(310)])
+    assert calls == ["moe_adamw_step"]
+    calls.clear()
+    a.data = new(a, b)
+    refused_twice(opt, [there(300), there(310)], calls)
+    a.data = there(300)
+    opt.step([there(300), there(310)])
+    assert calls == ["moe_adamw_step"] and opt._tab["p"][0] == a.data_ptr()

@@ -236,10 +236,10 @@ class AdamW:
         self.ws = z(256, torch.uint8)
 
     def _addresses(self):
-        """Reads the parameters' and copies' addresses and checks that no two overlap."""
+        """Reads the parameters' and copies' addresses and checks that no two overlap. The table is written when all
+        of them are found right: a step that is refused is refused again."""
         w, dev, tab = "AdamW", self.dev, self._tab
-        tab["p"] = p = [_elements(t, "every parameter", w, dev) for t in self.params]
-        tab["p_dtype"] = [_DTYPES[t.dtype] for t in self.params]
+        p = [_elements(t, "every parameter", w, dev) for t in self.params]
         spans = []
         for i, (t, c) in enumerate(zip(self.params, self.copies)):
             k = int(self._n[i])
@@ -252,10 +252,12 @@ class AdamW:
                                      f"device {dev}")
                 spans.append((c.data_ptr(), 2 * k))
             spans.append((p[i], t.element_size() * k))
-        tab["copy"] = [0 if c is None else c.data_ptr() for c in self.copies]
         spans = sorted(s for s in spans if s[1])
         if any(a + k > b for (a, k), (b, _) in zip(spans, spans[1:])):
             raise ValueError(f"{w}: parameters or copies overlap in memory")
+        tab["p"] = p
+        tab["p_dtype"] = [_DTYPES[t.dtype] for t in self.params]
+        tab["copy"] = [0 if c is None else c.data_ptr() for c in self.copies]
 
     def step(self, grads, *, lr=None, norm=None, stream=None):
         """One step with a gradient for each parameter (None: that parameter is left as it is). lr: a
