@@ -55,3 +55,21 @@ def test_a_refused_step_is_refused_again(calls, new):
     a.data = there(300)
     opt.step([there(300), there(310)])
     assert calls == ["moe_adamw_step"] and opt._tab["p"][0] == a.data_ptr()
+
+
+def test_a_parameter_changed_in_place(calls):
+    """The same memory as another tensor (transposed, shorter, of another type), a copy likewise: seen at every step."""
+    a, cp = there(20, 30), there(20, 30, dtype=torch.bfloat16)
+    opt = train.AdamW([a], copies=[cp])
+    held = a.data
+    for t, other in ((a, held.t()), (a, held[:10]), (a, held.view(torch.int32)), (cp, cp.data.t()), (cp, cp.data[:3])):
+        was = t.data
+        t.data = other
+        assert t.data_ptr() == was.data_ptr()
+        refused_twice(opt, [there(600)], calls)
+        t.data = was
+    opt.step([there(20, 30)])
+    a.data = held.view(30, 20)  # the same elements in the same order
+    opt.copies[0] = None
+    opt.step([there(30, 20)])
+    assert calls == ["moe_adamw_step"] * 2 and opt._tab["copy"][0] == 0

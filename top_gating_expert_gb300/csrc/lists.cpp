@@ -20,9 +20,9 @@ namespace {
 int element_type(PyObject* o, long dev, const char* where, const char* what) {
   if (THPVariable_Check(o)) {
     const at::Tensor& t = THPVariable_Unpack(o);
-    // the device as the object itself has it: a subclass may answer otherwise
+    // the device as the object itself has it: a subclass (other than Parameter) may answer otherwise
     long at = -1;
-    if (Py_TYPE(o) == reinterpret_cast<PyTypeObject*>(THPVariableClass)) {
+    if (THPVariable_CheckExact(o)) {
       at = t.get_device();
     } else {
       PyObject* d = PyObject_CallMethod(o, "get_device", nullptr);
@@ -76,8 +76,11 @@ PyObject* gradients(PyObject*, PyObject* args) {
                        Py_ssize_t(tab.size()));
 }
 
+// Whether a gradient's elements are those of its parameter, one for one: the same shape, or one of them flat.
+bool same_order(const at::Tensor& g, const at::Tensor& p) { return g.dim() == 1 || p.dim() == 1 || g.sizes() == p.sizes(); }
+
 // step(table's address, sizes' address, their length, gradients, parameters, copies, device) -> whether a parameter or
-// copy has another address than the table. Writes g, n and g_dtype (no gradient: n = 0).
+// copy is not what the table says (address, type, size). Writes g, n and g_dtype (no gradient: n = 0).
 PyObject* step(PyObject*, PyObject* args) {
   unsigned long long table, sizes;
   PyObject *grads, *params, *copies;
@@ -96,9 +99,16 @@ PyObject* step(PyObject*, PyObject* args) {
   bool moved = false;
   for (Py_ssize_t i = 0; i < g.size(); ++i) {
     moe_param_t& e = tab[i];
-    if (!THPVariable_Check(p[i]) || (c[i] != Py_None && !THPVariable_Check(c[i])))
-      return PyErr_Format(PyExc_ValueError, "AdamW.step: parameter or copy %zd is no tensor", i);
-    moved |= address(p[i]) != e.p || (c[i] != Py_None && address(c[i]) != e.copy);
+    const int pt = element_type(p[i], dev, "AdamW.step", "every parameter");
+    if (pt < 0) return nullptr;
+    moved |= address(p[i]) != e.p || pt != e.p_dtype || THPVariable_Unpack(p[i]).numel() != n[i];
+    if (c[i] != Py_None) {
+      const int ct = element_type(c[i], dev, "AdamW.step", "every copy");
+      if (ct < 0) return nullptr;
+      moved |= address(c[i]) != e.copy || ct != MOE_BF16 || THPVariable_Unpack(c[i]).numel() != n[i];
+    } else {
+      moved |= e.copy != nullptr;
+    }
     if (g[i] == Py_None) {
       e.g = nullptr;
       e.n = 0;
