@@ -73,3 +73,16 @@ def test_a_parameter_changed_in_place(calls):
     opt.copies[0] = None
     opt.step([there(30, 20)])
     assert calls == ["moe_adamw_step"] * 2 and opt._tab["copy"][0] == 0
+
+
+def test_gradients_of_another_shape(calls):
+    """As many elements in another order are refused; a flat gradient, or a flat parameter's, has one order only."""
+    a, b = there(20, 30), there(3, 4, 5)
+    opt = train.AdamW([a, b])
+    for ga, gb in (((30, 20), (3, 4, 5)), ((20, 30), (12, 5)), ((20, 30), (3, 5, 4)), ((1, 30, 20), (60,))):
+        refused_twice(opt, [there(*ga), there(*gb)], calls)
+    refused_twice(opt, [None, there(5, 4, 3)], calls)
+    for ga, gb in (((20, 30), (3, 4, 5)), ((600,), (60,)), ((1, 20, 1, 30), (3, 4, 5, 1))):
+        opt.step([there(*ga), there(*gb)])
+    train.AdamW([there(600)]).step([there(20, 30)])
+    assert calls == ["moe_adamw_step"] * 4

@@ -10,6 +10,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
+#include <sstream>
 #include <vector>
 
 #include "moe.h"
@@ -76,8 +77,19 @@ PyObject* gradients(PyObject*, PyObject* args) {
                        Py_ssize_t(tab.size()));
 }
 
-// Whether a gradient's elements are those of its parameter, one for one: the same shape, or one of them flat.
-bool same_order(const at::Tensor& g, const at::Tensor& p) { return g.dim() == 1 || p.dim() == 1 || g.sizes() == p.sizes(); }
+// Whether a gradient's elements are those of its parameter, one for one: the same shape (sides of 1 apart), or one of
+// them flat.
+bool same_order(const at::Tensor& g, const at::Tensor& p) {
+  const auto a = g.sizes(), b = p.sizes();
+  if (a == b || a.size() == 1 || b.size() == 1) return true;
+  size_t i = 0, j = 0;
+  for (;; ++i, ++j) {
+    while (i < a.size() && a[i] == 1) ++i;
+    while (j < b.size() && b[j] == 1) ++j;
+    if (i == a.size() || j == b.size()) return i == a.size() && j == b.size();
+    if (a[i] != b[j]) return false;
+  }
+}
 
 // step(table's address, sizes' address, their length, gradients, parameters, copies, device) -> whether a parameter or
 // copy is not what the table says (address, type, size). Writes g, n and g_dtype (no gradient: n = 0).
@@ -121,6 +133,13 @@ PyObject* step(PyObject*, PyObject* args) {
     if (t.numel() != n[i]) {
       PyErr_Format(PyExc_ValueError, "AdamW.step: gradient %zd has %lld elements and its parameter %lld", i,
                    (long long)t.numel(), (long long)n[i]);
+      return nullptr;
+    }
+    if (!same_order(t, THPVariable_Unpack(p[i]))) {
+      std::ostringstream say;
+      say << "AdamW.step: gradient " << i << " has shape " << t.sizes() << " and its parameter "
+          << THPVariable_Unpack(p[i]).sizes();
+      PyErr_SetString(PyExc_ValueError, say.str().c_str());
       return nullptr;
     }
     e.g = address(g[i]);

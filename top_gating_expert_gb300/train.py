@@ -260,7 +260,7 @@ class AdamW:
         tab["copy"] = [0 if c is None else c.data_ptr() for c in self.copies]
 
     def step(self, grads, *, lr=None, norm=None, stream=None):
-        """One step with a gradient for each parameter (None: that parameter is left as it is). lr: a
+        """One step with a gradient for each parameter, of its shape or flat (None: that parameter is left as it is). lr: a
         number for this step, or a float32 CUDA tensor [1] that the device reads. norm: float32 [1], as
         grad_norm gives it; with max_norm the gradients are scaled by min(1, max_norm / (norm + 1e-6))."""
         w, dev = "AdamW.step", self.dev
@@ -358,7 +358,7 @@ class TrainStep:
         self.ws = linear_cross_entropy_workspace(T, head.shape[0], M, head.dtype, head.device) if self.blocks else None
 
     def gradients(self, x, target, u=None):
-        """(stats, gradients): the head's stats (see linear_cross_entropy) and a gradient for each of `masters`.
+        """(stats, gradients): the head's stats (see linear_cross_entropy) and a gradient for each of `masters`, of its shape.
         u: the draws for blocks with random routing."""
         inputs = []
         for b in self.blocks:
@@ -384,7 +384,8 @@ class TrainStep:
             if c.n_shared > 1:  # the shared experts' hidden units lie side by side
                 got[-1] = got[-1].view(c.M, c.n_shared, c.H_shared).transpose(0, 1).contiguous()
             found.append([t for t in (*got, g.dbias) if t is not None] + [dgamma, dbeta])
-        return stats, [t for part in reversed(found) for t in part]
+        grads = [t for part in reversed(found) for t in part]
+        return stats, [t if t.shape == p.shape else t.view(p.shape) for t, (_, p) in zip(grads, self.masters)]
 
     def step(self, x, target, u=None, lr=None):
         """One step; returns the stats of its forward (float32 [2], on the device)."""
