@@ -86,3 +86,30 @@ def test_gradients_of_another_shape(calls):
         opt.step([there(*ga), there(*gb)])
     train.AdamW([there(600)]).step([there(20, 30)])
     assert calls == ["moe_adamw_step"] * 4
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_state_that_is_replaced(calls, bits):
+    """Moments, scales and clock of another device, type or length, as a checkpoint may hold them, are refused."""
+    opt = train.AdamW([there(300), there(5)], bits=bits)
+    g = [there(300), there(5)]
+    dt, ut = (torch.float32, torch.float32) if bits == 32 else (torch.int8, torch.uint8)
+    good = dict(m=there(768, dtype=dt), v=there(768, dtype=ut), clock=there(3, dtype=torch.float64))
+    bad = [("m", torch.empty(768, dtype=dt)), ("m", there(767, dtype=dt)), ("v", there(1536, dtype=ut)[::2]),
+           ("v", there(768, dtype=torch.float16)), ("clock", there(3)), ("clock", there(2, dtype=torch.float64)),
+           ("m", None), ("clock", [0.0, 1.0, 1.0])]
+    if bits == 8:
+        good.update(m_scale=there(3), v_scale=there(3))
+        bad += [("m_scale", there(2)), ("v_scale", None), ("v_scale", torch.empty(3)), ("v", there(768, dtype=dt))]
+    for name, t in bad:
+        was = getattr(opt, name)
+        setattr(opt, name, t)
+        refused_twice(opt, g, calls)
+        if bits == 8 and name != "clock":
+            with pytest.raises(ValueError):
+                opt.moments()
+        setattr(opt, name, was)
+    for name, t in good.items():
+        setattr(opt, name, t)
+    opt.step(g)
+    assert calls == ["moe_adamw_step"]

@@ -17,25 +17,31 @@
 
 namespace {
 
+// Whether o is a contiguous tensor on the device; false, with no error set or with Python's, if not.
+bool there(PyObject* o, long dev) {
+  if (!THPVariable_Check(o)) return false;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  // the device as the object itself has it: a subclass (other than Parameter) may answer otherwise
+  long at = -1;
+  if (THPVariable_CheckExact(o)) {
+    at = t.get_device();
+  } else {
+    PyObject* d = PyObject_CallMethod(o, "get_device", nullptr);
+    if (!d) return false;
+    at = PyLong_AsLong(d);
+    Py_DECREF(d);
+    if (at == -1 && PyErr_Occurred()) return false;
+  }
+  return at == dev && t.layout() == at::kStrided && t.is_contiguous();
+}
+
 // The element type of a tensor as the kernels take it, or -1 with a ValueError set.
 int element_type(PyObject* o, long dev, const char* where, const char* what) {
-  if (THPVariable_Check(o)) {
-    const at::Tensor& t = THPVariable_Unpack(o);
-    // the device as the object itself has it: a subclass (other than Parameter) may answer otherwise
-    long at = -1;
-    if (THPVariable_CheckExact(o)) {
-      at = t.get_device();
-    } else {
-      PyObject* d = PyObject_CallMethod(o, "get_device", nullptr);
-      if (!d) return -1;
-      at = PyLong_AsLong(d);
-      Py_DECREF(d);
-      if (at == -1 && PyErr_Occurred()) return -1;
-    }
-    const auto st = t.scalar_type();
-    if (at == dev && t.layout() == at::kStrided && (st == at::kFloat || st == at::kBFloat16) && t.is_contiguous())
-      return st == at::kFloat ? MOE_F32 : MOE_BF16;
+  if (there(o, dev)) {
+    const auto st = THPVariable_Unpack(o).scalar_type();
+    if (st == at::kFloat || st == at::kBFloat16) return st == at::kFloat ? MOE_F32 : MOE_BF16;
   }
+  if (PyErr_Occurred()) return -1;
   PyErr_Format(PyExc_ValueError, "%s: %s must be a contiguous float32 or bfloat16 tensor on CUDA device %ld", where,
                what, dev);
   return -1;
@@ -149,6 +155,31 @@ PyObject* step(PyObject*, PyObject* args) {
   return PyBool_FromLong(moved);
 }
 
+// state(device, elements, bits, m, v, m_scale, v_scale, clock): nothing, or a ValueError for what an optimiser of that
+// many elements does not hold. They are attributes that a program may replace.
+PyObject* state(PyObject*, PyObject* args) {
+  long dev, bits;
+  long long n;
+  PyObject* t[5];
+  if (!PyArg_ParseTuple(args, "lLlOOOOO", &dev, &n, &bits, t, t + 1, t + 2, t + 3, t + 4)) return nullptr;
+  static const char* const name[5] = {"m", "v", "m_scale", "v_scale", "clock"};
+  const bool codes = bits == 8;
+  const at::ScalarType type[5] = {codes ? at::kChar : at::kFloat, codes ? at::kByte : at::kFloat, at::kFloat, at::kFloat,
+                                  at::kDouble};
+  const long long size[5] = {n, n, n / 256, n / 256, 3};
+  for (int i = 0; i < 5; ++i) {
+    if (!codes && (i == 2 || i == 3)) continue;
+    if (there(t[i], dev) && THPVariable_Unpack(t[i]).scalar_type() == type[i] &&
+        THPVariable_Unpack(t[i]).numel() == size[i])
+      continue;
+    if (!PyErr_Occurred())
+      PyErr_Format(PyExc_ValueError, "AdamW: %s must be a contiguous %s tensor of %lld elements on CUDA device %ld",
+                   name[i], c10::toString(type[i]), size[i], dev);
+    return nullptr;
+  }
+  Py_RETURN_NONE;
+}
+
 // A contiguous tensor over a part of base's storage. (An allocation between two launches costs 3 to 6 us on the
 // host, 1 us alone: small outputs of one call share one.)
 at::Tensor part(const at::Tensor& base, int64_t offset, at::IntArrayRef sizes) {
@@ -220,6 +251,7 @@ PyObject* guarded(PyObject* self, PyObject* args) {
 
 PyMethodDef methods[] = {{"gradients", guarded<gradients>, METH_VARARGS, nullptr},
                          {"step", guarded<step>, METH_VARARGS, nullptr},
+                         {"state", guarded<state>, METH_VARARGS, nullptr},
                          {"outputs", guarded<outputs>, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lists", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -190,7 +190,7 @@ class AdamW:
 
     `clock` (float64 [3]: the steps made, and both betas to that power) is on the device and advanced by
     the step itself, so a captured step counts at every replay. A checkpoint is m, v, the scales and
-    clock. A parameter that gets no gradient keeps its moments; the bias corrections are those of the
+    clock: copied into them, or put in their place as tensors of the same type and length on the same device. A parameter that gets no gradient keeps its moments; the bias corrections are those of the
     common clock."""
 
     def __init__(self, params, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32, seed=None,
@@ -224,6 +224,7 @@ class AdamW:
         at = np.concatenate([[0], np.cumsum((self._n + _BLOCK - 1) // _BLOCK * _BLOCK)])
         self._tab["first"] = at[:-1]
         self.first, total = at[:-1].tolist(), int(at[-1])
+        self._total = total
         self._addresses()
         z = lambda k, dt: torch.zeros(k, dtype=dt, device=_device(self.dev))
         if bits == 8:
@@ -264,6 +265,7 @@ class AdamW:
         number for this step, or a float32 CUDA tensor [1] that the device reads. norm: float32 [1], as
         grad_norm gives it; with max_norm the gradients are scaled by min(1, max_norm / (norm + 1e-6))."""
         w, dev = "AdamW.step", self.dev
+        self._state_ok()
         if _lists().step(self._tab_at, self._n_at, len(self._n), grads, self.params, self.copies, dev):
             self._addresses()  # a parameter's memory is another one now
         if norm is not None:
@@ -280,10 +282,15 @@ class AdamW:
                 self.v.data_ptr(), _p(self.m_scale), _p(self.v_scale), self.clock.data_ptr(), _p(lr_dev), _p(norm),
                 self.ws.data_ptr(), self.ws.numel())
 
+    def _state_ok(self):
+        """Checks what a program may have put in the place of the moments and the clock."""
+        _lists().state(self.dev, self._total, self.bits, self.m, self.v, self.m_scale, self.v_scale, self.clock)
+
     def moments(self, stream=None):
         """(m, v) as float32 buffers: themselves with bits 32, what the codes stand for with bits 8."""
         if self.bits == 32:
             return self.m, self.v
+        self._state_ok()
         with _on(stream):
             m, v = torch.empty_like(self.m, dtype=_F32), torch.empty_like(self.v, dtype=_F32)
         _launch("moe_adamw_values", m, stream, self.m.data_ptr(), self.v.data_ptr(), self.m_scale.data_ptr(),
