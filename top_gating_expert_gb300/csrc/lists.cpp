@@ -7,6 +7,7 @@
 #include <ATen/core/TensorBody.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/TensorImpl.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -236,11 +237,19 @@ PyObject* outputs(PyObject*, PyObject* args) {
   return tuple_of(ts);
 }
 
-// No C++ exception (a tensor without storage throws one) leaves the module.
+// No C++ exception leaves the module: torch's own become what torch raises for them (no memory, no device); a tensor
+// that cannot be read (one without storage throws) is the caller's ValueError.
+PyObject* allocated(PyObject* self, PyObject* args) {
+  HANDLE_TH_ERRORS
+  return outputs(self, args);
+  END_HANDLE_TH_ERRORS
+}
 template <PyObject* (*F)(PyObject*, PyObject*)>
 PyObject* guarded(PyObject* self, PyObject* args) {
   try {
     return F(self, args);
+  } catch (const std::bad_alloc&) {
+    return PyErr_NoMemory();
   } catch (const std::exception& e) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, e.what());
   } catch (...) {
@@ -252,7 +261,7 @@ PyObject* guarded(PyObject* self, PyObject* args) {
 PyMethodDef methods[] = {{"gradients", guarded<gradients>, METH_VARARGS, nullptr},
                          {"step", guarded<step>, METH_VARARGS, nullptr},
                          {"state", guarded<state>, METH_VARARGS, nullptr},
-                         {"outputs", guarded<outputs>, METH_VARARGS, nullptr},
+                         {"outputs", allocated, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lists", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
