@@ -133,7 +133,8 @@ def _lists():
     except ImportError as e:
         raise RuntimeError("the extension _lists is not built; run `python -m top_gating_expert_gb300.build`") from e
     if m.built_for != torch.__version__:
-        raise RuntimeError(f"_lists was built for torch {m.built_for}, not {torch.__version__}: build it again")
+        raise RuntimeError(f"_lists was built for torch {m.built_for}, not {torch.__version__}; run `python -m "
+                           "top_gating_expert_gb300.build` again")
     return m
 
 
