@@ -323,14 +323,15 @@ class TrainStep:
         self.aux_coef, self.router_z, self.z_coef, self.ignore = aux_coef, router_z, z_coef, ignore_index
         self.masters, copies, decay = [], [], []
 
-        def train(name, value, held=None, vector=False):
-            """Adds a weight: `held` is what the forward reads (None: a tensor of its own); returns that."""
+        def train(name, value, held=None, vector=False, kind=None):
+            """Adds a weight: `held` is what the forward reads (None: a tensor of its own, `kind` its device and type);
+            returns that. The master is the value as it was given."""
             if vector or held is not None and held.dtype is _F32:
                 self.masters.append((name, held)); copies.append(None)
             else:
-                t = value if held is None else held
-                master = value.to(t.device, _F32, copy=True).contiguous()
-                low = t.dtype is torch.bfloat16
+                dev, dt = (held.device, held.dtype) if kind is None else kind
+                master = value.to(dev, _F32, copy=True).contiguous()
+                low = dt is torch.bfloat16
                 if low and held is None:
                     held = master.bfloat16()
                 self.masters.append((name, master)); copies.append(held if low else None)
@@ -348,10 +349,10 @@ class TrainStep:
                     train(at(n), None, t, vector=True)
                 self._unpacked.append(None)
             else:
-                dev, dt = b.layer.device, b.n.dtype
+                kind = b.layer.device, b.n.dtype
                 if not hasattr(b, "norm_ws"):
                     b.enable_backward(w)
-                u = {n: train(at(n), w[n].to(dev, dt)) for n in _MOE_MATRICES if w.get(n) is not None}
+                u = {n: train(at(n), w[n], kind=kind) for n in _MOE_MATRICES if w.get(n) is not None}
                 if b.layer.bias is not None:
                     u["bias"] = train(at("bias"), None, b.layer.bias, vector=True)
                 if b.layer.select_bias is not None:
