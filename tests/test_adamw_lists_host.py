@@ -113,3 +113,16 @@ def test_a_state_that_is_replaced(calls, bits):
         setattr(opt, name, t)
     opt.step(g)
     assert calls == ["moe_adamw_step"]
+
+
+def test_clipping_takes_a_norm(calls, monkeypatch):
+    """With max_norm a step that is given no norm takes its own gradients' first; none without gradients."""
+    opt = train.AdamW([there(300), there(5)], max_norm=1.0)
+    opt.step([there(300), there(5)], norm=there(1))
+    assert calls == ["moe_adamw_step"]
+    calls.clear()
+    monkeypatch.setattr(train, "grad_norm", lambda grads, ws, stream: calls.append("moe_grad_norm") or there(1))
+    opt.step(g for g in [there(300), None])
+    opt.step([None, None])
+    train.AdamW([there(300)]).step([there(300)])
+    assert calls == ["moe_grad_norm"] + ["moe_adamw_step"] * 3

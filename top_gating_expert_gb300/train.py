@@ -187,7 +187,8 @@ class AdamW:
     a number >= 0 at random around the value, the same way for the same seed. All parameters' moments
     lie in one buffer, parameter i's from element first[i] on. weight_decay: one number or one for each
     parameter. copies: bfloat16 tensors (or None) that receive the rounded parameters, for float32
-    master weights. max_norm: a step given the gradients' norm scales them to at most this norm.
+    master weights. max_norm: a step scales the gradients to at most this norm, by the norm that it is given or else by
+    that of its own gradients.
 
     `clock` (float64 [3]: the steps made, and both betas to that power) is on the device and advanced by
     the step itself, so a captured step counts at every replay. A checkpoint is m, v, the scales and
@@ -236,6 +237,7 @@ class AdamW:
             self.m_scale = self.v_scale = None
         self.clock = torch.tensor([0.0, 1.0, 1.0], dtype=torch.float64, device=_device(self.dev))
         self.ws = z(256, torch.uint8)
+        self.norm_ws = None if max_norm is None else z(_grad_norm_ws_bytes(), torch.uint8)
 
     def _addresses(self):
         """Reads the parameters' and copies' addresses and checks that no two overlap. The table is written when all
@@ -263,9 +265,13 @@ class AdamW:
 
     def step(self, grads, *, lr=None, norm=None, stream=None):
         """One step with a gradient for each parameter, of its shape or flat (None: that parameter is left as it is). lr: a
-        number for this step, or a float32 CUDA tensor [1] that the device reads. norm: float32 [1], as
-        grad_norm gives it; with max_norm the gradients are scaled by min(1, max_norm / (norm + 1e-6))."""
+        number for this step, or a float32 CUDA tensor [1] that the device reads. With max_norm the gradients are scaled
+        by min(1, max_norm / (norm + 1e-6)); norm: float32 [1], as grad_norm gives it (None: that of these gradients,
+        one launch more)."""
         w, dev = "AdamW.step", self.dev
+        clip = self.max_norm is not None and norm is None
+        if clip:
+            grads = list(grads)  # read twice
         self._state_ok()
         if _lists().step(self._tab_at, self._n_at, len(self._n), grads, self.params, self.copies, dev):
             self._addresses()  # a parameter's memory is another one now
@@ -273,6 +279,8 @@ class AdamW:
             _vector(norm, "norm", w, 1, dev)
             if self.max_norm is None:
                 raise ValueError(f"{w}: norm given, but no max_norm to scale to")
+        elif clip and any(g is not None for g in grads):
+            norm = grad_norm(grads, ws=self.norm_ws, stream=stream)
         lr_dev = None
         if isinstance(lr, torch.Tensor):
             _vector(lr, "lr", w, 1, dev)
@@ -362,7 +370,6 @@ class TrainStep:
                 train(at(n), None, t, vector=True)
         train("head", head, head)
         self.opt = AdamW([t for _, t in self.masters], weight_decay=decay, copies=copies, **adamw)
-        self.norm_ws = grad_norm_workspace(head.device)
         T, M = self.blocks[0].n.shape if self.blocks else (0, head.shape[1])
         self.ws = linear_cross_entropy_workspace(T, head.shape[0], M, head.dtype, head.device) if self.blocks else None
 
@@ -399,8 +406,7 @@ class TrainStep:
     def step(self, x, target, u=None, lr=None):
         """One step; returns the stats of its forward (float32 [2], on the device)."""
         stats, grads = self.gradients(x, target, u)
-        norm = None if self.opt.max_norm is None else grad_norm(grads, ws=self.norm_ws)
-        self.opt.step(grads, lr=lr, norm=norm)
+        self.opt.step(grads, lr=lr)
         for b, w in zip(self.blocks, self._unpacked):
             if w is not None:
                 b.layer.set_weights(w)
