@@ -663,8 +663,12 @@ typedef struct {
  *   bits 32: m, v are float buffers. bits 8: m int8 and v uint8 codes in blocks of 256 elements with
  *     a float each in m_scale, v_scale (index = place / 256): m = sign(c) (c / 127)^2 m_scale, v =
  *     ((c / 255)^2 v_scale)^2. Codes are those of the nearest value (seed < 0), or of one of the two
- *     around it at random, with the value as expectation, by a hash of seed (its low 32 bits), t and place. Only v = 0
- *     has code 0. A value that is not finite makes its block's scale NaN.
+ *     around it at random, by a hash of seed (its low 32 bits), t and place, with m or sqrt(v) as expectation. Only v = 0
+ *     has code 0: a sqrt(v) below code 1's value takes code 1. So m keeps its mean, and sqrt(v) from code 1 on; the v that
+ *     the codes stand for is high by the variance of its root, f (1 - f) (2 c + 1)^2 (v_scale / 255^2)^2 a step for a
+ *     root the fraction f of the way from code c to the next; over many steps with normal gradients by about 1 / c of
+ *     itself (2 at code 1, 0.14 at 8, 0.01 at 81; such elements' steps are shorter by half of that). A value that is not
+ *     finite makes its block's scale NaN.
  *     Blocks whose largest |m| or sqrt(v) is below 2^-100 become 0.
  *   Buffers: m, v 16-byte aligned; what lies behind a tensor's n elements up to its block's end must
  *     be 0 at first and stays so.

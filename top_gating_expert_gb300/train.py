@@ -184,7 +184,8 @@ class AdamW:
 
     bits 32 holds both moments as float32 (`m`, `v`), bits 8 as codes (int8, uint8) of blocks of 256
     elements with a float32 scale each (`m_scale`, `v_scale`); seed: None rounds to the nearest code,
-    a number >= 0 at random around the value, the same way for the same seed. All parameters' moments
+    a number >= 0 at random around the value, the same way for the same seed (m and sqrt(v) keep their means; v is
+    high by its root's variance, about 1 / c of itself at code c). All parameters' moments
     lie in one buffer, parameter i's from element first[i] on. weight_decay: one number or one for each
     parameter. copies: bfloat16 tensors (or None) that receive the rounded parameters, for float32
     master weights. max_norm: a step scales the gradients to at most this norm, by the norm that it is given or else by
