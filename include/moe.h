@@ -667,7 +667,7 @@ typedef struct {
  *     has code 0: a sqrt(v) below code 1's value takes code 1. So m keeps its mean, and sqrt(v) from code 1 on; the v that
  *     the codes stand for is high by the variance of its root, f (1 - f) (2 c + 1)^2 (v_scale / 255^2)^2 a step for a
  *     root the fraction f of the way from code c to the next; over many steps with normal gradients by about 1 / c of
- *     itself (2 at code 1, 0.14 at 8, 0.01 at 81; such elements' steps are shorter by half of that). A value that is not
+ *     itself (1.7 at code 1, 0.13 at 8, 0.01 at 81), and the mean of 1 / sqrt(v) by about 0.3 / c. A value that is not
  *     finite makes its block's scale NaN.
  *     Blocks whose largest |m| or sqrt(v) is below 2^-100 become 0.
  *   Buffers: m, v 16-byte aligned; what lies behind a tensor's n elements up to its block's end must

@@ -22,7 +22,7 @@
 // moves v by 0.1 % a step, codes are 0.8 % apart at best). r comes from a hash of seed, step and
 // place. No sqrt(v) above 0 goes to code 0: m / sqrt(v) would grow without bound. What keeps its mean is the root: v
 // itself is high by the root's variance, in a run of steps by about 1 / c of itself at code c (normal gradients, beta2 0.95
-// and 0.999 alike: 14 % at code 8, 1 % at 81), which makes the steps of a block's smallest elements shorter.
+// and 0.999 alike: 13 % at code 8, 1 % at 81), and 1 / sqrt(v), by which a step is as long, by about 0.3 / c.
 // The update takes the moments before they are rounded. Operations on the way to a code are
 // rounded one by one (no fused multiply-add), so the codes are a function of the formula alone.
 #include <cuda_bf16.h>
