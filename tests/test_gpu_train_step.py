@@ -30,3 +30,20 @@ def test_masters_are_the_values_given(native_lib):
         assert (c is None) == (values[n].dim() == 1), n
     step.blocks[0].layer.set_weights(step._unpacked[0])
     assert torch.equal(blocks[0].forward(x), before)
+
+
+@pytest.mark.parametrize("M,lead", [(64, 0), (64, 1), (68, 0), (67, 3)])
+def test_workspace_of_the_head(native_lib, M, lead):
+    """Room for copies of x and the head only where rows are on no 16-byte boundary; a step runs in what there is."""
+    T, V = 200, 3001
+    d = dense_weights(M, 96, 6, torch.bfloat16)
+    head = torch.zeros(V * M + 8, device="cuda", dtype=torch.bfloat16)[lead:lead + V * M].view(V, M)
+    head.copy_(torch.randn(V, M, generator=generator(7), device="cuda") * M ** -0.5)
+    first = head.clone()
+    step = train.TrainStep([block.DenseBlock(T, d)], [d], head, lr=1e-2)
+    least, most = (train.linear_cross_entropy_workspace(T, V, M, aligned=a).numel() for a in (True, False))
+    copies = lead or M % 8
+    assert step.ws.numel() == (most if copies else least) and (most - least > 2 * V * M or M % 8)
+    x = torch.randn(T, M, generator=generator(8), device="cuda").bfloat16()
+    stats = step.step(x, torch.randint(0, V, (T,), generator=generator(9), device="cuda"))
+    assert torch.isfinite(stats).all() and not torch.equal(head, first)

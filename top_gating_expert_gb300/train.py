@@ -372,7 +372,9 @@ class TrainStep:
         train("head", head, head)
         self.opt = AdamW([t for _, t in self.masters], weight_decay=decay, copies=copies, **adamw)
         T, M = self.blocks[0].n.shape if self.blocks else (0, head.shape[1])
-        self.ws = linear_cross_entropy_workspace(T, head.shape[0], M, head.dtype, head.device) if self.blocks else None
+        # room for copies only where the head starts on no 16-byte boundary (a block's output does not)
+        self.ws = linear_cross_entropy_workspace(T, head.shape[0], M, head.dtype, head.device,
+                                                 aligned=head.data_ptr() % 16 == 0) if self.blocks else None
 
     def gradients(self, x, target, u=None):
         """(stats, gradients): the head's stats (see linear_cross_entropy) and a gradient for each of `masters`, of its shape.
