@@ -3,8 +3,8 @@
 import pytest
 import torch
 
-from block_util import generator
-from test_gpu_train import MOE, SCORE, dense_weights, moe_weights
+from block_util import assert_within, generator
+from test_gpu_train import MOE, SCORE, dense64, dense_weights, moe_weights
 from top_gating_expert_gb300 import block, train
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +47,23 @@ def test_workspace_of_the_head(native_lib, M, lead):
     x = torch.randn(T, M, generator=generator(8), device="cuda").bfloat16()
     stats = step.step(x, torch.randint(0, V, (T,), generator=generator(9), device="cuda"))
     assert torch.isfinite(stats).all() and not torch.equal(head, first)
+
+
+@pytest.mark.parametrize("blocks", [0, 2])
+def test_gradient_of_the_input(native_lib, blocks):
+    """Against the same model in 64 bits; tolerance as in the float32 steps' test: 1e-4 of a gradient and of their
+    root mean square."""
+    T, M, V = 130, 64, 700
+    ws = [dense_weights(M, 96, s, torch.float32) for s in range(blocks)]
+    head = torch.randn(V, M, generator=generator(7), device="cuda") * M ** -0.5
+    step = train.TrainStep([block.DenseBlock(T, w, dtype=torch.float32) for w in ws], ws, head, lr=1e-2)
+    x = torch.randn(T, M, generator=generator(8), device="cuda")
+    y = torch.randint(0, V, (T,), generator=generator(9), device="cuda")
+    x64 = x.double().requires_grad_(True)
+    h = x64
+    for w in ws:
+        h = dense64(h, {n: t.double() for n, t in w.items()})
+    want, = torch.autograd.grad(torch.nn.functional.cross_entropy(h @ head.double().t(), y), x64)
+    step.step(x, y)
+    assert step.dx.shape == x.shape
+    assert_within(step.dx, want, 1e-4 * (want.abs() + want.square().mean().sqrt()), "dx")

@@ -370,6 +370,7 @@ class TrainStep:
             for n, t in (("norm_gamma", b.gamma), ("norm_beta", b.beta)):
                 train(at(n), None, t, vector=True)
         train("head", head, head)
+        self.dx = None
         self.opt = AdamW([t for _, t in self.masters], weight_decay=decay, copies=copies, **adamw)
         T, M = self.blocks[0].n.shape if self.blocks else (0, head.shape[1])
         # room for copies only where the head starts on no 16-byte boundary (a block's output does not)
@@ -378,7 +379,8 @@ class TrainStep:
 
     def gradients(self, x, target, u=None):
         """(stats, gradients): the head's stats (see linear_cross_entropy) and a gradient for each of `masters`, of its shape.
-        u: the draws for blocks with random routing."""
+        u: the draws for blocks with random routing. The gradient of x itself is in `dx` afterwards, for what stands in
+        front of the blocks (an embedding)."""
         inputs = []
         for b in self.blocks:
             inputs.append(x)
@@ -403,6 +405,7 @@ class TrainStep:
             if c.n_shared > 1:  # the shared experts' hidden units lie side by side
                 got[-1] = got[-1].view(c.M, c.n_shared, c.H_shared).transpose(0, 1).contiguous()
             found.append([t for t in (*got, g.dbias) if t is not None] + [dgamma, dbeta])
+        self.dx = dx
         grads = [t for part in reversed(found) for t in part]
         return stats, [t if t.shape == p.shape else t.view(p.shape) for t, (_, p) in zip(grads, self.masters)]
 
