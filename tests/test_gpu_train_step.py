@@ -67,3 +67,25 @@ def test_gradient_of_the_input(native_lib, blocks):
     step.step(x, y)
     assert step.dx.shape == x.shape
     assert_within(step.dx, want, 1e-4 * (want.abs() + want.square().mean().sqrt()), "dx")
+
+
+def test_draws_of_each_block(native_lib):
+    """Blocks with random routing take draws of their own from a list; one tensor serves all of them."""
+    cfg = dict(MOE, act="relu", n_shared=0, H_shared=0, random_routing=1, capacity_factor=1.0, bias=False)
+    w, x = moe_weights(cfg, 5)
+    w.pop("select_bias")
+    d = dense_weights(cfg["M"], 96, 6, torch.bfloat16)
+    head = (torch.randn(1003, cfg["M"], generator=generator(7), device="cuda") * 0.1).bfloat16()
+    make = lambda: [block.MoeBlock(cfg, w), block.DenseBlock(cfg["S"], d), block.MoeBlock(cfg, w)]
+    step, own = train.TrainStep(make(), [w, d, w], head, lr=1e-3), make()
+    y = torch.randint(0, 1003, (cfg["S"],), generator=generator(8), device="cuda")
+    u = torch.rand(2, cfg["S"], generator=generator(9), device="cuda")
+    for draws, each in ((u[0], (u[0], u[0])), ([u[0], None, u[1]], (u[0], u[1])), ((u[1], u[0], u[0]), (u[1], u[0]))):
+        step.gradients(x, y, draws)
+        want = own[2].forward(own[1].forward(own[0].forward(x, each[0])), each[1])
+        assert torch.equal(step.blocks[2].y, want)
+        for a, b in ((0, 0), (2, 2)):
+            assert torch.equal(step.blocks[a].layer.route_out.row, own[b].layer.route_out.row)
+    assert not torch.equal(step.blocks[0].layer.route_out.drop_reason, step.blocks[2].layer.route_out.drop_reason)
+    with pytest.raises(ValueError):
+        step.gradients(x, y, [u[0], u[1]])

@@ -379,15 +379,19 @@ class TrainStep:
 
     def gradients(self, x, target, u=None):
         """(stats, gradients): the head's stats (see linear_cross_entropy) and a gradient for each of `masters`, of its shape.
-        u: the draws for blocks with random routing. The gradient of x itself is in `dx` afterwards, for what stands in
+        u: the draws for blocks with random routing, a tensor that all of them read or a list with an entry for each block
+        (None for those without). The gradient of x itself is in `dx` afterwards, for what stands in
         front of the blocks (an embedding)."""
         inputs = []
-        for b in self.blocks:
+        draws = u if isinstance(u, (list, tuple)) else [u] * len(self.blocks)
+        if len(draws) != len(self.blocks):
+            raise ValueError(f"TrainStep: draws for {len(draws)} of {len(self.blocks)} blocks")
+        for b, d in zip(self.blocks, draws):
             inputs.append(x)
             if isinstance(b, block.DenseBlock):
                 x = b.forward(x)
             else:
-                x = b.forward(x, u if b.layer.cfg.random_routing else None)
+                x = b.forward(x, d if b.layer.cfg.random_routing else None)
         _, lse, stats = linear_cross_entropy(x, self.head, target, ignore_index=self.ignore, z_coef=self.z_coef,
                                              ws=self.ws)
         dx, dhead = linear_cross_entropy_backward(x, self.head, target, lse, stats=stats, ignore_index=self.ignore,
