@@ -89,3 +89,21 @@ def test_draws_of_each_block(native_lib):
     assert not torch.equal(step.blocks[0].layer.route_out.drop_reason, step.blocks[2].layer.route_out.drop_reason)
     with pytest.raises(ValueError):
         step.gradients(x, y, [u[0], u[1]])
+
+
+def test_weights_that_a_step_would_refuse(native_lib):
+    """Experts in another shape, as a layer packs them by address: refused before the first step changes anything.
+    A layer made from other values takes the dict's at once."""
+    cfg = dict(MOE, bias=False)
+    w, x = moe_weights(cfg, 5)
+    w.pop("select_bias")
+    head = torch.zeros(100, cfg["M"], device="cuda", dtype=torch.bfloat16)
+    flat_ = dict(w, W_in=w["W_in"].reshape(-1, cfg["M"]))
+    with pytest.raises(ValueError):
+        train.TrainStep([block.MoeBlock(cfg, flat_)], [flat_], head)
+    other = dict(w, W_in=2 * w["W_in"])
+    b = block.MoeBlock(cfg, other)
+    before = b.forward(x).clone()
+    train.TrainStep([b], [w], head)
+    after = b.forward(x).clone()
+    assert torch.equal(after, block.MoeBlock(cfg, w).forward(x)) and not torch.equal(after, before)

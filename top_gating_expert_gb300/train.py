@@ -366,6 +366,7 @@ class TrainStep:
                     u["bias"] = train(at("bias"), None, b.layer.bias, vector=True)
                 if b.layer.select_bias is not None:
                     u["select_bias"] = b.layer.select_bias
+                b.layer.set_weights(u)  # what a step would refuse is refused here, and the layer's are the dict's
                 self._unpacked.append(u)
             for n, t in (("norm_gamma", b.gamma), ("norm_beta", b.beta)):
                 train(at(n), None, t, vector=True)
