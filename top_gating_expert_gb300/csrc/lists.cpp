@@ -84,6 +84,14 @@ PyObject* gradients(PyObject*, PyObject* args) {
                        Py_ssize_t(tab.size()));
 }
 
+// Whether a tensor is what the table says: address (which implies the device), type, size, contiguous.
+bool as_it_was(PyObject* o, const void* held, int type, int64_t n) {
+  if (!THPVariable_Check(o)) return false;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  return address(o) == held && t.scalar_type() == (type == MOE_BF16 ? at::kBFloat16 : at::kFloat) && t.numel() == n &&
+         t.is_contiguous();
+}
+
 // Whether a gradient's elements are those of its parameter, one for one: the same shape (sides of 1 apart), or one of
 // them flat.
 bool same_order(const at::Tensor& g, const at::Tensor& p) {
@@ -118,15 +126,15 @@ PyObject* step(PyObject*, PyObject* args) {
   bool moved = false;
   for (Py_ssize_t i = 0; i < g.size(); ++i) {
     moe_param_t& e = tab[i];
-    const int pt = element_type(p[i], dev, "AdamW.step", "every parameter");
-    if (pt < 0) return nullptr;
-    moved |= address(p[i]) != e.p || pt != e.p_dtype || THPVariable_Unpack(p[i]).numel() != n[i];
-    if (c[i] != Py_None) {
-      const int ct = element_type(c[i], dev, "AdamW.step", "every copy");
-      if (ct < 0) return nullptr;
-      moved |= address(c[i]) != e.copy || ct != MOE_BF16 || THPVariable_Unpack(c[i]).numel() != n[i];
-    } else {
+    if (!as_it_was(p[i], e.p, e.p_dtype, n[i])) {
+      if (element_type(p[i], dev, "AdamW.step", "every parameter") < 0) return nullptr;
+      moved = true;
+    }
+    if (c[i] == Py_None) {
       moved |= e.copy != nullptr;
+    } else if (!as_it_was(c[i], e.copy, MOE_BF16, n[i])) {
+      if (element_type(c[i], dev, "AdamW.step", "every copy") < 0) return nullptr;
+      moved = true;
     }
     if (g[i] == Py_None) {
       e.g = nullptr;
