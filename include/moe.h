@@ -696,7 +696,8 @@ int moe_adamw_values(const void* m, const void* v, const float* m_scale, const f
 /*
  * out[0] = sqrt of the sum of squares of all elements of the tensors' g (of moe_param_t, g, n and
  * g_dtype are read). Squares are summed in fp32 within a CTA's share and in fp64 over the shares, in
- * an order fixed by the sizes: an element above 1.8e19 gives infinity.
+ * an order fixed by the sizes: an element above 1.8e19 gives infinity, one below 1e-19 counts with fewer digits and
+ * below 2e-23 not at all (its square is a denormal number, or 0).
  */
 int moe_grad_norm_workspace_bytes(size_t* bytes);
 int moe_grad_norm(const moe_param_t* params, int n, float* out, void* ws, size_t ws_bytes,

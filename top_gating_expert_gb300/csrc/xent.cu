@@ -10,8 +10,10 @@
 // Backward, bf16: a piece of the vocabulary at a time, the logits once more, d in bf16 into the
 // workspace, then its share of dx (fp32 sums over the pieces) and the rows of dW, which are whole. Pieces of
 // about 512 MB of d: small enough for memory (the logits of 8192 tokens and 131072 entries take 4.3 GB in
-// fp32), large enough that the sums' way through memory, 8 bytes an element of dx and piece, stays below
-// 2 % of the products.
+// fp32). The sums' way through memory, 8 bytes an element of dx and piece, is about 350 / entries of the products'
+// time, and a piece has 2^28 / tokens entries: 1 % at 8192 tokens, 2 at 16384, 9 at 65536 (65536 x 32768 x 1024: 8.2 to 8.9 ms,
+// in one piece of 4.3 GB 8.1), 68 with the least piece, from half a million tokens on. Who has memory for larger
+// pieces gives their size.
 // d of the mean loss is kept without the weight that all tokens share, which the products' results take:
 // rounding to bf16 then leaves the target's entry, near -1, almost as it is, where w (p - 1) would be off by up to
 // 2^-8, the same way in every token (8192 x 65536 x 2048: gradients 3.1e-3 off in all with w in d, now 1.7e-3,

@@ -64,7 +64,8 @@ def linear_cross_entropy(x, W, target, *, ignore_index=-100, z_coef=0.0, loss=No
     the logsumexp lse of its logits, float32 [T], and stats, float32 [2]: the mean loss over the
     tokens with a target, and their number. The logits are not stored. A target outside of the
     vocabulary gives a NaN loss and, in ws, the status MOE_ERR_DEVICE_DATA. piece: vocabulary entries
-    at a time (0: chosen from the sizes)."""
+    at a time (0: chosen from the sizes). Outputs that are not given may share an allocation (up to 1 MB): who keeps
+    stats for long and little memory gives a tensor for it, or clones it."""
     w = "linear_cross_entropy"
     T, V, K, dt, dev, ldx, ldw = _xent_checked(x, W, target, w)
     if loss is None and lse is None and stats is None:
@@ -90,7 +91,8 @@ def linear_cross_entropy_backward(x, W, target, lse, *, dloss=None, stats=None, 
                                   stream=None):
     """(dx, dW) of linear_cross_entropy, in the element type: the gradient of sum(dloss * loss) for
     dloss float32 [T], or without it of scale times the mean loss, from the forward's stats. lse,
-    ignore_index and z_coef as in the forward; None for what is not needed."""
+    ignore_index and z_coef as in the forward; None for what is not needed. A token without a gradient has its row of x
+    in dW's sums with weight 0: the row has to be finite."""
     w = "linear_cross_entropy_backward"
     T, V, K, dt, dev, ldx, ldw = _xent_checked(x, W, target, w)
     _vector(lse, "lse", w, T, dev)
