@@ -195,7 +195,8 @@ class AdamW:
 
     `clock` (float64 [3]: the steps made, and both betas to that power) is on the device and advanced by
     the step itself, so a captured step counts at every replay. A checkpoint is m, v, the scales and
-    clock: copied into them, or put in their place as tensors of the same type and length on the same device. A parameter that gets no gradient keeps its moments; the bias corrections are those of the
+    clock: copied into them, or put in their place as tensors of the same type and length on the same
+    device. A parameter that gets no gradient keeps its moments; the bias corrections are those of the
     common clock."""
 
     def __init__(self, params, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32, seed=None,
